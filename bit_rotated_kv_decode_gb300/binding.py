@@ -48,6 +48,13 @@ class oscar_cache_layout(ctypes.Structure):
         "hist_pt_offset", "bf16_pt_offset", "error_word_offset", "decode_count_offset", "decode_flag_offset")]
 
 
+class oscar_rope(ctypes.Structure):
+    _fields_ = [("table", c_void_p), ("length", c_int32), ("dim", c_int32), ("interleaved", c_int32)]
+
+
+OSCAR_F32, OSCAR_BF16 = 0, 1
+
+
 class OscarError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -82,6 +89,21 @@ _SIGNATURES = {
     "oscar_bf16_decode_workspace_bytes": (c_size_t, [c_int32, POINTER(c_int32), c_int32, c_int32]),
     "oscar_bf16_decode": (c_int32, [_P, c_int64, _P, c_int32, POINTER(c_int32), c_int32, c_int32, c_int32, c_float,
                                     _P, _P, _P, c_size_t, _P]),
+    "oscar_bf16_append": (c_int32, [_P, c_int64, _P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, c_int32,
+                                    c_int32, POINTER(oscar_rope), _P, c_int64, _P, c_int64, _P, c_int64, _P, _P, _P]),
+    "oscar_int4_append": (c_int32, [_P, c_int64, _P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, c_int32,
+                                    c_int32, c_int32, POINTER(oscar_rope), _P, c_int64, _P, c_int64, _P, c_int64, _P,
+                                    _P, _P]),
+    "oscar_int4_read": (c_int32, [_P, c_int64, _P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, c_int32,
+                                  c_int32, _P, _P, c_int32, _P, _P]),
+    "oscar_attention_workspace_bytes": (c_size_t, [c_int32, POINTER(c_int32), c_int32, c_int32]),
+    "oscar_window_attention": (c_int32, [_P, c_int64, _P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, c_int32,
+                                         c_int32, c_int32, c_int32, c_float, _P, c_int64, _P, c_int32, _P, _P, _P,
+                                         c_size_t, _P]),
+    "oscar_int4_attention": (c_int32, [_P, c_int64, _P, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, c_int32,
+                                       c_int32, c_int32, c_int32, c_int32, c_float, _P, c_int64, _P, c_int32, _P, _P,
+                                       _P, c_size_t, _P]),
+    "oscar_paged_last_error": (c_char_p, []),
 }
 
 _lib = None
@@ -330,3 +352,232 @@ def new_workspace(nbytes: int, device="cuda"):
     t = torch.zeros(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-t.data_ptr()) % 256
     return t[off:off + nbytes]
+
+
+# ---- paged caches: position rotation, windowed attention, 4 bits ----------------
+INT4_RECORD_BYTES = {128: 8704, 64: 9216}
+
+
+def rope_table(length: int, dim: int = HEAD_DIM, theta: float = 10000.0, scale: float = 1.0, device="cuda"):
+    """fp32 [length][dim]: cosines, then sines, of position * scale * theta^(-2 i / dim).  The angles are
+    taken in float64, so that far positions keep theirs; scale 1 / s stretches the positions by s."""
+    import torch
+    inv = scale * theta ** (-2.0 * torch.arange(dim // 2, dtype=torch.float64) / dim)
+    a = torch.arange(length, dtype=torch.float64)[:, None] * inv
+    return torch.cat([a.cos(), a.sin()], 1).float().to(device)
+
+
+def int4_pool(num_pages: int, num_kv_heads: int, group_size: int = 128, device="cuda"):
+    """Zeroed 4-bit page pool uint8 [num_pages][num_kv_heads][record]."""
+    import torch
+    return torch.zeros(num_pages, num_kv_heads, INT4_RECORD_BYTES[group_size], dtype=torch.uint8, device=device)
+
+
+def _refuse(what: str):
+    raise OscarError(OSCAR_ERR_INVALID_ARG, what)
+
+
+def _paged_check(st: int, what: str) -> None:
+    if st != OSCAR_OK:
+        raise OscarError(st, f"{what}: {load().oscar_paged_last_error().decode()}")
+
+
+def _device(name: str, t) -> None:
+    import torch
+    if not t.is_cuda:
+        _refuse(f"{name}: a CUDA tensor is wanted")
+    if t.get_device() != torch.cuda.current_device():
+        _refuse(f"{name} is on another device than the current one")
+
+
+def _on_device(name: str, t, dtype, shape=None, device=None) -> int:
+    """Address of a dense CUDA tensor of the current device with the given type and shape."""
+    if t.dtype is not dtype or not t.is_contiguous():
+        _refuse(f"{name}: a dense {dtype} CUDA tensor is wanted")
+    if device is None or t.get_device() != device:
+        _device(name, t)
+    if shape is not None and t.shape != shape:
+        _refuse(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _heads(name: str, t, rows: int, heads: int, device: int):
+    """Address and token stride of bf16 [rows][heads][128] whose heads lie densely."""
+    import torch
+    if t.dtype is not torch.bfloat16:
+        _refuse(f"{name}: a bfloat16 CUDA tensor is wanted")
+    if t.get_device() != device:
+        _device(name, t)
+    if t.shape != (rows, heads, HEAD_DIM):
+        _refuse(f"{name}: shape {tuple(t.shape)}, wanted {(rows, heads, HEAD_DIM)}")
+    stride, inner, last = t.stride()
+    if (heads > 1 and inner != HEAD_DIM) or last != 1:
+        _refuse(f"{name}: heads must lie densely")
+    return t.data_ptr(), stride if rows > 1 else heads * HEAD_DIM
+
+
+def _current(stream):
+    """(device, raw stream) that a call goes to; the device -1 without a GPU, which no tensor is on."""
+    import torch
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    device = torch.cuda.current_device()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, _stream_ptr(stream)
+
+
+def _counts(values, n: int, name: str):
+    """(ctypes array, sum) of one host int per request; None stands for one each."""
+    if values is None:
+        return None, n
+    if len(values) != n:
+        _refuse(f"{name}: one per request is wanted")
+    arr = (c_int32 * n)(*values)
+    return arr, sum(values)
+
+
+def _pool16(kv, num_kv_heads, device):
+    import torch
+    return _on_device("kv", kv, torch.bfloat16, (kv.shape[0], num_kv_heads, 2, 64, HEAD_DIM), device)
+
+
+def _pool4(kv, num_kv_heads, group_size, device):
+    import torch
+    if group_size not in INT4_RECORD_BYTES:
+        _refuse("group_size must be 128 or 64")
+    return _on_device("kv", kv, torch.uint8, (kv.shape[0], num_kv_heads, INT4_RECORD_BYTES[group_size]), device)
+
+
+def _pool(kv, num_kv_heads, group, device):
+    return _pool4(kv, num_kv_heads, group[0], device) if group else _pool16(kv, num_kv_heads, device)
+
+
+def _append(fn, group, kv, page_table, lens, k, v, rope, q, q_out, new_lens, interleaved, error, stream):
+    import torch
+    device, s = _current(stream)
+    n, hkv = len(lens), k.shape[1]
+    pool = _pool(kv, hkv, group, device)
+    old, _ = _counts(lens, n, "lens")
+    new, rows = _counts(new_lens, n, "new_lens")
+    if n == 0 or min(lens) < 0 or (new is not None and min(new_lens) < 0):
+        _refuse("no requests, or negative lens or new_lens")
+    table = _on_device("page_table", page_table, torch.int32, (n, page_table.shape[1]), device)
+    kp, ks = _heads("k", k, rows, hkv, device)
+    vp, vs = _heads("v", v, rows, hkv, device)
+    hq, qp, qs, qo = 0, None, 0, None
+    if (q is None) != (q_out is None):
+        _refuse("q and q_out come together")
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _heads("q", q, rows, hq, device)
+        qo = _on_device("q_out", q_out, torch.bfloat16, (rows, hq, HEAD_DIM), device)
+    r = None
+    if rope is not None:
+        length, dim = rope.shape
+        r = ctypes.byref(oscar_rope(_on_device("rope", rope, torch.float32, None, device), length, dim, interleaved))
+    err = None if error is None else _on_device("error", error, torch.int32, None, device)
+    if rows:
+        _paged_check(fn(pool, kv.shape[0], table, page_table.shape[1], old, new, n, hq, hkv, *group, r, qp, qs, kp, ks,
+                        vp, vs, qo, err, s), "append")
+
+
+def bf16_append(kv, page_table, lens, k, v, rope=None, q=None, q_out=None, new_lens=None, interleaved: bool = False,
+                error=None, stream=None) -> None:
+    """Rotate q and k by their positions and append k and v to BF16 pages [pages][Hkv][2][64][128]: request i's
+    new_lens[i] tokens (one each by default) go to positions lens[i], lens[i] + 1, ...  k, v bf16 [rows][Hkv][128] and
+    q [rows][Hq][128] may be slices of one projection's output; the rotated q goes to q_out.  rope: rope_table(), or
+    None for no rotation.  error: int32 [1] device word for bad page ids."""
+    _append(load().oscar_bf16_append, (), kv, page_table, lens, k, v, rope, q, q_out, new_lens, interleaved, error,
+            stream)
+
+
+def int4_append(kv, page_table, lens, k, v, rope=None, q=None, q_out=None, new_lens=None, interleaved: bool = False,
+                group_size: int = 128, error=None, stream=None) -> None:
+    """bf16_append into a 4-bit pool (int4_pool), quantised per token, kv head and group of group_size channels."""
+    _append(load().oscar_int4_append, (group_size,), kv, page_table, lens, k, v, rope, q, q_out, new_lens, interleaved,
+            error, stream)
+
+
+def int4_read(kv, page_table, starts, counts, k_out, v_out, group_size: int = 128, error=None, stream=None) -> None:
+    """The values of tokens [starts[i], starts[i] + counts[i]) of each request of a 4-bit pool, into k_out and v_out
+    [rows][Hkv][128], fp32 or bf16."""
+    import torch
+    device, s = _current(stream)
+    n, hkv = len(starts), kv.shape[1]
+    pool = _pool4(kv, hkv, group_size, device)
+    first, _ = _counts(starts, n, "starts")
+    count, rows = _counts(counts, n, "counts")
+    if n == 0 or min(starts) < 0 or min(counts) < 0:
+        _refuse("no requests, or negative starts or counts")
+    table = _on_device("page_table", page_table, torch.int32, (n, page_table.shape[1]), device)
+    kind = k_out.dtype
+    if kind is not torch.float32 and kind is not torch.bfloat16:
+        _refuse("k_out and v_out: float32 or bfloat16")
+    ko = _on_device("k_out", k_out, kind, (rows, hkv, HEAD_DIM), device)
+    vo = _on_device("v_out", v_out, kind, (rows, hkv, HEAD_DIM), device)
+    err = None if error is None else _on_device("error", error, torch.int32, None, device)
+    if rows:
+        _paged_check(load().oscar_int4_read(pool, kv.shape[0], table, page_table.shape[1], first, count, n, hkv,
+                                            group_size, ko, vo, OSCAR_F32 if kind is torch.float32 else OSCAR_BF16,
+                                            err, s), "read")
+
+
+def attention_workspace(n: int, num_q_heads: int, num_kv_heads: int, q_lens=None, stream=None):
+    """Zeroed workspace for window_attention / int4_attention calls of n requests."""
+    import torch
+    device, s = _current(stream)
+    need = load().oscar_attention_workspace_bytes(n, _counts(q_lens, n, "q_lens")[0], num_q_heads, num_kv_heads)
+    if need == 0:
+        _refuse("arguments outside the supported limits")
+    with torch.cuda.stream(torch.cuda.ExternalStream(s, device) if stream is not None else None):
+        return new_workspace(need)
+
+
+def _attention(fn, group, kv, page_table, lens, q, out, hkv, window, sinks, q_lens, scale, lse, workspace, error,
+               stream):
+    import torch
+    device, s = _current(stream)
+    n, hq = len(lens), q.shape[1]
+    pool = _pool(kv, hkv, group, device)
+    total, _ = _counts(lens, n, "lens")
+    new, rows = _counts(q_lens, n, "q_lens")
+    if n == 0 or (new is not None and min(q_lens) < 0):
+        _refuse("no requests, or negative q_lens")
+    table = _on_device("page_table", page_table, torch.int32, (n, page_table.shape[1]), device)
+    qp, qs = _heads("q", q, rows, hq, device)
+    kind = out.dtype
+    if kind is not torch.float32 and kind is not torch.bfloat16:
+        _refuse("out: float32 or bfloat16")
+    op = _on_device("out", out, kind, (rows, hq, HEAD_DIM), device)
+    lp = None if lse is None else _on_device("lse", lse, torch.float32, (rows, hq), device)
+    err = None if error is None else _on_device("error", error, torch.int32, None, device)
+    if workspace is None:
+        workspace = attention_workspace(n, hq, hkv, q_lens, stream)
+    while rows:
+        st = fn(pool, kv.shape[0], table, page_table.shape[1], total, new, n, hq, hkv, *group, window, sinks, scale, qp,
+                qs, op, OSCAR_F32 if kind is torch.float32 else OSCAR_BF16, lp, err,
+                _on_device("workspace", workspace, torch.uint8, None, device), workspace.numel(), s)
+        if st == OSCAR_ERR_INVALID_ARG and load().oscar_paged_last_error() == b"workspace too small":
+            workspace = attention_workspace(n, hq, hkv, q_lens, stream)
+            continue
+        _paged_check(st, "attention")
+        break
+    return workspace
+
+
+def window_attention(kv, page_table, lens, q, out, num_kv_heads: int, window: int = -1, sinks: int = 0, q_lens=None,
+                     scale: float = 0.0, lse=None, workspace=None, error=None, stream=None):
+    """Attention of the last q_lens[i] positions (one each by default) of every request over BF16 pages: the query at
+    position p sees the tokens t <= p with t < sinks or t > p - window (window < 0: no bound).  q bf16 [rows][Hq][128]
+    (rows may be strided), out [rows][Hq][128] fp32 or bf16, lse fp32 [rows][Hq] or None.  Returns the workspace to
+    pass to the next call: a new one where none is given or it is too small (attention_workspace() makes one)."""
+    return _attention(load().oscar_window_attention, (), kv, page_table, lens, q, out, num_kv_heads, window, sinks,
+                      q_lens, scale, lse, workspace, error, stream)
+
+
+def int4_attention(kv, page_table, lens, q, out, num_kv_heads: int, window: int = -1, sinks: int = 0, q_lens=None,
+                   group_size: int = 128, scale: float = 0.0, lse=None, workspace=None, error=None, stream=None):
+    """window_attention over a 4-bit pool, for at most 16 / (Hq / Hkv) query tokens a request."""
+    return _attention(load().oscar_int4_attention, (group_size,), kv, page_table, lens, q, out, num_kv_heads, window,
+                      sinks, q_lens, scale, lse, workspace, error, stream)

@@ -1,0 +1,912 @@
+// Attention of a few query rows per request over a paged cache, BF16 or 4-bit:
+// the decode form of the windowed attention, and speculative steps of a few
+// tokens.
+//
+//   o_r = sum_t p_rt v_t / sum_t p_rt,  p_rt = exp(scale q_r . k_t)
+// over the tokens t <= p_r that the row sees: t < sinks or t > p_r - window.  The
+// rows of one (request, kv head) -- its m query tokens times the G heads of the
+// group, up to 16 -- share one pass over the keys and values ("segment").
+//
+// Traffic bounds it (512 B per token and kv head in BF16, 136 or 144 B in 4 bits,
+// for 2 x 2 x 128 flops per row), so the split serves the copies alone.  One
+// persistent CTA per SM takes an equal contiguous share of all the segments'
+// visible units (16 tokens of a BF16 page, 32 of a 4-bit one; units that no row
+// sees are not in the list, and pages that hold none are never touched).  Each
+// warp streams its own units through its own TMA ring, the copies running on
+// across segment borders, and keeps a running (max, sum, o); a segment's warps
+// are folded in shared memory, its CTAs by the last of them to finish.
+//
+// Both contractions run on warp-level mma.sync m16n8k16 with tokens, then channels,
+// as the 16 rows: at 4 to 16 query rows the fixed 128-row tile of the tcgen05 MMA
+// would be mostly padding, and the products take a tenth of the copies' time.
+//  * BF16: q and v are bf16 already; p is carried as three bf16 parts (24 bits; two
+//    parts at 9 to 16 rows, where the third has no registers), so every product is
+//    exact in fp32.
+//  * 4 bits: a code c is or-ed into the fp16 number 1024 (or 1024 + 16 c) and one
+//    half2 fma makes it c - 8, exact and centred: sums of the positive codes
+//    themselves would lose the mean of many values to their common offset and to the
+//    matrix unit's one-sided truncation (2.4e-5 of the output at 30K tokens; codes
+//    used in place as fp16 subnormals, one operation less, lost the same to the
+//    unit's alignment).  q is exact in fp16 after scaling by a power of two (bf16 has
+//    8 bits); p s is carried as two fp16 parts (22 bits), scaled by a running power
+//    of two that keeps it inside fp16's range:
+//      logit = s (q . (c - 8)) + (z + 8 s) sum(q),
+//      sum p v = sum (p s) (c - 8) + sum p (z + 8 s).
+// The probabilities come out of the first product with a lane holding two tokens
+// of a row; movmatrix turns them into the second product's operand.
+#include "paged_device.cuh"
+
+namespace oscar {
+namespace {
+
+using namespace paged;
+
+template <int GK>
+struct Format {
+  static constexpr int UT = GK == 0 ? 16 : 32;                                    // tokens per unit
+  static constexpr int META = GK == 0 ? 0 : UT * i4_meta_row(GK == 0 ? D : GK);   // bytes of {s, z} of K (or V)
+  static constexpr int BYTES = GK == 0 ? UT * 4 * D : 2 * UT * I4_ROW + 2 * META; // bytes of one unit
+};
+// where a staged 4-bit unit has its parts
+constexpr int U4_V = 32 * I4_ROW, U4_META = 2 * U4_V;
+
+template <int GK, int NR>
+struct DecodeShape {
+  // Warps: the BF16 unit is a few instructions for 8 KB, so eight warps keep the
+  // copies going; the 4-bit unit is bound by its instructions' latency, so as many
+  // warps as the registers allow.
+  static constexpr int NW = GK == 0 ? 8 : NR == 4 ? 16 : NR == 8 ? 12 : 8;
+  static constexpr int THREADS = 32 * NW;
+  static constexpr size_t LIMIT = 232448 - 1024;   // shared memory of a CTA, less the alignment
+  static constexpr size_t FIXED = sizeof(float) * NW * NR * PARTIAL_FLOATS + 1024;
+  static constexpr int FIT = static_cast<int>((LIMIT - FIXED) / (NW * Format<GK>::BYTES));
+  static constexpr int STAGES = FIT > 3 ? 3 : FIT;
+  static_assert(STAGES >= 2, "a ring needs two stages");
+};
+
+template <int GK, int NR>
+struct alignas(1024) DecodeSmem {
+  static constexpr int STAGES = DecodeShape<GK, NR>::STAGES, NW = DecodeShape<GK, NR>::NW;
+  alignas(1024) uint8_t ring[NW][STAGES][Format<GK>::BYTES];
+  alignas(16) float state[NW][NR][PARTIAL_FLOATS];
+  uint64_t full[NW][STAGES];
+  int last;
+};
+
+struct DecodeArgs {
+  PagedView p;
+  AttnArgs a;
+  int n, m, G, ncta;
+  int32_t total;                            // units of the call
+  float* partials;
+  int32_t* counters;
+  int32_t len[PAGED_MAX_REQ];
+  int32_t row[PAGED_MAX_REQ];
+  int32_t table[PAGED_MAX_REQ];
+  int32_t ustart[PAGED_MAX_REQ + 1];        // units before request i (all its kv heads)
+};
+
+// The visible units of a request: [0, sink) and [first, first + units - sink).  An
+// empty list still counts as one unit, so that some CTA writes the zero rows.
+struct Units {
+  int sink, first, units;
+  __host__ __device__ static Units of(int len, int m, int window, int sinks, int ut) {
+    const int64_t lo64 = (int64_t)len - m - window + 1;
+    const int lo = lo64 > 0 ? static_cast<int>(lo64) : 0;
+    Units u;
+    u.sink = ((sinks < len ? sinks : len) + ut - 1) / ut;
+    const int end = (len + ut - 1) / ut;
+    u.first = lo / ut > u.sink ? lo / ut : u.sink;
+    // window 0: only the sinks are seen
+    u.units = u.sink + (window > 0 && end > u.first ? end - u.first : 0);
+    return u;
+  }
+  __host__ __device__ int unit(int v) const { return v < sink ? v : first + (v - sink); }
+};
+
+// Position of a CTA's walk over the units u of the call.
+struct Cursor {
+  int req, head, base, seg_end;   // current segment: units [base, seg_end)
+  Units un;
+};
+template <int UT>
+__device__ __forceinline__ void cursor_load(const DecodeArgs& A, Cursor& c) {
+  c.un = Units::of(A.len[c.req], A.m, A.a.window, A.a.sinks, UT);
+  c.seg_end = c.base + max(c.un.units, 1);
+}
+template <int UT>
+__device__ __forceinline__ void cursor_first(const DecodeArgs& A, Cursor& c, int u) {
+  int lo = 0, hi = A.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (A.ustart[mid] <= u) lo = mid; else hi = mid;
+  }
+  c.req = lo;
+  c.base = A.ustart[lo];
+  cursor_load<UT>(A, c);
+  const int per = c.seg_end - c.base;
+  c.head = (u - c.base) / per;
+  c.base += c.head * per;
+  c.seg_end = c.base + per;
+}
+template <int UT>
+__device__ __forceinline__ void cursor_next(const DecodeArgs& A, Cursor& c) {
+  const int per = c.seg_end - c.base;
+  c.base = c.seg_end;
+  if (++c.head == A.p.Hkv) {
+    c.head = 0;
+    ++c.req;
+    if (c.req < A.n) cursor_load<UT>(A, c);
+  } else {
+    c.seg_end = c.base + per;
+  }
+}
+
+// Columns of the products.  Up to 4 rows: column 2 r is row r's first part and
+// 2 r + 1 its second, in one tile (the first product holds the row in both); a
+// third part takes the even columns of a second tile.  More rows: column n of
+// tile j is row 8 j + n, and the second product has a tile for each part.
+template <int GK, int NR>
+struct Cols {
+  static constexpr bool DUP = NR <= 4;
+  static constexpr int PARTS = GK == 0 && NR <= 8 ? 3 : 2;
+  static constexpr int QT = DUP ? 1 : NR / 8;        // tiles of the first product
+  static constexpr int PT = DUP ? PARTS - 1 : PARTS * QT;   // tiles of the second
+  static constexpr int HPL = DUP ? 1 : 2;            // rows of a tile that a lane holds
+  static constexpr int H = QT * HPL;                 // rows that a lane holds
+  // row of the lane's h-th
+  __device__ static int row(int h, int tid) { return DUP ? tid : 8 * (h / 2) + 2 * tid + (h & 1); }
+};
+
+template <int GK, int NR>
+struct State {
+  using C = Cols<GK, NR>;
+  static constexpr int NG = GK == 64 ? 2 : 1;
+  float o[C::PT][8][4];
+  float m[C::H], l[C::H];
+  float z[NG][C::H];      // sum p z (4 bits)
+  int e[NG];              // p s is scaled by 2^(6 - e)
+  __device__ void reset() {
+#pragma unroll
+    for (int i = 0; i < C::PT; ++i)
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][t][k] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < C::H; ++h) {
+      m[h] = NEG_INF;
+      l[h] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) z[g][h] = 0.0f;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) e[g] = -24;
+  }
+  // scale row h's accumulators
+  __device__ void rescale(int h, float f) {
+    l[h] *= f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) z[g][h] *= f;
+    if constexpr (C::DUP) {
+#pragma unroll
+      for (int i = 0; i < C::PT; ++i)
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][t][k] *= f;
+    } else {
+#pragma unroll
+      for (int part = 0; part < C::PARTS; ++part)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          o[C::PARTS * (h / 2) + part][t][h & 1] *= f;
+          o[C::PARTS * (h / 2) + part][t][2 + (h & 1)] *= f;
+        }
+    }
+  }
+  // new maximum of row h over the whole warp's tokens
+  __device__ void raise(int h, float pm) {
+    pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 4));
+    pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 8));
+    pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 16));
+    if (pm > m[h] + LAZY_MAX || (m[h] == NEG_INF && pm > NEG_INF)) {
+      rescale(h, m[h] == NEG_INF ? 0.0f : ex2f(m[h] - pm));
+      m[h] = pm;
+    }
+  }
+};
+
+// Whether the row at position pos sees token t.
+__device__ __forceinline__ bool sees(const AttnArgs& a, int pos, int t) {
+  return t <= pos && (t < a.sinks || (int64_t)t > (int64_t)pos - a.window);
+}
+
+// q as the first product's B operand: column n (= lane / 4), registers of k-step s.
+template <int GK, int NR>
+struct Query {
+  using C = Cols<GK, NR>;
+  uint32_t b[C::QT][8][2];
+  float scale[C::H];        // softmax scale (x q's power of two in 4 bits) of the lane's rows
+  float qsum[GK == 64 ? 2 : 1][C::H];   // 4 bits: sum of q over the group, x softmax scale
+  int pos[C::H];
+};
+
+__device__ __forceinline__ const uint16_t* q_row(const DecodeArgs& A, int req, int head, int r) {
+  return A.a.q + (int64_t)(A.row[req] + r / A.G) * A.a.q_stride + (int64_t)(head * A.G + r % A.G) * D;
+}
+
+template <int GK, int NR>
+__device__ __forceinline__ void load_query(const DecodeArgs& A, int req, int head, Query<GK, NR>& Q) {
+  using C = Cols<GK, NR>;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const int R = A.m * A.G, len = A.len[req];
+#pragma unroll
+  for (int h = 0; h < C::H; ++h) {
+    const int r = min(C::row(h, tid), R - 1);
+    Q.pos[h] = len - A.m + r / A.G;
+    Q.scale[h] = A.a.scale2;
+  }
+#pragma unroll
+  for (int j = 0; j < C::QT; ++j) {
+    const int r = C::DUP ? gid >> 1 : 8 * j + gid;
+    const uint16_t* q = q_row(A, req, head, r < R ? r : 0);
+    if constexpr (GK == 0) {
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const uint32_t x0 = __ldg(reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * tid));
+        const uint32_t x1 = __ldg(reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * tid + 8));
+        Q.b[j][s][0] = r < R ? x0 : 0u;
+        Q.b[j][s][1] = r < R ? x1 : 0u;
+      }
+    } else {
+      // the lane's 32 channels (those of its share of a code row), scaled so that the
+      // row's largest |q| lies in [2^13, 2^14): exact in fp16 down to 2^-27 of it
+      float f[32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ch = GK == 128 ? 32 * tid + 8 * i : 64 * (i / 2) + 16 * tid + 8 * (i % 2);
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(q + ch));
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[8 * i + 2 * k] = __uint_as_float(ww[k] << 16);
+          f[8 * i + 2 * k + 1] = __uint_as_float(ww[k] & 0xffff0000u);
+        }
+      }
+      float mx = 0.0f, sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        mx = fmaxf(mx, fabsf(f[c]));
+        sum[GK == 64 ? c / 16 : 0] += f[c];
+      }
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
+        if (GK == 64) sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], off);
+      }
+      // exponent of the largest, from its bits; clamped so that both powers of two are normal
+      int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
+      ex = max(-112, min(ex, 112));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - ex) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          const float* x = f + 8 * i + 2 * sub;   // codes 2 sub, 2 sub + 1 of the word and those 4 behind
+          Q.b[j][2 * i + sub][0] = r < R ? f16x2(x[0] * up, x[4] * up) : 0u;
+          Q.b[j][2 * i + sub][1] = r < R ? f16x2(x[1] * up, x[5] * up) : 0u;
+        }
+      // column n's scale and sums to the lanes that hold its row: lane 4 n of the
+      // column's group has them
+      const float down = __uint_as_float(static_cast<uint32_t>(127 + ex - 13) << 23) * A.a.scale2;
+#pragma unroll
+      for (int k = 0; k < C::HPL; ++k) {
+        const int h = C::HPL * j + k, src = C::DUP ? 8 * tid : 4 * (2 * tid + k);
+        Q.scale[h] = __shfl_sync(0xffffffffu, down, src);
+        Q.qsum[0][h] = __shfl_sync(0xffffffffu, sum[0], src) * A.a.scale2;
+        if (GK == 64) Q.qsum[GK == 64][h] = __shfl_sync(0xffffffffu, sum[1], src) * A.a.scale2;
+      }
+    }
+  }
+}
+
+// B operand of the second product from the weights of the lane's rows: w0[h] and
+// w1[h] for tokens gid and gid + 8 of a 16-token tile.  hi rounds to the part's type.
+template <int GK, int NR, typename Hi, typename Pack>
+__device__ __forceinline__ void weights(const float (&w0)[Cols<GK, NR>::H], const float (&w1)[Cols<GK, NR>::H],
+                                        uint32_t (&b)[Cols<GK, NR>::PT][2], Hi hi, Pack pack) {
+  using C = Cols<GK, NR>;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float (&w)[C::H] = u ? w1 : w0;
+    if constexpr (C::DUP) {
+      const float h = hi(w[0]), l = w[0] - h;
+      b[0][u] = movmatrix(pack(h, l));
+      if constexpr (C::PARTS == 3) b[1][u] = movmatrix(pack(l - hi(l), 0.0f));
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::QT; ++j) {
+        float a = w[2 * j], c = w[2 * j + 1];
+#pragma unroll
+        for (int part = 0; part < C::PARTS; ++part) {
+          b[C::PARTS * j + part][u] = movmatrix(pack(a, c));
+          a -= hi(a);
+          c -= hi(c);
+        }
+      }
+    }
+  }
+}
+
+// One unit of 16 BF16 tokens from t0: stage = two halves of 64 channels, each K
+// [16][128 B] and V [16][128 B], 16-byte pieces swizzled within 8 rows by the TMA.
+template <int NR>
+__device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR>& Q, State<0, NR>& S, uint8_t* stage,
+                                          int t0, bool masked) {
+  using C = Cols<0, NR>;
+  const int lane = threadIdx.x & 31, gid = lane >> 2;
+  if (masked) {
+    // value rows that no row of the segment sees may hold anything: zero them
+    const int row = lane & 15, p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);   // the first query token
+    bool any = false;
+    for (int k = 0; k < A.m; ++k) any = any || sees(A.a, p0 + k, t0 + row);
+    if (!any) {
+      uint4* v = reinterpret_cast<uint4*>(stage + (lane >> 4) * 4096 + 2048 + row * 128);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+    __syncwarp();
+  }
+  const uint32_t base = smem_u32(stage);
+  float s[C::QT][4];
+#pragma unroll
+  for (int j = 0; j < C::QT; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[j][k] = 0.0f;
+  const int krow = lane & 15, kc = lane >> 4;
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    uint32_t af[4];
+    ldsm4(af, base + (ks >> 2) * 4096 + krow * 128 + (((2 * (ks & 3) + kc) ^ (krow & 7)) << 4));
+#pragma unroll
+    for (int j = 0; j < C::QT; ++j) mma_bf16(s[j], af, Q.b[j][ks][0], Q.b[j][ks][1]);
+  }
+  float x0[C::H], x1[C::H];
+#pragma unroll
+  for (int h = 0; h < C::H; ++h) {
+    x0[h] = s[h / C::HPL][h % C::HPL] * Q.scale[h];
+    x1[h] = s[h / C::HPL][2 + h % C::HPL] * Q.scale[h];
+    if (masked) {
+      if (!sees(A.a, Q.pos[h], t0 + gid)) x0[h] = NEG_INF;
+      if (!sees(A.a, Q.pos[h], t0 + gid + 8)) x1[h] = NEG_INF;
+    }
+    S.raise(h, fmaxf(x0[h], x1[h]));
+    const float ref = S.m[h] == NEG_INF ? 0.0f : S.m[h];
+    x0[h] = ex2f(x0[h] - ref);
+    x1[h] = ex2f(x1[h] - ref);
+    S.l[h] += x0[h] + x1[h];
+  }
+  uint32_t b[C::PT][2];
+  weights<0, NR>(x0, x1, b, bf16_hi, bf16x2);
+  const int vrow = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    uint32_t af[4];
+    ldsm4_t(af, base + (mt >> 2) * 4096 + 2048 + vrow * 128 + (((2 * (mt & 3) + vc) ^ (vrow & 7)) << 4));
+#pragma unroll
+    for (int j = 0; j < C::PT; ++j) mma_bf16(S.o[j][mt], af, b[j][0], b[j][1]);
+  }
+}
+
+// Codes (bits 0-3 and 16-19, or 4-7 and 20-23, of w) as a pair of fp16 numbers c - 8.
+__device__ __forceinline__ uint32_t code_lo(uint32_t w) {
+  uint32_t x = (w & 0x000F000Fu) | 0x64006400u;   // 1024 + c
+  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE408E408u));   // - 1032
+  return x;
+}
+__device__ __forceinline__ uint32_t code_hi(uint32_t w) {
+  uint32_t x = (w & 0x00F000F0u) | 0x64006400u;   // 1024 + 16 c
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(x) : "r"(0x2C002C00u), "r"(0xD480D480u));   // / 16 - 72
+  return x;
+}
+
+// One 4-bit unit (32 tokens from t0): K codes [32][64 B], V codes, K meta, V meta as
+// in the record.  Row r of a 16-token tile is token r ^ ((r >> 1) & 1), which spreads
+// both products' reads over the banks.
+template <int GK, int NR>
+__device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, NR>& Q, State<GK, NR>& S,
+                                          const uint8_t* stage, int t0, bool masked) {
+  using C = Cols<GK, NR>;
+  constexpr int NG = State<GK, NR>::NG, TILES = Format<GK>::UT / 16, MROW = i4_meta_row(GK);
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+  const int tok = gid ^ ((gid >> 1) & 1);
+  // ---- logits of the unit
+  float x[TILES][2][C::H];
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    float s[C::QT][2][4];
+#pragma unroll
+    for (int j = 0; j < C::QT; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[j][0][k] = s[j][1][k] = 0.0f;
+    uint32_t w[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* row = stage + (16 * t + 8 * u + tok) * I4_ROW;
+      if constexpr (GK == 128) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * tid);
+        w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+      } else {
+        // half of the rows read the second group first: no bank conflicts
+        const int first = (gid >> 1) & 1;
+        const uint2 va = *reinterpret_cast<const uint2*>(row + 32 * first + 8 * tid);
+        const uint2 vb = *reinterpret_cast<const uint2*>(row + 32 * (first ^ 1) + 8 * tid);
+        w[u][0] = first ? vb.x : va.x, w[u][1] = first ? vb.y : va.y;
+        w[u][2] = first ? va.x : vb.x, w[u][3] = first ? va.y : vb.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {   // the two accumulators (groups, at 64) in turn
+          const int word = 2 * g + i;
+          const uint32_t wa = w[0][word] >> (8 * sub), wb = w[1][word] >> (8 * sub);
+          const uint32_t a0 = code_lo(wa), a1 = code_lo(wb), a2 = code_hi(wa), a3 = code_hi(wb);
+#pragma unroll
+          for (int j = 0; j < C::QT; ++j)
+            mma_f16(s[j][g], a0, a1, a2, a3, Q.b[j][2 * word + sub][0], Q.b[j][2 * word + sub][1]);
+        }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int slot = 16 * t + 8 * u + tok;
+      float sk[2], zk[2];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const __half2 m = *reinterpret_cast<const __half2*>(stage + U4_META + MROW * slot + 4 * g);
+        sk[g] = __low2float(m);
+        zk[g] = fmaf(8.0f, sk[g], __high2float(m));
+      }
+#pragma unroll
+      for (int h = 0; h < C::H; ++h) {
+        const int j = h / C::HPL, k = 2 * u + h % C::HPL;
+        float y;
+        if constexpr (NG == 1)
+          y = fmaf(sk[0], (s[j][0][k] + s[j][1][k]) * Q.scale[h], zk[0] * Q.qsum[0][h]);
+        else
+          y = fmaf(sk[0], s[j][0][k] * Q.scale[h], zk[0] * Q.qsum[0][h]) +
+              fmaf(sk[1], s[j][1][k] * Q.scale[h], zk[1] * Q.qsum[1][h]);
+        if (masked && !sees(A.a, Q.pos[h], t0 + slot)) y = NEG_INF;
+        x[t][u][h] = y;
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < C::H; ++h) {
+    float pm = NEG_INF;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) pm = fmaxf(pm, fmaxf(x[t][0][h], x[t][1][h]));
+    S.raise(h, pm);
+    const float ref = S.m[h] == NEG_INF ? 0.0f : S.m[h];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        x[t][u][h] = ex2f(x[t][u][h] - ref);
+        S.l[h] += x[t][u][h];
+      }
+  }
+  // ---- the value scales' power of two: their largest in the unit
+  const uint8_t* vmeta = stage + U4_META + Format<GK>::META;
+  float mult[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    uint32_t big = *reinterpret_cast<const uint16_t*>(vmeta + MROW * lane + 4 * g) & 0x7fffu;
+    if (masked) {   // a token that no row sees may hold anything
+      bool any = false;
+      const int p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);
+      for (int q = 0; q < A.m; ++q) any = any || sees(A.a, p0 + q, t0 + lane);
+      if (!any) big = 0;
+    }
+    big = __reduce_max_sync(0xffffffffu, big);
+    // s < 2^e: normal numbers have e = (bits >> 10) - 14, subnormal ones e <= -14
+    const int e = max(S.e[g], big >= 0x400u ? static_cast<int>(big >> 10) - 14 : (big ? -14 : -24));
+    if (e > S.e[g]) {
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + S.e[g] - e) << 23);
+#pragma unroll
+      for (int j = 0; j < C::PT; ++j)
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt)
+          if (NG == 1 || mt / 4 == g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) S.o[j][mt][k] *= f;
+      S.e[g] = e;
+    }
+    mult[g] = __uint_as_float(static_cast<uint32_t>(127 + 6 - e) << 23);
+  }
+  // ---- values
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    uint32_t b[NG][C::PT][2];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float w0[C::H], w1[C::H];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int slot = 16 * t + 8 * u + tok;
+        const __half2 m = *reinterpret_cast<const __half2*>(vmeta + MROW * slot + 4 * g);
+        const float sv = __low2float(m) * mult[g], zv = fmaf(8.0f, __low2float(m), __high2float(m));
+#pragma unroll
+        for (int h = 0; h < C::H; ++h) {
+          const float pr = x[t][u][h];
+          const bool dead = masked && pr == 0.0f;   // its scale and zero may be anything
+          (u ? w1[h] : w0[h]) = dead ? 0.0f : pr * sv;
+          S.z[g][h] = dead ? S.z[g][h] : fmaf(pr, zv, S.z[g][h]);
+        }
+      }
+      weights<GK, NR>(w0, w1, b[g], f16_hi, f16x2);
+    }
+    // the lane's four tokens of the tile: rows 2 tid, 2 tid + 1, + 8; two words of 8 channels of each
+    uint32_t v[4][2];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = 2 * tid + (q & 1) + 8 * (q >> 1);
+      const uint8_t* row = stage + U4_V + (16 * t + (r ^ ((r >> 1) & 1))) * I4_ROW;
+      const int first = tid >> 1;   // half of the lanes read the second word first: no bank conflicts
+      const uint32_t va = *reinterpret_cast<const uint32_t*>(row + 32 * first + 4 * gid);
+      const uint32_t vb = *reinterpret_cast<const uint32_t*>(row + 32 * (first ^ 1) + 4 * gid);
+      v[q][0] = first ? vb : va;
+      v[q][1] = first ? va : vb;
+    }
+#pragma unroll
+    for (int word = 0; word < 2; ++word)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t sel = half ? 0x7632u : 0x5410u;
+        const uint32_t pa = __byte_perm(v[0][word], v[1][word], sel), pb = __byte_perm(v[2][word], v[3][word], sel);
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          const uint32_t qa = pa >> (8 * sub), qb = pb >> (8 * sub);
+          const uint32_t a0 = code_lo(qa), a1 = code_hi(qa), a2 = code_lo(qb), a3 = code_hi(qb);
+          const int mt = 4 * word + 2 * half + sub;
+#pragma unroll
+          for (int j = 0; j < C::PT; ++j)
+            mma_f16(S.o[j][mt], a0, a1, a2, a3, b[NG == 1 ? 0 : word][j][0], b[NG == 1 ? 0 : word][j][1]);
+        }
+      }
+  }
+}
+
+// This warp's state into shared memory: o in channel order, m, l.
+template <int GK, int NR>
+__device__ __forceinline__ void put_state(const State<GK, NR>& S, float (*st)[PARTIAL_FLOATS]) {
+  using C = Cols<GK, NR>;
+  constexpr int NG = State<GK, NR>::NG;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+#pragma unroll
+  for (int h = 0; h < C::H; ++h) {
+    float l = S.l[h], z[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) z[g] = S.z[g][h];
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) z[g] += __shfl_xor_sync(0xffffffffu, z[g], off);
+    }
+    const int r = C::row(h, tid);
+    if (r >= NR) continue;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      float a, b;
+      if constexpr (C::DUP) {
+        a = S.o[0][mt][0] + S.o[0][mt][1];
+        b = S.o[0][mt][2] + S.o[0][mt][3];
+        if constexpr (C::PARTS == 3) {
+          a += S.o[1][mt][0];
+          b += S.o[1][mt][2];
+        }
+      } else {
+        const int j = C::PARTS * (h / 2), k = h & 1;
+        a = S.o[j][mt][k];
+        b = S.o[j][mt][2 + k];
+#pragma unroll
+        for (int part = 1; part < C::PARTS; ++part) {
+          a += S.o[j + part][mt][k];
+          b += S.o[j + part][mt][2 + k];
+        }
+      }
+      if constexpr (GK == 0) {
+        st[r][16 * mt + gid] = a;
+        st[r][16 * mt + gid + 8] = b;
+      } else {
+        const int g = NG == 1 ? 0 : mt / 4;
+        const float back = __uint_as_float(static_cast<uint32_t>(127 + S.e[g] - 6) << 23);
+        const int ch = 64 * (mt / 4) + 8 * gid + 2 * (mt % 4);
+        st[r][ch] = fmaf(a, back, z[g]);
+        st[r][ch + 1] = fmaf(b, back, z[g]);
+      }
+    }
+    if (gid == 0) {
+      st[r][PARTIAL_M] = S.m[h];
+      st[r][PARTIAL_L] = l;
+    }
+  }
+}
+
+__device__ __forceinline__ void write_row(const DecodeArgs& A, int req, int head, int r, int lane, float4 o, float m,
+                                          float l) {
+  const size_t row = (size_t)(A.row[req] + r / A.G) * A.a.Hq + (size_t)head * A.G + r % A.G;
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+  if (A.a.f32) {
+    reinterpret_cast<float4*>(static_cast<float*>(A.a.out) + row * D)[lane] = o;
+  } else {
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.a.out) + row * D)[lane] =
+        make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+  }
+  if (A.a.lse && lane == 0) A.a.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : NEG_INF;
+}
+
+// Fold count states of one row, the warp's lanes holding 4 channels each.
+template <typename P>
+__device__ __forceinline__ void fold(int count, P at, int lane, float4& o, float& m, float& l) {
+  m = NEG_INF;
+  for (int c = lane; c < count; c += 32) m = fmaxf(m, __ldcg(at(c) + PARTIAL_M));
+#pragma unroll
+  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  l = 0.0f;
+  if (m == NEG_INF) return;
+  constexpr int U = 8;
+  for (int c0 = 0; c0 < count; c0 += U) {
+    float4 v[U];
+    float mv[U], lv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float* p = at(min(c0 + u, count - 1));
+      v[u] = __ldcg(reinterpret_cast<const float4*>(p) + lane);
+      mv[u] = __ldcg(p + PARTIAL_M);
+      lv[u] = __ldcg(p + PARTIAL_L);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = c0 + u < count ? ex2f(mv[u] - m) : 0.0f;
+      if (f == 0.0f) continue;
+      l = fmaf(lv[u], f, l);
+      o.x = fmaf(v[u].x, f, o.x);
+      o.y = fmaf(v[u].y, f, o.y);
+      o.z = fmaf(v[u].z, f, o.z);
+      o.w = fmaf(v[u].w, f, o.w);
+    }
+  }
+}
+
+template <int GK, int NR>
+__global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
+    paged_decode_kernel(const __grid_constant__ DecodeArgs A, const __grid_constant__ CUtensorMap map) {
+  using F = Format<GK>;
+  using SM = DecodeSmem<GK, NR>;
+  constexpr int UT = F::UT, STAGES = SM::STAGES, NW = SM::NW;
+  extern __shared__ uint8_t dec_raw[];
+  SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(dec_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  const int u0 = static_cast<int>((int64_t)A.total * cta / A.ncta);
+  const int u1 = static_cast<int>((int64_t)A.total * (cta + 1) / A.ncta);
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(&sm.full[warp][s], 1);
+    mbar_init_fence();
+  }
+  __syncwarp();
+
+  // ---- the warp's copies: units u0 + warp, + NW, ... of the CTA's range
+  Cursor pc;
+  int pu = u0 + warp;
+  if (pu < u1) cursor_first<UT>(A, pc, pu);
+  int issued = 0;
+  bool dead = false;   // a wait gave up: no further copies
+  auto issue = [&]() {
+    if (pu >= u1 || dead) return;
+    while (pu >= pc.seg_end) cursor_next<UT>(A, pc);
+    const int v = pu - pc.base;
+    const int st = issued % STAGES;
+    if (v < pc.un.units) {
+      const int t0 = pc.un.unit(v) * UT;
+      int32_t page = __ldg(A.p.table + (size_t)A.table[pc.req] * A.p.max_pages + t0 / PAGE);
+      if (page < 0 || page >= A.p.num_pages) {
+        if (lane == 0 && A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
+        page = 0;
+      }
+      const int64_t rec = (int64_t)page * A.p.Hkv + pc.head;
+      if (lane == 0) {
+        uint8_t* dst = sm.ring[warp][st];
+        mbar_expect_tx(&sm.full[warp][st], F::BYTES);
+        if constexpr (GK == 0) {
+          tma_load_3d(dst, &map, 0, t0 % PAGE, static_cast<int>(2 * rec), &sm.full[warp][st]);
+          tma_load_3d(dst + F::BYTES / 2, &map, 64, t0 % PAGE, static_cast<int>(2 * rec), &sm.full[warp][st]);
+        } else {
+          const uint8_t* src = static_cast<const uint8_t*>(A.p.pool) + rec * i4_record(GK);
+          const int r0 = t0 % PAGE;
+          tma_load_1d(dst, src + r0 * I4_ROW, U4_V, &sm.full[warp][st]);
+          tma_load_1d(dst + U4_V, src + I4_V_CODES + r0 * I4_ROW, U4_V, &sm.full[warp][st]);
+          tma_load_1d(dst + U4_META, src + I4_META + r0 * i4_meta_row(GK), F::META, &sm.full[warp][st]);
+          tma_load_1d(dst + U4_META + F::META, src + i4_v_meta(GK) + r0 * i4_meta_row(GK), F::META, &sm.full[warp][st]);
+        }
+      }
+    } else if (lane == 0) {
+      mbar_arrive(&sm.full[warp][st]);   // nothing to copy
+    }
+    ++issued;
+    pu += NW;
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) issue();
+
+  Cursor cc;
+  int cu = u0 + warp, taken = 0;
+  if (u0 < u1) cursor_first<UT>(A, cc, u0);
+  State<GK, NR> S;
+  Query<GK, NR> Q;
+  const int R = A.m * A.G;
+  for (int seg_u = u0; seg_u < u1;) {
+    const int seg_end = min(cc.seg_end, u1);
+    load_query<GK, NR>(A, cc.req, cc.head, Q);
+    S.reset();
+    const int len = A.len[cc.req];
+    for (; cu < seg_end; cu += NW) {
+      const int v = cu - cc.base, st = taken % STAGES;
+      if (!dead && !mbar_wait(&sm.full[warp][st], (taken / STAGES) & 1)) {
+        if (lane == 0 && A.p.err) atomicOr(A.p.err, PAGED_ERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      if (!dead && v < cc.un.units) {
+        const int t0 = cc.un.unit(v) * UT;
+        const bool masked = !(t0 + UT - 1 <= len - A.m &&
+                              (t0 + UT <= A.a.sinks || (int64_t)t0 > (int64_t)len - 1 - A.a.window));
+        if constexpr (GK == 0)
+          bf16_unit<NR>(A, Q, S, sm.ring[warp][st], t0, masked);
+        else
+          int4_unit<GK, NR>(A, Q, S, sm.ring[warp][st], t0, masked);
+      }
+      __syncwarp();
+      ++taken;
+      issue();
+    }
+    // ---- the CTA's share of the segment
+    put_state<GK, NR>(S, sm.state[warp]);
+    __syncthreads();
+    const int full_units = cc.seg_end - cc.base;
+    const int seg = cc.req * A.p.Hkv + cc.head;
+    const int c_lo = static_cast<int>((((int64_t)cc.base + 1) * A.ncta - 1) / A.total);
+    const int c_hi = static_cast<int>(((int64_t)cc.seg_end * A.ncta - 1) / A.total);
+    const bool whole = seg_end - seg_u == full_units;
+    float* rec = A.partials + (size_t)(seg + cta) * NR * PARTIAL_FLOATS;
+    for (int r = warp; r < R; r += NW) {
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float m = NEG_INF, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, sm.state[w][r][PARTIAL_M]);
+      if (m != NEG_INF) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float f = ex2f(sm.state[w][r][PARTIAL_M] - m);
+          if (f == 0.0f) continue;
+          const float4 x = reinterpret_cast<const float4*>(sm.state[w][r])[lane];
+          l = fmaf(sm.state[w][r][PARTIAL_L], f, l);
+          o.x = fmaf(x.x, f, o.x);
+          o.y = fmaf(x.y, f, o.y);
+          o.z = fmaf(x.z, f, o.z);
+          o.w = fmaf(x.w, f, o.w);
+        }
+      }
+      if (whole) {
+        write_row(A, cc.req, cc.head, r, lane, o, m, l);
+      } else {
+        reinterpret_cast<float4*>(rec + r * PARTIAL_FLOATS)[lane] = o;
+        if (lane == 0) {
+          rec[r * PARTIAL_FLOATS + PARTIAL_M] = m;
+          rec[r * PARTIAL_FLOATS + PARTIAL_L] = l;
+        }
+      }
+    }
+    if (!whole) {
+      // the last CTA of the segment to get here folds its records
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) sm.last = atomicAdd(A.counters + seg, 1) == c_hi - c_lo;
+      __syncthreads();
+      if (sm.last) {
+        __threadfence();
+        const float* first = A.partials + (size_t)(seg + c_lo) * NR * PARTIAL_FLOATS;
+        for (int r = warp; r < R; r += NW) {
+          float4 o;
+          float m, l;
+          fold(c_hi - c_lo + 1,
+               [&](int c) { return first + ((size_t)c * NR + r) * PARTIAL_FLOATS; }, lane, o, m, l);
+          write_row(A, cc.req, cc.head, r, lane, o, m, l);
+        }
+        if (threadIdx.x == 0) A.counters[seg] = 0;
+      }
+    }
+    __syncthreads();   // the states and the flag are free
+    seg_u = seg_end;
+    if (seg_u < u1) cursor_next<UT>(A, cc);
+  }
+  // a warp that gave up leaves no copy in flight behind (bounded again)
+  if (dead)
+    for (; taken < issued; ++taken) mbar_wait(&sm.full[warp][taken % STAGES], (taken / STAGES) & 1);
+}
+
+template <int GK, int NR>
+cudaError_t launch_decode_t(DecodeArgs& A, const CUtensorMap& map, int sms, cudaStream_t s) {
+  constexpr int bytes = static_cast<int>(sizeof(DecodeSmem<GK, NR>)) + 1024;
+  static unsigned done = 0;   // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 32 || !(done & (1u << dev))) {
+    e = cudaFuncSetAttribute(paged_decode_kernel<GK, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 32) done |= 1u << dev;
+  }
+  // one CTA per SM, fewer where a CTA's warps would have no unit each
+  constexpr int NW = DecodeShape<GK, NR>::NW;
+  const int most = (A.total - 1) / NW + 1, ctas = most < sms ? most : sms;
+  A.ncta = ctas;
+  paged_decode_kernel<GK, NR><<<ctas, DecodeShape<GK, NR>::THREADS, bytes, s>>>(A, map);
+  return cudaGetLastError();
+}
+
+template <int GK>
+cudaError_t launch_decode_g(DecodeArgs& A, const CUtensorMap& map, int sms, cudaStream_t s) {
+  const int R = A.m * A.G;
+  if (R <= 4) return launch_decode_t<GK, 4>(A, map, sms, s);
+  if (R <= 8) return launch_decode_t<GK, 8>(A, map, sms, s);
+  return launch_decode_t<GK, 16>(A, map, sms, s);
+}
+
+int row_class(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+
+}  // namespace
+
+size_t paged_decode_record_bytes(int segments, int rows, int sms) {
+  return (size_t)(segments + sms) * row_class(rows) * PARTIAL_FLOATS * sizeof(float);
+}
+
+cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, int gk,
+                                void* workspace, const CUtensorMap* map, int sms, cudaStream_t s) {
+  DecodeArgs A;
+  A.p = p;
+  A.a = a;
+  A.n = n;
+  A.m = reqs[0].m;
+  A.G = a.Hq / p.Hkv;
+  A.counters = static_cast<int32_t*>(workspace);
+  A.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + PAGED_COUNTER_BYTES);
+  const int ut = gk == 0 ? Format<0>::UT : Format<128>::UT;
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    A.len[i] = reqs[i].len;
+    A.row[i] = reqs[i].row;
+    A.table[i] = reqs[i].table;
+    A.ustart[i] = static_cast<int32_t>(total);
+    const Units u = Units::of(reqs[i].len, A.m, a.window, a.sinks, ut);
+    total += (int64_t)p.Hkv * (u.units > 0 ? u.units : 1);
+    if (total > INT32_MAX) return cudaErrorInvalidValue;
+  }
+  A.ustart[n] = static_cast<int32_t>(total);
+  A.total = static_cast<int32_t>(total);
+  static const CUtensorMap none = {};
+  const CUtensorMap& m = map ? *map : none;
+  if (gk == 0) return launch_decode_g<0>(A, m, sms, s);
+  if (gk == 128) return launch_decode_g<128>(A, m, sms, s);
+  return launch_decode_g<64>(A, m, sms, s);
+}
+
+}  // namespace oscar

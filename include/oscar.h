@@ -316,6 +316,110 @@ oscar_status oscar_bf16_decode(const void* kv, int64_t num_pages, const int32_t*
                                float scale, const void* q, float* out, void* workspace, size_t workspace_bytes,
                                void* stream);
 
+/* ---- Paged caches: position rotation, windowed attention, 4 bits ------------
+ * Operators on caller-owned page pools, without a cache handle.  Tokens of
+ * request i sit at position t in page page_table[i][t / 64], row t % 64.
+ *   BF16 pool  bf16 [num_pages][Hkv][2][64][128], as oscar_bf16_decode reads it.
+ *   4-bit pool [num_pages][Hkv][record]: K codes [64][64 B], V codes [64][64 B]
+ *              (channel 2j in the low, 2j + 1 in the high nibble of byte j), K
+ *              meta [64][128 / group]{fp16 s, fp16 z}, V meta the same: 8704
+ *              bytes at group 128, 9216 at group 64.  A code c stands for
+ *              s c + z, with s >= 0.
+ * Common arguments and rules:
+ *   page_table  device int32 [n][max_pages]; entries of pages that a call does
+ *               not touch are never read into an address.  Its row i belongs to
+ *               request i; 1 <= n <= 256.
+ *   lens, new_lens, q_lens, starts, counts  host int32 [n]; NULL new_lens or
+ *               q_lens: one token per request.  Rows of q, k, v and out are the
+ *               requests' tokens one after another (no padding); a request may
+ *               have none.
+ *   strides     elements from one token's heads to the next one's, a multiple of
+ *               8, at least heads x 128 (heads lie densely, so q, k and v can be
+ *               parts of one projection's output).  Pointers are 16-byte aligned.
+ *   error       device int32 or NULL: bit 1 is OR-ed in where a page id is out of
+ *               range (a store to it is dropped, a read sees page 0 in an
+ *               attention and zeros in oscar_int4_read), bit 2 where a bounded
+ *               device wait gave up.  The caller zeroes it.
+ * Calls are asynchronous on "stream", check every argument before the first
+ * launch, allocate nothing, and may be captured (the host arrays are read at
+ * capture).  The text of the last refusal on the calling thread is
+ * oscar_paged_last_error(). */
+typedef enum { OSCAR_F32 = 0, OSCAR_BF16 = 1 } oscar_type;
+
+/* Position rotation: over the pairs (i, j) of the first dim channels, j = i +
+ * dim / 2, or j = i + 1 for even i if interleaved,
+ *   y_i = x_i cos - x_j sin,  y_j = x_j cos + x_i sin,
+ * with cos and sin of the token's position; each product and sum is rounded to
+ * fp32, the result to bf16. */
+typedef struct {
+  const float* table;    /* device fp32 [length][dim]: dim / 2 cosines, then dim / 2 sines, of each position */
+  int32_t length;        /* positions in the table */
+  int32_t dim;           /* rotated channels: a multiple of 16, 16 to 128 */
+  int32_t interleaved;
+} oscar_rope;
+
+/* Rotate q and k by their positions and append k and v: request i's new_lens[i]
+ * tokens go to positions lens[i], lens[i] + 1, ...  k and v device bf16
+ * [rows][Hkv][128], q [rows][Hq][128] or NULL, q_out dense bf16 [rows][Hq][128]
+ * (may be q itself if q is dense).  rope NULL: no rotation (q is copied).  No two
+ * rows of a call may go to the same place.  Bytes of other tokens are left as
+ * they were.
+ * In 4 bits, per token, kv head and group of group_size (128 or 64) channels of
+ * the values that the BF16 cache would hold (saturated to +-65504, NaN as 0):
+ *   z = fp16(min), s = fp16((max - min) / 15),
+ *   code = clamp(round((x - z) / s), 0, 15), ties to even, 0 where s is 0,
+ * every step rounded to fp32, the conversions to nearest. */
+oscar_status oscar_bf16_append(void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,
+                               const int32_t* lens, const int32_t* new_lens, int32_t n, int32_t num_q_heads,
+                               int32_t num_kv_heads, const oscar_rope* rope, const uint16_t* q, int64_t q_stride,
+                               const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                               uint16_t* q_out, int32_t* error, void* stream);
+oscar_status oscar_int4_append(void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,
+                               const int32_t* lens, const int32_t* new_lens, int32_t n, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t group_size, const oscar_rope* rope, const uint16_t* q,
+                               int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                               int64_t v_stride, uint16_t* q_out, int32_t* error, void* stream);
+
+/* Values s c + z of the tokens [starts[i], starts[i] + counts[i]) of each request,
+ * k_out and v_out dense [rows][Hkv][128] of out_type: a 4-bit prefix for an
+ * attention of many queries, or for a move to BF16 pages. */
+oscar_status oscar_int4_read(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,
+                             const int32_t* starts, const int32_t* counts, int32_t n, int32_t num_kv_heads,
+                             int32_t group_size, void* k_out, void* v_out, int32_t out_type, int32_t* error,
+                             void* stream);
+
+/* Attention with a sliding window and sinks.  The queries of request i are its last
+ * q_lens[i] positions (0 <= q_lens[i] <= lens[i] <= 64 max_pages; lens counts the
+ * tokens in the cache, the queries' own among them).  The query at position p sees
+ * the tokens t <= p with t < sinks or t > p - window:
+ *   out = sum_t softmax_t(scale q . k_t) v_t,  lse = log sum_t exp(scale q . k_t),
+ * query head h against kv head h / (Hq / Hkv).
+ *   window  tokens, the query's own among them; negative: no bound.  Where a query
+ *           sees nothing (window 0, no sinks), out is 0 and lse -infinity.
+ *   scale   <= 0 selects 1 / sqrt(128).
+ *   q       device bf16 [rows][Hq][128]; out dense [rows][Hq][128] of out_type; lse
+ *           device fp32 [rows][Hq] or NULL.
+ *   workspace  device, >= oscar_attention_workspace_bytes() (whatever lens, window
+ *           and sinks), 256-byte aligned, zeroed once by the caller before its first
+ *           use; every call leaves it ready for the next, of any shape.  Calls that
+ *           share a workspace must not overlap on the GPU.
+ * Hq / Hkv in {1, 2, 4, 8}; n Hkv <= 16384.  Pages that no query sees are not
+ * touched.  Tokens that no query of a request sees may hold anything (NaN too);
+ * those that some see and others do not must hold finite values.  4 bits: at most
+ * 16 / (Hq / Hkv) query tokens a request; read a prefix back for more. */
+size_t oscar_attention_workspace_bytes(int32_t n, const int32_t* q_lens, int32_t num_q_heads, int32_t num_kv_heads);
+oscar_status oscar_window_attention(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,
+                                    const int32_t* lens, const int32_t* q_lens, int32_t n, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t window, int32_t sinks, float scale,
+                                    const uint16_t* q, int64_t q_stride, void* out, int32_t out_type, float* lse,
+                                    int32_t* error, void* workspace, size_t workspace_bytes, void* stream);
+oscar_status oscar_int4_attention(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,
+                                  const int32_t* lens, const int32_t* q_lens, int32_t n, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t group_size, int32_t window, int32_t sinks, float scale,
+                                  const uint16_t* q, int64_t q_stride, void* out, int32_t out_type, float* lse,
+                                  int32_t* error, void* workspace, size_t workspace_bytes, void* stream);
+const char* oscar_paged_last_error(void);
+
 #ifdef __cplusplus
 }
 #endif

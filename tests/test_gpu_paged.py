@@ -1,0 +1,462 @@
+"""Paged-cache operators against the float64 oracle: append with position rotation
+(bit for bit), the 4-bit cache, attention with a sliding window and sinks.
+
+Pools start as NaN bit patterns (BF16) or 0xFF bytes (4 bits: NaN scales), pages
+are shuffled, and the table entries of pages that no query sees are -1, so any
+read of what a call must not see shows as a NaN or in the error word.
+
+Tolerances of the attention, per output value, relative to sum p |v| (a weight's
+relative error multiplies p |v|; normalising doubles it).  A 4-bit value s c + z is
+summed in two parts, about the middle of its codes; without that care s c = x - z is at
+most |x| + |z|, so |x| + 2 |z| stands for |x|:
+  logit   each of 128 products is exact, their sum takes 8 steps of a fp32 matrix
+          accumulator, at most 2^-22 of the running magnitude each (truncated, and
+          aligned to the largest product): 8 2^-22 max |q| |k| scale; in 4 bits three
+          more roundings (scale, product, sum), counted by doubling;
+  weight  ex2 2^-22, and p's parts: two bf16 parts leave 2^-17, two fp16 parts
+          2^-21; one bf16 part (long bf16 outputs) leaves 2^-8;
+  sums    one rounding of 2^-22 per 16 tokens of a warp's share, 64 to fold.
+A bf16 output adds 2^-8 of itself.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import paged
+
+torch = pytest.importorskip("torch")
+PAGE, D = 64, 128
+
+
+@pytest.fixture(scope="module")
+def b():
+    from bit_rotated_kv_decode_gb300 import binding, build
+    build.build()
+    binding.load()
+    return binding
+
+
+class Pool:
+    """A BF16 (group 0) or 4-bit pool with known keys and values, host and device."""
+
+    def __init__(self, b, lens, hkv, group=0, seed=0, visible=None, spare=3):
+        g = np.random.default_rng(seed)
+        self.lens, self.hkv, self.group = lens, hkv, group
+        need = [-(-t // PAGE) for t in lens]
+        self.pages = sum(need) + spare
+        order = g.permutation(self.pages)
+        self.table = np.full((len(lens), max(1, max(need))), -1, np.int32)
+        at = 0
+        for i, m in enumerate(need):
+            self.table[i, :m] = order[at:at + m]
+            at += m
+        if group == 0:
+            self.host = np.full((self.pages, hkv, 2, PAGE, D), 0x7FFF, np.uint16)
+        else:
+            self.host = np.full((self.pages, hkv, paged.record_bytes(group)), 0xFF, np.uint8)
+        self.k, self.v, self.kmag, self.vmag = [], [], [], []
+        for i, t in enumerate(lens):
+            k = g.standard_normal((t, hkv, D)).astype(np.float32)
+            k[:, :, 5] *= 6
+            v = (g.standard_normal((t, hkv, D)) * np.exp(0.5 * g.standard_normal((t, hkv, 1)))).astype(np.float32)
+            kb, vb = paged.bf16_bits(k), paged.bf16_bits(v)
+            if group == 0:
+                kf, vf = paged.bf16_values(kb).astype(np.float64), paged.bf16_values(vb).astype(np.float64)
+                for t0 in range(0, t, PAGE):
+                    page, m = self.table[i, t0 // PAGE], min(PAGE, t - t0)
+                    self.host[page, :, 0, :m] = kb[t0:t0 + m].transpose(1, 0, 2)
+                    self.host[page, :, 1, :m] = vb[t0:t0 + m].transpose(1, 0, 2)
+            else:
+                (kc, km), (vc, vm) = paged.quantise4(kb, group), paged.quantise4(vb, group)
+                kf, vf = paged.dequantise4(kc, km), paged.dequantise4(vc, vm)
+                kz, vz = (np.repeat(np.abs(m[..., 1].astype(np.float64)), group, -1) for m in (km, vm))
+                for tok in range(t):
+                    for h in range(hkv):
+                        rec = self.host[self.table[i, tok // PAGE], h]
+                        paged.put4(rec, 0, tok % PAGE, kc[tok, h], km[tok, h])
+                        paged.put4(rec, 1, tok % PAGE, vc[tok, h], vm[tok, h])
+            self.k.append(kf)
+            self.v.append(vf)
+            self.kmag.append(np.abs(kf) + (2 * kz if group else 0))
+            self.vmag.append(np.abs(vf) + (2 * vz if group else 0))
+
+    def hide(self, q_lens, window, sinks):
+        """Poison what no query of a request sees: -1 for whole pages, NaN for tokens (as a fresh pool holds)."""
+        table = self.table.copy()
+        for i, (t, m) in enumerate(zip(self.lens, q_lens)):
+            vis = np.zeros(t, bool)
+            for p in range(t - m, t):
+                vis[paged.seen(p, window, sinks)] = True
+            for page in range(-(-t // PAGE)):
+                rows = vis[page * PAGE:(page + 1) * PAGE]
+                if not rows.any():
+                    table[i, page] = -1
+                    continue
+                if self.group == 0:
+                    for r in np.nonzero(~rows)[0]:
+                        self.host[self.table[i, page], :, :, r] = 0x7FC0
+                else:
+                    ng = D // self.group
+                    for r in np.nonzero(~rows)[0]:
+                        at = PAGE * D + r * 4 * ng
+                        for which in range(2):
+                            o = at + which * PAGE * 4 * ng
+                            self.host[self.table[i, page], :, o:o + 4 * ng] = 0xFF
+        self.table = table
+
+    def device(self):
+        kv = torch.from_numpy(self.host.view(np.int16) if self.group == 0 else self.host).cuda()
+        return kv.view(torch.bfloat16) if self.group == 0 else kv, torch.from_numpy(self.table).cuda()
+
+
+def bf16(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).view(torch.bfloat16).cuda()
+
+
+def tolerance(out, mag, logit, tokens, four, one_part, out_bf16):
+    weight = 2.0 ** -22 + (2.0 ** -8 if one_part else 2.0 ** -21 if four else 2.0 ** -17)
+    rel = 2 * ((2 if four else 1) * 8 * 2.0 ** -22 * logit + weight) + 2.0 ** -22 * (tokens / 16 + 64)
+    return rel * mag + (2.0 ** -8 * np.abs(out) if out_bf16 else 0)
+
+
+def check_attention(pool, q, q_lens, window, sinks, got, lse, scale=0.0, one_part=lambda m: False):
+    scale = scale if scale > 0 else 1 / math.sqrt(D)
+    out_bf16 = got.dtype == torch.bfloat16
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    qf = paged.bf16_values(q).astype(np.float64)
+    g = q.shape[1] // pool.hkv
+    row = 0
+    for i, (t, m) in enumerate(zip(pool.lens, q_lens)):
+        for p in range(t - m, t):
+            for h in range(q.shape[1]):
+                out, ls, mag, logit = paged.attend(qf[row, h], pool.k[i][:, h // g], pool.v[i][:, h // g], p, window,
+                                                   sinks, scale, pool.kmag[i][:, h // g], pool.vmag[i][:, h // g])
+                n = len(paged.seen(p, window, sinks))
+                tol = tolerance(out, mag, logit, n, pool.group, one_part(m), out_bf16)
+                bad = ~(np.abs(got[row, h] - out) <= tol)
+                assert not bad.any(), (i, p, h, np.abs(got[row, h] - out)[bad].max(), tol[bad].min())
+                if ls == -np.inf:
+                    assert lse[row, h] == -np.inf
+                else:
+                    assert abs(lse[row, h] - ls) <= 2 * 8 * 2.0 ** -22 * logit + 2.0 ** -20 + 2.0 ** -22 * (n / 16 + 64)
+            row += 1
+
+
+def run_attention(b, pool, q_lens, hq, window, sinks, out_dtype=torch.float32, seed=1, scale=0.0, workspace=None,
+                  one_part=lambda m: False):
+    rows = sum(q_lens)
+    q = paged.bf16_bits(np.random.default_rng(seed).standard_normal((rows, hq, D)).astype(np.float32))
+    pool.hide(q_lens, window, sinks)
+    kv, table = pool.device()
+    out = torch.full((rows + 1, hq, D), 7.0, dtype=out_dtype, device="cuda")
+    lse = torch.full((rows + 1, hq), 7.0, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = dict(q_lens=q_lens, lse=lse[:rows], error=err, scale=scale, workspace=workspace)
+    if pool.group:
+        ws = b.int4_attention(kv, table, pool.lens, bf16(q), out[:rows], pool.hkv, window, sinks,
+                              group_size=pool.group, **args)
+    else:
+        ws = b.window_attention(kv, table, pool.lens, bf16(q), out[:rows], pool.hkv, window, sinks, **args)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    assert (out[rows] == 7).all() and (lse[rows] == 7).all()          # rows behind the last are left as they were
+    assert int(ws[:65536].view(torch.int32).abs().sum()) == 0         # the merge counters are back at zero
+    check_attention(pool, q, q_lens, window, sinks, out[:rows], lse[:rows], scale, one_part)
+    return ws
+
+
+# ---- decode: every group size, ragged lengths, windows, sinks ------------------
+DECODE = [
+    # lens, window, sinks
+    ([1], -1, 0),
+    ([1, 63, 64, 65, 16, 17], -1, 0),
+    ([1000, 37, 4133], -1, 0),
+    ([1000, 5, 4133, 320], 256, 64),
+    ([777, 130, 129, 2500], 100, 4),
+    ([500, 3], 1, 0),
+    ([300, 64, 65], 0, 64),
+    ([300, 1], 0, 0),
+    ([200, 90], 50, 1000),
+    ([2000], 333, 70),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (2, 2), (2, 1), (16, 2)])
+@pytest.mark.parametrize("lens,window,sinks", DECODE)
+def test_window_decode(b, hq, hkv, lens, window, sinks):
+    run_attention(b, Pool(b, lens, hkv, seed=len(lens) + hq), [1] * len(lens), hq, window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [128, 64])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (1, 1), (4, 2), (8, 1)])
+@pytest.mark.parametrize("lens,window,sinks", [c for c in DECODE if sum(c[0]) < 4500])
+def test_int4_decode(b, group, hq, hkv, lens, window, sinks):
+    run_attention(b, Pool(b, lens, hkv, group, seed=len(lens) + hq), [1] * len(lens), hq, window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 128, 64])
+@pytest.mark.parametrize("hq,hkv,q_lens", [(4, 1, [4, 2, 0, 1]), (8, 1, [2, 1, 0, 2]), (2, 2, [16, 7, 0, 3]),
+                                           (4, 2, [3, 8, 0, 5])])
+def test_a_few_query_tokens(b, group, hq, hkv, q_lens):
+    lens = [300, 70, 0, 129]
+    run_attention(b, Pool(b, lens, hkv, group, seed=hq), q_lens, hq, -1, 0)
+    run_attention(b, Pool(b, lens, hkv, group, seed=hq), q_lens, hq, 40, 5, torch.bfloat16, scale=0.2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 128])
+def test_many_short_requests_and_a_long_one(b, group):
+    # more segments than CTAs, then one segment over many CTAs, on one workspace
+    lens = [1 + (37 * i) % 200 for i in range(90)]
+    ws = run_attention(b, Pool(b, lens, 2, group, seed=5), [1] * 90, 4, -1, 0)
+    lens = [9001 if group == 0 else 5001]
+    run_attention(b, Pool(b, lens, 1, group, seed=6), [1], 4, -1, 0, workspace=ws)
+    run_attention(b, Pool(b, [150] * 70, 2, group, seed=7), [1] * 70, 4, 64, 3, workspace=ws)
+
+
+# ---- prefill --------------------------------------------------------------------
+PREFILL = [
+    # lens, q_lens, window, sinks
+    ([100], [100], -1, 0),
+    ([513], [513], -1, 0),
+    ([40, 300, 1, 257], [40, 300, 1, 130], -1, 0),
+    ([700, 65, 333], [90, 65, 1], 128, 64),
+    ([600], [600], 100, 4),
+    ([600], [300], 1, 0),
+    ([300, 200], [33, 150], 0, 70),
+    ([300], [40], 0, 0),
+    ([900], [200], 130, 200),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (2, 2), (8, 1), (2, 1)])
+@pytest.mark.parametrize("lens,q_lens,window,sinks", PREFILL)
+def test_window_prefill(b, hq, hkv, lens, q_lens, window, sinks):
+    run_attention(b, Pool(b, lens, hkv, seed=len(lens) + hq), q_lens, hq, window, sinks)
+    run_attention(b, Pool(b, lens, hkv, seed=len(lens) + hq), q_lens, hq, window, sinks, torch.bfloat16, scale=0.13,
+                  one_part=lambda m: True)
+
+
+# ---- append ----------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 128, 64])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (1, 1), (5, 3), (32, 8)])
+@pytest.mark.parametrize("dim,interleaved", [(128, False), (128, True), (32, False), (96, False), (48, True), (0, False)])
+def test_append_matches_the_oracle_bit_for_bit(b, group, hq, hkv, dim, interleaved):
+    lens, new = [0, 63, 200, 5], [70, 1, 0, 129]
+    rows, n = sum(new), len(lens)
+    g = np.random.default_rng(hq * 7 + dim)
+    x = g.standard_normal((rows, hq + 2 * hkv, D)).astype(np.float32)
+    x[3] = 0.25                                   # a constant token: scale 0
+    x[4, :, 7] = 300000.0                         # beyond fp16
+    bits = paged.bf16_bits(x)
+    qkv = bf16(bits)
+    q, k, v = qkv.split([hq, hkv, hkv], 1)        # strided views of one tensor
+    need = [-(-(a + m) // PAGE) for a, m in zip(lens, new)]
+    pages = sum(need) + 2
+    order = g.permutation(pages)
+    table = np.full((n, max(need)), -1, np.int32)
+    at = 0
+    for i, m in enumerate(need):
+        table[i, :m] = order[at:at + m]
+        at += m
+    length = max(a + m for a, m in zip(lens, new))
+    pos = np.concatenate([np.arange(a, a + m) for a, m in zip(lens, new)])
+    req = np.repeat(np.arange(n), new)
+    rope = b.rope_table(length, dim) if dim else None
+    qb, kb, vb = bits[:, :hq], bits[:, hq:hq + hkv], bits[:, hq + hkv:]
+    if dim:
+        t = rope.cpu().numpy()
+        qb, kb = paged.rotate(qb, t, pos, interleaved), paged.rotate(kb, t, pos, interleaved)
+    if group == 0:
+        host = g.integers(0, 65536, (pages, hkv, 2, PAGE, D)).astype(np.uint16)
+        kv = bf16(host)
+    else:
+        host = g.integers(0, 256, (pages, hkv, paged.record_bytes(group))).astype(np.uint8)
+        kv = torch.from_numpy(host.copy()).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = torch.empty(rows, hq, D, dtype=torch.bfloat16, device="cuda")
+    args = dict(q=q, q_out=q_out, new_lens=new, interleaved=interleaved, error=err)
+    dt = torch.from_numpy(table).cuda()
+    if group == 0:
+        b.bf16_append(kv, dt, lens, k, v, rope, **args)
+    else:
+        b.int4_append(kv, dt, lens, k, v, rope, group_size=group, **args)
+    for r in range(rows):
+        page, slot = table[req[r], pos[r] // PAGE], pos[r] % PAGE
+        if group == 0:
+            host[page, :, 0, slot], host[page, :, 1, slot] = kb[r], vb[r]
+        else:
+            (kc, km), (vc, vm) = paged.quantise4(kb[r], group), paged.quantise4(vb[r], group)
+            for h in range(hkv):
+                paged.put4(host[page, h], 0, slot, kc[h], km[h])
+                paged.put4(host[page, h], 1, slot, vc[h], vm[h])
+    assert err.item() == 0
+    assert np.array_equal(q_out.view(torch.int16).cpu().numpy().view(np.uint16), qb)
+    got = kv.view(torch.int16).cpu().numpy().view(np.uint16) if group == 0 else kv.cpu().numpy()
+    assert np.array_equal(got, host)              # the other tokens' bytes among them
+    if group:
+        starts, counts = [3, 60, 0, 100], [60, 4, 0, 34]
+        m = sum(counts)
+        for kind in (torch.float32, torch.bfloat16):
+            ko, vo = (torch.empty(m, hkv, D, dtype=kind, device="cuda") for _ in range(2))
+            b.int4_read(kv, dt, starts, counts, ko, vo, group_size=group, error=err)
+            at = 0
+            for i, (a, c) in enumerate(zip(starts, counts)):
+                for tok in range(a, a + c):
+                    new_row = tok - lens[i]
+                    if 0 <= new_row < new[i]:
+                        r = sum(new[:i]) + new_row
+                        for want, out in ((kb[r], ko), (vb[r], vo)):
+                            w = paged.dequantise4(*paged.quantise4(want, group)).astype(np.float32)
+                            w = paged.bf16_values(paged.bf16_bits(w)) if kind == torch.bfloat16 else w
+                            assert np.array_equal(out[at].float().cpu().numpy(), w)
+                    at += 1
+        assert err.item() == 0
+
+
+# ---- together ---------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 64])
+def test_prefill_then_decode_steps(b, group):
+    """A prompt appended and attended, then decode steps, as a serving loop makes them, on a stream of its own and the
+    steps captured into a graph each; the outputs against the oracle on the oracle's own cache."""
+    hq, hkv, steps = 8, 2, 3
+    prompt = [70, 200]
+    total = [t + steps for t in prompt]
+    g = np.random.default_rng(11)
+    table = g.permutation(2 * 5).reshape(2, 5).astype(np.int32)
+    dt = torch.from_numpy(table).cuda()
+    rope = b.rope_table(max(total))
+    host = rope.cpu().numpy()
+    kv = b.int4_pool(10, hkv, group) if group else torch.full((10, hkv, 2, PAGE, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    held = Pool(b, total, hkv, group)
+    append = (lambda *a, **k: b.int4_append(*a, group_size=group, **k)) if group else b.bf16_append
+    attend = (lambda *a, **k: b.int4_attention(*a, group_size=group, **k)) if group else b.window_attention
+    stream = torch.cuda.Stream()
+    lens = [0, 0]
+    ws = b.attention_workspace(2, hq, hkv, prompt)
+    torch.cuda.synchronize()
+    for step in range(steps + 1):
+        new = prompt if step == 0 else [1, 1]
+        rows = sum(new)
+        bits = paged.bf16_bits(g.standard_normal((rows, hq + 2 * hkv, D)).astype(np.float32))
+        pos = np.concatenate([np.arange(a, a + m) for a, m in zip(lens, new)])
+        qr = paged.rotate(bits[:, :hq], host, pos, False)
+        kr = paged.rotate(bits[:, hq:hq + hkv], host, pos, False)
+        vr = bits[:, hq + hkv:]
+        row = 0
+        for i, m in enumerate(new):
+            for j in range(m):
+                for dst, mag, x in ((held.k, held.kmag, kr[row]), (held.v, held.vmag, vr[row])):
+                    if group:
+                        code, meta = paged.quantise4(x, group)
+                        y = paged.dequantise4(code, meta)
+                        z = np.repeat(np.abs(meta[..., 1].astype(np.float64)), group, -1)
+                    else:
+                        y, z = paged.bf16_values(x).astype(np.float64), 0
+                    dst[i][lens[i] + j], mag[i][lens[i] + j] = y, np.abs(y) + 2 * z
+                row += 1
+        q, k, v = bf16(bits).split([hq, hkv, hkv], 1)
+        q_out = torch.empty(rows, hq, D, dtype=torch.bfloat16, device="cuda")
+        now = [a + m for a, m in zip(lens, new)]
+        q_lens = [min(m, 2) for m in new] if group else new
+        last = np.concatenate([np.arange(sum(new[:i + 1]) - ql, sum(new[:i + 1])) for i, ql in enumerate(q_lens)])
+        out = torch.empty(len(last), hq, D, device="cuda")
+        lse = torch.empty(len(last), hq, device="cuda")
+        torch.cuda.synchronize()
+
+        def go():
+            append(kv, dt, lens, k, v, rope, q=q, q_out=q_out, new_lens=new)
+            attend(kv, dt, now, q_out[torch.from_numpy(last).cuda()] if step == 0 else q_out, out, hkv, 100, 8,
+                   q_lens=q_lens, lse=lse, workspace=ws)
+
+        with torch.cuda.stream(stream):
+            if step == 0:
+                go()
+            else:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=stream):
+                    go()
+                graph.replay()
+                graph.replay()
+        torch.cuda.synchronize()
+        held.lens = now
+        sub = Pool.__new__(Pool)
+        sub.lens, sub.hkv, sub.group = now, hkv, group
+        sub.k = [x[:t] for x, t in zip(held.k, now)]
+        sub.v = [x[:t] for x, t in zip(held.v, now)]
+        sub.kmag = [x[:t] for x, t in zip(held.kmag, now)]
+        sub.vmag = [x[:t] for x, t in zip(held.vmag, now)]
+        check_attention(sub, qr[last], q_lens, 100, 8, out, lse)
+        lens = now
+
+
+# ---- errors -------------------------------------------------------------------------
+@pytest.mark.gpu
+def test_bad_pages_set_the_error_word(b):
+    kv = torch.ones(3, 2, 2, PAGE, D, dtype=torch.bfloat16, device="cuda")
+    table = torch.tensor([[1, 99], [-5, 0]], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.zeros(2, 2, D, dtype=torch.bfloat16, device="cuda")
+    b.bf16_append(kv, table, [64, 3], x, x, error=err)
+    assert err.item() == 1 and (kv == 1).all()                 # both stores are dropped
+    err.zero_()
+    q = torch.ones(2, 4, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(2, 4, D, device="cuda")
+    b.window_attention(kv, table, [100, 4], q, out, 2, error=err)
+    assert err.item() == 1 and (out == 1).all()                # a bad page reads as page 0
+    err.zero_()
+    kv4 = b.int4_pool(3, 2)
+    b.int4_append(kv4, table, [64, 3], x, x, error=err)
+    assert err.item() == 1 and (kv4 == 0).all()
+    err.zero_()
+    b.int4_attention(kv4, table, [100, 4], q, out, 2, error=err)
+    assert err.item() == 1 and (out == 0).all()
+    ko, vo = torch.ones(2, 2, 2, D, device="cuda")
+    err.zero_()
+    b.int4_read(kv4, table, [64, 0], [1, 1], ko, vo, error=err)
+    assert err.item() == 1 and (ko == 0).all() and (vo == 0).all()
+    b.window_attention(kv, table, [10, 4], q[:1], out[:1], 2, q_lens=[1, 0])   # no error word: nothing to tell
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_binding_refusals(b):
+    kv = torch.zeros(4, 2, 2, PAGE, D, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 4, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(2, 4, D, device="cuda")
+    k = torch.zeros(2, 2, D, dtype=torch.bfloat16, device="cuda")
+    good = (kv, table, [5, 9], q, out, 2)
+    b.window_attention(*good)
+    for change in [dict(kv=kv.float()), dict(kv=kv[:, :1]), dict(table=table.long()), dict(table=table.cpu()),
+                   dict(lens=[5, 129]), dict(lens=[5, 0]), dict(lens=[5]), dict(q=q[:1]), dict(q=q.float()),
+                   dict(q=q.transpose(0, 1)), dict(out=out.half()), dict(out=out[:, :2]), dict(hkv=1), dict(hkv=4)]:
+        args = dict(zip(("kv", "table", "lens", "q", "out", "hkv"), good))
+        args.update(change)
+        with pytest.raises(b.OscarError):
+            b.window_attention(*args.values())
+    for more in [dict(q_lens=[1, 2]), dict(q_lens=[3, -1]), dict(sinks=-1), dict(scale=float("nan")),
+                 dict(lse=torch.zeros(2, 2, device="cuda")), dict(error=torch.zeros(1, device="cuda")),
+                 dict(workspace=torch.zeros(1 << 20, device="cuda", dtype=torch.uint8)[1:])]:
+        with pytest.raises(b.OscarError):
+            b.window_attention(*good, **more)
+    rope = b.rope_table(9)
+    with pytest.raises(b.OscarError):
+        b.bf16_append(kv, table, [5, 9], k, k, rope)             # position 9 is beyond the table
+    for more in [dict(q=q), dict(q_out=q), dict(new_lens=[1, 2]), dict(new_lens=[3, -1]), dict(rope=rope[:, :24])]:
+        with pytest.raises(b.OscarError):
+            b.bf16_append(kv, table, [5, 6], k, k, **more)
+    kv4 = b.int4_pool(4, 2)
+    with pytest.raises(b.OscarError):
+        b.int4_attention(kv4, table, [5, 9], q, out, 2, group_size=64)
+    with pytest.raises(b.OscarError):
+        b.int4_attention(kv4, table, [20, 20], torch.cat([q] * 9), torch.cat([out] * 9), 2, q_lens=[9, 9])
+    with pytest.raises(b.OscarError):
+        b.int4_append(kv4, table, [5, 9], k, k, group_size=32)

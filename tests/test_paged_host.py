@@ -1,0 +1,154 @@
+"""Argument checks of the paged-cache operators (no GPU: every refusal comes before
+any CUDA call) and pins of their oracle."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import paged
+
+
+@pytest.fixture(scope="module")
+def b():
+    from bit_rotated_kv_decode_gb300 import binding, build
+    build.build()
+    binding.load()
+    return binding
+
+
+def ints(*v):
+    return (ctypes.c_int32 * len(v))(*v)
+
+
+A = 0x10000   # an aligned address that no refused call reaches
+
+APPEND = dict(kv=A, pages=8, table=A, max_pages=4, lens=ints(3, 64), new=ints(1, 2), n=2, hq=8, hkv=2, rope=None, q=A,
+              qs=1536, k=A, ks=1536, v=A, vs=1536, q_out=A, error=None, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(kv=None), dict(kv=A + 8), dict(pages=0), dict(table=None), dict(max_pages=0), dict(lens=None),
+    dict(lens=ints(-1, 0)), dict(lens=ints(3, 255)), dict(new=ints(1, -1)), dict(n=0), dict(n=257), dict(hkv=0),
+    dict(hq=0), dict(q=A + 2), dict(q_out=None), dict(q=None), dict(k=None), dict(k=A + 4), dict(v=None),
+    dict(ks=255), dict(ks=260), dict(vs=128), dict(qs=1000), dict(qs=1028), dict(rope=(A, 65, 128)),
+    dict(rope=(A, 66, 8)), dict(rope=(A, 66, 136)), dict(rope=(A, 66, 40)), dict(rope=(None, 66, 128)),
+    dict(rope=(A + 4, 66, 128)), dict(group=32), dict(group=0)])
+def test_append_refusals(b, change):
+    args = {**APPEND, **change}
+    group = args.pop("group", None)
+    if args["rope"] is not None:
+        args["rope"] = ctypes.byref(b.oscar_rope(*args["rope"], 0))
+    v = list(args.values())
+    lib = b.load()
+    if group is None:
+        assert lib.oscar_bf16_append(*v) == b.OSCAR_ERR_INVALID_ARG
+        assert lib.oscar_paged_last_error() != b""
+    v.insert(9, 128 if group is None else group)
+    assert lib.oscar_int4_append(*v) == b.OSCAR_ERR_INVALID_ARG
+
+
+def test_append_of_nothing_is_a_no_op(b):
+    v = list({**APPEND, "new": ints(0, 0)}.values())
+    assert b.load().oscar_bf16_append(*v) == b.OSCAR_OK
+
+
+ATTEND = dict(kv=A, pages=8, table=A, max_pages=4, lens=ints(3, 64), q_lens=ints(1, 2), n=2, hq=8, hkv=2, window=5,
+              sinks=1, scale=0.0, q=A, qs=1024, out=A, kind=0, lse=None, error=None, ws=A, ws_bytes=1 << 40,
+              stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(kv=None), dict(kv=A + 2), dict(pages=0), dict(table=None), dict(max_pages=0), dict(lens=None),
+    dict(lens=ints(0, 5)), dict(lens=ints(3, 257)), dict(q_lens=ints(-1, 1)), dict(n=0), dict(n=257), dict(hkv=3),
+    dict(hq=6), dict(hq=32), dict(sinks=-1), dict(scale=float("inf")), dict(q=None), dict(q=A + 2), dict(qs=1000),
+    dict(qs=1028), dict(out=None), dict(out=A + 4), dict(kind=2), dict(ws=None), dict(ws=A + 16), dict(ws_bytes=100),
+    dict(group=96)])
+def test_attention_refusals(b, change):
+    args = {**ATTEND, **change}
+    group = args.pop("group", None)
+    v = list(args.values())
+    lib = b.load()
+    if group is None:
+        assert lib.oscar_window_attention(*v) == b.OSCAR_ERR_INVALID_ARG
+    v.insert(9, 128 if group is None else group)
+    assert lib.oscar_int4_attention(*v) == b.OSCAR_ERR_INVALID_ARG
+
+
+def test_int4_attention_takes_a_few_query_tokens(b):
+    v = list({**ATTEND, "q_lens": ints(1, 5)}.values())
+    v.insert(9, 128)
+    assert b.load().oscar_int4_attention(*v) == b.OSCAR_ERR_INVALID_ARG
+    assert b"query tokens" in b.load().oscar_paged_last_error()
+
+
+@pytest.mark.parametrize("change", [dict(kv=None), dict(starts=None), dict(counts=None), dict(starts=ints(-1, 0)),
+                                    dict(counts=ints(1, 256)), dict(k=None), dict(v=A + 4), dict(kind=3), dict(group=1)])
+def test_read_refusals(b, change):
+    args = dict(kv=A, pages=8, table=A, max_pages=4, starts=ints(0, 3), counts=ints(4, 5), n=2, hkv=2, group=64, k=A,
+                v=A, kind=1, error=None, stream=None)
+    args.update(change)
+    assert b.load().oscar_int4_read(*args.values()) == b.OSCAR_ERR_INVALID_ARG
+
+
+def test_workspace_size(b):
+    lib = b.load()
+    size = lib.oscar_attention_workspace_bytes
+    assert size(0, None, 8, 2) == 0 and size(257, None, 8, 2) == 0 and size(1, None, 6, 2) == 0
+    assert size(1, None, 24, 8) == 0 and size(256, None, 1024, 512) == 0 and size(1, ints(-1), 8, 2) == 0
+    assert size(4, None, 8, 2) >= 65536 + 8 * 4 * 132 * 4
+    assert size(1, ints(0), 8, 2) > 0
+
+
+# ---- the oracle ------------------------------------------------------------------
+def test_rotation_keeps_lengths_and_turns_by_the_angle():
+    g = np.random.default_rng(0)
+    bits = paged.bf16_bits(g.standard_normal((4, 2, 128)).astype(np.float32))
+    angle = np.arange(4)[:, None] * np.ones(32)
+    table = np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)
+    for inter in (False, True):
+        y = paged.bf16_values(paged.rotate(bits, table, np.arange(4), inter)).astype(np.float64)
+        x = paged.bf16_values(bits).astype(np.float64)
+        i = np.arange(0, 64, 2) if inter else np.arange(32)
+        j = i + 1 if inter else i + 32
+        z = (x[..., i] + 1j * x[..., j]) * np.exp(1j * np.arange(4))[:, None, None]
+        assert np.abs(y[..., i] - z.real).max() < 2 ** -7 * 4 and np.abs(y[..., j] - z.imag).max() < 2 ** -7 * 4
+        assert np.array_equal(y[..., 64:], x[..., 64:]) and np.array_equal(y[0], x[0])
+
+
+@pytest.mark.parametrize("group", [128, 64])
+def test_quantise4_takes_the_nearest_level(group):
+    g = np.random.default_rng(1)
+    bits = paged.bf16_bits(g.standard_normal((50, 128)).astype(np.float32))
+    code, meta = paged.quantise4(bits, group)
+    x = paged.bf16_values(bits).astype(np.float64).reshape(50, -1, group)
+    s, z = meta[..., :1].astype(np.float64), meta[..., 1:].astype(np.float64)
+    levels = np.arange(16) * s[..., None] + z[..., None]
+    best = np.abs(x[..., None] - levels).min(-1)
+    mine = np.abs(x - paged.dequantise4(code, meta).reshape(x.shape))
+    assert (mine <= best + 1e-6).all()
+    const, m = paged.quantise4(paged.bf16_bits(np.full((1, 128), 0.5, np.float32)), group)
+    assert (const == 0).all() and (m[..., 0] == 0).all() and (m[..., 1] == 0.5).all()
+
+
+def test_record_holds_what_was_put():
+    rec = np.zeros(paged.record_bytes(64), np.uint8)
+    code = np.arange(128, dtype=np.uint8) % 16
+    meta = np.array([[1, 2], [3, 4]], np.float16)
+    paged.put4(rec, 1, 9, code, meta)
+    assert np.array_equal(rec[4096 + 9 * 64:4096 + 10 * 64] & 15, code[0::2])
+    assert np.array_equal(rec[8192 + 512 + 72:8192 + 512 + 80].view(np.float16), [1, 2, 3, 4])
+    assert rec.astype(bool).sum() <= 64 + 8
+
+
+def test_window_and_sinks():
+    assert list(paged.seen(5, -1, 0)) == [0, 1, 2, 3, 4, 5]
+    assert list(paged.seen(5, 2, 1)) == [0, 4, 5]
+    assert list(paged.seen(5, 0, 2)) == [0, 1] and list(paged.seen(5, 0, 0)) == []
+    assert list(paged.seen(1, 9, 4)) == [0, 1]
+
+
+def test_rope_table_keeps_far_angles(b):
+    t = b.rope_table(100001, 64, device="cpu").numpy()
+    inv = np.longdouble(10000) ** (-2 * np.arange(32, dtype=np.longdouble) / 64)
+    a = np.longdouble(100000) * inv
+    assert np.abs(t[100000, :32] - np.cos(a)).max() < 2 ** -23 and np.abs(t[100000, 32:] - np.sin(a)).max() < 2 ** -23
