@@ -96,4 +96,10 @@ size_t paged_decode_record_bytes(int segments, int rows, int sms);
 cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, int gk,
                                 void* workspace, const CUtensorMap* map, int sms, cudaStream_t s);
 
+// Prefill: any number of query rows per request, BF16 pages.  q_map: q as (128
+// channels, Hq, rows), boxes of 64 channels x G heads x 128 / G rows; kv_map: the pool,
+// boxes of 64 channels x 64 tokens x 1.
+cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a,
+                                 const CUtensorMap& q_map, const CUtensorMap& kv_map, cudaStream_t s);
+
 }  // namespace oscar

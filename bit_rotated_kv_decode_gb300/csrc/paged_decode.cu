@@ -641,7 +641,7 @@ __device__ __forceinline__ void put_state(const State<GK, NR>& S, float (*st)[PA
 __device__ __forceinline__ void write_row(const DecodeArgs& A, int req, int head, int r, int lane, float4 o, float m,
                                           float l) {
   const size_t row = (size_t)(A.row[req] + r / A.G) * A.a.Hq + (size_t)head * A.G + r % A.G;
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
   if (A.a.f32) {
     reinterpret_cast<float4*>(static_cast<float*>(A.a.out) + row * D)[lane] = o;
@@ -649,7 +649,7 @@ __device__ __forceinline__ void write_row(const DecodeArgs& A, int req, int head
     reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.a.out) + row * D)[lane] =
         make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
   }
-  if (A.a.lse && lane == 0) A.a.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : NEG_INF;
+  if (A.a.lse && lane == 0) A.a.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : NEG_INF;
 }
 
 // Fold count states of one row, the warp's lanes holding 4 channels each.

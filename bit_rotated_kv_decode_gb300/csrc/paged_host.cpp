@@ -109,16 +109,20 @@ EncodeTiled encode_entry() {
   return fn;
 }
 
-bool pool_map(CUtensorMap* map, const void* pool, int64_t records, uint32_t tokens, uint32_t parts) {
+bool map_3d(CUtensorMap* map, const void* base, cuuint64_t d1, cuuint64_t d2, cuuint64_t stride1, cuuint64_t stride2,
+            uint32_t box1, uint32_t box2) {
   const EncodeTiled fn = encode_entry();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {D, PAGE, static_cast<cuuint64_t>(2 * records)};
-  const cuuint64_t strides[2] = {D * 2, (cuuint64_t)PAGE * D * 2};
-  const cuuint32_t box[3] = {64, tokens, parts};
+  const cuuint64_t dims[3] = {D, d1, d2};
+  const cuuint64_t strides[2] = {stride1, stride2};   // bytes
+  const cuuint32_t box[3] = {64, box1, box2};
   const cuuint32_t steps[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, steps,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool pool_map(CUtensorMap* map, const void* pool, int64_t records, uint32_t tokens, uint32_t parts) {
+  return map_3d(map, pool, PAGE, static_cast<cuuint64_t>(2 * records), D * 2, (cuuint64_t)PAGE * D * 2, tokens, parts);
 }
 
 int sm_count() {
@@ -171,33 +175,43 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
   a.window = window < 0 || window > (1 << 30) ? (1 << 30) + (1 << 29) : window;
   a.sinks = sinks;
   a.scale2 = (scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(D))) * 1.4426950408889634f;
-  CUtensorMap map;
-  if (gk == 0 && !pool_map(&map, pool, num_pages * hkv, 16, 2)) return fail(OSCAR_ERR_CUDA, "tensor map of the pool");
   const int sms = sm_count();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // requests of the same number of query tokens go together; longer ones in blocks
   AttnReq reqs[PAGED_MAX_REQ];
-  for (int32_t m = step; m >= 1; --m) {
-    int count = 0;
-    int32_t row = 0;
+  // requests of more than 16 rows a kv head: the tiled kernel
+  int count = 0, few = 0;
+  int32_t row = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t m = q_lens ? q_lens[i] : 1;
+    if (m > step) reqs[count++] = AttnReq{lens[i], m, row, i};
+    if (m >= 1 && m <= step) ++few;
+    row += m;
+  }
+  CUtensorMap kv_map, q_map;
+  if (count) {
+    if (!pool_map(&kv_map, pool, num_pages * hkv, PAGE, 1) ||
+        !map_3d(&q_map, q, static_cast<cuuint64_t>(hq), static_cast<cuuint64_t>(rows), D * 2,
+                static_cast<cuuint64_t>(q_stride) * 2, static_cast<uint32_t>(G), static_cast<uint32_t>(128 / G)))
+      return fail(OSCAR_ERR_CUDA, "tensor map of the pool or of q");
+    const cudaError_t e = launch_paged_prefill(p, reqs, count, a, q_map, kv_map, s);
+    if (e != cudaSuccess) return from_cuda(e);
+  }
+  if (!few) return OSCAR_OK;
+  // the others: those of the same number of query tokens go together
+  if (gk == 0 && !pool_map(&kv_map, pool, num_pages * hkv, 16, 2))
+    return fail(OSCAR_ERR_CUDA, "tensor map of the pool");
+  for (int32_t m = step; m >= 1 && few; --m) {
+    count = 0;
+    row = 0;
     for (int32_t i = 0; i < n; ++i) {
       const int32_t mi = q_lens ? q_lens[i] : 1;
-      const int32_t blocks = m == step ? mi / step : (mi % step == m ? 1 : 0);
-      const int32_t first = m == step ? 0 : mi - m;
-      for (int32_t b = 0; b < blocks; ++b) {
-        reqs[count++] = AttnReq{lens[i] - mi + first + (b + 1) * m, m, row + first + b * m, i};
-        if (count == PAGED_MAX_REQ || (int64_t)(count + 1) * hkv > (int64_t)PAGED_COUNTERS) {
-          const cudaError_t e = launch_paged_decode(p, reqs, count, a, gk, workspace, gk == 0 ? &map : nullptr, sms, s);
-          if (e != cudaSuccess) return from_cuda(e);
-          count = 0;
-        }
-      }
+      if (mi == m) reqs[count++] = AttnReq{lens[i], m, row, i};
       row += mi;
     }
-    if (count) {
-      const cudaError_t e = launch_paged_decode(p, reqs, count, a, gk, workspace, gk == 0 ? &map : nullptr, sms, s);
-      if (e != cudaSuccess) return from_cuda(e);
-    }
+    if (!count) continue;
+    few -= count;
+    const cudaError_t e = launch_paged_decode(p, reqs, count, a, gk, workspace, gk == 0 ? &kv_map : nullptr, sms, s);
+    if (e != cudaSuccess) return from_cuda(e);
   }
   return OSCAR_OK;
 }
@@ -257,9 +271,7 @@ size_t oscar_attention_workspace_bytes(int32_t n, const int32_t* q_lens, int32_t
     most = m > most ? m : most;
   }
   const int rows = most * G > DECODE_MAX_ROWS ? DECODE_MAX_ROWS : (most ? most : 1) * G;
-  int64_t segs = (int64_t)(most * G > DECODE_MAX_ROWS ? PAGED_MAX_REQ : n) * num_kv_heads;
-  if (segs > (int64_t)PAGED_COUNTERS) segs = PAGED_COUNTERS;
-  return PAGED_COUNTER_BYTES + paged_decode_record_bytes(static_cast<int>(segs), rows, sm_count());
+  return PAGED_COUNTER_BYTES + paged_decode_record_bytes(n * num_kv_heads, rows, sm_count());
 }
 
 oscar_status oscar_window_attention(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,

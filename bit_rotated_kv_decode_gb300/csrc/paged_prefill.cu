@@ -1,0 +1,471 @@
+// Windowed attention of many query rows over BF16 pages (prefill), on tcgen05.
+//
+// A CTA takes 256 query rows of one kv head: two tiles of 128 rows, a row being a
+// (token, head of the group) pair, token by token, so the G heads of a group share
+// every key and value that is loaded and the causal edge crosses few tiles.  It
+// walks the 128-key tiles (two pages) that its rows see: the sinks' first, then the
+// window's.  Per key tile and query tile
+//   S = Q K^T            128 x 128 x 128, tcgen05.mma, both operands in shared memory
+//   p = exp2(S scale - m)   one thread per row, m the running maximum
+//   O = O + P V          tcgen05.mma, P from TMEM, O in TMEM
+// The reference m of a row moves only when exceeded by 2^8; then the row's sum and
+// its O are scaled (tcgen05.ld / st), otherwise O stays where it is.  P is rounded to
+// bf16 for bf16 outputs (each weight off by at most 2^-9, as much as the output's own
+// rounding); for fp32 outputs it is carried as two bf16 parts, in the columns that S
+// leaves.  Sums are taken of the unrounded weights, in fp32.
+//
+// Roles: warps 0-3 and 4-7 the softmax of query tile 0 and 1 (TMEM lane = row), warp 8
+// issues the products, warp 9 the TMA copies (Q once, K and V tiles through a ring of
+// five 32 KB stages).  While one query tile's softmax runs, the tensor core works on
+// the other's products.  TMEM: S0, S1 (P over them), O0, O1, 128 columns each.
+#include "paged_device.cuh"
+
+namespace oscar {
+namespace {
+
+using namespace paged;
+
+constexpr int PF_THREADS = 320;
+constexpr int PF_STAGES = 5;
+constexpr int PF_ROWS = 128;                   // rows of a query tile
+constexpr int PF_KEYS = 128;                   // keys of a tile: two pages
+constexpr int TILE_BYTES = 128 * D * 2;        // a Q, K or V tile
+
+struct alignas(1024) PrefillSmem {
+  alignas(1024) uint8_t q[2][TILE_BYTES];      // per tile: two halves of 64 channels, [128 rows][128 B] swizzled
+  alignas(1024) uint8_t kv[PF_STAGES][TILE_BYTES];
+  uint64_t q_full, kv_full[PF_STAGES], kv_empty[PF_STAGES];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint32_t tmem;
+};
+static_assert(sizeof(PrefillSmem) + 1024 <= 232448, "shared memory of a CTA");
+
+struct PrefillArgs {
+  PagedView p;
+  AttnArgs a;
+  int n, G, lg;                           // lg = log2 G
+  int32_t len[PAGED_MAX_REQ];
+  int32_t m[PAGED_MAX_REQ];
+  int32_t row[PAGED_MAX_REQ];
+  int32_t table[PAGED_MAX_REQ];
+  int32_t bstart[PAGED_MAX_REQ + 1];      // 256-row blocks before request i (one kv head)
+};
+
+// The key tiles that the rows at positions [pmin, pmax] see: [0, sink), then
+// [first, first + count - sink).
+struct KeyTiles {
+  int sink, first, count;
+  int lo, sinks, pmax;     // tokens t <= pmax with t < sinks or t >= lo are seen by some row
+  __device__ static KeyTiles of(int pmin, int pmax, int window, int sinks) {
+    KeyTiles k;
+    k.pmax = pmax;
+    k.sinks = min(sinks, pmax + 1);
+    k.lo = window > 0 ? max(0, pmin - window + 1) : pmax + 1;
+    k.sink = (k.sinks + PF_KEYS - 1) / PF_KEYS;
+    k.first = max(k.lo / PF_KEYS, k.sink);
+    const int end = window > 0 ? pmax / PF_KEYS + 1 : 0;
+    k.count = k.sink + max(0, end - k.first);
+    return k;
+  }
+  __device__ int base(int j) const { return (j < sink ? j : first + (j - sink)) * PF_KEYS; }
+  // whether some row sees a token of [t, t + n)
+  __device__ bool any(int t, int n) const { return t <= pmax && (t < sinks || t + n > lo); }
+  __device__ bool all(int t, int n) const { return t + n - 1 <= pmax && (t + n <= sinks || t >= lo); }
+};
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+#define OSCAR_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define OSCAR_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+// 32 columns of the warp's lanes
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : OSCAR_R8(r, 0), OSCAR_R8(r, 8), OSCAR_R8(r, 16), OSCAR_R8(r, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      OSCAR_W8(r, 0), OSCAR_W8(r, 8), OSCAR_W8(r, 16), OSCAR_W8(r, 24)
+      : "memory");
+}
+#undef OSCAR_R8
+#undef OSCAR_W8
+
+// Shared-memory descriptors with the 128-byte swizzle.  K-major (Q, K): rows of 128 B,
+// groups of 8 rows 1024 B apart.  N-major (V): groups of 8 keys 1024 B apart, the
+// second 64 channels 16 KB on.
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_nmajor(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, bf16 operands, fp32 result, M = N = 128; PV has its B operand N-major.
+constexpr uint32_t IDESC_QK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t IDESC_PV = IDESC_QK | (1u << 16);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(PF_THREADS, 1)
+    paged_prefill_kernel(const __grid_constant__ PrefillArgs A, const __grid_constant__ CUtensorMap q_map,
+                         const __grid_constant__ CUtensorMap kv_map) {
+  extern __shared__ uint8_t pf_raw[];
+  PrefillSmem& sm =
+      *reinterpret_cast<PrefillSmem*>((reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- the CTA's rows: later blocks of a request see more keys, so they go first
+  const int head = blockIdx.x % A.p.Hkv, blk = A.bstart[A.n] - 1 - static_cast<int>(blockIdx.x / A.p.Hkv);
+  int ri = 0;
+  {
+    int hi = A.n;
+    while (hi - ri > 1) {
+      const int mid = (ri + hi) >> 1;
+      if (A.bstart[mid] <= blk) ri = mid; else hi = mid;
+    }
+  }
+  const int m = A.m[ri], per_tile = PF_ROWS >> A.lg;
+  const int tok0 = (blk - A.bstart[ri]) * 2 * per_tile;          // first token of the block, of the request's m
+  const int tokens = min(2 * per_tile, m - tok0);
+  const int tiles = tokens > per_tile ? 2 : 1;
+  const int p0 = A.len[ri] - m + tok0;                           // its position
+  const KeyTiles kt = KeyTiles::of(p0, p0 + tokens - 1, A.a.window, A.a.sinks);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.q_full, 1);
+    for (int s = 0; s < PF_STAGES; ++s) {
+      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sm.s_full[a], 1);
+      mbar_init(&sm.p_full[a], 4);
+      mbar_init(&sm.o_full[a], 1);
+    }
+    mbar_init_fence();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  auto gave_up = [&]() {
+    if (A.p.err) atomicOr(A.p.err, PAGED_ERR_TIMEOUT);
+  };
+
+  if (warp == 9) {
+    // ---- copies
+    if (lane == 0 && kt.count > 0) {
+      mbar_expect_tx(&sm.q_full, tiles * TILE_BYTES);
+      for (int a = 0; a < tiles; ++a)
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, head * A.G, A.row[ri] + tok0 + a * per_tile,
+                      &sm.q_full);
+      const int32_t* pt = A.p.table + (size_t)A.table[ri] * A.p.max_pages;
+      int it = 0;
+      bool ok = true;
+      for (int j = 0; j < kt.count && ok; ++j) {
+        const int t0 = kt.base(j);
+        int page[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          page[u] = -1;
+          if (kt.any(t0 + PAGE * u, PAGE)) {
+            page[u] = __ldg(pt + t0 / PAGE + u);
+            if (page[u] < 0 || page[u] >= A.p.num_pages) {
+              if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
+              page[u] = 0;
+            }
+          }
+        }
+        for (int v = 0; v < 2 && ok; ++v, ++it) {   // K, then V
+          const int st = it % PF_STAGES;
+          if (it >= PF_STAGES && !mbar_wait(&sm.kv_empty[st], (it / PF_STAGES - 1) & 1)) {
+            gave_up();
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&sm.kv_full[st], ((page[0] >= 0) + (page[1] >= 0)) * (TILE_BYTES / 2));
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (page[u] >= 0)
+              for (int h = 0; h < 2; ++h)
+                tma_load_3d(sm.kv[st] + h * (TILE_BYTES / 2) + u * (TILE_BYTES / 4), &kv_map, 64 * h, 0,
+                            static_cast<int>(2 * ((int64_t)page[u] * A.p.Hkv + head)) + v, &sm.kv_full[st]);
+        }
+      }
+      // no copy of this CTA is in flight when it ends (the products wait for each)
+      if (!ok) {
+        mbar_wait(&sm.q_full, 0);
+        for (int k = max(0, it - PF_STAGES); k < it; ++k) mbar_wait(&sm.kv_full[k % PF_STAGES], (k / PF_STAGES) & 1);
+      }
+    }
+  } else if (warp == 8) {
+    // ---- products
+    if (kt.count > 0) {
+      // waits end the same way for the whole warp
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
+      bool ok = wait(&sm.q_full, 0);
+      auto full = [&](int it) { return ok && wait(&sm.kv_full[it % PF_STAGES], (it / PF_STAGES) & 1); };
+      auto score = [&](int a, int it) {
+        const uint32_t q = smem_u32(sm.q[a]), k = smem_u32(sm.kv[it % PF_STAGES]);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const uint32_t off = (s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32;
+          mma_ss(tmem + 128 * a, desc_kmajor(q + off), desc_kmajor(k + off), IDESC_QK, s > 0);
+        }
+        mma_commit(&sm.s_full[a]);
+      };
+      ok = full(0);
+      if (ok && lane == 0) {
+        tc_fence_after();
+        for (int a = 0; a < tiles; ++a) score(a, 0);
+        mma_commit(&sm.kv_empty[0]);
+      }
+      __syncwarp();
+      for (int j = 0; j < kt.count && ok; ++j) {
+        const int itv = 2 * j + 1, itk = 2 * j + 2;
+        const bool more = j + 1 < kt.count;
+        for (int a = 0; a < tiles && ok; ++a) {
+          if (a == 0) {
+            ok = full(itv);
+            const int t0 = kt.base(j);
+            if (ok && !kt.all(t0, PF_KEYS)) {
+              // value rows that no row sees may hold anything (or were not copied): zero them
+              uint8_t* v = sm.kv[itv % PF_STAGES];
+              for (int r = lane >> 3; r < PF_KEYS; r += 4)
+                if (!kt.any(t0 + r, 1)) {
+                  uint4* dst = reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16);
+                  dst[0] = make_uint4(0, 0, 0, 0);
+                  dst[TILE_BYTES / 32] = make_uint4(0, 0, 0, 0);
+                }
+              fence_async_smem();
+              __syncwarp();
+            }
+          }
+          ok = ok && wait(&sm.p_full[a], j & 1);
+          if (ok && lane == 0) {
+            tc_fence_after();
+            const uint32_t v = smem_u32(sm.kv[itv % PF_STAGES]);
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ts(tmem + 256 + 128 * a, tmem + 128 * a + 8 * s, desc_nmajor(v + 2048 * s), IDESC_PV,
+                     (j > 0 || s > 0) ? 1u : 0u);
+            if constexpr (F32) {
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                mma_ts(tmem + 256 + 128 * a, tmem + 128 * a + 64 + 8 * s, desc_nmajor(v + 2048 * s), IDESC_PV, 1u);
+            }
+          }
+          __syncwarp();
+          if (more) {
+            if (a == 0) ok = full(itk);
+            if (ok && lane == 0) score(a, itk);
+          } else if (ok && lane == 0) {
+            mma_commit(&sm.o_full[a]);
+          }
+          // (nobody waits for the last stages; an arrival must not come after the CTA)
+          if (ok && lane == 0 && a == tiles - 1 && more) {
+            mma_commit(&sm.kv_empty[itv % PF_STAGES]);
+            mma_commit(&sm.kv_empty[itk % PF_STAGES]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) gave_up();
+    }
+  } else {
+    // ---- softmax of query tile a
+    const int a = warp >> 2, r = threadIdx.x & 127;
+    if (a < tiles) {
+      const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+      const uint32_t ts = tmem + lane_off + 128 * a, to = tmem + lane_off + 256 + 128 * a;
+      const int tok = a * per_tile + (r >> A.lg);
+      const bool valid = tok < tokens;
+      const int pmin = p0 + a * per_tile, pmax = p0 + min(tokens, (a + 1) * per_tile) - 1;
+      const int pos = valid ? p0 + tok : pmax;
+      const float scale2 = A.a.scale2;
+      float mx = NEG_INF, l = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < kt.count; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[a], j & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t xr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, xr + 32 * c);
+        tc_wait_ld();
+        float* x = reinterpret_cast<float*>(xr);
+        const int t0 = kt.base(j);
+        if (!(t0 + PF_KEYS - 1 <= pmin && (t0 + PF_KEYS <= A.a.sinks || t0 > pmax - A.a.window))) {
+          const int hi = pos - t0, lo = pos - A.a.window + 1 - t0, sk = A.a.sinks - t0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = i <= hi && (i >= lo || i < sk) ? x[i] : NEG_INF;
+        }
+        float t[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = x[k];
+#pragma unroll
+        for (int i = 4; i < 128; ++i) t[i & 3] = fmaxf(t[i & 3], x[i]);
+        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale2;
+        const bool raise = top > mx + LAZY_MAX || (mx == NEG_INF && top > NEG_INF);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
+          l *= f;
+          if (raise) mx = top;
+          if (j > 0) {   // the product before S is done: S was issued after it
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+        }
+        const float ref = mx == NEG_INF ? 0.0f : -mx;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          x[i] = ex2f(fmaf(x[i], scale2, ref));
+          sum[i & 1] += x[i];
+        }
+        l += sum[0] + sum[1];
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) pk[i] = bf16x2(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
+          tmem_st32(ts + 32 * c, pk);
+        }
+        if constexpr (F32) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float u = x[64 * c + 2 * i], v = x[64 * c + 2 * i + 1];
+              pk[i] = bf16x2(u - bf16_hi(u), v - bf16_hi(v));
+            }
+            tmem_st32(ts + 64 + 32 * c, pk);
+          }
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[a]);
+      }
+      ok = ok && (kt.count == 0 || mbar_wait(&sm.o_full[a], 0));
+      if (!ok) gave_up();
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        const size_t row = (size_t)(A.row[ri] + tok0 + tok) * A.a.Hq + (size_t)head * A.G + (r & (A.G - 1));
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (valid && A.a.lse) A.a.lse[row] = l != 0.0f ? (mx + log2f(l)) * 0.6931471805599453f : NEG_INF;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          __syncwarp();
+          if (kt.count > 0) {
+            tmem_ld32(to + 32 * c, o);
+            tc_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+          if (!valid) {
+          } else if constexpr (F32) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(A.a.out) + row * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + row * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        __syncwarp();
+        tc_fence_before();
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a,
+                                 const CUtensorMap& q_map, const CUtensorMap& kv_map, cudaStream_t s) {
+  PrefillArgs A;
+  A.p = p;
+  A.a = a;
+  A.n = n;
+  A.G = a.Hq / p.Hkv;
+  A.lg = A.G == 1 ? 0 : A.G == 2 ? 1 : A.G == 4 ? 2 : 3;
+  const int per_block = 2 * PF_ROWS / A.G;
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    A.len[i] = reqs[i].len;
+    A.m[i] = reqs[i].m;
+    A.row[i] = reqs[i].row;
+    A.table[i] = reqs[i].table;
+    A.bstart[i] = static_cast<int32_t>(blocks);
+    blocks += (reqs[i].m + per_block - 1) / per_block;
+  }
+  A.bstart[n] = static_cast<int32_t>(blocks);
+  if (blocks * p.Hkv > INT32_MAX) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks * p.Hkv);
+  constexpr int bytes = static_cast<int>(sizeof(PrefillSmem)) + 1024;
+  auto kernel = a.f32 ? paged_prefill_kernel<true> : paged_prefill_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
+  return cudaGetLastError();
+}
+
+}  // namespace oscar
