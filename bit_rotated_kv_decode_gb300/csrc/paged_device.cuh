@@ -11,8 +11,7 @@
 namespace oscar {
 namespace paged {
 
-constexpr uint32_t SUSPEND_NS = 20000;        // a waiting thread sleeps until the phase completes
-constexpr uint32_t WAIT_ROUNDS = 100000;      // rounds (up to SUSPEND_NS each) before a wait gives up
+constexpr uint64_t WAIT_NS = 2000000000;      // time before a wait gives up
 constexpr float LAZY_MAX = 8.0f;              // the softmax reference moves only when exceeded by 2^8
 constexpr float NEG_INF = -INFINITY;
 
@@ -34,16 +33,28 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(SUSPEND_NS)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return done != 0;
 }
-// Bounded wait for the phase with the given parity; false if it gave up.
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait for the phase with the given parity; false if it gave up after
+// WAIT_NS.  (Without a suspend hint: with one of 20 us a warp woke up to 700 cycles
+// after the phase.)
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
-  for (uint32_t it = 0; it < WAIT_ROUNDS; ++it)
-    if (mbar_try(bar, parity)) return true;
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t start = now_ns();
+  do {
+#pragma unroll 1
+    for (int it = 0; it < 64; ++it)
+      if (mbar_try(bar, parity)) return true;
+  } while (now_ns() - start < WAIT_NS);
   return false;
 }
 __device__ __forceinline__ void tma_load_1d(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

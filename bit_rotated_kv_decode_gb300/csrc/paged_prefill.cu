@@ -14,10 +14,17 @@
 // rounding); for fp32 outputs it is carried as two bf16 parts, in the columns that S
 // leaves.  Sums are taken of the unrounded weights, in fp32.
 //
-// Roles: warps 0-3 and 4-7 the softmax of query tile 0 and 1 (TMEM lane = row), warp 8
-// issues the products, warp 9 the TMA copies (Q once, K and V tiles through a ring of
-// five 32 KB stages).  While one query tile's softmax runs, the tensor core works on
-// the other's products.  TMEM: S0, S1 (P over them), O0, O1, 128 columns each.
+// Roles: warps 0-3 and 4-7 the softmax of query tile 0 and 1, one thread per row (TMEM
+// lane = row); warps 8 and 9 the products of query tile 0 and 1; warp 10 the TMA copies.
+// A query tile's chain is S -> softmax -> PV -> S of the next key tile, since P lies over
+// S in TMEM (S0, S1, O0, O1 take all 512 columns); the two query tiles' chains interleave.
+// P is handed over in halves of 64 keys.  Issuing is synchronous (64 cycles a product of
+// 128 x 128 x 16, as long as it runs; 110 a commit, 140 a wait even when ready), so one
+// warp issuing for both tiles left the tensor core idle for 1100 of 3430 cycles a key
+// tile; hence a warp for each, and V of a key tile and K of the next share a stage (two
+// stages of 64 KB), one wait and one commit.  The two take turns, [PV, S] of a key tile
+// each: left to themselves both tiles fall into step, softmax against softmax and product
+// against product (3540 cycles a key tile).
 #include "paged_device.cuh"
 
 namespace oscar {
@@ -25,17 +32,19 @@ namespace {
 
 using namespace paged;
 
-constexpr int PF_THREADS = 320;
-constexpr int PF_STAGES = 5;
+constexpr int PF_MMA_WARP = 8, PF_TMA_WARP = 10;
+constexpr int PF_THREADS = 32 * 11;
+constexpr int PF_STAGES = 2;                   // of V of a key tile and K of the next
 constexpr int PF_ROWS = 128;                   // rows of a query tile
 constexpr int PF_KEYS = 128;                   // keys of a tile: two pages
 constexpr int TILE_BYTES = 128 * D * 2;        // a Q, K or V tile
 
 struct alignas(1024) PrefillSmem {
   alignas(1024) uint8_t q[2][TILE_BYTES];      // per tile: two halves of 64 channels, [128 rows][128 B] swizzled
-  alignas(1024) uint8_t kv[PF_STAGES][TILE_BYTES];
+  alignas(1024) uint8_t kv[PF_STAGES][2][TILE_BYTES];   // V of key tile j - 1, K of key tile j
   uint64_t q_full, kv_full[PF_STAGES], kv_empty[PF_STAGES];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];   // per query tile (and half of the keys)
+  uint64_t turn[2];                              // the other tile's products of a key tile are issued
   uint32_t tmem;
 };
 static_assert(sizeof(PrefillSmem) + 1024 <= 232448, "shared memory of a CTA");
@@ -89,11 +98,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      OSCAR_W8(r, 0), OSCAR_W8(r, 8), OSCAR_W8(r, 16), OSCAR_W8(r, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : OSCAR_R8(r, 0), OSCAR_R8(r, 8)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      OSCAR_W8(r, 0), OSCAR_W8(r, 8)
       : "memory");
 }
 #undef OSCAR_R8
@@ -114,22 +130,60 @@ __device__ __forceinline__ uint64_t desc_nmajor(uint32_t addr) {
 constexpr uint32_t IDESC_QK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t IDESC_PV = IDESC_QK | (1u << 16);
 
+// Issued by one elected lane of a converged warp: the code around stays uniform, so that
+// descriptors are computed in uniform registers (under an if of one lane, each product
+// cost its six operand moves, and a key tile of the issuing warp 4700 cycles).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(
-          d),
+      "{\n .reg .pred p, q;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// A warp's wait (skipped where an earlier one gave up), the same answer for all lanes.
+// All lanes poll: handing one lane's answer round took 200 cycles more.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, bool ok) {
+  return ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
 template <bool F32>
@@ -162,16 +216,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     mbar_init(&sm.q_full, 1);
     for (int s = 0; s < PF_STAGES; ++s) {
       mbar_init(&sm.kv_full[s], 1);
-      mbar_init(&sm.kv_empty[s], 1);
+      mbar_init(&sm.kv_empty[s], tiles);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sm.s_full[a], 1);
-      mbar_init(&sm.p_full[a], 4);
+      mbar_init(&sm.p_full[a][0], 4);
+      mbar_init(&sm.p_full[a][1], 4);
       mbar_init(&sm.o_full[a], 1);
+      mbar_init(&sm.turn[a], 1);
     }
     mbar_init_fence();
   }
-  if (warp == 8) {
+  if (warp == PF_MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -179,12 +235,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  constexpr uint32_t tmem = 0;   // all 512 columns are the CTA's
   auto gave_up = [&]() {
     if (A.p.err) atomicOr(A.p.err, PAGED_ERR_TIMEOUT);
   };
 
-  if (warp == 9) {
+  if (warp == PF_TMA_WARP) {
     // ---- copies
     if (lane == 0 && kt.count > 0) {
       mbar_expect_tx(&sm.q_full, tiles * TILE_BYTES);
@@ -193,120 +249,126 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, head * A.G, A.row[ri] + tok0 + a * per_tile,
                       &sm.q_full);
       const int32_t* pt = A.p.table + (size_t)A.table[ri] * A.p.max_pages;
-      int it = 0;
-      bool ok = true;
-      for (int j = 0; j < kt.count && ok; ++j) {
+      // records of the pages of key tile j, -1: none that a row sees
+      auto tile_records = [&](int j, int (&rec)[2]) {
         const int t0 = kt.base(j);
-        int page[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          page[u] = -1;
-          if (kt.any(t0 + PAGE * u, PAGE)) {
-            page[u] = __ldg(pt + t0 / PAGE + u);
-            if (page[u] < 0 || page[u] >= A.p.num_pages) {
-              if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
-              page[u] = 0;
-            }
+          rec[u] = -1;
+          if (!kt.any(t0 + PAGE * u, PAGE)) continue;
+          int page = __ldg(pt + t0 / PAGE + u);
+          if (page < 0 || page >= A.p.num_pages) {
+            if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
+            page = 0;
           }
+          rec[u] = static_cast<int>(2 * ((int64_t)page * A.p.Hkv + head));
         }
-        for (int v = 0; v < 2 && ok; ++v, ++it) {   // K, then V
-          const int st = it % PF_STAGES;
-          if (it >= PF_STAGES && !mbar_wait(&sm.kv_empty[st], (it / PF_STAGES - 1) & 1)) {
-            gave_up();
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(&sm.kv_full[st], ((page[0] >= 0) + (page[1] >= 0)) * (TILE_BYTES / 2));
+      };
+      auto load = [&](uint8_t* dst, const int (&rec)[2], int which, uint64_t* bar) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (page[u] >= 0)
-              for (int h = 0; h < 2; ++h)
-                tma_load_3d(sm.kv[st] + h * (TILE_BYTES / 2) + u * (TILE_BYTES / 4), &kv_map, 64 * h, 0,
-                            static_cast<int>(2 * ((int64_t)page[u] * A.p.Hkv + head)) + v, &sm.kv_full[st]);
+        for (int u = 0; u < 2; ++u)
+          if (rec[u] >= 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(dst + h * (TILE_BYTES / 2) + u * (TILE_BYTES / 4), &kv_map, 64 * h, 0, rec[u] + which, bar);
+      };
+      int cur[2], next[2] = {-1, -1}, last[2] = {-1, -1};
+      tile_records(0, next);
+      for (int i = 0; i <= kt.count; ++i) {   // stage i: V of tile i - 1, K of tile i
+        const int st = i % PF_STAGES;
+        cur[0] = next[0], cur[1] = next[1];   // tile i (none behind the last)
+        int prev[2] = {-1, -1};
+        if (i > 0) prev[0] = last[0], prev[1] = last[1];
+        if (i >= PF_STAGES && !mbar_wait(&sm.kv_empty[st], (i / PF_STAGES - 1) & 1)) {
+          gave_up();
+          // no copy may be in flight when the CTA ends
+          mbar_wait(&sm.q_full, 0);
+          for (int k = i - PF_STAGES; k < i; ++k) mbar_wait(&sm.kv_full[k % PF_STAGES], (k / PF_STAGES) & 1);
+          break;
         }
-      }
-      // no copy of this CTA is in flight when it ends (the products wait for each)
-      if (!ok) {
-        mbar_wait(&sm.q_full, 0);
-        for (int k = max(0, it - PF_STAGES); k < it; ++k) mbar_wait(&sm.kv_full[k % PF_STAGES], (k / PF_STAGES) & 1);
+        const int tiles_of = (prev[0] >= 0) + (prev[1] >= 0) + (i < kt.count ? (cur[0] >= 0) + (cur[1] >= 0) : 0);
+        mbar_expect_tx(&sm.kv_full[st], tiles_of * (TILE_BYTES / 2));
+        load(sm.kv[st][0], prev, 1, &sm.kv_full[st]);
+        if (i < kt.count) load(sm.kv[st][1], cur, 0, &sm.kv_full[st]);
+        last[0] = cur[0], last[1] = cur[1];
+        if (i + 1 < kt.count) tile_records(i + 1, next);
       }
     }
-  } else if (warp == 8) {
-    // ---- products
-    if (kt.count > 0) {
-      // waits end the same way for the whole warp
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
-      bool ok = wait(&sm.q_full, 0);
-      auto full = [&](int it) { return ok && wait(&sm.kv_full[it % PF_STAGES], (it / PF_STAGES) & 1); };
-      auto score = [&](int a, int it) {
-        const uint32_t q = smem_u32(sm.q[a]), k = smem_u32(sm.kv[it % PF_STAGES]);
+  } else if (warp >= PF_MMA_WARP) {
+    // ---- products of query tile a
+    const int a = warp - PF_MMA_WARP;
+    if (a < tiles && kt.count > 0) {
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { ok = mbar_wait_warp(bar, parity, ok); };
+      const uint64_t q = desc_kmajor(smem_u32(sm.q[a])), k_desc = desc_kmajor(smem_u32(sm.kv[0][1])),
+                     v_desc = desc_nmajor(smem_u32(sm.kv[0][0]));
+      const uint32_t s_col = 128 * a, o_col = 256 + 128 * a;
+      auto pass_turn = [&]() {
+        if (tiles == 2) mbar_arrive_elected(&sm.turn[a ^ 1]);
+      };
+      auto score = [&](int st, bool pass) {
+        const uint64_t k = k_desc + st * (2 * TILE_BYTES >> 4);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          const uint32_t off = (s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32;
-          mma_ss(tmem + 128 * a, desc_kmajor(q + off), desc_kmajor(k + off), IDESC_QK, s > 0);
+          if (s == 6 && pass) pass_turn();   // the last two cover the other warp's waking
+          const uint64_t off = ((s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32) >> 4;
+          mma_ss(s_col, q + off, k + off, IDESC_QK, s > 0);
         }
         mma_commit(&sm.s_full[a]);
       };
-      ok = full(0);
-      if (ok && lane == 0) {
+      wait(&sm.q_full, 0);
+      wait(&sm.kv_full[0], 0);
+      if (ok) {
         tc_fence_after();
-        for (int a = 0; a < tiles; ++a) score(a, 0);
+        score(0, false);
         mma_commit(&sm.kv_empty[0]);
       }
-      __syncwarp();
       for (int j = 0; j < kt.count && ok; ++j) {
-        const int itv = 2 * j + 1, itk = 2 * j + 2;
-        const bool more = j + 1 < kt.count;
-        for (int a = 0; a < tiles && ok; ++a) {
-          if (a == 0) {
-            ok = full(itv);
-            const int t0 = kt.base(j);
-            if (ok && !kt.all(t0, PF_KEYS)) {
-              // value rows that no row sees may hold anything (or were not copied): zero them
-              uint8_t* v = sm.kv[itv % PF_STAGES];
-              for (int r = lane >> 3; r < PF_KEYS; r += 4)
-                if (!kt.any(t0 + r, 1)) {
-                  uint4* dst = reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16);
-                  dst[0] = make_uint4(0, 0, 0, 0);
-                  dst[TILE_BYTES / 32] = make_uint4(0, 0, 0, 0);
-                }
-              fence_async_smem();
-              __syncwarp();
+        const int i = j + 1, st = i % PF_STAGES, t0 = kt.base(j);
+        wait(&sm.kv_full[st], (i / PF_STAGES) & 1);
+        if (!kt.all(t0, PF_KEYS)) {
+          // value rows that no row sees may hold anything (or were not copied): zero them
+          // (both tiles' warps do, each before its own product)
+          uint8_t* v = sm.kv[st][0];
+          for (int r = lane >> 3; r < PF_KEYS; r += 4)
+            if (!kt.any(t0 + r, 1)) {
+              uint4* dst = reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16);
+              dst[0] = make_uint4(0, 0, 0, 0);
+              dst[TILE_BYTES / 32] = make_uint4(0, 0, 0, 0);
             }
-          }
-          ok = ok && wait(&sm.p_full[a], j & 1);
-          if (ok && lane == 0) {
-            tc_fence_after();
-            const uint32_t v = smem_u32(sm.kv[itv % PF_STAGES]);
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-              mma_ts(tmem + 256 + 128 * a, tmem + 128 * a + 8 * s, desc_nmajor(v + 2048 * s), IDESC_PV,
-                     (j > 0 || s > 0) ? 1u : 0u);
-            if constexpr (F32) {
-#pragma unroll
-              for (int s = 0; s < 8; ++s)
-                mma_ts(tmem + 256 + 128 * a, tmem + 128 * a + 64 + 8 * s, desc_nmajor(v + 2048 * s), IDESC_PV, 1u);
-            }
-          }
+          fence_async_smem();
           __syncwarp();
-          if (more) {
-            if (a == 0) ok = full(itk);
-            if (ok && lane == 0) score(a, itk);
-          } else if (ok && lane == 0) {
-            mma_commit(&sm.o_full[a]);
+        }
+        const uint64_t v = v_desc + st * (2 * TILE_BYTES >> 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // P's halves, 64 keys each
+          wait(&sm.p_full[a][h], j & 1);
+          if (h == 0 && tiles == 2 && a + j > 0) wait(&sm.turn[a], (a == 0 ? j - 1 : j) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mma_ts(o_col, s_col + 64 * h + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV,
+                   (j > 0 || h > 0 || s > 0) ? 1u : 0u);
+          if constexpr (F32) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              mma_ts(o_col, s_col + 64 * h + 32 + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV, 1u);
           }
-          // (nobody waits for the last stages; an arrival must not come after the CTA)
-          if (ok && lane == 0 && a == tiles - 1 && more) {
-            mma_commit(&sm.kv_empty[itv % PF_STAGES]);
-            mma_commit(&sm.kv_empty[itk % PF_STAGES]);
-          }
-          __syncwarp();
+        }
+        if (!ok) break;
+        if (j + 1 < kt.count) {
+          score(st, true);
+          mma_commit(&sm.kv_empty[st]);
+        } else {   // (nobody waits for the last stage)
+          pass_turn();
+          mma_commit(&sm.o_full[a]);
         }
       }
       if (!ok && lane == 0) gave_up();
     }
   } else {
-    // ---- softmax of query tile a
+    // ---- softmax of query tile a, one thread per row
     const int a = warp >> 2, r = threadIdx.x & 127;
     if (a < tiles) {
       const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -319,10 +381,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       float mx = NEG_INF, l = 0.0f;
       bool ok = true;
       for (int j = 0; j < kt.count; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[a], j & 1))) {
-          ok = false;
-          break;
-        }
+        ok = mbar_wait_warp(&sm.s_full[a], j & 1, ok);
+        if (!ok) break;
         tc_fence_after();
         uint32_t xr[128];
 #pragma unroll
@@ -339,81 +399,81 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) t[k] = x[k];
 #pragma unroll
-        for (int i = 4; i < 128; ++i) t[i & 3] = fmaxf(t[i & 3], x[i]);
-        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale2;
+        for (int i = 4; i < 124; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[i + 2 * k], x[i + 2 * k + 1]);
+        const float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])) * scale2;
         const bool raise = top > mx + LAZY_MAX || (mx == NEG_INF && top > NEG_INF);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
           l *= f;
           if (raise) mx = top;
           if (j > 0) {   // the product before S is done: S was issued after it
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32(to + 32 * c, o);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 16) {   // in small pieces: the logits are live
+              uint32_t o[16];
+              tmem_ld16(to + c, o);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(to + 32 * c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(to + c, o);
             }
           }
         }
         const float ref = mx == NEG_INF ? 0.0f : -mx;
-        float sum[2] = {0.0f, 0.0f};
+        const float2 scale_2 = make_float2(scale2, scale2), ref_2 = make_float2(ref, ref);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        // 64 keys at a time: the product of the first half starts while the second is computed
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
-          x[i] = ex2f(fmaf(x[i], scale2, ref));
-          sum[i & 1] += x[i];
-        }
-        l += sum[0] + sum[1];
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = bf16x2(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
-          tmem_st32(ts + 32 * c, pk);
-        }
-        if constexpr (F32) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16], low[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float u = x[64 * c + 2 * i], v = x[64 * c + 2 * i + 1];
-              pk[i] = bf16x2(u - bf16_hi(u), v - bf16_hi(v));
+            for (int i = 0; i < 16; ++i) {
+              const int e = 64 * h + 32 * c + 2 * i;
+              float2 y = fma2(make_float2(x[e], x[e + 1]), scale_2, ref_2);
+              y.x = ex2f(y.x);
+              y.y = ex2f(y.y);
+              sum[i & 1] = add2(sum[i & 1], y);
+              pk[i] = bf16x2(y.x, y.y);
+              if constexpr (F32)
+                low[i] = bf16x2(y.x - __uint_as_float(pk[i] << 16), y.y - __uint_as_float(pk[i] & 0xffff0000u));
             }
-            tmem_st32(ts + 64 + 32 * c, pk);
+            tmem_st16(ts + 64 * h + 16 * c, pk);
+            if constexpr (F32) tmem_st16(ts + 64 * h + 32 + 16 * c, low);
           }
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[a][h]);
         }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[a]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      ok = ok && (kt.count == 0 || mbar_wait(&sm.o_full[a], 0));
+      if (kt.count > 0) ok = mbar_wait_warp(&sm.o_full[a], 0, ok);
       if (!ok) gave_up();
-      ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
         const size_t row = (size_t)(A.row[ri] + tok0 + tok) * A.a.Hq + (size_t)head * A.G + (r & (A.G - 1));
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         if (valid && A.a.lse) A.a.lse[row] = l != 0.0f ? (mx + log2f(l)) * 0.6931471805599453f : NEG_INF;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 128; c += 32) {
           uint32_t o[32];
           __syncwarp();
           if (kt.count > 0) {
-            tmem_ld32(to + 32 * c, o);
+            tmem_ld32(to + c, o);
             tc_wait_ld();
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
           if (!valid) {
           } else if constexpr (F32) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(A.a.out) + row * D + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(A.a.out) + row * D + c);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + row * D + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + row * D + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t w[4];
@@ -431,7 +491,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == PF_MMA_WARP) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
@@ -462,8 +522,15 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   const unsigned grid = static_cast<unsigned>(blocks * p.Hkv);
   constexpr int bytes = static_cast<int>(sizeof(PrefillSmem)) + 1024;
   auto kernel = a.f32 ? paged_prefill_kernel<true> : paged_prefill_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static unsigned done[2] = {0, 0};   // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 32 || !(done[a.f32 != 0] & (1u << dev))) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 32) done[a.f32 != 0] |= 1u << dev;
+  }
   kernel<<<grid, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
   return cudaGetLastError();
 }
