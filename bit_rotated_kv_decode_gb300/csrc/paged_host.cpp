@@ -193,7 +193,8 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
         !map_3d(&q_map, q, static_cast<cuuint64_t>(hq), static_cast<cuuint64_t>(rows), D * 2,
                 static_cast<cuuint64_t>(q_stride) * 2, static_cast<uint32_t>(G), static_cast<uint32_t>(128 / G)))
       return fail(OSCAR_ERR_CUDA, "tensor map of the pool or of q");
-    const cudaError_t e = launch_paged_prefill(p, reqs, count, a, q_map, kv_map, s);
+    const cudaError_t e = launch_paged_prefill(p, reqs, count, a, q_map, kv_map,
+                                               static_cast<char*>(workspace) + PAGED_COUNTER_BYTES, sms, s);
     if (e != cudaSuccess) return from_cuda(e);
   }
   if (!few) return OSCAR_OK;
@@ -263,15 +264,21 @@ size_t oscar_attention_workspace_bytes(int32_t n, const int32_t* q_lens, int32_t
   if (n < 1 || n > PAGED_MAX_REQ || !group_ok(num_q_heads, num_kv_heads) ||
       (int64_t)n * num_kv_heads > (int64_t)PAGED_COUNTERS)
     return 0;
-  const int G = num_q_heads / num_kv_heads;
-  int most = 0;
+  const int G = num_q_heads / num_kv_heads, sms = sm_count();
+  int few = 1;            // most rows of a decode segment
+  int64_t blocks = 0;     // 256-row blocks of the longer requests
   for (int32_t i = 0; i < n; ++i) {
-    const int32_t m = q_lens ? q_lens[i] : 1;
+    const int64_t m = q_lens ? q_lens[i] : 1;
     if (m < 0) return 0;
-    most = m > most ? m : most;
+    if (m * G > DECODE_MAX_ROWS)
+      blocks += paged_prefill_blocks(static_cast<int>(m), G);
+    else if (m * G > few)
+      few = static_cast<int>(m) * G;
   }
-  const int rows = most * G > DECODE_MAX_ROWS ? DECODE_MAX_ROWS : (most ? most : 1) * G;
-  return PAGED_COUNTER_BYTES + paged_decode_record_bytes(n * num_kv_heads, rows, sm_count());
+  // both kernels use the same bytes, one after the other
+  const size_t decode = paged_decode_record_bytes(n * num_kv_heads, few, sms);
+  const size_t prefill = paged_prefill_partial_bytes(blocks, num_kv_heads, sms);
+  return PAGED_COUNTER_BYTES + (decode > prefill ? decode : prefill);
 }
 
 oscar_status oscar_window_attention(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,

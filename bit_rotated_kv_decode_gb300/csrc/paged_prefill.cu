@@ -3,7 +3,7 @@
 // A CTA takes 256 query rows of one kv head: two tiles of 128 rows, a row being a
 // (token, head of the group) pair, token by token, so the G heads of a group share
 // every key and value that is loaded and the causal edge crosses few tiles.  It
-// walks the 128-key tiles (two pages) that its rows see: the sinks' first, then the
+// walks the pages that its rows see, two at a time: the sinks' first, then the
 // window's.  Per key tile and query tile
 //   S = Q K^T            128 x 128 x 128, tcgen05.mma, both operands in shared memory
 //   p = exp2(S scale - m)   one thread per row, m the running maximum
@@ -25,6 +25,11 @@
 // stages of 64 KB), one wait and one commit.  The two take turns, [PV, S] of a key tile
 // each: left to themselves both tiles fall into step, softmax against softmax and product
 // against product (3540 cycles a key tile).
+//
+// One persistent CTA per SM walks the items (256 rows x kv head), so that the copies and
+// the first products of an item run under the end of the one before.  Where the items
+// would leave most SMs idle (a few query tokens on a long cache) an item's key tiles are
+// split, its unnormalised rows go to the workspace and a second kernel folds them.
 #include "paged_device.cuh"
 
 namespace oscar {
@@ -33,17 +38,21 @@ namespace {
 using namespace paged;
 
 constexpr int PF_MMA_WARP = 8, PF_TMA_WARP = 10;
-constexpr int PF_THREADS = 32 * 11;
+constexpr int PF_THREADS = 32 * 12;            // three warpgroups, the last with one idle warp
+// Registers a thread: 168 at launch (three warpgroups share 504), then 208 for the
+// softmax's two warpgroups, which hold a row of logits each, and 88 for the third.
+constexpr int PF_REGS = 168, PF_SOFTMAX_REGS = 208, PF_OTHER_REGS = 88;
+static_assert(2 * PF_SOFTMAX_REGS + PF_OTHER_REGS <= 3 * PF_REGS, "a split above the launch's registers waits forever");
 constexpr int PF_STAGES = 2;                   // of V of a key tile and K of the next
 constexpr int PF_ROWS = 128;                   // rows of a query tile
-constexpr int PF_KEYS = 128;                   // keys of a tile: two pages
+constexpr int PF_KEYS = 2 * PAGE;              // keys of a tile
 constexpr int TILE_BYTES = 128 * D * 2;        // a Q, K or V tile
 
 struct alignas(1024) PrefillSmem {
   alignas(1024) uint8_t q[2][TILE_BYTES];      // per tile: two halves of 64 channels, [128 rows][128 B] swizzled
   alignas(1024) uint8_t kv[PF_STAGES][2][TILE_BYTES];   // V of key tile j - 1, K of key tile j
-  uint64_t q_full, kv_full[PF_STAGES], kv_empty[PF_STAGES];
-  uint64_t s_full[2], p_full[2][2], o_full[2];   // per query tile (and half of the keys)
+  uint64_t q_full[2], q_empty[2], kv_full[PF_STAGES], kv_empty[PF_STAGES];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];   // per query tile (and half of the keys)
   uint64_t turn[2];                              // the other tile's products of a key tile are issued
   uint32_t tmem;
 };
@@ -53,6 +62,8 @@ struct PrefillArgs {
   PagedView p;
   AttnArgs a;
   int n, G, lg;                           // lg = log2 G
+  int splits, items;                      // parts of an item's key tiles; items in all, parts counted
+  float* partials;                        // [items][256][PARTIAL_FLOATS] where splits > 1
   int32_t len[PAGED_MAX_REQ];
   int32_t m[PAGED_MAX_REQ];
   int32_t row[PAGED_MAX_REQ];
@@ -60,27 +71,66 @@ struct PrefillArgs {
   int32_t bstart[PAGED_MAX_REQ + 1];      // 256-row blocks before request i (one kv head)
 };
 
-// The key tiles that the rows at positions [pmin, pmax] see: [0, sink), then
-// [first, first + count - sink).
+// The keys that the rows at positions [pmin, pmax] see, as a list of pages: [0, sink),
+// then [first, first + pages - sink).  A key tile is two neighbours of the list, not of
+// the cache: four sinks cost a window of 1024 half a tile, not a whole one.
 struct KeyTiles {
-  int sink, first, count;
+  int sink, first, pages, count;
   int lo, sinks, pmax;     // tokens t <= pmax with t < sinks or t >= lo are seen by some row
   __device__ static KeyTiles of(int pmin, int pmax, int window, int sinks) {
     KeyTiles k;
     k.pmax = pmax;
     k.sinks = min(sinks, pmax + 1);
     k.lo = window > 0 ? max(0, pmin - window + 1) : pmax + 1;
-    k.sink = (k.sinks + PF_KEYS - 1) / PF_KEYS;
-    k.first = max(k.lo / PF_KEYS, k.sink);
-    const int end = window > 0 ? pmax / PF_KEYS + 1 : 0;
-    k.count = k.sink + max(0, end - k.first);
+    k.sink = (k.sinks + PAGE - 1) / PAGE;
+    k.first = max(k.lo / PAGE, k.sink);
+    const int end = window > 0 ? pmax / PAGE + 1 : 0;
+    k.pages = k.sink + max(0, end - k.first);
+    k.count = (k.pages + 1) / 2;
     return k;
   }
-  __device__ int base(int j) const { return (j < sink ? j : first + (j - sink)) * PF_KEYS; }
-  // whether some row sees a token of [t, t + n)
-  __device__ bool any(int t, int n) const { return t <= pmax && (t < sinks || t + n > lo); }
-  __device__ bool all(int t, int n) const { return t + n - 1 <= pmax && (t + n <= sinks || t >= lo); }
+  // first token of page v of the list; behind its end, tokens that no row sees
+  __device__ int base(int v) const { return v >= pages ? 1 << 30 : (v < sink ? v : first + (v - sink)) * PAGE; }
+  // whether some row sees token t; all of page v of the list
+  __device__ bool any(int t) const { return t <= pmax && (t < sinks || t >= lo); }
+  __device__ bool all(int v) const {
+    const int t = base(v);
+    return t + PAGE - 1 <= pmax && (t + PAGE <= sinks || t >= lo);
+  }
 };
+
+// One item: up to 256 query rows of a kv head and their key tiles [j0, j1) of kt.
+struct Item {
+  int index, ri, head, tok0, tokens, tiles, p0, j0, j1;
+  KeyTiles kt;
+  // Item of a CTA's turn, false behind the last.  Later blocks of a request see more
+  // keys and come first; every other round goes through the CTAs backwards, so that the
+  // longer items of a round fall to different CTAs.
+  __device__ bool load(const PrefillArgs& A, int turn) {
+    const int grid = gridDim.x, at = turn & 1 ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
+    index = turn * grid + at;
+    if (index >= A.items) return false;
+    head = index % A.p.Hkv;
+    const int rest = index / A.p.Hkv, split = rest % A.splits, blk = A.bstart[A.n] - 1 - rest / A.splits;
+    int hi = A.n;
+    ri = 0;
+    while (hi - ri > 1) {
+      const int mid = (ri + hi) >> 1;
+      if (A.bstart[mid] <= blk) ri = mid; else hi = mid;
+    }
+    const int m = A.m[ri], per_tile = PF_ROWS >> A.lg;
+    tok0 = (blk - A.bstart[ri]) * 2 * per_tile;   // first token of the block, of the request's m
+    tokens = min(2 * per_tile, m - tok0);
+    tiles = tokens > per_tile ? 2 : 1;
+    p0 = A.len[ri] - m + tok0;                    // its position
+    kt = KeyTiles::of(p0, p0 + tokens - 1, A.a.window, A.a.sinks);
+    j0 = kt.count * split / A.splits;
+    j1 = kt.count * (split + 1) / A.splits;
+    return true;
+  }
+};
+// turns of a CTA: all but the last are full rounds
+__device__ __forceinline__ int turns(const PrefillArgs& A) { return (A.items + gridDim.x - 1) / gridDim.x; }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -193,33 +243,19 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   extern __shared__ uint8_t pf_raw[];
   PrefillSmem& sm =
       *reinterpret_cast<PrefillSmem*>((reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // ---- the CTA's rows: later blocks of a request see more keys, so they go first
-  const int head = blockIdx.x % A.p.Hkv, blk = A.bstart[A.n] - 1 - static_cast<int>(blockIdx.x / A.p.Hkv);
-  int ri = 0;
-  {
-    int hi = A.n;
-    while (hi - ri > 1) {
-      const int mid = (ri + hi) >> 1;
-      if (A.bstart[mid] <= blk) ri = mid; else hi = mid;
-    }
-  }
-  const int m = A.m[ri], per_tile = PF_ROWS >> A.lg;
-  const int tok0 = (blk - A.bstart[ri]) * 2 * per_tile;          // first token of the block, of the request's m
-  const int tokens = min(2 * per_tile, m - tok0);
-  const int tiles = tokens > per_tile ? 2 : 1;
-  const int p0 = A.len[ri] - m + tok0;                           // its position
-  const KeyTiles kt = KeyTiles::of(p0, p0 + tokens - 1, A.a.window, A.a.sinks);
+  // (through a shuffle: uniform for the compiler too)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&sm.q_full, 1);
     for (int s = 0; s < PF_STAGES; ++s) {
       mbar_init(&sm.kv_full[s], 1);
-      mbar_init(&sm.kv_empty[s], tiles);
+      mbar_init(&sm.kv_empty[s], 2);
     }
     for (int a = 0; a < 2; ++a) {
+      mbar_init(&sm.q_full[a], 1);
+      mbar_init(&sm.q_empty[a], 1);
       mbar_init(&sm.s_full[a], 1);
+      mbar_init(&sm.o_empty[a], 4);
       mbar_init(&sm.p_full[a][0], 4);
       mbar_init(&sm.p_full[a][1], 4);
       mbar_init(&sm.o_full[a], 1);
@@ -240,148 +276,195 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     if (A.p.err) atomicOr(A.p.err, PAGED_ERR_TIMEOUT);
   };
 
-  if (warp == PF_TMA_WARP) {
-    // ---- copies
-    if (lane == 0 && kt.count > 0) {
-      mbar_expect_tx(&sm.q_full, tiles * TILE_BYTES);
-      for (int a = 0; a < tiles; ++a)
-        for (int h = 0; h < 2; ++h)
-          tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, head * A.G, A.row[ri] + tok0 + a * per_tile,
-                      &sm.q_full);
-      const int32_t* pt = A.p.table + (size_t)A.table[ri] * A.p.max_pages;
-      // records of the pages of key tile j, -1: none that a row sees
-      auto tile_records = [&](int j, int (&rec)[2]) {
-        const int t0 = kt.base(j);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          rec[u] = -1;
-          if (!kt.any(t0 + PAGE * u, PAGE)) continue;
-          int page = __ldg(pt + t0 / PAGE + u);
-          if (page < 0 || page >= A.p.num_pages) {
-            if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
-            page = 0;
-          }
-          rec[u] = static_cast<int>(2 * ((int64_t)page * A.p.Hkv + head));
-        }
-      };
-      auto load = [&](uint8_t* dst, const int (&rec)[2], int which, uint64_t* bar) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (rec[u] >= 0)
-#pragma unroll
+  const int rounds = turns(A), per_tile = PF_ROWS >> A.lg;
+  if (warp >= PF_MMA_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PF_OTHER_REGS));
+    Item it;
+    if (warp == PF_TMA_WARP) {
+      // ---- copies
+      if (lane == 0) {
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity); };
+        int stage = 0, q_loads[2] = {0, 0};   // stages and query tiles loaded so far
+        for (int turn = 0; turn < rounds && ok; ++turn) {
+          if (!it.load(A, turn)) break;
+          const KeyTiles& kt = it.kt;
+          if (it.j0 == it.j1) continue;
+          for (int a = 0; a < it.tiles; ++a) {
+            if (q_loads[a] > 0) wait(&sm.q_empty[a], (q_loads[a] - 1) & 1);
+            if (!ok) break;
+            ++q_loads[a];
+            mbar_expect_tx(&sm.q_full[a], TILE_BYTES);
             for (int h = 0; h < 2; ++h)
-              tma_load_3d(dst + h * (TILE_BYTES / 2) + u * (TILE_BYTES / 4), &kv_map, 64 * h, 0, rec[u] + which, bar);
-      };
-      int cur[2], next[2] = {-1, -1}, last[2] = {-1, -1};
-      tile_records(0, next);
-      for (int i = 0; i <= kt.count; ++i) {   // stage i: V of tile i - 1, K of tile i
-        const int st = i % PF_STAGES;
-        cur[0] = next[0], cur[1] = next[1];   // tile i (none behind the last)
-        int prev[2] = {-1, -1};
-        if (i > 0) prev[0] = last[0], prev[1] = last[1];
-        if (i >= PF_STAGES && !mbar_wait(&sm.kv_empty[st], (i / PF_STAGES - 1) & 1)) {
-          gave_up();
-          // no copy may be in flight when the CTA ends
-          mbar_wait(&sm.q_full, 0);
-          for (int k = i - PF_STAGES; k < i; ++k) mbar_wait(&sm.kv_full[k % PF_STAGES], (k / PF_STAGES) & 1);
-          break;
+              tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, it.head * A.G,
+                          A.row[it.ri] + it.tok0 + a * per_tile, &sm.q_full[a]);
+          }
+          const int32_t* pt = A.p.table + (size_t)A.table[it.ri] * A.p.max_pages;
+          // records of the pages of key tile j, -1: no second one
+          auto tile_records = [&](int j, int (&rec)[2]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              rec[u] = -1;
+              if (2 * j + u >= kt.pages) continue;
+              int page = __ldg(pt + kt.base(2 * j + u) / PAGE);
+              if (page < 0 || page >= A.p.num_pages) {
+                if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
+                page = 0;
+              }
+              rec[u] = static_cast<int>(2 * ((int64_t)page * A.p.Hkv + it.head));
+            }
+          };
+          auto load = [&](uint8_t* dst, const int (&rec)[2], int which, uint64_t* bar) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (rec[u] >= 0)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  tma_load_3d(dst + h * (TILE_BYTES / 2) + u * (TILE_BYTES / 4), &kv_map, 64 * h, 0, rec[u] + which, bar);
+          };
+          int prev[2] = {-1, -1}, cur[2];
+          tile_records(it.j0, cur);
+          for (int j = it.j0; j <= it.j1 && ok; ++j, ++stage) {   // V of tile j - 1, K of tile j
+            const int st = stage % PF_STAGES;
+            if (stage >= PF_STAGES) wait(&sm.kv_empty[st], (stage / PF_STAGES - 1) & 1);
+            if (!ok) break;
+            const int pages = (prev[0] >= 0) + (prev[1] >= 0) + (cur[0] >= 0) + (cur[1] >= 0);
+            mbar_expect_tx(&sm.kv_full[st], pages * (TILE_BYTES / 2));
+            load(sm.kv[st][0], prev, 1, &sm.kv_full[st]);
+            load(sm.kv[st][1], cur, 0, &sm.kv_full[st]);
+            prev[0] = cur[0], prev[1] = cur[1];
+            cur[0] = cur[1] = -1;
+            if (j + 1 < it.j1) tile_records(j + 1, cur);
+          }
         }
-        const int tiles_of = (prev[0] >= 0) + (prev[1] >= 0) + (i < kt.count ? (cur[0] >= 0) + (cur[1] >= 0) : 0);
-        mbar_expect_tx(&sm.kv_full[st], tiles_of * (TILE_BYTES / 2));
-        load(sm.kv[st][0], prev, 1, &sm.kv_full[st]);
-        if (i < kt.count) load(sm.kv[st][1], cur, 0, &sm.kv_full[st]);
-        last[0] = cur[0], last[1] = cur[1];
-        if (i + 1 < kt.count) tile_records(i + 1, next);
+        if (!ok) gave_up();
+        // nothing may arrive after the CTA: copies in flight, and the last commits
+        for (int k = max(0, stage - PF_STAGES); k < stage; ++k) {
+          mbar_wait(&sm.kv_full[k % PF_STAGES], (k / PF_STAGES) & 1);
+          if (ok) mbar_wait(&sm.kv_empty[k % PF_STAGES], (k / PF_STAGES) & 1);
+        }
+        for (int a = 0; a < 2; ++a)
+          if (q_loads[a] > 0) {
+            mbar_wait(&sm.q_full[a], (q_loads[a] - 1) & 1);
+            if (ok) mbar_wait(&sm.q_empty[a], (q_loads[a] - 1) & 1);
+          }
       }
-    }
-  } else if (warp >= PF_MMA_WARP) {
-    // ---- products of query tile a
-    const int a = warp - PF_MMA_WARP;
-    if (a < tiles && kt.count > 0) {
+    } else if (warp < PF_TMA_WARP) {
+      // ---- products of query tile a
+      const int a = warp - PF_MMA_WARP;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) { ok = mbar_wait_warp(bar, parity, ok); };
       const uint64_t q = desc_kmajor(smem_u32(sm.q[a])), k_desc = desc_kmajor(smem_u32(sm.kv[0][1])),
                      v_desc = desc_nmajor(smem_u32(sm.kv[0][0]));
       const uint32_t s_col = 128 * a, o_col = 256 + 128 * a;
-      auto pass_turn = [&]() {
-        if (tiles == 2) mbar_arrive_elected(&sm.turn[a ^ 1]);
-      };
-      auto score = [&](int st, bool pass) {
-        const uint64_t k = k_desc + st * (2 * TILE_BYTES >> 4);
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          if (s == 6 && pass) pass_turn();   // the last two cover the other warp's waking
-          const uint64_t off = ((s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32) >> 4;
-          mma_ss(s_col, q + off, k + off, IDESC_QK, s > 0);
+      int stage = 0;      // stages taken so far
+      int batch = 0;      // [PV, S] turns of items with two tiles
+      int tile = 0;       // key tiles of this query tile
+      int done = 0;       // items of this query tile
+      for (int turn = 0; turn < rounds && ok; ++turn) {
+        if (!it.load(A, turn)) break;
+        const KeyTiles& kt = it.kt;
+        if (it.j0 == it.j1) continue;
+        const bool two = it.tiles == 2;
+        if (a >= it.tiles) {   // no rows: only free the stages
+          for (int j = it.j0; j <= it.j1 && ok; ++j, ++stage) {
+            wait(&sm.kv_full[stage % PF_STAGES], (stage / PF_STAGES) & 1);
+            if (ok) mbar_arrive_elected(&sm.kv_empty[stage % PF_STAGES]);
+          }
+          continue;
         }
-        mma_commit(&sm.s_full[a]);
-      };
-      wait(&sm.q_full, 0);
-      wait(&sm.kv_full[0], 0);
-      if (ok) {
+        auto pass_turn = [&]() {
+          if (two) mbar_arrive_elected(&sm.turn[a ^ 1]);
+        };
+        auto score = [&](int st, bool pass) {
+          const uint64_t k = k_desc + st * (2 * TILE_BYTES >> 4);
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            if (s == 6 && pass) pass_turn();   // the last two cover the other warp's waking
+            const uint64_t off = ((s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32) >> 4;
+            mma_ss(s_col, q + off, k + off, IDESC_QK, s > 0);
+          }
+          mma_commit(&sm.s_full[a]);
+        };
+        wait(&sm.q_full[a], done & 1);
+        wait(&sm.kv_full[stage % PF_STAGES], (stage / PF_STAGES) & 1);
+        if (!ok) break;
         tc_fence_after();
-        score(0, false);
-        mma_commit(&sm.kv_empty[0]);
-      }
-      for (int j = 0; j < kt.count && ok; ++j) {
-        const int i = j + 1, st = i % PF_STAGES, t0 = kt.base(j);
-        wait(&sm.kv_full[st], (i / PF_STAGES) & 1);
-        if (!kt.all(t0, PF_KEYS)) {
-          // value rows that no row sees may hold anything (or were not copied): zero them
-          // (both tiles' warps do, each before its own product)
-          uint8_t* v = sm.kv[st][0];
-          for (int r = lane >> 3; r < PF_KEYS; r += 4)
-            if (!kt.any(t0 + r, 1)) {
-              uint4* dst = reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16);
-              dst[0] = make_uint4(0, 0, 0, 0);
-              dst[TILE_BYTES / 32] = make_uint4(0, 0, 0, 0);
-            }
-          fence_async_smem();
-          __syncwarp();
-        }
-        const uint64_t v = v_desc + st * (2 * TILE_BYTES >> 4);
+        score(stage % PF_STAGES, false);
+        mma_commit(&sm.kv_empty[stage % PF_STAGES]);
+        ++stage;
+        if (done > 0) wait(&sm.o_empty[a], (done - 1) & 1);   // the last item's rows are out of O
+        for (int j = it.j0; j < it.j1 && ok; ++j, ++stage, ++tile, batch += two) {
+          const int st = stage % PF_STAGES;
+          wait(&sm.kv_full[st], (stage / PF_STAGES) & 1);
+          if (!kt.all(2 * j) || !kt.all(2 * j + 1)) {
+            // value rows that no row sees may hold anything (or were not copied): zero them
+            // (both tiles' warps do, each before its own product)
+            uint8_t* v = sm.kv[st][0];
+            for (int r = lane >> 3; r < PF_KEYS; r += 4)
+              if (!kt.any(kt.base(2 * j + r / PAGE) + r % PAGE)) {
+                uint4* dst = reinterpret_cast<uint4*>(v + r * 128 + (lane & 7) * 16);
+                dst[0] = make_uint4(0, 0, 0, 0);
+                dst[TILE_BYTES / 32] = make_uint4(0, 0, 0, 0);
+              }
+            fence_async_smem();
+            __syncwarp();
+          }
+          const uint64_t v = v_desc + st * (2 * TILE_BYTES >> 4);
+          if (two && a + batch > 0) wait(&sm.turn[a], (a == 0 ? batch - 1 : batch) & 1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // P's halves, 64 keys each
-          wait(&sm.p_full[a][h], j & 1);
-          if (h == 0 && tiles == 2 && a + j > 0) wait(&sm.turn[a], (a == 0 ? j - 1 : j) & 1);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mma_ts(o_col, s_col + 64 * h + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV,
-                   (j > 0 || h > 0 || s > 0) ? 1u : 0u);
-          if constexpr (F32) {
+          for (int h = 0; h < 2; ++h) {   // P's halves, 64 keys each
+            wait(&sm.p_full[a][h], tile & 1);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              mma_ts(o_col, s_col + 64 * h + 32 + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV, 1u);
+              mma_ts(o_col, s_col + 64 * h + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV,
+                     (j > it.j0 || h > 0 || s > 0) ? 1u : 0u);
+            if constexpr (F32) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                mma_ts(o_col, s_col + 64 * h + 32 + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV, 1u);
+            }
           }
-        }
-        if (!ok) break;
-        if (j + 1 < kt.count) {
-          score(st, true);
+          if (!ok) break;
+          if (j + 1 < it.j1) {
+            score(st, true);
+            if (j + 2 == it.j1) mma_commit(&sm.q_empty[a]);
+          } else {
+            pass_turn();
+            mma_commit(&sm.o_full[a]);
+            if (it.j0 + 1 == it.j1) mma_commit(&sm.q_empty[a]);   // the one tile's S was the first
+          }
           mma_commit(&sm.kv_empty[st]);
-        } else {   // (nobody waits for the last stage)
-          pass_turn();
-          mma_commit(&sm.o_full[a]);
         }
+        ++done;
       }
       if (!ok && lane == 0) gave_up();
     }
   } else {
     // ---- softmax of query tile a, one thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PF_SOFTMAX_REGS));
+    Item it;
     const int a = warp >> 2, r = threadIdx.x & 127;
-    if (a < tiles) {
-      const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-      const uint32_t ts = tmem + lane_off + 128 * a, to = tmem + lane_off + 256 + 128 * a;
-      const int tok = a * per_tile + (r >> A.lg);
-      const bool valid = tok < tokens;
-      const int pmin = p0 + a * per_tile, pmax = p0 + min(tokens, (a + 1) * per_tile) - 1;
-      const int pos = valid ? p0 + tok : pmax;
-      const float scale2 = A.a.scale2;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lane_off + 128 * a, to = tmem + lane_off + 256 + 128 * a;
+    const float scale2 = A.a.scale2;
+    const int tok = a * per_tile + (r >> A.lg);
+    bool ok = true;
+    int tile = 0, done = 0;   // key tiles and items so far
+    for (int turn = 0; turn < rounds && ok; ++turn) {
+      if (!it.load(A, turn)) break;
+      if (a >= it.tiles) continue;
+      const int pmin = it.p0 + a * per_tile, pmax = it.p0 + min(it.tokens, (a + 1) * per_tile) - 1;
+      const int pos = min(it.p0 + tok, pmax);
+      // pages from t0 that every row sees whole: t0 <= all_to and (t0 <= all_sinks or t0 > all_from)
+      const int all_to = pmin - (PAGE - 1), all_sinks = A.a.sinks - PAGE, all_from = pmax - A.a.window;
+      const int lo0 = pos - A.a.window + 1;
+      const int sink = it.kt.sink, skip = it.kt.first - it.kt.sink, pages = it.kt.pages, j0 = it.j0, j1 = it.j1;
       float mx = NEG_INF, l = 0.0f;
-      bool ok = true;
-      for (int j = 0; j < kt.count; ++j) {
-        ok = mbar_wait_warp(&sm.s_full[a], j & 1, ok);
+      for (int j = j0; j < j1; ++j, ++tile) {
+        ok = mbar_wait_warp(&sm.s_full[a], tile & 1, ok);
         if (!ok) break;
         tc_fence_after();
         uint32_t xr[128];
@@ -389,11 +472,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, xr + 32 * c);
         tc_wait_ld();
         float* x = reinterpret_cast<float*>(xr);
-        const int t0 = kt.base(j);
-        if (!(t0 + PF_KEYS - 1 <= pmin && (t0 + PF_KEYS <= A.a.sinks || t0 > pmax - A.a.window))) {
-          const int hi = pos - t0, lo = pos - A.a.window + 1 - t0, sk = A.a.sinks - t0;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = i <= hi && (i >= lo || i < sk) ? x[i] : NEG_INF;
+        for (int u = 0; u < 2; ++u) {
+          const int v = 2 * j + u, t0 = v >= pages ? 1 << 30 : (v < sink ? v : v + skip) * PAGE;
+          if (!(t0 <= all_to && (t0 <= all_sinks || t0 > all_from))) {
+            const int hi = pos - t0, lo = lo0 - t0, sk = A.a.sinks - t0;
+#pragma unroll
+            for (int i = 0; i < PAGE; ++i) x[PAGE * u + i] = i <= hi && (i >= lo || i < sk) ? x[PAGE * u + i] : NEG_INF;
+          }
         }
         float t[4];
 #pragma unroll
@@ -408,7 +494,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
           l *= f;
           if (raise) mx = top;
-          if (j > 0) {   // the product before S is done: S was issued after it
+          if (j > j0) {   // the product before S is done: S was issued after it
 #pragma unroll 1
             for (int c = 0; c < 128; c += 16) {   // in small pieces: the logits are live
               uint32_t o[16];
@@ -450,44 +536,60 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      if (kt.count > 0) ok = mbar_wait_warp(&sm.o_full[a], 0, ok);
-      if (!ok) gave_up();
-      if (ok) {
-        tc_fence_after();
-        const size_t row = (size_t)(A.row[ri] + tok0 + tok) * A.a.Hq + (size_t)head * A.G + (r & (A.G - 1));
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        if (valid && A.a.lse) A.a.lse[row] = l != 0.0f ? (mx + log2f(l)) * 0.6931471805599453f : NEG_INF;
+      // the item once more: nothing of it is held in registers over the loop
+      int again = turn;
+      asm volatile("" : "+r"(again));
+      it.load(A, again);
+      const bool some = it.j1 > it.j0, valid = tok < it.tokens;
+      if (some) ok = mbar_wait_warp(&sm.o_full[a], done & 1, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool split = A.splits > 1;
+      const size_t row = (size_t)(A.row[it.ri] + it.tok0 + tok) * A.a.Hq + (size_t)it.head * A.G + (r & (A.G - 1));
+      const float inv = split ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      float* part = A.partials + ((size_t)it.index * 2 * PF_ROWS + a * PF_ROWS + r) * PARTIAL_FLOATS;
+      if (split) {
+        part[PARTIAL_M] = mx;
+        part[PARTIAL_L] = l;
+      } else if (valid && A.a.lse) {
+        A.a.lse[row] = l != 0.0f ? (mx + log2f(l)) * 0.6931471805599453f : NEG_INF;
+      }
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t o[32];
-          __syncwarp();
-          if (kt.count > 0) {
-            tmem_ld32(to + c, o);
-            tc_wait_ld();
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-          if (!valid) {
-          } else if constexpr (F32) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(A.a.out) + row * D + c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + row * D + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        if (some) {
+          tmem_ld32(to + c, o);
+          tc_wait_ld();
+          if (c == 96) {   // O is read: the next item may write it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.o_empty[a]);
           }
         }
-        __syncwarp();
-        tc_fence_before();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+        if (F32 || split) {
+          uint4* dst = reinterpret_cast<uint4*>((split ? part : static_cast<float*>(A.a.out) + row * D) + c);
+          if (valid || split) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        } else if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + row * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
       }
+      done += some;
     }
+    if (!ok && lane == 0) gave_up();
   }
   __syncwarp();
   __syncthreads();
@@ -497,29 +599,97 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   }
 }
 
+// Fold the parts of split items: one warp per query row of (token, head).
+constexpr int FOLD_WARPS = 8;
+__global__ void __launch_bounds__(32 * FOLD_WARPS)
+    paged_prefill_fold_kernel(const __grid_constant__ PrefillArgs A) {
+  const int lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * FOLD_WARPS + (threadIdx.x >> 5);   // ((block, head), row of 256)
+  const int r = unit % (2 * PF_ROWS), bh = unit / (2 * PF_ROWS), head = bh % A.p.Hkv, back = bh / A.p.Hkv;
+  const int blk = A.bstart[A.n] - 1 - back;
+  if (blk < 0) return;
+  int ri = 0, hi = A.n;
+  while (hi - ri > 1) {
+    const int mid = (ri + hi) >> 1;
+    if (A.bstart[mid] <= blk) ri = mid; else hi = mid;
+  }
+  const int tok = (blk - A.bstart[ri]) * (2 * PF_ROWS >> A.lg) + (r >> A.lg);
+  if (tok >= A.m[ri]) return;
+  // part s of the item is at item ((back splits + s) Hkv + head)
+  auto at = [&](int s) {
+    return A.partials + (((size_t)(back * A.splits + s) * A.p.Hkv + head) * 2 * PF_ROWS + r) * PARTIAL_FLOATS;
+  };
+  float m = NEG_INF, l = 0.0f;
+  for (int s = 0; s < A.splits; ++s) m = fmaxf(m, at(s)[PARTIAL_M]);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (m != NEG_INF) {
+#pragma unroll 4
+    for (int s = 0; s < A.splits; ++s) {
+      const float* p = at(s);
+      const float f = ex2f(p[PARTIAL_M] - m);
+      const float4 v = reinterpret_cast<const float4*>(p)[lane];
+      l = fmaf(p[PARTIAL_L], f, l);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  const size_t row = (size_t)(A.row[ri] + tok) * A.a.Hq + (size_t)head * A.G + (r & (A.G - 1));
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+  if (A.a.f32)
+    reinterpret_cast<float4*>(static_cast<float*>(A.a.out) + row * D)[lane] = o;
+  else
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.a.out) + row * D)[lane] =
+        make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+  if (A.a.lse && lane == 0) A.a.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : NEG_INF;
+}
+
+int64_t row_blocks(int m, int G) { return ((int64_t)m * G + 2 * PF_ROWS - 1) / (2 * PF_ROWS); }
+
 }  // namespace
 
+// Parts of an item's key tiles, whatever the lengths: as many as fill the SMs once,
+// where the items alone fill less than half of them.
+int paged_prefill_splits(int64_t blocks, int hkv, int sms) {
+  const int64_t items = blocks * hkv;
+  return items == 0 || 2 * items > sms ? 1 : static_cast<int>(sms / items < 32 ? sms / items : 32);
+}
+int64_t paged_prefill_blocks(int m, int G) { return row_blocks(m, G); }
+size_t paged_prefill_partial_bytes(int64_t blocks, int hkv, int sms) {
+  const int splits = paged_prefill_splits(blocks, hkv, sms);
+  return splits == 1 ? 0 : (size_t)blocks * hkv * splits * 2 * PF_ROWS * PARTIAL_FLOATS * sizeof(float);
+}
+
 cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a,
-                                 const CUtensorMap& q_map, const CUtensorMap& kv_map, cudaStream_t s) {
+                                 const CUtensorMap& q_map, const CUtensorMap& kv_map, void* partials, int sms,
+                                 cudaStream_t s) {
   PrefillArgs A;
   A.p = p;
   A.a = a;
   A.n = n;
   A.G = a.Hq / p.Hkv;
   A.lg = A.G == 1 ? 0 : A.G == 2 ? 1 : A.G == 4 ? 2 : 3;
-  const int per_block = 2 * PF_ROWS / A.G;
-  int64_t blocks = 0;
+  int64_t blocks = 0, longest = 0;   // longest: key tiles of an item, at most
   for (int i = 0; i < n; ++i) {
     A.len[i] = reqs[i].len;
     A.m[i] = reqs[i].m;
     A.row[i] = reqs[i].row;
     A.table[i] = reqs[i].table;
     A.bstart[i] = static_cast<int32_t>(blocks);
-    blocks += (reqs[i].m + per_block - 1) / per_block;
+    blocks += row_blocks(reqs[i].m, A.G);
+    const int64_t seen = (int64_t)a.window + a.sinks + 2 * PF_ROWS < reqs[i].len ? (int64_t)a.window + a.sinks + 2 * PF_ROWS
+                                                                                 : reqs[i].len;
+    longest = seen / PF_KEYS + 1 > longest ? seen / PF_KEYS + 1 : longest;
   }
   A.bstart[n] = static_cast<int32_t>(blocks);
-  if (blocks * p.Hkv > INT32_MAX) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks * p.Hkv);
+  const int most = paged_prefill_splits(blocks, p.Hkv, sms);
+  // a part has four key tiles or more
+  A.splits = static_cast<int>(longest / 4 < most ? (longest / 4 > 1 ? longest / 4 : 1) : most);
+  A.partials = static_cast<float*>(partials);
+  if (blocks * p.Hkv * A.splits > INT32_MAX / 2) return cudaErrorInvalidValue;
+  A.items = static_cast<int>(blocks * p.Hkv * A.splits);
   constexpr int bytes = static_cast<int>(sizeof(PrefillSmem)) + 1024;
   auto kernel = a.f32 ? paged_prefill_kernel<true> : paged_prefill_kernel<false>;
   static unsigned done[2] = {0, 0};   // devices whose attribute is set
@@ -527,11 +697,19 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 32 || !(done[a.f32 != 0] & (1u << dev))) {
+    cudaFuncAttributes attr;   // the build has the registers that the split counts on
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != PF_REGS) return cudaErrorInvalidKernelImage;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (dev < 32) done[a.f32 != 0] |= 1u << dev;
   }
-  kernel<<<grid, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
+  kernel<<<A.items < sms ? A.items : sms, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || A.splits == 1) return e;
+  const int64_t warps = blocks * p.Hkv * 2 * PF_ROWS;
+  paged_prefill_fold_kernel<<<static_cast<unsigned>((warps + FOLD_WARPS - 1) / FOLD_WARPS), 32 * FOLD_WARPS, 0, s>>>(A);
   return cudaGetLastError();
 }
 

@@ -230,7 +230,19 @@ PREFILL = [
     ([300, 200], [33, 150], 0, 70),
     ([300], [40], 0, 0),
     ([900], [200], 130, 200),
+    # few rows on many keys: the keys are split
+    ([2500, 40], [20, 40], -1, 0),
+    ([2500], [70], 1500, 10),
+    ([1300, 1100], [40, 18], 0, 3),
 ]
+
+
+@pytest.mark.gpu
+def test_more_items_than_ctas(b):
+    """Prefill of more 256-row items than the GPU has SMs, one-tile ones among them, then a small one, on one workspace."""
+    lens = [70 + 13 * i % 90 for i in range(100)]
+    ws = run_attention(b, Pool(b, lens, 2, seed=3), lens, 4, 60, 3)
+    run_attention(b, Pool(b, [300], 1, seed=4), [300], 4, -1, 0, workspace=ws)
 
 
 @pytest.mark.gpu
