@@ -10,7 +10,7 @@
 // Traffic bounds it (512 B per token and kv head in BF16, 136 or 144 B in 4 bits,
 // for 2 x 2 x 128 flops per row), so the split serves the copies alone.  One
 // persistent CTA per SM takes an equal contiguous share of all the segments'
-// visible units (16 tokens of a BF16 page, 32 of a 4-bit one; units that no row
+// visible units (16 tokens of a BF16 page, a page in 4 bits; units that no row
 // sees are not in the list, and pages that hold none are never touched).  Each
 // warp streams its own units through its own TMA ring, the copies running on
 // across segment borders, and keeps a running (max, sum, o); a segment's warps
@@ -43,22 +43,20 @@ using namespace paged;
 
 template <int GK>
 struct Format {
-  static constexpr int UT = GK == 0 ? 16 : 32;                                    // tokens per unit
-  static constexpr int META = GK == 0 ? 0 : UT * i4_meta_row(GK == 0 ? D : GK);   // bytes of {s, z} of K (or V)
-  static constexpr int BYTES = GK == 0 ? UT * 4 * D : 2 * UT * I4_ROW + 2 * META; // bytes of one unit
+  static constexpr int UT = GK == 0 ? 16 : PAGE;                      // tokens per unit
+  static constexpr int BYTES = GK == 0 ? UT * 4 * D : i4_record(GK);  // bytes of one unit
 };
-// where a staged 4-bit unit has its parts
-constexpr int U4_V = 32 * I4_ROW, U4_META = 2 * U4_V;
 
 template <int GK, int NR>
 struct DecodeShape {
   // Warps: the BF16 unit is a few instructions for 8 KB, so eight warps keep the
-  // copies going; the 4-bit unit is bound by its instructions' latency, so as many
-  // warps as the registers allow.
-  static constexpr int NW = GK == 0 ? 8 : NR == 4 ? 16 : NR == 8 ? 12 : 8;
+  // copies going; the 4-bit unit is bound by its instructions, so as many warps as the
+  // registers and two pages each in shared memory allow.
+  static constexpr int NW = GK == 0 || NR == 16 ? 8 : 12;
   static constexpr int THREADS = 32 * NW;
+  static constexpr int FOLD = NR == 4 ? 4 : NR == 8 ? 2 : 1;   // warps folded at a time
   static constexpr size_t LIMIT = 232448 - 1024;   // shared memory of a CTA, less the alignment
-  static constexpr size_t FIXED = sizeof(float) * NW * NR * PARTIAL_FLOATS + 1024;
+  static constexpr size_t FIXED = sizeof(float) * FOLD * NR * PARTIAL_FLOATS + 1024;
   static constexpr int FIT = static_cast<int>((LIMIT - FIXED) / (NW * Format<GK>::BYTES));
   static constexpr int STAGES = FIT > 3 ? 3 : FIT;
   static_assert(STAGES >= 2, "a ring needs two stages");
@@ -67,8 +65,9 @@ struct DecodeShape {
 template <int GK, int NR>
 struct alignas(1024) DecodeSmem {
   static constexpr int STAGES = DecodeShape<GK, NR>::STAGES, NW = DecodeShape<GK, NR>::NW;
+  static constexpr int FOLD = DecodeShape<GK, NR>::FOLD;
   alignas(1024) uint8_t ring[NW][STAGES][Format<GK>::BYTES];
-  alignas(16) float state[NW][NR][PARTIAL_FLOATS];
+  alignas(16) float state[FOLD][NR][PARTIAL_FLOATS];
   uint64_t full[NW][STAGES];
   int last;
 };
@@ -342,12 +341,12 @@ __device__ __forceinline__ void weights(const float (&w0)[Cols<GK, NR>::H], cons
 
 // One unit of 16 BF16 tokens from t0: stage = two halves of 64 channels, each K
 // [16][128 B] and V [16][128 B], 16-byte pieces swizzled within 8 rows by the TMA.
-template <int NR>
+template <int NR, bool MASKED>
 __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR>& Q, State<0, NR>& S, uint8_t* stage,
-                                          int t0, bool masked) {
+                                          int t0) {
   using C = Cols<0, NR>;
   const int lane = threadIdx.x & 31, gid = lane >> 2;
-  if (masked) {
+  if constexpr (MASKED) {
     // value rows that no row of the segment sees may hold anything: zero them
     const int row = lane & 15, p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);   // the first query token
     bool any = false;
@@ -379,7 +378,7 @@ __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR
   for (int h = 0; h < C::H; ++h) {
     x0[h] = s[h / C::HPL][h % C::HPL] * Q.scale[h];
     x1[h] = s[h / C::HPL][2 + h % C::HPL] * Q.scale[h];
-    if (masked) {
+    if constexpr (MASKED) {
       if (!sees(A.a, Q.pos[h], t0 + gid)) x0[h] = NEG_INF;
       if (!sees(A.a, Q.pos[h], t0 + gid + 8)) x1[h] = NEG_INF;
     }
@@ -402,28 +401,33 @@ __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR
 }
 
 // Codes (bits 0-3 and 16-19, or 4-7 and 20-23, of w) as a pair of fp16 numbers c - 8.
-__device__ __forceinline__ uint32_t code_lo(uint32_t w) {
-  uint32_t x = (w & 0x000F000Fu) | 0x64006400u;   // 1024 + c
-  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE408E408u));   // - 1032
+// magic (0x64006400: 1024, twice) comes in a register: as a constant beside the mask it
+// would cost a second logic operation.
+__device__ __forceinline__ uint32_t code_lo(uint32_t w, uint32_t magic) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(x) : "r"(w), "r"(magic));   // 1024 + c
+  asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE408E408u));                    // - 1032
   return x;
 }
-__device__ __forceinline__ uint32_t code_hi(uint32_t w) {
-  uint32_t x = (w & 0x00F000F0u) | 0x64006400u;   // 1024 + 16 c
+__device__ __forceinline__ uint32_t code_hi(uint32_t w, uint32_t magic) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(x) : "r"(w), "r"(magic));   // 1024 + 16 c
   asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(x) : "r"(0x2C002C00u), "r"(0xD480D480u));   // / 16 - 72
   return x;
 }
 
-// One 4-bit unit (32 tokens from t0): K codes [32][64 B], V codes, K meta, V meta as
-// in the record.  Row r of a 16-token tile is token r ^ ((r >> 1) & 1), which spreads
+// One 4-bit page (64 tokens from t0) as it lies in memory.  Row r of a 16-token tile is token r ^ ((r >> 1) & 1), which spreads
 // both products' reads over the banks.
-template <int GK, int NR>
+template <int GK, int NR, bool MASKED>
 __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, NR>& Q, State<GK, NR>& S,
-                                          const uint8_t* stage, int t0, bool masked) {
+                                          const uint8_t* stage, int t0) {
   using C = Cols<GK, NR>;
-  constexpr int NG = State<GK, NR>::NG, TILES = Format<GK>::UT / 16, MROW = i4_meta_row(GK);
+  constexpr int NG = State<GK, NR>::NG, TILES = PAGE / 16, MROW = i4_meta_row(GK);
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   const int tok = gid ^ ((gid >> 1) & 1);
-  // ---- logits of the unit
+  uint32_t magic = 0x64006400u;
+  asm volatile("" : "+r"(magic));
+  // ---- logits of the page
   float x[TILES][2][C::H];
 #pragma unroll
   for (int t = 0; t < TILES; ++t) {
@@ -456,7 +460,7 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
         for (int g = 0; g < 2; ++g) {   // the two accumulators (groups, at 64) in turn
           const int word = 2 * g + i;
           const uint32_t wa = w[0][word] >> (8 * sub), wb = w[1][word] >> (8 * sub);
-          const uint32_t a0 = code_lo(wa), a1 = code_lo(wb), a2 = code_hi(wa), a3 = code_hi(wb);
+          const uint32_t a0 = code_lo(wa, magic), a1 = code_lo(wb, magic), a2 = code_hi(wa, magic), a3 = code_hi(wb, magic);
 #pragma unroll
           for (int j = 0; j < C::QT; ++j)
             mma_f16(s[j][g], a0, a1, a2, a3, Q.b[j][2 * word + sub][0], Q.b[j][2 * word + sub][1]);
@@ -467,7 +471,7 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
       float sk[2], zk[2];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const __half2 m = *reinterpret_cast<const __half2*>(stage + U4_META + MROW * slot + 4 * g);
+        const __half2 m = *reinterpret_cast<const __half2*>(stage + I4_META + MROW * slot + 4 * g);
         sk[g] = __low2float(m);
         zk[g] = fmaf(8.0f, sk[g], __high2float(m));
       }
@@ -480,7 +484,7 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
         else
           y = fmaf(sk[0], s[j][0][k] * Q.scale[h], zk[0] * Q.qsum[0][h]) +
               fmaf(sk[1], s[j][1][k] * Q.scale[h], zk[1] * Q.qsum[1][h]);
-        if (masked && !sees(A.a, Q.pos[h], t0 + slot)) y = NEG_INF;
+        if (MASKED && !sees(A.a, Q.pos[h], t0 + slot)) y = NEG_INF;
         x[t][u][h] = y;
       }
     }
@@ -500,17 +504,23 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
         S.l[h] += x[t][u][h];
       }
   }
-  // ---- the value scales' power of two: their largest in the unit
-  const uint8_t* vmeta = stage + U4_META + Format<GK>::META;
+  // ---- the value scales' power of two: their largest in the page
+  const uint8_t* vmeta = stage + i4_v_meta(GK);
   float mult[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    uint32_t big = *reinterpret_cast<const uint16_t*>(vmeta + MROW * lane + 4 * g) & 0x7fffu;
-    if (masked) {   // a token that no row sees may hold anything
-      bool any = false;
-      const int p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);
-      for (int q = 0; q < A.m; ++q) any = any || sees(A.a, p0 + q, t0 + lane);
-      if (!any) big = 0;
+    uint32_t big = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int slot = lane + 32 * k;
+      uint32_t bits = *reinterpret_cast<const uint16_t*>(vmeta + MROW * slot + 4 * g) & 0x7fffu;
+      if constexpr (MASKED) {   // a token that no row sees may hold anything
+        bool any = false;
+        const int p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);
+        for (int q = 0; q < A.m; ++q) any = any || sees(A.a, p0 + q, t0 + slot);
+        if (!any) bits = 0;
+      }
+      big = max(big, bits);
     }
     big = __reduce_max_sync(0xffffffffu, big);
     // s < 2^e: normal numbers have e = (bits >> 10) - 14, subnormal ones e <= -14
@@ -543,24 +553,30 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
 #pragma unroll
         for (int h = 0; h < C::H; ++h) {
           const float pr = x[t][u][h];
-          const bool dead = masked && pr == 0.0f;   // its scale and zero may be anything
+          const bool dead = MASKED && pr == 0.0f;   // its scale and zero may be anything
           (u ? w1[h] : w0[h]) = dead ? 0.0f : pr * sv;
           S.z[g][h] = dead ? S.z[g][h] : fmaf(pr, zv, S.z[g][h]);
         }
       }
       weights<GK, NR>(w0, w1, b[g], f16_hi, f16x2);
     }
-    // the lane's four tokens of the tile: rows 2 tid, 2 tid + 1, + 8; two words of 8 channels of each
+    // the lane's four tokens of the tile: rows 2 tid, 2 tid + 1, + 8; two words of 8
+    // channels of each (at group 64 one of each group)
     uint32_t v[4][2];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int r = 2 * tid + (q & 1) + 8 * (q >> 1);
-      const uint8_t* row = stage + U4_V + (16 * t + (r ^ ((r >> 1) & 1))) * I4_ROW;
-      const int first = tid >> 1;   // half of the lanes read the second word first: no bank conflicts
-      const uint32_t va = *reinterpret_cast<const uint32_t*>(row + 32 * first + 4 * gid);
-      const uint32_t vb = *reinterpret_cast<const uint32_t*>(row + 32 * (first ^ 1) + 4 * gid);
-      v[q][0] = first ? vb : va;
-      v[q][1] = first ? va : vb;
+      const uint8_t* row = stage + I4_V_CODES + (16 * t + (r ^ ((r >> 1) & 1))) * I4_ROW;
+      if constexpr (GK == 128) {
+        const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * gid);
+        v[q][0] = w.x, v[q][1] = w.y;
+      } else {
+        const int first = tid >> 1;   // half of the lanes read the second word first: no bank conflicts
+        const uint32_t va = *reinterpret_cast<const uint32_t*>(row + 32 * first + 4 * gid);
+        const uint32_t vb = *reinterpret_cast<const uint32_t*>(row + 32 * (first ^ 1) + 4 * gid);
+        v[q][0] = first ? vb : va;
+        v[q][1] = first ? va : vb;
+      }
     }
 #pragma unroll
     for (int word = 0; word < 2; ++word)
@@ -571,7 +587,7 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
           const uint32_t qa = pa >> (8 * sub), qb = pb >> (8 * sub);
-          const uint32_t a0 = code_lo(qa), a1 = code_hi(qa), a2 = code_lo(qb), a3 = code_hi(qb);
+          const uint32_t a0 = code_lo(qa, magic), a1 = code_hi(qa, magic), a2 = code_lo(qb, magic), a3 = code_hi(qb, magic);
           const int mt = 4 * word + 2 * half + sub;
 #pragma unroll
           for (int j = 0; j < C::PT; ++j)
@@ -626,7 +642,7 @@ __device__ __forceinline__ void put_state(const State<GK, NR>& S, float (*st)[PA
       } else {
         const int g = NG == 1 ? 0 : mt / 4;
         const float back = __uint_as_float(static_cast<uint32_t>(127 + S.e[g] - 6) << 23);
-        const int ch = 64 * (mt / 4) + 8 * gid + 2 * (mt % 4);
+        const int ch = GK == 128 ? 16 * gid + 2 * mt : 64 * (mt / 4) + 8 * gid + 2 * (mt % 4);
         st[r][ch] = fmaf(a, back, z[g]);
         st[r][ch + 1] = fmaf(b, back, z[g]);
       }
@@ -693,7 +709,8 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
   using SM = DecodeSmem<GK, NR>;
   constexpr int UT = F::UT, STAGES = SM::STAGES, NW = SM::NW;
   extern __shared__ uint8_t dec_raw[];
-  SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(dec_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (aligned by an offset, not by a cast of the address: the accesses stay shared ones)
+  SM& sm = *reinterpret_cast<SM*>(dec_raw + (-smem_u32(dec_raw) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
   const int u0 = static_cast<int>((int64_t)A.total * cta / A.ncta);
@@ -730,12 +747,7 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
           tma_load_3d(dst, &map, 0, t0 % PAGE, static_cast<int>(2 * rec), &sm.full[warp][st]);
           tma_load_3d(dst + F::BYTES / 2, &map, 64, t0 % PAGE, static_cast<int>(2 * rec), &sm.full[warp][st]);
         } else {
-          const uint8_t* src = static_cast<const uint8_t*>(A.p.pool) + rec * i4_record(GK);
-          const int r0 = t0 % PAGE;
-          tma_load_1d(dst, src + r0 * I4_ROW, U4_V, &sm.full[warp][st]);
-          tma_load_1d(dst + U4_V, src + I4_V_CODES + r0 * I4_ROW, U4_V, &sm.full[warp][st]);
-          tma_load_1d(dst + U4_META, src + I4_META + r0 * i4_meta_row(GK), F::META, &sm.full[warp][st]);
-          tma_load_1d(dst + U4_META + F::META, src + i4_v_meta(GK) + r0 * i4_meta_row(GK), F::META, &sm.full[warp][st]);
+          tma_load_1d(dst, static_cast<const uint8_t*>(A.p.pool) + rec * F::BYTES, F::BYTES, &sm.full[warp][st]);
         }
       }
     } else if (lane == 0) {
@@ -769,49 +781,76 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
         const int t0 = cc.un.unit(v) * UT;
         const bool masked = !(t0 + UT - 1 <= len - A.m &&
                               (t0 + UT <= A.a.sinks || (int64_t)t0 > (int64_t)len - 1 - A.a.window));
-        if constexpr (GK == 0)
-          bf16_unit<NR>(A, Q, S, sm.ring[warp][st], t0, masked);
-        else
-          int4_unit<GK, NR>(A, Q, S, sm.ring[warp][st], t0, masked);
+        if constexpr (GK == 0) {
+          if (masked) bf16_unit<NR, true>(A, Q, S, sm.ring[warp][st], t0);
+          else bf16_unit<NR, false>(A, Q, S, sm.ring[warp][st], t0);
+        } else {
+          if (masked) int4_unit<GK, NR, true>(A, Q, S, sm.ring[warp][st], t0);
+          else int4_unit<GK, NR, false>(A, Q, S, sm.ring[warp][st], t0);
+        }
       }
       __syncwarp();
       ++taken;
       issue();
     }
-    // ---- the CTA's share of the segment
-    put_state<GK, NR>(S, sm.state[warp]);
-    __syncthreads();
+    // ---- the CTA's share of the segment: the warps' states folded a few at a time
+    // (all of them at once would take the ring's room)
     const int full_units = cc.seg_end - cc.base;
     const int seg = cc.req * A.p.Hkv + cc.head;
     const int c_lo = static_cast<int>((((int64_t)cc.base + 1) * A.ncta - 1) / A.total);
     const int c_hi = static_cast<int>(((int64_t)cc.seg_end * A.ncta - 1) / A.total);
     const bool whole = seg_end - seg_u == full_units;
-    float* rec = A.partials + (size_t)(seg + cta) * NR * PARTIAL_FLOATS;
-    for (int r = warp; r < R; r += NW) {
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float m = NEG_INF, l = 0.0f;
+    constexpr int FOLD = SM::FOLD, MINE = (NR + NW - 1) / NW;   // rows of a warp
+    float4 fo[MINE];
+    float fm[MINE], fl[MINE];
 #pragma unroll
-      for (int w = 0; w < NW; ++w) m = fmaxf(m, sm.state[w][r][PARTIAL_M]);
-      if (m != NEG_INF) {
+    for (int i = 0; i < MINE; ++i) {
+      fo[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      fm[i] = NEG_INF;
+      fl[i] = 0.0f;
+    }
+    for (int w0 = 0; w0 < NW; w0 += FOLD) {
+      if (warp >= w0 && warp < w0 + FOLD) put_state<GK, NR>(S, sm.state[warp - w0]);
+      __syncthreads();
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
+      for (int i = 0; i < MINE; ++i) {
+        const int r = warp + NW * i;
+        if (r >= R) continue;
+        float m = fm[i];
+#pragma unroll
+        for (int w = 0; w < FOLD; ++w) m = fmaxf(m, sm.state[w][r][PARTIAL_M]);
+        if (m == NEG_INF) continue;
+        float4& o = fo[i];
+        const float f0 = ex2f(fm[i] - m);
+        fm[i] = m;
+        fl[i] *= f0;
+        o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+        for (int w = 0; w < FOLD; ++w) {
           const float f = ex2f(sm.state[w][r][PARTIAL_M] - m);
           if (f == 0.0f) continue;
           const float4 x = reinterpret_cast<const float4*>(sm.state[w][r])[lane];
-          l = fmaf(sm.state[w][r][PARTIAL_L], f, l);
+          fl[i] = fmaf(sm.state[w][r][PARTIAL_L], f, fl[i]);
           o.x = fmaf(x.x, f, o.x);
           o.y = fmaf(x.y, f, o.y);
           o.z = fmaf(x.z, f, o.z);
           o.w = fmaf(x.w, f, o.w);
         }
       }
+      __syncthreads();
+    }
+    float* rec = A.partials + (size_t)(seg + cta) * NR * PARTIAL_FLOATS;
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const int r = warp + NW * i;
+      if (r >= R) continue;
       if (whole) {
-        write_row(A, cc.req, cc.head, r, lane, o, m, l);
+        write_row(A, cc.req, cc.head, r, lane, fo[i], fm[i], fl[i]);
       } else {
-        reinterpret_cast<float4*>(rec + r * PARTIAL_FLOATS)[lane] = o;
+        reinterpret_cast<float4*>(rec + r * PARTIAL_FLOATS)[lane] = fo[i];
         if (lane == 0) {
-          rec[r * PARTIAL_FLOATS + PARTIAL_M] = m;
-          rec[r * PARTIAL_FLOATS + PARTIAL_L] = l;
+          rec[r * PARTIAL_FLOATS + PARTIAL_M] = fm[i];
+          rec[r * PARTIAL_FLOATS + PARTIAL_L] = fl[i];
         }
       }
     }
@@ -889,7 +928,7 @@ cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, 
   A.G = a.Hq / p.Hkv;
   A.counters = static_cast<int32_t*>(workspace);
   A.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + PAGED_COUNTER_BYTES);
-  const int ut = gk == 0 ? Format<0>::UT : Format<128>::UT;
+  const int ut = gk == 0 ? Format<0>::UT : PAGE;
   int64_t total = 0;
   for (int i = 0; i < n; ++i) {
     A.len[i] = reqs[i].len;

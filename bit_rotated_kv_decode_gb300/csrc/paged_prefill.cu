@@ -241,8 +241,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     paged_prefill_kernel(const __grid_constant__ PrefillArgs A, const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap kv_map) {
   extern __shared__ uint8_t pf_raw[];
-  PrefillSmem& sm =
-      *reinterpret_cast<PrefillSmem*>((reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  PrefillSmem& sm = *reinterpret_cast<PrefillSmem*>(pf_raw + (-smem_u32(pf_raw) & 1023u));
   // (through a shuffle: uniform for the compiler too)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
