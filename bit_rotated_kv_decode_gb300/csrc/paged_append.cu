@@ -25,14 +25,19 @@ constexpr int APP_THREADS = 128;
 constexpr int APP_ROWS = 4;                    // head rows per lane group in flight
 constexpr int APP_HEADS = 4 * APP_ROWS;        // head rows per warp: four groups of 8 lanes
 
-struct alignas(16) Bf8 {
-  uint16_t x[8];
-};
-__device__ __forceinline__ float bf_f(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
-__device__ __forceinline__ uint16_t f_bf(float x) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(x);
-  return *reinterpret_cast<const uint16_t*>(&h);
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t neg_bf2(uint32_t a) { return a ^ 0x80008000u; }
+__device__ __forceinline__ uint32_t swap16(uint32_t a) { return __byte_perm(a, a, 0x1032); }
 
 __device__ __forceinline__ int find_req(const PagedRows& r, int n, int row) {
   int lo = 0, hi = n;   // row0[lo] <= row < row0[hi]
@@ -51,47 +56,115 @@ __device__ __forceinline__ int64_t page_of(const PagedView& p, int i, int pos) {
   return -1;
 }
 
-// Quantise one head row held by 8 lanes, 16 channels each: chunks of 8 channels
-// c[0] and c[1] with values x[0] and x[1].  Writes the codes and, from the lane
-// that holds a group's first chunk, {s, z}.
-template <int GK>
-__device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, const int (&c)[2], Bf8 (&x)[2], bool ok) {
-  constexpr int NG = D / GK;
-  float f[2][8], mn[NG], mx[NG];
+// Codes of 8 channels (four words of bf16 pairs) with scale s > 0 or s = 0 and zero z.
+// t = (x - z) * (1 / s) with an approximate reciprocal is within 15 (2^-22 + 2^-23) of
+// the quotient (one reciprocal and one product, quotients up to 15 and a little), so
+// its rounding decides the code unless it lies within 2^-16 of a half; then the exact
+// quotient does.  Magic: adding 1.5 2^23 rounds to the nearest integer, ties to even.
+template <bool SATURATE>
+__device__ __forceinline__ float value_of(float x) {
+  return !SATURATE ? x : x == x ? fminf(fmaxf(x, -65504.0f), 65504.0f) : 0.0f;
+}
+template <bool SATURATE>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&x)[4], float s, float z) {
+  constexpr float MAGIC = 12582912.0f;
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  if (s == 0.0f) inv = 0.0f;
+  float worst = 0.0f;
+  uint32_t w = 0;
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    mn[g] = INFINITY;
-    mx[g] = -INFINITY;
+  for (int e = 0; e < 8; ++e) {
+    const float v = value_of<SATURATE>(e & 1 ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1]));
+    const float t = fminf(fmaxf(__fsub_rn(v, z) * inv, 0.0f), 15.0f);
+    const float r = __fadd_rn(t, MAGIC);
+    worst = fmaxf(worst, fabsf(t - __fsub_rn(r, MAGIC)));
+    w |= (__float_as_uint(r) & 15u) << (4 * e);
   }
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    float lo = INFINITY, hi = -INFINITY;
+  if (worst > 0.5f - 0x1p-16f) {
+    w = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float y = bf_f(x[u].x[e]);
-      y = y == y ? fminf(fmaxf(y, -65504.0f), 65504.0f) : 0.0f;
-      f[u][e] = y;
-      lo = fminf(lo, y);
-      hi = fmaxf(hi, y);
+      const float v = value_of<SATURATE>(e & 1 ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1]));
+      const float t = rintf(__fdiv_rn(__fsub_rn(v, z), s));
+      const int code = s == 0.0f ? 0 : static_cast<int>(fminf(fmaxf(t, 0.0f), 15.0f));
+      w |= static_cast<uint32_t>(code) << (4 * e);
     }
+  }
+  return w;
+}
+
+// Quantise one head row held by 8 lanes, 16 channels each: chunks c[0] and c[1] of 8
+// channels.  Writes the codes and, from the lane that holds a group's first chunk, {s, z}.
+// Maxima and negated minima of a group travel as one bf16 pair.
+template <int GK>
+__device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, const int (&c)[2],
+                                           const uint32_t (&x)[2][4], bool ok) {
+  constexpr int NG = D / GK;
+  uint32_t top = 0;   // largest magnitude, NaN above infinity
+  uint32_t mm[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) mm[g] = 0xff80ff80u;   // -infinity, twice
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t hi = x[u][0], lo = neg_bf2(x[u][0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      top = __vmaxu2(top, x[u][k] & 0x7fff7fffu);
+      if (k > 0) {
+        hi = max_bf2(hi, x[u][k]);
+        lo = max_bf2(lo, neg_bf2(x[u][k]));
+      }
+    }
+    hi = max_bf2(hi, swap16(hi));
+    lo = max_bf2(lo, swap16(lo));
+    const uint32_t both = __byte_perm(hi, lo, 0x5410);
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-      if (NG == 1 || c[u] / (GK / 8) == g) {
-        mn[g] = fminf(mn[g], lo);
-        mx[g] = fmaxf(mx[g], hi);
-      }
+      if (NG == 1 || c[u] / (GK / 8) == g) mm[g] = max_bf2(mm[g], both);
   }
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
-    for (int off = 1; off < 8; off <<= 1) {
-      mn[g] = fminf(mn[g], __shfl_xor_sync(0xffffffffu, mn[g], off));
-      mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
+    for (int off = 1; off < 8; off <<= 1) mm[g] = max_bf2(mm[g], __shfl_xor_sync(0xffffffffu, mm[g], off));
+  float mx[NG], mn[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    mx[g] = bf_lo(mm[g]);
+    mn[g] = -bf_hi(mm[g]);
+  }
+  // values beyond fp16 (65280 is bf16's last below 65504) or NaN in the warp: once more, with care
+  const bool wild = __any_sync(0xffffffffu, (top & 0xffffu) > 0x477fu || (top >> 16) > 0x477fu);
+  if (wild) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      mn[g] = INFINITY;
+      mx[g] = -INFINITY;
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = value_of<true>(e & 1 ? bf_hi(x[u][e >> 1]) : bf_lo(x[u][e >> 1]));
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          if (NG == 1 || c[u] / (GK / 8) == g) {
+            mn[g] = fminf(mn[g], v);
+            mx[g] = fmaxf(mx[g], v);
+          }
+      }
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) {
+        mn[g] = fminf(mn[g], __shfl_xor_sync(0xffffffffu, mn[g], off));
+        mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
+      }
+  }
   __half s[NG], z[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    z[g] = __float2half_rn(mn[g]);
+    z[g] = __float2half_rn(__fadd_rn(mn[g], 0.0f));
     s[g] = __float2half_rn(__fdiv_rn(__fsub_rn(mx[g], mn[g]), 15.0f));
   }
   if (!ok) return;
@@ -102,14 +175,7 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
     const int g = NG == 1 ? 0 : c[u] / (GK / 8);
     const __half sh = NG == 1 || g == 0 ? s[0] : s[NG - 1], zh = NG == 1 || g == 0 ? z[0] : z[NG - 1];
     const float sf = __half2float(sh), zf = __half2float(zh);
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float t = rintf(__fdiv_rn(__fsub_rn(f[u][e], zf), sf));
-      const int code = sf == 0.0f ? 0 : static_cast<int>(fminf(fmaxf(t, 0.0f), 15.0f));
-      w |= static_cast<uint32_t>(code) << (4 * e);
-    }
-    *reinterpret_cast<uint32_t*>(codes + 4 * c[u]) = w;
+    *reinterpret_cast<uint32_t*>(codes + 4 * c[u]) = wild ? codes_of<true>(x[u], sf, zf) : codes_of<false>(x[u], sf, zf);
     if (c[u] % (GK / 8) == 0)
       *reinterpret_cast<uint32_t*>(meta + 4 * g) =
           static_cast<uint32_t>(__half_as_ushort(sh)) | (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
@@ -121,49 +187,43 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
 // so that the rotation needs no exchange and the cosines and sines are loaded
 // once for all rows.  The kernel moves each byte once; all loads of a lane
 // (8 x 16 B) are in flight together.
-template <int GK>
+template <int GK, bool INTERLEAVED>
 __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_constant__ PagedView p,
                                                                    const __grid_constant__ PagedRows rows,
                                                                    const __grid_constant__ RopeArgs rope,
                                                                    const __grid_constant__ AppendRows in,
-                                                                   int tasks_per_token, int64_t tasks) {
-  const int64_t task = ((int64_t)blockIdx.x * APP_THREADS + threadIdx.x) >> 5;
+                                                                   uint32_t tasks_per_token, uint32_t tasks) {
+  const uint32_t task = (blockIdx.x * APP_THREADS + threadIdx.x) >> 5;
   if (task >= tasks) return;
   const int lane = threadIdx.x & 31, pc = lane & 7, sub = lane >> 3;
   const int row = static_cast<int>(task / tasks_per_token);
   const int head0 = static_cast<int>(task % tasks_per_token) * APP_HEADS + sub;
-  const int i = find_req(rows, p.n, row);
-  const int pos = rows.pos0[i] + (row - rows.row0[i]);
   const int hq = in.q ? in.Hq : 0, total = hq + 2 * p.Hkv;
 
   // the lane's two chunks, and whether they hold rotated pairs
+  const int half_chunks = rope.dim / 16;   // pairs of chunks that are rotated
+  const bool rot = rope.table != nullptr && pc < half_chunks;
   int c[2];
-  const int half_chunks = rope.dim / 16;   // rotated pairs of chunks (half layout)
-  bool rot = rope.table != nullptr;
-  if (rope.interleaved) {
-    c[0] = 2 * pc;
-    c[1] = 2 * pc + 1;
-    rot = rot && pc < half_chunks;
-  } else if (rot && pc < half_chunks) {
-    c[0] = pc;
-    c[1] = pc + half_chunks;
-  } else {
-    rot = false;
-    c[0] = rope.table ? 2 * pc : 2 * pc;
-    c[1] = c[0] + 1;
-  }
-  Bf8 x[APP_ROWS][2];
+  c[0] = !INTERLEAVED && rot ? pc : 2 * pc;
+  c[1] = !INTERLEAVED && rot ? pc + half_chunks : 2 * pc + 1;
+  uint32_t x[APP_ROWS][2][4];
 #pragma unroll
   for (int r = 0; r < APP_ROWS; ++r) {
     const int h = head0 + 4 * r;
-    if (h >= total) continue;
-    const uint16_t* src = h < hq            ? in.q + row * in.q_stride + (int64_t)h * D
-                          : h < hq + p.Hkv  ? in.k + row * in.k_stride + (int64_t)(h - hq) * D
-                                            : in.v + row * in.v_stride + (int64_t)(h - hq - p.Hkv) * D;
-    x[r][0] = *reinterpret_cast<const Bf8*>(src + 8 * c[0]);
-    x[r][1] = *reinterpret_cast<const Bf8*>(src + 8 * c[1]);
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (h < total) {
+      const uint16_t* src = h < hq           ? in.q + row * in.q_stride + h * D
+                            : h < hq + p.Hkv ? in.k + row * in.k_stride + (h - hq) * D
+                                             : in.v + row * in.v_stride + (h - hq - p.Hkv) * D;
+      a = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c[0]));
+      b = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c[1]));
+    }
+    x[r][0][0] = a.x, x[r][0][1] = a.y, x[r][0][2] = a.z, x[r][0][3] = a.w;
+    x[r][1][0] = b.x, x[r][1][1] = b.y, x[r][1][2] = b.z, x[r][1][3] = b.w;
   }
-  // pair e of the lane: channels (c[0], c[1]) element e, or (2e, 2e + 1) of the two chunks
+  const int i = find_req(rows, p.n, row);
+  const int pos = rows.pos0[i] + (row - rows.row0[i]);
+  // pair e of the lane: element e of both chunks, or elements 2e, 2e + 1 of the 16
   float cs[8], sn[8];
   if (rot) {
     const float* t = rope.table + (size_t)pos * rope.dim + 8 * pc;
@@ -181,28 +241,39 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
     const int h = head0 + 4 * r;
     if (rot && h < hq + p.Hkv) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint16_t& xa = rope.interleaved ? x[r][e >> 2].x[2 * (e & 3)] : x[r][0].x[e];
-        uint16_t& xb = rope.interleaved ? x[r][e >> 2].x[2 * (e & 3) + 1] : x[r][1].x[e];
-        const float a = bf_f(xa), b = bf_f(xb);
-        xa = f_bf(__fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e])));
-        xb = f_bf(__fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e])));
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float a = bf_lo(x[r][u][k]), b = bf_hi(x[r][u][k]), co = cs[4 * u + k], si = sn[4 * u + k];
+            x[r][u][k] = pack_bf(__fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si)),
+                                 __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si)));
+          }
+        } else {
+          const float a0 = bf_lo(x[r][0][k]), a1 = bf_hi(x[r][0][k]), b0 = bf_lo(x[r][1][k]), b1 = bf_hi(x[r][1][k]);
+          x[r][0][k] = pack_bf(__fsub_rn(__fmul_rn(a0, cs[2 * k]), __fmul_rn(b0, sn[2 * k])),
+                               __fsub_rn(__fmul_rn(a1, cs[2 * k + 1]), __fmul_rn(b1, sn[2 * k + 1])));
+          x[r][1][k] = pack_bf(__fadd_rn(__fmul_rn(b0, cs[2 * k]), __fmul_rn(a0, sn[2 * k])),
+                               __fadd_rn(__fmul_rn(b1, cs[2 * k + 1]), __fmul_rn(a1, sn[2 * k + 1])));
+        }
       }
     }
     const bool is_q = h < hq;
     const int which = h >= hq + p.Hkv, kvh = h - hq - (which ? p.Hkv : 0);
+    const uint4 a = make_uint4(x[r][0][0], x[r][0][1], x[r][0][2], x[r][0][3]);
+    const uint4 b = make_uint4(x[r][1][0], x[r][1][1], x[r][1][2], x[r][1][3]);
     if (is_q) {
       uint16_t* dst = in.q_out + ((size_t)row * in.Hq + h) * D;
-      *reinterpret_cast<Bf8*>(dst + 8 * c[0]) = x[r][0];
-      *reinterpret_cast<Bf8*>(dst + 8 * c[1]) = x[r][1];
+      *reinterpret_cast<uint4*>(dst + 8 * c[0]) = a;
+      *reinterpret_cast<uint4*>(dst + 8 * c[1]) = b;
     }
     const bool ok = !is_q && h < total && page >= 0;
     if constexpr (GK == 0) {
       if (ok) {
         uint16_t* dst = static_cast<uint16_t*>(p.pool) + ((size_t)page * p.Hkv + kvh) * BF16_RECORD_ELEMS +
                         (size_t)which * PAGE * D + (size_t)slot * D;
-        *reinterpret_cast<Bf8*>(dst + 8 * c[0]) = x[r][0];
-        *reinterpret_cast<Bf8*>(dst + 8 * c[1]) = x[r][1];
+        *reinterpret_cast<uint4*>(dst + 8 * c[0]) = a;
+        *reinterpret_cast<uint4*>(dst + 8 * c[1]) = b;
       }
     } else {
       // the whole warp takes part in the reductions' shuffles
@@ -249,10 +320,8 @@ __global__ void __launch_bounds__(READ_THREADS) int4_read_kernel(const __grid_co
     dst[0] = make_float4(y[0], y[1], y[2], y[3]);
     dst[1] = make_float4(y[4], y[5], y[6], y[7]);
   } else {
-    Bf8 b;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) b.x[e] = f_bf(y[e]);
-    *reinterpret_cast<Bf8*>(static_cast<uint16_t*>(which ? v_out : k_out) + at) = b;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(which ? v_out : k_out) + at) =
+        make_uint4(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]), pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
   }
 }
 
@@ -263,15 +332,16 @@ cudaError_t launch_paged_append(const PagedView& p, const PagedRows& rows, const
   const int heads = (in.q ? in.Hq : 0) + 2 * p.Hkv;
   const int per_token = (heads + APP_HEADS - 1) / APP_HEADS;
   const int64_t tasks = (int64_t)rows.row0[p.n] * per_token;
-  const int64_t blocks = (tasks * 32 + APP_THREADS - 1) / APP_THREADS;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
+  if (tasks * 32 > UINT32_MAX - APP_THREADS) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>((tasks * 32 + APP_THREADS - 1) / APP_THREADS);
+  const uint32_t n = static_cast<uint32_t>(tasks), per = static_cast<uint32_t>(per_token);
+  auto go = [&](auto kernel) { kernel<<<grid, APP_THREADS, 0, s>>>(p, rows, rope, in, per, n); };
   if (gk == 0)
-    paged_append_kernel<0><<<grid, APP_THREADS, 0, s>>>(p, rows, rope, in, per_token, tasks);
+    rope.interleaved ? go(paged_append_kernel<0, true>) : go(paged_append_kernel<0, false>);
   else if (gk == 128)
-    paged_append_kernel<128><<<grid, APP_THREADS, 0, s>>>(p, rows, rope, in, per_token, tasks);
+    rope.interleaved ? go(paged_append_kernel<128, true>) : go(paged_append_kernel<128, false>);
   else
-    paged_append_kernel<64><<<grid, APP_THREADS, 0, s>>>(p, rows, rope, in, per_token, tasks);
+    rope.interleaved ? go(paged_append_kernel<64, true>) : go(paged_append_kernel<64, false>);
   return cudaGetLastError();
 }
 

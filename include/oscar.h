@@ -366,7 +366,7 @@ typedef struct {
  * they were.
  * In 4 bits, per token, kv head and group of group_size (128 or 64) channels of
  * the values that the BF16 cache would hold (saturated to +-65504, NaN as 0):
- *   z = fp16(min), s = fp16((max - min) / 15),
+ *   z = fp16(min) (a zero as +0), s = fp16((max - min) / 15),
  *   code = clamp(round((x - z) / s), 0, 15), ties to even, 0 where s is 0,
  * every step rounded to fp32, the conversions to nearest. */
 oscar_status oscar_bf16_append(void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,

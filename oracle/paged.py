@@ -5,7 +5,7 @@ Definitions:
   * rotation over the pairs (i, j) of the first dim channels: y_i = x_i cos -
     x_j sin, y_j = x_j cos + x_i sin, each product and sum rounded to fp32, the
     result to bf16 (nearest, ties to even);
-  * 4-bit group of 128 or 64 channels: z = fp16(min), s = fp16(fl32(fl32(max -
+  * 4-bit group of 128 or 64 channels: z = fp16(min) (a zero as +0), s = fp16(fl32(fl32(max -
     min) / 15)), code = clamp(rint(fl32(fl32(x - z) / s)), 0, 15), 0 where s is 0,
     of bf16 values saturated to +-65504 with NaN as 0; a code stands for s code + z;
   * the query at position p sees the tokens t <= p with t < sinks or t > p -
@@ -49,7 +49,7 @@ def quantise4(bits: np.ndarray, group: int):
     x = np.where(np.isnan(x), np.float32(0), np.clip(x, np.float32(-65504), np.float32(65504)))
     x = x.reshape(*x.shape[:-1], D // group, group)
     mn, mx = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
-    z = mn.astype(np.float16)
+    z = (mn + np.float32(0)).astype(np.float16)          # a zero is +0
     s = ((mx - mn).astype(np.float32) / np.float32(15)).astype(np.float16)
     with np.errstate(divide="ignore", invalid="ignore"):
         t = ((x - z.astype(np.float32)).astype(np.float32) / s.astype(np.float32)).astype(np.float32)

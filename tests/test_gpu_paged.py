@@ -266,6 +266,8 @@ def test_append_matches_the_oracle_bit_for_bit(b, group, hq, hkv, dim, interleav
     x = g.standard_normal((rows, hq + 2 * hkv, D)).astype(np.float32)
     x[3] = 0.25                                   # a constant token: scale 0
     x[4, :, 7] = 300000.0                         # beyond fp16
+    x[5, hq + hkv:, 3] = np.nan                   # (values are stored as they are, or saturated)
+    x[6, hq + hkv:, 9] = -np.inf
     bits = paged.bf16_bits(x)
     qkv = bf16(bits)
     q, k, v = qkv.split([hq, hkv, hkv], 1)        # strided views of one tensor
