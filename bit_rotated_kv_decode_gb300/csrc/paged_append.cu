@@ -37,6 +37,21 @@ __device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
   return d;
 }
 __device__ __forceinline__ uint32_t neg_bf2(uint32_t a) { return a ^ 0x80008000u; }
+// two fp32 operations in one instruction, each rounded by itself
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
 __device__ __forceinline__ uint32_t swap16(uint32_t a) { return __byte_perm(a, a, 0x1032); }
 
 __device__ __forceinline__ int find_req(const PagedRows& r, int n, int row) {
@@ -56,41 +71,65 @@ __device__ __forceinline__ int64_t page_of(const PagedView& p, int i, int pos) {
   return -1;
 }
 
-// Codes of 8 channels (four words of bf16 pairs) with scale s > 0 or s = 0 and zero z.
-// t = (x - z) * (1 / s) with an approximate reciprocal is within 15 (2^-22 + 2^-23) of
-// the quotient (one reciprocal and one product, quotients up to 15 and a little), so
-// its rounding decides the code unless it lies within 2^-16 of a half; then the exact
-// quotient does.  Magic: adding 1.5 2^23 rounds to the nearest integer, ties to even.
-template <bool SATURATE>
-__device__ __forceinline__ float value_of(float x) {
-  return !SATURATE ? x : x == x ? fminf(fmaxf(x, -65504.0f), 65504.0f) : 0.0f;
+// The rare paths are functions of their own: inlined for every row, they made the kernel
+// wait for its instructions.
+__device__ __forceinline__ float saturated(float x) {
+  return x == x ? fminf(fmaxf(x, -65504.0f), 65504.0f) : 0.0f;
 }
-template <bool SATURATE>
-__device__ __forceinline__ uint32_t codes_of(const uint32_t (&x)[4], float s, float z) {
+__device__ __forceinline__ float element(const uint4& x, int e) {
+  const uint32_t w = e < 4 ? (e < 2 ? x.x : x.y) : (e < 6 ? x.z : x.w);
+  return e & 1 ? bf_hi(w) : bf_lo(w);
+}
+// Codes of 8 channels by the definition.
+__device__ __noinline__ uint32_t codes_exact(uint4 x, float s, float z) {
+  uint32_t w = 0;
+#pragma unroll 1
+  for (int e = 7; e >= 0; --e) {
+    const float t = rintf(__fdiv_rn(__fsub_rn(saturated(element(x, e)), z), s));
+    const int code = s == 0.0f ? 0 : static_cast<int>(fminf(fmaxf(t, 0.0f), 15.0f));
+    w = w << 4 | static_cast<uint32_t>(code);
+  }
+  return w;
+}
+// Least and greatest of 8 saturated channels.
+__device__ __noinline__ float2 range_exact(uint4 x) {
+  float2 r = make_float2(INFINITY, -INFINITY);
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {
+    const float v = saturated(element(x, e));
+    r.x = fminf(r.x, v);
+    r.y = fmaxf(r.y, v);
+  }
+  return r;
+}
+
+// Codes of 8 finite channels within fp16 (four words of bf16 pairs) with scale s > 0 or
+// s = 0 and zero z.  t = (x - z) * (1 / s) with an approximate reciprocal is within
+// 15 (2^-23 + 2^-24) of the quotient (one reciprocal and one product, quotients up to 15
+// and a little), so its rounding decides the code unless it lies within 2^-16 of a half;
+// then the exact quotient does.  Magic: adding 1.5 2^23 rounds to the nearest integer,
+// ties to even.
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&x)[4], float s, float z, bool wild) {
   constexpr float MAGIC = 12582912.0f;
   float inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
   if (s == 0.0f) inv = 0.0f;
-  float worst = 0.0f;
-  uint32_t w = 0;
+  float worst = wild ? 1.0f : 0.0f;
+  const float2 zz = make_float2(-z, -z), ii = make_float2(inv, inv), mm = make_float2(MAGIC, MAGIC),
+               nn = make_float2(-MAGIC, -MAGIC);
+  // r's bits are those of MAGIC plus the code: weighted by 16^e they add up to the word
+  // plus a constant
+  uint32_t w = 0u - 0x4B400000u * 0x11111111u;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float v = value_of<SATURATE>(e & 1 ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1]));
-    const float t = fminf(fmaxf(__fsub_rn(v, z) * inv, 0.0f), 15.0f);
-    const float r = __fadd_rn(t, MAGIC);
-    worst = fmaxf(worst, fabsf(t - __fsub_rn(r, MAGIC)));
-    w |= (__float_as_uint(r) & 15u) << (4 * e);
+  for (int k = 0; k < 4; ++k) {
+    float2 t = mul2(add2(make_float2(bf_lo(x[k]), bf_hi(x[k])), zz), ii);
+    t.x = fminf(fmaxf(t.x, 0.0f), 15.0f);
+    t.y = fminf(fmaxf(t.y, 0.0f), 15.0f);
+    const float2 r = add2(t, mm), back = add2(r, nn);
+    worst = fmaxf(worst, fmaxf(fabsf(t.x - back.x), fabsf(t.y - back.y)));
+    w += (__float_as_uint(r.x) << (8 * k)) + (__float_as_uint(r.y) << (8 * k + 4));
   }
-  if (worst > 0.5f - 0x1p-16f) {
-    w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = value_of<SATURATE>(e & 1 ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1]));
-      const float t = rintf(__fdiv_rn(__fsub_rn(v, z), s));
-      const int code = s == 0.0f ? 0 : static_cast<int>(fminf(fmaxf(t, 0.0f), 15.0f));
-      w |= static_cast<uint32_t>(code) << (4 * e);
-    }
-  }
+  if (worst > 0.5f - 0x1p-16f) w = codes_exact(make_uint4(x[0], x[1], x[2], x[3]), s, z);
   return w;
 }
 
@@ -141,21 +180,20 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
       mn[g] = INFINITY;
       mx[g] = -INFINITY;
     }
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+      const float2 v = range_exact(u ? make_uint4(x[1][0], x[1][1], x[1][2], x[1][3])
+                                     : make_uint4(x[0][0], x[0][1], x[0][2], x[0][3]));
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = value_of<true>(e & 1 ? bf_hi(x[u][e >> 1]) : bf_lo(x[u][e >> 1]));
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-          if (NG == 1 || c[u] / (GK / 8) == g) {
-            mn[g] = fminf(mn[g], v);
-            mx[g] = fmaxf(mx[g], v);
-          }
-      }
+      for (int g = 0; g < NG; ++g)
+        if (NG == 1 || (u ? c[1] : c[0]) / (GK / 8) == g) {
+          mn[g] = fminf(mn[g], v.x);
+          mx[g] = fmaxf(mx[g], v.y);
+        }
+    }
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-#pragma unroll
+#pragma unroll 1
       for (int off = 1; off < 8; off <<= 1) {
         mn[g] = fminf(mn[g], __shfl_xor_sync(0xffffffffu, mn[g], off));
         mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
@@ -170,23 +208,29 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
   if (!ok) return;
   uint8_t* codes = rec + (which ? I4_V_CODES : 0) + slot * I4_ROW;
   uint8_t* meta = rec + (which ? i4_v_meta(GK) : I4_META) + slot * i4_meta_row(GK);
+  uint32_t w[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int g = NG == 1 ? 0 : c[u] / (GK / 8);
     const __half sh = NG == 1 || g == 0 ? s[0] : s[NG - 1], zh = NG == 1 || g == 0 ? z[0] : z[NG - 1];
-    const float sf = __half2float(sh), zf = __half2float(zh);
-    *reinterpret_cast<uint32_t*>(codes + 4 * c[u]) = wild ? codes_of<true>(x[u], sf, zf) : codes_of<false>(x[u], sf, zf);
+    w[u] = codes_of(x[u], __half2float(sh), __half2float(zh), wild);
     if (c[u] % (GK / 8) == 0)
       *reinterpret_cast<uint32_t*>(meta + 4 * g) =
           static_cast<uint32_t>(__half_as_ushort(sh)) | (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
+  }
+  if (c[1] == c[0] + 1) {
+    *reinterpret_cast<uint2*>(codes + 4 * c[0]) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint32_t*>(codes + 4 * c[0]) = w[0];
+    *reinterpret_cast<uint32_t*>(codes + 4 * c[1]) = w[1];
   }
 }
 
 // One warp takes 16 head rows (query, key and value heads in this order) of one
 // token: four groups of 8 lanes, a lane holding both chunks of its channel pairs,
 // so that the rotation needs no exchange and the cosines and sines are loaded
-// once for all rows.  The kernel moves each byte once; all loads of a lane
-// (8 x 16 B) are in flight together.
+// once for all rows.  The kernel moves each byte once, and its traffic bounds it: in BF16
+// all loads of a lane (8 x 16 B) are in flight together.
 template <int GK, bool INTERLEAVED>
 __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_constant__ PagedView p,
                                                                    const __grid_constant__ PagedRows rows,
@@ -206,9 +250,7 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
   int c[2];
   c[0] = !INTERLEAVED && rot ? pc : 2 * pc;
   c[1] = !INTERLEAVED && rot ? pc + half_chunks : 2 * pc + 1;
-  uint32_t x[APP_ROWS][2][4];
-#pragma unroll
-  for (int r = 0; r < APP_ROWS; ++r) {
+  auto load_row = [&](int r, uint32_t (&x)[2][4]) {
     const int h = head0 + 4 * r;
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     if (h < total) {
@@ -218,9 +260,13 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
       a = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c[0]));
       b = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c[1]));
     }
-    x[r][0][0] = a.x, x[r][0][1] = a.y, x[r][0][2] = a.z, x[r][0][3] = a.w;
-    x[r][1][0] = b.x, x[r][1][1] = b.y, x[r][1][2] = b.z, x[r][1][3] = b.w;
-  }
+    x[0][0] = a.x, x[0][1] = a.y, x[0][2] = a.z, x[0][3] = a.w;
+    x[1][0] = b.x, x[1][1] = b.y, x[1][2] = b.z, x[1][3] = b.w;
+  };
+  constexpr int AHEAD = GK == 0 ? APP_ROWS : 1;   // rows loaded before the first is worked on
+  uint32_t first[AHEAD][2][4];
+#pragma unroll
+  for (int r = 0; r < AHEAD; ++r) load_row(r, first[r]);
   const int i = find_req(rows, p.n, row);
   const int pos = rows.pos0[i] + (row - rows.row0[i]);
   // pair e of the lane: element e of both chunks, or elements 2e, 2e + 1 of the 16
@@ -236,32 +282,32 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
   const bool writes_kv = head0 + 4 * (APP_ROWS - 1) >= hq;
   const int64_t page = writes_kv ? page_of(p, i, pos) : -1;
   const int slot = pos % PAGE;
-#pragma unroll
-  for (int r = 0; r < APP_ROWS; ++r) {
+  auto do_row = [&](int r, uint32_t (&x)[2][4]) {
     const int h = head0 + 4 * r;
     if (rot && h < hq + p.Hkv) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        // (scalar operations: packed ones of two are contracted to fused multiply-adds)
         if constexpr (INTERLEAVED) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float a = bf_lo(x[r][u][k]), b = bf_hi(x[r][u][k]), co = cs[4 * u + k], si = sn[4 * u + k];
-            x[r][u][k] = pack_bf(__fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si)),
+            const float a = bf_lo(x[u][k]), b = bf_hi(x[u][k]), co = cs[4 * u + k], si = sn[4 * u + k];
+            x[u][k] = pack_bf(__fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si)),
                                  __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si)));
           }
         } else {
-          const float a0 = bf_lo(x[r][0][k]), a1 = bf_hi(x[r][0][k]), b0 = bf_lo(x[r][1][k]), b1 = bf_hi(x[r][1][k]);
-          x[r][0][k] = pack_bf(__fsub_rn(__fmul_rn(a0, cs[2 * k]), __fmul_rn(b0, sn[2 * k])),
+          const float a0 = bf_lo(x[0][k]), a1 = bf_hi(x[0][k]), b0 = bf_lo(x[1][k]), b1 = bf_hi(x[1][k]);
+          x[0][k] = pack_bf(__fsub_rn(__fmul_rn(a0, cs[2 * k]), __fmul_rn(b0, sn[2 * k])),
                                __fsub_rn(__fmul_rn(a1, cs[2 * k + 1]), __fmul_rn(b1, sn[2 * k + 1])));
-          x[r][1][k] = pack_bf(__fadd_rn(__fmul_rn(b0, cs[2 * k]), __fmul_rn(a0, sn[2 * k])),
+          x[1][k] = pack_bf(__fadd_rn(__fmul_rn(b0, cs[2 * k]), __fmul_rn(a0, sn[2 * k])),
                                __fadd_rn(__fmul_rn(b1, cs[2 * k + 1]), __fmul_rn(a1, sn[2 * k + 1])));
         }
       }
     }
     const bool is_q = h < hq;
     const int which = h >= hq + p.Hkv, kvh = h - hq - (which ? p.Hkv : 0);
-    const uint4 a = make_uint4(x[r][0][0], x[r][0][1], x[r][0][2], x[r][0][3]);
-    const uint4 b = make_uint4(x[r][1][0], x[r][1][1], x[r][1][2], x[r][1][3]);
+    const uint4 a = make_uint4(x[0][0], x[0][1], x[0][2], x[0][3]);
+    const uint4 b = make_uint4(x[1][0], x[1][1], x[1][2], x[1][3]);
     if (is_q) {
       uint16_t* dst = in.q_out + ((size_t)row * in.Hq + h) * D;
       *reinterpret_cast<uint4*>(dst + 8 * c[0]) = a;
@@ -278,7 +324,28 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
     } else {
       // the whole warp takes part in the reductions' shuffles
       uint8_t* rec = static_cast<uint8_t*>(p.pool) + (ok ? ((size_t)page * p.Hkv + kvh) * i4_record(GK) : 0);
-      if (__any_sync(0xffffffffu, ok)) store_int4<GK>(rec, which, slot, c, x[r], ok);
+      if (__any_sync(0xffffffffu, ok)) store_int4<GK>(rec, which, slot, c, x, ok);
+    }
+  };
+  if constexpr (GK == 0) {
+#pragma unroll
+    for (int r = 0; r < APP_ROWS; ++r) do_row(r, first[r]);
+  } else {
+    // one copy of the quantiser's code (four do not fit the instruction cache: 102 us for
+    // 16K tokens); the next row is loaded under it
+#pragma unroll 1
+    for (int r = 0; r < APP_ROWS; ++r) {
+      uint32_t x[2][4], next[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[u][k] = first[0][u][k];
+      if (r + 1 < APP_ROWS) load_row(r + 1, next);
+      do_row(r, x);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) first[0][u][k] = next[u][k];
     }
   }
 }
