@@ -382,49 +382,53 @@ def _paged_check(st: int, what: str) -> None:
         raise OscarError(st, f"{what}: {load().oscar_paged_last_error().decode()}")
 
 
-def _device(name: str, t) -> None:
-    import torch
+# These calls are made for every layer of a decode step, so their checks are kept to a
+# few attribute reads per tensor; what fails one is explained by _explain().
+_torch = None
+
+
+def _context(stream):
+    """(torch, device, raw stream) that a call goes to."""
+    global _torch
+    if _torch is None:
+        import torch
+        torch.cuda.init()
+        _torch = torch
+    device = _torch._C._cuda_getDevice()
+    if stream is None:
+        return _torch, device, _torch._C._cuda_getCurrentRawStream(device)
+    return _torch, device, _stream_ptr(stream)
+
+
+def _explain(name: str, t, dtype, shape, device: int):
     if not t.is_cuda:
         _refuse(f"{name}: a CUDA tensor is wanted")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != device:
         _refuse(f"{name} is on another device than the current one")
-
-
-def _on_device(name: str, t, dtype, shape=None, device=None) -> int:
-    """Address of a dense CUDA tensor of the current device with the given type and shape."""
-    if t.dtype is not dtype or not t.is_contiguous():
-        _refuse(f"{name}: a dense {dtype} CUDA tensor is wanted")
-    if device is None or t.get_device() != device:
-        _device(name, t)
+    if t.dtype is not dtype:
+        _refuse(f"{name}: {t.dtype}, wanted {dtype}")
     if shape is not None and t.shape != shape:
         _refuse(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    _refuse(f"{name} must be dense")
+
+
+def _dense(name: str, t, dtype, shape, device: int) -> int:
+    """Address of a dense tensor of the current device with the given type and shape (None: any)."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or (
+            shape is not None and t.shape != shape):
+        _explain(name, t, dtype, shape, device)
     return t.data_ptr()
 
 
-def _heads(name: str, t, rows: int, heads: int, device: int):
+def _heads(name: str, t, bf16, rows: int, heads: int, device: int):
     """Address and token stride of bf16 [rows][heads][128] whose heads lie densely."""
-    import torch
-    if t.dtype is not torch.bfloat16:
-        _refuse(f"{name}: a bfloat16 CUDA tensor is wanted")
-    if t.get_device() != device:
-        _device(name, t)
-    if t.shape != (rows, heads, HEAD_DIM):
-        _refuse(f"{name}: shape {tuple(t.shape)}, wanted {(rows, heads, HEAD_DIM)}")
+    shape = (rows, heads, HEAD_DIM)
+    if t.dtype is not bf16 or t.get_device() != device or t.shape != shape:
+        _explain(name, t, bf16, shape, device)
     stride, inner, last = t.stride()
-    if (heads > 1 and inner != HEAD_DIM) or last != 1:
+    if last != 1 or (inner != HEAD_DIM and heads > 1):
         _refuse(f"{name}: heads must lie densely")
     return t.data_ptr(), stride if rows > 1 else heads * HEAD_DIM
-
-
-def _current(stream):
-    """(device, raw stream) that a call goes to; the device -1 without a GPU, which no tensor is on."""
-    import torch
-    if not torch.cuda.is_initialized():
-        torch.cuda.init()
-    device = torch.cuda.current_device()
-    if stream is None:
-        return device, torch._C._cuda_getCurrentRawStream(device)
-    return device, _stream_ptr(stream)
 
 
 def _counts(values, n: int, name: str):
@@ -433,53 +437,45 @@ def _counts(values, n: int, name: str):
         return None, n
     if len(values) != n:
         _refuse(f"{name}: one per request is wanted")
-    arr = (c_int32 * n)(*values)
-    return arr, sum(values)
+    if n == 0 or min(values) < 0:
+        _refuse(f"{name}: no requests, or negative")
+    return (c_int32 * n)(*values), sum(values)
 
 
-def _pool16(kv, num_kv_heads, device):
-    import torch
-    return _on_device("kv", kv, torch.bfloat16, (kv.shape[0], num_kv_heads, 2, 64, HEAD_DIM), device)
-
-
-def _pool4(kv, num_kv_heads, group_size, device):
-    import torch
-    if group_size not in INT4_RECORD_BYTES:
+def _pool(kv, torch, num_kv_heads, group, device):
+    if not group:
+        return _dense("kv", kv, torch.bfloat16, (kv.shape[0], num_kv_heads, 2, 64, HEAD_DIM), device)
+    if group[0] not in INT4_RECORD_BYTES:
         _refuse("group_size must be 128 or 64")
-    return _on_device("kv", kv, torch.uint8, (kv.shape[0], num_kv_heads, INT4_RECORD_BYTES[group_size]), device)
-
-
-def _pool(kv, num_kv_heads, group, device):
-    return _pool4(kv, num_kv_heads, group[0], device) if group else _pool16(kv, num_kv_heads, device)
+    return _dense("kv", kv, torch.uint8, (kv.shape[0], num_kv_heads, INT4_RECORD_BYTES[group[0]]), device)
 
 
 def _append(fn, group, kv, page_table, lens, k, v, rope, q, q_out, new_lens, interleaved, error, stream):
-    import torch
-    device, s = _current(stream)
-    n, hkv = len(lens), k.shape[1]
-    pool = _pool(kv, hkv, group, device)
+    torch, device, s = _context(stream)
+    n, hkv, bf16 = len(lens), k.shape[1], torch.bfloat16
+    pool = _pool(kv, torch, hkv, group, device)
     old, _ = _counts(lens, n, "lens")
     new, rows = _counts(new_lens, n, "new_lens")
-    if n == 0 or min(lens) < 0 or (new is not None and min(new_lens) < 0):
-        _refuse("no requests, or negative lens or new_lens")
-    table = _on_device("page_table", page_table, torch.int32, (n, page_table.shape[1]), device)
-    kp, ks = _heads("k", k, rows, hkv, device)
-    vp, vs = _heads("v", v, rows, hkv, device)
-    hq, qp, qs, qo = 0, None, 0, None
-    if (q is None) != (q_out is None):
-        _refuse("q and q_out come together")
-    if q is not None:
+    max_pages = page_table.shape[1]
+    table = _dense("page_table", page_table, torch.int32, (n, max_pages), device)
+    kp, ks = _heads("k", k, bf16, rows, hkv, device)
+    vp, vs = _heads("v", v, bf16, rows, hkv, device)
+    hq, qp, qs, qo, r, err = 0, None, 0, None, None, None
+    if q is not None and q_out is not None:
         hq = q.shape[1]
-        qp, qs = _heads("q", q, rows, hq, device)
-        qo = _on_device("q_out", q_out, torch.bfloat16, (rows, hq, HEAD_DIM), device)
-    r = None
+        qp, qs = _heads("q", q, bf16, rows, hq, device)
+        qo = _dense("q_out", q_out, bf16, (rows, hq, HEAD_DIM), device)
+    elif q is not q_out:
+        _refuse("q and q_out come together")
     if rope is not None:
         length, dim = rope.shape
-        r = ctypes.byref(oscar_rope(_on_device("rope", rope, torch.float32, None, device), length, dim, interleaved))
-    err = None if error is None else _on_device("error", error, torch.int32, None, device)
+        r = oscar_rope(_dense("rope", rope, torch.float32, None, device), length, dim, interleaved)
+    if error is not None:
+        err = _dense("error", error, torch.int32, None, device)
     if rows:
-        _paged_check(fn(pool, kv.shape[0], table, page_table.shape[1], old, new, n, hq, hkv, *group, r, qp, qs, kp, ks,
-                        vp, vs, qo, err, s), "append")
+        st = fn(pool, kv.shape[0], table, max_pages, old, new, n, hq, hkv, *group, r, qp, qs, kp, ks, vp, vs, qo, err, s)
+        if st:
+            _paged_check(st, "append")
 
 
 def bf16_append(kv, page_table, lens, k, v, rope=None, q=None, q_out=None, new_lens=None, interleaved: bool = False,
@@ -502,67 +498,63 @@ def int4_append(kv, page_table, lens, k, v, rope=None, q=None, q_out=None, new_l
 def int4_read(kv, page_table, starts, counts, k_out, v_out, group_size: int = 128, error=None, stream=None) -> None:
     """The values of tokens [starts[i], starts[i] + counts[i]) of each request of a 4-bit pool, into k_out and v_out
     [rows][Hkv][128], fp32 or bf16."""
-    import torch
-    device, s = _current(stream)
+    torch, device, s = _context(stream)
     n, hkv = len(starts), kv.shape[1]
-    pool = _pool4(kv, hkv, group_size, device)
+    pool = _pool(kv, torch, hkv, (group_size,), device)
     first, _ = _counts(starts, n, "starts")
     count, rows = _counts(counts, n, "counts")
-    if n == 0 or min(starts) < 0 or min(counts) < 0:
-        _refuse("no requests, or negative starts or counts")
-    table = _on_device("page_table", page_table, torch.int32, (n, page_table.shape[1]), device)
+    max_pages = page_table.shape[1]
+    table = _dense("page_table", page_table, torch.int32, (n, max_pages), device)
     kind = k_out.dtype
     if kind is not torch.float32 and kind is not torch.bfloat16:
         _refuse("k_out and v_out: float32 or bfloat16")
-    ko = _on_device("k_out", k_out, kind, (rows, hkv, HEAD_DIM), device)
-    vo = _on_device("v_out", v_out, kind, (rows, hkv, HEAD_DIM), device)
-    err = None if error is None else _on_device("error", error, torch.int32, None, device)
+    shape = (rows, hkv, HEAD_DIM)
+    ko = _dense("k_out", k_out, kind, shape, device)
+    vo = _dense("v_out", v_out, kind, shape, device)
+    err = None if error is None else _dense("error", error, torch.int32, None, device)
     if rows:
-        _paged_check(load().oscar_int4_read(pool, kv.shape[0], table, page_table.shape[1], first, count, n, hkv,
-                                            group_size, ko, vo, OSCAR_F32 if kind is torch.float32 else OSCAR_BF16,
-                                            err, s), "read")
+        st = load().oscar_int4_read(pool, kv.shape[0], table, max_pages, first, count, n, hkv, group_size, ko, vo,
+                                    OSCAR_F32 if kind is torch.float32 else OSCAR_BF16, err, s)
+        if st:
+            _paged_check(st, "read")
 
 
 def attention_workspace(n: int, num_q_heads: int, num_kv_heads: int, q_lens=None, stream=None):
     """Zeroed workspace for window_attention / int4_attention calls of n requests."""
-    import torch
-    device, s = _current(stream)
+    torch, device, s = _context(stream)
     need = load().oscar_attention_workspace_bytes(n, _counts(q_lens, n, "q_lens")[0], num_q_heads, num_kv_heads)
     if need == 0:
         _refuse("arguments outside the supported limits")
-    with torch.cuda.stream(torch.cuda.ExternalStream(s, device) if stream is not None else None):
+    with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device)):
         return new_workspace(need)
 
 
 def _attention(fn, group, kv, page_table, lens, q, out, hkv, window, sinks, q_lens, scale, lse, workspace, error,
                stream):
-    import torch
-    device, s = _current(stream)
-    n, hq = len(lens), q.shape[1]
-    pool = _pool(kv, hkv, group, device)
+    torch, device, s = _context(stream)
+    n, hq, kind, f32 = len(lens), q.shape[1], out.dtype, torch.float32
+    pool = _pool(kv, torch, hkv, group, device)
     total, _ = _counts(lens, n, "lens")
     new, rows = _counts(q_lens, n, "q_lens")
-    if n == 0 or (new is not None and min(q_lens) < 0):
-        _refuse("no requests, or negative q_lens")
-    table = _on_device("page_table", page_table, torch.int32, (n, page_table.shape[1]), device)
-    qp, qs = _heads("q", q, rows, hq, device)
-    kind = out.dtype
-    if kind is not torch.float32 and kind is not torch.bfloat16:
+    max_pages = page_table.shape[1]
+    table = _dense("page_table", page_table, torch.int32, (n, max_pages), device)
+    qp, qs = _heads("q", q, torch.bfloat16, rows, hq, device)
+    if kind is not f32 and kind is not torch.bfloat16:
         _refuse("out: float32 or bfloat16")
-    op = _on_device("out", out, kind, (rows, hq, HEAD_DIM), device)
-    lp = None if lse is None else _on_device("lse", lse, torch.float32, (rows, hq), device)
-    err = None if error is None else _on_device("error", error, torch.int32, None, device)
+    op = _dense("out", out, kind, (rows, hq, HEAD_DIM), device)
+    lp = None if lse is None else _dense("lse", lse, f32, (rows, hq), device)
+    err = None if error is None else _dense("error", error, torch.int32, None, device)
     if workspace is None:
         workspace = attention_workspace(n, hq, hkv, q_lens, stream)
     while rows:
-        st = fn(pool, kv.shape[0], table, page_table.shape[1], total, new, n, hq, hkv, *group, window, sinks, scale, qp,
-                qs, op, OSCAR_F32 if kind is torch.float32 else OSCAR_BF16, lp, err,
-                _on_device("workspace", workspace, torch.uint8, None, device), workspace.numel(), s)
-        if st == OSCAR_ERR_INVALID_ARG and load().oscar_paged_last_error() == b"workspace too small":
-            workspace = attention_workspace(n, hq, hkv, q_lens, stream)
-            continue
-        _paged_check(st, "attention")
-        break
+        st = fn(pool, kv.shape[0], table, max_pages, total, new, n, hq, hkv, *group, window, sinks, scale, qp, qs, op,
+                OSCAR_F32 if kind is f32 else OSCAR_BF16, lp, err,
+                _dense("workspace", workspace, torch.uint8, None, device), workspace.numel(), s)
+        if not st:
+            break
+        if load().oscar_paged_last_error() != b"workspace too small":
+            _paged_check(st, "attention")
+        workspace = attention_workspace(n, hq, hkv, q_lens, stream)
     return workspace
 
 

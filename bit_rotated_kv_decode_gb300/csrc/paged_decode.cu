@@ -54,9 +54,9 @@ struct DecodeShape {
   // registers and two pages each in shared memory allow.
   static constexpr int NW = GK == 0 || NR == 16 ? 8 : 12;
   static constexpr int THREADS = 32 * NW;
-  static constexpr int FOLD = NR == 4 ? 4 : NR == 8 ? 2 : 1;   // warps folded at a time
+  static constexpr int FOLD = NR == 4 ? 2 : 1;   // warps folded at a time between segments
   static constexpr size_t LIMIT = 232448 - 1024;   // shared memory of a CTA, less the alignment
-  static constexpr size_t FIXED = sizeof(float) * FOLD * NR * PARTIAL_FLOATS + 1024;
+  static constexpr size_t FIXED = sizeof(float) * FOLD * NR * PARTIAL_FLOATS + 2048 * ((NR + 7) / 8) + 1024;
   static constexpr int FIT = static_cast<int>((LIMIT - FIXED) / (NW * Format<GK>::BYTES));
   static constexpr int STAGES = FIT > 3 ? 3 : FIT;
   static_assert(STAGES >= 2, "a ring needs two stages");
@@ -68,6 +68,8 @@ struct alignas(1024) DecodeSmem {
   static constexpr int FOLD = DecodeShape<GK, NR>::FOLD;
   alignas(1024) uint8_t ring[NW][STAGES][Format<GK>::BYTES];
   alignas(16) float state[FOLD][NR][PARTIAL_FLOATS];
+  alignas(16) uint32_t q[(NR + 7) / 8][8][4][16];   // the first product's B operand: [tile][column][lane % 4][register]
+  float q_scale[NR], q_sum[2][NR];
   uint64_t full[NW][STAGES];
   int last;
 };
@@ -79,10 +81,11 @@ struct DecodeArgs {
   int32_t total;                            // units of the call
   float* partials;
   int32_t* counters;
-  int32_t len[PAGED_MAX_REQ];
-  int32_t row[PAGED_MAX_REQ];
-  int32_t table[PAGED_MAX_REQ];
-  int32_t ustart[PAGED_MAX_REQ + 1];        // units before request i (all its kv heads)
+  // request i; side by side, since each line of the arguments comes from a cold cache
+  struct Req {
+    int32_t len, row, table;
+    int32_t ustart;                         // units before it (all its kv heads)
+  } req[PAGED_MAX_REQ];
 };
 
 // The visible units of a request: [0, sink) and [first, first + units - sink).  An
@@ -110,7 +113,7 @@ struct Cursor {
 };
 template <int UT>
 __device__ __forceinline__ void cursor_load(const DecodeArgs& A, Cursor& c) {
-  c.un = Units::of(A.len[c.req], A.m, A.a.window, A.a.sinks, UT);
+  c.un = Units::of(A.req[c.req].len, A.m, A.a.window, A.a.sinks, UT);
   c.seg_end = c.base + max(c.un.units, 1);
 }
 template <int UT>
@@ -118,10 +121,10 @@ __device__ __forceinline__ void cursor_first(const DecodeArgs& A, Cursor& c, int
   int lo = 0, hi = A.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (A.ustart[mid] <= u) lo = mid; else hi = mid;
+    if (A.req[mid].ustart <= u) lo = mid; else hi = mid;
   }
   c.req = lo;
-  c.base = A.ustart[lo];
+  c.base = A.req[lo].ustart;
   cursor_load<UT>(A, c);
   const int per = c.seg_end - c.base;
   c.head = (u - c.base) / per;
@@ -231,82 +234,84 @@ struct Query {
   int pos[C::H];
 };
 
-__device__ __forceinline__ const uint16_t* q_row(const DecodeArgs& A, int req, int head, int r) {
-  return A.a.q + (int64_t)(A.row[req] + r / A.G) * A.a.q_stride + (int64_t)(head * A.G + r % A.G) * D;
+// The segment's query rows into shared memory as the B operand, 16 lanes a row, 8
+// channels a lane, by the first NR / 2 warps; take_query() is behind a barrier.  (A warp
+// of its own for every row made the same operand twelve times, 7000 cycles of it.)
+template <int GK, int NR>
+__device__ __forceinline__ void put_query(const DecodeArgs& A, int req, int head, DecodeSmem<GK, NR>& sm) {
+  using C = Cols<GK, NR>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 15;
+  if (warp >= NR / 2) return;
+  const int r = 2 * warp + (lane >> 4);
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (r < A.m * A.G)
+    w = __ldg(reinterpret_cast<const uint4*>(A.a.q + (int64_t)(A.req[req].row + r / A.G) * A.a.q_stride +
+                                             (int64_t)(head * A.G + r % A.G) * D) + part);
+  if constexpr (GK == 0) {
+    // channels 8 part ..: k-step part / 2, register part % 2, one word for each of the four lanes
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (C::DUP) sm.q[0][2 * r][k][part] = sm.q[0][2 * r + 1][k][part] = ww[k];
+      else sm.q[r / 8][r % 8][k][part] = ww[k];
+    }
+  } else {
+    // scaled so that the row's largest |q| lies in [2^13, 2^14): exact in fp16 down to 2^-27 of it
+    float f[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                  __uint_as_float(w.y & 0xffff0000u), __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u),
+                  __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u)};
+    float mx = 0.0f, sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      mx = fmaxf(mx, fabsf(f[e]));
+      sum += f[e];
+    }
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      if (GK == 128 || off < 8) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    }
+    // exponent of the largest, from its bits; clamped so that both powers of two are normal
+    int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
+    ex = max(-112, min(ex, 112));
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - ex) << 23);
+    // the 8 channels are one code word's: codes 2 sub, 2 sub + 1 and those 4 behind
+    const uint4 o = make_uint4(f16x2(f[0] * up, f[4] * up), f16x2(f[1] * up, f[5] * up), f16x2(f[2] * up, f[6] * up),
+                               f16x2(f[3] * up, f[7] * up));
+    const int tid = GK == 128 ? part / 4 : (part % 8) / 2, word = GK == 128 ? part % 4 : 2 * (part / 8) + part % 2;
+    if constexpr (C::DUP)
+      *reinterpret_cast<uint4*>(&sm.q[0][2 * r][tid][4 * word]) =
+          *reinterpret_cast<uint4*>(&sm.q[0][2 * r + 1][tid][4 * word]) = o;
+    else
+      *reinterpret_cast<uint4*>(&sm.q[r / 8][r % 8][tid][4 * word]) = o;
+    if (part % 8 == 0) {
+      sm.q_scale[r] = __uint_as_float(static_cast<uint32_t>(127 + ex - 13) << 23) * A.a.scale2;
+      sm.q_sum[part / 8][r] = sum * A.a.scale2;
+    }
+  }
 }
 
 template <int GK, int NR>
-__device__ __forceinline__ void load_query(const DecodeArgs& A, int req, int head, Query<GK, NR>& Q) {
+__device__ __forceinline__ void take_query(const DecodeArgs& A, int req, const DecodeSmem<GK, NR>& sm,
+                                           Query<GK, NR>& Q) {
   using C = Cols<GK, NR>;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-  const int R = A.m * A.G, len = A.len[req];
+  const int first = A.req[req].len - A.m;
+#pragma unroll
+  for (int j = 0; j < C::QT; ++j)
+#pragma unroll
+    for (int s = 0; s < 8; s += 2) {
+      const uint4 w = *reinterpret_cast<const uint4*>(&sm.q[j][gid][tid][2 * s]);
+      Q.b[j][s][0] = w.x, Q.b[j][s][1] = w.y, Q.b[j][s + 1][0] = w.z, Q.b[j][s + 1][1] = w.w;
+    }
 #pragma unroll
   for (int h = 0; h < C::H; ++h) {
-    const int r = min(C::row(h, tid), R - 1);
-    Q.pos[h] = len - A.m + r / A.G;
-    Q.scale[h] = A.a.scale2;
-  }
+    const int r = C::row(h, tid);
+    Q.pos[h] = first + min(r, A.m * A.G - 1) / A.G;
+    Q.scale[h] = GK == 0 ? A.a.scale2 : sm.q_scale[r];
+    if constexpr (GK != 0) {
 #pragma unroll
-  for (int j = 0; j < C::QT; ++j) {
-    const int r = C::DUP ? gid >> 1 : 8 * j + gid;
-    const uint16_t* q = q_row(A, req, head, r < R ? r : 0);
-    if constexpr (GK == 0) {
-#pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const uint32_t x0 = __ldg(reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * tid));
-        const uint32_t x1 = __ldg(reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * tid + 8));
-        Q.b[j][s][0] = r < R ? x0 : 0u;
-        Q.b[j][s][1] = r < R ? x1 : 0u;
-      }
-    } else {
-      // the lane's 32 channels (those of its share of a code row), scaled so that the
-      // row's largest |q| lies in [2^13, 2^14): exact in fp16 down to 2^-27 of it
-      float f[32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ch = GK == 128 ? 32 * tid + 8 * i : 64 * (i / 2) + 16 * tid + 8 * (i % 2);
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(q + ch));
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[8 * i + 2 * k] = __uint_as_float(ww[k] << 16);
-          f[8 * i + 2 * k + 1] = __uint_as_float(ww[k] & 0xffff0000u);
-        }
-      }
-      float mx = 0.0f, sum[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        mx = fmaxf(mx, fabsf(f[c]));
-        sum[GK == 64 ? c / 16 : 0] += f[c];
-      }
-#pragma unroll
-      for (int off = 1; off < 4; off <<= 1) {
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
-        if (GK == 64) sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], off);
-      }
-      // exponent of the largest, from its bits; clamped so that both powers of two are normal
-      int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
-      ex = max(-112, min(ex, 112));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - ex) << 23);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          const float* x = f + 8 * i + 2 * sub;   // codes 2 sub, 2 sub + 1 of the word and those 4 behind
-          Q.b[j][2 * i + sub][0] = r < R ? f16x2(x[0] * up, x[4] * up) : 0u;
-          Q.b[j][2 * i + sub][1] = r < R ? f16x2(x[1] * up, x[5] * up) : 0u;
-        }
-      // column n's scale and sums to the lanes that hold its row: lane 4 n of the
-      // column's group has them
-      const float down = __uint_as_float(static_cast<uint32_t>(127 + ex - 13) << 23) * A.a.scale2;
-#pragma unroll
-      for (int k = 0; k < C::HPL; ++k) {
-        const int h = C::HPL * j + k, src = C::DUP ? 8 * tid : 4 * (2 * tid + k);
-        Q.scale[h] = __shfl_sync(0xffffffffu, down, src);
-        Q.qsum[0][h] = __shfl_sync(0xffffffffu, sum[0], src) * A.a.scale2;
-        if (GK == 64) Q.qsum[GK == 64][h] = __shfl_sync(0xffffffffu, sum[1], src) * A.a.scale2;
-      }
+      for (int g = 0; g < (GK == 64 ? 2 : 1); ++g) Q.qsum[g][h] = sm.q_sum[g][r];
     }
   }
 }
@@ -341,12 +346,12 @@ __device__ __forceinline__ void weights(const float (&w0)[Cols<GK, NR>::H], cons
 
 // One unit of 16 BF16 tokens from t0: stage = two halves of 64 channels, each K
 // [16][128 B] and V [16][128 B], 16-byte pieces swizzled within 8 rows by the TMA.
-template <int NR, bool MASKED>
+template <int NR>
 __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR>& Q, State<0, NR>& S, uint8_t* stage,
-                                          int t0) {
+                                          int t0, bool masked) {
   using C = Cols<0, NR>;
   const int lane = threadIdx.x & 31, gid = lane >> 2;
-  if constexpr (MASKED) {
+  if (masked) {
     // value rows that no row of the segment sees may hold anything: zero them
     const int row = lane & 15, p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);   // the first query token
     bool any = false;
@@ -378,7 +383,7 @@ __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR
   for (int h = 0; h < C::H; ++h) {
     x0[h] = s[h / C::HPL][h % C::HPL] * Q.scale[h];
     x1[h] = s[h / C::HPL][2 + h % C::HPL] * Q.scale[h];
-    if constexpr (MASKED) {
+    if (masked) {
       if (!sees(A.a, Q.pos[h], t0 + gid)) x0[h] = NEG_INF;
       if (!sees(A.a, Q.pos[h], t0 + gid + 8)) x1[h] = NEG_INF;
     }
@@ -418,15 +423,33 @@ __device__ __forceinline__ uint32_t code_hi(uint32_t w, uint32_t magic) {
 
 // One 4-bit page (64 tokens from t0) as it lies in memory.  Row r of a 16-token tile is token r ^ ((r >> 1) & 1), which spreads
 // both products' reads over the banks.
-template <int GK, int NR, bool MASKED>
+template <int GK, int NR>
 __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, NR>& Q, State<GK, NR>& S,
-                                          const uint8_t* stage, int t0) {
+                                          uint8_t* stage, int t0, bool masked) {
   using C = Cols<GK, NR>;
   constexpr int NG = State<GK, NR>::NG, TILES = PAGE / 16, MROW = i4_meta_row(GK);
   const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
   const int tok = gid ^ ((gid >> 1) & 1);
   uint32_t magic = 0x64006400u;
   asm volatile("" : "+r"(magic));
+  if (masked) {
+    // the scale and zero of a token that no row sees may be anything: zero them (its codes
+    // are finite whatever they are)
+    const int p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);   // the first query token
+#pragma unroll 1
+    for (int slot = lane; slot < PAGE; slot += 32) {
+      bool any = false;
+      for (int k = 0; k < A.m; ++k) any = any || sees(A.a, p0 + k, t0 + slot);
+      if (any) continue;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        *reinterpret_cast<uint32_t*>(stage + I4_META + MROW * slot + 4 * g) = 0;
+        *reinterpret_cast<uint32_t*>(stage + i4_v_meta(GK) + MROW * slot + 4 * g) = 0;
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+  }
   // ---- logits of the page
   float x[TILES][2][C::H];
 #pragma unroll
@@ -484,10 +507,18 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
         else
           y = fmaf(sk[0], s[j][0][k] * Q.scale[h], zk[0] * Q.qsum[0][h]) +
               fmaf(sk[1], s[j][1][k] * Q.scale[h], zk[1] * Q.qsum[1][h]);
-        if (MASKED && !sees(A.a, Q.pos[h], t0 + slot)) y = NEG_INF;
         x[t][u][h] = y;
       }
     }
+  }
+  if (masked) {
+#pragma unroll
+    for (int h = 0; h < C::H; ++h)
+#pragma unroll
+      for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (!sees(A.a, Q.pos[h], t0 + 16 * t + 8 * u + tok)) x[t][u][h] = NEG_INF;
   }
 #pragma unroll
   for (int h = 0; h < C::H; ++h) {
@@ -509,19 +540,9 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
   float mult[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    uint32_t big = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int slot = lane + 32 * k;
-      uint32_t bits = *reinterpret_cast<const uint16_t*>(vmeta + MROW * slot + 4 * g) & 0x7fffu;
-      if constexpr (MASKED) {   // a token that no row sees may hold anything
-        bool any = false;
-        const int p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);
-        for (int q = 0; q < A.m; ++q) any = any || sees(A.a, p0 + q, t0 + slot);
-        if (!any) bits = 0;
-      }
-      big = max(big, bits);
-    }
+    const uint32_t b0 = *reinterpret_cast<const uint16_t*>(vmeta + MROW * lane + 4 * g),
+                   b1 = *reinterpret_cast<const uint16_t*>(vmeta + MROW * (lane + 32) + 4 * g);
+    uint32_t big = max(b0 & 0x7fffu, b1 & 0x7fffu);
     big = __reduce_max_sync(0xffffffffu, big);
     // s < 2^e: normal numbers have e = (bits >> 10) - 14, subnormal ones e <= -14
     const int e = max(S.e[g], big >= 0x400u ? static_cast<int>(big >> 10) - 14 : (big ? -14 : -24));
@@ -553,9 +574,8 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
 #pragma unroll
         for (int h = 0; h < C::H; ++h) {
           const float pr = x[t][u][h];
-          const bool dead = MASKED && pr == 0.0f;   // its scale and zero may be anything
-          (u ? w1[h] : w0[h]) = dead ? 0.0f : pr * sv;
-          S.z[g][h] = dead ? S.z[g][h] : fmaf(pr, zv, S.z[g][h]);
+          (u ? w1[h] : w0[h]) = pr * sv;
+          S.z[g][h] = fmaf(pr, zv, S.z[g][h]);
         }
       }
       weights<GK, NR>(w0, w1, b[g], f16_hi, f16x2);
@@ -656,7 +676,7 @@ __device__ __forceinline__ void put_state(const State<GK, NR>& S, float (*st)[PA
 
 __device__ __forceinline__ void write_row(const DecodeArgs& A, int req, int head, int r, int lane, float4 o, float m,
                                           float l) {
-  const size_t row = (size_t)(A.row[req] + r / A.G) * A.a.Hq + (size_t)head * A.G + r % A.G;
+  const size_t row = (size_t)(A.req[req].row + r / A.G) * A.a.Hq + (size_t)head * A.G + r % A.G;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
   if (A.a.f32) {
@@ -668,37 +688,28 @@ __device__ __forceinline__ void write_row(const DecodeArgs& A, int req, int head
   if (A.a.lse && lane == 0) A.a.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : NEG_INF;
 }
 
-// Fold count states of one row, the warp's lanes holding 4 channels each.
+// Fold count states of one row, the warp's lanes holding 4 channels each.  The code runs
+// once in a launch, from a cold instruction cache: short, and no wider than it pays.
 template <typename P>
 __device__ __forceinline__ void fold(int count, P at, int lane, float4& o, float& m, float& l) {
   m = NEG_INF;
+#pragma unroll 1
   for (int c = lane; c < count; c += 32) m = fmaxf(m, __ldcg(at(c) + PARTIAL_M));
 #pragma unroll
   for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   l = 0.0f;
-  if (m == NEG_INF) return;
-  constexpr int U = 8;
-  for (int c0 = 0; c0 < count; c0 += U) {
-    float4 v[U];
-    float mv[U], lv[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float* p = at(min(c0 + u, count - 1));
-      v[u] = __ldcg(reinterpret_cast<const float4*>(p) + lane);
-      mv[u] = __ldcg(p + PARTIAL_M);
-      lv[u] = __ldcg(p + PARTIAL_L);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float f = c0 + u < count ? ex2f(mv[u] - m) : 0.0f;
-      if (f == 0.0f) continue;
-      l = fmaf(lv[u], f, l);
-      o.x = fmaf(v[u].x, f, o.x);
-      o.y = fmaf(v[u].y, f, o.y);
-      o.z = fmaf(v[u].z, f, o.z);
-      o.w = fmaf(v[u].w, f, o.w);
-    }
+  const float ref = m == NEG_INF ? 0.0f : m;
+#pragma unroll 4
+  for (int c = 0; c < count; ++c) {
+    const float* p = at(c);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + lane);
+    const float f = ex2f(__ldcg(p + PARTIAL_M) - ref);
+    l = fmaf(__ldcg(p + PARTIAL_L), f, l);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
   }
 }
 
@@ -720,56 +731,72 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
     mbar_init_fence();
   }
   __syncwarp();
+  Cursor cc;
+  cursor_first<UT>(A, cc, u0);
+  put_query<GK, NR>(A, cc.req, cc.head, sm);
 
-  // ---- the warp's copies: units u0 + warp, + NW, ... of the CTA's range
-  Cursor pc;
-  int pu = u0 + warp;
-  if (pu < u1) cursor_first<UT>(A, pc, pu);
-  int issued = 0;
+  // ---- the warp's copies: units u0 + warp, + NW, ... of the CTA's range.  Lane l looks
+  // up the place of unit 32 k + l of them, so that the page ids of 32 copies come at the
+  // price of one; place: record index (-1: nothing to copy) and first token in the page.
+  const int mine = u1 - u0 > warp ? (u1 - u0 - warp + NW - 1) / NW : 0;
+  int issued = 0, place_rec = -1, place_row = 0;
   bool dead = false;   // a wait gave up: no further copies
   auto issue = [&]() {
-    if (pu >= u1 || dead) return;
-    while (pu >= pc.seg_end) cursor_next<UT>(A, pc);
-    const int v = pu - pc.base;
-    const int st = issued % STAGES;
-    if (v < pc.un.units) {
-      const int t0 = pc.un.unit(v) * UT;
-      int32_t page = __ldg(A.p.table + (size_t)A.table[pc.req] * A.p.max_pages + t0 / PAGE);
-      if (page < 0 || page >= A.p.num_pages) {
-        if (lane == 0 && A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
-        page = 0;
-      }
-      const int64_t rec = (int64_t)page * A.p.Hkv + pc.head;
-      if (lane == 0) {
-        uint8_t* dst = sm.ring[warp][st];
-        mbar_expect_tx(&sm.full[warp][st], F::BYTES);
-        if constexpr (GK == 0) {
-          tma_load_3d(dst, &map, 0, t0 % PAGE, static_cast<int>(2 * rec), &sm.full[warp][st]);
-          tma_load_3d(dst + F::BYTES / 2, &map, 64, t0 % PAGE, static_cast<int>(2 * rec), &sm.full[warp][st]);
-        } else {
-          tma_load_1d(dst, static_cast<const uint8_t*>(A.p.pool) + rec * F::BYTES, F::BYTES, &sm.full[warp][st]);
+    if (issued >= mine || dead) return;
+    if ((issued & 31) == 0) {
+      place_rec = -1;
+      if (issued + lane < mine) {
+        Cursor c;
+        const int u = u0 + warp + NW * (issued + lane);
+        cursor_first<UT>(A, c, u);
+        const int v = u - c.base;
+        if (v < c.un.units) {
+          const int t0 = c.un.unit(v) * UT;
+          int32_t page = __ldg(A.p.table + (size_t)A.req[c.req].table * A.p.max_pages + t0 / PAGE);
+          if (page < 0 || page >= A.p.num_pages) {
+            if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
+            page = 0;
+          }
+          place_rec = page * A.p.Hkv + c.head;
+          place_row = t0 % PAGE;
         }
       }
-    } else if (lane == 0) {
-      mbar_arrive(&sm.full[warp][st]);   // nothing to copy
+      __syncwarp();
+    }
+    const int rec = __shfl_sync(0xffffffffu, place_rec, issued & 31);
+    const int row = __shfl_sync(0xffffffffu, place_row, issued & 31);
+    const int st = issued % STAGES;
+    if (lane == 0) {
+      uint64_t* full = &sm.full[warp][st];
+      if (rec >= 0) {
+        uint8_t* dst = sm.ring[warp][st];
+        mbar_expect_tx(full, F::BYTES);
+        if constexpr (GK == 0) {
+          tma_load_3d(dst, &map, 0, row, 2 * rec, full);
+          tma_load_3d(dst + F::BYTES / 2, &map, 64, row, 2 * rec, full);
+        } else {
+          tma_load_1d(dst, static_cast<const uint8_t*>(A.p.pool) + (size_t)rec * F::BYTES, F::BYTES, full);
+        }
+      } else {
+        mbar_arrive(full);
+      }
     }
     ++issued;
-    pu += NW;
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < STAGES; ++s) issue();
 
-  Cursor cc;
   int cu = u0 + warp, taken = 0;
-  if (u0 < u1) cursor_first<UT>(A, cc, u0);
   State<GK, NR> S;
   Query<GK, NR> Q;
   const int R = A.m * A.G;
   for (int seg_u = u0; seg_u < u1;) {
     const int seg_end = min(cc.seg_end, u1);
-    load_query<GK, NR>(A, cc.req, cc.head, Q);
+    if (seg_u > u0) put_query<GK, NR>(A, cc.req, cc.head, sm);
+    __syncthreads();
+    take_query<GK, NR>(A, cc.req, sm, Q);
     S.reset();
-    const int len = A.len[cc.req];
+    const int len = A.req[cc.req].len;
     for (; cu < seg_end; cu += NW) {
       const int v = cu - cc.base, st = taken % STAGES;
       if (!dead && !mbar_wait(&sm.full[warp][st], (taken / STAGES) & 1)) {
@@ -781,13 +808,10 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
         const int t0 = cc.un.unit(v) * UT;
         const bool masked = !(t0 + UT - 1 <= len - A.m &&
                               (t0 + UT <= A.a.sinks || (int64_t)t0 > (int64_t)len - 1 - A.a.window));
-        if constexpr (GK == 0) {
-          if (masked) bf16_unit<NR, true>(A, Q, S, sm.ring[warp][st], t0);
-          else bf16_unit<NR, false>(A, Q, S, sm.ring[warp][st], t0);
-        } else {
-          if (masked) int4_unit<GK, NR, true>(A, Q, S, sm.ring[warp][st], t0);
-          else int4_unit<GK, NR, false>(A, Q, S, sm.ring[warp][st], t0);
-        }
+        if constexpr (GK == 0)
+          bf16_unit<NR>(A, Q, S, sm.ring[warp][st], t0, masked);
+        else
+          int4_unit<GK, NR>(A, Q, S, sm.ring[warp][st], t0, masked);
       }
       __syncwarp();
       ++taken;
@@ -801,6 +825,10 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
     const int c_hi = static_cast<int>(((int64_t)cc.seg_end * A.ncta - 1) / A.total);
     const bool whole = seg_end - seg_u == full_units;
     constexpr int FOLD = SM::FOLD, MINE = (NR + NW - 1) / NW;   // rows of a warp
+    using StateRows = float (*)[PARTIAL_FLOATS];
+    static_assert(sizeof(float) * NR * PARTIAL_FLOATS <= sizeof(sm.ring[0]), "a state fits its warp's ring");
+    const bool final_seg = seg_end == u1;   // no copy is in flight: every warp's state over its own ring, at once
+    const int step = final_seg ? NW : FOLD;
     float4 fo[MINE];
     float fm[MINE], fl[MINE];
 #pragma unroll
@@ -809,35 +837,31 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
       fm[i] = NEG_INF;
       fl[i] = 0.0f;
     }
-    for (int w0 = 0; w0 < NW; w0 += FOLD) {
-      if (warp >= w0 && warp < w0 + FOLD) put_state<GK, NR>(S, sm.state[warp - w0]);
+#pragma unroll 1
+    for (int w0 = 0; w0 < NW; w0 += step) {
+      if (warp >= w0 && warp < w0 + step)
+        put_state<GK, NR>(S, final_seg ? reinterpret_cast<StateRows>(sm.ring[warp][0]) : sm.state[warp - w0]);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < MINE; ++i) {
         const int r = warp + NW * i;
         if (r >= R) continue;
-        float m = fm[i];
-#pragma unroll
-        for (int w = 0; w < FOLD; ++w) m = fmaxf(m, sm.state[w][r][PARTIAL_M]);
-        if (m == NEG_INF) continue;
         float4& o = fo[i];
-        const float f0 = ex2f(fm[i] - m);
-        fm[i] = m;
-        fl[i] *= f0;
-        o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
-#pragma unroll
-        for (int w = 0; w < FOLD; ++w) {
-          const float f = ex2f(sm.state[w][r][PARTIAL_M] - m);
-          if (f == 0.0f) continue;
-          const float4 x = reinterpret_cast<const float4*>(sm.state[w][r])[lane];
-          fl[i] = fmaf(sm.state[w][r][PARTIAL_L], f, fl[i]);
-          o.x = fmaf(x.x, f, o.x);
-          o.y = fmaf(x.y, f, o.y);
-          o.z = fmaf(x.z, f, o.z);
-          o.w = fmaf(x.w, f, o.w);
+#pragma unroll 2
+        for (int w = 0; w < step; ++w) {
+          const float* st = final_seg ? reinterpret_cast<StateRows>(sm.ring[w][0])[r] : sm.state[w][r];
+          const float ms = st[PARTIAL_M], m = fmaxf(fm[i], ms), ref = m == NEG_INF ? 0.0f : m;
+          const float f0 = ex2f(fm[i] - ref), f = ex2f(ms - ref);
+          const float4 x = reinterpret_cast<const float4*>(st)[lane];
+          fm[i] = m;
+          fl[i] = fmaf(st[PARTIAL_L], f, fl[i] * f0);
+          o.x = fmaf(x.x, f, o.x * f0);
+          o.y = fmaf(x.y, f, o.y * f0);
+          o.z = fmaf(x.z, f, o.z * f0);
+          o.w = fmaf(x.w, f, o.w * f0);
         }
       }
-      __syncthreads();
+      if (!final_seg) __syncthreads();
     }
     float* rec = A.partials + (size_t)(seg + cta) * NR * PARTIAL_FLOATS;
 #pragma unroll
@@ -894,9 +918,13 @@ cudaError_t launch_decode_t(DecodeArgs& A, const CUtensorMap& map, int sms, cuda
     if (e != cudaSuccess) return e;
     if (dev < 32) done |= 1u << dev;
   }
-  // one CTA per SM, fewer where a CTA's warps would have no unit each
+  // One CTA per SM; where a CTA's warps would have no unit each, fewer; and one per
+  // segment where that leaves its warps at most three units, since folding a segment's
+  // CTAs takes longer than two units.
   constexpr int NW = DecodeShape<GK, NR>::NW;
-  const int most = (A.total - 1) / NW + 1, ctas = most < sms ? most : sms;
+  const int most = (A.total - 1) / NW + 1, segments = A.n * A.p.Hkv;
+  int ctas = most < sms ? most : sms;
+  if (segments <= sms && A.total <= 3 * NW * segments) ctas = segments;
   A.ncta = ctas;
   paged_decode_kernel<GK, NR><<<ctas, DecodeShape<GK, NR>::THREADS, bytes, s>>>(A, map);
   return cudaGetLastError();
@@ -931,15 +959,11 @@ cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, 
   const int ut = gk == 0 ? Format<0>::UT : PAGE;
   int64_t total = 0;
   for (int i = 0; i < n; ++i) {
-    A.len[i] = reqs[i].len;
-    A.row[i] = reqs[i].row;
-    A.table[i] = reqs[i].table;
-    A.ustart[i] = static_cast<int32_t>(total);
+    A.req[i] = {reqs[i].len, reqs[i].row, reqs[i].table, static_cast<int32_t>(total)};
     const Units u = Units::of(reqs[i].len, A.m, a.window, a.sinks, ut);
     total += (int64_t)p.Hkv * (u.units > 0 ? u.units : 1);
     if (total > INT32_MAX) return cudaErrorInvalidValue;
   }
-  A.ustart[n] = static_cast<int32_t>(total);
   A.total = static_cast<int32_t>(total);
   static const CUtensorMap none = {};
   const CUtensorMap& m = map ? *map : none;

@@ -38,6 +38,7 @@ const char* check_pages(const void* pool, int64_t num_pages, const int32_t* tabl
   if (n < 1 || n > PAGED_MAX_REQ) return "between 1 and 256 requests";
   if (num_pages < 1 || num_pages > INT32_MAX || max_pages < 1) return "bad page counts";
   if (hkv < 1 || hkv > 1024) return "bad number of kv heads";
+  if (num_pages * hkv > INT32_MAX / 2) return "pages x kv heads: below 2^30";
   return nullptr;
 }
 
@@ -125,6 +126,7 @@ bool pool_map(CUtensorMap* map, const void* pool, int64_t records, uint32_t toke
   return map_3d(map, pool, PAGE, static_cast<cuuint64_t>(2 * records), D * 2, (cuuint64_t)PAGE * D * 2, tokens, parts);
 }
 
+// SMs of the current device; 152 where there is none.
 int sm_count() {
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
