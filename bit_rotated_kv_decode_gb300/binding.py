@@ -13,7 +13,7 @@ from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uin
 
 import numpy as np
 
-from .build import LIB
+from .build import CALLS, LIB
 
 OSCAR_OK = 0
 OSCAR_ERR_INVALID_ARG = 1
@@ -382,9 +382,33 @@ def _paged_check(st: int, what: str) -> None:
         raise OscarError(st, f"{what}: {load().oscar_paged_last_error().decode()}")
 
 
-# These calls are made for every layer of a decode step, so their checks are kept to a
-# few attribute reads per tensor; what fails one is explained by _explain().
+# These calls are made for every layer of a decode step, so they are marshalled in C
+# (csrc/calls.c).  What that does not take as it is -- a tensor that fails a check, no
+# workspace yet, a stream of its own, lengths that are no list of ints -- goes the same way
+# in Python below, which says what is wrong.
 _torch = None
+_calls = None
+
+
+def calls():
+    """The extension that marshals the paged calls (loaded once; raises if it has not been built)."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
+        if not os.path.exists(CALLS):
+            raise RuntimeError(f"extension {CALLS} is missing: run bit_rotated_kv_decode_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_oscar_calls", CALLS)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_oscar_calls", loader))
+        loader.exec_module(mod)
+        torch, lib = _context(None)[0], load()
+        mod.setup((torch.bfloat16, torch.float32, torch.int32, torch.uint8),
+                  (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream),
+                  tuple(ctypes.cast(fn, c_void_p).value for fn in (
+                      lib.oscar_bf16_append, lib.oscar_int4_append, lib.oscar_int4_read, lib.oscar_window_attention,
+                      lib.oscar_int4_attention)))
+        _calls = mod
+    return _calls
 
 
 def _context(stream):
@@ -451,6 +475,12 @@ def _pool(kv, torch, num_kv_heads, group, device):
 
 
 def _append(fn, group, kv, page_table, lens, k, v, rope, q, q_out, new_lens, interleaved, error, stream):
+    st = (_calls or calls()).append(group[0] if group else 0, kv, page_table, lens, k, v, rope, q, q_out, new_lens,
+                                    interleaved, error, stream)
+    if st == 0:
+        return
+    if st is not None:
+        _paged_check(st, "append")
     torch, device, s = _context(stream)
     n, hkv, bf16 = len(lens), k.shape[1], torch.bfloat16
     pool = _pool(kv, torch, hkv, group, device)
@@ -498,6 +528,11 @@ def int4_append(kv, page_table, lens, k, v, rope=None, q=None, q_out=None, new_l
 def int4_read(kv, page_table, starts, counts, k_out, v_out, group_size: int = 128, error=None, stream=None) -> None:
     """The values of tokens [starts[i], starts[i] + counts[i]) of each request of a 4-bit pool, into k_out and v_out
     [rows][Hkv][128], fp32 or bf16."""
+    st = (_calls or calls()).read(group_size, kv, page_table, starts, counts, k_out, v_out, error, stream)
+    if st == 0:
+        return
+    if st is not None:
+        _paged_check(st, "read")
     torch, device, s = _context(stream)
     n, hkv = len(starts), kv.shape[1]
     pool = _pool(kv, torch, hkv, (group_size,), device)
@@ -531,6 +566,12 @@ def attention_workspace(n: int, num_q_heads: int, num_kv_heads: int, q_lens=None
 
 def _attention(fn, group, kv, page_table, lens, q, out, hkv, window, sinks, q_lens, scale, lse, workspace, error,
                stream):
+    st = (_calls or calls()).attend(group[0] if group else 0, kv, page_table, lens, q, out, hkv, window, sinks, q_lens,
+                                    scale, lse, workspace, error, stream)
+    if st == 0:
+        return workspace
+    if st is not None and load().oscar_paged_last_error() != b"workspace too small":
+        _paged_check(st, "attention")
     torch, device, s = _context(stream)
     n, hq, kind, f32 = len(lens), q.shape[1], out.dtype, torch.float32
     pool = _pool(kv, torch, hkv, group, device)

@@ -2,7 +2,8 @@
 
 Produces ``bit_rotated_kv_decode_gb300/_lib/liboscar_gb300.so`` (CUDA runtime
 linked statically).  Translation units are compiled in parallel; a unit is
-rebuilt when its source or a header is newer than its object.
+rebuilt when its source or a header is newer than its object.  Beside it goes
+``_oscar_calls.so``, the Python extension that marshals the arguments of the paged calls.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "liboscar_gb300.so")
+CALLS = os.path.join(LIBDIR, "_oscar_calls.so")   # argument marshalling for Python (csrc/calls.c)
 SOURCES = ["host.cpp", "write_kernels.cu", "decode_kernels.cu", "decode_scratch.cu", "bf16_decode.cu",
            "paged_host.cpp", "paged_append.cu", "paged_decode.cu", "paged_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -58,6 +61,11 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or _stale(obj, [path] + headers):
             extra = ["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []
             jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", path, "-o", obj])
+
+    calls_src = os.path.join(CSRC, "calls.c")
+    if force or _stale(CALLS, [calls_src] + headers):
+        jobs.append([shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-Wall", "-I" + INCLUDE,
+                     "-I" + sysconfig.get_paths()["include"], calls_src, "-o", CALLS])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -411,6 +411,48 @@ def test_prefill_then_decode_steps(b, group):
         lens = now
 
 
+# ---- the two ways through the binding -----------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 128])
+def test_both_ways_through_the_binding_agree(b, group):
+    """Calls marshalled in C (lists, the current stream, a workspace) and in Python (other sequences, a stream given):
+    the same results; and the first kind is taken where it should be."""
+    n, hq, hkv = 3, 8, 2
+    kv = b.int4_pool(6, hkv) if group else torch.zeros(6, hkv, 2, PAGE, D, dtype=torch.bfloat16, device="cuda")
+    kv2 = kv.clone()
+    table = torch.tensor([[5, 0], [1, 2], [3, 4]], dtype=torch.int32, device="cuda")
+    qkv = torch.randn(n, hq + 2 * hkv, D, device="cuda").to(torch.bfloat16)
+    q, k, v = qkv.split([hq, hkv, hkv], 1)
+    rope = b.rope_table(128)
+    s = torch.cuda.current_stream()
+    lens, new = [0, 70, 64], [1, 1, 1]
+    extra = dict(group_size=group) if group else {}
+    append, attend = (b.int4_append, b.int4_attention) if group else (b.bf16_append, b.window_attention)
+    ws = b.attention_workspace(n, hq, hkv)
+    qa, qb = torch.empty_like(q), torch.empty_like(q)
+    oa, ob = torch.empty(n, hq, D, device="cuda"), torch.empty(n, hq, D, device="cuda")
+    taken = b.calls().append(group, kv, table, lens, k, v, rope, q, qa, new, False, None, None)
+    assert taken == 0
+    append(kv2, table, np.array(lens), k, v, rope, q=q, q_out=qb, stream=s, **extra)
+    assert torch.equal(qa, qb) and torch.equal(kv, kv2)
+    now = [1, 71, 65]
+    assert b.calls().attend(group, kv, table, now, qa, oa, hkv, 50, 2, None, 0.0, None, ws, None, None) == 0
+    attend(kv2, table, np.array(now), qb, ob, hkv, 50, 2, workspace=ws, stream=s, **extra)
+    assert torch.equal(oa, ob)
+    # what the C side does not take
+    for bad in (np.array(now), [1, 71], [1, 71, -1], [1, 71, 2.0], None, [1, 71, 2 ** 40]):
+        assert b.calls().attend(group, kv, table, bad, qa, oa, hkv, 50, 2, None, 0.0, None, ws, None, None) is None
+    assert b.calls().attend(group, kv, table, now, qa, oa, hkv, 50, 2, None, 0.0, None, None, None, None) is None
+    assert b.calls().attend("x", kv, table, now, qa, oa, hkv, 50, 2, None, 0.0, None, ws, None, None) is None
+    assert b.calls().attend(group, kv, table, now, qa.float(), oa, hkv, 50, 2, None, 0.0, None, ws, None, None) is None
+    assert b.calls().attend(group, kv, table.cpu(), now, qa, oa, hkv, 50, 2, None, 0.0, None, ws, None, None) is None
+    with pytest.raises(b.OscarError):
+        attend(kv, table, [1, 71, 200], qa, oa, hkv, 50, 2, workspace=ws, **extra)
+    small = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    grown = attend(kv, table, now, qa, ob, hkv, 50, 2, workspace=small, **extra)
+    assert grown.numel() > small.numel() and torch.equal(oa, ob)
+
+
 # ---- errors -------------------------------------------------------------------------
 @pytest.mark.gpu
 def test_bad_pages_set_the_error_word(b):

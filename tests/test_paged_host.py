@@ -152,3 +152,16 @@ def test_rope_table_keeps_far_angles(b):
     inv = np.longdouble(10000) ** (-2 * np.arange(32, dtype=np.longdouble) / 64)
     a = np.longdouble(100000) * inv
     assert np.abs(t[100000, :32] - np.cos(a)).max() < 2 ** -23 and np.abs(t[100000, 32:] - np.sin(a)).max() < 2 ** -23
+
+
+def test_marshalling_extension_takes_nothing_before_its_setup(b):
+    import importlib.machinery
+    import importlib.util
+    from bit_rotated_kv_decode_gb300 import build
+    loader = importlib.machinery.ExtensionFileLoader("_oscar_calls", build.CALLS)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_oscar_calls", loader))
+    loader.exec_module(mod)
+    assert mod.attend(*[None] * 15) is None and mod.append(*[None] * 13) is None and mod.read(*[None] * 9) is None
+    assert mod.attend() is None and mod.append(1) is None and mod.read("x", *[1] * 8) is None
+    with pytest.raises(TypeError):
+        mod.setup(1, 2, 3)
