@@ -120,12 +120,12 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float bf16_hi(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ float f16_hi(float x) { return __half2float(__float2half_rn(x)); }
-__device__ __forceinline__ void store_out(void* out, size_t at, float x, bool f32) {
-  if (f32)
-    static_cast<float*>(out)[at] = x;
-  else
-    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
+// Bits i of 64 tokens with i <= hi and (i >= lo or i < sinks): what a row sees of a page.
+__device__ __forceinline__ uint64_t visible_bits(int hi, int lo, int sinks) {
+  const uint64_t upto = hi < 0 ? 0 : ~0ull >> (63 - min(hi, 63));
+  const uint64_t from = lo > 63 ? 0 : ~0ull << max(lo, 0);
+  const uint64_t sink = sinks <= 0 ? 0 : ~0ull >> (64 - min(sinks, 64));
+  return upto & (from | sink);
 }
-
 }  // namespace paged
 }  // namespace oscar

@@ -15,10 +15,12 @@
 // leaves.  Sums are taken of the unrounded weights, in fp32.
 //
 // Roles: warps 0-3 and 4-7 the softmax of query tile 0 and 1, one thread per row (TMEM
-// lane = row); warps 8 and 9 the products of query tile 0 and 1; warp 10 the TMA copies.
+// lane = row); warps 8 and 9 the products of query tile 0 and 1; warp 10 the TMA copies;
+// warp 11 looks the items up, four ahead (each role doing that for itself took up to 2500
+// cycles between two items).
 // A query tile's chain is S -> softmax -> PV -> S of the next key tile, since P lies over
 // S in TMEM (S0, S1, O0, O1 take all 512 columns); the two query tiles' chains interleave.
-// P is handed over in halves of 64 keys.  Issuing is synchronous (64 cycles a product of
+// P is handed over in two parts.  Issuing is synchronous (64 cycles a product of
 // 128 x 128 x 16, as long as it runs; 110 a commit, 140 a wait even when ready), so one
 // warp issuing for both tiles left the tensor core idle for 1100 of 3430 cycles a key
 // tile; hence a warp for each, and V of a key tile and K of the next share a stage (two
@@ -37,26 +39,20 @@ namespace {
 
 using namespace paged;
 
-constexpr int PF_MMA_WARP = 8, PF_TMA_WARP = 10;
-constexpr int PF_THREADS = 32 * 12;            // three warpgroups, the last with one idle warp
+constexpr int PF_MMA_WARP = 8, PF_TMA_WARP = 10, PF_ITEM_WARP = 11;
+constexpr int PF_THREADS = 32 * 12;            // three warpgroups
 // Registers a thread: 168 at launch (three warpgroups share 504), then 208 for the
 // softmax's two warpgroups, which hold a row of logits each, and 88 for the third.
 constexpr int PF_REGS = 168, PF_SOFTMAX_REGS = 208, PF_OTHER_REGS = 88;
 static_assert(2 * PF_SOFTMAX_REGS + PF_OTHER_REGS <= 3 * PF_REGS, "a split above the launch's registers waits forever");
 constexpr int PF_STAGES = 2;                   // of V of a key tile and K of the next
+constexpr int PF_FIRST = 64;                   // keys of P handed over first
+constexpr int PF_ITEMS = 4;                    // items looked up ahead
+constexpr int PF_READERS = 11;                 // warps that read them
 constexpr int PF_ROWS = 128;                   // rows of a query tile
 constexpr int PF_KEYS = 2 * PAGE;              // keys of a tile
 constexpr int TILE_BYTES = 128 * D * 2;        // a Q, K or V tile
 
-struct alignas(1024) PrefillSmem {
-  alignas(1024) uint8_t q[2][TILE_BYTES];      // per tile: two halves of 64 channels, [128 rows][128 B] swizzled
-  alignas(1024) uint8_t kv[PF_STAGES][2][TILE_BYTES];   // V of key tile j - 1, K of key tile j
-  uint64_t q_full[2], q_empty[2], kv_full[PF_STAGES], kv_empty[PF_STAGES];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];   // per query tile (and half of the keys)
-  uint64_t turn[2];                              // the other tile's products of a key tile are issued
-  uint32_t tmem;
-};
-static_assert(sizeof(PrefillSmem) + 1024 <= 232448, "shared memory of a CTA");
 
 struct PrefillArgs {
   PagedView p;
@@ -64,6 +60,7 @@ struct PrefillArgs {
   int n, G, lg;                           // lg = log2 G
   int splits, items;                      // parts of an item's key tiles; items in all, parts counted
   float* partials;                        // [items][256][PARTIAL_FLOATS] where splits > 1
+  int wide;                               // out is 32-byte aligned
   int32_t len[PAGED_MAX_REQ];
   int32_t m[PAGED_MAX_REQ];
   int32_t row[PAGED_MAX_REQ];
@@ -100,37 +97,52 @@ struct KeyTiles {
 };
 
 // One item: up to 256 query rows of a kv head and their key tiles [j0, j1) of kt.
-struct Item {
-  int index, ri, head, tok0, tokens, tiles, p0, j0, j1;
+struct alignas(16) Item {
+  int index;               // -1: no more items
+  int head, table, row;    // kv head, row of the page table, first row of q and out
+  int tokens, p0, j0, j1;  // query tokens and the first one's position; key tiles
   KeyTiles kt;
-  // Item of a CTA's turn, false behind the last.  Later blocks of a request see more
-  // keys and come first; every other round goes through the CTAs backwards, so that the
-  // longer items of a round fall to different CTAs.
-  __device__ bool load(const PrefillArgs& A, int turn) {
+  __device__ int tiles(int per_tile) const { return tokens > per_tile ? 2 : 1; }
+  // Item of a CTA's turn.  Later blocks of a request see more keys and come first; every
+  // other round goes through the CTAs backwards, so that the longer items of a round fall
+  // to different CTAs.
+  __device__ void load(const PrefillArgs& A, int turn) {
     const int grid = gridDim.x, at = turn & 1 ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x);
     index = turn * grid + at;
-    if (index >= A.items) return false;
+    if (index >= A.items) {
+      index = -1;
+      return;
+    }
     head = index % A.p.Hkv;
     const int rest = index / A.p.Hkv, split = rest % A.splits, blk = A.bstart[A.n] - 1 - rest / A.splits;
-    int hi = A.n;
-    ri = 0;
+    int hi = A.n, ri = 0;
     while (hi - ri > 1) {
       const int mid = (ri + hi) >> 1;
       if (A.bstart[mid] <= blk) ri = mid; else hi = mid;
     }
     const int m = A.m[ri], per_tile = PF_ROWS >> A.lg;
-    tok0 = (blk - A.bstart[ri]) * 2 * per_tile;   // first token of the block, of the request's m
+    const int tok0 = (blk - A.bstart[ri]) * 2 * per_tile;   // first token of the block, of the request's m
+    table = A.table[ri];
+    row = A.row[ri] + tok0;
     tokens = min(2 * per_tile, m - tok0);
-    tiles = tokens > per_tile ? 2 : 1;
-    p0 = A.len[ri] - m + tok0;                    // its position
+    p0 = A.len[ri] - m + tok0;
     kt = KeyTiles::of(p0, p0 + tokens - 1, A.a.window, A.a.sinks);
     j0 = kt.count * split / A.splits;
     j1 = kt.count * (split + 1) / A.splits;
-    return true;
   }
 };
-// turns of a CTA: all but the last are full rounds
-__device__ __forceinline__ int turns(const PrefillArgs& A) { return (A.items + gridDim.x - 1) / gridDim.x; }
+
+struct alignas(1024) PrefillSmem {
+  alignas(1024) uint8_t q[2][TILE_BYTES];      // per tile: two halves of 64 channels, [128 rows][128 B] swizzled
+  alignas(1024) uint8_t kv[PF_STAGES][2][TILE_BYTES];   // V of key tile j - 1, K of key tile j
+  uint64_t q_full[2], q_empty[2], kv_full[PF_STAGES], kv_empty[PF_STAGES];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];   // per query tile (and half of the keys)
+  uint64_t turn[2];                              // the other tile's products of a key tile are issued
+  uint64_t item_full[PF_ITEMS], item_empty[PF_ITEMS];
+  Item item[PF_ITEMS];
+  uint32_t tmem;
+};
+static_assert(sizeof(PrefillSmem) + 1024 <= 232448, "shared memory of a CTA");
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -180,6 +192,18 @@ __device__ __forceinline__ uint64_t desc_nmajor(uint32_t addr) {
 constexpr uint32_t IDESC_QK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t IDESC_PV = IDESC_QK | (1u << 16);
 
+// 32 bytes of a row, one sector in one store where the address allows (a thread writes a
+// row of its own, so a warp's store touches 32 lines whatever its width).
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 // Issued by one elected lane of a converged warp: the code around stays uniform, so that
 // descriptors are computed in uniform registers (under an if of one lane, each product
 // cost its six operand moves, and a key tile of the issuing warp 4700 cycles).
@@ -260,6 +284,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       mbar_init(&sm.o_full[a], 1);
       mbar_init(&sm.turn[a], 1);
     }
+    for (int s = 0; s < PF_ITEMS; ++s) {
+      mbar_init(&sm.item_full[s], 1);
+      mbar_init(&sm.item_empty[s], PF_READERS);
+    }
     mbar_init_fence();
   }
   if (warp == PF_MMA_WARP) {
@@ -275,30 +303,51 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     if (A.p.err) atomicOr(A.p.err, PAGED_ERR_TIMEOUT);
   };
 
-  const int rounds = turns(A), per_tile = PF_ROWS >> A.lg;
+  const int per_tile = PF_ROWS >> A.lg;
   if (warp >= PF_MMA_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PF_OTHER_REGS));
-    Item it;
-    if (warp == PF_TMA_WARP) {
+    if (warp == PF_ITEM_WARP) {
+      // ---- items
+      if (lane == 0) {
+        for (int turn = 0;; ++turn) {
+          const int at = turn % PF_ITEMS;
+          if (turn >= PF_ITEMS && !mbar_wait(&sm.item_empty[at], (turn / PF_ITEMS - 1) & 1)) {
+            gave_up();
+            break;
+          }
+          Item next;
+          next.load(A, turn);
+          sm.item[at] = next;
+          mbar_arrive(&sm.item_full[at]);
+          if (next.index < 0) break;
+        }
+      }
+    } else if (warp == PF_TMA_WARP) {
       // ---- copies
       if (lane == 0) {
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity); };
         int stage = 0, q_loads[2] = {0, 0};   // stages and query tiles loaded so far
-        for (int turn = 0; turn < rounds && ok; ++turn) {
-          if (!it.load(A, turn)) break;
+        for (int turn = 0; ok; ++turn) {
+          const int at = turn % PF_ITEMS;
+          wait(&sm.item_full[at], (turn / PF_ITEMS) & 1);
+          if (!ok) break;
+          const Item it = sm.item[at];
+          mbar_arrive(&sm.item_empty[at]);
+          if (it.index < 0) break;
           const KeyTiles& kt = it.kt;
           if (it.j0 == it.j1) continue;
-          for (int a = 0; a < it.tiles; ++a) {
+          const int tiles = it.tiles(per_tile);
+          for (int a = 0; a < tiles; ++a) {
             if (q_loads[a] > 0) wait(&sm.q_empty[a], (q_loads[a] - 1) & 1);
             if (!ok) break;
             ++q_loads[a];
             mbar_expect_tx(&sm.q_full[a], TILE_BYTES);
             for (int h = 0; h < 2; ++h)
               tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, it.head * A.G,
-                          A.row[it.ri] + it.tok0 + a * per_tile, &sm.q_full[a]);
+                          it.row + a * per_tile, &sm.q_full[a]);
           }
-          const int32_t* pt = A.p.table + (size_t)A.table[it.ri] * A.p.max_pages;
+          const int32_t* pt = A.p.table + (size_t)it.table * A.p.max_pages;
           // records of the pages of key tile j, -1: no second one
           auto tile_records = [&](int j, int (&rec)[2]) {
 #pragma unroll
@@ -360,12 +409,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       int batch = 0;      // [PV, S] turns of items with two tiles
       int tile = 0;       // key tiles of this query tile
       int done = 0;       // items of this query tile
-      for (int turn = 0; turn < rounds && ok; ++turn) {
-        if (!it.load(A, turn)) break;
+      for (int turn = 0; ok; ++turn) {
+        const int at = turn % PF_ITEMS;
+        wait(&sm.item_full[at], (turn / PF_ITEMS) & 1);
+        if (!ok) break;
+        const Item it = sm.item[at];
+        __syncwarp();
+        mbar_arrive_elected(&sm.item_empty[at]);
+        if (it.index < 0) break;
         const KeyTiles& kt = it.kt;
         if (it.j0 == it.j1) continue;
-        const bool two = it.tiles == 2;
-        if (a >= it.tiles) {   // no rows: only free the stages
+        const bool two = it.tiles(per_tile) == 2;
+        if (a > 0 && !two) {   // no rows: only free the stages
           for (int j = it.j0; j <= it.j1 && ok; ++j, ++stage) {
             wait(&sm.kv_full[stage % PF_STAGES], (stage / PF_STAGES) & 1);
             if (ok) mbar_arrive_elected(&sm.kv_empty[stage % PF_STAGES]);
@@ -412,18 +467,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const uint64_t v = v_desc + st * (2 * TILE_BYTES >> 4);
           if (two && a + batch > 0) wait(&sm.turn[a], (a == 0 ? batch - 1 : batch) & 1);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {   // P's halves, 64 keys each
+          for (int h = 0; h < 2; ++h) {   // P's parts
             wait(&sm.p_full[a][h], tile & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_ts(o_col, s_col + 64 * h + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV,
-                     (j > it.j0 || h > 0 || s > 0) ? 1u : 0u);
-            if constexpr (F32) {
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                mma_ts(o_col, s_col + 64 * h + 32 + 8 * s, v + ((8192 * h + 2048 * s) >> 4), IDESC_PV, 1u);
+            for (int s = h ? PF_FIRST / 16 : 0; s < (h ? 8 : PF_FIRST / 16); ++s) {   // 16 keys
+              const uint32_t col = s_col + 64 * (s / 4) + 8 * (s % 4);
+              mma_ts(o_col, col, v + (2048 * s >> 4), IDESC_PV, (j > it.j0 || s > 0) ? 1u : 0u);
+              if constexpr (F32) mma_ts(o_col, col + 32, v + (2048 * s >> 4), IDESC_PV, 1u);
             }
           }
           if (!ok) break;
@@ -444,7 +496,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   } else {
     // ---- softmax of query tile a, one thread per row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PF_SOFTMAX_REGS));
-    Item it;
     const int a = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lane_off + 128 * a, to = tmem + lane_off + 256 + 128 * a;
@@ -452,9 +503,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     const int tok = a * per_tile + (r >> A.lg);
     bool ok = true;
     int tile = 0, done = 0;   // key tiles and items so far
-    for (int turn = 0; turn < rounds && ok; ++turn) {
-      if (!it.load(A, turn)) break;
-      if (a >= it.tiles) continue;
+    for (int turn = 0; ok; ++turn) {
+      const int at = turn % PF_ITEMS;
+      ok = mbar_wait_warp(&sm.item_full[at], (turn / PF_ITEMS) & 1, ok);
+      if (!ok) break;
+      const Item& it = sm.item[at];
+      auto release = [&]() {   // the warp has read the item
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty[at]);
+      };
+      if (it.index < 0) break;
+      if (a >= it.tiles(per_tile)) {
+        release();
+        continue;
+      }
       const int pmin = it.p0 + a * per_tile, pmax = it.p0 + min(it.tokens, (a + 1) * per_tile) - 1;
       const int pos = min(it.p0 + tok, pmax);
       // pages from t0 that every row sees whole: t0 <= all_to and (t0 <= all_sinks or t0 > all_from)
@@ -475,9 +537,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int u = 0; u < 2; ++u) {
           const int v = 2 * j + u, t0 = v >= pages ? 1 << 30 : (v < sink ? v : v + skip) * PAGE;
           if (!(t0 <= all_to && (t0 <= all_sinks || t0 > all_from))) {
-            const int hi = pos - t0, lo = lo0 - t0, sk = A.a.sinks - t0;
+            // (bits first: comparing every key took 1500 cycles a page)
+            const uint64_t see = visible_bits(pos - t0, lo0 - t0, A.a.sinks - t0);
+            const uint32_t half[2] = {static_cast<uint32_t>(see), static_cast<uint32_t>(see >> 32)};
 #pragma unroll
-            for (int i = 0; i < PAGE; ++i) x[PAGE * u + i] = i <= hi && (i >= lo || i < sk) ? x[PAGE * u + i] : NEG_INF;
+            for (int i = 0; i < PAGE; ++i)
+              x[PAGE * u + i] = half[i / 32] & (1u << (i % 32)) ? x[PAGE * u + i] : NEG_INF;
           }
         }
         float t[4];
@@ -507,46 +572,52 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
         const float ref = mx == NEG_INF ? 0.0f : -mx;
         const float2 scale_2 = make_float2(scale2, scale2), ref_2 = make_float2(ref, ref);
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        // 64 keys at a time: the product of the first half starts while the second is computed
+        float2 sum[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
+        // 32 keys at a time: the product of the first part starts while the last is computed
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[16], low[16];
+        for (int c = 0; c < 4; ++c) {
+          float2 y[16];
+          uint32_t pk[16], low[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int e = 64 * h + 32 * c + 2 * i;
-              float2 y = fma2(make_float2(x[e], x[e + 1]), scale_2, ref_2);
-              y.x = ex2f(y.x);
-              y.y = ex2f(y.y);
-              sum[i & 1] = add2(sum[i & 1], y);
-              pk[i] = bf16x2(y.x, y.y);
-              if constexpr (F32)
-                low[i] = bf16x2(y.x - __uint_as_float(pk[i] << 16), y.y - __uint_as_float(pk[i] & 0xffff0000u));
-            }
-            tmem_st16(ts + 64 * h + 16 * c, pk);
-            if constexpr (F32) tmem_st16(ts + 64 * h + 32 + 16 * c, low);
+          for (int i = 0; i < 16; ++i)
+            y[i] = fma2(make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), scale_2, ref_2);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            y[i].x = ex2f(y[i].x);
+            y[i].y = ex2f(y[i].y);
           }
-          tc_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_full[a][h]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            pk[i] = bf16x2(y[i].x, y[i].y);
+            sum[i & 3] = add2(sum[i & 3], y[i]);
+            if constexpr (F32)
+              low[i] = bf16x2(y[i].x - __uint_as_float(pk[i] << 16), y[i].y - __uint_as_float(pk[i] & 0xffff0000u));
+          }
+          // P lies over S, 64 keys in 32 columns (and their second parts in the next 32)
+          const int col = 64 * (c / 2) + 16 * (c % 2);
+          tmem_st16(ts + col, pk);
+          if constexpr (F32) tmem_st16(ts + col + 32, low);
+          if (c == PF_FIRST / 32 - 1 || c == 3) {
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[a][c == 3]);
+          }
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
       }
-      // the item once more: nothing of it is held in registers over the loop
-      int again = turn;
-      asm volatile("" : "+r"(again));
-      it.load(A, again);
-      const bool some = it.j1 > it.j0, valid = tok < it.tokens;
+      const bool some = j1 > j0, valid = tok < it.tokens;
+      const size_t row = (size_t)(it.row + tok) * A.a.Hq + (size_t)it.head * A.G + (r & (A.G - 1));
+      float* part = A.partials + ((size_t)it.index * 2 * PF_ROWS + a * PF_ROWS + r) * PARTIAL_FLOATS;
+      release();
       if (some) ok = mbar_wait_warp(&sm.o_full[a], done & 1, ok);
       if (!ok) break;
       tc_fence_after();
       const bool split = A.splits > 1;
-      const size_t row = (size_t)(A.row[it.ri] + it.tok0 + tok) * A.a.Hq + (size_t)it.head * A.G + (r & (A.G - 1));
       const float inv = split ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-      float* part = A.partials + ((size_t)it.index * 2 * PF_ROWS + a * PF_ROWS + r) * PARTIAL_FLOATS;
       if (split) {
         part[PARTIAL_M] = mx;
         part[PARTIAL_L] = l;
@@ -568,21 +639,23 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-        if (F32 || split) {
-          uint4* dst = reinterpret_cast<uint4*>((split ? part : static_cast<float*>(A.a.out) + row * D) + c);
-          if (valid || split) {
+        if (split) {   // (rows of 528 bytes: 16-byte aligned)
+          uint4* dst = reinterpret_cast<uint4*>(part + c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else if (valid && F32) {
+          float* dst = static_cast<float*>(A.a.out) + row * D + c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) store32(dst + i, o + i, A.wide);
         } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + row * D + c);
+          uint16_t* dst = static_cast<uint16_t*>(A.a.out) + row * D + c;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]), __uint_as_float(o[8 * i + 2 * k + 1]));
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 8; ++k)
+              w[k] = bf16x2(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1]));
+            store32(dst + i, w, A.wide);
           }
         }
       }
@@ -687,6 +760,7 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   // a part has four key tiles or more
   A.splits = static_cast<int>(longest / 4 < most ? (longest / 4 > 1 ? longest / 4 : 1) : most);
   A.partials = static_cast<float*>(partials);
+  A.wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   if (blocks * p.Hkv * A.splits > INT32_MAX / 2) return cudaErrorInvalidValue;
   A.items = static_cast<int>(blocks * p.Hkv * A.splits);
   constexpr int bytes = static_cast<int>(sizeof(PrefillSmem)) + 1024;
