@@ -74,25 +74,11 @@ struct alignas(1024) DecodeSmem {
   int last;
 };
 
-struct DecodeArgs {
-  PagedView p;
-  AttnArgs a;
-  int n, m, G, ncta;
-  int32_t total;                            // units of the call
-  float* partials;
-  int32_t* counters;
-  // request i; side by side, since each line of the arguments comes from a cold cache
-  struct Req {
-    int32_t len, row, table;
-    int32_t ustart;                         // units before it (all its kv heads)
-  } req[PAGED_MAX_REQ];
-};
-
 // The visible units of a request: [0, sink) and [first, first + units - sink).  An
 // empty list still counts as one unit, so that some CTA writes the zero rows.
 struct Units {
-  int sink, first, units;
-  __host__ __device__ static Units of(int len, int m, int window, int sinks, int ut) {
+  int32_t sink, first, units;
+  static Units of(int len, int m, int window, int sinks, int ut) {
     const int64_t lo64 = (int64_t)len - m - window + 1;
     const int lo = lo64 > 0 ? static_cast<int>(lo64) : 0;
     Units u;
@@ -106,6 +92,21 @@ struct Units {
   __host__ __device__ int unit(int v) const { return v < sink ? v : first + (v - sink); }
 };
 
+struct DecodeArgs {
+  PagedView p;
+  AttnArgs a;
+  int n, m, G, ncta;
+  int32_t total;                            // units of the call
+  float* partials;
+  int32_t* counters;
+  // request i; side by side, since each line of the arguments comes from a cold cache
+  struct Req {
+    int32_t len, row, table;
+    int32_t ustart;                         // units before it (all its kv heads)
+    Units un;
+  } req[PAGED_MAX_REQ];
+};
+
 // Position of a CTA's walk over the units u of the call.
 struct Cursor {
   int req, head, base, seg_end;   // current segment: units [base, seg_end)
@@ -113,7 +114,7 @@ struct Cursor {
 };
 template <int UT>
 __device__ __forceinline__ void cursor_load(const DecodeArgs& A, Cursor& c) {
-  c.un = Units::of(A.req[c.req].len, A.m, A.a.window, A.a.sinks, UT);
+  c.un = A.req[c.req].un;
   c.seg_end = c.base + max(c.un.units, 1);
 }
 template <int UT>
@@ -219,9 +220,13 @@ struct State {
   }
 };
 
-// Whether the row at position pos sees token t.
-__device__ __forceinline__ bool sees(const AttnArgs& a, int pos, int t) {
-  return t <= pos && (t < a.sinks || (int64_t)t > (int64_t)pos - a.window);
+// What the row at position pos sees of the 64 tokens from t0; and what any of m rows from
+// position pos on sees of them (their windows overlap, or there are only sinks).
+__device__ __forceinline__ uint64_t row_sees(const AttnArgs& a, int pos, int t0) {
+  return visible_bits(pos - t0, pos - a.window + 1 - t0, a.sinks - t0);
+}
+__device__ __forceinline__ uint64_t any_sees(const AttnArgs& a, int pos, int m, int t0) {
+  return visible_bits(pos + m - 1 - t0, a.window > 0 ? pos - a.window + 1 - t0 : 64, a.sinks - t0);
 }
 
 // q as the first product's B operand: column n (= lane / 4), registers of k-step s.
@@ -354,9 +359,7 @@ __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR
   if (masked) {
     // value rows that no row of the segment sees may hold anything: zero them
     const int row = lane & 15, p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);   // the first query token
-    bool any = false;
-    for (int k = 0; k < A.m; ++k) any = any || sees(A.a, p0 + k, t0 + row);
-    if (!any) {
+    if (!(any_sees(A.a, p0, A.m, t0) >> row & 1)) {
       uint4* v = reinterpret_cast<uint4*>(stage + (lane >> 4) * 4096 + 2048 + row * 128);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
@@ -384,8 +387,9 @@ __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR
     x0[h] = s[h / C::HPL][h % C::HPL] * Q.scale[h];
     x1[h] = s[h / C::HPL][2 + h % C::HPL] * Q.scale[h];
     if (masked) {
-      if (!sees(A.a, Q.pos[h], t0 + gid)) x0[h] = NEG_INF;
-      if (!sees(A.a, Q.pos[h], t0 + gid + 8)) x1[h] = NEG_INF;
+      const uint32_t see = static_cast<uint32_t>(row_sees(A.a, Q.pos[h], t0)) >> gid;
+      if (!(see & 1)) x0[h] = NEG_INF;
+      if (!(see & 0x100)) x1[h] = NEG_INF;
     }
     S.raise(h, fmaxf(x0[h], x1[h]));
     const float ref = S.m[h] == NEG_INF ? 0.0f : S.m[h];
@@ -435,12 +439,10 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
   if (masked) {
     // the scale and zero of a token that no row sees may be anything: zero them (its codes
     // are finite whatever they are)
-    const int p0 = __shfl_sync(0xffffffffu, Q.pos[0], 0);   // the first query token
+    const uint64_t any = any_sees(A.a, __shfl_sync(0xffffffffu, Q.pos[0], 0), A.m, t0);
 #pragma unroll 1
     for (int slot = lane; slot < PAGE; slot += 32) {
-      bool any = false;
-      for (int k = 0; k < A.m; ++k) any = any || sees(A.a, p0 + k, t0 + slot);
-      if (any) continue;
+      if (any >> slot & 1) continue;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         *reinterpret_cast<uint32_t*>(stage + I4_META + MROW * slot + 4 * g) = 0;
@@ -467,12 +469,10 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
         const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * tid);
         w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
       } else {
-        // half of the rows read the second group first: no bank conflicts
-        const int first = (gid >> 1) & 1;
-        const uint2 va = *reinterpret_cast<const uint2*>(row + 32 * first + 8 * tid);
-        const uint2 vb = *reinterpret_cast<const uint2*>(row + 32 * (first ^ 1) + 8 * tid);
-        w[u][0] = first ? vb.x : va.x, w[u][1] = first ? vb.y : va.y;
-        w[u][2] = first ? va.x : vb.x, w[u][3] = first ? va.y : vb.y;
+        // (two-way bank conflicts; putting them right took two selects a word)
+        const uint2 va = *reinterpret_cast<const uint2*>(row + 8 * tid);
+        const uint2 vb = *reinterpret_cast<const uint2*>(row + 32 + 8 * tid);
+        w[u][0] = va.x, w[u][1] = va.y, w[u][2] = vb.x, w[u][3] = vb.y;
       }
     }
 #pragma unroll
@@ -513,12 +513,15 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
   }
   if (masked) {
 #pragma unroll
-    for (int h = 0; h < C::H; ++h)
+    for (int h = 0; h < C::H; ++h) {
+      const uint64_t see = row_sees(A.a, Q.pos[h], t0) >> tok;
+      const uint32_t part[2] = {static_cast<uint32_t>(see), static_cast<uint32_t>(see >> 32)};
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          if (!sees(A.a, Q.pos[h], t0 + 16 * t + 8 * u + tok)) x[t][u][h] = NEG_INF;
+          if (!(part[t / 2] >> (16 * (t % 2) + 8 * u) & 1)) x[t][u][h] = NEG_INF;
+    }
   }
 #pragma unroll
   for (int h = 0; h < C::H; ++h) {
@@ -591,11 +594,8 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
         const uint2 w = *reinterpret_cast<const uint2*>(row + 8 * gid);
         v[q][0] = w.x, v[q][1] = w.y;
       } else {
-        const int first = tid >> 1;   // half of the lanes read the second word first: no bank conflicts
-        const uint32_t va = *reinterpret_cast<const uint32_t*>(row + 32 * first + 4 * gid);
-        const uint32_t vb = *reinterpret_cast<const uint32_t*>(row + 32 * (first ^ 1) + 4 * gid);
-        v[q][0] = first ? vb : va;
-        v[q][1] = first ? va : vb;
+        v[q][0] = *reinterpret_cast<const uint32_t*>(row + 4 * gid);
+        v[q][1] = *reinterpret_cast<const uint32_t*>(row + 32 + 4 * gid);
       }
     }
 #pragma unroll
@@ -688,28 +688,42 @@ __device__ __forceinline__ void write_row(const DecodeArgs& A, int req, int head
   if (A.a.lse && lane == 0) A.a.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : NEG_INF;
 }
 
-// Fold count states of one row, the warp's lanes holding 4 channels each.  The code runs
-// once in a launch, from a cold instruction cache: short, and no wider than it pays.
+// Fold count states of one row, the warp's lanes holding 4 channels each: weights by 32
+// lanes at once, then eight rows in flight.  The code runs once in a launch, from a cold
+// instruction cache, so it is short.
 template <typename P>
 __device__ __forceinline__ void fold(int count, P at, int lane, float4& o, float& m, float& l) {
   m = NEG_INF;
-#pragma unroll 1
-  for (int c = lane; c < count; c += 32) m = fmaxf(m, __ldcg(at(c) + PARTIAL_M));
-#pragma unroll
-  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   l = 0.0f;
-  const float ref = m == NEG_INF ? 0.0f : m;
-#pragma unroll 4
-  for (int c = 0; c < count; ++c) {
-    const float* p = at(c);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + lane);
-    const float f = ex2f(__ldcg(p + PARTIAL_M) - ref);
-    l = fmaf(__ldcg(p + PARTIAL_L), f, l);
-    o.x = fmaf(v.x, f, o.x);
-    o.y = fmaf(v.y, f, o.y);
-    o.z = fmaf(v.z, f, o.z);
-    o.w = fmaf(v.w, f, o.w);
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+  for (int base = 0; base < count; base += 32) {
+    const float* mine = at(min(base + lane, count - 1));
+    const float mc = base + lane < count ? __ldcg(mine + PARTIAL_M) : NEG_INF, lc = __ldcg(mine + PARTIAL_L);
+    float top = fmaxf(mc, m);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float ref = top == NEG_INF ? 0.0f : top, f0 = ex2f(m - ref), f = ex2f(mc - ref);
+    float sum = lc * f;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    l = fmaf(l, f0, sum);
+    m = top;
+    o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll 1
+    for (int c = 0; c < 32 && base + c < count; c += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = __ldcg(reinterpret_cast<const float4*>(at(min(base + c + u, count - 1))) + lane);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = __shfl_sync(0xffffffffu, f, c + u);   // 0 behind the last
+        o.x = fmaf(v[u].x, w, o.x);
+        o.y = fmaf(v[u].y, w, o.y);
+        o.z = fmaf(v[u].z, w, o.z);
+        o.w = fmaf(v[u].w, w, o.w);
+      }
+    }
   }
 }
 
@@ -959,8 +973,8 @@ cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, 
   const int ut = gk == 0 ? Format<0>::UT : PAGE;
   int64_t total = 0;
   for (int i = 0; i < n; ++i) {
-    A.req[i] = {reqs[i].len, reqs[i].row, reqs[i].table, static_cast<int32_t>(total)};
     const Units u = Units::of(reqs[i].len, A.m, a.window, a.sinks, ut);
+    A.req[i] = {reqs[i].len, reqs[i].row, reqs[i].table, static_cast<int32_t>(total), u};
     total += (int64_t)p.Hkv * (u.units > 0 ? u.units : 1);
     if (total > INT32_MAX) return cudaErrorInvalidValue;
   }
