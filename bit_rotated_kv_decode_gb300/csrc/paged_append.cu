@@ -226,8 +226,8 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
   }
 }
 
-// One warp takes 16 head rows (query, key and value heads in this order) of one
-// token: four groups of 8 lanes, a lane holding both chunks of its channel pairs,
+// One warp takes 16 head rows (query, key and value heads in this order; in 4 bits key
+// and value rows or query rows) of one token: four groups of 8 lanes, a lane holding both chunks of its channel pairs,
 // so that the rotation needs no exchange and the cosines and sines are loaded
 // once for all rows.  The kernel moves each byte once, and its traffic bounds it: in BF16
 // all loads of a lane (8 x 16 B) are in flight together.
@@ -236,13 +236,18 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
                                                                    const __grid_constant__ PagedRows rows,
                                                                    const __grid_constant__ RopeArgs rope,
                                                                    const __grid_constant__ AppendRows in,
-                                                                   uint32_t tasks_per_token, uint32_t tasks) {
+                                                                   uint32_t kv_per_token, uint32_t per_token,
+                                                                   uint32_t tasks) {
   const uint32_t task = (blockIdx.x * APP_THREADS + threadIdx.x) >> 5;
   if (task >= tasks) return;
   const int lane = threadIdx.x & 31, pc = lane & 7, sub = lane >> 3;
-  const int row = static_cast<int>(task / tasks_per_token);
-  const int head0 = static_cast<int>(task % tasks_per_token) * APP_HEADS + sub;
-  const int hq = in.q ? in.Hq : 0, total = hq + 2 * p.Hkv;
+  const int hq = in.q ? in.Hq : 0;
+  // a token's tasks: kv_per_token of key and value rows alone (4 bits), then those of query
+  // rows (in BF16 with key and value rows behind them)
+  const int row = static_cast<int>(task / per_token), of_token = static_cast<int>(task % per_token);
+  const bool kv_only = GK != 0 && of_token < static_cast<int>(kv_per_token);
+  const int head0 = (kv_only ? hq + of_token * APP_HEADS : (of_token - static_cast<int>(kv_per_token)) * APP_HEADS) + sub;
+  const int total = GK == 0 || kv_only ? hq + 2 * p.Hkv : hq;
 
   // the lane's two chunks, and whether they hold rotated pairs
   const int half_chunks = rope.dim / 16;   // pairs of chunks that are rotated
@@ -263,10 +268,12 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
     x[0][0] = a.x, x[0][1] = a.y, x[0][2] = a.z, x[0][3] = a.w;
     x[1][0] = b.x, x[1][1] = b.y, x[1][2] = b.z, x[1][3] = b.w;
   };
-  constexpr int AHEAD = GK == 0 ? APP_ROWS : 1;   // rows loaded before the first is worked on
-  uint32_t first[AHEAD][2][4];
+  uint32_t x[APP_ROWS][2][4];
+  load_row(0, x[0]);
+  if (!kv_only) {
 #pragma unroll
-  for (int r = 0; r < AHEAD; ++r) load_row(r, first[r]);
+    for (int r = 1; r < APP_ROWS; ++r) load_row(r, x[r]);
+  }
   const int i = find_req(rows, p.n, row);
   const int pos = rows.pos0[i] + (row - rows.row0[i]);
   // pair e of the lane: element e of both chunks, or elements 2e, 2e + 1 of the 16
@@ -279,11 +286,10 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
       *reinterpret_cast<float4*>(sn + e) = __ldg(reinterpret_cast<const float4*>(t + rope.dim / 2 + e));
     }
   }
-  const bool writes_kv = head0 + 4 * (APP_ROWS - 1) >= hq;
+  const bool writes_kv = total > hq && head0 + 4 * (APP_ROWS - 1) >= hq;
   const int64_t page = writes_kv ? page_of(p, i, pos) : -1;
   const int slot = pos % PAGE;
-  auto do_row = [&](int r, uint32_t (&x)[2][4]) {
-    const int h = head0 + 4 * r;
+  auto rotate_row = [&](int h, uint32_t (&x)[2][4]) {
     if (rot && h < hq + p.Hkv) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -293,59 +299,53 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
           for (int u = 0; u < 2; ++u) {
             const float a = bf_lo(x[u][k]), b = bf_hi(x[u][k]), co = cs[4 * u + k], si = sn[4 * u + k];
             x[u][k] = pack_bf(__fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si)),
-                                 __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si)));
+                              __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si)));
           }
         } else {
           const float a0 = bf_lo(x[0][k]), a1 = bf_hi(x[0][k]), b0 = bf_lo(x[1][k]), b1 = bf_hi(x[1][k]);
           x[0][k] = pack_bf(__fsub_rn(__fmul_rn(a0, cs[2 * k]), __fmul_rn(b0, sn[2 * k])),
-                               __fsub_rn(__fmul_rn(a1, cs[2 * k + 1]), __fmul_rn(b1, sn[2 * k + 1])));
+                            __fsub_rn(__fmul_rn(a1, cs[2 * k + 1]), __fmul_rn(b1, sn[2 * k + 1])));
           x[1][k] = pack_bf(__fadd_rn(__fmul_rn(b0, cs[2 * k]), __fmul_rn(a0, sn[2 * k])),
-                               __fadd_rn(__fmul_rn(b1, cs[2 * k + 1]), __fmul_rn(a1, sn[2 * k + 1])));
+                            __fadd_rn(__fmul_rn(b1, cs[2 * k + 1]), __fmul_rn(a1, sn[2 * k + 1])));
         }
       }
     }
-    const bool is_q = h < hq;
-    const int which = h >= hq + p.Hkv, kvh = h - hq - (which ? p.Hkv : 0);
-    const uint4 a = make_uint4(x[0][0], x[0][1], x[0][2], x[0][3]);
-    const uint4 b = make_uint4(x[1][0], x[1][1], x[1][2], x[1][3]);
-    if (is_q) {
-      uint16_t* dst = in.q_out + ((size_t)row * in.Hq + h) * D;
-      *reinterpret_cast<uint4*>(dst + 8 * c[0]) = a;
-      *reinterpret_cast<uint4*>(dst + 8 * c[1]) = b;
-    }
-    const bool ok = !is_q && h < total && page >= 0;
-    if constexpr (GK == 0) {
-      if (ok) {
-        uint16_t* dst = static_cast<uint16_t*>(p.pool) + ((size_t)page * p.Hkv + kvh) * BF16_RECORD_ELEMS +
-                        (size_t)which * PAGE * D + (size_t)slot * D;
-        *reinterpret_cast<uint4*>(dst + 8 * c[0]) = a;
-        *reinterpret_cast<uint4*>(dst + 8 * c[1]) = b;
-      }
-    } else {
-      // the whole warp takes part in the reductions' shuffles
-      uint8_t* rec = static_cast<uint8_t*>(p.pool) + (ok ? ((size_t)page * p.Hkv + kvh) * i4_record(GK) : 0);
-      if (__any_sync(0xffffffffu, ok)) store_int4<GK>(rec, which, slot, c, x, ok);
-    }
   };
-  if constexpr (GK == 0) {
+  if (!kv_only) {
 #pragma unroll
-    for (int r = 0; r < APP_ROWS; ++r) do_row(r, first[r]);
-  } else {
+    for (int r = 0; r < APP_ROWS; ++r) {
+      const int h = head0 + 4 * r;
+      rotate_row(h, x[r]);
+      uint16_t* dst = nullptr;
+      if (h < hq) {
+        dst = in.q_out + ((size_t)row * in.Hq + h) * D;
+      } else if (GK == 0 && h < total && page >= 0) {
+        const int which = h >= hq + p.Hkv, kvh = h - hq - (which ? p.Hkv : 0);
+        dst = static_cast<uint16_t*>(p.pool) + ((size_t)page * p.Hkv + kvh) * BF16_RECORD_ELEMS +
+              (size_t)which * PAGE * D + (size_t)slot * D;
+      }
+      if (dst) {
+        *reinterpret_cast<uint4*>(dst + 8 * c[0]) = make_uint4(x[r][0][0], x[r][0][1], x[r][0][2], x[r][0][3]);
+        *reinterpret_cast<uint4*>(dst + 8 * c[1]) = make_uint4(x[r][1][0], x[r][1][1], x[r][1][2], x[r][1][3]);
+      }
+    }
+  } else if constexpr (GK != 0) {
     // one copy of the quantiser's code (four do not fit the instruction cache: 102 us for
-    // 16K tokens); the next row is loaded under it
+    // 16K tokens, 95 rolled up); the next row is loaded under it
 #pragma unroll 1
     for (int r = 0; r < APP_ROWS; ++r) {
-      uint32_t x[2][4], next[2][4];
+      const int h = head0 + 4 * r, which = h >= hq + p.Hkv, kvh = h - hq - (which ? p.Hkv : 0);
+      uint32_t y[2][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[u][k] = first[0][u][k];
-      if (r + 1 < APP_ROWS) load_row(r + 1, next);
-      do_row(r, x);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) first[0][u][k] = next[u][k];
+        for (int k = 0; k < 4; ++k) y[u][k] = x[0][u][k];
+      if (r + 1 < APP_ROWS) load_row(r + 1, x[0]);
+      rotate_row(h, y);
+      // the whole warp takes part in the reductions' shuffles
+      const bool ok = h < total && page >= 0;
+      uint8_t* rec = static_cast<uint8_t*>(p.pool) + (ok ? ((size_t)page * p.Hkv + kvh) * i4_record(GK) : 0);
+      if (__any_sync(0xffffffffu, ok)) store_int4<GK>(rec, which, slot, c, y, ok);
     }
   }
 }
@@ -396,13 +396,15 @@ __global__ void __launch_bounds__(READ_THREADS) int4_read_kernel(const __grid_co
 
 cudaError_t launch_paged_append(const PagedView& p, const PagedRows& rows, const RopeArgs& rope, const AppendRows& in,
                                 int gk, cudaStream_t s) {
-  const int heads = (in.q ? in.Hq : 0) + 2 * p.Hkv;
-  const int per_token = (heads + APP_HEADS - 1) / APP_HEADS;
-  const int64_t tasks = (int64_t)rows.row0[p.n] * per_token;
+  const int hq = in.q ? in.Hq : 0, tokens = rows.row0[p.n];
+  auto tasks_for = [](int heads) { return (heads + APP_HEADS - 1) / APP_HEADS; };
+  const uint32_t kv_per = gk == 0 ? 0 : tasks_for(2 * p.Hkv), per = kv_per + tasks_for(gk == 0 ? hq + 2 * p.Hkv : hq);
+  const int64_t tasks = (int64_t)tokens * per;
   if (tasks * 32 > UINT32_MAX - APP_THREADS) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>((tasks * 32 + APP_THREADS - 1) / APP_THREADS);
-  const uint32_t n = static_cast<uint32_t>(tasks), per = static_cast<uint32_t>(per_token);
-  auto go = [&](auto kernel) { kernel<<<grid, APP_THREADS, 0, s>>>(p, rows, rope, in, per, n); };
+  auto go = [&](auto kernel) {
+    kernel<<<grid, APP_THREADS, 0, s>>>(p, rows, rope, in, kv_per, per, static_cast<uint32_t>(tasks));
+  };
   if (gk == 0)
     rope.interleaved ? go(paged_append_kernel<0, true>) : go(paged_append_kernel<0, false>);
   else if (gk == 128)

@@ -34,6 +34,8 @@
 //      sum p v = sum (p s) (c - 8) + sum p (z + 8 s).
 // The probabilities come out of the first product with a lane holding two tokens
 // of a row; movmatrix turns them into the second product's operand.
+#include <atomic>
+
 #include "paged_device.cuh"
 
 namespace oscar {
@@ -923,14 +925,14 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
 template <int GK, int NR>
 cudaError_t launch_decode_t(DecodeArgs& A, const CUtensorMap& map, int sms, cudaStream_t s) {
   constexpr int bytes = static_cast<int>(sizeof(DecodeSmem<GK, NR>)) + 1024;
-  static unsigned done = 0;   // devices whose attribute is set
+  static std::atomic<unsigned> done{0};   // devices whose attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 32 || !(done & (1u << dev))) {
+  if (dev >= 32 || !(done.load() & (1u << dev))) {
     e = cudaFuncSetAttribute(paged_decode_kernel<GK, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (dev < 32) done |= 1u << dev;
+    if (dev < 32) done.fetch_or(1u << dev);
   }
   // One CTA per SM; where a CTA's warps would have no unit each, fewer; and one per
   // segment where that leaves its warps at most three units, since folding a segment's

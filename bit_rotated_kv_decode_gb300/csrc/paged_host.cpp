@@ -158,8 +158,8 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
   int64_t rows = 0;
   for (int32_t i = 0; i < n; ++i) {
     const int32_t m = q_lens ? q_lens[i] : 1;
-    if (m < 0 || lens[i] < m || (int64_t)lens[i] > (int64_t)PAGE * max_pages)
-      return bad("0 <= q_lens <= lens <= 64 max_pages");
+    if (m < 0 || lens[i] < m || (int64_t)lens[i] > (int64_t)PAGE * max_pages || lens[i] > (1 << 30))
+      return bad("0 <= q_lens <= lens <= 64 max_pages, and lens at most 2^30");
     if (gk != 0 && m > step) return bad("4-bit attention: at most 16 / (query heads per kv head) query tokens a request");
     rows += m;
     if (rows > INT32_MAX / 64) return bad("too many query rows");

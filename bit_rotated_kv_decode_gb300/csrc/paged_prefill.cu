@@ -32,6 +32,8 @@
 // the first products of an item run under the end of the one before.  Where the items
 // would leave most SMs idle (a few query tokens on a long cache) an item's key tiles are
 // split, its unnormalised rows go to the workspace and a second kernel folds them.
+#include <atomic>
+
 #include "paged_device.cuh"
 
 namespace oscar {
@@ -765,18 +767,18 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   A.items = static_cast<int>(blocks * p.Hkv * A.splits);
   constexpr int bytes = static_cast<int>(sizeof(PrefillSmem)) + 1024;
   auto kernel = a.f32 ? paged_prefill_kernel<true> : paged_prefill_kernel<false>;
-  static unsigned done[2] = {0, 0};   // devices whose attribute is set
+  static std::atomic<unsigned> done[2];   // devices that have been set up
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 32 || !(done[a.f32 != 0] & (1u << dev))) {
+  if (dev >= 32 || !(done[a.f32 != 0].load() & (1u << dev))) {
     cudaFuncAttributes attr;   // the build has the registers that the split counts on
     e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
     if (attr.numRegs != PF_REGS) return cudaErrorInvalidKernelImage;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (dev < 32) done[a.f32 != 0] |= 1u << dev;
+    if (dev < 32) done[a.f32 != 0].fetch_or(1u << dev);
   }
   kernel<<<A.items < sms ? A.items : sms, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
   e = cudaGetLastError();

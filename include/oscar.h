@@ -328,7 +328,7 @@ oscar_status oscar_bf16_decode(const void* kv, int64_t num_pages, const int32_t*
  * Common arguments and rules:
  *   page_table  device int32 [n][max_pages]; entries of pages that a call does
  *               not touch are never read into an address.  Its row i belongs to
- *               request i; 1 <= n <= 256.
+ *               request i; 1 <= n <= 256, num_pages Hkv < 2^30.
  *   lens, new_lens, q_lens, starts, counts  host int32 [n]; NULL new_lens or
  *               q_lens: one token per request.  Rows of q, k, v and out are the
  *               requests' tokens one after another (no padding); a request may
@@ -389,8 +389,8 @@ oscar_status oscar_int4_read(const void* kv, int64_t num_pages, const int32_t* p
                              void* stream);
 
 /* Attention with a sliding window and sinks.  The queries of request i are its last
- * q_lens[i] positions (0 <= q_lens[i] <= lens[i] <= 64 max_pages; lens counts the
- * tokens in the cache, the queries' own among them).  The query at position p sees
+ * q_lens[i] positions (0 <= q_lens[i] <= lens[i] <= 64 max_pages and 2^30; lens counts
+ * the tokens in the cache, the queries' own among them).  The query at position p sees
  * the tokens t <= p with t < sinks or t > p - window:
  *   out = sum_t softmax_t(scale q . k_t) v_t,  lse = log sum_t exp(scale q . k_t),
  * query head h against kv head h / (Hq / Hkv).
@@ -398,14 +398,17 @@ oscar_status oscar_int4_read(const void* kv, int64_t num_pages, const int32_t* p
  *           sees nothing (window 0, no sinks), out is 0 and lse -infinity.
  *   scale   <= 0 selects 1 / sqrt(128).
  *   q       device bf16 [rows][Hq][128]; out dense [rows][Hq][128] of out_type; lse
- *           device fp32 [rows][Hq] or NULL.
+ *           device fp32 [rows][Hq] or NULL.  Neither may overlap q.
  *   workspace  device, >= oscar_attention_workspace_bytes() (whatever lens, window
  *           and sinks), 256-byte aligned, zeroed once by the caller before its first
  *           use; every call leaves it ready for the next, of any shape.  Calls that
  *           share a workspace must not overlap on the GPU.
  * Hq / Hkv in {1, 2, 4, 8}; n Hkv <= 16384.  Pages that no query sees are not
  * touched.  Tokens that no query of a request sees may hold anything (NaN too);
- * those that some see and others do not must hold finite values.  4 bits: at most
+ * those that some see and others do not must hold finite values.  Sums and softmax
+ * statistics are fp32; weights enter the product with V to 24 bits (16 where a request
+ * has more than 8 rows a kv head, 8 where it has more than 16 and out is bf16; 22 in 4
+ * bits).  4 bits: at most
  * 16 / (Hq / Hkv) query tokens a request; read a prefix back for more. */
 size_t oscar_attention_workspace_bytes(int32_t n, const int32_t* q_lens, int32_t num_q_heads, int32_t num_kv_heads);
 oscar_status oscar_window_attention(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,

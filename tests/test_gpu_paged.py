@@ -411,6 +411,80 @@ def test_prefill_then_decode_steps(b, group):
         lens = now
 
 
+# ---- far addresses, shared pages, replays ------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 128])
+def test_pages_beyond_4_gib(b, group):
+    """Pages at the end of a pool of more than 2^32 bytes, for every operator."""
+    hq, hkv, t = 4, 2, 150
+    per = hkv * (2 * PAGE * D * 2 if group == 0 else 8704)
+    pages = (1 << 32) // per + 40
+    kv = (torch.empty(pages, hkv, 2, PAGE, D, dtype=torch.bfloat16, device="cuda") if group == 0
+          else torch.empty(pages, hkv, 8704, dtype=torch.uint8, device="cuda"))
+    table = torch.tensor([[pages - 1, pages - 7, pages - 3]], dtype=torch.int32, device="cuda")
+    g = np.random.default_rng(2)
+    bits = paged.bf16_bits(g.standard_normal((t, hq + 2 * hkv, D)).astype(np.float32))
+    q, k, v = bf16(bits).split([hq, hkv, hkv], 1)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    held = Pool.__new__(Pool)
+    held.lens, held.hkv, held.group = [t], hkv, group
+    if group == 0:
+        b.bf16_append(kv, table, [0], k, v, new_lens=[t], error=err)
+        held.k, held.v = ([paged.bf16_values(x).astype(np.float64)] for x in (bits[:, hq:hq + hkv], bits[:, hq + hkv:]))
+        held.kmag, held.vmag = [np.abs(held.k[0])], [np.abs(held.v[0])]
+        q_lens = [40]
+        call = b.window_attention
+    else:
+        b.int4_append(kv, table, [0], k, v, new_lens=[t], error=err)
+        both = [paged.quantise4(x, group) for x in (bits[:, hq:hq + hkv], bits[:, hq + hkv:])]
+        held.k, held.v = ([paged.dequantise4(*x)] for x in both)
+        held.kmag, held.vmag = ([np.abs(y[0]) + 2 * np.repeat(np.abs(x[1][..., 1].astype(np.float64)), group, -1)]
+                                for x, y in zip(both, (held.k, held.v)))
+        ko, vo = torch.empty(t, hkv, D, device="cuda"), torch.empty(t, hkv, D, device="cuda")
+        b.int4_read(kv, table, [0], [t], ko, vo, error=err)
+        assert np.array_equal(ko.cpu().numpy(), held.k[0].astype(np.float32))
+        assert np.array_equal(vo.cpu().numpy(), held.v[0].astype(np.float32))
+        q_lens = [4]
+        call = b.int4_attention
+    for m in ([1], q_lens):
+        qq = bits[t - m[0]:, :hq]
+        out, lse = torch.empty(m[0], hq, D, device="cuda"), torch.empty(m[0], hq, device="cuda")
+        call(kv, table, [t], bf16(qq), out, hkv, 100, 3, q_lens=m, lse=lse, error=err)
+        check_attention(held, qq, m, 100, 3, out, lse)
+    assert err.item() == 0
+
+
+@pytest.mark.gpu
+def test_graphs_that_share_a_workspace_and_new_lengths(b):
+    """Two graphs of different batches on one workspace, replayed in turn, with new contents of the same tensors; a
+    split prefill and a decode among them; requests that share their prefix's pages."""
+    hq, hkv = 8, 2
+    pool = Pool(b, [700, 700, 130], hkv, seed=9)
+    pool.table[1, :8] = pool.table[0, :8]                       # a shared prefix of 512 tokens
+    pool.k[1][:512], pool.v[1][:512] = pool.k[0][:512], pool.v[0][:512]
+    pool.kmag[1][:512], pool.vmag[1][:512] = pool.kmag[0][:512], pool.vmag[0][:512]
+    kv, table = pool.device()
+    ws = b.attention_workspace(3, hq, hkv, [1, 40, 1])
+    stream = torch.cuda.Stream()
+    sets = []
+    for q_lens in ([1, 1, 1], [1, 40, 0]):
+        rows = sum(q_lens)
+        q = torch.zeros(rows, hq, D, dtype=torch.bfloat16, device="cuda")
+        out, lse = torch.empty(rows, hq, D, device="cuda"), torch.empty(rows, hq, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            b.window_attention(kv, table, pool.lens, q, out, hkv, 300, 4, q_lens=q_lens, lse=lse, workspace=ws)
+        sets.append((q_lens, q, out, lse, graph))
+    for turn in range(3):
+        for q_lens, q, out, lse, graph in sets:
+            bits = paged.bf16_bits(np.random.default_rng(turn).standard_normal(tuple(q.shape)).astype(np.float32))
+            q.copy_(bf16(bits))
+            graph.replay()
+            torch.cuda.synchronize()
+            check_attention(pool, bits, q_lens, 300, 4, out, lse)
+
+
 # ---- the two ways through the binding -----------------------------------------------
 @pytest.mark.gpu
 @pytest.mark.parametrize("group", [0, 128])
