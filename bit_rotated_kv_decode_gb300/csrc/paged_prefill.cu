@@ -62,7 +62,6 @@ struct PrefillArgs {
   int n, G, lg;                           // lg = log2 G
   int splits, items;                      // parts of an item's key tiles; items in all, parts counted
   float* partials;                        // [items][256][PARTIAL_FLOATS] where splits > 1
-  int wide;                               // out is 32-byte aligned
   int32_t len[PAGED_MAX_REQ];
   int32_t m[PAGED_MAX_REQ];
   int32_t row[PAGED_MAX_REQ];
@@ -137,6 +136,7 @@ struct alignas(16) Item {
 struct alignas(1024) PrefillSmem {
   alignas(1024) uint8_t q[2][TILE_BYTES];      // per tile: two halves of 64 channels, [128 rows][128 B] swizzled
   alignas(1024) uint8_t kv[PF_STAGES][2][TILE_BYTES];   // V of key tile j - 1, K of key tile j
+  alignas(16) uint8_t out[8][32 * 128];                 // per softmax warp: 128 bytes of its 32 rows
   uint64_t q_full[2], q_empty[2], kv_full[PF_STAGES], kv_empty[PF_STAGES];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];   // per query tile (and half of the keys)
   uint64_t turn[2];                              // the other tile's products of a key tile are issued
@@ -194,18 +194,6 @@ __device__ __forceinline__ uint64_t desc_nmajor(uint32_t addr) {
 constexpr uint32_t IDESC_QK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t IDESC_PV = IDESC_QK | (1u << 16);
 
-// 32 bytes of a row, one sector in one store where the address allows (a thread writes a
-// row of its own, so a warp's store touches 32 lines whatever its width).
-__device__ __forceinline__ void store32(void* dst, const uint32_t* w, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
 // Issued by one elected lane of a converged warp: the code around stays uniform, so that
 // descriptors are computed in uniform registers (under an if of one lane, each product
 // cost its six operand moves, and a key tile of the issuing warp 4700 cycles).
@@ -262,7 +250,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, b
   return ok && __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
-template <bool F32>
+template <bool F32, bool SPLIT>
 __global__ void __launch_bounds__(PF_THREADS, 1)
     paged_prefill_kernel(const __grid_constant__ PrefillArgs A, const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap kv_map) {
@@ -611,55 +599,72 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
       }
-      const bool some = j1 > j0, valid = tok < it.tokens;
-      const size_t row = (size_t)(it.row + tok) * A.a.Hq + (size_t)it.head * A.G + (r & (A.G - 1));
-      float* part = A.partials + ((size_t)it.index * 2 * PF_ROWS + a * PF_ROWS + r) * PARTIAL_FLOATS;
+      const bool some = j1 > j0;
+      const int tokens = it.tokens;
+      const size_t row0 = (size_t)it.row * A.a.Hq + (size_t)it.head * A.G;   // of token 0, head 0 of the group
+      float* part = A.partials + ((size_t)it.index * 2 * PF_ROWS + a * PF_ROWS) * PARTIAL_FLOATS;
       release();
       if (some) ok = mbar_wait_warp(&sm.o_full[a], done & 1, ok);
       if (!ok) break;
       tc_fence_after();
-      const bool split = A.splits > 1;
-      const float inv = split ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-      if (split) {
-        part[PARTIAL_M] = mx;
-        part[PARTIAL_L] = l;
-      } else if (valid && A.a.lse) {
-        A.a.lse[row] = l != 0.0f ? (mx + log2f(l)) * 0.6931471805599453f : NEG_INF;
+      const float inv = SPLIT ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      if constexpr (SPLIT) {
+        part[r * PARTIAL_FLOATS + PARTIAL_M] = mx;
+        part[r * PARTIAL_FLOATS + PARTIAL_L] = l;
+      } else if (tok < tokens && A.a.lse) {
+        A.a.lse[row0 + (size_t)(r >> A.lg) * A.a.Hq + (size_t)a * per_tile * A.a.Hq + (r & (A.G - 1))] =
+            l != 0.0f ? (mx + log2f(l)) * 0.6931471805599453f : NEG_INF;
       }
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t o[32];
-        __syncwarp();
+      // O's rows, 128 bytes at a time, turned through shared memory so that eight lanes
+      // store a row's piece together: a store of one row per lane touches 32 lines, and
+      // those of a tile held up the load-store unit for 5500 cycles
+      constexpr bool WIDE = F32 || SPLIT;   // fp32 rows: four pieces of 32 channels, else two of 64
+      constexpr int PIECE = WIDE ? 32 : 64;
+      uint8_t* stage = sm.out[warp];
+#pragma unroll 1
+      for (int c = 0; c < 128; c += PIECE) {
+        uint32_t w[32];
         if (some) {
+          uint32_t o[PIECE];
           tmem_ld32(to + c, o);
+          if constexpr (!WIDE) tmem_ld32(to + c + 32, o + 32);
           tc_wait_ld();
-          if (c == 96) {   // O is read: the next item may write it
+          if (c + PIECE == 128) {   // O is read: the next item may write it
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_empty[a]);
           }
-        }
+          if constexpr (WIDE) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-        if (split) {   // (rows of 528 bytes: 16-byte aligned)
-          uint4* dst = reinterpret_cast<uint4*>(part + c);
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else if (valid && F32) {
-          float* dst = static_cast<float*>(A.a.out) + row * D + c;
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) store32(dst + i, o + i, A.wide);
-        } else if (valid) {
-          uint16_t* dst = static_cast<uint16_t*>(A.a.out) + row * D + c;
-#pragma unroll
-          for (int i = 0; i < 32; i += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              w[k] = bf16x2(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1]));
-            store32(dst + i, w, A.wide);
+            for (int i = 0; i < 32; ++i)
+              w[i] = bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
           }
         }
+        if (!some || l == 0.0f) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rw = 4 * k + lane / 8, rr = 32 * (warp & 3) + rw, tk = a * per_tile + (rr >> A.lg);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
+          const size_t to_row = row0 + (size_t)tk * A.a.Hq + (rr & (A.G - 1));
+          if constexpr (SPLIT)
+            reinterpret_cast<uint4*>(part + rr * PARTIAL_FLOATS + c)[lane & 7] = v;
+          else if (tk < tokens && F32)
+            reinterpret_cast<uint4*>(static_cast<float*>(A.a.out) + to_row * D + c)[lane & 7] = v;
+          else if (tk < tokens)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + to_row * D + c)[lane & 7] = v;
+        }
+        __syncwarp();
       }
       done += some;
     }
@@ -762,23 +767,26 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   // a part has four key tiles or more
   A.splits = static_cast<int>(longest / 4 < most ? (longest / 4 > 1 ? longest / 4 : 1) : most);
   A.partials = static_cast<float*>(partials);
-  A.wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   if (blocks * p.Hkv * A.splits > INT32_MAX / 2) return cudaErrorInvalidValue;
   A.items = static_cast<int>(blocks * p.Hkv * A.splits);
   constexpr int bytes = static_cast<int>(sizeof(PrefillSmem)) + 1024;
-  auto kernel = a.f32 ? paged_prefill_kernel<true> : paged_prefill_kernel<false>;
-  static std::atomic<unsigned> done[2];   // devices that have been set up
+  const int which = (a.f32 ? 1 : 0) + (A.splits > 1 ? 2 : 0);
+  auto kernel = which == 0   ? paged_prefill_kernel<false, false>
+                : which == 1 ? paged_prefill_kernel<true, false>
+                : which == 2 ? paged_prefill_kernel<false, true>
+                             : paged_prefill_kernel<true, true>;
+  static std::atomic<unsigned> done[4];   // devices that have been set up
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 32 || !(done[a.f32 != 0].load() & (1u << dev))) {
+  if (dev >= 32 || !(done[which].load() & (1u << dev))) {
     cudaFuncAttributes attr;   // the build has the registers that the split counts on
     e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
     if (attr.numRegs != PF_REGS) return cudaErrorInvalidKernelImage;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    if (dev < 32) done[a.f32 != 0].fetch_or(1u << dev);
+    if (dev < 32) done[which].fetch_or(1u << dev);
   }
   kernel<<<A.items < sms ? A.items : sms, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
   e = cudaGetLastError();
