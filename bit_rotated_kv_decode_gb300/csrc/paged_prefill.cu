@@ -612,14 +612,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         part[r * PARTIAL_FLOATS + PARTIAL_M] = mx;
         part[r * PARTIAL_FLOATS + PARTIAL_L] = l;
       } else if (tok < tokens && A.a.lse) {
-        A.a.lse[row0 + (size_t)(r >> A.lg) * A.a.Hq + (size_t)a * per_tile * A.a.Hq + (r & (A.G - 1))] =
+        A.a.lse[row0 + (size_t)tok * A.a.Hq + (r & (A.G - 1))] =
             l != 0.0f ? (mx + log2f(l)) * 0.6931471805599453f : NEG_INF;
       }
       // O's rows, 128 bytes at a time, turned through shared memory so that eight lanes
       // store a row's piece together: a store of one row per lane touches 32 lines, and
       // those of a tile held up the load-store unit for 5500 cycles
       constexpr bool WIDE = F32 || SPLIT;   // fp32 rows: four pieces of 32 channels, else two of 64
-      constexpr int PIECE = WIDE ? 32 : 64;
+      constexpr int PIECE = WIDE ? 32 : 64, SIZE = WIDE ? 4 : 2;
+      char* out = SPLIT ? reinterpret_cast<char*>(part)
+                        : static_cast<char*>(A.a.out) + (row0 + (size_t)a * per_tile * A.a.Hq) * (D * SIZE);
+      const int left = tokens - a * per_tile;   // the tile's tokens
       uint8_t* stage = sm.out[warp];
 #pragma unroll 1
       for (int c = 0; c < 128; c += PIECE) {
@@ -652,17 +655,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
               make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         __syncwarp();
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < 8; ++k) {
-          const int rw = 4 * k + lane / 8, rr = 32 * (warp & 3) + rw, tk = a * per_tile + (rr >> A.lg);
+          const int rw = 4 * k + lane / 8, rr = 32 * (warp & 3) + rw, tk = rr >> A.lg;
           const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
-          const size_t to_row = row0 + (size_t)tk * A.a.Hq + (rr & (A.G - 1));
-          if constexpr (SPLIT)
-            reinterpret_cast<uint4*>(part + rr * PARTIAL_FLOATS + c)[lane & 7] = v;
-          else if (tk < tokens && F32)
-            reinterpret_cast<uint4*>(static_cast<float*>(A.a.out) + to_row * D + c)[lane & 7] = v;
-          else if (tk < tokens)
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.a.out) + to_row * D + c)[lane & 7] = v;
+          const int at_row = SPLIT ? rr * PARTIAL_FLOATS * SIZE : (tk * A.a.Hq + (rr & (A.G - 1))) * (D * SIZE);
+          if (SPLIT || tk < left) *reinterpret_cast<uint4*>(out + at_row + c * SIZE + 16 * (lane & 7)) = v;
         }
         __syncwarp();
       }
