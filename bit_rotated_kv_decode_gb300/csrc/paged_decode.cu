@@ -237,7 +237,7 @@ struct Query {
   using C = Cols<GK, NR>;
   uint32_t b[C::QT][8][2];
   float scale[C::H];        // softmax scale (x q's power of two in 4 bits) of the lane's rows
-  float qsum[GK == 64 ? 2 : 1][C::H];   // 4 bits: sum of q over the group, x softmax scale
+  float qsum[GK == 64 ? 2 : 1][C::H];   // 4 bits: sum of q over the group, in the operand's scale
   int pos[C::H];
 };
 
@@ -292,8 +292,9 @@ __device__ __forceinline__ void put_query(const DecodeArgs& A, int req, int head
     else
       *reinterpret_cast<uint4*>(&sm.q[r / 8][r % 8][tid][4 * word]) = o;
     if (part % 8 == 0) {
-      sm.q_scale[r] = __uint_as_float(static_cast<uint32_t>(127 + ex - 13) << 23) * A.a.scale2;
-      sm.q_sum[part / 8][r] = sum * A.a.scale2;
+      // (not 0: it multiplies the -infinity of masked logits)
+      sm.q_scale[r] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex - 13) << 23) * A.a.scale2, 1.2e-38f);
+      sm.q_sum[part / 8][r] = sum * up;   // in the operand's scale
     }
   }
 }
@@ -324,32 +325,46 @@ __device__ __forceinline__ void take_query(const DecodeArgs& A, int req, const D
 }
 
 // B operand of the second product from the weights of the lane's rows: w0[h] and
-// w1[h] for tokens gid and gid + 8 of a 16-token tile.  hi rounds to the part's type.
-template <int GK, int NR, typename Hi, typename Pack>
+// w1[h] for tokens gid and gid + 8 of a 16-token tile.  P: the parts' type (pack rounds
+// two values to it, lo and hi give them back).
+template <int GK, int NR, typename P>
 __device__ __forceinline__ void weights(const float (&w0)[Cols<GK, NR>::H], const float (&w1)[Cols<GK, NR>::H],
-                                        uint32_t (&b)[Cols<GK, NR>::PT][2], Hi hi, Pack pack) {
+                                        uint32_t (&b)[Cols<GK, NR>::PT][2], P) {
   using C = Cols<GK, NR>;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float (&w)[C::H] = u ? w1 : w0;
     if constexpr (C::DUP) {
-      const float h = hi(w[0]), l = w[0] - h;
-      b[0][u] = movmatrix(pack(h, l));
-      if constexpr (C::PARTS == 3) b[1][u] = movmatrix(pack(l - hi(l), 0.0f));
+      const float h = P::round(w[0]), l = w[0] - h;
+      b[0][u] = movmatrix(P::pack(h, l));
+      if constexpr (C::PARTS == 3) b[1][u] = movmatrix(P::pack(l - P::round(l), 0.0f));
     } else {
 #pragma unroll
       for (int j = 0; j < C::QT; ++j) {
         float a = w[2 * j], c = w[2 * j + 1];
 #pragma unroll
         for (int part = 0; part < C::PARTS; ++part) {
-          b[C::PARTS * j + part][u] = movmatrix(pack(a, c));
-          a -= hi(a);
-          c -= hi(c);
+          const uint32_t both = P::pack(a, c);
+          b[C::PARTS * j + part][u] = movmatrix(both);
+          a -= P::lo(both);
+          c -= P::hi(both);
         }
       }
     }
   }
 }
+struct PartsBf16 {
+  __device__ static float round(float x) { return bf16_hi(x); }
+  __device__ static uint32_t pack(float a, float b) { return bf16x2(a, b); }
+  __device__ static float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  __device__ static float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+};
+struct PartsF16 {
+  __device__ static float round(float x) { return f16_hi(x); }
+  __device__ static uint32_t pack(float a, float b) { return f16x2(a, b); }
+  __device__ static float lo(uint32_t w) { return __low2float(*reinterpret_cast<const __half2*>(&w)); }
+  __device__ static float hi(uint32_t w) { return __high2float(*reinterpret_cast<const __half2*>(&w)); }
+};
 
 // One unit of 16 BF16 tokens from t0: stage = two halves of 64 channels, each K
 // [16][128 B] and V [16][128 B], 16-byte pieces swizzled within 8 rows by the TMA.
@@ -400,7 +415,7 @@ __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR
     S.l[h] += x0[h] + x1[h];
   }
   uint32_t b[C::PT][2];
-  weights<0, NR>(x0, x1, b, bf16_hi, bf16x2);
+  weights<0, NR>(x0, x1, b, PartsBf16());
   const int vrow = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) {
@@ -505,10 +520,9 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
         const int j = h / C::HPL, k = 2 * u + h % C::HPL;
         float y;
         if constexpr (NG == 1)
-          y = fmaf(sk[0], (s[j][0][k] + s[j][1][k]) * Q.scale[h], zk[0] * Q.qsum[0][h]);
+          y = fmaf(sk[0], s[j][0][k] + s[j][1][k], zk[0] * Q.qsum[0][h]);
         else
-          y = fmaf(sk[0], s[j][0][k] * Q.scale[h], zk[0] * Q.qsum[0][h]) +
-              fmaf(sk[1], s[j][1][k] * Q.scale[h], zk[1] * Q.qsum[1][h]);
+          y = fmaf(sk[0], s[j][0][k], fmaf(sk[1], s[j][1][k], fmaf(zk[0], Q.qsum[0][h], zk[1] * Q.qsum[1][h])));
         x[t][u][h] = y;
       }
     }
@@ -530,13 +544,13 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
     float pm = NEG_INF;
 #pragma unroll
     for (int t = 0; t < TILES; ++t) pm = fmaxf(pm, fmaxf(x[t][0][h], x[t][1][h]));
-    S.raise(h, pm);
-    const float ref = S.m[h] == NEG_INF ? 0.0f : S.m[h];
+    S.raise(h, pm * Q.scale[h]);
+    const float ref = S.m[h] == NEG_INF ? 0.0f : -S.m[h];
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        x[t][u][h] = ex2f(x[t][u][h] - ref);
+        x[t][u][h] = ex2f(fmaf(x[t][u][h], Q.scale[h], ref));
         S.l[h] += x[t][u][h];
       }
   }
@@ -583,7 +597,7 @@ __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, N
           S.z[g][h] = fmaf(pr, zv, S.z[g][h]);
         }
       }
-      weights<GK, NR>(w0, w1, b[g], f16_hi, f16x2);
+      weights<GK, NR>(w0, w1, b[g], PartsF16());
     }
     // the lane's four tokens of the tile: rows 2 tid, 2 tid + 1, + 8; two words of 8
     // channels of each (at group 64 one of each group)

@@ -218,6 +218,29 @@ def test_many_short_requests_and_a_long_one(b, group):
     run_attention(b, Pool(b, [150] * 70, 2, group, seed=7), [1] * 70, 4, 64, 3, workspace=ws)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 128, 64])
+def test_extreme_queries_and_scales(b, group):
+    """A zero query under a tiny scale (equal weights), large and small queries in one batch."""
+    hq, hkv, lens = 4, 1, [100, 70, 90]
+    pool = Pool(b, lens, hkv, group, seed=8)
+    x = np.random.default_rng(8).standard_normal((3, hq, D)).astype(np.float32)
+    x[0] = 0
+    x[1] *= 2.0 ** -40
+    x[2] *= 8
+    q = paged.bf16_bits(x)
+    pool.hide([1] * 3, 50, 3)
+    kv, table = pool.device()
+    for scale in (1e-30, 0.0):
+        out, lse = torch.empty(3, hq, D, device="cuda"), torch.empty(3, hq, device="cuda")
+        args = (kv, table, lens, bf16(q), out, hkv, 50, 3)
+        if group:
+            b.int4_attention(*args, group_size=group, lse=lse, scale=scale)
+        else:
+            b.window_attention(*args, lse=lse, scale=scale)
+        check_attention(pool, q, [1] * 3, 50, 3, out, lse, scale)
+
+
 # ---- prefill --------------------------------------------------------------------
 PREFILL = [
     # lens, q_lens, window, sinks
