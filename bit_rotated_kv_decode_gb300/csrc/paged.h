@@ -99,10 +99,11 @@ cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, 
 // Prefill: any number of query rows per request, BF16 pages.  q_map: q as (128
 // channels, Hq, rows), boxes of 64 channels x G heads x 128 / G rows; kv_map: the pool,
 // boxes of 64 channels x 64 tokens x 1.
-// partials: paged_prefill_partial_bytes() of the call's 256-row blocks (the sum of
-// paged_prefill_blocks()), used where few blocks meet many keys.
-int64_t paged_prefill_blocks(int m, int G);
-size_t paged_prefill_partial_bytes(int64_t blocks, int hkv, int sms);
+// partials: paged_prefill_partial_bytes() of the call's row blocks (the sum of
+// paged_prefill_blocks()), used where few blocks meet many keys.  f32: fp32 outputs,
+// whose blocks are smaller.
+int64_t paged_prefill_blocks(int m, int G, bool f32);
+size_t paged_prefill_partial_bytes(int64_t blocks, int hkv, int sms, bool f32);
 cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a,
                                  const CUtensorMap& q_map, const CUtensorMap& kv_map, void* partials, int sms,
                                  cudaStream_t s);

@@ -19,9 +19,8 @@
 // Both contractions run on warp-level mma.sync m16n8k16 with tokens, then channels,
 // as the 16 rows: at 4 to 16 query rows the fixed 128-row tile of the tcgen05 MMA
 // would be mostly padding, and the products take a tenth of the copies' time.
-//  * BF16: q and v are bf16 already; p is carried as three bf16 parts (24 bits; two
-//    parts at 9 to 16 rows, where the third has no registers), so every product is
-//    exact in fp32.
+//  * BF16: q and v are bf16 already; p is carried as three bf16 parts (24 bits), so
+//    every product is exact in fp32.
 //  * 4 bits: a code c is or-ed into the fp16 number 1024 (or 1024 + 16 c) and one
 //    half2 fma makes it c - 8, exact and centred: sums of the positive codes
 //    themselves would lose the mean of many values to their common offset and to the
@@ -150,13 +149,16 @@ __device__ __forceinline__ void cursor_next(const DecodeArgs& A, Cursor& c) {
 // Columns of the products.  Up to 4 rows: column 2 r is row r's first part and
 // 2 r + 1 its second, in one tile (the first product holds the row in both); a
 // third part takes the even columns of a second tile.  More rows: column n of
-// tile j is row 8 j + n, and the second product has a tile for each part.
+// tile j is row 8 j + n, and the second product has a tile for each part; the small
+// parts share one accumulator.
 template <int GK, int NR>
 struct Cols {
   static constexpr bool DUP = NR <= 4;
-  static constexpr int PARTS = GK == 0 && NR <= 8 ? 3 : 2;
+  static constexpr int PARTS = GK == 0 ? 3 : 2;
   static constexpr int QT = DUP ? 1 : NR / 8;        // tiles of the first product
   static constexpr int PT = DUP ? PARTS - 1 : PARTS * QT;   // tiles of the second
+  static constexpr int OT = DUP ? PT : 2 * QT;       // its accumulators
+  __device__ static constexpr int acc(int j) { return DUP ? j : 2 * (j / PARTS) + (j % PARTS ? 1 : 0); }   // of tile j
   static constexpr int HPL = DUP ? 1 : 2;            // rows of a tile that a lane holds
   static constexpr int H = QT * HPL;                 // rows that a lane holds
   // row of the lane's h-th
@@ -167,13 +169,13 @@ template <int GK, int NR>
 struct State {
   using C = Cols<GK, NR>;
   static constexpr int NG = GK == 64 ? 2 : 1;
-  float o[C::PT][8][4];
+  float o[C::OT][8][4];
   float m[C::H], l[C::H];
   float z[NG][C::H];      // sum p z (4 bits)
   int e[NG];              // p s is scaled by 2^(6 - e)
   __device__ void reset() {
 #pragma unroll
-    for (int i = 0; i < C::PT; ++i)
+    for (int i = 0; i < C::OT; ++i)
 #pragma unroll
       for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -195,18 +197,18 @@ struct State {
     for (int g = 0; g < NG; ++g) z[g][h] *= f;
     if constexpr (C::DUP) {
 #pragma unroll
-      for (int i = 0; i < C::PT; ++i)
+      for (int i = 0; i < C::OT; ++i)
 #pragma unroll
         for (int t = 0; t < 8; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[i][t][k] *= f;
     } else {
 #pragma unroll
-      for (int part = 0; part < C::PARTS; ++part)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-          o[C::PARTS * (h / 2) + part][t][h & 1] *= f;
-          o[C::PARTS * (h / 2) + part][t][2 + (h & 1)] *= f;
+          o[2 * (h / 2) + i][t][h & 1] *= f;
+          o[2 * (h / 2) + i][t][2 + (h & 1)] *= f;
         }
     }
   }
@@ -422,7 +424,7 @@ __device__ __forceinline__ void bf16_unit(const DecodeArgs& A, const Query<0, NR
     uint32_t af[4];
     ldsm4_t(af, base + (mt >> 2) * 4096 + 2048 + vrow * 128 + (((2 * (mt & 3) + vc) ^ (vrow & 7)) << 4));
 #pragma unroll
-    for (int j = 0; j < C::PT; ++j) mma_bf16(S.o[j][mt], af, b[j][0], b[j][1]);
+    for (int j = 0; j < C::PT; ++j) mma_bf16(S.o[C::acc(j)][mt], af, b[j][0], b[j][1]);
   }
 }
 
@@ -663,14 +665,9 @@ __device__ __forceinline__ void put_state(const State<GK, NR>& S, float (*st)[PA
           b += S.o[1][mt][2];
         }
       } else {
-        const int j = C::PARTS * (h / 2), k = h & 1;
-        a = S.o[j][mt][k];
-        b = S.o[j][mt][2 + k];
-#pragma unroll
-        for (int part = 1; part < C::PARTS; ++part) {
-          a += S.o[j + part][mt][k];
-          b += S.o[j + part][mt][2 + k];
-        }
+        const int j = 2 * (h / 2), k = h & 1;
+        a = S.o[j][mt][k] + S.o[j + 1][mt][k];
+        b = S.o[j][mt][2 + k] + S.o[j + 1][mt][2 + k];
       }
       if constexpr (GK == 0) {
         st[r][16 * mt + gid] = a;

@@ -268,19 +268,22 @@ size_t oscar_attention_workspace_bytes(int32_t n, const int32_t* q_lens, int32_t
     return 0;
   const int G = num_q_heads / num_kv_heads, sms = sm_count();
   int few = 1;            // most rows of a decode segment
-  int64_t blocks = 0;     // 256-row blocks of the longer requests
+  int64_t blocks[2] = {0, 0};   // row blocks of the longer requests, for bf16 and fp32 outputs
   for (int32_t i = 0; i < n; ++i) {
     const int64_t m = q_lens ? q_lens[i] : 1;
     if (m < 0) return 0;
     if (m * G > DECODE_MAX_ROWS)
-      blocks += paged_prefill_blocks(static_cast<int>(m), G);
+      for (int f32 = 0; f32 < 2; ++f32) blocks[f32] += paged_prefill_blocks(static_cast<int>(m), G, f32);
     else if (m * G > few)
       few = static_cast<int>(m) * G;
   }
   // both kernels use the same bytes, one after the other
-  const size_t decode = paged_decode_record_bytes(n * num_kv_heads, few, sms);
-  const size_t prefill = paged_prefill_partial_bytes(blocks, num_kv_heads, sms);
-  return PAGED_COUNTER_BYTES + (decode > prefill ? decode : prefill);
+  size_t most = paged_decode_record_bytes(n * num_kv_heads, few, sms);
+  for (int f32 = 0; f32 < 2; ++f32) {
+    const size_t prefill = paged_prefill_partial_bytes(blocks[f32], num_kv_heads, sms, f32);
+    if (prefill > most) most = prefill;
+  }
+  return PAGED_COUNTER_BYTES + most;
 }
 
 oscar_status oscar_window_attention(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,

@@ -10,9 +10,13 @@
 //   O = O + P V          tcgen05.mma, P from TMEM, O in TMEM
 // The reference m of a row moves only when exceeded by 2^8; then the row's sum and
 // its O are scaled (tcgen05.ld / st), otherwise O stays where it is.  P is rounded to
-// bf16 for bf16 outputs (each weight off by at most 2^-9, as much as the output's own
-// rounding); for fp32 outputs it is carried as two bf16 parts, in the columns that S
-// leaves.  Sums are taken of the unrounded weights, in fp32.
+// bf16 for bf16 outputs (each weight off by at most 2^-8, as much as the output's own
+// rounding); for fp32 outputs it is carried as three bf16 parts (24 bits).  Sums are taken
+// of the unrounded weights, in fp32.
+//
+// fp32 outputs take one query tile a CTA: the second's S holds half of P's parts and its O
+// the sum of the small parts' products, which would else add 16 roundings a key tile to O's
+// 8 (1700 query tokens, a window of 512: error 6.5e-7 and 41 us against 1.5e-6 and 31 us).
 //
 // Roles: warps 0-3 and 4-7 the softmax of query tile 0 and 1, one thread per row (TMEM
 // lane = row); warps 8 and 9 the products of query tile 0 and 1; warp 10 the TMA copies;
@@ -49,24 +53,25 @@ constexpr int PF_REGS = 168, PF_SOFTMAX_REGS = 208, PF_OTHER_REGS = 88;
 static_assert(2 * PF_SOFTMAX_REGS + PF_OTHER_REGS <= 3 * PF_REGS, "a split above the launch's registers waits forever");
 constexpr int PF_STAGES = 2;                   // of V of a key tile and K of the next
 constexpr int PF_FIRST = 64;                   // keys of P handed over first
+constexpr int PF_PARTS = 3;                    // parts of P for fp32 outputs
 constexpr int PF_ITEMS = 4;                    // items looked up ahead
 constexpr int PF_READERS = 11;                 // warps that read them
 constexpr int PF_ROWS = 128;                   // rows of a query tile
 constexpr int PF_KEYS = 2 * PAGE;              // keys of a tile
 constexpr int TILE_BYTES = 128 * D * 2;        // a Q, K or V tile
 
-
 struct PrefillArgs {
   PagedView p;
   AttnArgs a;
   int n, G, lg;                           // lg = log2 G
+  int tiles;                              // query tiles of an item, at most
   int splits, items;                      // parts of an item's key tiles; items in all, parts counted
-  float* partials;                        // [items][256][PARTIAL_FLOATS] where splits > 1
+  float* partials;                        // [items][128 tiles][PARTIAL_FLOATS] where splits > 1
   int32_t len[PAGED_MAX_REQ];
   int32_t m[PAGED_MAX_REQ];
   int32_t row[PAGED_MAX_REQ];
   int32_t table[PAGED_MAX_REQ];
-  int32_t bstart[PAGED_MAX_REQ + 1];      // 256-row blocks before request i (one kv head)
+  int32_t bstart[PAGED_MAX_REQ + 1];      // blocks of 128 tiles rows before request i (one kv head)
 };
 
 // The keys that the rows at positions [pmin, pmax] see, as a list of pages: [0, sink),
@@ -97,7 +102,7 @@ struct KeyTiles {
   }
 };
 
-// One item: up to 256 query rows of a kv head and their key tiles [j0, j1) of kt.
+// One item: up to 256 query rows (128 for fp32 outputs) of a kv head and their key tiles [j0, j1) of kt.
 struct alignas(16) Item {
   int index;               // -1: no more items
   int head, table, row;    // kv head, row of the page table, first row of q and out
@@ -122,10 +127,10 @@ struct alignas(16) Item {
       if (A.bstart[mid] <= blk) ri = mid; else hi = mid;
     }
     const int m = A.m[ri], per_tile = PF_ROWS >> A.lg;
-    const int tok0 = (blk - A.bstart[ri]) * 2 * per_tile;   // first token of the block, of the request's m
+    const int tok0 = (blk - A.bstart[ri]) * A.tiles * per_tile;   // first token of the block, of the request's m
     table = A.table[ri];
     row = A.row[ri] + tok0;
-    tokens = min(2 * per_tile, m - tok0);
+    tokens = min(A.tiles * per_tile, m - tok0);
     p0 = A.len[ri] - m + tok0;
     kt = KeyTiles::of(p0, p0 + tokens - 1, A.a.window, A.a.sinks);
     j0 = kt.count * split / A.splits;
@@ -463,9 +468,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_after();
 #pragma unroll
             for (int s = h ? PF_FIRST / 16 : 0; s < (h ? 8 : PF_FIRST / 16); ++s) {   // 16 keys
-              const uint32_t col = s_col + 64 * (s / 4) + 8 * (s % 4);
-              mma_ts(o_col, col, v + (2048 * s >> 4), IDESC_PV, (j > it.j0 || s > 0) ? 1u : 0u);
-              if constexpr (F32) mma_ts(o_col, col + 32, v + (2048 * s >> 4), IDESC_PV, 1u);
+              const uint32_t col = s_col + (F32 ? 128 : 64) * (s / 4) + 8 * (s % 4);
+#pragma unroll
+              for (int part = 0; part < (F32 ? PF_PARTS : 1); ++part)
+                mma_ts(o_col + (part ? 128 : 0), col + 32 * part, v + (2048 * s >> 4), IDESC_PV,
+                       (j > it.j0 || s > 0 || part > 1) ? 1u : 0u);
             }
           }
           if (!ok) break;
@@ -550,7 +557,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (raise) mx = top;
           if (j > j0) {   // the product before S is done: S was issued after it
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {   // in small pieces: the logits are live
+            for (int c = 0; c < (F32 ? 256 : 128); c += 16) {   // in small pieces: the logits are live
               uint32_t o[16];
               tmem_ld16(to + c, o);
               tc_wait_ld();
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float2 y[16];
-          uint32_t pk[16], low[16];
+          uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             y[i] = fma2(make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), scale_2, ref_2);
@@ -582,13 +589,22 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           for (int i = 0; i < 16; ++i) {
             pk[i] = bf16x2(y[i].x, y[i].y);
             sum[i & 3] = add2(sum[i & 3], y[i]);
-            if constexpr (F32)
-              low[i] = bf16x2(y[i].x - __uint_as_float(pk[i] << 16), y[i].y - __uint_as_float(pk[i] & 0xffff0000u));
           }
-          // P lies over S, 64 keys in 32 columns (and their second parts in the next 32)
-          const int col = 64 * (c / 2) + 16 * (c % 2);
+          // P lies over S, 64 keys in 32 columns (and their other parts in the next ones)
+          const int col = (F32 ? 128 : 64) * (c / 2) + 16 * (c % 2);
           tmem_st16(ts + col, pk);
-          if constexpr (F32) tmem_st16(ts + col + 32, low);
+          if constexpr (F32) {
+#pragma unroll
+            for (int part = 1; part < PF_PARTS; ++part) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                y[i].x -= __uint_as_float(pk[i] << 16);
+                y[i].y -= __uint_as_float(pk[i] & 0xffff0000u);
+                pk[i] = bf16x2(y[i].x, y[i].y);
+              }
+              tmem_st16(ts + col + 32 * part, pk);
+            }
+          }
           if (c == PF_FIRST / 32 - 1 || c == 3) {
             tc_wait_st();
             tc_fence_before();
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       const bool some = j1 > j0;
       const int tokens = it.tokens;
       const size_t row0 = (size_t)it.row * A.a.Hq + (size_t)it.head * A.G;   // of token 0, head 0 of the group
-      float* part = A.partials + ((size_t)it.index * 2 * PF_ROWS + a * PF_ROWS) * PARTIAL_FLOATS;
+      float* part = A.partials + ((size_t)it.index * A.tiles * PF_ROWS + a * PF_ROWS) * PARTIAL_FLOATS;
       release();
       if (some) ok = mbar_wait_warp(&sm.o_full[a], done & 1, ok);
       if (!ok) break;
@@ -631,7 +647,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           uint32_t o[PIECE];
           tmem_ld32(to + c, o);
           if constexpr (!WIDE) tmem_ld32(to + c + 32, o + 32);
+          if constexpr (F32) tmem_ld32(to + 128 + c, w);   // the small parts' sum
           tc_wait_ld();
+          if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(w[i]));
+          }
           if (c + PIECE == 128) {   // O is read: the next item may write it
             tc_fence_before();
             __syncwarp();
@@ -681,8 +702,8 @@ constexpr int FOLD_WARPS = 8;
 __global__ void __launch_bounds__(32 * FOLD_WARPS)
     paged_prefill_fold_kernel(const __grid_constant__ PrefillArgs A) {
   const int lane = threadIdx.x & 31;
-  const int unit = blockIdx.x * FOLD_WARPS + (threadIdx.x >> 5);   // ((block, head), row of 256)
-  const int r = unit % (2 * PF_ROWS), bh = unit / (2 * PF_ROWS), head = bh % A.p.Hkv, back = bh / A.p.Hkv;
+  const int unit = blockIdx.x * FOLD_WARPS + (threadIdx.x >> 5);   // ((block, head), row of the block)
+  const int rows = A.tiles * PF_ROWS, r = unit % rows, bh = unit / rows, head = bh % A.p.Hkv, back = bh / A.p.Hkv;
   const int blk = A.bstart[A.n] - 1 - back;
   if (blk < 0) return;
   int ri = 0, hi = A.n;
@@ -690,11 +711,11 @@ __global__ void __launch_bounds__(32 * FOLD_WARPS)
     const int mid = (ri + hi) >> 1;
     if (A.bstart[mid] <= blk) ri = mid; else hi = mid;
   }
-  const int tok = (blk - A.bstart[ri]) * (2 * PF_ROWS >> A.lg) + (r >> A.lg);
+  const int tok = (blk - A.bstart[ri]) * (rows >> A.lg) + (r >> A.lg);
   if (tok >= A.m[ri]) return;
   // part s of the item is at item ((back splits + s) Hkv + head)
   auto at = [&](int s) {
-    return A.partials + (((size_t)(back * A.splits + s) * A.p.Hkv + head) * 2 * PF_ROWS + r) * PARTIAL_FLOATS;
+    return A.partials + (((size_t)(back * A.splits + s) * A.p.Hkv + head) * rows + r) * PARTIAL_FLOATS;
   };
   float m = NEG_INF, l = 0.0f;
   for (int s = 0; s < A.splits; ++s) m = fmaxf(m, at(s)[PARTIAL_M]);
@@ -723,7 +744,7 @@ __global__ void __launch_bounds__(32 * FOLD_WARPS)
   if (A.a.lse && lane == 0) A.a.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : NEG_INF;
 }
 
-int64_t row_blocks(int m, int G) { return ((int64_t)m * G + 2 * PF_ROWS - 1) / (2 * PF_ROWS); }
+int item_rows(bool f32) { return f32 ? PF_ROWS : 2 * PF_ROWS; }
 
 }  // namespace
 
@@ -733,10 +754,12 @@ int paged_prefill_splits(int64_t blocks, int hkv, int sms) {
   const int64_t items = blocks * hkv;
   return items == 0 || 2 * items > sms ? 1 : static_cast<int>(sms / items < 32 ? sms / items : 32);
 }
-int64_t paged_prefill_blocks(int m, int G) { return row_blocks(m, G); }
-size_t paged_prefill_partial_bytes(int64_t blocks, int hkv, int sms) {
+int64_t paged_prefill_blocks(int m, int G, bool f32) {
+  return ((int64_t)m * G + item_rows(f32) - 1) / item_rows(f32);
+}
+size_t paged_prefill_partial_bytes(int64_t blocks, int hkv, int sms, bool f32) {
   const int splits = paged_prefill_splits(blocks, hkv, sms);
-  return splits == 1 ? 0 : (size_t)blocks * hkv * splits * 2 * PF_ROWS * PARTIAL_FLOATS * sizeof(float);
+  return splits == 1 ? 0 : (size_t)blocks * hkv * splits * item_rows(f32) * PARTIAL_FLOATS * sizeof(float);
 }
 
 cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a,
@@ -748,6 +771,8 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   A.n = n;
   A.G = a.Hq / p.Hkv;
   A.lg = A.G == 1 ? 0 : A.G == 2 ? 1 : A.G == 4 ? 2 : 3;
+  const int rows = item_rows(a.f32);
+  A.tiles = rows / PF_ROWS;
   int64_t blocks = 0, longest = 0;   // longest: key tiles of an item, at most
   for (int i = 0; i < n; ++i) {
     A.len[i] = reqs[i].len;
@@ -755,9 +780,8 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
     A.row[i] = reqs[i].row;
     A.table[i] = reqs[i].table;
     A.bstart[i] = static_cast<int32_t>(blocks);
-    blocks += row_blocks(reqs[i].m, A.G);
-    const int64_t seen = (int64_t)a.window + a.sinks + 2 * PF_ROWS < reqs[i].len ? (int64_t)a.window + a.sinks + 2 * PF_ROWS
-                                                                                 : reqs[i].len;
+    blocks += paged_prefill_blocks(reqs[i].m, A.G, a.f32);
+    const int64_t most = (int64_t)a.window + a.sinks + rows, seen = most < reqs[i].len ? most : reqs[i].len;
     longest = seen / PF_KEYS + 1 > longest ? seen / PF_KEYS + 1 : longest;
   }
   A.bstart[n] = static_cast<int32_t>(blocks);
@@ -789,7 +813,7 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   kernel<<<A.items < sms ? A.items : sms, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
   e = cudaGetLastError();
   if (e != cudaSuccess || A.splits == 1) return e;
-  const int64_t warps = blocks * p.Hkv * 2 * PF_ROWS;
+  const int64_t warps = blocks * p.Hkv * rows;
   paged_prefill_fold_kernel<<<static_cast<unsigned>((warps + FOLD_WARPS - 1) / FOLD_WARPS), 32 * FOLD_WARPS, 0, s>>>(A);
   return cudaGetLastError();
 }

@@ -13,7 +13,7 @@ most |x| + |z|, so |x| + 2 |z| stands for |x|:
           accumulator, at most 2^-22 of the running magnitude each (truncated, and
           aligned to the largest product): 8 2^-22 max |q| |k| scale; in 4 bits three
           more roundings (scale, product, sum), counted by doubling;
-  weight  ex2 2^-22, and p's parts: two bf16 parts leave 2^-17, two fp16 parts
+  weight  ex2 2^-22, and p's parts: three bf16 parts leave 2^-24, two fp16 parts
           2^-21; one bf16 part (long bf16 outputs) leaves 2^-8;
   sums    one rounding of 2^-22 per 16 tokens of a warp's share, 64 to fold.
 A bf16 output adds 2^-8 of itself.
@@ -115,7 +115,7 @@ def bf16(bits):
 
 
 def tolerance(out, mag, logit, tokens, four, one_part, out_bf16):
-    weight = 2.0 ** -22 + (2.0 ** -8 if one_part else 2.0 ** -21 if four else 2.0 ** -17)
+    weight = 2.0 ** -22 + (2.0 ** -8 if one_part else 2.0 ** -21 if four else 2.0 ** -24)
     rel = 2 * ((2 if four else 1) * 8 * 2.0 ** -22 * logit + weight) + 2.0 ** -22 * (tokens / 16 + 64)
     return rel * mag + (2.0 ** -8 * np.abs(out) if out_bf16 else 0)
 
@@ -261,11 +261,13 @@ PREFILL = [
 
 
 @pytest.mark.gpu
-def test_more_items_than_ctas(b):
-    """Prefill of more 256-row items than the GPU has SMs, one-tile ones among them, then a small one, on one workspace."""
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_more_items_than_ctas(b, out):
+    """Prefill of more items than the GPU has SMs (bf16: of one and of two tiles), then a small one, on one workspace."""
     lens = [70 + 13 * i % 90 for i in range(100)]
-    ws = run_attention(b, Pool(b, lens, 2, seed=3), lens, 4, 60, 3)
-    run_attention(b, Pool(b, [300], 1, seed=4), [300], 4, -1, 0, workspace=ws)
+    kind = dict(out_dtype=torch.float32 if out == "f32" else torch.bfloat16, one_part=lambda m: out == "bf16")
+    ws = run_attention(b, Pool(b, lens, 2, seed=3), lens, 4, 60, 3, **kind)
+    run_attention(b, Pool(b, [300], 1, seed=4), [300], 4, -1, 0, workspace=ws, **kind)
 
 
 @pytest.mark.gpu
