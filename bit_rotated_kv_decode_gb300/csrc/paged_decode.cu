@@ -33,6 +33,11 @@
 //      sum p v = sum (p s) (c - 8) + sum p (z + 8 s).
 // The probabilities come out of the first product with a lane holding two tokens
 // of a row; movmatrix turns them into the second product's operand.
+//
+// Measured, GQA 4 unless noted: BF16, 32 requests with an 8K window 169 us (0.96 of the
+// copy's rate), one of 100K 70 us (0.88), the smallest call 6 us on the GPU.  4 bits, 32
+// of 16K to 64K 243 us (0.88; 59 % of the issue slots, 1080 instructions a page); one of
+// 100K at GQA 8 39 us, of 30K 16 us: instructions, and 7 us to start and to fold.
 #include <atomic>
 
 #include "paged_device.cuh"
@@ -444,8 +449,8 @@ __device__ __forceinline__ uint32_t code_hi(uint32_t w, uint32_t magic) {
   return x;
 }
 
-// One 4-bit page (64 tokens from t0) as it lies in memory.  Row r of a 16-token tile is token r ^ ((r >> 1) & 1), which spreads
-// both products' reads over the banks.
+// One 4-bit page (64 tokens from t0) as it lies in memory.  Row r of a 16-token tile is
+// token r ^ ((r >> 1) & 1), which spreads both products' reads over the banks.
 template <int GK, int NR>
 __device__ __forceinline__ void int4_unit(const DecodeArgs& A, const Query<GK, NR>& Q, State<GK, NR>& S,
                                           uint8_t* stage, int t0, bool masked) {
