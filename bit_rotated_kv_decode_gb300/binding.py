@@ -370,6 +370,8 @@ def rope_table(length: int, dim: int = HEAD_DIM, theta: float = 10000.0, scale: 
 def int4_pool(num_pages: int, num_kv_heads: int, group_size: int = 128, device="cuda"):
     """Zeroed 4-bit page pool uint8 [num_pages][num_kv_heads][record]."""
     import torch
+    if group_size not in INT4_RECORD_BYTES:
+        _refuse("group_size must be 128 or 64")
     return torch.zeros(num_pages, num_kv_heads, INT4_RECORD_BYTES[group_size], dtype=torch.uint8, device=device)
 
 

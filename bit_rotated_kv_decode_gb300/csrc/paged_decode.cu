@@ -978,6 +978,11 @@ size_t paged_decode_record_bytes(int segments, int rows, int sms) {
   return (size_t)(segments + sms) * row_class(rows) * PARTIAL_FLOATS * sizeof(float);
 }
 
+int64_t paged_decode_units(const AttnReq& r, const AttnArgs& a, int gk, int hkv) {
+  const Units u = Units::of(r.len, r.m, a.window, a.sinks, gk == 0 ? Format<0>::UT : PAGE);
+  return (int64_t)hkv * (u.units > 0 ? u.units : 1);
+}
+
 cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, int gk,
                                 void* workspace, const CUtensorMap* map, int sms, cudaStream_t s) {
   DecodeArgs A;
@@ -993,7 +998,7 @@ cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, 
   for (int i = 0; i < n; ++i) {
     const Units u = Units::of(reqs[i].len, A.m, a.window, a.sinks, ut);
     A.req[i] = {reqs[i].len, reqs[i].row, reqs[i].table, static_cast<int32_t>(total), u};
-    total += (int64_t)p.Hkv * (u.units > 0 ? u.units : 1);
+    total += paged_decode_units(reqs[i], a, gk, p.Hkv);
     if (total > INT32_MAX) return cudaErrorInvalidValue;
   }
   A.total = static_cast<int32_t>(total);

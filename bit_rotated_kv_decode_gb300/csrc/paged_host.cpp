@@ -177,18 +177,24 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
   a.window = window < 0 || window > (1 << 30) ? (1 << 30) + (1 << 29) : window;
   a.sinks = sinks;
   a.scale2 = (scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(D))) * 1.4426950408889634f;
+  if (!std::isfinite(a.scale2)) return bad("scale too large");
   const int sms = sm_count();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AttnReq reqs[PAGED_MAX_REQ];
   // requests of more than 16 rows a kv head: the tiled kernel
   int count = 0, few = 0;
+  int64_t units = 0;
   int32_t row = 0;
   for (int32_t i = 0; i < n; ++i) {
     const int32_t m = q_lens ? q_lens[i] : 1;
     if (m > step) reqs[count++] = AttnReq{lens[i], m, row, i};
-    if (m >= 1 && m <= step) ++few;
+    if (m >= 1 && m <= step) {
+      ++few;
+      units += paged_decode_units(AttnReq{lens[i], m, row, i}, a, gk, hkv);
+    }
     row += m;
   }
+  if (units > INT32_MAX) return bad("too many visible tokens for one call");
   CUtensorMap kv_map, q_map;
   if (count) {
     if (!pool_map(&kv_map, pool, num_pages * hkv, PAGE, 1) ||

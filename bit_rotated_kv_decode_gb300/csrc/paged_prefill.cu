@@ -724,19 +724,19 @@ __global__ void __launch_bounds__(32 * FOLD_WARPS)
   };
   float m = NEG_INF, l = 0.0f;
   for (int s = 0; s < A.splits; ++s) m = fmaxf(m, at(s)[PARTIAL_M]);
+  // (a row without a maximum goes the same way: a NaN query's sums are NaN)
+  const float ref = m == NEG_INF ? 0.0f : m;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (m != NEG_INF) {
 #pragma unroll 4
-    for (int s = 0; s < A.splits; ++s) {
-      const float* p = at(s);
-      const float f = ex2f(p[PARTIAL_M] - m);
-      const float4 v = reinterpret_cast<const float4*>(p)[lane];
-      l = fmaf(p[PARTIAL_L], f, l);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
-    }
+  for (int s = 0; s < A.splits; ++s) {
+    const float* p = at(s);
+    const float f = ex2f(p[PARTIAL_M] - ref);
+    const float4 v = reinterpret_cast<const float4*>(p)[lane];
+    l = fmaf(p[PARTIAL_L], f, l);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
   }
   const size_t row = (size_t)(A.row[ri] + tok) * A.a.Hq + (size_t)head * A.G + (r & (A.G - 1));
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;

@@ -407,8 +407,9 @@ oscar_status oscar_int4_read(const void* kv, int64_t num_pages, const int32_t* p
  * touched.  Tokens that no query of a request sees may hold anything (NaN too);
  * those that some see and others do not must hold finite values.  Sums and softmax
  * statistics are fp32; weights enter the product with V to 24 bits (8 where a request
- * has more than 16 rows a kv head and out is bf16; 22 in 4 bits).  4 bits: at most
- * 16 / (Hq / Hkv) query tokens a request; read a prefix back for more. */
+ * has more than 16 rows a kv head and out is bf16; in 4 bits 22 of weight x value scale,
+ * not below 2^-31 of the largest value scale).  4 bits: at most 16 / (Hq / Hkv) query
+ * tokens a request; read a prefix back for more. */
 size_t oscar_attention_workspace_bytes(int32_t n, const int32_t* q_lens, int32_t num_q_heads, int32_t num_kv_heads);
 oscar_status oscar_window_attention(const void* kv, int64_t num_pages, const int32_t* page_table, int32_t max_pages,
                                     const int32_t* lens, const int32_t* q_lens, int32_t n, int32_t num_q_heads,

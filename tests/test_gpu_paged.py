@@ -241,6 +241,75 @@ def test_extreme_queries_and_scales(b, group):
         check_attention(pool, q, [1] * 3, 50, 3, out, lse, scale)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("group,m,t,out_dtype", [(0, 1, 300, "f32"), (0, 4, 3000, "f32"), (0, 100, 300, "f32"),
+                                                 (0, 100, 300, "bf16"), (0, 70, 2500, "f32"), (0, 70, 2500, "bf16"),
+                                                 (128, 1, 300, "f32"), (64, 4, 3000, "f32")])
+def test_rows_that_are_not_finite_keep_to_themselves(b, group, m, t, out_dtype):
+    """A NaN and an infinite query row: every other row has the bits that it has without them."""
+    hq, hkv, window = 8, 2, 90 if t == 300 else -1
+    pool = Pool(b, [t], hkv, group, seed=10)
+    pool.hide([m], window, 3)
+    kv, table = pool.device()
+    q = torch.randn(m, hq, D, device="cuda", generator=torch.Generator("cuda").manual_seed(4)).to(torch.bfloat16)
+    bad = q.clone()
+    bad[m // 2, 1, 5] = float("nan")
+    bad[m - 1, 6, 70] = float("inf")
+    outs = []
+    for x in (q, bad):
+        out = torch.empty(m, hq, D, dtype=torch.float32 if out_dtype == "f32" else torch.bfloat16, device="cuda")
+        lse = torch.empty(m, hq, device="cuda")
+        args = (kv, table, [t], x, out, hkv, window, 3)
+        if group:
+            b.int4_attention(*args, q_lens=[m], group_size=group, lse=lse)
+        else:
+            b.window_attention(*args, q_lens=[m], lse=lse)
+        outs.append((out, lse))
+    (o0, l0), (o1, l1) = outs
+    same = torch.ones(m, hq, dtype=torch.bool, device="cuda")
+    same[m // 2, 1] = same[m - 1, 6] = False
+    assert torch.equal(o0[same], o1[same]) and torch.equal(l0[same], l1[same])
+    assert o1[m // 2, 1].isnan().all()
+
+
+@pytest.mark.gpu
+def test_two_threads_on_streams_of_their_own(b):
+    """Calls from two threads at once, each with its stream, workspace and outputs."""
+    import threading
+    hq, hkv, lens = 8, 2, [2000, 300, 900]
+    pool = Pool(b, lens, hkv, seed=11)
+    pool.hide([1] * 3, 700, 5)
+    kv, table = pool.device()
+    bits = paged.bf16_bits(np.random.default_rng(11).standard_normal((3, hq, D)).astype(np.float32))
+    q, got, wrong = bf16(bits), {}, []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                out, lse, ws = torch.empty(3, hq, D, device="cuda"), torch.empty(3, hq, device="cuda"), None
+                for k in range(50):
+                    ws = b.window_attention(kv, table, lens, q, out, hkv, 700, 5, lse=lse, workspace=ws)
+                    if k % 7 == i:
+                        try:
+                            b.window_attention(kv, table, lens, q, out, hkv, 700, -1 - i, workspace=ws)
+                        except b.OscarError as e:
+                            assert "sinks" in str(e)
+                torch.cuda.current_stream().synchronize()
+                got[i] = (out, lse)
+        except Exception as e:   # to the test's thread
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong
+    for out, lse in got.values():
+        check_attention(pool, bits, [1] * 3, 700, 5, out, lse)
+
+
 # ---- prefill --------------------------------------------------------------------
 PREFILL = [
     # lens, q_lens, window, sinks

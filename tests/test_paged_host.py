@@ -60,7 +60,7 @@ ATTEND = dict(kv=A, pages=8, table=A, max_pages=4, lens=ints(3, 64), q_lens=ints
 @pytest.mark.parametrize("change", [
     dict(kv=None), dict(kv=A + 2), dict(pages=0), dict(table=None), dict(max_pages=0), dict(lens=None),
     dict(lens=ints(0, 5)), dict(lens=ints(3, 257)), dict(q_lens=ints(-1, 1)), dict(n=0), dict(n=257), dict(hkv=3),
-    dict(hq=6), dict(hq=32), dict(sinks=-1), dict(scale=float("inf")), dict(q=None), dict(q=A + 2), dict(qs=1000),
+    dict(hq=6), dict(hq=32), dict(sinks=-1), dict(scale=float("inf")), dict(scale=3e38), dict(q=None), dict(q=A + 2), dict(qs=1000),
     dict(qs=1028), dict(out=None), dict(out=A + 4), dict(kind=2), dict(ws=None), dict(ws=A + 16), dict(ws_bytes=100),
     dict(group=96)])
 def test_attention_refusals(b, change):
@@ -72,6 +72,19 @@ def test_attention_refusals(b, change):
         assert lib.oscar_window_attention(*v) == b.OSCAR_ERR_INVALID_ARG
     v.insert(9, 128 if group is None else group)
     assert lib.oscar_int4_attention(*v) == b.OSCAR_ERR_INVALID_ARG
+
+
+def test_attention_bounds_the_visible_tokens(b):
+    """Kv heads x visible 16-token units (4 bits: pages) of the decoded requests are below 2^31; a window counts."""
+    lib = b.load()
+    big = {**ATTEND, "hq": 1024, "hkv": 1024, "qs": 1024 * 128, "pages": 1024, "n": 16, "max_pages": 1 << 24,
+           "lens": ints(*[1 << 25] * 16), "q_lens": ints(40, *[1] * 15), "window": -1}
+    assert lib.oscar_window_attention(*big.values()) == b.OSCAR_ERR_INVALID_ARG
+    assert b"visible tokens" in lib.oscar_paged_last_error()
+    v = list({**big, "q_lens": None, "lens": ints(*[1 << 28] * 16)}.values())
+    v.insert(9, 128)
+    assert lib.oscar_int4_attention(*v) == b.OSCAR_ERR_INVALID_ARG
+    assert b"visible tokens" in lib.oscar_paged_last_error()
 
 
 def test_int4_attention_takes_a_few_query_tokens(b):
@@ -88,6 +101,12 @@ def test_read_refusals(b, change):
                 v=A, kind=1, error=None, stream=None)
     args.update(change)
     assert b.load().oscar_int4_read(*args.values()) == b.OSCAR_ERR_INVALID_ARG
+
+
+def test_int4_pool(b):
+    assert b.int4_pool(3, 2, device="cpu").shape == (3, 2, 8704) and b.int4_pool(1, 1, 64, "cpu").shape == (1, 1, 9216)
+    with pytest.raises(b.OscarError):
+        b.int4_pool(3, 2, 32, "cpu")
 
 
 def test_workspace_size(b):
