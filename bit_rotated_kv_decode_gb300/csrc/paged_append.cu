@@ -59,6 +59,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
 __device__ __forceinline__ uint32_t swap16(uint32_t a) { return __byte_perm(a, a, 0x1032); }
 
 __device__ __forceinline__ int find_req(const PagedRows& r, int n, int row) {
@@ -111,32 +118,35 @@ __device__ __noinline__ float2 range_exact(uint4 x) {
 }
 
 // Codes of 8 finite channels within fp16 (four words of bf16 pairs) with scale s > 0 or
-// s = 0 and zero z.  t = (x - z) * (1 / s) with an approximate reciprocal is within
-// 15 (2^-23 + 2^-24) of the quotient (one reciprocal and one product, quotients up to 15
-// and a little), so its rounding decides the code unless it lies within 2^-16 of a half;
-// then the exact quotient does.  Magic: adding 1.5 2^23 rounds to the nearest integer,
-// ties to even.
+// s = 0 and zero z.  The quotient (x - z) / s, rounded as the definition has it, by one
+// step of residual correction (Markstein, IBM J. Res. Dev. 34, 1990): t = d (1 / s) from an
+// approximate reciprocal is within 15.5 (2^-23 + 2^-24) of it; e = d - t s is exact (t s has
+// 35 bits, and what is left of d 14); t + e (1 / s) is within 2^-39 of the quotient before
+// its one rounding, while no quotient of a fp32 number by one of 11 bits lies nearer than
+// 2^-32 to the middle between two fp32 numbers from 1/4 to 16 (nor in it).  (Deciding the
+// quotients near a half by a division took 18 % of the kernel: with 11-bit scales one warp
+// in seven holds an exact tie.)  Magic: adding 1.5 2^23 rounds to the nearest integer, ties
+// to even.
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&x)[4], float s, float z, bool wild) {
   constexpr float MAGIC = 12582912.0f;
   float inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
   if (s == 0.0f) inv = 0.0f;
-  float worst = wild ? 1.0f : 0.0f;
-  const float2 zz = make_float2(-z, -z), ii = make_float2(inv, inv), mm = make_float2(MAGIC, MAGIC),
-               nn = make_float2(-MAGIC, -MAGIC);
+  const float2 zz = make_float2(-z, -z), ii = make_float2(inv, inv), ss = make_float2(-s, -s),
+               mm = make_float2(MAGIC, MAGIC);
   // r's bits are those of MAGIC plus the code: weighted by 16^e they add up to the word
   // plus a constant
   uint32_t w = 0u - 0x4B400000u * 0x11111111u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    float2 t = mul2(add2(make_float2(bf_lo(x[k]), bf_hi(x[k])), zz), ii);
+    const float2 d = add2(make_float2(bf_lo(x[k]), bf_hi(x[k])), zz), t0 = mul2(d, ii);
+    float2 t = fma2(fma2(t0, ss, d), ii, t0);
     t.x = fminf(fmaxf(t.x, 0.0f), 15.0f);
     t.y = fminf(fmaxf(t.y, 0.0f), 15.0f);
-    const float2 r = add2(t, mm), back = add2(r, nn);
-    worst = fmaxf(worst, fmaxf(fabsf(t.x - back.x), fabsf(t.y - back.y)));
+    const float2 r = add2(t, mm);
     w += (__float_as_uint(r.x) << (8 * k)) + (__float_as_uint(r.y) << (8 * k + 4));
   }
-  if (worst > 0.5f - 0x1p-16f) w = codes_exact(make_uint4(x[0], x[1], x[2], x[3]), s, z);
+  if (wild) w = codes_exact(make_uint4(x[0], x[1], x[2], x[3]), s, z);
   return w;
 }
 
@@ -187,20 +197,19 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
       mn[g] = INFINITY;
       mx[g] = -INFINITY;
     }
-#pragma unroll 1
+#pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float2 v = range_exact(u ? make_uint4(x[1][0], x[1][1], x[1][2], x[1][3])
-                                     : make_uint4(x[0][0], x[0][1], x[0][2], x[0][3]));
+      const float2 v = range_exact(make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]));
 #pragma unroll
       for (int g = 0; g < NG; ++g)
-        if (NG == 1 || (u ? c[1] : c[0]) / (GK / 8) == g) {
+        if (NG == 1 || c[u] / (GK / 8) == g) {
           mn[g] = fminf(mn[g], v.x);
           mx[g] = fmaxf(mx[g], v.y);
         }
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-#pragma unroll 1
+#pragma unroll
       for (int off = 1; off < 8; off <<= 1) {
         mn[g] = fminf(mn[g], __shfl_xor_sync(0xffffffffu, mn[g], off));
         mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
@@ -210,7 +219,10 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     z[g] = __float2half_rn(__fadd_rn(mn[g], 0.0f));
-    s[g] = __float2half_rn(__fdiv_rn(__fsub_rn(mx[g], mn[g]), 15.0f));
+    // a / 15, rounded: the residual correction again, with the rounded reciprocal (where a
+    // is so small that the residual is not exact, s is 0)
+    const float a = __fsub_rn(mx[g], mn[g]), q = __fmul_rn(a, 1.0f / 15.0f);
+    s[g] = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.0f, q, a), 1.0f / 15.0f, q));
   }
   if (!ok) return;
   uint8_t* codes = rec + (which ? I4_V_CODES : 0) + slot * I4_ROW;
@@ -357,48 +369,66 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
   }
 }
 
-// ---- 4-bit read-back: one thread per word of 8 codes -------------------------
-// Bound by its stores: K and V of 16K tokens of 8 heads as fp32 in 30 us (5.1 TB/s).  A
-// warp for four heads, with fewer address computations a word, took 34 against 31 us.
+// ---- 4-bit read-back: one thread per word of 8 key codes and that of the values --
+// Bound by its stores: K and V of 16K tokens of 8 heads as fp32 in READ_US us.
 constexpr int READ_THREADS = 256;
+
+// The 8 values s c + z of a word.  s c is exact in fp32 (11 + 4 bits), so a value is rounded
+// once.  Pairs of codes become fp16 numbers 1024 + c (or 1024 + 16 c), then c.
+template <bool F32>
+__device__ __forceinline__ void put_values(void* out, size_t at, uint32_t w, float s, float z) {
+  float y[8];
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {   // codes 2 half + odd and that + 4
+      const uint32_t bits = ((w >> (8 * half)) & (odd ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+      __half2 c = *reinterpret_cast<const __half2*>(&bits);
+      c = odd ? __hfma2(c, __half2half2(__ushort_as_half(0x2C00)), __half2half2(__ushort_as_half(0xD400)))   // / 16 - 64
+              : __hadd2(c, __half2half2(__ushort_as_half(0xE400)));                                          // - 1024
+      y[2 * half + odd] = fmaf(__low2float(c), s, z);
+      y[2 * half + odd + 4] = fmaf(__high2float(c), s, z);
+    }
+  if constexpr (F32) {
+    float* dst = static_cast<float*>(out) + at;
+    if ((reinterpret_cast<uintptr_t>(out) & 31) == 0) {   // at once: stores of 16 bytes each send half of every sector
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(y[0]), "f"(y[1]),
+                   "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<float4*>(dst)[0] = make_float4(y[0], y[1], y[2], y[3]);
+      reinterpret_cast<float4*>(dst)[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+        make_uint4(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]), pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
+  }
+}
 
 template <int GK, bool F32>
 __global__ void __launch_bounds__(READ_THREADS) int4_read_kernel(const __grid_constant__ PagedView p,
                                                                  const __grid_constant__ PagedRows rows, void* k_out,
-                                                                 void* v_out, int64_t words) {
-  const int64_t idx = (int64_t)blockIdx.x * READ_THREADS + threadIdx.x;
-  if (idx >= words) return;
-  // word = ((row Hkv + head) 2 + which) 16 + chunk
-  const int chunk = static_cast<int>(idx & 15), which = static_cast<int>((idx >> 4) & 1);
-  const int64_t rh = idx >> 5;
-  const int row = static_cast<int>(rh / p.Hkv), head = static_cast<int>(rh % p.Hkv);
+                                                                 void* v_out, uint32_t heads) {
+  // 16 threads a (row, head)
+  const uint32_t rh = blockIdx.x * (READ_THREADS / 16) + threadIdx.x / 16, chunk = threadIdx.x & 15;
+  if (rh >= heads) return;
+  const int row = static_cast<int>(rh / static_cast<uint32_t>(p.Hkv)), head = static_cast<int>(rh - row * p.Hkv);
   const int i = find_req(rows, p.n, row);
   const int pos = rows.pos0[i] + (row - rows.row0[i]);
   const int64_t page = page_of(p, i, pos);
-  uint32_t w = 0;
-  float s = 0.0f, z = 0.0f;
+  uint32_t kw = 0, vw = 0;
+  __half2 km = __half2half2(__ushort_as_half(0)), vm = km;
   if (page >= 0) {
     const uint8_t* rec = static_cast<const uint8_t*>(p.pool) + ((size_t)page * p.Hkv + head) * i4_record(GK);
-    const int slot = pos % PAGE;
-    w = *reinterpret_cast<const uint32_t*>(rec + (which ? I4_V_CODES : 0) + slot * I4_ROW + 4 * chunk);
-    const __half2 m = *reinterpret_cast<const __half2*>(rec + (which ? i4_v_meta(GK) : I4_META) +
-                                                        slot * i4_meta_row(GK) + 4 * (chunk / (GK / 8)));
-    s = __low2float(m);
-    z = __high2float(m);
+    const int code = (pos % PAGE) * I4_ROW + 4 * chunk, meta = (pos % PAGE) * i4_meta_row(GK) + 4 * (chunk / (GK / 8));
+    kw = *reinterpret_cast<const uint32_t*>(rec + code);
+    vw = *reinterpret_cast<const uint32_t*>(rec + I4_V_CODES + code);
+    km = *reinterpret_cast<const __half2*>(rec + I4_META + meta);
+    vm = *reinterpret_cast<const __half2*>(rec + i4_v_meta(GK) + meta);
   }
-  // s code is exact in fp32 (11 + 4 bits), so the value is rounded once
-  float y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = fmaf(static_cast<float>((w >> (4 * e)) & 15), s, z);
   const size_t at = (size_t)rh * D + 8 * chunk;
-  if constexpr (F32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(which ? v_out : k_out) + at);
-    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(which ? v_out : k_out) + at) =
-        make_uint4(pack_bf(y[0], y[1]), pack_bf(y[2], y[3]), pack_bf(y[4], y[5]), pack_bf(y[6], y[7]));
-  }
+  put_values<F32>(k_out, at, kw, __low2float(km), __high2float(km));
+  put_values<F32>(v_out, at, vw, __low2float(vm), __high2float(vm));
 }
 
 }  // namespace
@@ -425,16 +455,16 @@ cudaError_t launch_paged_append(const PagedView& p, const PagedRows& rows, const
 
 cudaError_t launch_int4_read(const PagedView& p, const PagedRows& rows, int gk, void* k_out, void* v_out, bool f32,
                              cudaStream_t s) {
-  const int64_t words = (int64_t)rows.row0[p.n] * p.Hkv * 32;
-  const int64_t blocks = (words + READ_THREADS - 1) / READ_THREADS;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(blocks);
+  const int64_t all = (int64_t)rows.row0[p.n] * p.Hkv;
+  if (all > INT32_MAX) return cudaErrorInvalidValue;   // (1 TB of values)
+  const uint32_t heads = static_cast<uint32_t>(all);
+  const unsigned grid = (heads + READ_THREADS / 16 - 1) / (READ_THREADS / 16);
   if (gk == 128) {
-    if (f32) int4_read_kernel<128, true><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, words);
-    else int4_read_kernel<128, false><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, words);
+    if (f32) int4_read_kernel<128, true><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
+    else int4_read_kernel<128, false><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
   } else {
-    if (f32) int4_read_kernel<64, true><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, words);
-    else int4_read_kernel<64, false><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, words);
+    if (f32) int4_read_kernel<64, true><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
+    else int4_read_kernel<64, false><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
   }
   return cudaGetLastError();
 }

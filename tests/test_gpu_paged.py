@@ -579,6 +579,37 @@ def test_graphs_that_share_a_workspace_and_new_lengths(b):
             check_attention(pool, bits, q_lens, 300, 4, out, lse)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [128, 64])
+def test_codes_of_exact_ties(b, group):
+    """Half of the quotients lie exactly between two codes, for scales from fp16's least to 2^12; and a read into
+    outputs that are aligned to 16 bytes only."""
+    g = np.random.default_rng(12)
+    rows, hkv = 64, 2
+    k = g.integers(0, 31, (rows, hkv, D)).astype(np.float64)
+    k[..., ::64], k[..., 1::64] = 0, 30
+    scale = np.array([m * 2.0 ** e for m in (1, 3, 5, 7) for e in (-24, -20, -15, -9, -4, 0, 3, 10)])
+    first = g.choice([0.0, -8.0, -15.0, 3.0], rows)            # the group's least value, in scales
+    x = ((k / 2 + first[:, None, None]) * np.resize(scale, rows)[:, None, None]).astype(np.float32)
+    bits = paged.bf16_bits(x)
+    kv, table = b.int4_pool(1, hkv, group), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    b.int4_append(kv, table, [0], bf16(bits), bf16(bits[::-1]), new_lens=[rows], group_size=group)
+    host = np.zeros((hkv, paged.record_bytes(group)), np.uint8)
+    levels = []
+    for which, values in enumerate((bits, bits[::-1])):
+        code, meta = paged.quantise4(values, group)
+        levels.append(paged.dequantise4(code, meta).astype(np.float32))
+        for r in range(rows):
+            for h in range(hkv):
+                paged.put4(host[h], which, r, code[r, h], meta[r, h])
+    assert np.array_equal(kv[0].cpu().numpy(), host)
+    out = torch.full((2, rows * hkv * D + 8), 7.0, device="cuda")
+    ko, vo = (o[4:-4].view(rows, hkv, D) for o in out)         # 16 bytes off a 32-byte boundary
+    b.int4_read(kv, table, [0], [rows], ko, vo, group_size=group)
+    assert np.array_equal(ko.cpu().numpy(), levels[0]) and np.array_equal(vo.cpu().numpy(), levels[1])
+    assert (out[:, :4] == 7).all() and (out[:, -4:] == 7).all()
+
+
 # ---- the two ways through the binding -----------------------------------------------
 @pytest.mark.gpu
 @pytest.mark.parametrize("group", [0, 128])
