@@ -237,17 +237,13 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
       *reinterpret_cast<uint32_t*>(meta + 4 * g) =
           static_cast<uint32_t>(__half_as_ushort(sh)) | (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
   }
-  if (c[1] == c[0] + 1) {
-    *reinterpret_cast<uint2*>(codes + 4 * c[0]) = make_uint2(w[0], w[1]);
-  } else {
-    *reinterpret_cast<uint32_t*>(codes + 4 * c[0]) = w[0];
-    *reinterpret_cast<uint32_t*>(codes + 4 * c[1]) = w[1];
-  }
+  *reinterpret_cast<uint32_t*>(codes + 4 * c[0]) = w[0];
+  *reinterpret_cast<uint32_t*>(codes + 4 * c[1]) = w[1];
 }
 
 // One warp takes 16 head rows (query, key and value heads in this order; in 4 bits key
-// and value rows or query rows) of one token: four groups of 8 lanes, a lane holding both chunks of its channel pairs,
-// so that the rotation needs no exchange and the cosines and sines are loaded
+// and value rows or query rows) of one token: four groups of 8 lanes, a lane holding both
+// chunks of its channel pairs, so that the rotation needs no exchange and the cosines and sines are loaded
 // once for all rows.  The kernel moves each byte once, and its traffic bounds it: in BF16
 // all loads of a lane (8 x 16 B) are in flight together.
 template <int GK, bool INTERLEAVED>
@@ -268,12 +264,13 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
   const int head0 = (kv_only ? hq + of_token * APP_HEADS : (of_token - static_cast<int>(kv_per_token)) * APP_HEADS) + sub;
   const int total = GK == 0 || kv_only ? hq + 2 * p.Hkv : hq;
 
-  // the lane's two chunks, and whether they hold rotated pairs
-  const int half_chunks = rope.dim / 16;   // pairs of chunks that are rotated
-  const bool rot = rope.table != nullptr && pc < half_chunks;
+  // the lane's two chunks, and whether they hold rotated pairs; neighbours of a chunk are in
+  // the next lane, so that an access of the warp takes whole sectors
+  const int half_chunks = rope.table ? rope.dim / 16 : 0;   // half the rotated chunks
   int c[2];
-  c[0] = !INTERLEAVED && rot ? pc : 2 * pc;
-  c[1] = !INTERLEAVED && rot ? pc + half_chunks : 2 * pc + 1;
+  c[0] = INTERLEAVED || pc < half_chunks ? pc : pc + half_chunks;
+  c[1] = INTERLEAVED || pc >= half_chunks ? pc + 8 : pc + half_chunks;
+  const bool rot[2] = {c[0] < 2 * half_chunks, c[1] < 2 * half_chunks};   // (the same unless interleaved)
   auto load_row = [&](int r, uint32_t (&x)[2][4]) {
     const int h = head0 + 4 * r;
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
@@ -297,36 +294,38 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
   const int pos = rows.pos0[i] + (row - rows.row0[i]);
   // pair e of the lane: element e of both chunks, or elements 2e, 2e + 1 of the 16
   float cs[8], sn[8];
-  if (rot) {
-    const float* t = rope.table + (size_t)pos * rope.dim + 8 * pc;
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      *reinterpret_cast<float4*>(cs + e) = __ldg(reinterpret_cast<const float4*>(t + e));
-      *reinterpret_cast<float4*>(sn + e) = __ldg(reinterpret_cast<const float4*>(t + rope.dim / 2 + e));
+  for (int u = 0; u < 2; ++u)
+    if (rot[u]) {
+      const float* t = rope.table + (size_t)pos * rope.dim + (INTERLEAVED ? 4 * c[u] : 8 * pc + 4 * u);
+      *reinterpret_cast<float4*>(cs + 4 * u) = __ldg(reinterpret_cast<const float4*>(t));
+      *reinterpret_cast<float4*>(sn + 4 * u) = __ldg(reinterpret_cast<const float4*>(t + rope.dim / 2));
     }
-  }
   const bool writes_kv = total > hq && head0 + 4 * (APP_ROWS - 1) >= hq;
   const int64_t page = writes_kv ? page_of(p, i, pos) : -1;
   const int slot = pos % PAGE;
   auto rotate_row = [&](int h, uint32_t (&x)[2][4]) {
-    if (rot && h < hq + p.Hkv) {
+    if (h >= hq + p.Hkv) return;
+    // (scalar operations: packed ones of two are contracted to fused multiply-adds)
+    if constexpr (INTERLEAVED) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (!rot[u]) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = bf_lo(x[u][k]), b = bf_hi(x[u][k]), co = cs[4 * u + k], si = sn[4 * u + k];
+          x[u][k] = pack_bf(__fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si)),
+                            __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si)));
+        }
+      }
+    } else if (rot[0]) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // (scalar operations: packed ones of two are contracted to fused multiply-adds)
-        if constexpr (INTERLEAVED) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float a = bf_lo(x[u][k]), b = bf_hi(x[u][k]), co = cs[4 * u + k], si = sn[4 * u + k];
-            x[u][k] = pack_bf(__fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si)),
-                              __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si)));
-          }
-        } else {
-          const float a0 = bf_lo(x[0][k]), a1 = bf_hi(x[0][k]), b0 = bf_lo(x[1][k]), b1 = bf_hi(x[1][k]);
-          x[0][k] = pack_bf(__fsub_rn(__fmul_rn(a0, cs[2 * k]), __fmul_rn(b0, sn[2 * k])),
-                            __fsub_rn(__fmul_rn(a1, cs[2 * k + 1]), __fmul_rn(b1, sn[2 * k + 1])));
-          x[1][k] = pack_bf(__fadd_rn(__fmul_rn(b0, cs[2 * k]), __fmul_rn(a0, sn[2 * k])),
-                            __fadd_rn(__fmul_rn(b1, cs[2 * k + 1]), __fmul_rn(a1, sn[2 * k + 1])));
-        }
+        const float a0 = bf_lo(x[0][k]), a1 = bf_hi(x[0][k]), b0 = bf_lo(x[1][k]), b1 = bf_hi(x[1][k]);
+        x[0][k] = pack_bf(__fsub_rn(__fmul_rn(a0, cs[2 * k]), __fmul_rn(b0, sn[2 * k])),
+                          __fsub_rn(__fmul_rn(a1, cs[2 * k + 1]), __fmul_rn(b1, sn[2 * k + 1])));
+        x[1][k] = pack_bf(__fadd_rn(__fmul_rn(b0, cs[2 * k]), __fmul_rn(a0, sn[2 * k])),
+                          __fadd_rn(__fmul_rn(b1, cs[2 * k + 1]), __fmul_rn(a1, sn[2 * k + 1])));
       }
     }
   };
