@@ -14,11 +14,12 @@
 // fp16 range of z) with NaN taken as 0; it stands for s code + z.
 //
 // A warp takes 16 head rows of a token, eight lanes a row, a lane both halves of its
-// channel pairs: the rotation needs no exchange and every access is 16 bytes a lane.
-// BF16: bound by DRAM, 32K tokens of 32 + 8 heads in 123 us (6.7 TB/s).  4 bits: bound by
-// the quantiser's instructions, 16K tokens in 77 us (4.7 TB/s, 60 % of the issue slots);
-// its code is rolled up, since four copies do not fit the instruction cache.  A step of
-// one token is a launch, 3.5 us on the GPU.
+// channel pairs: the rotation needs no exchange, and an access is 16 bytes a lane, whole
+// sectors of eight lanes (two of 16 in one sector by turns: 66 against 58 us).  Bound by
+// DRAM: BF16, 32K tokens of 32 + 8 heads in 123 us (6.7 TB/s); 4 bits, 16K tokens in 58 us
+// (6.2 TB/s), with the quantiser's code rolled up, since four copies do not fit the
+// instruction cache, and seven CTAs an SM (five: 100 against 91 us with the read-back).  A
+// step of one token is a launch, 3.5 us on the GPU.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -176,8 +177,7 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
     lo = max_bf2(lo, swap16(lo));
     const uint32_t both = __byte_perm(hi, lo, 0x5410);
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-      if (NG == 1 || c[u] / (GK / 8) == g) mm[g] = max_bf2(mm[g], both);
+    for (int g = 0; g < NG; ++g) mm[g] = max_bf2(mm[g], NG == 1 || c[u] / (GK / 8) == g ? both : 0xff80ff80u);
   }
 #pragma unroll
   for (int g = 0; g < NG; ++g)
@@ -201,11 +201,11 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
     for (int u = 0; u < 2; ++u) {
       const float2 v = range_exact(make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]));
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-        if (NG == 1 || c[u] / (GK / 8) == g) {
-          mn[g] = fminf(mn[g], v.x);
-          mx[g] = fmaxf(mx[g], v.y);
-        }
+      for (int g = 0; g < NG; ++g) {
+        const bool in = NG == 1 || c[u] / (GK / 8) == g;
+        mn[g] = fminf(mn[g], in ? v.x : INFINITY);
+        mx[g] = fmaxf(mx[g], in ? v.y : -INFINITY);
+      }
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g)
@@ -215,14 +215,14 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
         mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], off));
       }
   }
-  __half s[NG], z[NG];
+  uint32_t sz[NG];   // {s, z}
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    z[g] = __float2half_rn(__fadd_rn(mn[g], 0.0f));
     // a / 15, rounded: the residual correction again, with the rounded reciprocal (where a
     // is so small that the residual is not exact, s is 0)
     const float a = __fsub_rn(mx[g], mn[g]), q = __fmul_rn(a, 1.0f / 15.0f);
-    s[g] = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.0f, q, a), 1.0f / 15.0f, q));
+    const __half2 both = __floats2half2_rn(__fmaf_rn(__fmaf_rn(-15.0f, q, a), 1.0f / 15.0f, q), __fadd_rn(mn[g], 0.0f));
+    sz[g] = *reinterpret_cast<const uint32_t*>(&both);
   }
   if (!ok) return;
   uint8_t* codes = rec + (which ? I4_V_CODES : 0) + slot * I4_ROW;
@@ -230,12 +230,10 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
   uint32_t w[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int g = NG == 1 ? 0 : c[u] / (GK / 8);
-    const __half sh = NG == 1 || g == 0 ? s[0] : s[NG - 1], zh = NG == 1 || g == 0 ? z[0] : z[NG - 1];
-    w[u] = codes_of(x[u], __half2float(sh), __half2float(zh), wild);
-    if (c[u] % (GK / 8) == 0)
-      *reinterpret_cast<uint32_t*>(meta + 4 * g) =
-          static_cast<uint32_t>(__half_as_ushort(sh)) | (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
+    const uint32_t mine = NG == 1 || c[u] < GK / 8 ? sz[0] : sz[NG - 1];
+    const __half2 both = *reinterpret_cast<const __half2*>(&mine);
+    w[u] = codes_of(x[u], __low2float(both), __high2float(both), wild);
+    if (c[u] % (GK / 8) == 0) *reinterpret_cast<uint32_t*>(meta + 4 * (c[u] / (GK / 8))) = mine;
   }
   *reinterpret_cast<uint32_t*>(codes + 4 * c[0]) = w[0];
   *reinterpret_cast<uint32_t*>(codes + 4 * c[1]) = w[1];
@@ -247,12 +245,10 @@ __device__ __forceinline__ void store_int4(uint8_t* rec, int which, int slot, co
 // once for all rows.  The kernel moves each byte once, and its traffic bounds it: in BF16
 // all loads of a lane (8 x 16 B) are in flight together.
 template <int GK, bool INTERLEAVED>
-__global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_constant__ PagedView p,
-                                                                   const __grid_constant__ PagedRows rows,
-                                                                   const __grid_constant__ RopeArgs rope,
-                                                                   const __grid_constant__ AppendRows in,
-                                                                   uint32_t kv_per_token, uint32_t per_token,
-                                                                   uint32_t tasks) {
+__global__ void __launch_bounds__(APP_THREADS, GK == 0 ? 1 : 7)
+    paged_append_kernel(const __grid_constant__ PagedView p, const __grid_constant__ PagedRows rows,
+                        const __grid_constant__ RopeArgs rope, const __grid_constant__ AppendRows in,
+                        uint32_t kv_per_token, uint32_t per_token, uint32_t tasks) {
   const uint32_t task = (blockIdx.x * APP_THREADS + threadIdx.x) >> 5;
   if (task >= tasks) return;
   const int lane = threadIdx.x & 31, pc = lane & 7, sub = lane >> 3;
@@ -369,7 +365,7 @@ __global__ void __launch_bounds__(APP_THREADS) paged_append_kernel(const __grid_
 }
 
 // ---- 4-bit read-back: one thread per word of 8 key codes and that of the values --
-// Bound by its stores: K and V of 16K tokens of 8 heads as fp32 in READ_US us.
+// Bound by its stores: K and V of 16K tokens of 8 heads as fp32 in 23.5 us (6.5 TB/s).
 constexpr int READ_THREADS = 256;
 
 // The 8 values s c + z of a word.  s c is exact in fp32 (11 + 4 bits), so a value is rounded
