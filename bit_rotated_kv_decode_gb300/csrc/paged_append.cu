@@ -24,7 +24,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "paged.h"
+#include "paged_device.cuh"
 
 namespace oscar {
 namespace {
@@ -280,6 +280,8 @@ __global__ void __launch_bounds__(APP_THREADS, GK == 0 ? 1 : 7)
     x[0][0] = a.x, x[0][1] = a.y, x[0][2] = a.z, x[0][3] = a.w;
     x[1][0] = b.x, x[1][1] = b.y, x[1][2] = b.z, x[1][3] = b.w;
   };
+  paged::grid_dep_wait();
+  paged::grid_dep_launch();
   uint32_t x[APP_ROWS][2][4];
   load_row(0, x[0]);
   if (!kv_only) {
@@ -410,6 +412,8 @@ __global__ void __launch_bounds__(READ_THREADS) int4_read_kernel(const __grid_co
   const int row = static_cast<int>(rh / static_cast<uint32_t>(p.Hkv)), head = static_cast<int>(rh - row * p.Hkv);
   const int i = find_req(rows, p.n, row);
   const int pos = rows.pos0[i] + (row - rows.row0[i]);
+  paged::grid_dep_wait();
+  paged::grid_dep_launch();
   const int64_t page = page_of(p, i, pos);
   uint32_t kw = 0, vw = 0;
   __half2 km = __half2half2(__ushort_as_half(0)), vm = km;
@@ -437,15 +441,12 @@ cudaError_t launch_paged_append(const PagedView& p, const PagedRows& rows, const
   if (tasks * 32 > UINT32_MAX - APP_THREADS) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>((tasks * 32 + APP_THREADS - 1) / APP_THREADS);
   auto go = [&](auto kernel) {
-    kernel<<<grid, APP_THREADS, 0, s>>>(p, rows, rope, in, kv_per, per, static_cast<uint32_t>(tasks));
+    return paged::launch_dependent(kernel, grid, APP_THREADS, 0, s, p, rows, rope, in, kv_per, per,
+                                   static_cast<uint32_t>(tasks));
   };
-  if (gk == 0)
-    rope.interleaved ? go(paged_append_kernel<0, true>) : go(paged_append_kernel<0, false>);
-  else if (gk == 128)
-    rope.interleaved ? go(paged_append_kernel<128, true>) : go(paged_append_kernel<128, false>);
-  else
-    rope.interleaved ? go(paged_append_kernel<64, true>) : go(paged_append_kernel<64, false>);
-  return cudaGetLastError();
+  if (gk == 0) return rope.interleaved ? go(paged_append_kernel<0, true>) : go(paged_append_kernel<0, false>);
+  if (gk == 128) return rope.interleaved ? go(paged_append_kernel<128, true>) : go(paged_append_kernel<128, false>);
+  return rope.interleaved ? go(paged_append_kernel<64, true>) : go(paged_append_kernel<64, false>);
 }
 
 cudaError_t launch_int4_read(const PagedView& p, const PagedRows& rows, int gk, void* k_out, void* v_out, bool f32,
@@ -454,14 +455,11 @@ cudaError_t launch_int4_read(const PagedView& p, const PagedRows& rows, int gk, 
   if (all > INT32_MAX) return cudaErrorInvalidValue;   // (1 TB of values)
   const uint32_t heads = static_cast<uint32_t>(all);
   const unsigned grid = (heads + READ_THREADS / 16 - 1) / (READ_THREADS / 16);
-  if (gk == 128) {
-    if (f32) int4_read_kernel<128, true><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
-    else int4_read_kernel<128, false><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
-  } else {
-    if (f32) int4_read_kernel<64, true><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
-    else int4_read_kernel<64, false><<<grid, READ_THREADS, 0, s>>>(p, rows, k_out, v_out, heads);
-  }
-  return cudaGetLastError();
+  auto go = [&](auto kernel) {
+    return paged::launch_dependent(kernel, grid, READ_THREADS, 0, s, p, rows, k_out, v_out, heads);
+  };
+  if (gk == 128) return f32 ? go(int4_read_kernel<128, true>) : go(int4_read_kernel<128, false>);
+  return f32 ? go(int4_read_kernel<64, true>) : go(int4_read_kernel<64, false>);
 }
 
 }  // namespace oscar

@@ -765,6 +765,8 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
   __syncwarp();
   Cursor cc;
   cursor_first<UT>(A, cc, u0);
+  grid_dep_wait();
+  grid_dep_launch();
   put_query<GK, NR>(A, cc.req, cc.head, sm);
 
   // ---- the warp's copies: units u0 + warp, + NW, ... of the CTA's range.  Lane l looks
@@ -958,8 +960,7 @@ cudaError_t launch_decode_t(DecodeArgs& A, const CUtensorMap& map, int sms, cuda
   int ctas = most < sms ? most : sms;
   if (segments <= sms && A.total <= 3 * NW * segments) ctas = segments;
   A.ncta = ctas;
-  paged_decode_kernel<GK, NR><<<ctas, DecodeShape<GK, NR>::THREADS, bytes, s>>>(A, map);
-  return cudaGetLastError();
+  return launch_dependent(paged_decode_kernel<GK, NR>, ctas, DecodeShape<GK, NR>::THREADS, bytes, s, A, map);
 }
 
 template <int GK>
