@@ -295,6 +295,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  grid_dep_wait();
+  grid_dep_launch();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -718,6 +720,8 @@ __global__ void __launch_bounds__(32 * FOLD_WARPS)
   }
   const int tok = (blk - A.bstart[ri]) * (rows >> A.lg) + (r >> A.lg);
   if (tok >= A.m[ri]) return;
+  grid_dep_wait();
+  grid_dep_launch();
   // part s of the item is at item ((back splits + s) Hkv + head)
   auto at = [&](int s) {
     return A.partials + (((size_t)(back * A.splits + s) * A.p.Hkv + head) * rows + r) * PARTIAL_FLOATS;
@@ -815,12 +819,11 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
     if (e != cudaSuccess) return e;
     if (dev < 32) done[which].fetch_or(1u << dev);
   }
-  kernel<<<A.items < sms ? A.items : sms, PF_THREADS, bytes, s>>>(A, q_map, kv_map);
-  e = cudaGetLastError();
+  e = launch_dependent(kernel, A.items < sms ? A.items : sms, PF_THREADS, bytes, s, A, q_map, kv_map);
   if (e != cudaSuccess || A.splits == 1) return e;
   const int64_t warps = blocks * p.Hkv * rows;
-  paged_prefill_fold_kernel<<<static_cast<unsigned>((warps + FOLD_WARPS - 1) / FOLD_WARPS), 32 * FOLD_WARPS, 0, s>>>(A);
-  return cudaGetLastError();
+  return launch_dependent(paged_prefill_fold_kernel, static_cast<unsigned>((warps + FOLD_WARPS - 1) / FOLD_WARPS),
+                          32 * FOLD_WARPS, 0, s, A);
 }
 
 }  // namespace oscar
