@@ -251,16 +251,19 @@ struct Query {
 // The segment's query rows into shared memory as the B operand, 16 lanes a row, 8
 // channels a lane, by the first NR / 2 warps; take_query() is behind a barrier.  (A warp
 // of its own for every row made the same operand twelve times, 7000 cycles of it.)
+template <int NR>
+__device__ __forceinline__ uint4 load_query(const DecodeArgs& A, int req, int head) {
+  const int r = 2 * (threadIdx.x >> 5) + (threadIdx.x >> 4 & 1);
+  if (r >= A.m * A.G) return make_uint4(0, 0, 0, 0);
+  return __ldg(reinterpret_cast<const uint4*>(A.a.q + (int64_t)(A.req[req].row + r / A.G) * A.a.q_stride +
+                                              (int64_t)(head * A.G + r % A.G) * D) + (threadIdx.x & 15));
+}
 template <int GK, int NR>
-__device__ __forceinline__ void put_query(const DecodeArgs& A, int req, int head, DecodeSmem<GK, NR>& sm) {
+__device__ __forceinline__ void put_query(const DecodeArgs& A, uint4 w, DecodeSmem<GK, NR>& sm) {
   using C = Cols<GK, NR>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 15;
   if (warp >= NR / 2) return;
   const int r = 2 * warp + (lane >> 4);
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (r < A.m * A.G)
-    w = __ldg(reinterpret_cast<const uint4*>(A.a.q + (int64_t)(A.req[req].row + r / A.G) * A.a.q_stride +
-                                             (int64_t)(head * A.G + r % A.G) * D) + part);
   if constexpr (GK == 0) {
     // channels 8 part ..: k-step part / 2, register part % 2, one word for each of the four lanes
     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
   cursor_first<UT>(A, cc, u0);
   grid_dep_wait();
   grid_dep_launch();
-  put_query<GK, NR>(A, cc.req, cc.head, sm);
+  const uint4 q_first = load_query<NR>(A, cc.req, cc.head);   // on its way while the copies are issued
 
   // ---- the warp's copies: units u0 + warp, + NW, ... of the CTA's range.  Lane l looks
   // up the place of unit 32 k + l of them, so that the page ids of 32 copies come at the
@@ -819,6 +822,7 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
   };
 #pragma unroll 1
   for (int s = 0; s < STAGES; ++s) issue();
+  put_query<GK, NR>(A, q_first, sm);
 
   int cu = u0 + warp, taken = 0;
   State<GK, NR> S;
@@ -826,7 +830,7 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
   const int R = A.m * A.G;
   for (int seg_u = u0; seg_u < u1;) {
     const int seg_end = min(cc.seg_end, u1);
-    if (seg_u > u0) put_query<GK, NR>(A, cc.req, cc.head, sm);
+    if (seg_u > u0) put_query<GK, NR>(A, load_query<NR>(A, cc.req, cc.head), sm);
     __syncthreads();
     take_query<GK, NR>(A, cc.req, sm, Q);
     S.reset();
