@@ -766,6 +766,7 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
     mbar_init_fence();
   }
   __syncwarp();
+  if (GK == 0 && threadIdx.x == 0) prefetch_map(&map);
   Cursor cc;
   cursor_first<UT>(A, cc, u0);
   grid_dep_wait();

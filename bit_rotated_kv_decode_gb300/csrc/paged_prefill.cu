@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       mbar_init(&sm.item_empty[s], PF_READERS);
     }
     mbar_init_fence();
+    prefetch_map(&q_map);
+    prefetch_map(&kv_map);
   }
   if (warp == PF_MMA_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
