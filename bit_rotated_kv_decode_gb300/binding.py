@@ -384,8 +384,8 @@ def _paged_check(st: int, what: str) -> None:
         raise OscarError(st, f"{what}: {load().oscar_paged_last_error().decode()}")
 
 
-# These calls are made for every layer of a decode step, so they are marshalled in C
-# (csrc/calls.c).  What that does not take as it is -- a tensor that fails a check, no
+# These calls are made for every layer of a decode step, so they are marshalled in C++
+# (csrc/calls.cpp).  What that does not take as it is -- a tensor that fails a check, no
 # workspace yet, a stream of its own, lengths that are no list of ints -- goes the same way
 # in Python below, which says what is wrong.
 _torch = None
@@ -403,12 +403,10 @@ def calls():
         loader = importlib.machinery.ExtensionFileLoader("_oscar_calls", CALLS)
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_oscar_calls", loader))
         loader.exec_module(mod)
-        torch, lib = _context(None)[0], load()
-        mod.setup((torch.bfloat16, torch.float32, torch.int32, torch.uint8),
-                  (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream),
-                  tuple(ctypes.cast(fn, c_void_p).value for fn in (
-                      lib.oscar_bf16_append, lib.oscar_int4_append, lib.oscar_int4_read, lib.oscar_window_attention,
-                      lib.oscar_int4_attention)))
+        lib = load()
+        mod.setup(tuple(ctypes.cast(fn, c_void_p).value for fn in (
+            lib.oscar_bf16_append, lib.oscar_int4_append, lib.oscar_int4_read, lib.oscar_window_attention,
+            lib.oscar_int4_attention)))
         _calls = mod
     return _calls
 

@@ -8,6 +8,7 @@ rebuilt when its source or a header is newer than its object.  Beside it goes
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -20,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "liboscar_gb300.so")
-CALLS = os.path.join(LIBDIR, "_oscar_calls.so")   # argument marshalling for Python (csrc/calls.c)
+CALLS = os.path.join(LIBDIR, "_oscar_calls.so")   # argument marshalling for Python (csrc/calls.cpp)
 SOURCES = ["host.cpp", "write_kernels.cu", "decode_kernels.cu", "decode_scratch.cu", "bf16_decode.cu",
            "paged_host.cpp", "paged_append.cu", "paged_decode.cu", "paged_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -62,10 +63,16 @@ def build(verbose: bool = False, force: bool = False) -> str:
             extra = ["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []
             jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", path, "-o", obj])
 
-    calls_src = os.path.join(CSRC, "calls.c")
+    calls_src = os.path.join(CSRC, "calls.cpp")
     if force or _stale(CALLS, [calls_src] + headers):
-        jobs.append([shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-Wall", "-I" + INCLUDE,
-                     "-I" + sysconfig.get_paths()["include"], calls_src, "-o", CALLS])
+        torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)   # (importing it takes longer than the build)
+        torch_lib = os.path.join(torch_dir, "lib")
+        dirs = [INCLUDE, os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
+                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+                sysconfig.get_paths()["include"]]
+        jobs.append([shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", *("-I" + d for d in dirs),
+                     calls_src, "-o", CALLS, "-L" + torch_lib, "-Wl,-rpath," + torch_lib, "-ltorch_python", "-ltorch_cpu",
+                     "-lc10", "-lc10_cuda"])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
