@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(APP_THREADS, GK == 0 ? 1 : 7)
     x[0][0] = a.x, x[0][1] = a.y, x[0][2] = a.z, x[0][3] = a.w;
     x[1][0] = b.x, x[1][1] = b.y, x[1][2] = b.z, x[1][3] = b.w;
   };
-  paged::grid_dep_wait();
   paged::grid_dep_launch();
+  paged::grid_dep_wait();
   uint32_t x[APP_ROWS][2][4];
   load_row(0, x[0]);
   if (!kv_only) {
@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(READ_THREADS) int4_read_kernel(const __grid_co
   const int row = static_cast<int>(rh / static_cast<uint32_t>(p.Hkv)), head = static_cast<int>(rh - row * p.Hkv);
   const int i = find_req(rows, p.n, row);
   const int pos = rows.pos0[i] + (row - rows.row0[i]);
-  paged::grid_dep_wait();
   paged::grid_dep_launch();
+  paged::grid_dep_wait();
   const int64_t page = page_of(p, i, pos);
   uint32_t kw = 0, vw = 0;
   __half2 km = __half2half2(__ushort_as_half(0)), vm = km;

@@ -769,8 +769,8 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
   if (GK == 0 && threadIdx.x == 0) prefetch_map(&map);
   Cursor cc;
   cursor_first<UT>(A, cc, u0);
-  grid_dep_wait();
   grid_dep_launch();
+  grid_dep_wait();
   const uint4 q_first = load_query<NR>(A, cc.req, cc.head);   // on its way while the copies are issued
 
   // ---- the warp's copies: units u0 + warp, + NW, ... of the CTA's range.  Lane l looks

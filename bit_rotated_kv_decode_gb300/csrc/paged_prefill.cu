@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  grid_dep_wait();
   grid_dep_launch();
+  grid_dep_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -722,8 +722,8 @@ __global__ void __launch_bounds__(32 * FOLD_WARPS)
   }
   const int tok = (blk - A.bstart[ri]) * (rows >> A.lg) + (r >> A.lg);
   if (tok >= A.m[ri]) return;
-  grid_dep_wait();
   grid_dep_launch();
+  grid_dep_wait();
   // part s of the item is at item ((back splits + s) Hkv + head)
   auto at = [&](int s) {
     return A.partials + (((size_t)(back * A.splits + s) * A.p.Hkv + head) * rows + r) * PARTIAL_FLOATS;
