@@ -14,9 +14,12 @@
 // rounding); for fp32 outputs it is carried as three bf16 parts (24 bits).  Sums are taken
 // of the unrounded weights, in fp32.
 //
-// fp32 outputs take one query tile a CTA: the second's S holds half of P's parts and its O
-// the sum of the small parts' products, which would else add 16 roundings a key tile to O's
-// 8 (1700 query tokens, a window of 512: error 6.5e-7 and 41 us against 1.5e-6 and 31 us).
+// fp32 outputs take one query tile a CTA, and the second's columns keep the tensor core's
+// accumulation, which truncates, from showing: the small parts' products go to a sum of
+// their own (in O's they would add 16 truncations a key tile to 8), and every four key tiles
+// O's sum is added to a total, by fp32 additions (900 queries on 16K keys: error 1.1e-6 and
+// 985 us, 1.9e-5 and 920 without the total, plain fp32 2.6e-6).  P is then handed over 64
+// keys at a time, in the columns that S leaves.
 //
 // Roles: warps 0-3 and 4-7 the softmax of query tile 0 and 1, one thread per row (TMEM
 // lane = row); warps 8 and 9 the products of query tile 0 and 1; warp 10 the TMA copies;
@@ -59,6 +62,7 @@ static_assert(2 * PF_SOFTMAX_REGS + PF_OTHER_REGS <= 3 * PF_REGS, "a split above
 constexpr int PF_STAGES = 2;                   // of V of a key tile and K of the next
 constexpr int PF_FIRST = 64;                   // keys of P handed over first
 constexpr int PF_PARTS = 3;                    // parts of P for fp32 outputs
+constexpr int PF_FLUSH = 4;                    // key tiles between additions to the total (fp32 outputs)
 constexpr int PF_ITEMS = 4;                    // items looked up ahead
 constexpr int PF_READERS = 11;                 // warps that read them
 constexpr int PF_ROWS = 128;                   // rows of a query tile
@@ -149,6 +153,7 @@ struct alignas(1024) PrefillSmem {
   alignas(16) uint8_t out[8][32 * 128];                 // per softmax warp: 128 bytes of its 32 rows
   uint64_t q_full[2], q_empty[2], kv_full[PF_STAGES], kv_empty[PF_STAGES];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2];   // per query tile (and half of the keys)
+  uint64_t p_empty;                              // the first half's products are done (fp32 outputs)
   uint64_t turn[2];                              // the other tile's products of a key tile are issued
   uint64_t item_full[PF_ITEMS], item_empty[PF_ITEMS];
   Item item[PF_ITEMS];
@@ -288,6 +293,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       mbar_init(&sm.item_full[s], 1);
       mbar_init(&sm.item_empty[s], PF_READERS);
     }
+    mbar_init(&sm.p_empty, 1);
     mbar_init_fence();
     prefetch_map(&q_map);
     prefetch_map(&kv_map);
@@ -477,12 +483,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tc_fence_after();
 #pragma unroll
             for (int s = h ? PF_FIRST / 16 : 0; s < (h ? 8 : PF_FIRST / 16); ++s) {   // 16 keys
-              const uint32_t col = s_col + (F32 ? 128 : 64) * (s / 4) + 8 * (s % 4);
+              const uint32_t col = s_col + (F32 ? 0 : 64 * (s / 4)) + 8 * (s % 4);
+              const bool first = s == 0 && (F32 ? (j - it.j0) % PF_FLUSH == 0 : j == it.j0);
 #pragma unroll
               for (int part = 0; part < (F32 ? PF_PARTS : 1); ++part)
                 mma_ts(o_col + (part ? 128 : 0), col + 32 * part, v + (2048 * s >> 4), IDESC_PV,
-                       (j > it.j0 || s > 0 || part > 1) ? 1u : 0u);
+                       (part == 0 ? !first : j > it.j0 || s > 0 || part > 1) ? 1u : 0u);
             }
+            if (F32 && h == 0) mma_commit(&sm.p_empty);
           }
           if (!ok) break;
           if (j + 1 < it.j1) {
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (raise) mx = top;
           if (j > j0) {   // the product before S is done: S was issued after it
 #pragma unroll 1
-            for (int c = 0; c < (F32 ? 256 : 128); c += 16) {   // in small pieces: the logits are live
+            for (int c = F32 ? -128 : 0; c < (F32 ? 256 : 128); c += 16) {   // in small pieces: the logits are live
               uint32_t o[16];
               tmem_ld16(to + c, o);
               tc_wait_ld();
@@ -574,6 +582,22 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
               tmem_st16(to + c, o);
             }
+          }
+        }
+        if (F32 && j > j0 && (j - j0) % PF_FLUSH == 0) {   // O's sum so far to the total
+          tc_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16], total[16];
+            tmem_ld16(to + c, o);
+            if (j - j0 > PF_FLUSH) {
+              tmem_ld16(to - 128 + c, total);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(total[i]));
+            }
+            tc_wait_ld();
+            tmem_st16(to - 128 + c, o);
           }
         }
         const float ref = mx == NEG_INF ? 0.0f : -mx;
@@ -600,7 +624,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             sum[i & 3] = add2(sum[i & 3], y[i]);
           }
           // P lies over S, 64 keys in 32 columns (and their other parts in the next ones)
-          const int col = (F32 ? 128 : 64) * (c / 2) + 16 * (c % 2);
+          const int col = (F32 ? 0 : 64 * (c / 2)) + 16 * (c % 2);
+          if (F32 && c == 2) {   // the second half lies where the first was
+            ok = mbar_wait_warp(&sm.p_empty, tile & 1, ok);
+            tc_fence_after();
+          }
           tmem_st16(ts + col, pk);
           if constexpr (F32) {
 #pragma unroll
@@ -661,6 +689,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if constexpr (F32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(w[i]));
+            if (j1 - j0 > PF_FLUSH) {   // the total
+              tmem_ld32(to - 128 + c, w);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(w[i]));
+            }
           }
           if (c + PIECE == 128) {   // O is read: the next item may write it
             tc_fence_before();
