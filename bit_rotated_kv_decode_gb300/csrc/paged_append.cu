@@ -16,7 +16,7 @@
 // A warp takes 16 head rows of a token, eight lanes a row, a lane both halves of its
 // channel pairs: the rotation needs no exchange, and an access is 16 bytes a lane, whole
 // sectors of eight lanes (two of 16 in one sector by turns: 66 against 58 us).  Bound by
-// DRAM: BF16, 32K tokens of 32 + 8 heads in 123 us (6.7 TB/s); 4 bits, 16K tokens in 58 us
+// DRAM: BF16, 32K tokens of 32 + 8 heads in 120 us (6.9 TB/s); 4 bits, 16K tokens in 58 us
 // (6.2 TB/s), with the quantiser's code rolled up, since four copies do not fit the
 // instruction cache, and seven CTAs an SM (five: 100 against 91 us with the read-back).  A
 // step of one token is a launch, 3.5 us on the GPU.

@@ -34,10 +34,10 @@
 // The probabilities come out of the first product with a lane holding two tokens
 // of a row; movmatrix turns them into the second product's operand.
 //
-// Measured, GQA 4 unless noted: BF16, 32 requests with an 8K window 169 us (0.96 of the
-// copy's rate), one of 100K 70 us (0.88), the smallest call 6 us on the GPU.  4 bits, 32
-// of 16K to 64K 243 us (0.88; 59 % of the issue slots, 1080 instructions a page); one of
-// 100K at GQA 8 39 us, of 30K 16 us: instructions, and 7 us to start and to fold.
+// Measured, GQA 4 unless noted: BF16, 32 requests with an 8K window 164 us (0.99 of the
+// copy's rate), one of 100K 67 us (0.92), the smallest call 6 us.  4 bits, 32 of 16K to
+// 64K 238 us (0.90; 59 % of the issue slots, 1080 instructions a page); one of 100K at
+// GQA 8 35 us, of 30K 14 us: instructions, and 6 us to start and to fold.
 #include <atomic>
 
 #include "paged_device.cuh"

@@ -40,9 +40,9 @@
 // would leave most SMs idle (a few query tokens on a long cache) an item's key tiles are
 // split, its unnormalised rows go to the workspace and a second kernel folds them.
 //
-// Bound by the tensor core: 16K tokens, GQA 4, window 4096: 540 us, 1.8 PFLOP/s, the
-// tensor pipe 81 % busy (a key tile of both query tiles takes 2310 cycles, its products
-// 2048).  Ragged, GQA 8, window 1024: 217 us and 67 %, since a quarter of an item's time
+// Bound by the tensor core: 16K tokens, GQA 4, window 4096: 536 us, 1.8 PFLOP/s, the
+// tensor pipe 80 % busy (a key tile of both query tiles takes 2310 cycles, its products
+// 2048).  Ragged, GQA 8, window 1024: 214 us and 66 %, since a quarter of an item's time
 // is its ends.
 #include <atomic>
 
