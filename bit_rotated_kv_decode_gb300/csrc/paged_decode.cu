@@ -710,8 +710,9 @@ __device__ __forceinline__ void write_row(const DecodeArgs& A, int req, int head
 }
 
 // Fold count states of one row, the warp's lanes holding 4 channels each: weights by 32
-// lanes at once, then eight rows in flight.  The code runs once in a launch, from a cold
-// instruction cache, so it is short.
+// lanes at once, rows FOLD_ROWS at a time, the first of them on their way with the weights.
+// The code runs once in a launch, from a cold instruction cache, so it is short.
+constexpr int FOLD_ROWS = 8;   // (16: the same times)
 template <typename P>
 __device__ __forceinline__ void fold(int count, P at, int lane, float4& o, float& m, float& l) {
   m = NEG_INF;
@@ -721,23 +722,28 @@ __device__ __forceinline__ void fold(int count, P at, int lane, float4& o, float
   for (int base = 0; base < count; base += 32) {
     const float* mine = at(min(base + lane, count - 1));
     const float mc = base + lane < count ? __ldcg(mine + PARTIAL_M) : NEG_INF, lc = __ldcg(mine + PARTIAL_L);
-    float top = fmaxf(mc, m);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float ref = top == NEG_INF ? 0.0f : top, f0 = ex2f(m - ref), f = ex2f(mc - ref);
-    float sum = lc * f;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    l = fmaf(l, f0, sum);
-    m = top;
-    o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+    float f = 0.0f;
 #pragma unroll 1
-    for (int c = 0; c < 32 && base + c < count; c += 8) {
-      float4 v[8];
+    for (int c = 0; c < 32 && base + c < count; c += FOLD_ROWS) {
+      float4 v[FOLD_ROWS];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = __ldcg(reinterpret_cast<const float4*>(at(min(base + c + u, count - 1))) + lane);
+      for (int u = 0; u < FOLD_ROWS; ++u)
+        v[u] = __ldcg(reinterpret_cast<const float4*>(at(min(base + c + u, count - 1))) + lane);
+      if (c == 0) {
+        float top = fmaxf(mc, m);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float ref = top == NEG_INF ? 0.0f : top, f0 = ex2f(m - ref);
+        f = ex2f(mc - ref);
+        float sum = lc * f;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l = fmaf(l, f0, sum);
+        m = top;
+        o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+      }
+#pragma unroll
+      for (int u = 0; u < FOLD_ROWS; ++u) {
         const float w = __shfl_sync(0xffffffffu, f, c + u);   // 0 behind the last
         o.x = fmaf(v[u].x, w, o.x);
         o.y = fmaf(v[u].y, w, o.y);
