@@ -840,40 +840,8 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
     if (seg_u > u0) put_query<GK, NR>(A, load_query<NR>(A, cc.req, cc.head), sm);
     __syncthreads();
     take_query<GK, NR>(A, cc.req, sm, Q);
-    S.reset();
     const int len = A.req[cc.req].len;
-    for (; cu < seg_end; cu += NW) {
-      const int v = cu - cc.base, st = taken % STAGES;
-      if (!dead && !mbar_wait(&sm.full[warp][st], (taken / STAGES) & 1)) {
-        if (lane == 0 && A.p.err) atomicOr(A.p.err, PAGED_ERR_TIMEOUT);
-        dead = true;
-      }
-      dead = __any_sync(0xffffffffu, dead);
-      if (!dead && v < cc.un.units) {
-        const int t0 = cc.un.unit(v) * UT;
-        const bool masked = !(t0 + UT - 1 <= len - A.m &&
-                              (t0 + UT <= A.a.sinks || (int64_t)t0 > (int64_t)len - 1 - A.a.window));
-        if constexpr (GK == 0)
-          bf16_unit<NR>(A, Q, S, sm.ring[warp][st], t0, masked);
-        else
-          int4_unit<GK, NR>(A, Q, S, sm.ring[warp][st], t0, masked);
-      }
-      __syncwarp();
-      ++taken;
-      issue();
-    }
-    // ---- the CTA's share of the segment: the warps' states folded a few at a time
-    // (all of them at once would take the ring's room)
-    const int full_units = cc.seg_end - cc.base;
-    const int seg = cc.req * A.p.Hkv + cc.head;
-    const int c_lo = static_cast<int>((((int64_t)cc.base + 1) * A.ncta - 1) / A.total);
-    const int c_hi = static_cast<int>(((int64_t)cc.seg_end * A.ncta - 1) / A.total);
-    const bool whole = seg_end - seg_u == full_units;
-    constexpr int FOLD = SM::FOLD, MINE = (NR + NW - 1) / NW;   // rows of a warp
-    using StateRows = float (*)[PARTIAL_FLOATS];
-    static_assert(sizeof(float) * NR * PARTIAL_FLOATS <= sizeof(sm.ring[0]), "a state fits its warp's ring");
-    const bool final_seg = seg_end == u1;   // no copy is in flight: every warp's state over its own ring, at once
-    const int step = final_seg ? NW : FOLD;
+    constexpr int MINE = (NR + NW - 1) / NW;   // rows of a warp
     float4 fo[MINE];
     float fm[MINE], fl[MINE];
 #pragma unroll
@@ -882,32 +850,77 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
       fm[i] = NEG_INF;
       fl[i] = 0.0f;
     }
-#pragma unroll 1
-    for (int w0 = 0; w0 < NW; w0 += step) {
-      if (warp >= w0 && warp < w0 + step)
-        put_state<GK, NR>(S, final_seg ? reinterpret_cast<StateRows>(sm.ring[warp][0]) : sm.state[warp - w0]);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < MINE; ++i) {
-        const int r = warp + NW * i;
-        if (r >= R) continue;
-        float4& o = fo[i];
-#pragma unroll 2
-        for (int w = 0; w < step; ++w) {
-          const float* st = final_seg ? reinterpret_cast<StateRows>(sm.ring[w][0])[r] : sm.state[w][r];
-          const float ms = st[PARTIAL_M], m = fmaxf(fm[i], ms), ref = m == NEG_INF ? 0.0f : m;
-          const float f0 = ex2f(fm[i] - ref), f = ex2f(ms - ref);
-          const float4 x = reinterpret_cast<const float4*>(st)[lane];
-          fm[i] = m;
-          fl[i] = fmaf(st[PARTIAL_L], f, fl[i] * f0);
-          o.x = fmaf(x.x, f, o.x * f0);
-          o.y = fmaf(x.y, f, o.y * f0);
-          o.z = fmaf(x.z, f, o.z * f0);
-          o.w = fmaf(x.w, f, o.w * f0);
+    // A share of more than 256 units a warp is taken in parts, since the matrix unit
+    // truncates its sums: 20 requests of 60K, error 6.2e-6 at once and 4.0e-6 in parts, plain
+    // fp32 4.5e-6, the same 702 us.  (Not where the sums in between cost more registers than
+    // there are: 16 rows 752 against 718 us; 4 bits 245 against 238 us, error 4.7e-6 against
+    // 5.1e-6.)
+    constexpr bool PARTS = GK == 0 && NR <= 8;
+    constexpr int PART = 256 * NW;
+    int part_u = seg_u;
+    do {
+      const int part_end = PARTS && seg_end - part_u > PART ? part_u + PART : seg_end;
+      S.reset();
+      for (; cu < part_end; cu += NW) {
+        const int v = cu - cc.base, st = taken % STAGES;
+        if (!dead && !mbar_wait(&sm.full[warp][st], (taken / STAGES) & 1)) {
+          if (lane == 0 && A.p.err) atomicOr(A.p.err, PAGED_ERR_TIMEOUT);
+          dead = true;
         }
+        dead = __any_sync(0xffffffffu, dead);
+        if (!dead && v < cc.un.units) {
+          const int t0 = cc.un.unit(v) * UT;
+          const bool masked = !(t0 + UT - 1 <= len - A.m &&
+                                (t0 + UT <= A.a.sinks || (int64_t)t0 > (int64_t)len - 1 - A.a.window));
+          if constexpr (GK == 0)
+            bf16_unit<NR>(A, Q, S, sm.ring[warp][st], t0, masked);
+          else
+            int4_unit<GK, NR>(A, Q, S, sm.ring[warp][st], t0, masked);
+        }
+        __syncwarp();
+        ++taken;
+        issue();
       }
-      if (!final_seg) __syncthreads();
-    }
+      // ---- the CTA's share of the segment: the warps' states folded a few at a time
+      // (all of them at once would take the ring's room)
+      constexpr int FOLD = SM::FOLD;
+      using StateRows = float (*)[PARTIAL_FLOATS];
+      static_assert(sizeof(float) * NR * PARTIAL_FLOATS <= sizeof(sm.ring[0]), "a state fits its warp's ring");
+      const bool final_seg = part_end == u1;   // no copy is in flight: every warp's state over its own ring, at once
+      const int step = final_seg ? NW : FOLD;
+#pragma unroll 1
+      for (int w0 = 0; w0 < NW; w0 += step) {
+        if (warp >= w0 && warp < w0 + step)
+          put_state<GK, NR>(S, final_seg ? reinterpret_cast<StateRows>(sm.ring[warp][0]) : sm.state[warp - w0]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int r = warp + NW * i;
+          if (r >= R) continue;
+          float4& o = fo[i];
+#pragma unroll 2
+          for (int w = 0; w < step; ++w) {
+            const float* st = final_seg ? reinterpret_cast<StateRows>(sm.ring[w][0])[r] : sm.state[w][r];
+            const float ms = st[PARTIAL_M], m = fmaxf(fm[i], ms), ref = m == NEG_INF ? 0.0f : m;
+            const float f0 = ex2f(fm[i] - ref), f = ex2f(ms - ref);
+            const float4 x = reinterpret_cast<const float4*>(st)[lane];
+            fm[i] = m;
+            fl[i] = fmaf(st[PARTIAL_L], f, fl[i] * f0);
+            o.x = fmaf(x.x, f, o.x * f0);
+            o.y = fmaf(x.y, f, o.y * f0);
+            o.z = fmaf(x.z, f, o.z * f0);
+            o.w = fmaf(x.w, f, o.w * f0);
+          }
+        }
+        if (!final_seg) __syncthreads();
+      }
+      part_u = part_end;
+    } while (PARTS && part_u < seg_end);
+    const int full_units = cc.seg_end - cc.base;
+    const int seg = cc.req * A.p.Hkv + cc.head;
+    const int c_lo = static_cast<int>((((int64_t)cc.base + 1) * A.ncta - 1) / A.total);
+    const int c_hi = static_cast<int>(((int64_t)cc.seg_end * A.ncta - 1) / A.total);
+    const bool whole = seg_end - seg_u == full_units;
     float* rec = A.partials + (size_t)(seg + cta) * NR * PARTIAL_FLOATS;
 #pragma unroll
     for (int i = 0; i < MINE; ++i) {

@@ -219,6 +219,31 @@ def test_many_short_requests_and_a_long_one(b, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq", [8, 16, 32])
+def test_long_shares(b, hq):
+    """More segments than CTAs, each with more tokens than a CTA sums up at once (up to 8 rows); the requests share
+    their pages.  A warp's sums are over 4096 tokens at most, or over an eighth of the segment (16 rows)."""
+    n, hkv, top = 84, 2, 40000
+    m = 2 if hq == 32 else 1                                  # 4, 8 and 16 rows
+    hq = 16 if hq == 32 else hq
+    pool = Pool(b, [top], hkv, seed=13)
+    lens = [top - 61 * i for i in range(n)]
+    kv, table = pool.device()
+    bits = paged.bf16_bits(np.random.default_rng(13).standard_normal((n * m, hq, D)).astype(np.float32))
+    out, lse = torch.empty(n * m, hq, D, device="cuda"), torch.empty(n * m, hq, device="cuda")
+    b.window_attention(kv, table.expand(n, -1).contiguous(), lens, bf16(bits), out, hkv, q_lens=[m] * n, lse=lse)
+    qf, out, lse = paged.bf16_values(bits).astype(np.float64), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for i in (0, 1, 40, 83):
+        for h in (0, hq - 1):
+            row, kh = i * m + m - 1, h // (hq // hkv)
+            want, ls, mag, logit = paged.attend(qf[row, h], pool.k[0][:, kh], pool.v[0][:, kh], lens[i] - 1, -1, 0,
+                                                1 / math.sqrt(D), pool.kmag[0][:, kh], pool.vmag[0][:, kh])
+            tol = tolerance(want, mag, logit, 4096 if m == 1 else top / 8, 0, False, False)
+            assert (np.abs(out[row, h] - want) <= tol).all()
+            assert abs(lse[row, h] - ls) <= 2 * 8 * 2.0 ** -22 * logit + 2.0 ** -20 + 2.0 ** -22 * (4096 / 16 + 64)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("group", [0, 128, 64])
 def test_extreme_queries_and_scales(b, group):
     """A zero query under a tiny scale (equal weights), large and small queries in one batch."""
