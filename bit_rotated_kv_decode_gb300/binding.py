@@ -8,6 +8,7 @@ loads the library and fails loudly if it has not been built.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
@@ -455,15 +456,40 @@ def _heads(name: str, t, bf16, rows: int, heads: int, device: int):
     return t.data_ptr(), stride if rows > 1 else heads * HEAD_DIM
 
 
+# ctypes cuts an int to the argument's width without a word, so every int is checked before a call.
+INT32_MIN, INT32_MAX = -2 ** 31, 2 ** 31 - 1
+
+
+def _int(name: str, value) -> int:
+    try:
+        return operator.index(value)
+    except TypeError:
+        _refuse(f"{name}: an int is wanted")
+
+
+def _int32(name: str, value) -> int:
+    v = _int(name, value)
+    if not INT32_MIN <= v <= INT32_MAX:
+        _refuse(f"{name}: {v} is beyond 32 bits")
+    return v
+
+
+def _window(value) -> int:
+    """A window beyond 32 bits holds every cache: no bound, as a negative one."""
+    v = _int("window", value)
+    return v if INT32_MIN <= v <= INT32_MAX else -1
+
+
 def _counts(values, n: int, name: str):
     """(ctypes array, sum) of one host int per request; None stands for one each."""
     if values is None:
         return None, n
     if len(values) != n:
         _refuse(f"{name}: one per request is wanted")
-    if n == 0 or min(values) < 0:
+    ints = [_int32(name, v) for v in values]
+    if n == 0 or min(ints) < 0:
         _refuse(f"{name}: no requests, or negative")
-    return (c_int32 * n)(*values), sum(values)
+    return (c_int32 * n)(*ints), sum(ints)
 
 
 def _pool(kv, torch, num_kv_heads, group, device):
@@ -481,25 +507,26 @@ def _append(fn, group, kv, page_table, lens, k, v, rope, q, q_out, new_lens, int
         return
     if st is not None:
         _paged_check(st, "append")
-    torch, device, s = _context(stream)
-    n, hkv, bf16 = len(lens), k.shape[1], torch.bfloat16
-    pool = _pool(kv, torch, hkv, group, device)
+    n, hkv = len(lens), _int32("kv heads", k.shape[1])
     old, _ = _counts(lens, n, "lens")
     new, rows = _counts(new_lens, n, "new_lens")
-    max_pages = page_table.shape[1]
+    max_pages = _int32("page_table's width", page_table.shape[1])
+    torch, device, s = _context(stream)
+    bf16 = torch.bfloat16
+    pool = _pool(kv, torch, hkv, group, device)
     table = _dense("page_table", page_table, torch.int32, (n, max_pages), device)
     kp, ks = _heads("k", k, bf16, rows, hkv, device)
     vp, vs = _heads("v", v, bf16, rows, hkv, device)
     hq, qp, qs, qo, r, err = 0, None, 0, None, None, None
     if q is not None and q_out is not None:
-        hq = q.shape[1]
+        hq = _int32("query heads", q.shape[1])
         qp, qs = _heads("q", q, bf16, rows, hq, device)
         qo = _dense("q_out", q_out, bf16, (rows, hq, HEAD_DIM), device)
     elif q is not q_out:
         _refuse("q and q_out come together")
     if rope is not None:
-        length, dim = rope.shape
-        r = oscar_rope(_dense("rope", rope, torch.float32, None, device), length, dim, interleaved)
+        length, dim = (_int32("rope's shape", x) for x in rope.shape)
+        r = oscar_rope(_dense("rope", rope, torch.float32, None, device), length, dim, 1 if interleaved else 0)
     if error is not None:
         err = _dense("error", error, torch.int32, None, device)
     if rows:
@@ -533,12 +560,12 @@ def int4_read(kv, page_table, starts, counts, k_out, v_out, group_size: int = 12
         return
     if st is not None:
         _paged_check(st, "read")
-    torch, device, s = _context(stream)
-    n, hkv = len(starts), kv.shape[1]
-    pool = _pool(kv, torch, hkv, (group_size,), device)
+    n, hkv = len(starts), _int32("kv heads", kv.shape[1])
     first, _ = _counts(starts, n, "starts")
     count, rows = _counts(counts, n, "counts")
-    max_pages = page_table.shape[1]
+    max_pages = _int32("page_table's width", page_table.shape[1])
+    torch, device, s = _context(stream)
+    pool = _pool(kv, torch, hkv, (group_size,), device)
     table = _dense("page_table", page_table, torch.int32, (n, max_pages), device)
     kind = k_out.dtype
     if kind is not torch.float32 and kind is not torch.bfloat16:
@@ -556,8 +583,10 @@ def int4_read(kv, page_table, starts, counts, k_out, v_out, group_size: int = 12
 
 def attention_workspace(n: int, num_q_heads: int, num_kv_heads: int, q_lens=None, stream=None):
     """Zeroed workspace for window_attention / int4_attention calls of n requests."""
+    n, hq, hkv = _int32("n", n), _int32("num_q_heads", num_q_heads), _int32("num_kv_heads", num_kv_heads)
+    rows, _ = _counts(q_lens, n, "q_lens")
     torch, device, s = _context(stream)
-    need = load().oscar_attention_workspace_bytes(n, _counts(q_lens, n, "q_lens")[0], num_q_heads, num_kv_heads)
+    need = load().oscar_attention_workspace_bytes(n, rows, hq, hkv)
     if need == 0:
         _refuse("arguments outside the supported limits")
     with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device)):
@@ -572,12 +601,14 @@ def _attention(fn, group, kv, page_table, lens, q, out, hkv, window, sinks, q_le
         return workspace
     if st is not None and load().oscar_paged_last_error() != b"workspace too small":
         _paged_check(st, "attention")
-    torch, device, s = _context(stream)
-    n, hq, kind, f32 = len(lens), q.shape[1], out.dtype, torch.float32
-    pool = _pool(kv, torch, hkv, group, device)
+    n, hq, hkv = len(lens), _int32("query heads", q.shape[1]), _int32("num_kv_heads", hkv)
+    window, sinks = _window(window), _int32("sinks", sinks)
     total, _ = _counts(lens, n, "lens")
     new, rows = _counts(q_lens, n, "q_lens")
-    max_pages = page_table.shape[1]
+    max_pages = _int32("page_table's width", page_table.shape[1])
+    torch, device, s = _context(stream)
+    kind, f32 = out.dtype, torch.float32
+    pool = _pool(kv, torch, hkv, group, device)
     table = _dense("page_table", page_table, torch.int32, (n, max_pages), device)
     qp, qs = _heads("q", q, torch.bfloat16, rows, hq, device)
     if kind is not f32 and kind is not torch.bfloat16:
@@ -602,9 +633,10 @@ def _attention(fn, group, kv, page_table, lens, q, out, hkv, window, sinks, q_le
 def window_attention(kv, page_table, lens, q, out, num_kv_heads: int, window: int = -1, sinks: int = 0, q_lens=None,
                      scale: float = 0.0, lse=None, workspace=None, error=None, stream=None):
     """Attention of the last q_lens[i] positions (one each by default) of every request over BF16 pages: the query at
-    position p sees the tokens t <= p with t < sinks or t > p - window (window < 0: no bound).  q bf16 [rows][Hq][128]
-    (rows may be strided), out [rows][Hq][128] fp32 or bf16, lse fp32 [rows][Hq] or None.  Returns the workspace to
-    pass to the next call: a new one where none is given or it is too small (attention_workspace() makes one)."""
+    position p sees the tokens t <= p with t < sinks or t > p - window (window < 0, or beyond 32 bits: no bound).  q
+    bf16 [rows][Hq][128] (rows may be strided), out [rows][Hq][128] fp32 or bf16, lse fp32 [rows][Hq] or None.  Returns
+    the workspace to pass to the next call: a new one where none is given or it is too small (attention_workspace()
+    makes one)."""
     return _attention(load().oscar_window_attention, (), kv, page_table, lens, q, out, num_kv_heads, window, sinks,
                       q_lens, scale, lse, workspace, error, stream)
 

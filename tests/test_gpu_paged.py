@@ -740,3 +740,32 @@ def test_binding_refusals(b):
         b.int4_attention(kv4, table, [20, 20], torch.cat([q] * 9), torch.cat([out] * 9), 2, q_lens=[9, 9])
     with pytest.raises(b.OscarError):
         b.int4_append(kv4, table, [5, 9], k, k, group_size=32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 128])
+def test_ints_beyond_32_bits(b, group):
+    """A window beyond 32 bits is no bound, whichever way the call takes; other such ints are refused and write nothing."""
+    hq, hkv, lens = 4, 1, [100, 70]
+    pool = Pool(b, lens, hkv, group, seed=14)
+    kv, table = pool.device()
+    q = torch.randn(2, hq, D, device="cuda").to(torch.bfloat16)
+    append, attend = (b.int4_append, b.int4_attention) if group else (b.bf16_append, b.window_attention)
+    want, got = torch.empty(2, hq, D, device="cuda"), torch.empty(2, hq, D, device="cuda")
+    ws = attend(kv, table, lens, q, want, hkv)
+    for window in (1 << 40, 2 ** 31, 2 ** 32 + 1, -2 ** 40):
+        for seq, stream in ((lens, None), (np.array(lens), torch.cuda.current_stream())):
+            got.fill_(7)
+            attend(kv, table, seq, q, got, hkv, window, workspace=ws, stream=stream)
+            assert torch.equal(got, want)
+    got.fill_(7)
+    before = kv.clone()
+    k = torch.ones(2, hkv, D, dtype=torch.bfloat16, device="cuda")
+    for far in (2 ** 32 + 3, 2 ** 40 + 64):
+        for change in (dict(lens=[far, 70]), dict(sinks=far), dict(q_lens=[1, far])):
+            with pytest.raises(b.OscarError, match="32 bits"):
+                attend(kv, table, change.pop("lens", lens), q, got, hkv, workspace=ws, **change)
+        for change in (dict(lens=[5, far]), dict(new_lens=[far, 1])):
+            with pytest.raises(b.OscarError, match="32 bits"):
+                append(kv, table, change.pop("lens", [5, 9]), k, k, **change)
+    assert (got == 7).all() and torch.equal(kv.view(torch.uint8), before.view(torch.uint8))

@@ -184,3 +184,74 @@ def test_marshalling_extension_takes_nothing_before_its_setup(b):
     assert mod.attend() is None and mod.append(1) is None and mod.read("x", *[1] * 8) is None
     with pytest.raises(TypeError):
         mod.setup(1, 2, 3)
+
+
+# ---- ints beyond 32 bits, through the public calls --------------------------------
+def tensors():
+    import torch
+    return dict(kv=torch.zeros(4, 2, 2, 64, 128, dtype=torch.bfloat16), table=torch.zeros(2, 2, dtype=torch.int32),
+                q=torch.zeros(2, 4, 128, dtype=torch.bfloat16), out=torch.zeros(2, 4, 128),
+                k=torch.zeros(2, 2, 128, dtype=torch.bfloat16), ws=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+@pytest.fixture
+def on_cpu(b, monkeypatch):
+    """The Python path on CPU tensors, up to the C call."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(b, "_context", lambda stream: (torch, -1, None))
+    return b
+
+
+BEYOND = [2 ** 31, 2 ** 32 + 3, 2 ** 40 + 64]
+
+
+@pytest.mark.parametrize("far", BEYOND)
+@pytest.mark.parametrize("four", [False, True])
+def test_lengths_beyond_32_bits_are_refused(on_cpu, far, four):
+    b, t = on_cpu, tensors()
+    kv = b.int4_pool(4, 2, device="cpu") if four else t["kv"]
+    append = b.int4_append if four else b.bf16_append
+    attend = b.int4_attention if four else b.window_attention
+    for lens in ([far, 5], (5, far), np.array([5, far])):
+        with pytest.raises(b.OscarError, match="32 bits"):
+            append(kv, t["table"], lens, t["k"], t["k"])
+        with pytest.raises(b.OscarError, match="32 bits"):
+            attend(kv, t["table"], lens, t["q"], t["out"], 2, workspace=t["ws"])
+        with pytest.raises(b.OscarError, match="32 bits"):
+            b.int4_read(kv, t["table"], lens, [1, 1], t["k"].float(), t["k"].float())
+    with pytest.raises(b.OscarError, match="32 bits"):
+        append(kv, t["table"], [5, 9], t["k"], t["k"], new_lens=[far, 1])
+    with pytest.raises(b.OscarError, match="32 bits"):
+        attend(kv, t["table"], [5, 9], t["q"], t["out"], 2, q_lens=[1, far], workspace=t["ws"])
+    with pytest.raises(b.OscarError, match="32 bits"):
+        b.int4_read(kv, t["table"], [0, 0], [far, 1], t["k"].float(), t["k"].float())
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_sinks_and_heads_beyond_32_bits_are_refused(on_cpu, four):
+    b, t = on_cpu, tensors()
+    kv = b.int4_pool(4, 2, device="cpu") if four else t["kv"]
+    attend = b.int4_attention if four else b.window_attention
+    for far in BEYOND + [-far for far in BEYOND[1:]]:
+        with pytest.raises(b.OscarError, match="32 bits"):
+            attend(kv, t["table"], [5, 9], t["q"], t["out"], 2, 4, far, workspace=t["ws"])
+        with pytest.raises(b.OscarError, match="32 bits"):
+            attend(kv, t["table"], [5, 9], t["q"], t["out"], far, workspace=t["ws"])
+        for args in ((far, 4, 2), (2, far, 2), (2, 4, far)):
+            with pytest.raises(b.OscarError, match="32 bits"):
+                b.attention_workspace(*args)
+        with pytest.raises(b.OscarError, match="32 bits"):
+            b.attention_workspace(2, 4, 2, q_lens=[1, abs(far)])
+    for odd in (1.5, "4", None):
+        with pytest.raises(b.OscarError, match="int"):
+            attend(kv, t["table"], [5, 9], t["q"], t["out"], 2, odd, workspace=t["ws"])
+
+
+@pytest.mark.parametrize("window,passed", [(2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, -1), (1 << 40, -1), (2 ** 32 + 5, -1),
+                                           (-2 ** 31, -2 ** 31), (-2 ** 40, -1), (np.int64(2 ** 33), -1), (7, 7)])
+def test_a_window_beyond_32_bits_is_no_bound(on_cpu, window, passed):
+    """A window of so many tokens holds every cache, as a negative one does."""
+    b, t, got = on_cpu, tensors(), []
+    b._attention(lambda *a: got.append(a[9]) or 0, (), t["kv"], t["table"], [5, 9], t["q"], t["out"], 2, window, 0,
+                 None, 0.0, None, t["ws"], None, None)
+    assert got == [passed]
