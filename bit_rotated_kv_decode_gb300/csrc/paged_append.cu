@@ -80,7 +80,7 @@ __device__ __forceinline__ int find_req(const PagedRows& r, int n, int row) {
 
 // Page of position pos of request i, -1 (and the error bit) if its id is out of range.
 __device__ __forceinline__ int64_t page_of(const PagedView& p, int i, int pos) {
-  const int32_t page = __ldg(p.table + (size_t)i * p.max_pages + pos / PAGE);
+  const int32_t page = __ldcg(p.table + (size_t)i * p.max_pages + pos / PAGE);
   if (page >= 0 && page < p.num_pages) return page;
   if (p.err) atomicOr(p.err, PAGED_ERR_PAGE);
   return -1;
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(APP_THREADS, GK == 0 ? 1 : 7)
   for (int u = 0; u < 2; ++u)
     if (rot[u]) {
       const float* t = rope.table + (size_t)pos * rope.dim + (INTERLEAVED ? 4 * c[u] : 8 * pc + 4 * u);
-      *reinterpret_cast<float4*>(cs + 4 * u) = __ldg(reinterpret_cast<const float4*>(t));
-      *reinterpret_cast<float4*>(sn + 4 * u) = __ldg(reinterpret_cast<const float4*>(t + rope.dim / 2));
+      *reinterpret_cast<float4*>(cs + 4 * u) = *reinterpret_cast<const float4*>(t);
+      *reinterpret_cast<float4*>(sn + 4 * u) = *reinterpret_cast<const float4*>(t + rope.dim / 2);
     }
   const bool writes_kv = total > hq && head0 + 4 * (APP_ROWS - 1) >= hq;
   const int64_t page = writes_kv ? page_of(p, i, pos) : -1;

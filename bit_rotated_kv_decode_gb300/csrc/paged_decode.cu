@@ -255,7 +255,7 @@ template <int NR>
 __device__ __forceinline__ uint4 load_query(const DecodeArgs& A, int req, int head) {
   const int r = 2 * (threadIdx.x >> 5) + (threadIdx.x >> 4 & 1);
   if (r >= A.m * A.G) return make_uint4(0, 0, 0, 0);
-  return __ldg(reinterpret_cast<const uint4*>(A.a.q + (int64_t)(A.req[req].row + r / A.G) * A.a.q_stride +
+  return __ldcg(reinterpret_cast<const uint4*>(A.a.q + (int64_t)(A.req[req].row + r / A.G) * A.a.q_stride +
                                               (int64_t)(head * A.G + r % A.G) * D) + (threadIdx.x & 15));
 }
 template <int GK, int NR>
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
         const int v = u - c.base;
         if (v < c.un.units) {
           const int t0 = c.un.unit(v) * UT;
-          int32_t page = __ldg(A.p.table + (size_t)A.req[c.req].table * A.p.max_pages + t0 / PAGE);
+          int32_t page = __ldcg(A.p.table + (size_t)A.req[c.req].table * A.p.max_pages + t0 / PAGE);
           if (page < 0 || page >= A.p.num_pages) {
             if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
             page = 0;

@@ -17,7 +17,10 @@ constexpr float NEG_INF = -INFINITY;
 
 // Programmatic dependent launch: a kernel's blocks are scheduled while the grid before it in
 // the stream ends.  It calls grid_dep_wait() before it touches global memory: the grid
-// before (and all before that) is then complete and its writes are visible.
+// before (and all before that) is then complete and its writes are visible -- to ordinary
+// loads.  Inputs (q, page ids, the rotation's table) may thus be written within this kernel's
+// life, where non-coherent loads (__ldg, ld.global.nc) promise nothing: none is used, but
+// __ldcg or plain loads.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... P, typename... A>

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             for (int u = 0; u < 2; ++u) {
               rec[u] = -1;
               if (2 * j + u >= kt.pages) continue;
-              int page = __ldg(pt + kt.base(2 * j + u) / PAGE);
+              int page = __ldcg(pt + kt.base(2 * j + u) / PAGE);
               if (page < 0 || page >= A.p.num_pages) {
                 if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
                 page = 0;

@@ -340,6 +340,8 @@ oscar_status oscar_bf16_decode(const void* kv, int64_t num_pages, const int32_t*
  *               range (a store to it is dropped, a read sees page 0 in an
  *               attention and zeros in oscar_int4_read), bit 2 where a bounded
  *               device wait gave up.  The caller zeroes it.
+ * What the work before a call in its stream writes (q, pages, page table, rotation
+ * table) the call sees, the last launch's writes among it.
  * Calls are asynchronous on "stream", check every argument before the first
  * launch, allocate nothing, and may be captured (the host arrays are read at
  * capture).  The text of the last refusal on the calling thread is

@@ -769,3 +769,53 @@ def test_ints_beyond_32_bits(b, group):
             with pytest.raises(b.OscarError, match="32 bits"):
                 append(kv, table, change.pop("lens", [5, 9]), k, k, **change)
     assert (got == 7).all() and torch.equal(kv.view(torch.uint8), before.view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group,m", [(0, 1), (0, 20), (128, 1), (64, 2)])
+def test_layers_that_share_their_buffers(b, group, m):
+    """Append, then attention, over 30 layers without a wait of the host: one q_out, one page table and one workspace,
+    the table changed by a kernel before each layer.  Every layer has the bits that it has by itself."""
+    hq, hkv, lens, layers = 8, 2, [300, 1000], 30
+    n, new = len(lens), [m] * len(lens)
+    need = [-(-(t + m) // PAGE) for t in lens]
+    pages = sum(need) + 2
+    gen = torch.Generator("cuda").manual_seed(15 + group)
+    append, attend = (b.int4_append, b.int4_attention) if group else (b.bf16_append, b.window_attention)
+    extra = dict(group_size=group) if group else {}
+    tables = torch.full((layers, n, max(need)), -1, dtype=torch.int32, device="cuda")
+    kvs, qkvs = [], []
+    for layer in range(layers):
+        order = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32)
+        tables[layer, 0, :need[0]], tables[layer, 1, :need[1]] = order[:need[0]], order[need[0]:need[0] + need[1]]
+        kv = b.int4_pool(pages, hkv, group) if group else torch.zeros(pages, hkv, 2, PAGE, D, dtype=torch.bfloat16,
+                                                                      device="cuda")
+        old = torch.randn(sum(lens), 2 * hkv, D, device="cuda", generator=gen).to(torch.bfloat16)
+        append(kv, tables[layer], [0, 0], old[:, :hkv], old[:, hkv:], new_lens=lens, **extra)
+        kvs.append(kv)
+        qkvs.append(torch.randn(n * m, hq + 2 * hkv, D, device="cuda", generator=gen).to(torch.bfloat16))
+    rope = b.rope_table(max(lens) + m)
+    now = [t + m for t in lens]
+    ws = b.attention_workspace(n, hq, hkv, new)
+
+    def layer_of(layer, kv, table, q_out, out, lse, workspace):
+        q, k, v = qkvs[layer].split([hq, hkv, hkv], 1)
+        append(kv, table, lens, k, v, rope, q=q, q_out=q_out, new_lens=new, **extra)
+        attend(kv, table, now, q_out, out, hkv, 400, 5, q_lens=new, lse=lse, workspace=workspace, **extra)
+
+    want = torch.empty(layers, n * m, hq, D, device="cuda"), torch.empty(layers, n * m, hq, device="cuda")
+    for layer in range(layers):
+        torch.cuda.synchronize()
+        layer_of(layer, kvs[layer].clone(), tables[layer].clone(), torch.empty(n * m, hq, D, dtype=torch.bfloat16,
+                 device="cuda"), want[0][layer], want[1][layer], torch.zeros_like(ws))
+        torch.cuda.synchronize()
+    table, q_out = torch.empty_like(tables[0]), torch.empty(n * m, hq, D, dtype=torch.bfloat16, device="cuda")
+    got = torch.empty_like(want[0]), torch.empty_like(want[1])
+    for turn in range(3):
+        for x in got:
+            x.fill_(7)
+        for layer in range(layers):
+            torch.add(tables[layer], 0, out=table)
+            layer_of(layer, kvs[layer], table, q_out, got[0][layer], got[1][layer], ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -255,3 +255,20 @@ def test_a_window_beyond_32_bits_is_no_bound(on_cpu, window, passed):
     b._attention(lambda *a: got.append(a[9]) or 0, (), t["kv"], t["table"], [5, 9], t["q"], t["out"], 2, window, 0,
                  None, 0.0, None, t["ws"], None, None)
     assert got == [passed]
+
+
+def test_kernels_that_overlap_the_grid_before_use_no_noncoherent_loads():
+    """They start while the grid before may still write their inputs; ld.global.nc is for memory that nobody writes in
+    a kernel's life."""
+    import os
+    import re
+    from bit_rotated_kv_decode_gb300 import build
+    seen = 0
+    for name in sorted(os.listdir(build.CSRC)):
+        text = open(os.path.join(build.CSRC, name)).read()
+        if not name.startswith("paged") or not name.endswith((".cu", ".cuh")):
+            continue
+        code = re.sub(r"//[^\n]*", "", text)
+        assert "__ldg" not in code and "global.nc" not in code and "__restrict__" not in code, name
+        seen += "launch_dependent(" in code
+    assert seen >= 4
