@@ -14,6 +14,8 @@ namespace oscar {
 
 constexpr int PAGED_MAX_REQ = 256;   // requests per call: their lengths travel in the kernel arguments
 
+constexpr int PAGED_MAX_TOKENS = 1 << 30;   // positions of a request
+
 // error bits of the caller's device word
 constexpr int PAGED_ERR_PAGE = 1;      // a page id out of range
 constexpr int PAGED_ERR_TIMEOUT = 2;   // a bounded device wait gave up

@@ -47,7 +47,9 @@ int64_t fill_rows(const int32_t* pos0, const int32_t* counts, int32_t n, int32_t
   int64_t rows = 0;
   for (int32_t i = 0; i < n; ++i) {
     const int32_t c = counts ? counts[i] : 1;
-    if (pos0[i] < 0 || c < 0 || (int64_t)pos0[i] + c > (int64_t)PAGE * max_pages) return -1;
+    // (positions are 32-bit ints in the kernels)
+    if (pos0[i] < 0 || c < 0 || (int64_t)pos0[i] + c > (int64_t)PAGE * max_pages || (int64_t)pos0[i] + c > PAGED_MAX_TOKENS)
+      return -1;
     r.row0[i] = static_cast<int32_t>(rows);
     r.pos0[i] = pos0[i];
     rows += c;
@@ -81,7 +83,7 @@ oscar_status append(void* pool, int64_t num_pages, const int32_t* table, int32_t
   }
   PagedRows rows;
   const int64_t total = fill_rows(lens, new_lens, n, max_pages, rows);
-  if (total < 0) return bad("lens / new_lens negative or beyond the page table");
+  if (total < 0) return bad("lens / new_lens negative, beyond the page table or 2^30 positions");
   if (rope)
     for (int32_t i = 0; i < n; ++i)
       if ((int64_t)lens[i] + (new_lens ? new_lens[i] : 1) > rope->length) return bad("position beyond the rotation table");
@@ -158,7 +160,7 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
   int64_t rows = 0;
   for (int32_t i = 0; i < n; ++i) {
     const int32_t m = q_lens ? q_lens[i] : 1;
-    if (m < 0 || lens[i] < m || (int64_t)lens[i] > (int64_t)PAGE * max_pages || lens[i] > (1 << 30))
+    if (m < 0 || lens[i] < m || (int64_t)lens[i] > (int64_t)PAGE * max_pages || lens[i] > PAGED_MAX_TOKENS)
       return bad("0 <= q_lens <= lens <= 64 max_pages, and lens at most 2^30");
     if (gk != 0 && m > step) return bad("4-bit attention: at most 16 / (query heads per kv head) query tokens a request");
     rows += m;
@@ -261,7 +263,7 @@ oscar_status oscar_int4_read(const void* kv, int64_t num_pages, const int32_t* p
   if (out_type != OSCAR_F32 && out_type != OSCAR_BF16) return bad("out is fp32 or bf16");
   PagedRows rows;
   const int64_t total = fill_rows(starts, counts, n, max_pages, rows);
-  if (total < 0) return bad("starts / counts negative or beyond the page table");
+  if (total < 0) return bad("starts / counts negative, beyond the page table or 2^30 positions");
   if (total == 0) return OSCAR_OK;
   const PagedView p{const_cast<void*>(kv), page_table, num_pages, max_pages, n, num_kv_heads, error};
   return from_cuda(launch_int4_read(p, rows, group_size, k_out, v_out, out_type == OSCAR_F32,

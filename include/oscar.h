@@ -361,8 +361,8 @@ typedef struct {
 } oscar_rope;
 
 /* Rotate q and k by their positions and append k and v: request i's new_lens[i]
- * tokens go to positions lens[i], lens[i] + 1, ...  k and v device bf16
- * [rows][Hkv][128], q [rows][Hq][128] or NULL, q_out dense bf16 [rows][Hq][128]
+ * tokens go to positions lens[i], lens[i] + 1, ..., below 64 max_pages and 2^30.
+ * k and v device bf16 [rows][Hkv][128], q [rows][Hq][128] or NULL, q_out dense bf16 [rows][Hq][128]
  * (may be q itself if q is dense).  rope NULL: no rotation (q is copied).  No two
  * rows of a call may go to the same place.  Bytes of other tokens are left as
  * they were.

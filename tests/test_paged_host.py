@@ -272,3 +272,21 @@ def test_kernels_that_overlap_the_grid_before_use_no_noncoherent_loads():
         assert "__ldg" not in code and "global.nc" not in code and "__restrict__" not in code, name
         seen += "launch_dependent(" in code
     assert seen >= 4
+
+
+@pytest.mark.parametrize("start,count", [(2 ** 31 - 5, 10), (2 ** 31 - 1, 1), (2 ** 30, 1), (2 ** 30 - 5, 6),
+                                         (0, 2 ** 30 + 1)])
+def test_positions_end_at_2_to_the_30(b, start, count):
+    """Positions are ints in the kernels, and 2^30 tokens are what an attention takes; a table wide enough for more
+    does not let them through."""
+    lib, wide = b.load(), dict(max_pages=1 << 26, lens=ints(start, 0))
+    for group in (None, 128, 64):
+        v = list({**APPEND, **wide, "new": ints(count, 1)}.values())
+        if group:
+            v.insert(9, group)
+        fn = lib.oscar_int4_append if group else lib.oscar_bf16_append
+        assert fn(*v) == b.OSCAR_ERR_INVALID_ARG and b"2^30" in lib.oscar_paged_last_error()
+    read = dict(kv=A, pages=8, table=A, max_pages=1 << 26, starts=ints(start, 0), counts=ints(count, 1), n=2, hkv=2,
+                group=64, k=A, v=A, kind=1, error=None, stream=None)
+    assert lib.oscar_int4_read(*read.values()) == b.OSCAR_ERR_INVALID_ARG
+    assert b"2^30" in lib.oscar_paged_last_error()
