@@ -95,7 +95,10 @@ constexpr int DECODE_MAX_ROWS = 16;   // query rows (tokens x heads of a group) 
 
 // Decode: m * G <= DECODE_MAX_ROWS rows per (request, kv head), the same m for all.
 size_t paged_decode_record_bytes(int segments, int rows, int sms);
-int64_t paged_decode_units(const AttnReq& r, const AttnArgs& a, int gk, int hkv);   // a launch takes up to 2^31 - 1
+// Units that a launch takes at most: a warp's index into them steps by the CTA's warps (up to
+// 12) past the end of its share, and stays an int.
+constexpr int32_t DECODE_MAX_UNITS = INT32_MAX - 64;
+int64_t paged_decode_units(const AttnReq& r, const AttnArgs& a, int gk, int hkv);
 cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, int gk,
                                 void* workspace, const CUtensorMap* map, int sms, cudaStream_t s);
 

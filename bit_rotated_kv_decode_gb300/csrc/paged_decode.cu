@@ -66,6 +66,7 @@ struct DecodeShape {
   static constexpr int FIT = static_cast<int>((LIMIT - FIXED) / (NW * Format<GK>::BYTES));
   static constexpr int STAGES = FIT > 3 ? 3 : FIT;
   static_assert(STAGES >= 2, "a ring needs two stages");
+  static_assert(NW <= INT32_MAX - DECODE_MAX_UNITS, "a step past the last unit is an int");
 };
 
 template <int GK, int NR>
@@ -1024,7 +1025,7 @@ cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, 
     const Units u = Units::of(reqs[i].len, A.m, a.window, a.sinks, ut);
     A.req[i] = {reqs[i].len, reqs[i].row, reqs[i].table, static_cast<int32_t>(total), u};
     total += paged_decode_units(reqs[i], a, gk, p.Hkv);
-    if (total > INT32_MAX) return cudaErrorInvalidValue;
+    if (total > DECODE_MAX_UNITS) return cudaErrorInvalidValue;
   }
   A.total = static_cast<int32_t>(total);
   static const CUtensorMap none = {};

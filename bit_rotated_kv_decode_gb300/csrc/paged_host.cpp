@@ -196,7 +196,7 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
     }
     row += m;
   }
-  if (units > INT32_MAX) return bad("too many visible tokens for one call");
+  if (units > DECODE_MAX_UNITS) return bad("too many visible tokens for one call");
   CUtensorMap kv_map, q_map;
   if (count) {
     if (!pool_map(&kv_map, pool, num_pages * hkv, PAGE, 1) ||

@@ -290,3 +290,13 @@ def test_positions_end_at_2_to_the_30(b, start, count):
                 group=64, k=A, v=A, kind=1, error=None, stream=None)
     assert lib.oscar_int4_read(*read.values()) == b.OSCAR_ERR_INVALID_ARG
     assert b"2^30" in lib.oscar_paged_last_error()
+
+
+@pytest.mark.parametrize("short", [1, 5, 11, 63])
+def test_visible_units_leave_room_for_a_warps_step(b, short):
+    """A warp steps through the units by the warps of its CTA, so the last ones must not come within a step of 2^31."""
+    lens = [1 << 30] * 31 + [(1 << 30) - 16 * short]            # 2^31 - short units of 16 tokens
+    v = {**ATTEND, "hq": 1, "hkv": 1, "qs": 128, "n": 32, "max_pages": 1 << 24, "lens": ints(*lens), "q_lens": None,
+         "window": -1}
+    assert b.load().oscar_window_attention(*v.values()) == b.OSCAR_ERR_INVALID_ARG
+    assert b"visible tokens" in b.load().oscar_paged_last_error()
