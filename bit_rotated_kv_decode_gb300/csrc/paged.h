@@ -15,6 +15,10 @@ namespace oscar {
 constexpr int PAGED_MAX_REQ = 256;   // requests per call: their lengths travel in the kernel arguments
 
 constexpr int PAGED_MAX_TOKENS = 1 << 30;   // positions of a request
+// A token behind every position; the bounds of what a row sees, taken from it, are ints (the
+// first row's window begins at 1 - PAGED_MAX_TOKENS).
+constexpr int PAGED_NO_TOKEN = PAGED_MAX_TOKENS;
+static_assert(1 - (int64_t)PAGED_MAX_TOKENS - PAGED_NO_TOKEN >= INT32_MIN, "a window's begin less a token is an int");
 
 // error bits of the caller's device word
 constexpr int PAGED_ERR_PAGE = 1;      // a page id out of range
@@ -78,7 +82,7 @@ struct AttnArgs {
   float* lse;             // or null
   int32_t f32;            // out type
   int32_t Hq;
-  int32_t window;         // 2^30 and more: no bound
+  int32_t window;         // PAGED_MAX_TOKENS: no bound
   int32_t sinks;
   float scale2;           // softmax scale x log2(e)
 };

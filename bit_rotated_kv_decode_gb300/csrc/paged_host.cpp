@@ -176,7 +176,7 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
   a.lse = lse;
   a.f32 = out_type == OSCAR_F32;
   a.Hq = hq;
-  a.window = window < 0 || window > (1 << 30) ? (1 << 30) + (1 << 29) : window;
+  a.window = window < 0 || window > PAGED_MAX_TOKENS ? PAGED_MAX_TOKENS : window;
   a.sinks = sinks;
   a.scale2 = (scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(D))) * 1.4426950408889634f;
   if (!std::isfinite(a.scale2)) return bad("scale too large");

@@ -102,7 +102,7 @@ struct KeyTiles {
     return k;
   }
   // first token of page v of the list; behind its end, tokens that no row sees
-  __device__ int base(int v) const { return v >= pages ? 1 << 30 : (v < sink ? v : first + (v - sink)) * PAGE; }
+  __device__ int base(int v) const { return v >= pages ? PAGED_NO_TOKEN : (v < sink ? v : first + (v - sink)) * PAGE; }
   // whether some row sees token t; all of page v of the list
   __device__ bool any(int t) const { return t <= pmax && (t < sinks || t >= lo); }
   __device__ bool all(int v) const {
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         float* x = reinterpret_cast<float*>(xr);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int v = 2 * j + u, t0 = v >= pages ? 1 << 30 : (v < sink ? v : v + skip) * PAGE;
+          const int v = 2 * j + u, t0 = v >= pages ? PAGED_NO_TOKEN : (v < sink ? v : v + skip) * PAGE;
           if (!(t0 <= all_to && (t0 <= all_sinks || t0 > all_from))) {
             // (bits first: comparing every key took 1500 cycles a page)
             const uint64_t see = visible_bits(pos - t0, lo0 - t0, A.a.sinks - t0);
