@@ -278,24 +278,25 @@ __device__ __forceinline__ void put_query(const DecodeArgs& A, uint4 w, DecodeSm
     float f[8] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                   __uint_as_float(w.y & 0xffff0000u), __uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u),
                   __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u)};
-    float mx = 0.0f, sum = 0.0f;
+    float mx = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    // exponent of the largest, from its bits; not below -112, so that both powers of two are normal
+    const int ex = max(-112, static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - ex) << 23);
+    // (the sum of the scaled channels: that of the channels themselves can overflow)
+    float sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      mx = fmaxf(mx, fabsf(f[e]));
+      f[e] *= up;
       sum += f[e];
     }
 #pragma unroll
-    for (int off = 1; off < 16; off <<= 1) {
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      if (GK == 128 || off < 8) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    }
-    // exponent of the largest, from its bits; clamped so that both powers of two are normal
-    int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
-    ex = max(-112, min(ex, 112));
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - ex) << 23);
+    for (int off = 1; off < (GK == 128 ? 16 : 8); off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     // the 8 channels are one code word's: codes 2 sub, 2 sub + 1 and those 4 behind
-    const uint4 o = make_uint4(f16x2(f[0] * up, f[4] * up), f16x2(f[1] * up, f[5] * up), f16x2(f[2] * up, f[6] * up),
-                               f16x2(f[3] * up, f[7] * up));
+    const uint4 o = make_uint4(f16x2(f[0], f[4]), f16x2(f[1], f[5]), f16x2(f[2], f[6]), f16x2(f[3], f[7]));
     const int tid = GK == 128 ? part / 4 : (part % 8) / 2, word = GK == 128 ? part % 4 : 2 * (part / 8) + part % 2;
     if constexpr (C::DUP)
       *reinterpret_cast<uint4*>(&sm.q[0][2 * r][tid][4 * word]) =
@@ -305,7 +306,7 @@ __device__ __forceinline__ void put_query(const DecodeArgs& A, uint4 w, DecodeSm
     if (part % 8 == 0) {
       // (not 0: it multiplies the -infinity of masked logits)
       sm.q_scale[r] = fmaxf(__uint_as_float(static_cast<uint32_t>(127 + ex - 13) << 23) * A.a.scale2, 1.2e-38f);
-      sm.q_sum[part / 8][r] = sum * up;   // in the operand's scale
+      sm.q_sum[part / 8][r] = sum;   // in the operand's scale
     }
   }
 }

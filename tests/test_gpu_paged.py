@@ -819,3 +819,35 @@ def test_layers_that_share_their_buffers(b, group, m):
             layer_of(layer, kvs[layer], table, q_out, got[0][layer], got[1][layer], ws)
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group,power", [(group, power) for group in (0, 128, 64) for power in (90, 115, 118, -60, -100)]
+                         + [(group, power) for group in (128, 64) for power in (111, 113, 122, 124)])
+def test_queries_of_any_size(b, group, power):
+    """Queries times 2^power under a scale divided by it: every product is the same but for its exponent, so the outputs
+    have the same bits.  (With BF16 pages q . k itself has to be finite in fp32; in 4 bits it carries its exponent
+    apart.)"""
+    hq, hkv, lens = 8, 2, [100, 700, 64]
+    pool = Pool(b, lens, hkv, group, seed=16)
+    pool.hide([1] * 3, 300, 3)
+    kv, table = pool.device()
+    x = np.clip(np.random.default_rng(16).standard_normal((3, hq, D)), -4, 4).astype(np.float32)
+    call = b.int4_attention if group else b.window_attention
+    extra = dict(group_size=group) if group else {}
+    got = []
+    for p in (0, power):
+        y = np.ldexp(paged.bf16_values(paged.bf16_bits(x)), p)
+        assert np.isfinite(y).all() and (power > 0 or np.abs(y[y != 0]).min() > 2.0 ** -126)
+        largest = max((np.abs(y[i].astype(np.float64)).max(0) * np.abs(pool.k[i]).max((0, 1))).sum() for i in range(3))
+        assert group or largest < np.finfo(np.float32).max      # (no partial sum of any q . k is larger)
+        out, lse = torch.empty(3, hq, D, device="cuda"), torch.empty(3, hq, device="cuda")
+        call(kv, table, lens, bf16(paged.bf16_bits(y)), out, hkv, 300, 3, scale=math.ldexp(0.0625, -p), lse=lse, **extra)
+        got.append((out, lse))
+    # scale x log2(e), which the kernels take, is 1.44 2^(-4 - power): exact for power <= 122.  Below 2^-126 it is
+    # subnormal, in steps of 2^-149: at power 124 within 2^-150 / (1.44 2^-128) < 2^-22 of itself, which the logits'
+    # tolerance holds eight times.
+    if power <= 122:
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    for out, lse in got:
+        check_attention(pool, paged.bf16_bits(x), [1] * 3, 300, 3, out, lse, 0.0625)
