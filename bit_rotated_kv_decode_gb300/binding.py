@@ -14,7 +14,7 @@ from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uin
 
 import numpy as np
 
-from .build import CALLS, LIB
+from .build import LIB, calls_path
 
 OSCAR_OK = 0
 OSCAR_ERR_INVALID_ARG = 1
@@ -388,20 +388,27 @@ def _paged_check(st: int, what: str) -> None:
 # These calls are made for every layer of a decode step, so they are marshalled in C++
 # (csrc/calls.cpp).  What that does not take as it is -- a tensor that fails a check, no
 # workspace yet, a stream of its own, lengths that are no list of ints -- goes the same way
-# in Python below, which says what is wrong.
+# in Python below, which says what is wrong; so does every call where the extension has not
+# been built for this torch.
 _torch = None
 _calls = None
+
+
+class _NotBuilt:
+    """Takes no call, as the extension where it leaves one to Python."""
+    append = read = attend = staticmethod(lambda *args: None)
 
 
 def calls():
     """The extension that marshals the paged calls (loaded once; raises if it has not been built)."""
     global _calls
-    if _calls is None:
+    if _calls is None or _calls is _NotBuilt:
         import importlib.machinery
         import importlib.util
-        if not os.path.exists(CALLS):
-            raise RuntimeError(f"extension {CALLS} is missing: run bit_rotated_kv_decode_gb300.build.build()")
-        loader = importlib.machinery.ExtensionFileLoader("_oscar_calls", CALLS)
+        path = calls_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"extension {path} is missing: run bit_rotated_kv_decode_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_oscar_calls", path)
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_oscar_calls", loader))
         loader.exec_module(mod)
         lib = load()
@@ -409,6 +416,14 @@ def calls():
             lib.oscar_bf16_append, lib.oscar_int4_append, lib.oscar_int4_read, lib.oscar_window_attention,
             lib.oscar_int4_attention)))
         _calls = mod
+    return _calls
+
+
+def _marshal():
+    global _calls
+    if os.path.exists(calls_path()):
+        return calls()
+    _calls = _NotBuilt
     return _calls
 
 
@@ -501,7 +516,7 @@ def _pool(kv, torch, num_kv_heads, group, device):
 
 
 def _append(fn, group, kv, page_table, lens, k, v, rope, q, q_out, new_lens, interleaved, error, stream):
-    st = (_calls or calls()).append(group[0] if group else 0, kv, page_table, lens, k, v, rope, q, q_out, new_lens,
+    st = (_calls or _marshal()).append(group[0] if group else 0, kv, page_table, lens, k, v, rope, q, q_out, new_lens,
                                     interleaved, error, stream)
     if st == 0:
         return
@@ -555,7 +570,7 @@ def int4_append(kv, page_table, lens, k, v, rope=None, q=None, q_out=None, new_l
 def int4_read(kv, page_table, starts, counts, k_out, v_out, group_size: int = 128, error=None, stream=None) -> None:
     """The values of tokens [starts[i], starts[i] + counts[i]) of each request of a 4-bit pool, into k_out and v_out
     [rows][Hkv][128], fp32 or bf16."""
-    st = (_calls or calls()).read(group_size, kv, page_table, starts, counts, k_out, v_out, error, stream)
+    st = (_calls or _marshal()).read(group_size, kv, page_table, starts, counts, k_out, v_out, error, stream)
     if st == 0:
         return
     if st is not None:
@@ -595,7 +610,7 @@ def attention_workspace(n: int, num_q_heads: int, num_kv_heads: int, q_lens=None
 
 def _attention(fn, group, kv, page_table, lens, q, out, hkv, window, sinks, q_lens, scale, lse, workspace, error,
                stream):
-    st = (_calls or calls()).attend(group[0] if group else 0, kv, page_table, lens, q, out, hkv, window, sinks, q_lens,
+    st = (_calls or _marshal()).attend(group[0] if group else 0, kv, page_table, lens, q, out, hkv, window, sinks, q_lens,
                                     scale, lse, workspace, error, stream)
     if st == 0:
         return workspace

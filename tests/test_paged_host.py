@@ -300,3 +300,62 @@ def test_visible_units_leave_room_for_a_warps_step(b, short):
          "window": -1}
     assert b.load().oscar_window_attention(*v.values()) == b.OSCAR_ERR_INVALID_ARG
     assert b"visible tokens" in b.load().oscar_paged_last_error()
+
+
+# ---- the build ---------------------------------------------------------------------
+@pytest.fixture
+def small_build(monkeypatch, tmp_path):
+    """A build of the host file alone, in a folder of its own."""
+    from bit_rotated_kv_decode_gb300 import build
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "obj"))
+    monkeypatch.setattr(build, "LIBDIR", str(tmp_path / "lib"))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "lib" / "lib.so"))
+    monkeypatch.setattr(build, "SOURCES", ["host.cpp"])
+    return build, tmp_path
+
+
+def test_the_library_builds_without_torch(small_build, monkeypatch, capfd):
+    import importlib.util
+    build, tmp = small_build
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    assert build.build() == str(tmp / "lib" / "lib.so")
+    assert [p.name for p in (tmp / "lib").iterdir()] == ["lib.so"]
+    assert "torch" in capfd.readouterr().err
+
+
+def test_the_library_is_there_though_the_extension_does_not_compile(small_build, monkeypatch):
+    build, tmp = small_build
+    monkeypatch.setattr(build, "_extension", lambda nvcc: (["false"], None))
+    with pytest.raises(RuntimeError, match="build failed"):
+        build.build()
+    assert (tmp / "lib" / "lib.so").exists()
+
+
+def test_another_torch_or_interpreter_takes_another_extension(monkeypatch):
+    """It reads tensors by torch's own layout: one built for another version must not be loaded."""
+    import importlib.metadata
+    import sysconfig
+    from bit_rotated_kv_decode_gb300 import build
+    paths = {build.calls_path()}
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "9.9.9+x")
+    paths.add(build.calls_path())
+    config = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else config(name))
+    paths.add(build.calls_path())
+    assert len(paths) == 3 and all(p.startswith(build.LIBDIR) and p.endswith(".so") for p in paths)
+
+
+def test_calls_are_marshalled_in_python_without_the_extension(on_cpu, monkeypatch):
+    b, t, got = on_cpu, tensors(), []
+    monkeypatch.setattr(b, "_calls", None)
+    monkeypatch.setattr(b, "calls_path", lambda: "/nonexistent/_oscar_calls.so")
+    with pytest.raises(RuntimeError, match="missing"):
+        b.calls()
+    b._attention(lambda *a: got.append(a) or 0, (), t["kv"], t["table"], [5, 9], t["q"], t["out"], 2, 7, 0, None, 0.0,
+                 None, t["ws"], None, None)
+    b._append(lambda *a: got.append(a) or 0, (), t["kv"], t["table"], [5, 9], t["k"], t["k"], None, None, None, None,
+              False, None, None)
+    assert len(got) == 2
+    with pytest.raises(b.OscarError):
+        b.int4_read(b.int4_pool(4, 2, device="cpu"), t["table"], [0, 0], [1], t["k"], t["k"])
