@@ -12,6 +12,7 @@ import concurrent.futures as cf
 import importlib.metadata
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -80,6 +81,22 @@ def _extension(nvcc: str):
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], None
 
 
+# Kernels that split their registers at run time (setmaxnreg) count on what they are launched
+# with: a file, a pattern of the kernels' names, how many of them, and the registers.
+REGISTERS = {"paged_prefill.cu": (r"paged_prefill_kernelI", 4, 168)}
+
+
+def check_registers(src: str, log: str) -> None:
+    """Checks a file's kernels in what ptxas -v says."""
+    if src not in REGISTERS:
+        return
+    pattern, count, want = REGISTERS[src]
+    used = [int(n) for name, n in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, re.S)
+            if re.search(pattern, name)]
+    if used != [want] * count:
+        raise RuntimeError(f"build failed: {src}: {count} kernels of {want} registers are wanted, the compiler has {used}")
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -92,8 +109,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
         if force or _stale(obj, [path] + headers):
-            extra = ["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []
-            jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", path, "-o", obj])
+            extra = ["-Xptxas", "-v"] if src.endswith(".cu") else []
+            jobs.append((src, obj, [nvcc, *ARCH, *FLAGS, *extra, "-c", path, "-o", obj]))
 
     extension, why = _extension(nvcc)
     if why:
@@ -107,9 +124,19 @@ def build(verbose: bool = False, force: bool = False) -> str:
             raise RuntimeError("build failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         return r.stdout + r.stderr
 
+    def compiled(job):
+        src, obj, cmd = job
+        out = run(cmd)
+        try:
+            check_registers(src, out)
+        except RuntimeError:
+            os.remove(obj)
+            raise
+        return out
+
     with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
         late = ex.submit(run, extension) if extension else None
-        for out in ex.map(run, jobs):
+        for out in ex.map(compiled, jobs):
             if verbose and out:
                 print(out)
     if force or jobs or _stale(LIB, objs):

@@ -847,7 +847,7 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 32 || !(done[which].load() & (1u << dev))) {
-    cudaFuncAttributes attr;   // the build has the registers that the split counts on
+    cudaFuncAttributes attr;   // the registers that the split counts on (the build checks them too)
     e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
     if (attr.numRegs != PF_REGS) return cudaErrorInvalidKernelImage;

@@ -359,3 +359,29 @@ def test_calls_are_marshalled_in_python_without_the_extension(on_cpu, monkeypatc
     assert len(got) == 2
     with pytest.raises(b.OscarError):
         b.int4_read(b.int4_pool(4, 2, device="cpu"), t["table"], [0, 0], [1], t["k"], t["k"])
+
+
+def test_the_build_checks_the_registers_that_the_prefill_counts_on():
+    from bit_rotated_kv_decode_gb300 import build
+    def log(*kernels):
+        return "".join(f"ptxas info    : Compiling entry function '{name}' for 'sm_103a'\nptxas info    : Function "
+                       f"properties for {name}\n    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads\n"
+                       f"ptxas info    : Used {regs} registers, used 2 barriers\n" for name, regs in kernels)
+    name, fold = "_ZN5oscar20paged_prefill_kernelILb%dELb%dEEEv", "_ZN5oscar25paged_prefill_fold_kernelEv"
+    four = [(name % (i, j), 168) for i in range(2) for j in range(2)]
+    source = open(build.os.path.join(build.CSRC, "paged_prefill.cu")).read()
+    assert "PF_REGS = 168," in source and build.REGISTERS["paged_prefill.cu"][2] == 168
+    build.check_registers("paged_prefill.cu", log(*four, (fold, 40)))
+    build.check_registers("paged_append.cu", log((fold, 40)))
+    for bad in (four[:3], four[:3] + [(four[3][0], 160)], []):
+        with pytest.raises(RuntimeError, match="168 registers"):
+            build.check_registers("paged_prefill.cu", log(*bad, (fold, 40)))
+
+
+def test_the_build_rejects_an_object_of_other_registers(small_build, monkeypatch):
+    build, tmp = small_build
+    monkeypatch.setattr(build, "check_registers", lambda src, out: (_ for _ in ()).throw(RuntimeError("registers")))
+    for _ in range(2):                                  # no object is left that a second build would take
+        with pytest.raises(RuntimeError, match="registers"):
+            build.build()
+        assert not (tmp / "lib" / "lib.so").exists()
