@@ -851,3 +851,103 @@ def test_queries_of_any_size(b, group, power):
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     for out, lse in got:
         check_attention(pool, paged.bf16_bits(x), [1] * 3, 300, 3, out, lse, 0.0625)
+
+
+# ---- one key at a time ----------------------------------------------------------------
+PEAKED = [
+    # len, query tokens, window, sinks
+    (700, 700, -1, 0),
+    (700, 500, 130, 70),
+    (600, 600, 64, 3),
+    (523, 301, 200, 0),
+    (2500, 70, -1, 0),        # few rows on many keys: split
+    (1500, 130, 65, 129),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (2, 2), (8, 1), (8, 2)])
+@pytest.mark.parametrize("t,m,window,sinks", PEAKED)
+def test_prefill_of_rows_that_look_at_one_key(b, out_type, hq, hkv, t, m, window, sinks):
+    """Every query is a multiple of one key that it sees, which holds all but 1e-9 of its weight; the keys are taken in
+    turn, those at the window's, the sinks' and the causal edge more often.  A value row that is dropped, doubled or
+    taken from another place in either form's product moves an output by its whole size."""
+    g, rng = hq // hkv, np.random.default_rng(17)
+    k = np.clip(rng.standard_normal((t, hkv, D)), -3, 3).astype(np.float32)
+    v = rng.standard_normal((t, hkv, D)).astype(np.float32)
+    kb, vb = paged.bf16_bits(k), paged.bf16_bits(v)
+    kf, vf = paged.bf16_values(kb).astype(np.float64), paged.bf16_values(vb).astype(np.float64)
+    pages = -(-t // PAGE)
+    table = rng.permutation(pages + 2)[:pages].astype(np.int32)[None]
+    host = np.full((pages + 2, hkv, 2, PAGE, D), 0x7FC0, np.uint16)
+    for t0 in range(0, t, PAGE):
+        n = min(PAGE, t - t0)
+        host[table[0, t0 // PAGE], :, 0, :n] = kb[t0:t0 + n].transpose(1, 0, 2)
+        host[table[0, t0 // PAGE], :, 1, :n] = vb[t0:t0 + n].transpose(1, 0, 2)
+    q, aim = np.zeros((m, hq, D), np.float32), np.zeros((m, hq), int)
+    see = np.zeros((m, t), bool)
+    for r in range(m):
+        s = paged.seen(t - m + r, window, sinks)
+        see[r, s] = True
+        edge = [s[0], s[-1], s[np.searchsorted(s, sinks) % len(s)], s[len(s) // 2]]
+        for h in range(hq):
+            aim[r, h] = edge[(r // 3) % 4] if (r + h) % 3 == 0 else s[(5 * r + 31 * h) % len(s)]
+            q[r, h] = 4 * kf[aim[r, h], h // g] / np.linalg.norm(kf[aim[r, h], h // g]) * math.sqrt(D)
+    qb = paged.bf16_bits(q)
+    out = torch.empty(m, hq, D, device="cuda", dtype=torch.bfloat16 if out_type == "bf16" else torch.float32)
+    lse = torch.empty(m, hq, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    b.window_attention(bf16(host), torch.from_numpy(table).cuda(), [t], bf16(qb), out, hkv, window, sinks, q_lens=[m],
+                       lse=lse, error=err)
+    got, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert err.item() == 0
+    qf = paged.bf16_values(qb).astype(np.float64)
+    for h in range(hq):
+        x = np.where(see, qf[:, h] @ kf[:, h // g].T / math.sqrt(D), -np.inf)
+        top = x.max(1, keepdims=True)
+        p = np.exp(x - top)
+        total = p.sum(1, keepdims=True)
+        assert (p[np.arange(m), aim[:, h]] > (1 - 1e-9) * total[:, 0]).all()
+        want, mag = (p / total) @ vf[:, h // g], (p / total) @ np.abs(vf[:, h // g])
+        logit = (np.where(see, np.abs(qf[:, h]) @ np.abs(kf[:, h // g]).T, 0).max(1) / math.sqrt(D))[:, None]
+        tol = tolerance(want, mag, logit, see.sum(1)[:, None], 0, out_type == "bf16" and m * g > 16, out_type == "bf16")
+        assert (np.abs(got[:, h] - want) <= tol).all(), h
+        n = see.sum(1)
+        assert (np.abs(lse[:, h] - (top + np.log(total))[:, 0])
+                <= 2 * 8 * 2.0 ** -22 * logit[:, 0] + 2.0 ** -20 + 2.0 ** -22 * (n / 16 + 64)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (2, 2), (8, 1)])
+@pytest.mark.parametrize("lens,q_lens,window,sinks", [([700, 65, 333], [90, 2, 1], 128, 64), ([900, 300, 257], [1, 40, 2], -1, 0)])
+def test_short_requests_beside_a_prompt(b, hq, hkv, lens, q_lens, window, sinks):
+    """bf16 outputs: weights of one bf16 part only where a request has more than 16 rows a kv head."""
+    run_attention(b, Pool(b, lens, hkv, seed=18), q_lens, hq, window, sinks, torch.bfloat16,
+                  one_part=lambda m: m * (hq // hkv) > 16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [128, 64])
+@pytest.mark.parametrize("hq", [8, 16, 32])
+def test_long_shares_in_4_bits(b, group, hq):
+    """As test_long_shares: 625 pages a segment, so that a warp (of 8 at least) sums up to 79 of them at once."""
+    n, hkv, top = 84, 2, 40000
+    m = 2 if hq == 32 else 1                                  # 4, 8 and 16 rows
+    hq = 16 if hq == 32 else hq
+    pool = Pool(b, [top], hkv, group, seed=13)
+    lens = [top - 61 * i for i in range(n)]
+    kv, table = pool.device()
+    bits = paged.bf16_bits(np.random.default_rng(13).standard_normal((n * m, hq, D)).astype(np.float32))
+    out, lse = torch.empty(n * m, hq, D, device="cuda"), torch.empty(n * m, hq, device="cuda")
+    b.int4_attention(kv, table.expand(n, -1).contiguous(), lens, bf16(bits), out, hkv, q_lens=[m] * n, group_size=group,
+                     lse=lse)
+    qf, out, lse = paged.bf16_values(bits).astype(np.float64), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for i in (0, 1, 40, 83):
+        for h in (0, hq - 1):
+            row, kh = i * m + m - 1, h // (hq // hkv)
+            want, ls, mag, logit = paged.attend(qf[row, h], pool.k[0][:, kh], pool.v[0][:, kh], lens[i] - 1, -1, 0,
+                                                1 / math.sqrt(D), pool.kmag[0][:, kh], pool.vmag[0][:, kh])
+            tol = tolerance(want, mag, logit, 79 * PAGE, group, False, False)
+            assert (np.abs(out[row, h] - want) <= tol).all()
+            assert abs(lse[row, h] - ls) <= 2 * 8 * 2.0 ** -22 * logit + 2.0 ** -20 + 2.0 ** -22 * (79 * 4 + 64)
