@@ -80,7 +80,7 @@ __device__ __forceinline__ int find_req(const PagedRows& r, int n, int row) {
 
 // Page of position pos of request i, -1 (and the error bit) if its id is out of range.
 __device__ __forceinline__ int64_t page_of(const PagedView& p, int i, int pos) {
-  const int32_t page = __ldcg(p.table + (size_t)i * p.max_pages + pos / PAGE);
+  const int32_t page = p.table[(size_t)i * p.max_pages + pos / PAGE];
   if (page >= 0 && page < p.num_pages) return page;
   if (p.err) atomicOr(p.err, PAGED_ERR_PAGE);
   return -1;
@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(APP_THREADS, GK == 0 ? 1 : 7)
 }
 
 // ---- 4-bit read-back: one thread per word of 8 key codes and that of the values --
-// Bound by its stores: K and V of 16K tokens of 8 heads as fp32 in 23.5 us (6.5 TB/s).
+// Bound by its stores: K and V of 16K tokens of 8 heads as fp32 in 24.7 us (6.2 TB/s), as
+// bf16 in 17.1 us (5.0 TB/s: half the bytes for the same loads and look-ups).
 constexpr int READ_THREADS = 256;
 
 // The 8 values s c + z of a word.  s c is exact in fp32 (11 + 4 bits), so a value is rounded

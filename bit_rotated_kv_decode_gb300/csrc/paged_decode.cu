@@ -34,10 +34,12 @@
 // The probabilities come out of the first product with a lane holding two tokens
 // of a row; movmatrix turns them into the second product's operand.
 //
-// Measured, GQA 4 unless noted: BF16, 32 requests with an 8K window 164 us (0.99 of the
-// copy's rate), one of 100K 67 us (0.92), the smallest call 6 us.  4 bits, 32 of 16K to
-// 64K 238 us (0.90; 59 % of the issue slots, 1080 instructions a page); one of 100K at
-// GQA 8 35 us, of 30K 14 us: instructions, and 6 us to start and to fold.
+// Measured, GQA 4 unless noted: BF16, 32 requests with an 8K window 165 us (0.98 of the
+// copy's rate), one of 100K 67 us (0.92), 16 rows (GQA 8, two query tokens) 20 of 60K 712 us
+// (the copy's rate), the smallest call 6 us.  4 bits, 32 of 16K to 64K 238 us (0.90; 59 % of
+// the issue slots, 1080 instructions a page), 316 us at 8 rows and 551 us at 16; one of 100K
+// at GQA 8 and group 64 35 us, of 30K 14 us: instructions and latency, neither the issue
+// slots nor DRAM full, and 6 us to start and to fold.
 #include <atomic>
 
 #include "paged_device.cuh"
@@ -256,7 +258,7 @@ template <int NR>
 __device__ __forceinline__ uint4 load_query(const DecodeArgs& A, int req, int head) {
   const int r = 2 * (threadIdx.x >> 5) + (threadIdx.x >> 4 & 1);
   if (r >= A.m * A.G) return make_uint4(0, 0, 0, 0);
-  return __ldcg(reinterpret_cast<const uint4*>(A.a.q + (int64_t)(A.req[req].row + r / A.G) * A.a.q_stride +
+  return *(reinterpret_cast<const uint4*>(A.a.q + (int64_t)(A.req[req].row + r / A.G) * A.a.q_stride +
                                               (int64_t)(head * A.G + r % A.G) * D) + (threadIdx.x & 15));
 }
 template <int GK, int NR>
@@ -798,7 +800,7 @@ __global__ void __launch_bounds__(DecodeShape<GK, NR>::THREADS, 1)
         const int v = u - c.base;
         if (v < c.un.units) {
           const int t0 = c.un.unit(v) * UT;
-          int32_t page = __ldcg(A.p.table + (size_t)A.req[c.req].table * A.p.max_pages + t0 / PAGE);
+          int32_t page = A.p.table[(size_t)A.req[c.req].table * A.p.max_pages + t0 / PAGE];
           if (page < 0 || page >= A.p.num_pages) {
             if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
             page = 0;

@@ -20,7 +20,8 @@ constexpr float NEG_INF = -INFINITY;
 // before (and all before that) is then complete and its writes are visible -- to ordinary
 // loads.  Inputs (q, page ids, the rotation's table) may thus be written within this kernel's
 // life, where non-coherent loads (__ldg, ld.global.nc) promise nothing: none is used, but
-// __ldcg or plain loads.
+// plain ones, as fast (through the L2, by __ldcg, the threads of a row look their page up
+// sixteen times: 4-bit read-back as bf16 20.0 against 17.1 us).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... P, typename... A>

@@ -17,9 +17,9 @@
 // fp32 outputs take one query tile a CTA, and the second's columns keep the tensor core's
 // accumulation, which truncates, from showing: the small parts' products go to a sum of
 // their own (in O's they would add 16 truncations a key tile to 8), and every four key tiles
-// O's sum is added to a total, by fp32 additions (900 queries on 16K keys: error 1.1e-6 and
-// 985 us, 1.9e-5 and 920 without the total, plain fp32 2.6e-6).  P is then handed over 64
-// keys at a time, in the columns that S leaves.
+// O's sum is added to a total, by fp32 additions (900 queries of 64 heads on 16K keys of 8:
+// error 1.1e-6 and 985 to 1012 us, 1.9e-5 and 920 without the total, plain fp32 2.6e-6; the
+// floor is 241 us).  P is then handed over 64 keys at a time, in the columns that S leaves.
 //
 // Roles: warps 0-3 and 4-7 the softmax of query tile 0 and 1, one thread per row (TMEM
 // lane = row); warps 8 and 9 the products of query tile 0 and 1; warp 10 the TMA copies;
@@ -40,10 +40,11 @@
 // would leave most SMs idle (a few query tokens on a long cache) an item's key tiles are
 // split, its unnormalised rows go to the workspace and a second kernel folds them.
 //
-// Bound by the tensor core: 16K tokens, GQA 4, window 4096: 536 us, 1.8 PFLOP/s, the
-// tensor pipe 80 % busy (a key tile of both query tiles takes 2310 cycles, its products
-// 2048).  Ragged, GQA 8, window 1024: 214 us and 66 %, since a quarter of an item's time
-// is its ends.
+// Bound by the tensor core: 16K tokens, GQA 4, window 4096: 602 us a call in a loop of
+// seconds (1.6 PFLOP/s; at the power cap, SM clock 1657 MHz), 540 us in one of a few ms (1.8
+// PFLOP/s), the tensor pipe 80 % busy (a key tile of both query tiles takes 2310 cycles, its
+// products 2048).  Ragged, GQA 8, window 1024: 229 us (1927 MHz) and 218 us, 66 %, since a
+// quarter of an item's time is its ends.
 #include <atomic>
 
 #include "paged_device.cuh"
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             for (int u = 0; u < 2; ++u) {
               rec[u] = -1;
               if (2 * j + u >= kt.pages) continue;
-              int page = __ldcg(pt + kt.base(2 * j + u) / PAGE);
+              int page = pt[kt.base(2 * j + u) / PAGE];
               if (page < 0 || page >= A.p.num_pages) {
                 if (A.p.err) atomicOr(A.p.err, PAGED_ERR_PAGE);
                 page = 0;
