@@ -29,12 +29,14 @@ oscar_status from_cuda(cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 // Checks shared by every call; null if they hold.
 const char* check_pages(const void* pool, int64_t num_pages, const int32_t* table, int32_t max_pages, int32_t n,
-                        int32_t hkv) {
+                        int32_t hkv, const int32_t* error) {
   if (!pool || !aligned16(pool)) return "null or misaligned page pool";
-  if (!table || (reinterpret_cast<uintptr_t>(table) & 3)) return "null or misaligned page table";
+  if (!table || !aligned4(table)) return "null or misaligned page table";
+  if (!aligned4(error)) return "misaligned error word";
   if (n < 1 || n > PAGED_MAX_REQ) return "between 1 and 256 requests";
   if (num_pages < 1 || num_pages > INT32_MAX || max_pages < 1) return "bad page counts";
   if (hkv < 1 || hkv > 1024) return "bad number of kv heads";
@@ -63,7 +65,7 @@ oscar_status append(void* pool, int64_t num_pages, const int32_t* table, int32_t
                     const int32_t* new_lens, int32_t n, int32_t hq, int32_t hkv, int32_t gk, const oscar_rope* rope,
                     const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                     int64_t v_stride, uint16_t* q_out, int32_t* error, void* stream) {
-  if (const char* why = check_pages(pool, num_pages, table, max_pages, n, hkv)) return bad(why);
+  if (const char* why = check_pages(pool, num_pages, table, max_pages, n, hkv, error)) return bad(why);
   if (!lens) return bad("null lens");
   if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out))
     return bad("null or misaligned q / k / v");
@@ -147,11 +149,11 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
                        int32_t window, int32_t sinks, float scale, const uint16_t* q, int64_t q_stride, void* out,
                        int32_t out_type, float* lse, int32_t* error, void* workspace, size_t workspace_bytes,
                        void* stream) {
-  if (const char* why = check_pages(pool, num_pages, table, max_pages, n, hkv)) return bad(why);
+  if (const char* why = check_pages(pool, num_pages, table, max_pages, n, hkv, error)) return bad(why);
   if (!group_ok(hq, hkv)) return bad("query heads per kv head: 1, 2, 4 or 8");
   if (!lens || !q || !out || !workspace) return bad("null lens, q, out or workspace");
-  if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255))
-    return bad("misaligned q, out or workspace");
+  if (!aligned16(q) || !aligned16(out) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return bad("misaligned q, out, lse or workspace");
   if (q_stride < (int64_t)hq * D || q_stride % 8) return bad("a token stride is a multiple of 8 elements and holds the token's heads");
   if (out_type != OSCAR_F32 && out_type != OSCAR_BF16) return bad("out is fp32 or bf16");
   if (sinks < 0) return bad("sinks must not be negative");
@@ -257,7 +259,7 @@ oscar_status oscar_int4_read(const void* kv, int64_t num_pages, const int32_t* p
                              int32_t group_size, void* k_out, void* v_out, int32_t out_type, int32_t* error,
                              void* stream) {
   if (group_size != 128 && group_size != 64) return bad("group_size must be 128 or 64");
-  if (const char* why = check_pages(kv, num_pages, page_table, max_pages, n, num_kv_heads)) return bad(why);
+  if (const char* why = check_pages(kv, num_pages, page_table, max_pages, n, num_kv_heads, error)) return bad(why);
   if (!starts || !counts || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
     return bad("null starts or counts, null or misaligned output");
   if (out_type != OSCAR_F32 && out_type != OSCAR_BF16) return bad("out is fp32 or bf16");

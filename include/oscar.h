@@ -335,7 +335,8 @@ oscar_status oscar_bf16_decode(const void* kv, int64_t num_pages, const int32_t*
  *               have none.
  *   strides     elements from one token's heads to the next one's, a multiple of
  *               8, at least heads x 128 (heads lie densely, so q, k and v can be
- *               parts of one projection's output).  Pointers are 16-byte aligned.
+ *               parts of one projection's output).  Pointers are 16-byte aligned
+ *               (page table, lse and error: 4).
  *   error       device int32 or NULL: bit 1 is OR-ed in where a page id is out of
  *               range (a store to it is dropped, a read sees page 0 in an
  *               attention and zeros in oscar_int4_read), bit 2 where a bounded

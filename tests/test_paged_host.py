@@ -380,8 +380,26 @@ def test_the_build_checks_the_registers_that_the_prefill_counts_on():
 
 def test_the_build_rejects_an_object_of_other_registers(small_build, monkeypatch):
     build, tmp = small_build
+    monkeypatch.setattr(build, "_extension", lambda nvcc: (None, "left out"))
     monkeypatch.setattr(build, "check_registers", lambda src, out: (_ for _ in ()).throw(RuntimeError("registers")))
     for _ in range(2):                                  # no object is left that a second build would take
         with pytest.raises(RuntimeError, match="registers"):
             build.build()
         assert not (tmp / "lib" / "lib.so").exists()
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_error_and_lse_are_4_byte_aligned(b, off):
+    """The kernels add to the error word and store the log-sum-exps as 32-bit values."""
+    lib = b.load()
+    for name, args, at in (("append", APPEND, 9), ("attention", ATTEND, 9)):
+        for change in [dict(error=A + off)] + ([dict(lse=A + off)] if name == "attention" else []):
+            v = list({**args, **change}.values())
+            one = lib.oscar_bf16_append if name == "append" else lib.oscar_window_attention
+            four = lib.oscar_int4_append if name == "append" else lib.oscar_int4_attention
+            assert one(*v) == b.OSCAR_ERR_INVALID_ARG and b"misaligned" in lib.oscar_paged_last_error()
+            v.insert(at, 128)
+            assert four(*v) == b.OSCAR_ERR_INVALID_ARG and b"misaligned" in lib.oscar_paged_last_error()
+    read = dict(kv=A, pages=8, table=A, max_pages=4, starts=ints(0, 3), counts=ints(4, 5), n=2, hkv=2, group=64, k=A,
+                v=A, kind=1, error=A + off, stream=None)
+    assert lib.oscar_int4_read(*read.values()) == b.OSCAR_ERR_INVALID_ARG
