@@ -507,6 +507,12 @@ def _counts(values, n: int, name: str):
     return (c_int32 * n)(*ints), sum(ints)
 
 
+def _error_word(error, torch, device: int) -> int:
+    if error.numel() < 1:
+        _refuse("error: one int32 is wanted")
+    return _dense("error", error, torch.int32, None, device)
+
+
 def _pool(kv, torch, num_kv_heads, group, device):
     if not group:
         return _dense("kv", kv, torch.bfloat16, (kv.shape[0], num_kv_heads, 2, 64, HEAD_DIM), device)
@@ -543,7 +549,7 @@ def _append(fn, group, kv, page_table, lens, k, v, rope, q, q_out, new_lens, int
         length, dim = (_int32("rope's shape", x) for x in rope.shape)
         r = oscar_rope(_dense("rope", rope, torch.float32, None, device), length, dim, 1 if interleaved else 0)
     if error is not None:
-        err = _dense("error", error, torch.int32, None, device)
+        err = _error_word(error, torch, device)
     if rows:
         st = fn(pool, kv.shape[0], table, max_pages, old, new, n, hq, hkv, *group, r, qp, qs, kp, ks, vp, vs, qo, err, s)
         if st:
@@ -588,7 +594,7 @@ def int4_read(kv, page_table, starts, counts, k_out, v_out, group_size: int = 12
     shape = (rows, hkv, HEAD_DIM)
     ko = _dense("k_out", k_out, kind, shape, device)
     vo = _dense("v_out", v_out, kind, shape, device)
-    err = None if error is None else _dense("error", error, torch.int32, None, device)
+    err = None if error is None else _error_word(error, torch, device)
     if rows:
         st = load().oscar_int4_read(pool, kv.shape[0], table, max_pages, first, count, n, hkv, group_size, ko, vo,
                                     OSCAR_F32 if kind is torch.float32 else OSCAR_BF16, err, s)
@@ -630,7 +636,7 @@ def _attention(fn, group, kv, page_table, lens, q, out, hkv, window, sinks, q_le
         _refuse("out: float32 or bfloat16")
     op = _dense("out", out, kind, (rows, hq, HEAD_DIM), device)
     lp = None if lse is None else _dense("lse", lse, f32, (rows, hq), device)
-    err = None if error is None else _dense("error", error, torch.int32, None, device)
+    err = None if error is None else _error_word(error, torch, device)
     if workspace is None:
         workspace = attention_workspace(n, hq, hkv, q_lens, stream)
     while rows:

@@ -76,6 +76,10 @@ const at::Tensor* heads_of(PyObject* o, int device, int64_t rows, int64_t heads,
   *stride = rows > 1 ? s[0] : n[1] * HEAD_DIM;
   return t;
 }
+const at::Tensor* error_word(PyObject* o, int device) {
+  const at::Tensor* t = dense(o, I32, device);
+  return t && t->numel() > 0 ? t : nullptr;
+}
 template <typename T>
 T* at_ptr(const at::Tensor* t) {
   return t ? static_cast<T*>(t->data_ptr()) : nullptr;
@@ -158,7 +162,7 @@ int append(PyObject* const* a, Py_ssize_t count) {
     r = {at_ptr<const float>(t), static_cast<int32_t>(t->size(0)), static_cast<int32_t>(t->size(1)), inter};
     rope = &r;
   }
-  if (a[11] != Py_None && !(err = dense(a[11], I32, device))) return -1;
+  if (a[11] != Py_None && !(err = error_word(a[11], device))) return -1;
   if (table->size(1) > INT32_MAX || hkv > INT32_MAX || hq > INT32_MAX) return -1;
   if (rows == 0) return OSCAR_OK;
   const int32_t* nl = a[9] == Py_None ? nullptr : news;
@@ -200,7 +204,7 @@ int read(PyObject* const* a, Py_ssize_t count) {
   const at::Tensor *vo = dense(a[6], kind, device, {rows, hkv, HEAD_DIM}), *kv = pool_of(a[1], group, device, hkv),
                    *table = dense(a[2], I32, device, {n, -1});
   if (!vo || !kv || !table || table->size(1) > INT32_MAX || hkv > INT32_MAX) return -1;
-  if (a[7] != Py_None && !(err = dense(a[7], I32, device))) return -1;
+  if (a[7] != Py_None && !(err = error_word(a[7], device))) return -1;
   if (rows == 0) return OSCAR_OK;
   const int64_t pages = kv->size(0);
   const int32_t max_pages = static_cast<int32_t>(table->size(1));
@@ -242,7 +246,7 @@ int attend(PyObject* const* a, Py_ssize_t count) {
                    *ws = dense(a[12], U8, device, {-1}), *lse = nullptr, *err = nullptr;
   if (!out || !kv || !table || !ws || table->size(1) > INT32_MAX || hq > INT32_MAX) return -1;
   if (a[11] != Py_None && !(lse = dense(a[11], F32, device, {rows, hq}))) return -1;
-  if (a[13] != Py_None && !(err = dense(a[13], I32, device))) return -1;
+  if (a[13] != Py_None && !(err = error_word(a[13], device))) return -1;
   if (rows == 0) return OSCAR_OK;
   const int32_t* qn = a[9] == Py_None ? nullptr : ql;
   const int64_t pages = kv->size(0);

@@ -951,3 +951,15 @@ def test_long_shares_in_4_bits(b, group, hq):
             tol = tolerance(want, mag, logit, 79 * PAGE, group, False, False)
             assert (np.abs(out[row, h] - want) <= tol).all()
             assert abs(lse[row, h] - ls) <= 2 * 8 * 2.0 ** -22 * logit + 2.0 ** -20 + 2.0 ** -22 * (79 * 4 + 64)
+
+
+@pytest.mark.gpu
+def test_an_empty_error_tensor_is_refused_whichever_way_the_call_takes(b):
+    kv = torch.zeros(2, 1, 2, PAGE, D, dtype=torch.bfloat16, device="cuda")
+    table, none = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    q, out = torch.zeros(1, 2, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 2, D, device="cuda")
+    ws = b.window_attention(kv, table, [5], q, out, 1)
+    assert b.calls().attend(0, kv, table, [5], q, out, 1, -1, 0, None, 0.0, None, ws, none, None) is None
+    assert b.calls().append(0, kv, table, [5], q[:, :1], q[:, :1], None, None, None, None, False, none, None) is None
+    with pytest.raises(b.OscarError, match="error"):
+        b.window_attention(kv, table, [5], q, out, 1, workspace=ws, error=none)

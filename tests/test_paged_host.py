@@ -403,3 +403,15 @@ def test_error_and_lse_are_4_byte_aligned(b, off):
     read = dict(kv=A, pages=8, table=A, max_pages=4, starts=ints(0, 3), counts=ints(4, 5), n=2, hkv=2, group=64, k=A,
                 v=A, kind=1, error=A + off, stream=None)
     assert lib.oscar_int4_read(*read.values()) == b.OSCAR_ERR_INVALID_ARG
+
+
+def test_an_empty_error_tensor_is_refused(on_cpu):
+    """It has no word to tell a bad page in: taken as none, the error would be lost."""
+    import torch
+    b, t, none = on_cpu, tensors(), torch.zeros(0, dtype=torch.int32)
+    with pytest.raises(b.OscarError, match="error"):
+        b.window_attention(t["kv"], t["table"], [5, 9], t["q"], t["out"], 2, workspace=t["ws"], error=none)
+    with pytest.raises(b.OscarError, match="error"):
+        b.bf16_append(t["kv"], t["table"], [5, 9], t["k"], t["k"], error=none)
+    with pytest.raises(b.OscarError, match="error"):
+        b.int4_read(b.int4_pool(4, 2, device="cpu"), t["table"], [0, 0], [1, 1], t["k"].float(), t["k"].float(), error=none)
