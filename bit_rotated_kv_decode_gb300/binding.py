@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import operator
 import os
+import warnings
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 import numpy as np
@@ -423,6 +424,8 @@ def _marshal():
     global _calls
     if os.path.exists(calls_path()):
         return calls()
+    warnings.warn("the extension that marshals the paged calls is not built for this torch: they are marshalled in "
+                  "Python, 9 us a call slower (bit_rotated_kv_decode_gb300.build.build() makes it)", RuntimeWarning)
     _calls = _NotBuilt
     return _calls
 

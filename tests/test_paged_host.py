@@ -352,8 +352,9 @@ def test_calls_are_marshalled_in_python_without_the_extension(on_cpu, monkeypatc
     monkeypatch.setattr(b, "calls_path", lambda: "/nonexistent/_oscar_calls.so")
     with pytest.raises(RuntimeError, match="missing"):
         b.calls()
-    b._attention(lambda *a: got.append(a) or 0, (), t["kv"], t["table"], [5, 9], t["q"], t["out"], 2, 7, 0, None, 0.0,
-                 None, t["ws"], None, None)
+    with pytest.warns(RuntimeWarning, match="not built"):
+        b._attention(lambda *a: got.append(a) or 0, (), t["kv"], t["table"], [5, 9], t["q"], t["out"], 2, 7, 0, None,
+                     0.0, None, t["ws"], None, None)
     b._append(lambda *a: got.append(a) or 0, (), t["kv"], t["table"], [5, 9], t["k"], t["k"], None, None, None, None,
               False, None, None)
     assert len(got) == 2
