@@ -106,6 +106,9 @@ _SIGNATURES = {
                                        c_int32, c_int32, c_int32, c_int32, c_float, _P, c_int64, _P, c_int32, _P, _P,
                                        _P, c_size_t, _P]),
     "oscar_paged_last_error": (c_char_p, []),
+    "oscar_prompt_workspace_bytes": (c_size_t, [c_int32, POINTER(c_int32), c_int32, c_int32]),
+    "oscar_prompt_attention": (c_int32, [POINTER(c_int32), c_int32, c_int32, c_int32, c_int32, c_int32, c_float, _P,
+                                         c_int64, _P, c_int64, _P, c_int64, _P, c_int32, _P, _P, _P, c_size_t, _P]),
 }
 
 _lib = None
@@ -670,3 +673,51 @@ def int4_attention(kv, page_table, lens, q, out, num_kv_heads: int, window: int 
     """window_attention over a 4-bit pool, for at most 16 / (Hq / Hkv) query tokens a request."""
     return _attention(load().oscar_int4_attention, (group_size,), kv, page_table, lens, q, out, num_kv_heads, window,
                       sinks, q_lens, scale, lse, workspace, error, stream)
+
+
+# ---- prompts: attention within packed sequences ---------------------------------
+def prompt_workspace(lens, num_q_heads: int, num_kv_heads: int, stream=None):
+    """Workspace for prompt_attention calls of sequences of these lengths."""
+    hq, hkv = _int32("num_q_heads", num_q_heads), _int32("num_kv_heads", num_kv_heads)
+    n = len(lens)
+    arr, _ = _counts(lens, n, "lens")
+    torch, device, s = _context(stream)
+    need = load().oscar_prompt_workspace_bytes(n, arr, hq, hkv)
+    if need == 0:
+        _refuse("arguments outside the supported limits")
+    with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device)):
+        return new_workspace(need)
+
+
+def prompt_attention(q, k, v, out, lens, window: int = -1, sinks: int = 0, scale: float = 0.0, lse=None, workspace=None,
+                     error=None, stream=None):
+    """Causal attention within packed sequences of lens[i] tokens: q bf16 [rows][Hq][128], k, v [rows][Hkv][128] (rows may
+    be strided, as the parts of one projection's output), out [rows][Hq][128] fp32 or bf16, lse fp32 [rows][Hq] or None.
+    The query at position p of its sequence sees the tokens t <= p with t < sinks or t > p - window (window < 0: all).
+    Returns the workspace to pass to the next call: a new one where none is given or it is too small."""
+    n = len(lens)
+    hq, hkv = _int32("query heads", q.shape[1]), _int32("kv heads", k.shape[1])
+    window, sinks = _window(window), _int32("sinks", sinks)
+    arr, rows = _counts(lens, n, "lens")
+    torch, device, s = _context(stream)
+    kind, f32 = out.dtype, torch.float32
+    qp, qs = _heads("q", q, torch.bfloat16, rows, hq, device)
+    kp, ks = _heads("k", k, torch.bfloat16, rows, hkv, device)
+    vp, vs = _heads("v", v, torch.bfloat16, rows, hkv, device)
+    if kind is not f32 and kind is not torch.bfloat16:
+        _refuse("out: float32 or bfloat16")
+    op = _dense("out", out, kind, (rows, hq, HEAD_DIM), device)
+    lp = None if lse is None else _dense("lse", lse, f32, (rows, hq), device)
+    err = None if error is None else _error_word(error, torch, device)
+    if workspace is None:
+        workspace = prompt_workspace(lens, hq, hkv, stream)
+    while rows:
+        st = load().oscar_prompt_attention(
+            arr, n, hq, hkv, window, sinks, scale, qp, qs, kp, ks, vp, vs, op, OSCAR_F32 if kind is f32 else OSCAR_BF16,
+            lp, err, _dense("workspace", workspace, torch.uint8, None, device), workspace.numel(), s)
+        if not st:
+            break
+        if load().oscar_paged_last_error() != b"workspace too small":
+            _paged_check(st, "prompt attention")
+        workspace = prompt_workspace(lens, hq, hkv, stream)
+    return workspace

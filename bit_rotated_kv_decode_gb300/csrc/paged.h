@@ -91,6 +91,7 @@ struct AttnReq {
   int32_t m;              // query rows
   int32_t row;            // first row of q / out
   int32_t table;          // row of the page table
+  int32_t hist = 0;       // three-segment cache: end of the history
 };
 
 constexpr size_t PAGED_COUNTERS = 16384;                                  // int32 merge counters, zero between calls
@@ -113,9 +114,16 @@ cudaError_t launch_paged_decode(const PagedView& p, const AttnReq* reqs, int n, 
 // paged_prefill_blocks()), used where few blocks meet many keys.  f32: fp32 outputs,
 // whose blocks are smaller.
 int64_t paged_prefill_blocks(int m, int G, bool f32);
+int paged_prefill_splits(int64_t blocks, int hkv, int sms);
 size_t paged_prefill_partial_bytes(int64_t blocks, int hkv, int sms, bool f32);
 cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a,
                                  const CUtensorMap& q_map, const CUtensorMap& kv_map, void* partials, int sms,
                                  cudaStream_t s);
+
+// The same over rows of k and v instead of pages (k_map, v_map: (128 channels, Hkv, rows),
+// boxes of 64 channels x 1 head x 64 rows): request i's keys are those of its m rows.
+cudaError_t launch_packed_prefill(const AttnReq* reqs, int n, int hkv, const AttnArgs& a, const CUtensorMap& q_map,
+                                  const CUtensorMap& k_map, const CUtensorMap& v_map, int32_t* err, void* partials,
+                                  int sms, cudaStream_t s);
 
 }  // namespace oscar

@@ -130,6 +130,13 @@ bool pool_map(CUtensorMap* map, const void* pool, int64_t records, uint32_t toke
   return map_3d(map, pool, PAGE, static_cast<cuuint64_t>(2 * records), D * 2, (cuuint64_t)PAGE * D * 2, tokens, parts);
 }
 
+// 3-D view of rows of q, k or v: 128 channels, heads, rows.
+bool rows_map(CUtensorMap* map, const void* base, int64_t heads, int64_t rows, int64_t stride, int box_heads,
+              int box_rows) {
+  return map_3d(map, base, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows), D * 2,
+                static_cast<cuuint64_t>(stride) * 2, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_rows));
+}
+
 // SMs of the current device; 152 where there is none.
 int sm_count() {
   int sms = 0, dev = 0;
@@ -202,8 +209,7 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
   CUtensorMap kv_map, q_map;
   if (count) {
     if (!pool_map(&kv_map, pool, num_pages * hkv, PAGE, 1) ||
-        !map_3d(&q_map, q, static_cast<cuuint64_t>(hq), static_cast<cuuint64_t>(rows), D * 2,
-                static_cast<cuuint64_t>(q_stride) * 2, static_cast<uint32_t>(G), static_cast<uint32_t>(128 / G)))
+        !rows_map(&q_map, q, hq, rows, q_stride, G, 128 / G))
       return fail(OSCAR_ERR_CUDA, "tensor map of the pool or of q");
     const cudaError_t e = launch_paged_prefill(p, reqs, count, a, q_map, kv_map,
                                                static_cast<char*>(workspace) + PAGED_COUNTER_BYTES, sms, s);
@@ -227,6 +233,71 @@ oscar_status attention(const void* pool, int64_t num_pages, const int32_t* table
     if (e != cudaSuccess) return from_cuda(e);
   }
   return OSCAR_OK;
+}
+
+// Lengths of packed sequences: their rows in all, or -1; their row blocks for an output type.
+int64_t packed_rows(const int32_t* lens, int32_t n) {
+  int64_t rows = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (lens[i] < 0 || lens[i] > PAGED_MAX_TOKENS) return -1;
+    rows += lens[i];
+    if (rows > INT32_MAX / 64) return -1;
+  }
+  return rows;
+}
+size_t prompt_bytes(const int32_t* lens, int32_t n, int G, int hkv, bool f32, int sms) {
+  int64_t blocks = 0;
+  for (int32_t i = 0; i < n; ++i) blocks += paged_prefill_blocks(lens[i], G, f32);
+  return 256 + paged_prefill_partial_bytes(blocks, hkv, sms, f32);
+}
+
+oscar_status prompt(const int32_t* lens, int32_t n, int32_t hq, int32_t hkv, int32_t window, int32_t sinks, float scale,
+                    const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                    int64_t v_stride, void* out, int32_t out_type, float* lse, int32_t* error, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (n < 1 || n > PAGED_MAX_REQ) return bad("between 1 and 256 sequences");
+  if (!group_ok(hq, hkv)) return bad("query heads per kv head: 1, 2, 4 or 8");
+  if (!lens) return bad("null lens");
+  if (!q || !k || !v || !out || !workspace) return bad("null q, k, v, out or workspace");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned4(lse) || !aligned4(error) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return bad("misaligned q, k, v, out, lse, error or workspace");
+  const int64_t need_kv = (int64_t)hkv * D, most = (int64_t)1 << 38;   // (a tensor map's strides stay below 2^40 bytes)
+  if (q_stride < (int64_t)hq * D || k_stride < need_kv || v_stride < need_kv || q_stride % 8 || k_stride % 8 ||
+      v_stride % 8 || q_stride > most || k_stride > most || v_stride > most)
+    return bad("a token stride is a multiple of 8 elements and holds the token's heads");
+  if (out_type != OSCAR_F32 && out_type != OSCAR_BF16) return bad("out is fp32 or bf16");
+  if (sinks < 0) return bad("sinks must not be negative");
+  if (!std::isfinite(scale)) return bad("scale must be finite");
+  const int64_t rows = packed_rows(lens, n);
+  if (rows < 0) return bad("lens negative, or too many rows");
+  AttnArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.lse = lse;
+  a.f32 = out_type == OSCAR_F32;
+  a.Hq = hq;
+  a.window = window < 0 || window > PAGED_MAX_TOKENS ? PAGED_MAX_TOKENS : window;
+  a.sinks = sinks;
+  a.scale2 = (scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(D))) * 1.4426950408889634f;
+  if (!std::isfinite(a.scale2)) return bad("scale too large");
+  const int G = hq / hkv, sms = sm_count();
+  if (workspace_bytes < prompt_bytes(lens, n, G, hkv, a.f32, sms)) return bad("workspace too small");
+  if (rows == 0) return OSCAR_OK;
+  AttnReq reqs[PAGED_MAX_REQ];
+  int count = 0;
+  int32_t row = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (lens[i]) reqs[count++] = AttnReq{lens[i], lens[i], row, 0};
+    row += lens[i];
+  }
+  CUtensorMap q_map, k_map, v_map;
+  if (!rows_map(&q_map, q, hq, rows, q_stride, G, 128 / G) || !rows_map(&k_map, k, hkv, rows, k_stride, 1, PAGE) ||
+      !rows_map(&v_map, v, hkv, rows, v_stride, 1, PAGE))
+    return fail(OSCAR_ERR_CUDA, "tensor map of q, k or v");
+  return from_cuda(launch_packed_prefill(reqs, count, hkv, a, q_map, k_map, v_map, error, workspace, sms,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -313,6 +384,22 @@ oscar_status oscar_int4_attention(const void* kv, int64_t num_pages, const int32
   if (group_size != 128 && group_size != 64) return bad("group_size must be 128 or 64");
   return attention(kv, num_pages, page_table, max_pages, lens, q_lens, n, num_q_heads, num_kv_heads, group_size, window,
                    sinks, scale, q, q_stride, out, out_type, lse, error, workspace, workspace_bytes, stream);
+}
+
+size_t oscar_prompt_workspace_bytes(int32_t n, const int32_t* lens, int32_t num_q_heads, int32_t num_kv_heads) {
+  if (n < 1 || n > PAGED_MAX_REQ || !lens || !group_ok(num_q_heads, num_kv_heads) || packed_rows(lens, n) < 0) return 0;
+  const int G = num_q_heads / num_kv_heads, sms = sm_count();
+  const size_t b16 = prompt_bytes(lens, n, G, num_kv_heads, false, sms), f32 = prompt_bytes(lens, n, G, num_kv_heads, true, sms);
+  return b16 > f32 ? b16 : f32;
+}
+
+oscar_status oscar_prompt_attention(const int32_t* lens, int32_t n, int32_t num_q_heads, int32_t num_kv_heads,
+                                    int32_t window, int32_t sinks, float scale, const uint16_t* q, int64_t q_stride,
+                                    const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, void* out,
+                                    int32_t out_type, float* lse, int32_t* error, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  return prompt(lens, n, num_q_heads, num_kv_heads, window, sinks, scale, q, q_stride, k, k_stride, v, v_stride, out,
+                out_type, lse, error, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

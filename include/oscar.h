@@ -426,6 +426,31 @@ oscar_status oscar_int4_attention(const void* kv, int64_t num_pages, const int32
                                   int32_t* error, void* workspace, size_t workspace_bytes, void* stream);
 const char* oscar_paged_last_error(void);
 
+/* ---- Prompts: attention within packed sequences ------------------------------
+ * Causal attention of whole prompts before they have a cache, straight from a
+ * projection's output: sequence i's lens[i] tokens are the rows of q, k and v after those
+ * of the sequences before it (no padding; a sequence may be empty).  Its query at
+ * position p sees its own tokens t <= p with t < sinks or t > p - window; the result is
+ * that of oscar_window_attention on pages that hold k and v, with q_lens = lens.
+ *   lens       host int32 [n], 1 <= n <= 256, each at most 2^30; fewer than 2^25 rows in all.
+ *   q          device bf16 [rows][Hq][128], k, v [rows][Hkv][128]; strides as in the
+ *              paged calls.  out dense [rows][Hq][128] of out_type, lse device fp32
+ *              [rows][Hq] or NULL; neither may overlap q, k or v.
+ *   error      device int32 or NULL: bit 2 where a bounded device wait gave up.
+ *   workspace  device, >= oscar_prompt_workspace_bytes() (0: arguments outside the limits),
+ *              256-byte aligned; no contents are needed.  Calls that share a workspace must
+ *              not overlap on the GPU.
+ * Hq / Hkv in {1, 2, 4, 8}.  Tokens that a query does not see do not touch its result,
+ * whatever other sequences hold; within a sequence, those that some queries see and others
+ * do not must hold finite values.  Sums and softmax statistics are fp32; weights enter the
+ * product with V to 24 bits for fp32 outputs, to 8 for bf16. */
+size_t oscar_prompt_workspace_bytes(int32_t n, const int32_t* lens, int32_t num_q_heads, int32_t num_kv_heads);
+oscar_status oscar_prompt_attention(const int32_t* lens, int32_t n, int32_t num_q_heads, int32_t num_kv_heads,
+                                    int32_t window, int32_t sinks, float scale, const uint16_t* q, int64_t q_stride,
+                                    const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, void* out,
+                                    int32_t out_type, float* lse, int32_t* error, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
