@@ -85,6 +85,9 @@ _SIGNATURES = {
     "oscar_decode_attention": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), _P, _P, _P, c_size_t, _P]),
     "oscar_decode_attention_noalloc": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), _P, _P, _P]),
     "oscar_decode_step": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), _P, _P, _P, _P, _P, c_size_t, _P]),
+    "oscar_extend": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), POINTER(c_int32), _P, c_int64, _P, c_int64, _P]),
+    "oscar_read": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), POINTER(c_int32), POINTER(c_int32), _P, _P, c_int32,
+                             _P]),
     "oscar_cache_check": (c_int32, [_P, _P]),
     "oscar_debug_decode_hooks": (c_int32, [_P, ctypes.c_uint32, c_int32]),
     "oscar_last_error": (c_char_p, [_P]),
@@ -299,6 +302,51 @@ class OscarCache:
         self._check(self.lib.oscar_decode_attention_noalloc(self.h, layer, len(reqs), arr, _ptr(q), _ptr(out),
                                                             None if self.dry else _stream_ptr(stream)),
                     "decode (fixed scratch)", allow_dry=True)
+
+    # -- chunks of tokens -----------------------------------------------------------
+    def extend(self, layer: int, reqs, k, v, new_lens=None, stream=None) -> None:
+        """Append new_lens[i] tokens (one each by default) to every request of one layer, byte for byte as that many
+        append() calls.  k, v bf16 [rows][Hkv][128], the requests' tokens one after another; rows may be strided."""
+        n, hkv = len(reqs), self.cfg.num_kv_heads
+        lens, rows = _counts(new_lens, n, "new_lens")
+        if self.dry:
+            kp = vp = s = None
+            ks = vs = hkv * HEAD_DIM
+        else:
+            torch, device, s = self._context(stream)
+            kp, ks = _heads("k", k, torch.bfloat16, rows, hkv, device)
+            vp, vs = _heads("v", v, torch.bfloat16, rows, hkv, device)
+            if rows == 0:
+                kp = vp = self.mem.data_ptr()   # (a tensor without rows has no address)
+        self._check(self.lib.oscar_extend(self.h, _int32("layer", layer), n, self._reqs(reqs), lens, kp, ks, vp, vs, s),
+                    "extend", allow_dry=True)
+
+    def read(self, layer: int, reqs, starts, counts, k_out, v_out, stream=None) -> None:
+        """The keys and values that the cache holds of tokens [starts[i], starts[i] + counts[i]) of every request, in
+        their own basis (history tokens dequantised and rotated back), into k_out and v_out [rows][Hkv][128], fp32 or
+        bf16.  A request may be given more than once."""
+        n, hkv = len(reqs), self.cfg.num_kv_heads
+        first, _ = _counts(starts, n, "starts")
+        count, rows = _counts(counts, n, "counts")
+        kp = vp = s = None
+        kind = OSCAR_F32
+        if not self.dry:
+            torch, device, s = self._context(stream)
+            if k_out.dtype is not torch.float32 and k_out.dtype is not torch.bfloat16:
+                _refuse("k_out and v_out: float32 or bfloat16")
+            kp = _dense("k_out", k_out, k_out.dtype, (rows, hkv, HEAD_DIM), device)
+            vp = _dense("v_out", v_out, k_out.dtype, (rows, hkv, HEAD_DIM), device)
+            kind = OSCAR_F32 if k_out.dtype is torch.float32 else OSCAR_BF16
+            if rows == 0:
+                kp = vp = self.mem.data_ptr()
+        self._check(self.lib.oscar_read(self.h, _int32("layer", layer), n, self._reqs(reqs), first, count, kp, vp, kind,
+                                        s), "read", allow_dry=True)
+
+    def _context(self, stream):
+        torch, device, s = _context(stream)
+        if self.mem.get_device() != device:
+            _refuse("the cache is on another device than the current one")
+        return torch, device, s
 
     def check(self, stream=None) -> None:
         self._check(self.lib.oscar_cache_check(self.h, None if self.dry else _stream_ptr(stream)), "device check")

@@ -26,7 +26,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "liboscar_gb300.so")
 SOURCES = ["host.cpp", "write_kernels.cu", "decode_kernels.cu", "decode_scratch.cu", "bf16_decode.cu",
-           "paged_host.cpp", "paged_append.cu", "paged_decode.cu", "paged_prefill.cu", "prompt_attention.cu"]
+           "paged_host.cpp", "paged_append.cu", "paged_decode.cu", "paged_prefill.cu", "prompt_attention.cu",
+           "extend.cu", "chunk_read.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -13,9 +13,11 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <new>
 #include <string>
 #include <vector>
 
+#include "chunk.h"
 #include "internal.h"
 #include "oscar.h"
 
@@ -741,6 +743,152 @@ oscar_status oscar_decode_step(oscar_cache* c, int32_t layer, int32_t n, const i
     if (err != cudaSuccess) return c->cuda_fail(err, "decode step launch");
   }
   return OSCAR_OK;
+}
+
+// ---- chunks of tokens ------------------------------------------------------------
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+bool stride_ok(int64_t stride, int64_t heads) {
+  return stride >= heads * D && stride % 8 == 0 && stride <= (int64_t)1 << 38;   // (a tensor map's strides stay below 2^40 bytes)
+}
+
+// Checks that the chunk calls share; null if they hold.  distinct: no request twice.
+const char* check_chunk(const oscar_cache* c, int32_t layer, int32_t n, const int32_t* reqs, bool distinct) {
+  if (!c->valid_layer(layer)) return "bad layer";
+  if (n < 1 || n > CHUNK_MAX_REQ || !reqs) return "between 1 and 256 requests";
+  for (int32_t i = 0; i < n; ++i) {
+    if (!c->valid_req(reqs[i])) return "bad request id";
+    if (distinct)
+      for (int32_t j = 0; j < i; ++j)
+        if (reqs[j] == reqs[i]) return "duplicate request id";
+  }
+  return nullptr;
+}
+
+}  // namespace
+
+oscar_status oscar_extend(oscar_cache* c, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* new_lens,
+                          const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, void* stream) {
+  if (!c) return OSCAR_ERR_INVALID_ARG;
+  if (const char* why = check_chunk(c, layer, n, reqs, true)) return c->fail(OSCAR_ERR_INVALID_ARG, why);
+  const int64_t H = c->cfg.num_kv_heads;
+  if (!c->dry && (!k || !v || !aligned16(k) || !aligned16(v)))
+    return c->fail(OSCAR_ERR_INVALID_ARG, "null or misaligned k / v");
+  if (!stride_ok(k_stride, H) || !stride_ok(v_stride, H))
+    return c->fail(OSCAR_ERR_INVALID_ARG, "a token stride is a multiple of 8 elements and holds the token's heads");
+  ExtendArgs a;
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.n = 0;
+  a.layer = layer;
+  int64_t rows = 0, hist = 0, kept = 0, fresh = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const int64_t m = new_lens ? new_lens[i] : 1;
+    const Request& r = c->reqs[reqs[i]];
+    const int64_t T = r.T[layer], he = r.he[layer], end = T + m;
+    if (m < 0 || end > PAGED_MAX_TOKENS) return c->fail(OSCAR_ERR_INVALID_ARG, "new_lens negative, or beyond 2^30 tokens");
+    if (m > 0) {
+      // as appends leave it: a full window demotes its oldest token first
+      const int64_t he1 = std::max<int64_t>(he, end - RECENT), need = pages_for(he1);
+      if (need > c->cfg.max_pages_per_request) return c->fail(OSCAR_ERR_INVALID_ARG, "request exceeds its page table");
+      fresh += std::max<int64_t>(0, need - (int64_t)r.hist_pt.size());
+      const int j = a.n++;
+      a.slot[j] = reqs[i];
+      a.row0[j] = static_cast<int32_t>(rows);
+      a.old[j] = static_cast<int32_t>(T);
+      a.h0[j] = static_cast<int32_t>(he);
+      a.h1[j] = static_cast<int32_t>(he1);
+      a.hist[j] = static_cast<int32_t>(hist);
+      a.rows[j] = static_cast<int32_t>(kept);
+      hist += he1 - he;
+      const int64_t in_sink = std::min<int64_t>(m, std::max<int64_t>(0, SINK - T));
+      kept += in_sink + std::max<int64_t>(0, end - std::max<int64_t>({T, he1, (int64_t)SINK}));
+    }
+    rows += m;
+    if (rows > INT32_MAX / 64) return c->fail(OSCAR_ERR_INVALID_ARG, "too many tokens");
+  }
+  a.hist[a.n] = static_cast<int32_t>(hist);
+  a.rows[a.n] = static_cast<int32_t>(kept);
+  if (fresh > c->int2.free_count()) return c->fail(OSCAR_ERR_OUT_OF_PAGES, "out of INT2 pages");
+  std::vector<PtEntry> entries;
+  try {   // memory first: nothing below throws
+    entries.reserve(fresh);
+    for (int j = 0; j < a.n; ++j) c->reqs[a.slot[j]].hist_pt.reserve(pages_for(a.h1[j]));
+  } catch (const std::bad_alloc&) {
+    return c->fail(OSCAR_ERR_INVALID_ARG, "out of host memory");
+  }
+  int32_t row = 0;
+  for (int32_t i = 0, j = 0; i < n; ++i) {
+    const int32_t m = new_lens ? new_lens[i] : 1;
+    if (m == 0) continue;
+    Request& r = c->reqs[reqs[i]];
+    for (const int64_t need = pages_for(a.h1[j]); (int64_t)r.hist_pt.size() < need;) {
+      const int32_t p = c->int2.alloc();
+      entries.push_back(PtEntry{0, static_cast<int32_t>((int64_t)reqs[i] * c->cfg.max_pages_per_request + r.hist_pt.size()), p});
+      r.hist_pt.push_back(p);
+    }
+    r.T[layer] += m;
+    r.he[layer] = a.h1[j++];
+    row += m;
+  }
+  if (c->dry) return OSCAR_ERR_DRY_RUN;
+  if (row == 0) return OSCAR_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  c->last_decode = false;
+  cudaError_t e = entries.empty() ? cudaSuccess : launch_pt_update(c->dc, entries.data(), static_cast<int>(entries.size()), s);
+  if (e == cudaSuccess && hist > 0) e = launch_extend_history(c->dc, a, c->num_sms, s);
+  if (e == cudaSuccess && kept > 0) e = launch_extend_bf16(c->dc, a, s);
+  return e == cudaSuccess ? OSCAR_OK : c->cuda_fail(e, "extend launch");
+}
+
+oscar_status oscar_read(oscar_cache* c, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* starts,
+                        const int32_t* counts, void* k_out, void* v_out, int32_t out_type, void* stream) {
+  if (!c) return OSCAR_ERR_INVALID_ARG;
+  if (const char* why = check_chunk(c, layer, n, reqs, false)) return c->fail(OSCAR_ERR_INVALID_ARG, why);
+  if (!starts || !counts) return c->fail(OSCAR_ERR_INVALID_ARG, "null starts or counts");
+  if (out_type != OSCAR_F32 && out_type != OSCAR_BF16) return c->fail(OSCAR_ERR_INVALID_ARG, "out is fp32 or bf16");
+  if (!c->dry && (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)))
+    return c->fail(OSCAR_ERR_INVALID_ARG, "null or misaligned output");
+  ReadArgs a;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.n = 0;
+  a.layer = layer;
+  int64_t rows = 0, hist = 0, near = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const Request& r = c->reqs[reqs[i]];
+    const int64_t T = r.T[layer], b = starts[i], m = counts[i], end = b + m;
+    if (b < 0 || m < 0 || end > T || end > PAGED_MAX_TOKENS)
+      return c->fail(OSCAR_ERR_INVALID_ARG, "tokens that the request does not hold");
+    if (m > 0) {
+      const int64_t before = std::max<int64_t>(0, std::min<int64_t>(end, SINK) - b), first = b + before;
+      const int64_t h = std::max<int64_t>(0, std::min<int64_t>(end, r.he[layer]) - first);
+      const int j = a.n++;
+      a.slot[j] = reqs[i];
+      a.start[j] = static_cast<int32_t>(b);
+      a.first[j] = static_cast<int32_t>(first);
+      a.out0[j] = static_cast<int32_t>(rows + before);
+      a.hist[j] = static_cast<int32_t>(hist);
+      a.near[j] = static_cast<int32_t>(near);
+      hist += h;
+      near += m - h;
+    }
+    rows += m;
+    if (rows > INT32_MAX / 64) return c->fail(OSCAR_ERR_INVALID_ARG, "too many tokens");
+  }
+  a.hist[a.n] = static_cast<int32_t>(hist);
+  a.near[a.n] = static_cast<int32_t>(near);
+  if (c->dry) return OSCAR_ERR_DRY_RUN;
+  if (rows == 0) return OSCAR_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  c->last_decode = false;
+  cudaError_t e = cudaSuccess;
+  if (hist > 0) e = launch_read_history(c->dc, a, out_type == OSCAR_F32, c->num_sms, s);
+  if (e == cudaSuccess && near > 0) e = launch_read_bf16(c->dc, a, out_type == OSCAR_F32, s);
+  return e == cudaSuccess ? OSCAR_OK : c->cuda_fail(e, "read launch");
 }
 
 oscar_status oscar_debug_decode_hooks(oscar_cache* c, uint32_t wait_limit, int32_t hold_copy) {

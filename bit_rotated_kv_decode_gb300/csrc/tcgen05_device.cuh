@@ -56,6 +56,8 @@ __device__ __forceinline__ uint64_t desc_nmajor(uint32_t addr) {
 // kind::f16, bf16 operands, fp32 result, M = N = 128; PV has its B operand N-major.
 constexpr uint32_t IDESC_QK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t IDESC_PV = IDESC_QK | (1u << 16);
+// the same with fp16 operands
+constexpr uint32_t IDESC_QK_F16 = IDESC_QK & ~((1u << 7) | (1u << 10)), IDESC_PV_F16 = IDESC_QK_F16 | (1u << 16);
 
 // Issued by one elected lane of a converged warp: the code around stays uniform, so that
 // descriptors are computed in uniform registers (under an if of one lane, each product

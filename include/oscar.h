@@ -267,6 +267,34 @@ oscar_status oscar_decode_step(oscar_cache* cache, int32_t layer, int32_t n, con
                                const uint16_t* k, const uint16_t* v, const uint16_t* q, float* out,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Chunks of tokens ------------------------------------------------------
+ * What a program needs to feed a prompt in pieces, to go on from a forked prefix and to
+ * check drafted tokens: several new tokens of each request at once.  reqs host int32 [n],
+ * 1 <= n <= 256; lengths are host int32 [n] (NULL new_lens: one each; 0 allowed); rows of
+ * tensors are the requests' tokens one after another.  Strides are elements from one
+ * token's heads to the next one's: a multiple of 8, at least heads x 128, heads lying
+ * densely (so that q, k and v can be parts of one projection's output).  A request holds
+ * at most 2^30 tokens, a call takes fewer than 2^25 rows.  Every check is made before any
+ * change; lengths and page ids are read at the call, so a captured call repeats them.
+ *
+ * Append new_lens[i] tokens to request reqs[i] (distinct) of one layer: the bytes, lengths
+ * and segments that as many oscar_append calls give, whatever the recent window holds.
+ * History pages are taken request by request.
+ *   k, v  device bf16 [rows][Hkv][128].
+ * Values that the quantiser's decision leaves open in fp32 are decided exactly, as in
+ * oscar_append ([MS] section "OSCAR的设计"; [MTP] section "The Serving System", write path). */
+oscar_status oscar_extend(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* new_lens,
+                          const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, void* stream);
+
+/* The keys and values that the cache holds of tokens [starts[i], starts[i] + counts[i]) of
+ * request reqs[i] (which may repeat), in their own basis: BF16 tokens as they are, history
+ * tokens (z + s c) R^T.
+ *   k_out, v_out  device [rows][Hkv][128] of out_type (oscar_type), 16-byte aligned.
+ * fp32 values are within 2^-20 of the token's largest term sum; bf16 ones are rounded once,
+ * from values whose R is rounded to 11 bits. */
+oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* starts,
+                        const int32_t* counts, void* k_out, void* v_out, int32_t out_type, void* stream);
+
 /* Failure-detection hooks of the decode launches of this cache (test use; the
  * pages have no counterpart).  wait_limit: rounds (up to 20 us each) a bounded
  * device wait on a page copy makes before it gives up and reports
