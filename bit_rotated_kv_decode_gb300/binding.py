@@ -88,6 +88,9 @@ _SIGNATURES = {
     "oscar_extend": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), POINTER(c_int32), _P, c_int64, _P, c_int64, _P]),
     "oscar_read": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), POINTER(c_int32), POINTER(c_int32), _P, _P, c_int32,
                              _P]),
+    "oscar_chunk_workspace_bytes": (c_int32, [_P, c_int32, POINTER(c_int32), POINTER(c_size_t)]),
+    "oscar_chunk_attention": (c_int32, [_P, c_int32, c_int32, POINTER(c_int32), POINTER(c_int32), _P, c_int64, _P,
+                                        c_int64, _P, c_int64, _P, _P, c_size_t, _P]),
     "oscar_cache_check": (c_int32, [_P, _P]),
     "oscar_debug_decode_hooks": (c_int32, [_P, ctypes.c_uint32, c_int32]),
     "oscar_last_error": (c_char_p, [_P]),
@@ -341,6 +344,48 @@ class OscarCache:
                 kp = vp = self.mem.data_ptr()
         self._check(self.lib.oscar_read(self.h, _int32("layer", layer), n, self._reqs(reqs), first, count, kp, vp, kind,
                                         s), "read", allow_dry=True)
+
+    def chunk_workspace(self, new_lens, stream=None):
+        """Workspace for chunk_attention calls of these numbers of new tokens, whatever the requests hold."""
+        n = len(new_lens)
+        lens, _ = _counts(new_lens, n, "new_lens")
+        b = c_size_t()
+        self._check(self.lib.oscar_chunk_workspace_bytes(self.h, n, lens, ctypes.byref(b)), "workspace")
+        torch, device, s = self._context(stream)
+        with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device)):
+            return new_workspace(b.value)
+
+    def chunk_attention(self, layer: int, reqs, q, k, v, out, new_lens=None, workspace=None, stream=None):
+        """Attention of new_lens[i] new tokens (one each by default) of every request over its cached tokens and, causally,
+        over the new ones; the cache is not changed.  q bf16 [rows][Hq][128], k, v [rows][Hkv][128] (rows may be strided),
+        out bf16 [rows][Hq][128].  Returns the workspace to pass to the next call: a new one where none is given or it is
+        too small."""
+        n, hkv, hq = len(reqs), self.cfg.num_kv_heads, self.cfg.num_q_heads
+        lens, rows = _counts(new_lens, n, "new_lens")
+        layer = _int32("layer", layer)
+        if self.dry:
+            self._check(self.lib.oscar_chunk_attention(self.h, layer, n, self._reqs(reqs), lens, None, hq * HEAD_DIM, None,
+                                                       hkv * HEAD_DIM, None, hkv * HEAD_DIM, None, None, 0, None),
+                        "chunk attention", allow_dry=True)
+            return workspace
+        torch, device, s = self._context(stream)
+        qp, qs = _heads("q", q, torch.bfloat16, rows, hq, device)
+        kp, ks = _heads("k", k, torch.bfloat16, rows, hkv, device)
+        vp, vs = _heads("v", v, torch.bfloat16, rows, hkv, device)
+        op = _dense("out", out, torch.bfloat16, (rows, hq, HEAD_DIM), device)
+        if rows == 0:
+            qp = kp = vp = op = self.mem.data_ptr()   # (a tensor without rows has no address)
+        if workspace is None:
+            workspace = self.chunk_workspace([1] * n if new_lens is None else new_lens, stream)
+        while True:
+            st = self.lib.oscar_chunk_attention(
+                self.h, layer, n, self._reqs(reqs), lens, qp, qs, kp, ks, vp, vs, op,
+                _dense("workspace", workspace, torch.uint8, None, device), workspace.numel(), s)
+            if st == OSCAR_OK or self.lib.oscar_last_error(self.h) != b"workspace too small":
+                break
+            workspace = self.chunk_workspace([1] * n if new_lens is None else new_lens, stream)
+        self._check(st, "chunk attention")
+        return workspace
 
     def _context(self, stream):
         torch, device, s = _context(stream)

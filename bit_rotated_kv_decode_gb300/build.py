@@ -27,7 +27,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "liboscar_gb300.so")
 SOURCES = ["host.cpp", "write_kernels.cu", "decode_kernels.cu", "decode_scratch.cu", "bf16_decode.cu",
            "paged_host.cpp", "paged_append.cu", "paged_decode.cu", "paged_prefill.cu", "prompt_attention.cu",
-           "extend.cu", "chunk_read.cu"]
+           "extend.cu", "chunk_read.cu", "chunk_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 
@@ -85,7 +85,8 @@ def _extension(nvcc: str):
 # Kernels that split their registers at run time (setmaxnreg) count on what they are launched
 # with: a file, a pattern of the kernels' names, how many of them, and the registers.
 REGISTERS = {"paged_prefill.cu": (r"paged_prefill_kernelI", 4, 168),
-             "prompt_attention.cu": (r"paged_prefill_kernelI", 4, 168)}
+             "prompt_attention.cu": (r"paged_prefill_kernelI", 6, 168),
+             "chunk_attention.cu": (r"chunk_scan_kernelI", 4, 128)}
 
 
 def check_registers(src: str, log: str) -> None:

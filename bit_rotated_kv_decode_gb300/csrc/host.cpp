@@ -891,6 +891,176 @@ oscar_status oscar_read(oscar_cache* c, int32_t layer, int32_t n, const int32_t*
   return e == cudaSuccess ? OSCAR_OK : c->cuda_fail(e, "read launch");
 }
 
+namespace {
+
+// The workspace of a chunk attention, whatever the caches hold: rotated queries, their scales, the
+// scan's records and the near rows' (each group of requests uses the last two in turn).
+struct ChunkSpace {
+  size_t scale, records, near, bytes;
+};
+bool chunk_pair(int64_t m, int G) { return m * G > 128; }   // two tiles of rows, not one (chunk_attention.cu)
+ChunkSpace chunk_space(const oscar_cache* c, int32_t n, const int32_t* new_lens) {
+  const int64_t H = c->cfg.num_kv_heads, G = c->G(), sms = c->num_sms;
+  int64_t rows = 0, blocks = 0, segments[2] = {0, 0}, longest = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const int64_t m = new_lens ? new_lens[i] : 1;
+    rows += m;
+    blocks += (m * G + 255) / 256;
+    segments[chunk_pair(m, c->G())] += H * ((m * G + 255) / 256);
+    longest = std::max(longest, m);
+  }
+  const size_t record = (size_t)256 * PARTIAL_FLOATS * sizeof(float);
+  // a group's near rows are split so that they fill the SMs at most, in parts of four key tiles or more
+  const int64_t items = blocks * H, parts = std::max<int64_t>(1, ((SINK + RECENT + PAGE + longest) / 128 + 1) / 4);
+  const size_t near = (size_t)std::min(items * parts, std::max(items, sms)) * record;
+  ChunkSpace s;
+  s.scale = align256((size_t)rows * c->cfg.num_q_heads * D * 2);
+  s.records = s.scale + align256((size_t)rows * c->cfg.num_q_heads * sizeof(float));
+  s.near = s.records + (size_t)(std::max(segments[0], segments[1]) + sms) * record;
+  s.bytes = s.near + near + 256;
+  return s;
+}
+// Rows of the new tokens, or -1.
+int64_t chunk_rows(int32_t n, const int32_t* new_lens) {
+  int64_t rows = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const int64_t m = new_lens ? new_lens[i] : 1;
+    if (m < 0) return -1;
+    rows += m;
+    if (rows > INT32_MAX / 64) return -1;
+  }
+  return rows;
+}
+
+// One group of requests: all without history, or all of one kind of the scan.
+cudaError_t chunk_group(oscar_cache* c, const AttnReq* reqs, int n, bool history, bool pair, const AttnArgs& a,
+                        const CUtensorMap* maps, const ChunkSpace& space, char* ws, ScanArgs& sa, cudaStream_t s) {
+  const DevCache& d = c->dc;
+  const PagedView p{nullptr, d.bf16_pt, d.n_bf16_pages, BF16_PAGES_PER_REQ, n, d.Hkv, d.err};
+  NearPlan plan;
+  cudaError_t e = launch_near_attention(p, reqs, n, a, history, maps[0], maps[1], maps[2], maps[3], ws + space.near, &plan,
+                                        c->num_sms, s);
+  if (e != cudaSuccess || !history) return e;
+  int64_t cost = 0, segments = 0;
+  sa.n = n;
+  sa.setup = CHUNK_SETUP;
+  for (int i = 0; i < n; ++i) {
+    sa.slot[i] = reqs[i].table;
+    sa.m[i] = reqs[i].m;
+    sa.row[i] = reqs[i].row;
+    sa.hist[i] = reqs[i].hist - SINK;
+    sa.tiles[i] = (sa.hist[i] + 127) / 128;
+    sa.blocks[i] = pair ? (reqs[i].m * d.G + 255) / 256 : 1;
+    sa.segment[i] = static_cast<int32_t>(segments);
+    sa.cost[i] = cost;
+    segments += (int64_t)d.Hkv * sa.blocks[i];
+    cost += (int64_t)d.Hkv * sa.blocks[i] * (sa.tiles[i] + sa.setup);
+  }
+  sa.total = cost;
+  sa.ctas = static_cast<int32_t>(std::min<int64_t>(cost, c->num_sms));
+  e = launch_chunk_scan(d, sa, pair, maps[4], s);
+  if (e != cudaSuccess) return e;
+  MergeArgs m;
+  m.near = reinterpret_cast<const float*>(ws + space.near);
+  m.out = static_cast<uint16_t*>(a.out);
+  m.near_splits = plan.splits;
+  m.near_blocks = plan.blocks;
+  for (int i = 0; i < n; ++i) m.near_start[i] = plan.start[i];
+  return launch_chunk_merge(d, sa, m, pair, c->num_sms, s);
+}
+
+}  // namespace
+
+oscar_status oscar_chunk_workspace_bytes(const oscar_cache* c, int32_t n, const int32_t* new_lens, size_t* bytes) {
+  if (!c || !bytes) return OSCAR_ERR_INVALID_ARG;
+  oscar_cache* mc = const_cast<oscar_cache*>(c);
+  if (n < 1 || n > CHUNK_MAX_REQ) return mc->fail(OSCAR_ERR_INVALID_ARG, "between 1 and 256 requests");
+  if (chunk_rows(n, new_lens) < 0) return mc->fail(OSCAR_ERR_INVALID_ARG, "new_lens negative, or too many tokens");
+  *bytes = chunk_space(c, n, new_lens).bytes;
+  return OSCAR_OK;
+}
+
+oscar_status oscar_chunk_attention(oscar_cache* c, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* new_lens,
+                                   const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                   const uint16_t* v, int64_t v_stride, uint16_t* out, void* workspace,
+                                   size_t ws_bytes, void* stream) {
+  if (!c) return OSCAR_ERR_INVALID_ARG;
+  if (const char* why = check_chunk(c, layer, n, reqs, false)) return c->fail(OSCAR_ERR_INVALID_ARG, why);
+  const int64_t H = c->cfg.num_kv_heads, Hq = c->cfg.num_q_heads;
+  if (!stride_ok(q_stride, Hq) || !stride_ok(k_stride, H) || !stride_ok(v_stride, H))
+    return c->fail(OSCAR_ERR_INVALID_ARG, "a token stride is a multiple of 8 elements and holds the token's heads");
+  const int64_t rows = chunk_rows(n, new_lens);
+  if (rows < 0 || rows * Hq > INT32_MAX) return c->fail(OSCAR_ERR_INVALID_ARG, "new_lens negative, or too many tokens");
+  if (c->cfg.num_bf16_pages * H > INT32_MAX / 2) return c->fail(OSCAR_ERR_INVALID_ARG, "BF16 pages x kv heads: below 2^30");
+  for (int32_t i = 0; i < n; ++i)
+    if (c->reqs[reqs[i]].T[layer] + (new_lens ? new_lens[i] : 1) > PAGED_MAX_TOKENS)
+      return c->fail(OSCAR_ERR_INVALID_ARG, "beyond 2^30 tokens");
+  if (c->dry) return OSCAR_ERR_DRY_RUN;
+  if (!q || !k || !v || !out || !workspace || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+    return c->fail(OSCAR_ERR_INVALID_ARG, "null or misaligned q / k / v / out / workspace");
+  const ChunkSpace space = chunk_space(c, n, new_lens);
+  if (space.bytes > ws_bytes) return c->fail(OSCAR_ERR_INVALID_ARG, "workspace too small");
+  if (rows == 0) return OSCAR_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const DevCache& d = c->dc;
+  const int G = d.G;
+  AttnArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.Hq = d.Hq;
+  a.window = PAGED_MAX_TOKENS;
+  a.scale2 = d.scale * 1.4426950408889634f;
+  ScanArgs sa;
+  sa.q_scale = reinterpret_cast<const float*>(ws + space.scale);
+  sa.records = reinterpret_cast<float*>(ws + space.records);
+  sa.layer = layer;
+  sa.Hq = d.Hq;
+  sa.Hkv = d.Hkv;
+  sa.G = G;
+  sa.lg = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
+  sa.scale2 = 2.0f * a.scale2;
+  // q, the BF16 pages, the new keys and values, the rotated q
+  CUtensorMap maps[5];
+  if (!tensor_map_rows(&maps[0], q, Hq, rows, q_stride, G, 128 / G) ||
+      !tensor_map_pages(&maps[1], d.bf16 + layer * d.bf16_layer_stride, d.n_bf16_pages * H) ||
+      !tensor_map_rows(&maps[2], k, H, rows, k_stride, 1, PAGE) ||
+      !tensor_map_rows(&maps[3], v, H, rows, v_stride, 1, PAGE) ||
+      !tensor_map_rows(&maps[4], ws, Hq, rows, Hq * D, G, 128 / G))
+    return c->fail(OSCAR_ERR_CUDA, "tensor map of q, k, v or the BF16 pages");
+  // groups: without history; rows of a kv head that fill one tile at most; more
+  AttnReq group[CHUNK_MAX_REQ];
+  c->last_decode = false;
+  bool rotated = false;
+  for (int which = 0; which < 3; ++which) {
+    int count = 0;
+    int32_t row = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      const int32_t m = new_lens ? new_lens[i] : 1;
+      const Request& r = c->reqs[reqs[i]];
+      const int64_t T = r.T[layer], he = r.he[layer];
+      if (m > 0 && which == (he <= SINK ? 0 : chunk_pair(m, G) ? 2 : 1)) {
+        group[count] = AttnReq{static_cast<int32_t>(T), m, row, reqs[i]};
+        group[count++].hist = static_cast<int32_t>(he);
+      }
+      row += m;
+    }
+    if (!count) continue;
+    cudaError_t e = cudaSuccess;
+    if (which > 0 && !rotated) {
+      const RotateArgs ra{q, q_stride, reinterpret_cast<uint16_t*>(ws), reinterpret_cast<float*>(ws + space.scale),
+                          static_cast<int32_t>(rows), sa.lg, layer};
+      e = launch_rotate_queries(d, ra, c->num_sms, s);
+      rotated = true;
+    }
+    if (e == cudaSuccess) e = chunk_group(c, group, count, which > 0, which == 2, a, maps, space, ws, sa, s);
+    if (e != cudaSuccess) return c->cuda_fail(e, "chunk attention launch");
+  }
+  return OSCAR_OK;
+}
+
 oscar_status oscar_debug_decode_hooks(oscar_cache* c, uint32_t wait_limit, int32_t hold_copy) {
   if (!c) return OSCAR_ERR_INVALID_ARG;
   // the device's other bounded waits take multiples of wait_limit in 32 bits

@@ -120,6 +120,12 @@ cudaError_t launch_paged_prefill(const PagedView& p, const AttnReq* reqs, int n,
                                  const CUtensorMap& q_map, const CUtensorMap& kv_map, void* partials, int sms,
                                  cudaStream_t s);
 
+// Tensor maps of 16-bit values in boxes of 64 channels: rows of q, k or v (128 channels, heads,
+// rows), and the pages of a BF16 pool (128 channels, 64 tokens, (record, K or V)).
+bool tensor_map_rows(CUtensorMap* map, const void* base, int64_t heads, int64_t rows, int64_t stride, int box_heads,
+                     int box_rows);
+bool tensor_map_pages(CUtensorMap* map, const void* pool, int64_t records);
+
 // The same over rows of k and v instead of pages (k_map, v_map: (128 channels, Hkv, rows),
 // boxes of 64 channels x 1 head x 64 rows): request i's keys are those of its m rows.
 cudaError_t launch_packed_prefill(const AttnReq* reqs, int n, int hkv, const AttnArgs& a, const CUtensorMap& q_map,

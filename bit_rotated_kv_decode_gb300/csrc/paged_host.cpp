@@ -302,6 +302,14 @@ oscar_status prompt(const int32_t* lens, int32_t n, int32_t hq, int32_t hkv, int
 
 }  // namespace
 
+bool oscar::tensor_map_rows(CUtensorMap* map, const void* base, int64_t heads, int64_t rows, int64_t stride,
+                            int box_heads, int box_rows) {
+  return rows_map(map, base, heads, rows, stride, box_heads, box_rows);
+}
+bool oscar::tensor_map_pages(CUtensorMap* map, const void* pool, int64_t records) {
+  return pool_map(map, pool, records, PAGE, 1);
+}
+
 extern "C" {
 
 const char* oscar_paged_last_error(void) { return g_message; }

@@ -773,17 +773,18 @@ cudaError_t plan(PrefillArgs& A, const PagedView& p, const AttnReq* reqs, int n,
   return cudaSuccess;
 }
 
-template <Source S>
-cudaError_t launch_source(const PrefillArgs& A, const PrefillMaps& maps, int sms, cudaStream_t s) {
-  cudaError_t e;
-  if (A.splits > 1)
-    e = A.a.f32 ? launch_tiles<true, true, S>(A, maps, sms, s) : launch_tiles<false, true, S>(A, maps, sms, s);
-  else
-    return A.a.f32 ? launch_tiles<true, false, S>(A, maps, sms, s) : launch_tiles<false, false, S>(A, maps, sms, s);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_fold(const PrefillArgs& A, cudaStream_t s) {
   const int64_t warps = (int64_t)A.items / A.splits * A.tiles * PF_ROWS;
   return launch_dependent(paged_prefill_fold_kernel, static_cast<unsigned>((warps + FOLD_WARPS - 1) / FOLD_WARPS),
                           32 * FOLD_WARPS, 0, s, A);
+}
+
+template <Source S>
+cudaError_t launch_source(const PrefillArgs& A, const PrefillMaps& maps, int sms, cudaStream_t s) {
+  if (A.splits == 1)
+    return A.a.f32 ? launch_tiles<true, false, S>(A, maps, sms, s) : launch_tiles<false, false, S>(A, maps, sms, s);
+  const cudaError_t e = A.a.f32 ? launch_tiles<true, true, S>(A, maps, sms, s) : launch_tiles<false, true, S>(A, maps, sms, s);
+  return e != cudaSuccess ? e : launch_fold(A, s);
 }
 
 }  // namespace

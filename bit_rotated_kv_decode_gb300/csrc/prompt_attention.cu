@@ -1,6 +1,8 @@
 // Attention of whole prompts within packed sequences, straight from the rows of q, k and v
 // that a projection wrote: the tiled kernel of paged_prefill.cu with its keys and values
-// loaded as rows (boxes of 64 tokens of one kv head) instead of pages.
+// loaded as rows (boxes of 64 tokens of one kv head) instead of pages.  And the near part of a
+// chunk's attention: the same over the three-segment cache's BF16 pages with the chunk's own
+// rows behind them.
 namespace oscar {
 namespace {
 // Registers a thread: 168 at launch (three warpgroups share 504), then 208 for the
@@ -9,6 +11,7 @@ constexpr int PF_REGS = 168, PF_SOFTMAX_REGS = 208, PF_OTHER_REGS = 88;
 }  // namespace
 }  // namespace oscar
 
+#include "chunk.h"
 #include "paged_prefill_device.cuh"
 
 namespace oscar {
@@ -22,6 +25,24 @@ cudaError_t launch_packed_prefill(const AttnReq* reqs, int n, int hkv, const Att
   if (e != cudaSuccess) return e;
   const PrefillMaps maps{q_map, {}, k_map, v_map};
   return launch_source<PACKED>(A, maps, sms, s);
+}
+
+cudaError_t launch_near_attention(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, bool partial,
+                                  const CUtensorMap& q_map, const CUtensorMap& pool_map, const CUtensorMap& k_map,
+                                  const CUtensorMap& v_map, void* partials, NearPlan* out, int sms, cudaStream_t s) {
+  PrefillArgs A;
+  const cudaError_t e = plan(A, p, reqs, n, a, partials, sms, CACHE);
+  if (e != cudaSuccess) return e;
+  const PrefillMaps maps{q_map, pool_map, k_map, v_map};
+  if (!partial && A.splits == 1) return launch_tiles<false, false, CACHE>(A, maps, sms, s);
+  if (!partial) {
+    const cudaError_t f = launch_tiles<false, true, CACHE>(A, maps, sms, s);
+    return f != cudaSuccess ? f : launch_fold(A, s);
+  }
+  out->splits = A.splits;
+  out->blocks = A.bstart[n];
+  for (int i = 0; i < n; ++i) out->start[i] = A.bstart[i];
+  return launch_tiles<false, true, CACHE>(A, maps, sms, s);
 }
 
 }  // namespace oscar

@@ -295,6 +295,28 @@ oscar_status oscar_extend(oscar_cache* cache, int32_t layer, int32_t n, const in
 oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* starts,
                         const int32_t* counts, void* k_out, void* v_out, int32_t out_type, void* stream);
 
+/* Attention of new_lens[i] new tokens of each request, at positions T, T + 1, ... of its T
+ * cached tokens: each sees every cached token and the new ones up to itself,
+ *   out = softmax(scale q [K_cache | K_new]^T) [V_cache | V_new],
+ * K_cache and V_cache being what oscar_read gives ([MS] section "OSCAR的设计").  The cache is
+ * not changed: tokens that are kept are then appended by oscar_extend, drafted ones that are
+ * not are dropped.  A request may have nothing cached, and may be given more than once
+ * (several drafts).  Query head h goes against kv head h / (Hq / Hkv).
+ *   q          device bf16 [rows][Hq][128], k and v [rows][Hkv][128], strided.
+ *   out        device bf16 [rows][Hq][128], dense; may not overlap q, k or v.
+ *   workspace  device, >= oscar_chunk_workspace_bytes() (for these new_lens, whatever the
+ *              requests hold), 256-byte aligned; no contents are needed.  Calls that share
+ *              a workspace must not overlap on the GPU.
+ * New tokens that a query does not see must hold finite values.  Sums and softmax statistics are
+ * fp32; in the history, q R_K, the values z + s c and the weights are rounded to 11 bits, elsewhere
+ * weights to 8.  Page ids out of range and waits that gave up are reported by
+ * oscar_cache_check. */
+oscar_status oscar_chunk_workspace_bytes(const oscar_cache* cache, int32_t n, const int32_t* new_lens, size_t* bytes);
+oscar_status oscar_chunk_attention(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs,
+                                   const int32_t* new_lens, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                                   int64_t k_stride, const uint16_t* v, int64_t v_stride, uint16_t* out,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Failure-detection hooks of the decode launches of this cache (test use; the
  * pages have no counterpart).  wait_limit: rounds (up to 20 us each) a bounded
  * device wait on a page copy makes before it gives up and reports
