@@ -64,7 +64,7 @@ struct ScanArgs {
   int64_t total;                          // units in all
   int32_t ctas, n, layer, setup;
   int32_t Hq, Hkv, G, lg;                 // lg = log2 G
-  float scale2;                           // softmax scale x log2(e) x 2 (keys are halves of themselves)
+  float scale2;                           // softmax scale x log2(e)
   int32_t slot[CHUNK_MAX_REQ];
   int32_t m[CHUNK_MAX_REQ];               // new tokens
   int32_t row[CHUNK_MAX_REQ];             // first row of q and out
@@ -90,8 +90,9 @@ struct MergeArgs {
   const float* near;
   uint16_t* out;
   int32_t near_splits, near_blocks;
+  int32_t chunks;                         // pieces of a kv head's rows, and those before request i
   int32_t near_start[CHUNK_MAX_REQ];
-  int32_t chunk[CHUNK_MAX_REQ];           // CTAs of a kv head before request i
+  int32_t chunk[CHUNK_MAX_REQ];
 };
 cudaError_t launch_chunk_merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, bool pair, int sms, cudaStream_t s);
 

@@ -9,9 +9,8 @@
 //   chunk_merge_kernel     their sum, the history's times R_V^T, over the weights' sum.
 //
 // chunk_scan_kernel: a CTA takes 128 keys at a time.  Four warps unpack them, a key a thread,
-// into fp16 values (z + s c) / 2 in shared memory (the half keeps thresholds up to 65504 in
-// range; rounded once, half a step 2^-12), from codes that were fetched into registers a step
-// before.  Per key tile and chain
+// into fp16 values z + s c in shared memory (times a power of two that keeps them in range;
+// rounded once, half a step 2^-12), from codes that were fetched into registers two steps before.  Per key tile and chain
 //   S = Q K^T            128 x 128 x 128, tcgen05.mma, both operands in shared memory
 //   p = exp2(S scale - m + 11)   one thread per row; fp16 (2^-12; the shift keeps weights down to
 //                        2^-25 of the row's largest in full, where fp16 alone would flush them)
@@ -37,31 +36,42 @@ namespace {
 using namespace paged;
 
 constexpr int SC_THREADS = 512;                // softmax of chain 0, of chain 1, unpacking, the others
-constexpr int SC_UNPACK_WARP = 8, SC_MMA_WARP = 12, SC_LOAD_WARP = 14;
-// Registers a thread: 128 at launch, then 168 for the softmax's two warpgroups, 104 for the one
-// that unpacks, 72 for the last.
-constexpr int SC_REGS = 128, SC_SOFTMAX_REGS = 168, SC_UNPACK_REGS = 104, SC_OTHER_REGS = 72;
-static_assert(2 * SC_SOFTMAX_REGS + SC_UNPACK_REGS + SC_OTHER_REGS <= 4 * SC_REGS,
-              "a split above the launch's registers waits forever");
+constexpr int SC_UNPACK_WARP = 8, SC_MMA_WARP = 12, SC_LOAD_WARP = 14, SC_FETCH_WARP = 15;
+// Registers a thread: 128 at launch, then 168 for the softmax's two warpgroups, which hold a row
+// of logits each, and 88 for the other two.
+constexpr int SC_REGS = 128, SC_SOFTMAX_REGS = 168, SC_OTHER_REGS = 88;
+static_assert(2 * SC_SOFTMAX_REGS + 2 * SC_OTHER_REGS <= 4 * SC_REGS, "a split above the launch's registers waits forever");
 constexpr int SC_STAGES = 2;                   // of V of a key tile and K of the next
 constexpr int SC_ROWS = 128, SC_KEYS = 128;
-constexpr int SC_FIRST = 64;                   // keys of P handed over first
 constexpr float SC_LAZY = 4.0f;                // the softmax reference moves only when exceeded by 2^4
 constexpr float SC_SHIFT = 11.0f;              // weights are at most 2^15, and fp16's steps below 2^-14 cost nothing
 
+// Packed keys and values of a step: K codes of 128 keys, V codes of 128, K {s, z}, V {s, z}.
+template <int GK>
+struct Raw {
+  static constexpr int META = SC_KEYS * meta_bytes_for(GK);
+  alignas(16) uint8_t code[2][SC_KEYS * CODE_BYTES];
+  alignas(16) uint8_t meta[2][META];
+};
+template <int GK, bool PAIR>
 struct alignas(1024) ScanSmem {
+  // steps of packed data in flight; where one tile of queries is enough, also in the other's place
+  static constexpr int SLOTS = PAIR ? 2 : 2 + static_cast<int>(TILE_BYTES / sizeof(Raw<GK>));
   alignas(1024) uint8_t q[2][TILE_BYTES];                // two halves of 64 channels, [128 rows][128 B] swizzled
   alignas(1024) uint8_t kv[SC_STAGES][2][TILE_BYTES];    // V of an earlier key tile, K of this one
-  alignas(16) uint8_t out[8][32 * 128];                  // per softmax warp: 128 bytes of its 32 rows
-  uint64_t q_full, q_empty, kv_full[SC_STAGES], kv_empty[SC_STAGES];
+  alignas(128) Raw<GK> raw[2];
+  alignas(16) uint8_t out[8][32 * 32];                   // per softmax warp: 32 bytes of its 32 rows
+  uint64_t q_full, q_empty, kv_full[SC_STAGES], kv_empty[SC_STAGES], raw_full[SLOTS], raw_empty[SLOTS];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], turn[2];
   uint32_t tmem;
+  __device__ Raw<GK>& slot(int i) {
+    return i < 2 ? raw[i] : reinterpret_cast<Raw<GK>*>(q[1])[i - 2];
+  }
 };
-static_assert(sizeof(ScanSmem) + 1024 <= 232448, "shared memory of a CTA");
+static_assert(sizeof(ScanSmem<64, true>) + 1024 <= 232448 && sizeof(ScanSmem<64, false>) + 1024 <= 232448 &&
+                  sizeof(ScanSmem<128, false>) + 1024 <= 232448,
+              "shared memory of a CTA");
 
-__device__ __forceinline__ uint32_t tile_at(int row, int part) {
-  return (part >> 3) * (TILE_BYTES / 2) + row * 128 + (((part & 7) ^ (row & 7)) << 4);
-}
 
 // A CTA's walk along its range of the line of key tiles.
 struct Segment {
@@ -121,16 +131,22 @@ struct Walk {
   }
 };
 
-// The 16 codes of a word as (z + s c) / 2, s and z given as halves in both halves: half2 i holds
-// channels i and i + 8.  A code in the low mantissa bits of 2^e, e such that they count ones, is 2^e + c.
-__device__ __forceinline__ void unpack(uint32_t w, __half2 s, __half2 z, uint32_t (&x)[8]) {
+// Values of a kv head in the scan are x 2^-k with 2^k from 2^8 tau to 2^9 tau (|x| <= tau, s <= 2/3 tau):
+// a code's two bits, as the half that they are where they stand in a word, count c 2^(2 at - 24), and
+// s 2^(24 - 2 at - k) is a half too, at most 2^16 2/3, so that one fma gives z + s c rounded once.
+// What falls below fp16's normal values is then off by at most 2^-17 tau.
+__device__ __forceinline__ int value_exponent(float tau) { return static_cast<int>(__float_as_uint(tau) >> 23) - 127 + 9; }
+__device__ __forceinline__ float pow2(int e) {   // (thresholds below 2^-100 hold nothing that fp16 can)
+  return __uint_as_float(static_cast<uint32_t>(127 + min(max(e, -126), 126)) << 23);
+}
+
+// The 16 codes of a word as values: half2 i holds channels i and i + 8.  s[at]: see above.
+__device__ __forceinline__ void unpack(uint32_t w, const __half2 (&s)[5], __half2 z, uint32_t (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int at = i % 5, shift = 2 * (i - at);
-    const uint32_t base = 0x6400u - (2u * at << 10);   // 2^(10 - 2 at)
-    const uint32_t bits = ((w >> shift) & (0x00030003u << (2 * at))) | (base | base << 16);
-    const __half2 one = __halves2half2(__ushort_as_half(base), __ushort_as_half(base));
-    const __half2 v = __hfma2(__hsub2(*reinterpret_cast<const __half2*>(&bits), one), s, z);
+    const uint32_t bits = (w >> shift) & (0x00030003u << (2 * at));
+    const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&bits), s[at], z);
     x[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
 }
@@ -140,8 +156,9 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
     chunk_scan_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
                       const __grid_constant__ CUtensorMap q_map) {
   extern __shared__ uint8_t sc_raw[];
-  ScanSmem& sm = *reinterpret_cast<ScanSmem*>(sc_raw + (-smem_u32(sc_raw) & 1023u));
-  constexpr int NG = D / GK;
+  using Smem = ScanSmem<GK, PAIR>;
+  Smem& sm = *reinterpret_cast<Smem*>(sc_raw + (-smem_u32(sc_raw) & 1023u));
+  constexpr int NG = D / GK, SLOTS = Smem::SLOTS;
   constexpr int LAG = PAIR ? 1 : 2;   // steps between a tile's K and its V: a chain takes every LAG-th step
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
@@ -149,6 +166,10 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
     for (int s = 0; s < SC_STAGES; ++s) {
       mbar_init(&sm.kv_full[s], 4);
       mbar_init(&sm.kv_empty[s], PAIR ? 2 : 1);
+    }
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&sm.raw_full[s], 1);
+      mbar_init(&sm.raw_empty[s], 4);
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 2);
@@ -205,6 +226,65 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
           mbar_wait(&sm.q_full, (loads - 1) & 1);
           if (ok) mbar_wait(&sm.q_empty, (loads - 1) & 1);
         }
+      }
+    } else if (warp == SC_FETCH_WARP) {
+      // ---- packed keys and values: 1152 bytes (1280 with two groups) of each page
+      if (lane == 0) {
+        const uint8_t* const pool = c.int2 + A.layer * c.int2_layer_stride;
+        const size_t page_bytes = (size_t)c.Hkv * c.record;
+        bool ok = true;
+        int step = 0;
+        auto copy = [&](Raw<GK>& raw, int u, int page, int head, int which, uint64_t* bar) {
+          const uint8_t* rec = pool + page * page_bytes + head * c.record;
+          tma_load_1d(raw.code[which] + u * (PAGE * CODE_BYTES), rec + (which ? V_CODES_OFF : K_CODES_OFF), PAGE * CODE_BYTES, bar);
+          tma_load_1d(raw.meta[which] + u * (Raw<GK>::META / 2), rec + (which ? v_meta_off_for(GK) : k_meta_off_for(GK)),
+                      Raw<GK>::META / 2, bar);
+        };
+        Walk w = Walk::begin(A);
+        for (; ok && w.next(A); w.done(A)) {
+          const int n = w.s.j1 - w.s.j0, pages = (A.hist[w.s.req] + PAGE - 1) / PAGE - 2 * w.s.j0, head = w.s.head;
+          const int32_t* table = c.hist_pt + (size_t)A.slot[w.s.req] * c.max_pages + 2 * w.s.j0;
+          // page ids of tile i, looked up a step ahead (-1: none); V takes those of LAG steps before
+          int id[LAG + 2][2];
+          auto look = [&](int i, int (&to)[2]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) to[u] = i < n && 2 * i + u < pages ? table[2 * i + u] : -1;
+          };
+#pragma unroll
+          for (int j = 0; j < LAG; ++j) id[j][0] = id[j][1] = -1;
+          look(0, id[LAG]);
+          for (int i = 0; i < n + LAG && ok; ++i, ++step) {
+            look(i + 1, id[LAG + 1]);
+            const int at = step % SLOTS;
+            if (step >= SLOTS) ok = mbar_wait(&sm.raw_empty[at], (step / SLOTS - 1) & 1);
+            if (!ok) break;
+            int use[2][2], some = 0;   // [K or V][page]
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int which = 0; which < 2; ++which) {
+                const bool there = which ? i >= LAG && 2 * (i - LAG) + u < pages : i < n && 2 * i + u < pages;
+                int page = id[which ? 0 : LAG][u];
+                if (there && (page < 0 || page >= c.n_int2_pages)) {
+                  atomicOr(c.err, ERR_INT2_PAGE);
+                  page = 0;
+                }
+                use[which][u] = there ? page : -1;
+                some += there;
+              }
+            mbar_expect_tx(&sm.raw_full[at], some * (PAGE * CODE_BYTES + Raw<GK>::META / 2));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int which = 0; which < 2; ++which)
+                if (use[which][u] >= 0) copy(sm.slot(at), u, use[which][u], head, which, &sm.raw_full[at]);
+#pragma unroll
+            for (int j = 0; j <= LAG; ++j) id[j][0] = id[j + 1][0], id[j][1] = id[j + 1][1];
+          }
+        }
+        if (!ok) gave_up();
+        // nothing may arrive after the CTA
+        for (int k = max(0, step - SLOTS); k < step; ++k) mbar_wait(&sm.raw_full[k % SLOTS], (k / SLOTS) & 1);
       }
     } else if (warp < SC_LOAD_WARP) {
       // ---- products of chain a
@@ -279,110 +359,59 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
     }
   } else if (warp >= SC_UNPACK_WARP) {
     // ---- keys and values, a key a thread
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SC_UNPACK_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SC_OTHER_REGS));
     const int r = threadIdx.x & (SC_KEYS - 1);
-    // steps looked up ahead: where the key's record is (null: zeros) for K of a step; V of a tile takes
-    // that of LAG steps before
-    struct Ahead {
-      Walk w;
-      int i, n;
-      bool some;
-    };
-    Ahead at;
-    at.w = Walk::begin(A);
-    at.some = at.w.next(A);
-    at.i = 0;
-    at.n = at.some ? at.w.s.j1 - at.w.s.j0 : 0;
-    // one step ahead of the data: page ids, and what else the record's address needs
-    struct Look {
-      int page, head;   // page as the table has it
-      bool some, live;  // a key; a step (not behind the end)
-    };
-    auto look = [&]() {
-      Look l{0, 0, false, at.some};
-      if (!at.some) return l;
-      if (at.i < at.n) {
-        const int t = (at.w.s.j0 + at.i) * SC_KEYS + r;
-        if (t < A.hist[at.w.s.req]) {
-          l.page = c.hist_pt[(size_t)A.slot[at.w.s.req] * c.max_pages + t / PAGE];
-          l.head = at.w.s.head;
-          l.some = true;
-        }
-      }
-      if (++at.i == at.n + LAG) {
-        at.w.done(A);
-        at.some = at.w.next(A);
-        at.i = 0;
-        at.n = at.some ? at.w.s.j1 - at.w.s.j0 : 0;
-      }
-      return l;
-    };
-    struct Data {
-      uint4 w[2];
-      uint32_t meta[NG];
-    };
-    auto fetch = [&](const Look& l, int which) {
-      Data d;
-      d.w[0] = d.w[1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int n = 0; n < NG; ++n) d.meta[n] = 0;
-      if (l.some && (l.page < 0 || l.page >= c.n_int2_pages)) {
-        atomicOr(c.err, ERR_INT2_PAGE);   // (zeros)
-      } else if (l.some) {
-        const uint8_t* rec = int2_record(c, A.layer, l.page, l.head);
-        const uint4* code = reinterpret_cast<const uint4*>(rec + (which ? V_CODES_OFF : K_CODES_OFF) + (r % PAGE) * CODE_BYTES);
-        d.w[0] = code[0];
-        d.w[1] = code[1];
-        const uint32_t* m = reinterpret_cast<const uint32_t*>(
-            rec + (which ? v_meta_off_for(GK) : k_meta_off_for(GK)) + (r % PAGE) * meta_bytes_for(GK));
-#pragma unroll
-        for (int n = 0; n < NG; ++n) d.meta[n] = m[n];
-      }
-      return d;
-    };
-    auto put = [&](uint8_t* tile, const Data& d) {
-      const uint32_t w[8] = {d.w[0].x, d.w[0].y, d.w[0].z, d.w[0].w, d.w[1].x, d.w[1].y, d.w[1].z, d.w[1].w};
-      const __half2 half = __float2half2_rn(0.5f);
-      __half2 s, z;
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        if (p % (8 / NG) == 0) {
-          const uint32_t m = d.meta[p / (8 / NG)], lo = m & 0xffff, hi = m >> 16;
-          const uint32_t ss = lo | lo << 16, zz = hi | hi << 16;
-          s = __hmul2(*reinterpret_cast<const __half2*>(&ss), half);
-          z = __hmul2(*reinterpret_cast<const __half2*>(&zz), half);
-        }
-        uint32_t x[8];
-        unpack(w[p], s, z, x);
-        *reinterpret_cast<uint4*>(tile + tile_at(r, 2 * p)) = make_uint4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<uint4*>(tile + tile_at(r, 2 * p + 1)) = make_uint4(x[4], x[5], x[6], x[7]);
-      }
-    };
     bool ok = true;
-    const Look none{0, 0, false, true};
-    Look back[LAG];                     // K's records of the LAG steps before
+    int step = 0;
+    Walk w = Walk::begin(A);
+    for (; ok && w.next(A); w.done(A)) {
+      const int n = w.s.j1 - w.s.j0, left = A.hist[w.s.req] - w.s.j0 * SC_KEYS - r;   // keys from this thread's of tile 0 on
+      const size_t lh = (size_t)A.layer * c.Hkv + w.s.head;
+      const int k_exp = value_exponent(c.tau_k[lh]), v_exp = value_exponent(c.tau_v[lh]);
+      for (int i = 0; i < n + LAG && ok; ++i, ++step) {
+        const int st = step % SC_STAGES, at = step % SLOTS;
+        const Raw<GK>& raw = sm.slot(at);
+        ok = mbar_wait_warp(&sm.raw_full[at], (step / SLOTS) & 1, ok);
+        if (step >= SC_STAGES) ok = mbar_wait_warp(&sm.kv_empty[st], (step / SC_STAGES - 1) & 1, ok);
+        if (!ok) break;
+        // V of tile i - LAG, K of tile i (a loop: the code of four roles together is more than the instruction
+        // caches hold)
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          const int which = u ^ 1, tile = u ? i : i - LAG, e = u ? k_exp : v_exp;
+          const bool some = tile >= 0 && tile < n && tile * SC_KEYS < left;
+          const uint2* code = reinterpret_cast<const uint2*>(raw.code[which]) + 4 * r;
+          const uint32_t* meta = reinterpret_cast<const uint32_t*>(raw.meta[which]) + NG * r;
+          const __half2 quarter = __float2half2_rn(0.25f);
 #pragma unroll
-    for (int i = 0; i < LAG; ++i) back[i] = none;
-    Look now = look(), next = look();
-    Data k = fetch(now, 0), v = fetch(none, 1);
-    for (int step = 0; now.live; ++step) {
-      const int st = step % SC_STAGES;
-      if (step >= SC_STAGES) ok = mbar_wait_warp(&sm.kv_empty[st], (step / SC_STAGES - 1) & 1, ok);
-      if (!ok) break;
-      const Data k_now = k, v_now = v;
-      // what this step's record was for K is, LAG steps on, V's
+          for (int h = 0; h < 2; ++h) {   // 64 channels
+            uint8_t* to = sm.kv[st][u] + h * (TILE_BYTES / 2) + r * 128;
+            const uint32_t m = some ? meta[NG == 2 ? h : 0] : 0;
+            __half2 s[5];
+            s[0] = __float2half2_rn(__half2float(__ushort_as_half(m & 0xffff)) * pow2(24 - e));
+            const __half2 z = __float2half2_rn(__half2float(__ushort_as_half(m >> 16)) * pow2(-e));
 #pragma unroll
-      for (int i = LAG - 1; i > 0; --i) back[i] = back[i - 1];
-      back[0] = now;
-      k = fetch(next, 0);
-      v = fetch(back[LAG - 1], 1);
-      now = next;
-      next = look();
-      put(sm.kv[st][0], v_now);
-      put(sm.kv[st][1], k_now);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.kv_full[st]);
+            for (int j = 1; j < 5; ++j) s[j] = __hmul2(s[j - 1], quarter);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const uint2 word = some ? code[2 * h + p] : make_uint2(0, 0);
+              uint32_t x[8];
+              unpack(word.x, s, z, x);
+              *reinterpret_cast<uint4*>(to + (((4 * p) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(to + (((4 * p + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+              unpack(word.y, s, z, x);
+              *reinterpret_cast<uint4*>(to + (((4 * p + 2) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(to + (((4 * p + 3) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.kv_full[st]);
+          mbar_arrive(&sm.raw_empty[at]);
+        }
+      }
     }
     if (!ok && lane == 0) gave_up();
   } else {
@@ -391,6 +420,15 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
     const int a = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = lane_off + 128 * a, to = lane_off + 256 + 128 * a;
+    auto meet_chain = [&](bool mine) {   // a barrier of the chain's four warps: whether all say yes
+      int all;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, 128, p;\n selp.b32 %0, 1, 0, q;\n}"
+          : "=r"(all)
+          : "r"(static_cast<int>(mine)), "r"(a + 1)
+          : "memory");
+      return all != 0;
+    };
     bool ok = true;
     int tile = 0, outs = 0, step0 = 0;   // key tiles and segments of this chain so far; steps of the CTA
     Walk w = Walk::begin(A);
@@ -401,34 +439,40 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       if (PAIR && a >= row_tiles(s)) continue;
       const int m = A.m[s.req], tok0 = (s.block * (PAIR ? 2 : 1) + (PAIR ? a : 0)) * per_tile, tok = tok0 + (r >> A.lg);
       const int row = A.row[s.req] + min(tok, m - 1);
-      const float scale2 = A.scale2 * A.q_scale[(size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))];
-      const int hist = A.hist[s.req];
+      const float scale2 = A.scale2 * A.q_scale[(size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))] *
+                           pow2(value_exponent(c.tau_k[(size_t)A.layer * c.Hkv + s.head]));
+      // warps of the tile that have rows; the first arrives for those without, which only meet the others behind the
+      // segment: whatever their rows of P are, a row of O has the same row of P alone
+      const int busy = min(4, (((m - tok0) << A.lg) + 31) / 32);
+      const uint32_t arrivals = (warp & 3) == 0 ? 5 - busy : 1;
+      const bool idle = (warp & 3) >= busy;
+      int left = A.hist[s.req] - (s.j0 + from) * SC_KEYS;   // keys from the tile on
       float mx = NEG_INF, l = 0.0f;
       bool any = false;
-      for (int i = from; i < n; i += LAG, ++tile) {
+      const int tiles = n > from ? (n - from + LAG - 1) / LAG : 0;   // of the chain
+      if (idle) tile += tiles;
+      for (int i = idle ? n : from; i < n; i += LAG, ++tile, left -= LAG * SC_KEYS) {
         ok = mbar_wait_warp(&sm.s_full[a], tile & 1, ok);
         if (!ok) break;
         tc_fence_after();
-        const int left = hist - (s.j0 + i) * SC_KEYS;   // keys of the tile, at least one
-        float t[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+        uint32_t xr[128];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[64];
-          tmem_ld32(ts + 64 * h, x);
-          tmem_ld32(ts + 64 * h + 32, x + 32);
-          tc_wait_ld();
-          if (left < SC_KEYS) {
+        for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, xr + 32 * h);
+        tc_wait_ld();
+        float* x = reinterpret_cast<float*>(xr);
+        if (left < SC_KEYS) {   // keys behind the end
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (64 * h + j >= left) x[j] = __float_as_uint(NEG_INF);
-          }
-#pragma unroll
-          for (int j = 0; j < 64; j += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              t[k] = max3(t[k], __uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1]));
+          for (int j = 0; j < SC_KEYS; ++j)
+            if (j >= left) x[j] = NEG_INF;
         }
-        const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * scale2;
+        float t[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = x[k];
+#pragma unroll
+        for (int j = 4; j < 124; j += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[j + 2 * k], x[j + 2 * k + 1]);
+        const float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])) * scale2;
         const bool raise = top > mx + SC_LAZY || (mx == NEG_INF && top > NEG_INF);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
@@ -436,7 +480,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
           if (raise) mx = top;
           if (any) {   // the product before S is done: S was issued after it
 #pragma unroll 1
-            for (int col = 0; col < 128; col += 16) {
+            for (int col = 0; col < 128; col += 16) {   // in small pieces: the logits are live
               uint32_t o[16];
               tmem_ld16(to + col, o);
               tc_wait_ld();
@@ -453,19 +497,11 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t x[32], pk[16];
-          tmem_ld32(ts + 32 * h, x);
-          tc_wait_ld();
-          if (left < SC_KEYS) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * h + j >= left) x[j] = __float_as_uint(NEG_INF);
-          }
+        for (int h = 0; h < 4; ++h) {   // 32 keys
           float2 y[16];
+          uint32_t pk[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            y[j] = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), scale_2, ref_2);
+          for (int j = 0; j < 16; ++j) y[j] = fma2(make_float2(x[32 * h + 2 * j], x[32 * h + 2 * j + 1]), scale_2, ref_2);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             y[j].x = ex2f(y[j].x);
@@ -476,27 +512,26 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
             pk[j] = f16x2(y[j].x, y[j].y);
             sum[j & 3] = add2(sum[j & 3], y[j]);
           }
-          tmem_st16(ts + 64 * (h / 2) + 16 * (h % 2), pk);   // P lies over S
-          if (h == SC_FIRST / 32 - 1 || h == 3) {
+          tmem_st16(ts + 64 * (h >> 1) + 16 * (h & 1), pk);   // P lies over S, 64 keys in 32 columns
+          if (h & 1) {
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[a][h == 3]);
+            if (lane == 0) mbar_arrive(&sm.p_full[a][h >> 1], arrivals);
           }
         }
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
       }
-      if (!ok) break;
       // the rows' sums, maximum and sum to the workspace
-      const int warp_tok = tok0 + (32 * (warp & 3) >> A.lg);
-      if (any) {
-        ok = mbar_wait_warp(&sm.o_full[a], outs & 1, ok);
+      if (tiles > 0) {
+        if (!idle) ok = mbar_wait_warp(&sm.o_full[a], outs & 1, ok);
+        ok = meet_chain(ok);
         if (!ok) break;
         tc_fence_after();
         ++outs;
       }
-      if (warp_tok < m) {
+      if (!idle) {
         float* part = A.records + ((size_t)(s.index + blockIdx.x) * 2 + a) * SC_ROWS * PARTIAL_FLOATS;
         part[r * PARTIAL_FLOATS + PARTIAL_M] = mx - SC_SHIFT;
         part[r * PARTIAL_FLOATS + PARTIAL_L] = l;
@@ -504,29 +539,33 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
 #pragma unroll 1
         for (int col = 0; col < 128; col += 32) {
           uint32_t o[32];
-          if (any) {
+          if (tiles > 0) {
             tmem_ld32(to + col, o);
             tc_wait_ld();
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0;
           }
+          // turned through shared memory, so that two lanes store 32 bytes of a row together
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          __syncwarp();
-#pragma unroll 4
-          for (int k = 0; k < 8; ++k) {
-            const int rw = 4 * k + lane / 8, rr = 32 * (warp & 3) + rw;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
-            if (tok0 + (rr >> A.lg) < m)
-              *reinterpret_cast<uint4*>(part + rr * PARTIAL_FLOATS + col + 4 * (lane & 7)) = v;
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ (lane >> 2 & 1)) << 4)) =
+                  make_uint4(o[8 * j + 4 * k], o[8 * j + 4 * k + 1], o[8 * j + 4 * k + 2], o[8 * j + 4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int rw = 16 * k + lane / 2, rr = 32 * (warp & 3) + rw;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * 32 + (((lane & 1) ^ (rw >> 2 & 1)) << 4));
+              if (tok0 + (rr >> A.lg) < m)
+                *reinterpret_cast<uint4*>(part + rr * PARTIAL_FLOATS + col + 8 * j + 4 * (lane & 1)) = v;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
-      if (any) {   // O is read: the next segment may write it
+      if (tiles > 0) {   // O is read: the next segment may write it
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_empty[a]);
@@ -546,10 +585,8 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
 constexpr int PITCH = D + 8;   // bf16 elements of a row in shared memory: ldmatrix without conflicts
 constexpr int MG_THREADS = 256;
 
-// Position 16 k + 2 i + b of a row that unpack() orders holds channel 16 k + 8 b + i.
-__device__ __forceinline__ int channel_at(int pos) { return (pos & ~15) + 8 * (pos & 1) + ((pos >> 1) & 7); }
-
-// A rotation (rows: outputs) as two bf16 parts, its columns as they are or in unpack()'s order.
+// A rotation (rows: outputs) as two bf16 parts, its columns as they are or in unpack()'s order:
+// position 16 k + 2 i + b holds channel 16 k + 8 b + i.
 struct Parts {
   alignas(16) uint16_t hi[D][PITCH], lo[D][PITCH];
 };
@@ -594,64 +631,78 @@ __device__ __forceinline__ void multiply_rows(float (&acc)[MT][2][4], const uint
   }
 }
 
-template <int MT>
+constexpr int UNIT = 16;       // rows of a warp's product
 struct RotateSmem {
   Parts r;
-  alignas(16) uint16_t q[16 * MT][PITCH];
-  alignas(16) float x[16 * MT][D + 4];
+  alignas(16) uint16_t q[8][UNIT][PITCH];
 };
-// 16 MT rows -- (token, head of the group), whatever requests they are of -- of one kv head.
-template <int MT>
-__global__ void __launch_bounds__(MG_THREADS)
-    rotate_queries_kernel(const __grid_constant__ DevCache c, const __grid_constant__ RotateArgs A) {
+// A warp takes 16 rows -- (token, head of the group), whatever requests they are of -- of one
+// kv head at a time; the CTA keeps that head's rotation.
+__global__ void __launch_bounds__(MG_THREADS, 2)
+    rotate_queries_kernel(const __grid_constant__ DevCache c, const __grid_constant__ RotateArgs A, int per_head) {
   extern __shared__ __align__(16) uint8_t rt_raw[];
-  RotateSmem<MT>& sm = *reinterpret_cast<RotateSmem<MT>*>(rt_raw);
+  RotateSmem& sm = *reinterpret_cast<RotateSmem*>(rt_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = blockIdx.x % c.Hkv;
-  const int64_t row0 = (int64_t)(blockIdx.x / c.Hkv) * (16 * MT), rows = (int64_t)A.rows << A.lg;
-  const int G = 1 << A.lg, Hq = G * c.Hkv;
+  const int head = blockIdx.x / per_head, G = 1 << A.lg, Hq = G * c.Hkv;
+  const int64_t rows = (int64_t)A.rows << A.lg;
   split_rotation<false>(c.rot_kt + ((size_t)A.layer * c.Hkv + head) * D * D, sm.r);   // (before the grid's dependency)
   grid_dep_launch();
   grid_dep_wait();
-#pragma unroll
-  for (int u = 0; u < MT; ++u) {
-    const int r = 16 * u + threadIdx.x / 16, p = threadIdx.x % 16;
-    const int64_t row = row0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rows)
-      v = reinterpret_cast<const uint4*>(A.q + (row >> A.lg) * A.q_stride + (size_t)(head * G + (row & (G - 1))) * D)[p];
-    *reinterpret_cast<uint4*>(&sm.q[r][8 * p]) = v;
-  }
   __syncthreads();
-  float acc[MT][2][4] = {};
-  multiply_rows<MT>(acc, sm.q, sm.r.lo);
-  multiply_rows<MT>(acc, sm.q, sm.r.hi);
+  uint16_t (*q)[PITCH] = sm.q[warp];
+  for (int64_t row0 = ((int64_t)(blockIdx.x % per_head) * 8 + warp) * UNIT; row0 < rows; row0 += (int64_t)per_head * 8 * UNIT) {
+    uint4 v[UNIT / 2];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int u = 0; u < UNIT / 2; ++u) {
+      const int64_t row = row0 + 2 * u + lane / 16;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        v[u] = reinterpret_cast<const uint4*>(A.q + (row >> A.lg) * A.q_stride + (size_t)(head * G + (row & (G - 1))) * D)[lane % 16];
+    }
+    __syncwarp();
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int u = 0; u < UNIT / 2; ++u) *reinterpret_cast<uint4*>(&q[2 * u + lane / 16][8 * (lane % 16)]) = v[u];
+    __syncwarp();
+    uint32_t a[8][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(&sm.x[16 * i + lane / 4 + 8 * h][16 * warp + 8 * n + 2 * (lane & 3)]) =
-            make_float2(acc[i][n][2 * h], acc[i][n][2 * h + 1]);
-  __syncthreads();
-#pragma unroll 2
-  for (int r = warp; r < 16 * MT && row0 + r < rows; r += 8) {
-    float y[4], top = 0.0f;
+    for (int s = 0; s < 8; ++s) ldsm4(a[s], smem_u32(&q[lane & 15][16 * s + 8 * (lane >> 4)]));
+    float x[16][4];
+    float top[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[j] = sm.x[r][channel_at(4 * lane + j)];
-      top = fmaxf(top, fabsf(y[j]));
+    for (int n = 0; n < 16; n += 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] = x[n + 1][i] = 0.0f;
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          uint32_t b[4];
+          const uint16_t (*w)[PITCH] = part ? sm.r.hi : sm.r.lo;
+          ldsm4(b, smem_u32(&w[8 * n + (lane & 7) + 8 * (lane >> 4)][16 * s + 8 * ((lane >> 3) & 1)]));
+          mma_bf16(x[n], a[s], b[0], b[1]);
+          mma_bf16(x[n + 1], a[s], b[2], b[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i / 2] = fmaxf(top[i / 2], fmaxf(fabsf(x[n][i]), fabsf(x[n + 1][i])));
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    // 2^e with 2^10 <= top 2^e < 2^11, so that what falls below fp16's normal values is below 2^-24 of the row's largest
-    const int e = min(max(137 - static_cast<int>(__float_as_uint(top) >> 23), -100), 100);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    const int64_t row = row0 + r;
-    const size_t at = (size_t)(row >> A.lg) * Hq + head * G + (row & (G - 1));
-    reinterpret_cast<uint2*>(A.out + at * D)[lane] = make_uint2(f16x2(y[0] * up, y[1] * up), f16x2(y[2] * up, y[3] * up));
-    if (lane == 0) A.scale[at] = down;
+    for (int h = 0; h < 2; ++h) {   // this thread's columns of row lane / 4 + 8 h
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+      // 2^e with 2^10 <= top 2^e < 2^11, so that what falls below fp16's normal values is below 2^-24 of the row's largest
+      const int e = min(max(137 - static_cast<int>(__float_as_uint(top[h]) >> 23), -100), 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const int64_t row = row0 + lane / 4 + 8 * h;
+      if (row >= rows) continue;
+      const size_t at = (size_t)(row >> A.lg) * Hq + head * G + (row & (G - 1));
+      // channels 16 k + 2 t, + 1, + 8, + 9 are positions 16 k + 4 t, + 2, + 1, + 3
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        reinterpret_cast<uint2*>(A.out + at * D)[4 * k + (lane & 3)] =
+            make_uint2(f16x2(x[2 * k][2 * h] * up, x[2 * k + 1][2 * h] * up),
+                       f16x2(x[2 * k][2 * h + 1] * up, x[2 * k + 1][2 * h + 1] * up));
+      if ((lane & 3) == 0) A.scale[at] = down;
+    }
   }
 }
 
@@ -690,6 +741,7 @@ __global__ void __launch_bounds__(MG_THREADS)
   grid_dep_wait();
   __syncthreads();
   const int64_t each = A.tiles[ri] + A.setup;
+  const float v_scale = pow2(value_exponent(c.tau_v[(size_t)A.layer * c.Hkv + head]));   // (of the scan's values)
   for (int r = warp / SHARE; r < ROWS; r += 8 / SHARE) {
     const int rr = row0 + r;
     float4 far = make_float4(0, 0, 0, 0), near = far;
@@ -750,9 +802,8 @@ __global__ void __launch_bounds__(MG_THREADS)
       near.x += y.x, near.y += y.y, near.z += y.z, near.w += y.w;
       l += sm.l[warp + 1];
     }
-    // (values are halves of themselves in the scan)
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l, twice = 2.0f * inv;
-    const float f[4] = {far.x * twice, far.y * twice, far.z * twice, far.w * twice};
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l, up = inv * v_scale;
+    const float f[4] = {far.x * up, far.y * up, far.z * up, far.w * up};
     const uint32_t h0 = bf16x2(f[0], f[1]), h1 = bf16x2(f[2], f[3]);
     *reinterpret_cast<uint2*>(&sm.hi[r][4 * lane]) = make_uint2(h0, h1);
     *reinterpret_cast<uint2*>(&sm.lo[r][4 * lane]) =
@@ -786,9 +837,151 @@ __global__ void __launch_bounds__(MG_THREADS)
   }
 }
 
-// A kernel's shared memory (and, where it counts on them, registers), set once per device.
+struct MergeRowsSmem {
+  alignas(16) uint16_t r[D][PITCH];            // fp16, columns in unpack()'s order
+  alignas(16) uint16_t row[8][UNIT][PITCH];    // a warp's rows: the history's sums (fp16), then the results (bf16)
+};
+// A warp takes 16 rows of one request and kv head at a time; the CTA keeps that head's rotation.  (The history's
+// sums over the weights' and R are rounded to fp16, 2^-12 each, an eighth of what the result's rounding adds.)
+template <bool PAIR>
+__global__ void __launch_bounds__(MG_THREADS, 2)
+    chunk_merge_rows_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
+                            const __grid_constant__ MergeArgs B, int per_head) {
+  extern __shared__ __align__(16) uint8_t mr_raw[];
+  MergeRowsSmem& sm = *reinterpret_cast<MergeRowsSmem*>(mr_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = 1 << A.lg;
+  const int head = blockIdx.x / per_head;
+  {
+    const float* m = c.rot_v + ((size_t)A.layer * c.Hkv + head) * D * D;   // (before the grid's dependency)
+#pragma unroll 4
+    for (int i = threadIdx.x; i < D * (D / 16); i += MG_THREADS) {
+      const int n = i / (D / 16), p = i % (D / 16);
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(f + 4 * j) = reinterpret_cast<const float4*>(m + (size_t)n * D + 16 * p)[j];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<uint4*>(&sm.r[n][16 * p + 8 * j]) =
+            make_uint4(f16x2(f[4 * j], f[4 * j + 8]), f16x2(f[4 * j + 1], f[4 * j + 9]), f16x2(f[4 * j + 2], f[4 * j + 10]),
+                       f16x2(f[4 * j + 3], f[4 * j + 11]));
+    }
+  }
+  grid_dep_launch();
+  grid_dep_wait();
+  __syncthreads();
+  constexpr int BLOCK = PAIR ? 2 * SC_ROWS : SC_ROWS;
+  constexpr size_t STEP = (size_t)(PAIR ? 2 : 1) * SC_ROWS * PARTIAL_FLOATS;
+  const size_t near_step = (size_t)c.Hkv * (2 * SC_ROWS) * PARTIAL_FLOATS;
+  uint16_t (*buf)[PITCH] = sm.row[warp];
+  // the scan's values are at most 2^-8: times 2^8 here, which fp16 holds, the rest of their exponent at the end
+  const int v_exp = value_exponent(c.tau_v[(size_t)A.layer * c.Hkv + head]);
+  const float down = pow2(v_exp - 8);
+  for (int unit = (blockIdx.x % per_head) * 8 + warp; unit < B.chunks; unit += per_head * 8) {
+    int ri = 0, hi = A.n;
+    while (hi - ri > 1) {
+      const int mid = (ri + hi) >> 1;
+      if (B.chunk[mid] <= unit) ri = mid; else hi = mid;
+    }
+    const int row0 = (unit - B.chunk[ri]) * UNIT, last = (A.m[ri] << A.lg) - 1 - row0;   // the unit's last row
+    const int64_t each = A.tiles[ri] + A.setup, k = (int64_t)head * A.blocks[ri] + row0 / BLOCK, start = A.cost[ri] + k * each;
+    const int64_t c0 = chunk_of(A, start + A.setup), c1 = chunk_of(A, start + each - 1);
+    const int count = static_cast<int>(c1 - c0 + 1) * (PAIR ? 1 : 2);
+    const float* scan = A.records + ((size_t)(A.segment[ri] + k + c0) * 2 + (PAIR ? row0 % BLOCK / SC_ROWS : 0)) * SC_ROWS * PARTIAL_FLOATS +
+                        (size_t)(row0 % SC_ROWS) * PARTIAL_FLOATS;
+    const int back = B.near_blocks - 1 - (B.near_start[ri] + row0 / (2 * SC_ROWS));
+    const float* bf = B.near + (((size_t)back * B.near_splits * c.Hkv + head) * (2 * SC_ROWS) + row0 % (2 * SC_ROWS)) * PARTIAL_FLOATS;
+    // lane r: row r's maximum, weights and their sum (rows behind the last one as that)
+    const int mine = min(lane % UNIT, last) * PARTIAL_FLOATS;
+    float top = NEG_INF, l = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) top = fmaxf(top, scan[j * STEP + mine + PARTIAL_M]);
+    for (int j = 0; j < B.near_splits; ++j) top = fmaxf(top, bf[j * near_step + mine + PARTIAL_M]);
+    // (a row without a maximum goes the same way: a NaN query's sums are NaN)
+    const float ref = top == NEG_INF ? 0.0f : top;
+    for (int j = 0; j < B.near_splits; ++j) l = fmaf(bf[j * near_step + mine + PARTIAL_L], ex2f(bf[j * near_step + mine + PARTIAL_M] - ref), l);
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) l = fmaf(scan[j * STEP + mine + PARTIAL_L], ex2f(scan[j * STEP + mine + PARTIAL_M] - ref), l);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __syncwarp();
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {   // eight rows, four channels a lane
+      float4 sum[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) sum[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int j = 0; j < count; ++j) {
+        const float f = ex2f(scan[j * STEP + mine + PARTIAL_M] - ref) * inv * 256.0f;
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          v[r] = reinterpret_cast<const float4*>(scan + j * STEP + min(8 * half + r, last) * PARTIAL_FLOATS)[lane];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float w = __shfl_sync(0xffffffffu, f, 8 * half + r);
+          sum[r].x = fmaf(v[r].x, w, sum[r].x);
+          sum[r].y = fmaf(v[r].y, w, sum[r].y);
+          sum[r].z = fmaf(v[r].z, w, sum[r].z);
+          sum[r].w = fmaf(v[r].w, w, sum[r].w);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        *reinterpret_cast<uint2*>(&buf[8 * half + r][4 * lane]) = make_uint2(f16x2(sum[r].x, sum[r].y), f16x2(sum[r].z, sum[r].w));
+    }
+    __syncwarp();
+    uint32_t a[8][4];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) ldsm4(a[s], smem_u32(&buf[lane & 15][16 * s + 8 * (lane >> 4)]));
+    __syncwarp();
+    const int r0 = min(lane / 4, last) * PARTIAL_FLOATS, r1 = min(lane / 4 + 8, last) * PARTIAL_FLOATS;
+    float x[16][4];
+#pragma unroll
+    for (int n = 0; n < 16; n += 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] = x[n + 1][i] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        uint32_t b[4];
+        ldsm4(b, smem_u32(&sm.r[8 * n + (lane & 7) + 8 * (lane >> 4)][16 * s + 8 * ((lane >> 3) & 1)]));
+        mma_f16(x[n], a[s][0], a[s][1], a[s][2], a[s][3], b[0], b[1]);
+        mma_f16(x[n + 1], a[s][0], a[s][1], a[s][2], a[s][3], b[2], b[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] *= down, x[n + 1][i] *= down;
+    }
+    for (int j = 0; j < B.near_splits; ++j) {
+      const float f = ex2f(bf[j * near_step + mine + PARTIAL_M] - ref) * inv;
+      const float w0 = __shfl_sync(0xffffffffu, f, lane / 4), w1 = __shfl_sync(0xffffffffu, f, lane / 4 + 8);
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const float2 y = *reinterpret_cast<const float2*>(bf + j * near_step + r0 + 8 * n + 2 * (lane & 3));
+        const float2 z = *reinterpret_cast<const float2*>(bf + j * near_step + r1 + 8 * n + 2 * (lane & 3));
+        x[n][0] = fmaf(y.x, w0, x[n][0]);
+        x[n][1] = fmaf(y.y, w0, x[n][1]);
+        x[n][2] = fmaf(z.x, w1, x[n][2]);
+        x[n][3] = fmaf(z.y, w1, x[n][3]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      *reinterpret_cast<uint32_t*>(&buf[lane / 4][8 * n + 2 * (lane & 3)]) = bf16x2(x[n][0], x[n][1]);
+      *reinterpret_cast<uint32_t*>(&buf[lane / 4 + 8][8 * n + 2 * (lane & 3)]) = bf16x2(x[n][2], x[n][3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < UNIT / 2; ++u) {
+      const int r = 2 * u + lane / 16, rr = row0 + r;
+      if (r <= last)
+        reinterpret_cast<uint4*>(B.out + ((size_t)(A.row[ri] + (rr >> A.lg)) * A.Hq + head * G + (rr & (G - 1))) * D)[lane % 16] =
+            *reinterpret_cast<const uint4*>(&buf[r][8 * (lane % 16)]);
+    }
+    __syncwarp();
+  }
+}
+
+// A kernel's shared memory, set once per device (regs: what a split at run time counts on; the build checks it too).
 template <typename K>
-cudaError_t set_up(K kernel, int bytes, int regs, std::atomic<unsigned>& done) {
+cudaError_t set_up(K kernel, int bytes, std::atomic<unsigned>& done, int regs = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev < 32 && (done.load() & (1u << dev)))) return e;
@@ -803,54 +996,63 @@ cudaError_t set_up(K kernel, int bytes, int regs, std::atomic<unsigned>& done) {
   return e;
 }
 
-template <int MT>
-cudaError_t rotate(const DevCache& c, const RotateArgs& a, cudaStream_t s) {
-  constexpr int bytes = static_cast<int>(sizeof(RotateSmem<MT>));
-  static std::atomic<unsigned> done;
-  const cudaError_t e = set_up(rotate_queries_kernel<MT>, bytes, 0, done);
-  if (e != cudaSuccess) return e;
-  const int64_t chunks = (((int64_t)a.rows << a.lg) + 16 * MT - 1) / (16 * MT);
-  return launch_dependent(rotate_queries_kernel<MT>, static_cast<unsigned>(chunks * c.Hkv), MG_THREADS, bytes, s, c, a);
-}
 template <int GK, bool PAIR>
 cudaError_t scan(const DevCache& c, const ScanArgs& a, const CUtensorMap& q_map, cudaStream_t s) {
-  constexpr int bytes = static_cast<int>(sizeof(ScanSmem)) + 1024;
+  constexpr int bytes = static_cast<int>(sizeof(ScanSmem<GK, PAIR>)) + 1024;
   static std::atomic<unsigned> done;
-  const cudaError_t e = set_up(chunk_scan_kernel<GK, PAIR>, bytes, SC_REGS, done);
+  const cudaError_t e = set_up(chunk_scan_kernel<GK, PAIR>, bytes, done, SC_REGS);
   if (e != cudaSuccess) return e;
   return launch_dependent(chunk_scan_kernel<GK, PAIR>, static_cast<unsigned>(a.ctas), SC_THREADS, bytes, s, c, a, q_map);
 }
-template <int ROWS, bool PAIR>
-cudaError_t merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, cudaStream_t s) {
-  constexpr int bytes = static_cast<int>(sizeof(MergeSmem<ROWS>));
-  static std::atomic<unsigned> done;
-  const cudaError_t e = set_up(chunk_merge_kernel<ROWS, PAIR>, bytes, 0, done);
-  if (e != cudaSuccess) return e;
-  int chunks = 0;
+// CTAs of a kv head, of work for so many warps: two per SM in all.
+int ctas_per_head(int64_t units, int hkv, int sms) {
+  const int64_t most = (units + 7) / 8, fair = 2 * sms / hkv > 1 ? 2 * sms / hkv : 1;
+  return static_cast<int>(most < fair ? most : fair);
+}
+void count_chunks(const ScanArgs& a, MergeArgs& b, int rows) {
+  b.chunks = 0;
   for (int i = 0; i < a.n; ++i) {
-    b.chunk[i] = chunks;
-    chunks += ((a.m[i] << a.lg) + ROWS - 1) / ROWS;
+    b.chunk[i] = b.chunks;
+    b.chunks += ((a.m[i] << a.lg) + rows - 1) / rows;
   }
-  return launch_dependent(chunk_merge_kernel<ROWS, PAIR>, static_cast<unsigned>(chunks * c.Hkv), MG_THREADS, bytes, s, c, a, b);
+}
+template <bool PAIR>
+cudaError_t merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, int sms, cudaStream_t s) {
+  static std::atomic<unsigned> done[2];
+  count_chunks(a, b, UNIT);
+  // few rows have many records: four rows a CTA spread them
+  if ((int64_t)b.chunks * c.Hkv < sms) {
+    constexpr int ROWS = 4, bytes = static_cast<int>(sizeof(MergeSmem<ROWS>));
+    const cudaError_t e = set_up(chunk_merge_kernel<ROWS, PAIR>, bytes, done[0]);
+    if (e != cudaSuccess) return e;
+    count_chunks(a, b, ROWS);
+    return launch_dependent(chunk_merge_kernel<ROWS, PAIR>, static_cast<unsigned>(b.chunks * c.Hkv), MG_THREADS, bytes, s,
+                            c, a, b);
+  }
+  constexpr int bytes = static_cast<int>(sizeof(MergeRowsSmem));
+  const cudaError_t e = set_up(chunk_merge_rows_kernel<PAIR>, bytes, done[1]);
+  if (e != cudaSuccess) return e;
+  const int per_head = ctas_per_head(b.chunks, c.Hkv, sms);
+  return launch_dependent(chunk_merge_rows_kernel<PAIR>, static_cast<unsigned>(per_head * c.Hkv), MG_THREADS, bytes, s, c, a,
+                          b, per_head);
 }
 
 }  // namespace
 
 cudaError_t launch_rotate_queries(const DevCache& c, const RotateArgs& a, int sms, cudaStream_t s) {
-  // rows of a CTA: 64, where that leaves every SM some, since each CTA splits a rotation of its own
-  return (((int64_t)a.rows << a.lg) * c.Hkv >= (int64_t)sms * 64) ? rotate<4>(c, a, s) : rotate<1>(c, a, s);
+  constexpr int bytes = static_cast<int>(sizeof(RotateSmem));
+  static std::atomic<unsigned> done;
+  const cudaError_t e = set_up(rotate_queries_kernel, bytes, done);
+  if (e != cudaSuccess) return e;
+  const int per_head = ctas_per_head((((int64_t)a.rows << a.lg) + UNIT - 1) / UNIT, c.Hkv, sms);
+  return launch_dependent(rotate_queries_kernel, static_cast<unsigned>(per_head * c.Hkv), MG_THREADS, bytes, s, c, a, per_head);
 }
 cudaError_t launch_chunk_scan(const DevCache& c, const ScanArgs& a, bool pair, const CUtensorMap& q_map, cudaStream_t s) {
   if (c.gk == 64) return pair ? scan<64, true>(c, a, q_map, s) : scan<64, false>(c, a, q_map, s);
   return pair ? scan<128, true>(c, a, q_map, s) : scan<128, false>(c, a, q_map, s);
 }
 cudaError_t launch_chunk_merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, bool pair, int sms, cudaStream_t s) {
-  int64_t rows = 0;
-  for (int i = 0; i < a.n; ++i) rows += (int64_t)a.m[i] << a.lg;
-  rows *= c.Hkv;
-  if (pair) return rows >= (int64_t)sms * 64 ? merge<64, true>(c, a, b, s) : merge<16, true>(c, a, b, s);
-  // few rows have many records: four rows a CTA spread them
-  return rows >= (int64_t)sms * 16 ? merge<16, false>(c, a, b, s) : merge<4, false>(c, a, b, s);
+  return pair ? merge<true>(c, a, b, sms, s) : merge<false>(c, a, b, sms, s);
 }
 
 }  // namespace oscar

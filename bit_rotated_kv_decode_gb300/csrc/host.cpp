@@ -1021,7 +1021,7 @@ oscar_status oscar_chunk_attention(oscar_cache* c, int32_t layer, int32_t n, con
   sa.Hkv = d.Hkv;
   sa.G = G;
   sa.lg = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
-  sa.scale2 = 2.0f * a.scale2;
+  sa.scale2 = a.scale2;
   // q, the BF16 pages, the new keys and values, the rotated q
   CUtensorMap maps[5];
   if (!tensor_map_rows(&maps[0], q, Hq, rows, q_stride, G, 128 / G) ||
