@@ -83,7 +83,7 @@ cudaError_t launch_chunk_scan(const DevCache& c, const ScanArgs& a, bool pair, c
 
 // The BF16 tokens' partial rows: [near_blocks from the last][near_splits][Hkv][256 rows][PARTIAL_FLOATS].
 struct NearPlan {
-  int splits, blocks;
+  int splits, blocks, ctas;
   int32_t start[CHUNK_MAX_REQ];           // blocks of 256 rows before request i
 };
 struct MergeArgs {

@@ -2,11 +2,11 @@
 // over the chunk itself ("TogetherAI开源OSCAR" (ModelScope), section "OSCAR的设计": unpack, scale and
 // zero, online-softmax merge of the segments; "Together AI Open-Sources OSCAR" (MarkTechPost),
 // section "The Serving System").  Four kernels:
-//   rotate_queries_kernel  q R_K in fp16, each row scaled by a power of two, its channels in the
+//   rotate_*_kernel        q R_K in fp16, each row scaled by a power of two, its channels in the
 //                          order that unpacking leaves the codes in;
 //   chunk_scan_kernel      the history: partial rows (unnormalised sums, maximum, sum);
 //   paged_prefill_kernel   the BF16 tokens and the new ones, likewise (paged_prefill_device.cuh);
-//   chunk_merge_kernel     their sum, the history's times R_V^T, over the weights' sum.
+//   chunk_merge_*_kernel   their sum, the history's times R_V^T, over the weights' sum.
 //
 // chunk_scan_kernel: a CTA takes 128 keys at a time.  Four warps unpack them, a key a thread,
 // into fp16 values z + s c in shared memory (times a power of two that keeps them in range;
@@ -189,8 +189,11 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // The grid before in the stream is the near rows' kernel, on which nothing here depends: its CTAs let
+  // this grid start only when what came before them, the rotated queries among it, is complete, and the
+  // two run side by side.  What was written so lately is read past the L1 caches.  Waiting for it at the
+  // end makes this grid's completion stand for both.
   grid_dep_launch();
-  grid_dep_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
           int id[LAG + 2][2];
           auto look = [&](int i, int (&to)[2]) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) to[u] = i < n && 2 * i + u < pages ? table[2 * i + u] : -1;
+            for (int u = 0; u < 2; ++u) to[u] = i < n && 2 * i + u < pages ? __ldcg(table + 2 * i + u) : -1;
           };
 #pragma unroll
           for (int j = 0; j < LAG; ++j) id[j][0] = id[j][1] = -1;
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       if (PAIR && a >= row_tiles(s)) continue;
       const int m = A.m[s.req], tok0 = (s.block * (PAIR ? 2 : 1) + (PAIR ? a : 0)) * per_tile, tok = tok0 + (r >> A.lg);
       const int row = A.row[s.req] + min(tok, m - 1);
-      const float scale2 = A.scale2 * A.q_scale[(size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))] *
+      const float scale2 = A.scale2 * __ldcg(A.q_scale + (size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))) *
                            pow2(value_exponent(c.tau_k[(size_t)A.layer * c.Hkv + s.head]));
       // warps of the tile that have rows; the first arrives for those without, which only meet the others behind the
       // segment: whatever their rows of P are, a row of O has the same row of P alone
@@ -574,6 +577,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
     if (!ok && lane == 0) gave_up();
   }
   __syncwarp();
+  grid_dep_wait();
   __syncthreads();
   if (warp == SC_MMA_WARP) {
     tc_fence_after();
@@ -585,50 +589,31 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
 constexpr int PITCH = D + 8;   // bf16 elements of a row in shared memory: ldmatrix without conflicts
 constexpr int MG_THREADS = 256;
 
-// A rotation (rows: outputs) as two bf16 parts, its columns as they are or in unpack()'s order:
-// position 16 k + 2 i + b holds channel 16 k + 8 b + i.
+// A rotation (rows: outputs) as two bf16 parts.
 struct Parts {
   alignas(16) uint16_t hi[D][PITCH], lo[D][PITCH];
 };
-template <bool ORDERED>
 __device__ __forceinline__ void split_rotation(const float* m, Parts& s) {
 #pragma unroll 4
-  for (int i = threadIdx.x; i < D * (D / 16); i += MG_THREADS) {
-    const int n = i / (D / 16), p = i % (D / 16);
-    float f[16];
+  for (int i = threadIdx.x; i < D * (D / 8); i += MG_THREADS) {
+    const int n = i / (D / 8), p = i % (D / 8);
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(f + 4 * j) = reinterpret_cast<const float4*>(m + (size_t)n * D + 16 * p)[j];
-    uint32_t hi[8], lo[8];
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<float4*>(f + 4 * j) = reinterpret_cast<const float4*>(m + (size_t)n * D + 8 * p)[j];
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = ORDERED ? f[j] : f[2 * j], b = ORDERED ? f[j + 8] : f[2 * j + 1];
-      hi[j] = bf16x2(a, b);
-      lo[j] = bf16x2(a - __uint_as_float(hi[j] << 16), b - __uint_as_float(hi[j] & 0xffff0000u));
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = bf16x2(f[2 * j], f[2 * j + 1]);
+      lo[j] = bf16x2(f[2 * j] - __uint_as_float(hi[j] << 16), f[2 * j + 1] - __uint_as_float(hi[j] & 0xffff0000u));
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      *reinterpret_cast<uint4*>(&s.hi[n][16 * p + 8 * j]) = make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-      *reinterpret_cast<uint4*>(&s.lo[n][16 * p + 8 * j]) = make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
-    }
+    *reinterpret_cast<uint4*>(&s.hi[n][8 * p]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(&s.lo[n][8 * p]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
-// acc += a b^T for MT tiles of 16 rows of a and this warp's 16 rows of b.
-template <int MT>
-__device__ __forceinline__ void multiply_rows(float (&acc)[MT][2][4], const uint16_t (*a)[PITCH], const uint16_t (*b)[PITCH]) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    uint32_t bf[4];
-    ldsm4(bf, smem_u32(&b[16 * warp + (lane & 7) + 8 * (lane >> 4)][16 * s + 8 * ((lane >> 3) & 1)]));
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      uint32_t af[4];
-      ldsm4(af, smem_u32(&a[16 * i + (lane & 15)][16 * s + 8 * (lane >> 4)]));
-      mma_bf16(acc[i][0], af, bf[0], bf[1]);
-      mma_bf16(acc[i][1], af, bf[2], bf[3]);
-    }
-  }
+// 2^e with 2^10 <= top 2^e < 2^11, so that what falls below fp16's normal values is below 2^-24 of the row's largest.
+__device__ __forceinline__ int row_exponent(float top) {
+  return min(max(137 - static_cast<int>(__float_as_uint(top) >> 23), -100), 100);
 }
 
 constexpr int UNIT = 16;       // rows of a warp's product
@@ -645,7 +630,7 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x / per_head, G = 1 << A.lg, Hq = G * c.Hkv;
   const int64_t rows = (int64_t)A.rows << A.lg;
-  split_rotation<false>(c.rot_kt + ((size_t)A.layer * c.Hkv + head) * D * D, sm.r);   // (before the grid's dependency)
+  split_rotation(c.rot_kt + ((size_t)A.layer * c.Hkv + head) * D * D, sm.r);   // (before the grid's dependency)
   grid_dep_launch();
   grid_dep_wait();
   __syncthreads();
@@ -689,9 +674,8 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
     for (int h = 0; h < 2; ++h) {   // this thread's columns of row lane / 4 + 8 h
       top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
       top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-      // 2^e with 2^10 <= top 2^e < 2^11, so that what falls below fp16's normal values is below 2^-24 of the row's largest
-      const int e = min(max(137 - static_cast<int>(__float_as_uint(top[h]) >> 23), -100), 100);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const int e = row_exponent(top[h]);
+      const float up = pow2(e), down = pow2(-e);
       const int64_t row = row0 + lane / 4 + 8 * h;
       if (row >= rows) continue;
       const size_t at = (size_t)(row >> A.lg) * Hq + head * G + (row & (G - 1));
@@ -706,134 +690,164 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
   }
 }
 
-template <int ROWS>
-struct MergeSmem {
-  static constexpr int MT = ROWS > 16 ? ROWS / 16 : 1;
-  Parts r;
-  alignas(16) uint16_t hi[16 * MT][PITCH], lo[16 * MT][PITCH];   // the history's sums over the weights'
-  alignas(16) float near[16 * MT][D + 4];                        // the other tokens'
-  alignas(16) float part[8][2][D];                               // a warp's sums, where two warps share a row
-  float m[8], l[8];
-};
-// ROWS rows of one request and kv head: partial rows of the scan's CTAs and of the BF16 tokens,
-// each weighed with its maximum; two warps a row where there are four rows.
-template <int ROWS, bool PAIR>
+// Few rows: four of a CTA, which takes the rotation from the L2 cache straight into registers (a thread half a
+// row of it), where staging it in shared memory would take longer than the rest.
+constexpr int FEW = 4;
+// y[r][n] = sum_k x[r][k] m[n][k], thread (n, half) having m's row n from 64 half on in f; the same sum in both.
+__device__ __forceinline__ void times_rotation(const float4 (&f)[16], const float (*x)[D], float (&y)[FEW]) {
+  const int half = threadIdx.x & 1;
+#pragma unroll
+  for (int r = 0; r < FEW; ++r) {
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&x[r][64 * half + 4 * i]);
+      s[0] = fmaf(f[i].x, v.x, s[0]);
+      s[1] = fmaf(f[i].y, v.y, s[1]);
+      s[0] = fmaf(f[i].z, v.z, s[0]);
+      s[1] = fmaf(f[i].w, v.w, s[1]);
+    }
+    y[r] = s[0] + s[1];
+    y[r] += __shfl_xor_sync(0xffffffffu, y[r], 1);
+  }
+}
+__device__ __forceinline__ void take_rotation(float4 (&f)[16], const float* m) {
+  const float4* row = reinterpret_cast<const float4*>(m + (size_t)(threadIdx.x >> 1) * D + 64 * (threadIdx.x & 1));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = row[i];
+}
+// Where unpack() leaves channel c of a row.
+__device__ __forceinline__ int position_of(int c) { return (c & ~15) + 2 * (c & 7) + (c >> 3 & 1); }
+
 __global__ void __launch_bounds__(MG_THREADS)
-    chunk_merge_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
-                       const __grid_constant__ MergeArgs B) {
-  extern __shared__ __align__(16) uint8_t mg_raw[];
-  using Smem = MergeSmem<ROWS>;
-  Smem& sm = *reinterpret_cast<Smem*>(mg_raw);
-  constexpr int MT = Smem::MT, SHARE = ROWS < 8 ? 8 / ROWS : 1;   // warps of a row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = blockIdx.x % c.Hkv, chunk = blockIdx.x / c.Hkv;
-  split_rotation<true>(c.rot_v + ((size_t)A.layer * c.Hkv + head) * D * D, sm.r);   // (before the grid's dependency)
+    rotate_few_kernel(const __grid_constant__ DevCache c, const __grid_constant__ RotateArgs A) {
+  __shared__ alignas(16) float x[FEW][D];
+  __shared__ float top[FEW][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = threadIdx.x >> 1;
+  const int head = blockIdx.x % c.Hkv, G = 1 << A.lg, Hq = G * c.Hkv;
+  const int64_t row0 = (int64_t)(blockIdx.x / c.Hkv) * FEW, rows = (int64_t)A.rows << A.lg;
+  float4 f[16];
+  take_rotation(f, c.rot_kt + ((size_t)A.layer * c.Hkv + head) * D * D);   // (before the grid's dependency)
+  grid_dep_launch();
+  grid_dep_wait();
+  for (int i = threadIdx.x; i < FEW * D / 2; i += MG_THREADS) {
+    const int64_t row = row0 + i / (D / 2);
+    uint32_t v = 0;
+    if (row < rows)
+      v = reinterpret_cast<const uint32_t*>(A.q + (row >> A.lg) * A.q_stride + (size_t)(head * G + (row & (G - 1))) * D)[i % (D / 2)];
+    x[i / (D / 2)][2 * (i % (D / 2))] = __uint_as_float(v << 16);
+    x[i / (D / 2)][2 * (i % (D / 2)) + 1] = __uint_as_float(v & 0xffff0000u);
+  }
+  __syncthreads();
+  float y[FEW];
+  times_rotation(f, x, y);
+#pragma unroll
+  for (int r = 0; r < FEW; ++r) {
+    float t = fabsf(y[r]);
+#pragma unroll
+    for (int off = 16; off > 1; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+    if (lane == 0) top[r][warp] = t;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < FEW; ++r) {
+    float t = top[r][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t = fmaxf(t, top[r][i]);
+    const int e = row_exponent(t);
+    const int64_t row = row0 + r;
+    if (row >= rows || (threadIdx.x & 1)) continue;
+    const size_t at = (size_t)(row >> A.lg) * Hq + head * G + (row & (G - 1));
+    A.out[at * D + position_of(n)] = __half_as_ushort(__float2half_rn(y[r] * pow2(e)));
+    if (n == 0) A.scale[at] = pow2(-e);
+  }
+}
+
+// Four rows of one request and kv head, two warps a row: partial rows of the scan's CTAs and of the BF16
+// tokens, each weighed with its maximum.
+template <bool PAIR>
+__global__ void __launch_bounds__(MG_THREADS)
+    chunk_merge_few_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
+                           const __grid_constant__ MergeArgs B) {
+  __shared__ alignas(16) float far[FEW][D], near[FEW][D], part[FEW][2][D];
+  __shared__ float part_l[FEW];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = threadIdx.x >> 1;
+  const int head = blockIdx.x % c.Hkv, chunk = blockIdx.x / c.Hkv, G = 1 << A.lg;
+  float4 f[16];
+  take_rotation(f, c.rot_v + ((size_t)A.layer * c.Hkv + head) * D * D);   // (before the grid's dependency)
   int ri = 0, hi = A.n;
   while (hi - ri > 1) {
     const int mid = (ri + hi) >> 1;
     if (B.chunk[mid] <= chunk) ri = mid; else hi = mid;
   }
-  const int row0 = (chunk - B.chunk[ri]) * ROWS, rows = A.m[ri] << A.lg;   // rows of the request and kv head
-  if (ROWS < 16)   // the product takes 16 rows
-    for (int i = threadIdx.x; i < 16 * PITCH / 8; i += MG_THREADS)
-      reinterpret_cast<uint4*>(sm.hi)[i] = reinterpret_cast<uint4*>(sm.lo)[i] = make_uint4(0, 0, 0, 0);
+  const int row0 = (chunk - B.chunk[ri]) * FEW, rows = A.m[ri] << A.lg;   // rows of the request and kv head
   grid_dep_launch();
   grid_dep_wait();
-  __syncthreads();
-  const int64_t each = A.tiles[ri] + A.setup;
-  const float v_scale = pow2(value_exponent(c.tau_v[(size_t)A.layer * c.Hkv + head]));   // (of the scan's values)
-  for (int r = warp / SHARE; r < ROWS; r += 8 / SHARE) {
-    const int rr = row0 + r;
-    float4 far = make_float4(0, 0, 0, 0), near = far;
-    float top = NEG_INF, l = 0.0f;
-    if (rr < rows) {
-      constexpr int BLOCK = PAIR ? 2 * SC_ROWS : SC_ROWS;
-      const int64_t k = (int64_t)head * A.blocks[ri] + rr / BLOCK, start = A.cost[ri] + k * each;
-      const int64_t c0 = chunk_of(A, start + A.setup), c1 = chunk_of(A, start + each - 1);
-      // record j of the row: of the scan's CTAs in turn, both chains of each unless they have rows of their own
-      const float* scan = A.records + ((size_t)(A.segment[ri] + k + c0) * 2 + (PAIR ? rr % BLOCK / SC_ROWS : 0)) * SC_ROWS * PARTIAL_FLOATS +
-                          (size_t)(rr % SC_ROWS) * PARTIAL_FLOATS;
-      const int count = static_cast<int>(c1 - c0 + 1) * (PAIR ? 1 : 2);
-      constexpr size_t STEP = (size_t)(PAIR ? 2 : 1) * SC_ROWS * PARTIAL_FLOATS;
-      const int back = B.near_blocks - 1 - (B.near_start[ri] + rr / (2 * SC_ROWS));
-      const float* bf = B.near + (((size_t)back * B.near_splits * c.Hkv + head) * (2 * SC_ROWS) + rr % (2 * SC_ROWS)) * PARTIAL_FLOATS;
-      const size_t near_step = (size_t)c.Hkv * (2 * SC_ROWS) * PARTIAL_FLOATS;
-      for (int j = lane; j < count; j += 32) top = fmaxf(top, scan[j * STEP + PARTIAL_M]);
-      for (int j = lane; j < B.near_splits; j += 32) top = fmaxf(top, bf[j * near_step + PARTIAL_M]);
+  const int r = warp >> 1, share = warp & 1, rr = row0 + r;
+  float4 x = make_float4(0, 0, 0, 0), y = x;
+  float l = 0.0f;
+  if (rr < rows) {
+    constexpr int BLOCK = PAIR ? 2 * SC_ROWS : SC_ROWS;
+    const int64_t each = A.tiles[ri] + A.setup, k = (int64_t)head * A.blocks[ri] + rr / BLOCK, start = A.cost[ri] + k * each;
+    const int64_t c0 = chunk_of(A, start + A.setup), c1 = chunk_of(A, start + each - 1);
+    // record j of the row: of the scan's CTAs in turn, both chains of each unless they have rows of their own
+    const float* scan = A.records + ((size_t)(A.segment[ri] + k + c0) * 2 + (PAIR ? rr % BLOCK / SC_ROWS : 0)) * SC_ROWS * PARTIAL_FLOATS +
+                        (size_t)(rr % SC_ROWS) * PARTIAL_FLOATS;
+    const int count = static_cast<int>(c1 - c0 + 1) * (PAIR ? 1 : 2);
+    constexpr size_t STEP = (size_t)(PAIR ? 2 : 1) * SC_ROWS * PARTIAL_FLOATS;
+    const int back = B.near_blocks - 1 - (B.near_start[ri] + rr / (2 * SC_ROWS));
+    const float* bf = B.near + (((size_t)back * B.near_splits * c.Hkv + head) * (2 * SC_ROWS) + rr % (2 * SC_ROWS)) * PARTIAL_FLOATS;
+    const size_t near_step = (size_t)c.Hkv * (2 * SC_ROWS) * PARTIAL_FLOATS;
+    float top = NEG_INF;
+    for (int j = lane; j < count; j += 32) top = fmaxf(top, scan[j * STEP + PARTIAL_M]);
+    for (int j = lane; j < B.near_splits; j += 32) top = fmaxf(top, bf[j * near_step + PARTIAL_M]);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      // (a row without a maximum goes the same way: a NaN query's sums are NaN)
-      const float ref = top == NEG_INF ? 0.0f : top;
-      const int mine = warp % SHARE;
-#pragma unroll 4
-      for (int j = mine; j < count; j += SHARE) {
-        const float* p = scan + j * STEP;
-        const float f = ex2f(p[PARTIAL_M] - ref);
-        const float4 v = reinterpret_cast<const float4*>(p)[lane];
-        l = fmaf(p[PARTIAL_L], f, l);
-        far.x = fmaf(v.x, f, far.x);
-        far.y = fmaf(v.y, f, far.y);
-        far.z = fmaf(v.z, f, far.z);
-        far.w = fmaf(v.w, f, far.w);
-      }
-      for (int j = mine; j < B.near_splits; j += SHARE) {
-        const float* p = bf + j * near_step;
-        const float f = ex2f(p[PARTIAL_M] - ref);
-        const float4 v = reinterpret_cast<const float4*>(p)[lane];
-        l = fmaf(p[PARTIAL_L], f, l);
-        near.x = fmaf(v.x, f, near.x);
-        near.y = fmaf(v.y, f, near.y);
-        near.z = fmaf(v.z, f, near.z);
-        near.w = fmaf(v.w, f, near.w);
-      }
-    }
-    if constexpr (SHARE > 1) {
-      static_assert(SHARE == 2 && ROWS * SHARE == 8, "a row's two warps meet once");
-      if (warp % SHARE) {
-        reinterpret_cast<float4*>(sm.part[warp][0])[lane] = far;
-        reinterpret_cast<float4*>(sm.part[warp][1])[lane] = near;
-        if (lane == 0) sm.l[warp] = l;
-      }
-      __syncthreads();
-      if (warp % SHARE) continue;
-      const float4 x = reinterpret_cast<const float4*>(sm.part[warp + 1][0])[lane];
-      const float4 y = reinterpret_cast<const float4*>(sm.part[warp + 1][1])[lane];
-      far.x += x.x, far.y += x.y, far.z += x.z, far.w += x.w;
-      near.x += y.x, near.y += y.y, near.z += y.z, near.w += y.w;
-      l += sm.l[warp + 1];
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l, up = inv * v_scale;
-    const float f[4] = {far.x * up, far.y * up, far.z * up, far.w * up};
-    const uint32_t h0 = bf16x2(f[0], f[1]), h1 = bf16x2(f[2], f[3]);
-    *reinterpret_cast<uint2*>(&sm.hi[r][4 * lane]) = make_uint2(h0, h1);
-    *reinterpret_cast<uint2*>(&sm.lo[r][4 * lane]) =
-        make_uint2(bf16x2(f[0] - __uint_as_float(h0 << 16), f[1] - __uint_as_float(h0 & 0xffff0000u)),
-                   bf16x2(f[2] - __uint_as_float(h1 << 16), f[3] - __uint_as_float(h1 & 0xffff0000u)));
-    *reinterpret_cast<float4*>(&sm.near[r][4 * lane]) = make_float4(near.x * inv, near.y * inv, near.z * inv, near.w * inv);
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    // (a row without a maximum goes the same way: a NaN query's sums are NaN)
+    const float ref = top == NEG_INF ? 0.0f : top;
+    auto add = [&](const float* p, float4& to) {
+      const float w = ex2f(p[PARTIAL_M] - ref);
+      const float4 v = reinterpret_cast<const float4*>(p)[lane];
+      l = fmaf(p[PARTIAL_L], w, l);
+      to.x = fmaf(v.x, w, to.x);
+      to.y = fmaf(v.y, w, to.y);
+      to.z = fmaf(v.z, w, to.z);
+      to.w = fmaf(v.w, w, to.w);
+    };
+#pragma unroll 8
+    for (int j = share; j < count; j += 2) add(scan + j * STEP, x);
+    for (int j = share; j < B.near_splits; j += 2) add(bf + j * near_step, y);
+  }
+  if (share) {
+    reinterpret_cast<float4*>(part[r][0])[lane] = x;
+    reinterpret_cast<float4*>(part[r][1])[lane] = y;
+    if (lane == 0) part_l[r] = l;
   }
   __syncthreads();
-  float acc[MT][2][4] = {};
-  multiply_rows<MT>(acc, sm.lo, sm.r.hi);
-  multiply_rows<MT>(acc, sm.hi, sm.r.lo);
-  multiply_rows<MT>(acc, sm.hi, sm.r.hi);
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float2* p = reinterpret_cast<float2*>(&sm.near[16 * i + lane / 4 + 8 * h][16 * warp + 8 * n + 2 * (lane & 3)]);
-        const float2 y = *p;
-        *p = make_float2(y.x + acc[i][n][2 * h], y.y + acc[i][n][2 * h + 1]);
-      }
+  if (!share) {
+    const float4 u = reinterpret_cast<const float4*>(part[r][0])[lane], v = reinterpret_cast<const float4*>(part[r][1])[lane];
+    l += part_l[r];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float up = inv * pow2(value_exponent(c.tau_v[(size_t)A.layer * c.Hkv + head]));   // (of the scan's values)
+    // positions 4 lane, ...: channels 16 (lane / 4) + 2 (lane % 4), + 8, + 1, + 9
+    float* to = &far[r][16 * (lane >> 2) + 2 * (lane & 3)];
+    to[0] = (x.x + u.x) * up;
+    to[8] = (x.y + u.y) * up;
+    to[1] = (x.z + u.z) * up;
+    to[9] = (x.w + u.w) * up;
+    reinterpret_cast<float4*>(near[r])[lane] =
+        make_float4((y.x + v.x) * inv, (y.y + v.y) * inv, (y.z + v.z) * inv, (y.w + v.w) * inv);
+  }
   __syncthreads();
-  const int G = 1 << A.lg;
-  for (int i = threadIdx.x; i < ROWS * 16; i += MG_THREADS) {
-    const int r = i / 16, p = i % 16, rr = row0 + r;
-    if (rr >= rows) continue;
-    const float4 x = *reinterpret_cast<const float4*>(&sm.near[r][8 * p]), y = *reinterpret_cast<const float4*>(&sm.near[r][8 * p + 4]);
-    uint16_t* out = B.out + ((size_t)(A.row[ri] + (rr >> A.lg)) * A.Hq + head * G + (rr & (G - 1))) * D;
-    reinterpret_cast<uint4*>(out)[p] = make_uint4(bf16x2(x.x, x.y), bf16x2(x.z, x.w), bf16x2(y.x, y.y), bf16x2(y.z, y.w));
+  float out[FEW];
+  times_rotation(f, far, out);
+#pragma unroll
+  for (int i = 0; i < FEW; ++i) {
+    const float z = out[i] + near[i][n], next = __shfl_xor_sync(0xffffffffu, z, 2);
+    const int row = row0 + i;
+    if ((threadIdx.x & 3) == 0 && row < rows)   // outputs n and n + 1
+      reinterpret_cast<uint32_t*>(B.out + ((size_t)(A.row[ri] + (row >> A.lg)) * A.Hq + head * G + (row & (G - 1))) * D)[n >> 1] =
+          bf16x2(z, next);
   }
 }
 
@@ -1018,19 +1032,15 @@ void count_chunks(const ScanArgs& a, MergeArgs& b, int rows) {
 }
 template <bool PAIR>
 cudaError_t merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, int sms, cudaStream_t s) {
-  static std::atomic<unsigned> done[2];
+  static std::atomic<unsigned> done;
   count_chunks(a, b, UNIT);
   // few rows have many records: four rows a CTA spread them
   if ((int64_t)b.chunks * c.Hkv < sms) {
-    constexpr int ROWS = 4, bytes = static_cast<int>(sizeof(MergeSmem<ROWS>));
-    const cudaError_t e = set_up(chunk_merge_kernel<ROWS, PAIR>, bytes, done[0]);
-    if (e != cudaSuccess) return e;
-    count_chunks(a, b, ROWS);
-    return launch_dependent(chunk_merge_kernel<ROWS, PAIR>, static_cast<unsigned>(b.chunks * c.Hkv), MG_THREADS, bytes, s,
-                            c, a, b);
+    count_chunks(a, b, FEW);
+    return launch_dependent(chunk_merge_few_kernel<PAIR>, static_cast<unsigned>(b.chunks * c.Hkv), MG_THREADS, 0, s, c, a, b);
   }
   constexpr int bytes = static_cast<int>(sizeof(MergeRowsSmem));
-  const cudaError_t e = set_up(chunk_merge_rows_kernel<PAIR>, bytes, done[1]);
+  const cudaError_t e = set_up(chunk_merge_rows_kernel<PAIR>, bytes, done);
   if (e != cudaSuccess) return e;
   const int per_head = ctas_per_head(b.chunks, c.Hkv, sms);
   return launch_dependent(chunk_merge_rows_kernel<PAIR>, static_cast<unsigned>(per_head * c.Hkv), MG_THREADS, bytes, s, c, a,
@@ -1040,6 +1050,8 @@ cudaError_t merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, int sms, c
 }  // namespace
 
 cudaError_t launch_rotate_queries(const DevCache& c, const RotateArgs& a, int sms, cudaStream_t s) {
+  const int64_t few = (((int64_t)a.rows << a.lg) + FEW - 1) / FEW * c.Hkv;
+  if (few <= 2 * sms) return launch_dependent(rotate_few_kernel, static_cast<unsigned>(few), MG_THREADS, 0, s, c, a);
   constexpr int bytes = static_cast<int>(sizeof(RotateSmem));
   static std::atomic<unsigned> done;
   const cudaError_t e = set_up(rotate_queries_kernel, bytes, done);

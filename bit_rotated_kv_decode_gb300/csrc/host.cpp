@@ -957,7 +957,9 @@ cudaError_t chunk_group(oscar_cache* c, const AttnReq* reqs, int n, bool history
     cost += (int64_t)d.Hkv * sa.blocks[i] * (sa.tiles[i] + sa.setup);
   }
   sa.total = cost;
-  sa.ctas = static_cast<int32_t>(std::min<int64_t>(cost, c->num_sms));
+  // the near rows' CTAs run beside the scan's, one per SM: where they are few, the scan leaves them theirs
+  const int64_t sms = plan.ctas <= c->num_sms / 4 ? c->num_sms - plan.ctas : c->num_sms;
+  sa.ctas = static_cast<int32_t>(std::min<int64_t>(cost, sms));
   e = launch_chunk_scan(d, sa, pair, maps[4], s);
   if (e != cudaSuccess) return e;
   MergeArgs m;

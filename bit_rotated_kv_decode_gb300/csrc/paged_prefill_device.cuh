@@ -210,8 +210,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  grid_dep_launch();
-  grid_dep_wait();
+  if constexpr (S == CACHE) {   // (the grid behind counts on what came before this one, not on this one)
+    grid_dep_wait();
+    grid_dep_launch();
+  } else {
+    grid_dep_launch();
+    grid_dep_wait();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const int rw = 4 * k + lane / 8, rr = 32 * (warp & 3) + rw, tk = rr >> A.lg;
           const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
           const int at_row = SPLIT ? rr * PARTIAL_FLOATS * SIZE : (tk * A.a.Hq + (rr & (A.G - 1))) * (D * SIZE);
-          if (SPLIT || tk < left) *reinterpret_cast<uint4*>(out + at_row + c * SIZE + 16 * (lane & 7)) = v;
+          if ((SPLIT && S != CACHE) || tk < left) *reinterpret_cast<uint4*>(out + at_row + c * SIZE + 16 * (lane & 7)) = v;
         }
         __syncwarp();
       }

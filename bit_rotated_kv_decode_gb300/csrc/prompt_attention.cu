@@ -41,6 +41,7 @@ cudaError_t launch_near_attention(const PagedView& p, const AttnReq* reqs, int n
   }
   out->splits = A.splits;
   out->blocks = A.bstart[n];
+  out->ctas = A.items < sms ? A.items : sms;
   for (int i = 0; i < n; ++i) out->start[i] = A.bstart[i];
   return launch_tiles<false, true, CACHE>(A, maps, sms, s);
 }
