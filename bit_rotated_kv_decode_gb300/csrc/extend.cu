@@ -8,9 +8,10 @@
 //                   first; a token is a row of the accumulator, so a TMEM lane, so a thread;
 //   min, max, code  the thread's 128 values, from TMEM twice: no exchange between lanes.
 // A value's code is decided from x~ where the decision holds for every x within the error
-// bound below; a token with a value, minimum or maximum that it does not hold for (1 in 20
-// with thresholds at the 0.9 quantile) is decided by its warp as in the append
-// (quantize_group_warp), from x~ and the same bound: every byte is that of fp32_rn(k . R).
+// bound below.  Where it does not (1 token in 20 with thresholds at the 0.9 quantile, a value
+// or an end of the range of each), the warp takes those values in turn by a compensated product
+// (warp_dot2), whose bound leaves nearly nothing open; a token that is still open goes the
+// append's way (quantize_group_warp): every byte is that of fp32_rn(k . R).
 //
 // Error of x~, with S = |k|_2 max_j |R_:j|_2 >= sum |k_i R_ij| and u = 2^-24: products are exact;
 // one product step adds 16 of them to the accumulator, each of the 17 terms cut by at most one
@@ -82,18 +83,20 @@ __device__ __forceinline__ float fma_sat(float a, float b, float c) {
 }
 __device__ __forceinline__ uint16_t half_bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
 
-// The group's scale, zero and code steps from its extremes; false where they are open.
+// The group's scale, zero and code steps from its extremes, each known to lie between two (clipped)
+// values; false where they are open.
+struct Range {
+  float mn_lo, mn_hi, mx_lo, mx_hi;
+};
 struct Grid {
   uint16_t s_bits, z_bits;
   float a, b, margin;   // code = rint(3 sat(a x + b)), where 3 sat() is not within margin of a half
 };
-__device__ __forceinline__ bool grid_of(float mn, float mx, float e, float tau, Grid& g) {
-  const float mn_lo = clip_canon(__fsub_rd(mn, e), tau), mn_hi = clip_canon(__fadd_ru(mn, e), tau);
-  const float mx_lo = clip_canon(__fsub_rd(mx, e), tau), mx_hi = clip_canon(__fadd_ru(mx, e), tau);
-  g.z_bits = half_bits(mn_lo);
-  const float s = scale_of(mx_lo, mn_hi);
+__device__ __forceinline__ bool grid_of(const Range& r, float e, Grid& g) {
+  g.z_bits = half_bits(r.mn_lo);
+  const float s = scale_of(r.mx_lo, r.mn_hi);
   g.s_bits = half_bits(s);
-  bool sure = g.z_bits == half_bits(mn_hi) && s == scale_of(mx_hi, mn_lo);
+  const bool sure = g.z_bits == half_bits(r.mn_hi) && s == scale_of(r.mx_hi, r.mn_lo);
   if (s == 0.0f) {   // every code is 0
     g.a = g.b = 0.0f;
     g.margin = 0.25f;
@@ -106,9 +109,10 @@ __device__ __forceinline__ bool grid_of(float mn, float mx, float e, float tau, 
   g.b = -z * g.a;
   g.margin = fmaf(fmaf(fabsf(z), 0x1p-21f, 1.001f * e), rs, 0x1p-18f);
   // values beyond the thresholds take the code of the threshold: 3 and 0, so that they need no clip
-  sure = sure && (mx_lo - z) * rs > 2.5f + g.margin && (mn_hi - z) * rs < 0.5f - g.margin && g.margin < 0.25f;
-  return sure;
+  return sure && (r.mx_lo - z) * rs > 2.5f + g.margin && (r.mn_hi - z) * rs < 0.5f - g.margin && g.margin < 0.25f;
 }
+
+constexpr float MAGIC = 12582912.0f;   // 1.5 2^23: adding it rounds to the nearest whole number
 
 template <int GK>
 __global__ void __launch_bounds__(EX_THREADS, 1)
@@ -273,6 +277,18 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 
     const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256 * group + 128 * buf;
     const float e = __fmul_ru(S, EX_MMA_ERR);
+    // value ch of lane from's token to within 2^-36 S, clipped; the whole warp together
+    auto narrow = [&](int from, int ch, float& lo, float& hi) {
+      const auto* s = reinterpret_cast<const uint16_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
+      const uint2 kw = reinterpret_cast<const uint2*>(s)[lane];
+      const float4 row4 = __ldg(reinterpret_cast<const float4*>(Rt + (size_t)ch * D) + lane);
+      const float4 k4 = make_float4(__uint_as_float(kw.x << 16), __uint_as_float(kw.x & 0xffff0000u),
+                                    __uint_as_float(kw.y << 16), __uint_as_float(kw.y & 0xffff0000u));
+      warp_dot2(k4, row4, __shfl_sync(0xffffffffu, S, from), lo, hi);
+      lo = clip_canon(lo, tau);
+      hi = clip_canon(hi, tau);
+    };
     Grid g[NG];
     bool sure = true;
 #pragma unroll
@@ -289,17 +305,50 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           mx = max3(mx, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
         }
       }
-      sure = grid_of(mn, mx, e, tau, g[n]) && sure;
+      Range range{clip_canon(__fsub_rd(mn, e), tau), clip_canon(__fadd_ru(mn, e), tau), clip_canon(__fsub_rd(mx, e), tau),
+                  clip_canon(__fadd_ru(mx, e), tau)};
+      bool known = grid_of(range, e, g[n]) || !dst;
+      if (!__all_sync(0xffffffffu, known)) {
+        // an end that is open: the values that may be it (the others lie inside), one after another
+        const bool low = range.mn_lo != range.mn_hi, high = range.mx_lo != range.mx_hi;
+        const float below = low && !known ? __fadd_ru(mn, 2.0f * e) : -INFINITY, above = high && !known ? __fsub_rd(mx, 2.0f * e) : INFINITY;
+        float lo0 = INFINITY, lo1 = INFINITY, hi0 = -INFINITY, hi1 = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < GK / 32; ++h) {
+          uint32_t w[32], mask = 0;
+          tmem_ld32(acc + n * GK + 32 * h, w);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            mask |= __uint_as_float(w[i]) <= below || __uint_as_float(w[i]) >= above ? 1u << i : 0u;
+          for (uint32_t open = __ballot_sync(0xffffffffu, mask != 0); open; open = __ballot_sync(0xffffffffu, mask != 0)) {
+            const int from = __ffs(open) - 1, i = __ffs(__shfl_sync(0xffffffffu, mask, from)) - 1;
+            float lo, hi;
+            narrow(from, n * GK + 32 * h + i, lo, hi);
+            if (lane == from) {
+              lo0 = fminf(lo0, lo), lo1 = fminf(lo1, hi);
+              hi0 = fmaxf(hi0, lo), hi1 = fmaxf(hi1, hi);
+              mask &= mask - 1;
+            }
+          }
+        }
+        if (!known) {
+          if (low) range.mn_lo = lo0, range.mn_hi = lo1;
+          if (high) range.mx_lo = hi0, range.mx_hi = hi1;
+          known = grid_of(range, e, g[n]);
+        }
+      }
+      sure = sure && known;
     }
     uint32_t code[8];
+    uint32_t close = 0;   // 32 channels with a value near a border
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       const Grid& q = g[h * 32 / GK];
       uint32_t w[32];
       tmem_ld32(acc + 32 * h, w);
       tc_wait_ld();
-      constexpr float MAGIC = 12582912.0f;   // 1.5 2^23: adding it rounds to the nearest whole number
-      constexpr uint32_t MAGIC_SUM = 0x4B400000u * 0x55555555u;   // its bits in every 2-bit place, modulo 2^32
+      constexpr uint32_t MAGIC_SUM = 0x4B400000u * 0x55555555u;   // MAGIC's bits in every 2-bit place, modulo 2^32
       float off = 0.0f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -317,7 +366,39 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
         code[2 * h + j] = bits;
       }
-      sure = sure && off < 0.5f - q.margin;
+      close |= off < 0.5f - q.margin ? 0u : 1u << h;
+    }
+    if (!dst || !sure) close = 0;
+    if (__any_sync(0xffffffffu, close != 0)) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if (!__any_sync(0xffffffffu, close >> h & 1)) continue;
+        const Grid& q = g[h * 32 / GK];
+        uint32_t w[32], mask = 0;
+        tmem_ld32(acc + 32 * h, w);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float y = fma_sat(__uint_as_float(w[i]), q.a, q.b), whole = fmaf(y, 3.0f, MAGIC) - MAGIC;
+          mask |= fabsf(fmaf(y, 3.0f, -whole)) < 0.5f - q.margin ? 0u : 1u << i;
+        }
+        if (!(close >> h & 1)) mask = 0;
+        for (uint32_t open = __ballot_sync(0xffffffffu, mask != 0); open; open = __ballot_sync(0xffffffffu, mask != 0)) {
+          const int from = __ffs(open) - 1, i = __ffs(__shfl_sync(0xffffffffu, mask, from)) - 1;
+          float lo, hi;
+          narrow(from, 32 * h + i, lo, hi);
+          if (lane == from) {
+            const float z = __half2float(__ushort_as_half(q.z_bits)), s = __half2float(__ushort_as_half(q.s_bits));
+            const uint32_t c0 = code_of(lo, z, s), at = 2 * (i & 15);
+            if (c0 != code_of(hi, z, s)) sure = false;
+            if (i < 16)
+              code[2 * h] = (code[2 * h] & ~(3u << at)) | c0 << at;
+            else
+              code[2 * h + 1] = (code[2 * h + 1] & ~(3u << at)) | c0 << at;
+            mask &= mask - 1;
+          }
+        }
+      }
     }
     tc_fence_before();
     if (dst && sure) {
@@ -329,7 +410,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 #pragma unroll
       for (int n = 0; n < NG; ++n) meta[n] = g[n].s_bits | (static_cast<uint32_t>(g[n].z_bits) << 16);
     }
-    // the warp decides the tokens that are open, one at a time
+    // the warp decides the tokens that are still open, one at a time
     for (uint32_t open = __ballot_sync(0xffffffffu, dst && !sure); open; open &= open - 1) {
       const int from = __ffs(open) - 1;
 #pragma unroll 1
