@@ -10,7 +10,7 @@
 // A value's code is decided from x~ where the decision holds for every x within the error
 // bound below.  Where it does not (1 token in 20 with thresholds at the 0.9 quantile, a value
 // or an end of the range of each), the warp takes those values in turn by a compensated product
-// (warp_dot2), whose bound leaves nearly nothing open; a token that is still open goes the
+// (four at a time), whose bound leaves nearly nothing open; a token that is still open goes the
 // append's way (quantize_group_warp): every byte is that of fp32_rn(k . R).
 //
 // Error of x~, with S = |k|_2 max_j |R_:j|_2 >= sum |k_i R_ij| and u = 2^-24: products are exact;
@@ -19,8 +19,9 @@
 // R2 before (2^-8 of that) 290 u S; what R1 + R2 leave of R 2^-18 S = 64 u S; x's own rounding
 // u S: 355 u S < 0x1.7p-16 S.
 //
-// Two groups of four warps per CTA take tiles in turn, each with two tiles of k in shared
-// memory, two accumulators, and the next tile's products under its own tile's decisions.
+// Four groups of four warps per CTA take tiles in turn, each with a tile of k in shared memory
+// and an accumulator: what a group waits for (its copy, its products, rows of R for an open
+// value), the others' decisions cover.
 #include <atomic>
 
 #include "append_device.cuh"
@@ -34,18 +35,16 @@ namespace {
 using namespace paged;
 
 constexpr int EX_ROWS = 128;                   // history tokens of a tile
-constexpr int EX_GROUPS = 2;                   // groups of four warps
+constexpr int EX_GROUPS = 4;                   // groups of four warps
 constexpr int EX_THREADS = EX_GROUPS * EX_ROWS;
 constexpr float EX_MMA_ERR = 0x1.7p-16f;
 
 struct alignas(1024) ExtendSmem {
   alignas(1024) uint8_t r[2][TILE_BYTES];                   // R2^T, R1^T: two halves of 64 inputs, [128 outputs][128 B] swizzled
-  alignas(1024) uint8_t k[EX_GROUPS][2][TILE_BYTES];        // tiles of tokens, likewise
-  const uint16_t* src[EX_GROUPS][2][EX_ROWS];               // where a tile's rows are, null: none
-  uint8_t* dst[EX_GROUPS][2][EX_ROWS];                      // their records, null: none
-  int32_t place[EX_GROUPS][2][EX_ROWS];                     // their rows in the records
+  alignas(1024) uint8_t k[EX_GROUPS][TILE_BYTES];           // tiles of tokens, likewise
+  const uint16_t* src[EX_GROUPS][EX_ROWS];                  // where a tile's rows are, null: none
   float x[EX_GROUPS * 4][D];                                // a token that its warp decides
-  uint64_t done[EX_GROUPS][2];                              // an accumulator's products are done
+  uint64_t done[EX_GROUPS];                                 // the accumulator's products are done
   uint32_t tmem;
 };
 static_assert(sizeof(ExtendSmem) + 1024 <= 232448, "shared memory of a CTA");
@@ -112,6 +111,43 @@ __device__ __forceinline__ bool grid_of(const Range& r, float e, Grid& g) {
   return sure && (r.mx_lo - z) * rs > 2.5f + g.margin && (r.mn_hi - z) * rs < 0.5f - g.margin && g.margin < 0.25f;
 }
 
+// The compensated product of warp_dot2 by eight lanes, 16 terms each: bounds lo <= exact <= hi.  The error terms
+// are at most 19 u S in all (a product's u, a sum's u of what it has so far) and their own sum, 21 additions deep,
+// is off by 21 u of that: 2^-39.4 S, within the 2^-36 S taken.
+__device__ __forceinline__ void dot2_of_eight(const uint4* k, const float4* r, float S, float& lo, float& hi) {
+  uint4 kw[2];
+  float4 rv[4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) kw[j] = k[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) rv[j] = __ldg(r + j);
+  float s = 0.0f, c = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w0 = j & 1 ? kw[j >> 1].z : kw[j >> 1].x, w1 = j & 1 ? kw[j >> 1].w : kw[j >> 1].y;
+    const float a[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
+                        __uint_as_float(w1 & 0xffff0000u)};
+    const float b[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = __fmul_rn(a[i], b[i]), q = __fmaf_rn(a[i], b[i], -p);
+      float e;
+      two_sum_f(s, p, s, e);
+      c = __fadd_rn(c, __fadd_rn(e, q));
+    }
+  }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) {
+    const float s2 = __shfl_xor_sync(0xffffffffu, s, off), c2 = __shfl_xor_sync(0xffffffffu, c, off);
+    float e;
+    two_sum_f(s, s2, s, e);
+    c = __fadd_rn(c, __fadd_rn(c2, e));
+  }
+  const float E = __fmul_ru(S, 0x1p-36f);
+  lo = __fsub_rd(__fadd_rd(s, c), E);
+  hi = __fadd_ru(__fadd_ru(s, c), E);
+}
+
 constexpr float MAGIC = 12582912.0f;   // 1.5 2^23: adding it rounds to the nearest whole number
 
 template <int GK>
@@ -132,8 +168,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   const int64_t stride = which ? A.v_stride : A.k_stride;
 
   if (threadIdx.x == 0) {
-    for (int g = 0; g < EX_GROUPS; ++g)
-      for (int b = 0; b < 2; ++b) mbar_init(&sm.done[g][b], 1);
+    for (int g = 0; g < EX_GROUPS; ++g) mbar_init(&sm.done[g], 1);
     mbar_init_fence();
   }
   if (warp == 0) {
@@ -166,13 +201,16 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   tc_fence_after();
 
   const int total = A.hist[A.n];
-  const int step = EX_GROUPS * per_matrix, first = EX_GROUPS * part + group;
+  // (few tiles go to CTAs of their own)
+  const int step = EX_GROUPS * per_matrix, first = part + per_matrix * group;
   // Tile t: this thread looks its row up, then the group copies all rows, 16 bytes at a time.
-  auto load = [&](int t, int buf) {
+  const uint16_t* src = nullptr;   // this thread's row
+  uint8_t* dst = nullptr;          // its record, and its row there
+  int row = 0;
+  auto load = [&](int t) {
     const int i = t * EX_ROWS + r;
-    const uint16_t* src = nullptr;
-    uint8_t* dst = nullptr;
-    int place = 0;
+    src = nullptr;
+    dst = nullptr;
     if (i < total) {
       int ri = 0, hi = A.n;
       while (hi - ri > 1) {
@@ -195,42 +233,40 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       else
         atomicOr(c.err, ERR_INT2_PAGE);
       if (!src) dst = nullptr;
-      place = at % PAGE;
+      row = at % PAGE;
     }
-    sm.src[group][buf][r] = src;
-    sm.dst[group][buf][r] = dst;
-    sm.place[group][buf][r] = place;
+    sm.src[group][r] = src;
     group_sync(group);
 #pragma unroll
     for (int u = 0; u < EX_ROWS * (D / 8) / EX_ROWS; ++u) {
-      const int row = u * (EX_ROWS / (D / 8)) + r / (D / 8), p = r % (D / 8);
-      const uint16_t* s = sm.src[group][buf][row];
-      cp_async16(sm.k[group][buf] + tile_at(row, p), s ? s + 8 * p : fresh, s != nullptr);
+      const int rw = u * (EX_ROWS / (D / 8)) + r / (D / 8), p = r % (D / 8);
+      const uint16_t* s = sm.src[group][rw];
+      cp_async16(sm.k[group] + tile_at(rw, p), s ? s + 8 * p : fresh, s != nullptr);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // the landed tile's products into its accumulator
-  auto multiply = [&](int buf) {
+  auto multiply = [&]() {
     if ((warp & 3) != 0) return;
     tc_fence_after();
-    const uint64_t k = desc_kmajor(smem_u32(sm.k[group][buf]));
+    const uint64_t k = desc_kmajor(smem_u32(sm.k[group]));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint64_t w = desc_kmajor(smem_u32(sm.r[h]));
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         const uint64_t off = ((s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32) >> 4;
-        mma_ss(256 * group + 128 * buf, k + off, w + off, IDESC_QK, h > 0 || s > 0);
+        mma_ss(128 * group, k + off, w + off, IDESC_QK, h > 0 || s > 0);
       }
     }
-    mma_commit(&sm.done[group][buf]);
+    mma_commit(&sm.done[group]);
   };
   // the bound S of this thread's row of a landed tile
-  auto bound = [&](int buf) {
+  auto bound = [&]() {
     float sq = 0.0f;
 #pragma unroll 4
     for (int p = 0; p < D / 8; ++p) {
-      const uint4 v = *reinterpret_cast<const uint4*>(sm.k[group][buf] + tile_at(r, p));
+      const uint4 v = *reinterpret_cast<const uint4*>(sm.k[group] + tile_at(r, p));
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -249,50 +285,58 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   };
 
   bool ok = true;
-  float S = 0.0f;
   int count = 0;   // tiles of this group so far
-  if (first < tiles) {
-    load(first, 0);
+  if (first < tiles) load(first);
+  for (int t = first; t < tiles; t += step, ++count) {
     landed();
-    multiply(0);
-    S = bound(0);
-    if (first + step < tiles) load(first + step, 1);
-  }
-  for (int t = first; t < tiles && ok; t += step, ++count) {
-    const int buf = count & 1;
-    float next_S = 0.0f;
-    if (t + step < tiles) {
-      landed();
-      multiply(buf ^ 1);
-      next_S = bound(buf ^ 1);
-    }
-    uint8_t* const dst = sm.dst[group][buf][r];
-    const uint16_t* const src = sm.src[group][buf][r];
-    const int row = sm.place[group][buf][r];
+    multiply();
+    const float S = bound();
+    const uint16_t* const mine = src;
+    uint8_t* const to = dst;
+    const int place = row;
     // a wait that gave up is the group's, whose warps leave together; the tile is free
-    ok = group_all(group, mbar_wait(&sm.done[group][buf], (count >> 1) & 1));
+    ok = group_all(group, mbar_wait(&sm.done[group], count & 1));
     if (!ok) break;
     tc_fence_after();
-    if (t + 2 * step < tiles) load(t + 2 * step, buf);
+    if (t + step < tiles) load(t + step);
 
-    const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256 * group + 128 * buf;
+    const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * group;
     const float e = __fmul_ru(S, EX_MMA_ERR);
-    // value ch of lane from's token to within 2^-36 S, clipped; the whole warp together
-    auto narrow = [&](int from, int ch, float& lo, float& hi) {
-      const auto* s = reinterpret_cast<const uint16_t*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
-      const uint2 kw = reinterpret_cast<const uint2*>(s)[lane];
-      const float4 row4 = __ldg(reinterpret_cast<const float4*>(Rt + (size_t)ch * D) + lane);
-      const float4 k4 = make_float4(__uint_as_float(kw.x << 16), __uint_as_float(kw.x & 0xffff0000u),
-                                    __uint_as_float(kw.y << 16), __uint_as_float(kw.y & 0xffff0000u));
-      warp_dot2(k4, row4, __shfl_sync(0xffffffffu, S, from), lo, hi);
-      lo = clip_canon(lo, tau);
-      hi = clip_canon(hi, tau);
+    // The values that lanes have open, bit i of a lane's mask channel ch0 + i of its token, each to within
+    // 2^-36 S and clipped: done(i, lo, hi) in its lane.  Four at a time, eight lanes each (one by one, every
+    // value waited for a row of R and of k of its own).
+    auto narrow = [&](uint32_t mask, int ch0, auto done) {
+      for (uint32_t open = __ballot_sync(0xffffffffu, mask != 0); open; open = __ballot_sync(0xffffffffu, mask != 0)) {
+        uint32_t rest = open;
+        int from = __ffs(open) - 1;   // the lane of these eight lanes' value
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (lane >> 3 == j && rest) from = __ffs(rest) - 1;
+          rest &= rest - 1;
+        }
+        const int i = __ffs(__shfl_sync(0xffffffffu, mask, from)) - 1;
+        const auto* row = reinterpret_cast<const uint16_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
+        const float bound_of = __shfl_sync(0xffffffffu, S, from);
+        float lo, hi;
+        dot2_of_eight(reinterpret_cast<const uint4*>(row) + 2 * (lane & 7),
+                      reinterpret_cast<const float4*>(Rt + (size_t)(ch0 + i) * D) + 4 * (lane & 7), bound_of, lo, hi);
+        const int rank = __popc(open & ((1u << lane) - 1));
+        lo = __shfl_sync(0xffffffffu, lo, 8 * (rank & 3));
+        hi = __shfl_sync(0xffffffffu, hi, 8 * (rank & 3));
+        if (mask != 0 && rank < 4) {
+          done(__ffs(mask) - 1, clip_canon(lo, tau), clip_canon(hi, tau));
+          mask &= mask - 1;
+        }
+      }
     };
+    // (Loops that stay loops: what is rare must not push what is not out of the instruction caches.  Arrays with a
+    // running index are taken apart into selects.)
     Grid g[NG];
     bool sure = true;
-#pragma unroll
+#pragma unroll 1
     for (int n = 0; n < NG; ++n) {
+      Grid gn;
       float mn = INFINITY, mx = -INFINITY;
 #pragma unroll
       for (int h = 0; h < GK / 32; ++h) {
@@ -307,7 +351,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       }
       Range range{clip_canon(__fsub_rd(mn, e), tau), clip_canon(__fadd_ru(mn, e), tau), clip_canon(__fsub_rd(mx, e), tau),
                   clip_canon(__fadd_ru(mx, e), tau)};
-      bool known = grid_of(range, e, g[n]) || !dst;
+      bool known = grid_of(range, e, gn) || !to;
       if (!__all_sync(0xffffffffu, known)) {
         // an end that is open: the values that may be it (the others lie inside), one after another
         const bool low = range.mn_lo != range.mn_hi, high = range.mx_lo != range.mx_hi;
@@ -321,31 +365,29 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             mask |= __uint_as_float(w[i]) <= below || __uint_as_float(w[i]) >= above ? 1u << i : 0u;
-          for (uint32_t open = __ballot_sync(0xffffffffu, mask != 0); open; open = __ballot_sync(0xffffffffu, mask != 0)) {
-            const int from = __ffs(open) - 1, i = __ffs(__shfl_sync(0xffffffffu, mask, from)) - 1;
-            float lo, hi;
-            narrow(from, n * GK + 32 * h + i, lo, hi);
-            if (lane == from) {
-              lo0 = fminf(lo0, lo), lo1 = fminf(lo1, hi);
-              hi0 = fmaxf(hi0, lo), hi1 = fmaxf(hi1, hi);
-              mask &= mask - 1;
-            }
-          }
+          narrow(mask, n * GK + 32 * h, [&](int, float lo, float hi) {
+            lo0 = fminf(lo0, lo), lo1 = fminf(lo1, hi);
+            hi0 = fmaxf(hi0, lo), hi1 = fmaxf(hi1, hi);
+          });
         }
         if (!known) {
           if (low) range.mn_lo = lo0, range.mn_hi = lo1;
           if (high) range.mx_lo = hi0, range.mx_hi = hi1;
-          known = grid_of(range, e, g[n]);
+          known = grid_of(range, e, gn);
         }
       }
       sure = sure && known;
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+        if (j == n) g[j] = gn;
     }
     uint32_t code[8];
     uint32_t close = 0;   // 32 channels with a value near a border
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 4; ++h) {
-      const Grid& q = g[h * 32 / GK];
-      uint32_t w[32];
+      Grid q = g[0];
+      if (NG == 2 && h >= 2) q = g[NG - 1];
+      uint32_t w[32], two[2];
       tmem_ld32(acc + 32 * h, w);
       tc_wait_ld();
       constexpr uint32_t MAGIC_SUM = 0x4B400000u * 0x55555555u;   // MAGIC's bits in every 2-bit place, modulo 2^32
@@ -364,16 +406,20 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           off = max3(off, fabsf(d.x), fabsf(d.y));
           bits += (__float_as_uint(near.x) << (2 * i)) + (__float_as_uint(near.y) << (2 * i + 2));
         }
-        code[2 * h + j] = bits;
+        two[j] = bits;
       }
       close |= off < 0.5f - q.margin ? 0u : 1u << h;
-    }
-    if (!dst || !sure) close = 0;
-    if (__any_sync(0xffffffffu, close != 0)) {
 #pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j == h) code[2 * j] = two[0], code[2 * j + 1] = two[1];
+    }
+    if (!to || !sure) close = 0;
+    if (__any_sync(0xffffffffu, close != 0)) {
+#pragma unroll 1
       for (int h = 0; h < 4; ++h) {
         if (!__any_sync(0xffffffffu, close >> h & 1)) continue;
-        const Grid& q = g[h * 32 / GK];
+        Grid q = g[0];
+        if (NG == 2 && h >= 2) q = g[NG - 1];
         uint32_t w[32], mask = 0;
         tmem_ld32(acc + 32 * h, w);
         tc_wait_ld();
@@ -383,35 +429,29 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           mask |= fabsf(fmaf(y, 3.0f, -whole)) < 0.5f - q.margin ? 0u : 1u << i;
         }
         if (!(close >> h & 1)) mask = 0;
-        for (uint32_t open = __ballot_sync(0xffffffffu, mask != 0); open; open = __ballot_sync(0xffffffffu, mask != 0)) {
-          const int from = __ffs(open) - 1, i = __ffs(__shfl_sync(0xffffffffu, mask, from)) - 1;
-          float lo, hi;
-          narrow(from, 32 * h + i, lo, hi);
-          if (lane == from) {
-            const float z = __half2float(__ushort_as_half(q.z_bits)), s = __half2float(__ushort_as_half(q.s_bits));
-            const uint32_t c0 = code_of(lo, z, s), at = 2 * (i & 15);
-            if (c0 != code_of(hi, z, s)) sure = false;
-            if (i < 16)
-              code[2 * h] = (code[2 * h] & ~(3u << at)) | c0 << at;
-            else
-              code[2 * h + 1] = (code[2 * h + 1] & ~(3u << at)) | c0 << at;
-            mask &= mask - 1;
-          }
-        }
+        narrow(mask, 32 * h, [&](int i, float lo, float hi) {
+          const float z = __half2float(__ushort_as_half(q.z_bits)), s = __half2float(__ushort_as_half(q.s_bits));
+          const uint32_t c0 = code_of(lo, z, s), at = 2 * (i & 15);
+          if (c0 != code_of(hi, z, s)) sure = false;
+          const int word = 2 * h + (i >> 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j == word) code[j] = (code[j] & ~(3u << at)) | c0 << at;
+        });
       }
     }
     tc_fence_before();
-    if (dst && sure) {
-      uint8_t* to = dst + (which ? V_CODES_OFF : K_CODES_OFF) + row * CODE_BYTES;
-      reinterpret_cast<uint4*>(to)[0] = make_uint4(code[0], code[1], code[2], code[3]);
-      reinterpret_cast<uint4*>(to)[1] = make_uint4(code[4], code[5], code[6], code[7]);
-      uint32_t* meta = reinterpret_cast<uint32_t*>(dst + (which ? v_meta_off_for(GK) : k_meta_off_for(GK)) +
-                                                   row * meta_bytes_for(GK));
+    if (to && sure) {
+      uint4* out = reinterpret_cast<uint4*>(to + (which ? V_CODES_OFF : K_CODES_OFF) + place * CODE_BYTES);
+      out[0] = make_uint4(code[0], code[1], code[2], code[3]);
+      out[1] = make_uint4(code[4], code[5], code[6], code[7]);
+      uint32_t* meta = reinterpret_cast<uint32_t*>(to + (which ? v_meta_off_for(GK) : k_meta_off_for(GK)) +
+                                                   place * meta_bytes_for(GK));
 #pragma unroll
       for (int n = 0; n < NG; ++n) meta[n] = g[n].s_bits | (static_cast<uint32_t>(g[n].z_bits) << 16);
     }
     // the warp decides the tokens that are still open, one at a time
-    for (uint32_t open = __ballot_sync(0xffffffffu, dst && !sure); open; open &= open - 1) {
+    for (uint32_t open = __ballot_sync(0xffffffffu, to && !sure); open; open &= open - 1) {
       const int from = __ffs(open) - 1;
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {
@@ -426,19 +466,18 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       __syncwarp();
       const float4 x = *reinterpret_cast<const float4*>(&sm.x[warp][4 * lane]);
       const auto* s = reinterpret_cast<const uint16_t*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), from));
-      auto* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from));
-      const int place = __shfl_sync(0xffffffffu, row, from);
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
+      auto* rec = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), from));
+      const int slot = __shfl_sync(0xffffffffu, place, from);
       const float sb = __shfl_sync(0xffffffffu, S, from), eb = __shfl_sync(0xffffffffu, e, from);
       const uint2 kw = reinterpret_cast<const uint2*>(s)[lane];
       const float4 k4 = make_float4(__uint_as_float(kw.x << 16), __uint_as_float(kw.x & 0xffff0000u),
                                     __uint_as_float(kw.y << 16), __uint_as_float(kw.y & 0xffff0000u));
       const GroupCode code_of_warp = quantize_group_warp<GK>(x, make_float4(eb, eb, eb, eb),
                                                              make_float4(sb, sb, sb, sb), tau, k4, Rt);
-      store_group_code_t<GK>(to, which, place, code_of_warp);
+      store_group_code_t<GK>(rec, which, slot, code_of_warp);
       __syncwarp();
     }
-    S = next_S;
   }
   if (!ok) {
     if (lane == 0) atomicOr(c.err, ERR_TIMEOUT);
@@ -496,10 +535,9 @@ cudaError_t launch_history(const DevCache& c, const ExtendArgs& a, int sms, cuda
     if (e != cudaSuccess) return e;
     if (dev < 32) done.fetch_or(1u << dev);
   }
-  // CTAs for each of the 2 Hkv matrices: one per SM in all, none without a tile for each of its groups
+  // CTAs for each of the 2 Hkv matrices: one per SM in all, none without a tile
   const int tiles = (a.hist[a.n] + EX_ROWS - 1) / EX_ROWS, matrices = 2 * c.Hkv;
-  const int most = (tiles + EX_GROUPS - 1) / EX_GROUPS, fair = sms / matrices > 1 ? sms / matrices : 1;
-  const int per_matrix = most < fair ? most : fair;
+  const int fair = sms / matrices > 1 ? sms / matrices : 1, per_matrix = tiles < fair ? tiles : fair;
   return launch_dependent(extend_history_kernel<GK>, static_cast<unsigned>(matrices * per_matrix), EX_THREADS, bytes, s,
                           c, a, tiles, per_matrix);
 }
