@@ -28,7 +28,7 @@
 
 #include "append_device.cuh"
 #include "chunk.h"
-#include "tcgen05_device.cuh"
+#include "values_device.cuh"
 
 namespace oscar {
 namespace {
@@ -130,26 +130,6 @@ struct Walk {
     if (lo < s.start) lo = s.start;
   }
 };
-
-// Values of a kv head in the scan are x 2^-k with 2^k from 2^8 tau to 2^9 tau (|x| <= tau, s <= 2/3 tau):
-// a code's two bits, as the half that they are where they stand in a word, count c 2^(2 at - 24), and
-// s 2^(24 - 2 at - k) is a half too, at most 2^16 2/3, so that one fma gives z + s c rounded once.
-// What falls below fp16's normal values is then off by at most 2^-17 tau.
-__device__ __forceinline__ int value_exponent(float tau) { return static_cast<int>(__float_as_uint(tau) >> 23) - 127 + 9; }
-__device__ __forceinline__ float pow2(int e) {   // (thresholds below 2^-100 hold nothing that fp16 can)
-  return __uint_as_float(static_cast<uint32_t>(127 + min(max(e, -126), 126)) << 23);
-}
-
-// The 16 codes of a word as values: half2 i holds channels i and i + 8.  s[at]: see above.
-__device__ __forceinline__ void unpack(uint32_t w, const __half2 (&s)[5], __half2 z, uint32_t (&x)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = i % 5, shift = 2 * (i - at);
-    const uint32_t bits = (w >> shift) & (0x00030003u << (2 * at));
-    const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&bits), s[at], z);
-    x[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
 
 template <int GK, bool PAIR>
 __global__ void __launch_bounds__(SC_THREADS, 1)
@@ -385,24 +365,20 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
           const bool some = tile >= 0 && tile < n && tile * SC_KEYS < left;
           const uint2* code = reinterpret_cast<const uint2*>(raw.code[which]) + 4 * r;
           const uint32_t* meta = reinterpret_cast<const uint32_t*>(raw.meta[which]) + NG * r;
-          const __half2 quarter = __float2half2_rn(0.25f);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {   // 64 channels
             uint8_t* to = sm.kv[st][u] + h * (TILE_BYTES / 2) + r * 128;
             const uint32_t m = some ? meta[NG == 2 ? h : 0] : 0;
-            __half2 s[5];
-            s[0] = __float2half2_rn(__half2float(__ushort_as_half(m & 0xffff)) * pow2(24 - e));
-            const __half2 z = __float2half2_rn(__half2float(__ushort_as_half(m >> 16)) * pow2(-e));
-#pragma unroll
-            for (int j = 1; j < 5; ++j) s[j] = __hmul2(s[j - 1], quarter);
+            __half2 s[5], z;
+            value_steps(m, e, s, z);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const uint2 word = some ? code[2 * h + p] : make_uint2(0, 0);
               uint32_t x[8];
-              unpack(word.x, s, z, x);
+              unpack_values(word.x, s, z, x);
               *reinterpret_cast<uint4*>(to + (((4 * p) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
               *reinterpret_cast<uint4*>(to + (((4 * p + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-              unpack(word.y, s, z, x);
+              unpack_values(word.y, s, z, x);
               *reinterpret_cast<uint4*>(to + (((4 * p + 2) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
               *reinterpret_cast<uint4*>(to + (((4 * p + 3) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
             }
@@ -716,7 +692,7 @@ __device__ __forceinline__ void take_rotation(float4 (&f)[16], const float* m) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) f[i] = row[i];
 }
-// Where unpack() leaves channel c of a row.
+// Where unpack_values() leaves channel c of a row.
 __device__ __forceinline__ int position_of(int c) { return (c & ~15) + 2 * (c & 7) + (c >> 3 & 1); }
 
 __global__ void __launch_bounds__(MG_THREADS)
@@ -852,7 +828,7 @@ __global__ void __launch_bounds__(MG_THREADS)
 }
 
 struct MergeRowsSmem {
-  alignas(16) uint16_t r[D][PITCH];            // fp16, columns in unpack()'s order
+  alignas(16) uint16_t r[D][PITCH];            // fp16, columns in unpack_values()'s order
   alignas(16) uint16_t row[8][UNIT][PITCH];    // a warp's rows: the history's sums (fp16), then the results (bf16)
 };
 // A warp takes 16 rows of one request and kv head at a time; the CTA keeps that head's rotation.  (The history's

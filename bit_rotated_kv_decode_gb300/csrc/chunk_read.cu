@@ -4,21 +4,22 @@
 // section "What OSCAR Does Differently", defines it).
 //
 // read_history_kernel takes 128 history tokens of one kv head, K or V, at a time, whatever
-// requests they are of.  With c' = c - 1, whole numbers that any type holds,
-//   x_j = s (c' R^T)_j + (z + s) sum_i R_ji     (per group of channels),
-// the product on tcgen05, 128 x 128 x 128, a token a row, a thread; the sums of R's rows once
-// per CTA.  For bf16 outputs R is one fp16 part (each weight off by 2^-12, an eighth of what the
-// output's rounding adds); for fp32 outputs three bf16 parts (24 bits), the small ones first.
-// Two groups of channels have an accumulator each.
+// requests they are of: a product of 128 x 128 x 128 on tcgen05, a token a row, a thread.
+//   bf16 outputs  the values z + s c in fp16, times a power of two that keeps them in range, by
+//                 R in fp16: each off by 2^-12, an eighth of what the output's rounding adds;
+//   fp32 outputs  with c' = c - 1, whole numbers that any type holds,
+//                   x_j = s (c' R^T)_j + (z + s) sum_i R_ji     (per group of channels),
+//                 R in three bf16 parts (24 bits), the small ones first, the sums of its rows
+//                 once per CTA; two groups of channels have an accumulator each.
 //
-// Two groups of four warps per CTA take tiles in turn: a tile's products run under the other
-// group's outputs, and under its own of the tile before where there are accumulators for two.
-// Rows go out through shared memory, eight lanes a piece of 128 bytes.
+// Two to four groups of four warps per CTA take tiles in turn: what one waits for (its codes, two
+// loads apart, and its products), the others' outputs cover.  Rows go out through shared memory, so
+// that several lanes store a row's piece together.
 #include <atomic>
 
 #include "append_device.cuh"
 #include "chunk.h"
-#include "tcgen05_device.cuh"
+#include "values_device.cuh"
 
 namespace oscar {
 namespace {
@@ -26,21 +27,23 @@ namespace {
 using namespace paged;
 
 constexpr int RD_ROWS = 128;
-constexpr int RD_GROUPS = 2;
-constexpr int RD_THREADS = RD_GROUPS * RD_ROWS;
 
-template <bool F32>
+// Groups that shared memory and the 512 columns of Tensor Memory hold.
+__host__ __device__ constexpr int read_groups(int gk, bool f32) { return !f32 ? 4 : gk == 64 ? 2 : 3; }
+
+template <int GK, bool F32>
 struct alignas(1024) ReadSmem {
-  static constexpr int PARTS = F32 ? 3 : 1;
-  alignas(1024) uint8_t r[PARTS][TILE_BYTES];              // R, smallest part first: two halves of 64 inputs, [128 outputs][128 B] swizzled
-  alignas(1024) uint8_t code[RD_GROUPS][TILE_BYTES];       // c' of a tile, likewise
-  alignas(16) uint8_t out[RD_GROUPS * 4][32 * 128];        // per warp: 128 bytes of its 32 rows
-  alignas(16) float sum[2][D];                             // sums of R's rows over a group of channels
-  int32_t to[RD_GROUPS][RD_ROWS];                          // rows of the output, -1: none
-  uint64_t done[RD_GROUPS];
+  static constexpr int PARTS = F32 ? 3 : 1, GROUPS = read_groups(GK, F32);
+  alignas(1024) uint8_t r[PARTS][TILE_BYTES];           // R, smallest part first: two halves of 64 inputs, [128 outputs][128 B] swizzled
+  alignas(1024) uint8_t code[GROUPS][TILE_BYTES];       // values or c' of a tile, likewise
+  alignas(16) uint8_t out[GROUPS * 4][32 * 64];         // per warp: 64 bytes of its 32 rows
+  alignas(16) float sum[2][D];                          // sums of R's rows over a group of channels
+  int32_t to[GROUPS][RD_ROWS];                          // rows of the output, -1: none
+  uint64_t done[GROUPS];
   uint32_t tmem;
 };
-static_assert(sizeof(ReadSmem<true>) + 1024 <= 232448, "shared memory of a CTA");
+static_assert(sizeof(ReadSmem<128, true>) + 1024 <= 232448 && sizeof(ReadSmem<128, false>) + 1024 <= 232448,
+              "shared memory of a CTA");
 
 __device__ __forceinline__ uint32_t tile_at(int row, int part) {
   return (part >> 3) * (TILE_BYTES / 2) + row * 128 + (((part & 7) ^ (row & 7)) << 4);
@@ -58,39 +61,29 @@ __device__ __forceinline__ bool group_all(int group, bool mine) {
   return all != 0;
 }
 
-// The 16 codes of a word as c - 1: half2 or bf16x2 i holds channels i and i + 8.  A code in the
-// low mantissa bits of 2^e, e such that they count ones, is 2^e + c.
-template <bool F16>
-__device__ __forceinline__ void unpack(uint32_t w, uint32_t (&x)[8]) {
-  constexpr int PER = F16 ? 5 : 3;   // codes that fit the mantissa without a shift
+// The 16 codes of a word as c - 1: bf16x2 i holds channels i and i + 8.  A code in the low mantissa bits of 2^e,
+// e such that they count ones, is 2^e + c.
+__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int at = i % PER, shift = 2 * (i - at);
-    const uint32_t bits = (w >> shift) & (0x00030003u << (2 * at));
-    if constexpr (F16) {
-      const uint32_t base = 0x6400u - (2u * at << 10), less = base | (1u << (2 * at));   // 2^(10 - 2 at), and one more
-      const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&(const uint32_t&)(bits | base | base << 16)),
-                                __halves2half2(__ushort_as_half(less), __ushort_as_half(less)));
-      x[i] = *reinterpret_cast<const uint32_t*>(&v);
-    } else {
-      const uint32_t base = 0x4300u - (2u * at << 7), less = base | (1u << (2 * at));    // 2^(7 - 2 at), and one more
-      const __nv_bfloat162 v =
-          __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&(const uint32_t&)(bits | base | base << 16)),
-                  __halves2bfloat162(__ushort_as_bfloat16(less), __ushort_as_bfloat16(less)));
-      x[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+    const int at = i % 3, shift = 2 * (i - at);   // three codes fit the mantissa without a shift
+    const uint32_t base = 0x4300u - (2u * at << 7), less = base | (1u << (2 * at));   // 2^(7 - 2 at), and one more
+    const uint32_t bits = ((w >> shift) & (0x00030003u << (2 * at))) | (base | base << 16);
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&bits),
+                                     __halves2bfloat162(__ushort_as_bfloat16(less), __ushort_as_bfloat16(less)));
+    x[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
 }
 
 template <int GK, bool F32>
-__global__ void __launch_bounds__(RD_THREADS, 1)
+__global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
     read_history_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ReadArgs A, int tiles,
                         int per_matrix) {
   extern __shared__ uint8_t rd_raw[];
-  using Smem = ReadSmem<F32>;
+  using Smem = ReadSmem<GK, F32>;
   Smem& sm = *reinterpret_cast<Smem*>(rd_raw + (-smem_u32(rd_raw) & 1023u));
-  constexpr int NG = D / GK, PARTS = Smem::PARTS;
-  constexpr int ACC = 2 / NG;                    // accumulators of a tile for each group: one under the other's outputs
+  constexpr int NG = D / GK, PARTS = Smem::PARTS, GROUPS = Smem::GROUPS, THREADS = GROUPS * RD_ROWS;
+  constexpr int SUMS = F32 ? NG : 1;             // accumulators of a tile
   constexpr uint32_t IDESC = F32 ? IDESC_QK : IDESC_QK_F16;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int group = warp >> 2, r = threadIdx.x & (RD_ROWS - 1);
@@ -99,7 +92,7 @@ __global__ void __launch_bounds__(RD_THREADS, 1)
   const float* R = (which ? c.rot_v : c.rot_k) + ((size_t)A.layer * c.Hkv + head) * D * D;
 
   if (threadIdx.x == 0) {
-    for (int g = 0; g < RD_GROUPS; ++g) mbar_init(&sm.done[g], 1);
+    for (int g = 0; g < GROUPS; ++g) mbar_init(&sm.done[g], 1);
     mbar_init_fence();
   }
   if (warp == 0) {
@@ -108,9 +101,9 @@ __global__ void __launch_bounds__(RD_THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   // R, written once at the cache's creation (before the grid's dependency): 16 inputs at a time, in the order
-  // that unpack() leaves channels in
+  // that unpack_*() leave channels in
 #pragma unroll 2
-  for (int i = threadIdx.x; i < D * (D / 16); i += RD_THREADS) {
+  for (int i = threadIdx.x; i < D * (D / 16); i += THREADS) {
     const int n = i / (D / 16), p = i % (D / 16);
     float f[16];
 #pragma unroll
@@ -133,15 +126,17 @@ __global__ void __launch_bounds__(RD_THREADS, 1)
       *reinterpret_cast<uint4*>(sm.r[u] + tile_at(n, 2 * p + 1)) = make_uint4(x[4], x[5], x[6], x[7]);
     }
   }
-  {   // sums of R's rows: thread (output, half of the inputs)
-    const int n = threadIdx.x & (D - 1), h = threadIdx.x >> 7;
-    float s = 0.0f;
+  if constexpr (F32) {   // sums of R's rows: thread (output, half of the inputs)
+    for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
+      const int n = i & (D - 1), h = i >> 7;
+      float s = 0.0f;
 #pragma unroll 8
-    for (int i = 0; i < D / 2; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(R + (size_t)n * D + h * (D / 2) + i);
-      s += (f.x + f.y) + (f.z + f.w);
+      for (int j = 0; j < D / 2; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(R + (size_t)n * D + h * (D / 2) + j);
+        s += (f.x + f.y) + (f.z + f.w);
+      }
+      sm.sum[h][n] = s;
     }
-    sm.sum[h][n] = s;
   }
   fence_async_smem();
   grid_dep_launch();
@@ -149,13 +144,16 @@ __global__ void __launch_bounds__(RD_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if constexpr (NG == 1) {
+  if constexpr (F32 && NG == 1) {
     if (threadIdx.x < D) sm.sum[0][threadIdx.x] += sm.sum[1][threadIdx.x];
     __syncthreads();
   }
 
   const int total = A.hist[A.n];
-  const int step = RD_GROUPS * per_matrix, first = RD_GROUPS * part + group;
+  const float tau = (which ? c.tau_v : c.tau_k)[(size_t)A.layer * c.Hkv + head];
+  const int scale = value_exponent(tau);         // of the values in shared memory
+  // (few tiles go to CTAs of their own)
+  const int step = GROUPS * per_matrix, first = part + per_matrix * group;
   uint4 words[2];          // codes of this thread's row of the next tile
   uint32_t meta[NG];       // its {s, z}
   int to = -1;             // its row of the output
@@ -190,121 +188,138 @@ __global__ void __launch_bounds__(RD_THREADS, 1)
   // the fetched row into the group's tile
   auto stage = [&]() {
     const uint32_t w[8] = {words[0].x, words[0].y, words[0].z, words[0].w, words[1].x, words[1].y, words[1].z, words[1].w};
+    __half2 s[5], z;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       uint32_t x[8];
-      unpack<!F32>(w[p], x);
+      if constexpr (F32) {
+        unpack_codes(w[p], x);
+      } else {
+        if (p % (8 / NG) == 0) value_steps(meta[p / (8 / NG)], scale, s, z);
+        unpack_values(w[p], s, z, x);
+      }
       *reinterpret_cast<uint4*>(sm.code[group] + tile_at(r, 2 * p)) = make_uint4(x[0], x[1], x[2], x[3]);
       *reinterpret_cast<uint4*>(sm.code[group] + tile_at(r, 2 * p + 1)) = make_uint4(x[4], x[5], x[6], x[7]);
     }
     fence_async_smem();
   };
-  const uint32_t acc0 = 256 * group;
-  auto multiply = [&](int buf) {
+  const uint32_t acc0 = 128 * SUMS * group;
+  auto multiply = [&]() {
     if ((warp & 3) != 0) return;
     tc_fence_after();
     const uint64_t a = desc_kmajor(smem_u32(sm.code[group]));
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
+    for (int n = 0; n < SUMS; ++n)
 #pragma unroll
       for (int u = 0; u < PARTS; ++u) {
         const uint64_t b = desc_kmajor(smem_u32(sm.r[u]));
 #pragma unroll
-        for (int s = 8 / NG * n; s < 8 / NG * (n + 1); ++s) {
+        for (int s = 8 / SUMS * n; s < 8 / SUMS * (n + 1); ++s) {
           const uint64_t off = ((s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32) >> 4;
-          mma_ss(acc0 + 128 * (NG == 2 ? n : buf), a + off, b + off, IDESC, u > 0 || s > 8 / NG * n);
+          mma_ss(acc0 + 128 * n, a + off, b + off, IDESC, u > 0 || s > 8 / SUMS * n);
         }
       }
     mma_commit(&sm.done[group]);
   };
 
+  // {scale, zero} and output row of a tile that is staged
+  struct Row {
+    float s[NG], o[NG];
+    int to;
+  };
+  auto staged = [&]() {
+    Row w;
+    w.to = to;
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      w.s[n] = __half2float(__ushort_as_half(meta[n] & 0xffff));
+      w.o[n] = __half2float(__ushort_as_half(meta[n] >> 16)) + w.s[n];
+    }
+    return w;
+  };
+
   bool ok = true;
   int count = 0;
+  Row next{};
   if (first < tiles) {
     fetch(first);
     stage();
+    next = staged();
     tc_fence_before();
     group_sync(group);
-    multiply(0);
+    multiply();
+    if (first + step < tiles) fetch(first + step);
   }
   for (int t = first; t < tiles && ok; t += step, ++count) {
-    const int buf = count % ACC;
-    float s[NG], o[NG];
-    const int mine = to;
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      s[n] = __half2float(__ushort_as_half(meta[n] & 0xffff));
-      o[n] = __half2float(__ushort_as_half(meta[n] >> 16)) + s[n];
-    }
+    const Row now = next;
     const bool more = t + step < tiles;
-    if (more) fetch(t + step);
     ok = group_all(group, mbar_wait(&sm.done[group], count & 1));
     if (!ok) break;
     tc_fence_after();
-    sm.to[group][r] = mine;
-    if (more) {
+    sm.to[group][r] = now.to;
+    if (more) {   // the next tile, fetched while the last one went out; the one after it is on its way meanwhile
       stage();
-      if (ACC == 2) {
-        tc_fence_before();
-        group_sync(group);
-        multiply(buf ^ 1);
-      }
+      next = staged();
+      if (t + 2 * step < tiles) fetch(t + 2 * step);
     }
     __syncwarp();
-    // this warp's 32 rows, 128 bytes at a time
-    const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + acc0 + 128 * (NG == 2 ? 0 : buf);
-    constexpr int PIECE = F32 ? 32 : 64;
+    // this warp's 32 rows, 64 bytes at a time
+    const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + acc0;
+    constexpr int SIZE = F32 ? 4 : 2, PIECE = 64 / SIZE;
+    const float up = pow2(scale);
     uint8_t* turn = sm.out[warp];
-    char* out = static_cast<char*>(which ? A.v_out : A.k_out) + (size_t)head * (D * (F32 ? 4 : 2));
+    char* out = static_cast<char*>(which ? A.v_out : A.k_out) + (size_t)head * (D * SIZE);
 #pragma unroll 1
-    for (int col = 0; col < D; col += PIECE) {
-      uint32_t w[32];
+    for (int col = 0; col < D; col += 32) {
+      uint32_t d[SUMS][32];
 #pragma unroll
-      for (int half = 0; half < PIECE / 32; ++half) {
-        uint32_t d[NG][32];
+      for (int n = 0; n < SUMS; ++n) tmem_ld32(acc + 128 * n + col, d[n]);
+      tc_wait_ld();
 #pragma unroll
-        for (int n = 0; n < NG; ++n) tmem_ld32(acc + 128 * n + col + 32 * half, d[n]);
-        tc_wait_ld();
+      for (int part = 0; part < 32; part += PIECE) {
+        uint32_t w[16];
+        if constexpr (F32) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float y[4];
-          const float4 m0 = *reinterpret_cast<const float4*>(&sm.sum[0][col + 32 * half + j]);
-          const float m[4] = {m0.x, m0.y, m0.z, m0.w};
+          for (int j = 0; j < 16; j += 4) {
+            const float4 m0 = *reinterpret_cast<const float4*>(&sm.sum[0][col + part + j]);
+            const float m[4] = {m0.x, m0.y, m0.z, m0.w};
+            float y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = fmaf(s[0], __uint_as_float(d[0][j + i]), o[0] * m[i]);
-          if constexpr (NG == 2) {
-            const float4 m1 = *reinterpret_cast<const float4*>(&sm.sum[1][col + 32 * half + j]);
-            const float n1[4] = {m1.x, m1.y, m1.z, m1.w};
+            for (int i = 0; i < 4; ++i) y[i] = fmaf(now.s[0], __uint_as_float(d[0][part + j + i]), now.o[0] * m[i]);
+            if constexpr (NG == 2) {
+              const float4 m1 = *reinterpret_cast<const float4*>(&sm.sum[1][col + part + j]);
+              const float n1[4] = {m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] += fmaf(s[1], __uint_as_float(d[1][j + i]), o[1] * n1[i]);
-          }
-          if constexpr (F32) {
+              for (int i = 0; i < 4; ++i) y[i] += fmaf(now.s[NG - 1], __uint_as_float(d[SUMS - 1][part + j + i]), now.o[NG - 1] * n1[i]);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[j + i] = __float_as_uint(y[i]);
-          } else {
-            w[16 * half + j / 2] = bf16x2(y[0], y[1]);
-            w[16 * half + j / 2 + 1] = bf16x2(y[2], y[3]);
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = bf16x2(__uint_as_float(d[0][2 * j]) * up, __uint_as_float(d[0][2 * j + 1]) * up);
         }
-      }
+        // (16 bytes of 8 neighbouring rows fall into different banks: piece i of row r at i ^ (r / 2))
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4*>(turn + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      __syncwarp();
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int rw = 4 * k + lane / 8, row = sm.to[group][32 * (warp & 3) + rw];
-        const uint4 v = *reinterpret_cast<const uint4*>(turn + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
-        if (row >= 0)
-          *reinterpret_cast<uint4*>(out + (size_t)row * c.Hkv * (D * (F32 ? 4 : 2)) + col * (F32 ? 4 : 2) + 16 * (lane & 7)) = v;
+        for (int k = 0; k < 4; ++k) {
+          const int rw = 8 * k + lane / 4, row = sm.to[group][32 * (warp & 3) + rw];
+          const uint4 v = *reinterpret_cast<const uint4*>(turn + rw * 64 + (((lane & 3) ^ (rw >> 1 & 3)) << 4));
+          if (row >= 0)
+            *reinterpret_cast<uint4*>(out + (size_t)row * c.Hkv * (D * SIZE) + (col + part) * SIZE + 16 * (lane & 3)) = v;
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-    if (more && ACC == 1) {
+    if (more) {
       tc_fence_before();
       group_sync(group);
-      multiply(0);
+      multiply();
     }
   }
   if (!ok && lane == 0) atomicOr(c.err, ERR_TIMEOUT);
@@ -358,7 +373,7 @@ __global__ void __launch_bounds__(RB_THREADS)
 
 template <int GK, bool F32>
 cudaError_t launch_history(const DevCache& c, const ReadArgs& a, int sms, cudaStream_t s) {
-  constexpr int bytes = static_cast<int>(sizeof(ReadSmem<F32>)) + 1024;
+  constexpr int bytes = static_cast<int>(sizeof(ReadSmem<GK, F32>)) + 1024;
   static std::atomic<unsigned> done;   // devices that have been set up
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -368,11 +383,10 @@ cudaError_t launch_history(const DevCache& c, const ReadArgs& a, int sms, cudaSt
     if (e != cudaSuccess) return e;
     if (dev < 32) done.fetch_or(1u << dev);
   }
-  // CTAs for each of the 2 Hkv matrices: one per SM in all, none without a tile for each of its groups
+  // CTAs for each of the 2 Hkv matrices: one per SM in all, none without a tile
   const int tiles = (a.hist[a.n] + RD_ROWS - 1) / RD_ROWS, matrices = 2 * c.Hkv;
-  const int most = (tiles + RD_GROUPS - 1) / RD_GROUPS, fair = sms / matrices > 1 ? sms / matrices : 1;
-  const int per_matrix = most < fair ? most : fair;
-  return launch_dependent(read_history_kernel<GK, F32>, static_cast<unsigned>(matrices * per_matrix), RD_THREADS, bytes,
+  const int fair = sms / matrices > 1 ? sms / matrices : 1, per_matrix = tiles < fair ? tiles : fair;
+  return launch_dependent(read_history_kernel<GK, F32>, static_cast<unsigned>(matrices * per_matrix), read_groups(GK, F32) * RD_ROWS, bytes,
                           s, c, a, tiles, per_matrix);
 }
 
