@@ -4,7 +4,7 @@
 // section "What OSCAR Does Differently", defines it).
 //
 // read_history_kernel takes 128 history tokens of one kv head, K or V, at a time, whatever
-// requests they are of: a product of 128 x 128 x 128 on tcgen05, a token a row, a thread.
+// requests they are of: a product of 128 x 128 x 128 on tcgen05.
 //   bf16 outputs  the values z + s c in fp16, times a power of two that keeps them in range, by
 //                 R in fp16: each off by 2^-12, an eighth of what the output's rounding adds;
 //   fp32 outputs  with c' = c - 1, whole numbers that any type holds,
@@ -13,9 +13,13 @@
 //                 once per CTA; two groups of channels have an accumulator each.
 //
 // Two to four groups of four warps per CTA take tiles in turn: what one waits for (its codes, two
-// loads apart, and its products), the others' outputs cover.  Rows go out through shared memory, so
-// that several lanes store a row's piece together.
+// loads apart, and its products), the others' outputs cover.
+// A lane of the accumulator is an output channel for fp32 outputs (R times the tokens), so that a
+// warp stores 128 neighbouring bytes straight from the registers that it reads; for bf16 it is a token,
+// whose row goes through shared memory, eight lanes a piece of 128 bytes (30K tokens: fp32 63 us, 73
+// that way; bf16 67 us the first way, its stores being half as wide).
 #include <atomic>
+#include <type_traits>
 
 #include "append_device.cuh"
 #include "chunk.h"
@@ -36,9 +40,17 @@ struct alignas(1024) ReadSmem {
   static constexpr int PARTS = F32 ? 3 : 1, GROUPS = read_groups(GK, F32);
   alignas(1024) uint8_t r[PARTS][TILE_BYTES];           // R, smallest part first: two halves of 64 inputs, [128 outputs][128 B] swizzled
   alignas(1024) uint8_t code[GROUPS][TILE_BYTES];       // values or c' of a tile, likewise
-  alignas(16) uint8_t out[GROUPS * 4][32 * 64];         // per warp: 64 bytes of its 32 rows
-  alignas(16) float sum[2][D];                          // sums of R's rows over a group of channels
-  int32_t to[GROUPS][RD_ROWS];                          // rows of the output, -1: none
+  // fp32: sums of R's rows over a group of channels; of a tile's tokens and those of the next s and z + s of each
+  // group of channels, and rows of the output (-1: none).  bf16: per warp 128 bytes of its 32 rows
+  struct Fp32 {
+    alignas(16) float sum[2][D];
+    alignas(16) float2 step[GROUPS][2][D / GK][RD_ROWS];
+    alignas(16) int32_t to[GROUPS][2][RD_ROWS];
+  };
+  struct Bf16 {
+    alignas(16) uint8_t out[GROUPS * 4][32 * 128];
+  };
+  std::conditional_t<F32, Fp32, Bf16> x;
   uint64_t done[GROUPS];
   uint32_t tmem;
 };
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
         const float4 f = *reinterpret_cast<const float4*>(R + (size_t)n * D + h * (D / 2) + j);
         s += (f.x + f.y) + (f.z + f.w);
       }
-      sm.sum[h][n] = s;
+      sm.x.sum[h][n] = s;
     }
   }
   fence_async_smem();
@@ -145,7 +157,7 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
   __syncthreads();
   tc_fence_after();
   if constexpr (F32 && NG == 1) {
-    if (threadIdx.x < D) sm.sum[0][threadIdx.x] += sm.sum[1][threadIdx.x];
+    if (threadIdx.x < D) sm.x.sum[0][threadIdx.x] += sm.x.sum[1][threadIdx.x];
     __syncthreads();
   }
 
@@ -185,8 +197,16 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
 #pragma unroll
     for (int n = 0; n < NG; ++n) meta[n] = m[n];
   };
-  // the fetched row into the group's tile
-  auto stage = [&]() {
+  // the fetched token into the group's tile, the buf-th of its two
+  auto stage = [&](int buf) {
+    if constexpr (F32) {
+      sm.x.to[group][buf][r] = to;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const float s = __half2float(__ushort_as_half(meta[n] & 0xffff)), z = __half2float(__ushort_as_half(meta[n] >> 16));
+        sm.x.step[group][buf][n][r] = make_float2(s, z + s);
+      }
+    }
     const uint32_t w[8] = {words[0].x, words[0].y, words[0].z, words[0].w, words[1].x, words[1].y, words[1].z, words[1].w};
     __half2 s[5], z;
 #pragma unroll
@@ -216,102 +236,90 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
 #pragma unroll
         for (int s = 8 / SUMS * n; s < 8 / SUMS * (n + 1); ++s) {
           const uint64_t off = ((s >> 2) * (TILE_BYTES / 2) + (s & 3) * 32) >> 4;
-          mma_ss(acc0 + 128 * n, a + off, b + off, IDESC, u > 0 || s > 8 / SUMS * n);
+          mma_ss(acc0 + 128 * n, (F32 ? b : a) + off, (F32 ? a : b) + off, IDESC, u > 0 || s > 8 / SUMS * n);
         }
       }
     mma_commit(&sm.done[group]);
   };
 
-  // {scale, zero} and output row of a tile that is staged
-  struct Row {
-    float s[NG], o[NG];
-    int to;
-  };
-  auto staged = [&]() {
-    Row w;
-    w.to = to;
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      w.s[n] = __half2float(__ushort_as_half(meta[n] & 0xffff));
-      w.o[n] = __half2float(__ushort_as_half(meta[n] >> 16)) + w.s[n];
-    }
-    return w;
-  };
-
   bool ok = true;
-  int count = 0;
-  Row next{};
+  int count = 0, now = -1;
   if (first < tiles) {
     fetch(first);
-    stage();
-    next = staged();
+    stage(0);
+    now = to;
     tc_fence_before();
     group_sync(group);
     multiply();
     if (first + step < tiles) fetch(first + step);
   }
+  constexpr int SIZE = F32 ? 4 : 2;
+  char* const out = static_cast<char*>(which ? A.v_out : A.k_out) + (size_t)head * (D * SIZE);
+  const size_t row_bytes = (size_t)c.Hkv * (D * SIZE);
+  const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + acc0;
   for (int t = first; t < tiles && ok; t += step, ++count) {
-    const Row now = next;
+    const int buf = count & 1, mine = now;   // (the row of this thread's token, staged a tile ago)
     const bool more = t + step < tiles;
     ok = group_all(group, mbar_wait(&sm.done[group], count & 1));
     if (!ok) break;
     tc_fence_after();
-    sm.to[group][r] = now.to;
     if (more) {   // the next tile, fetched while the last one went out; the one after it is on its way meanwhile
-      stage();
-      next = staged();
+      stage(buf ^ 1);
+      now = to;
       if (t + 2 * step < tiles) fetch(t + 2 * step);
     }
-    __syncwarp();
-    // this warp's 32 rows, 64 bytes at a time
-    const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + acc0;
-    constexpr int SIZE = F32 ? 4 : 2, PIECE = 64 / SIZE;
-    const float up = pow2(scale);
-    uint8_t* turn = sm.out[warp];
-    char* out = static_cast<char*>(which ? A.v_out : A.k_out) + (size_t)head * (D * SIZE);
+    if constexpr (F32) {
+      const int ch = 32 * (warp & 3) + lane;   // this thread's output channel
+      const float sum0 = sm.x.sum[0][ch], sum1 = NG == 2 ? sm.x.sum[1][ch] : 0.0f;
 #pragma unroll 1
-    for (int col = 0; col < D; col += 32) {
-      uint32_t d[SUMS][32];
+      for (int col = 0; col < RD_ROWS; col += 32) {   // 32 tokens
+        uint32_t d[SUMS][32];
 #pragma unroll
-      for (int n = 0; n < SUMS; ++n) tmem_ld32(acc + 128 * n + col, d[n]);
-      tc_wait_ld();
+        for (int n = 0; n < SUMS; ++n) tmem_ld32(acc + 128 * n + col, d[n]);
+        tc_wait_ld();
 #pragma unroll
-      for (int part = 0; part < 32; part += PIECE) {
-        uint32_t w[16];
-        if constexpr (F32) {
+        for (int i = 0; i < 32; i += 4) {
+          const int4 to4 = *reinterpret_cast<const int4*>(&sm.x.to[group][buf][col + i]);
+          const int rows[4] = {to4.x, to4.y, to4.z, to4.w};
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 m0 = *reinterpret_cast<const float4*>(&sm.sum[0][col + part + j]);
-            const float m[4] = {m0.x, m0.y, m0.z, m0.w};
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = fmaf(now.s[0], __uint_as_float(d[0][part + j + i]), now.o[0] * m[i]);
+          for (int j = 0; j < 4; j += 2) {
+            const float4 u = *reinterpret_cast<const float4*>(&sm.x.step[group][buf][0][col + i + j]);
+            float y0 = fmaf(u.x, __uint_as_float(d[0][i + j]), u.y * sum0), y1 = fmaf(u.z, __uint_as_float(d[0][i + j + 1]), u.w * sum0);
             if constexpr (NG == 2) {
-              const float4 m1 = *reinterpret_cast<const float4*>(&sm.sum[1][col + part + j]);
-              const float n1[4] = {m1.x, m1.y, m1.z, m1.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[i] += fmaf(now.s[NG - 1], __uint_as_float(d[SUMS - 1][part + j + i]), now.o[NG - 1] * n1[i]);
+              const float4 v = *reinterpret_cast<const float4*>(&sm.x.step[group][buf][NG - 1][col + i + j]);
+              y0 += fmaf(v.x, __uint_as_float(d[SUMS - 1][i + j]), v.y * sum1);
+              y1 += fmaf(v.z, __uint_as_float(d[SUMS - 1][i + j + 1]), v.w * sum1);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[j + i] = __float_as_uint(y[i]);
+            if (rows[j] >= 0) reinterpret_cast<float*>(out + rows[j] * row_bytes)[ch] = y0;
+            if (rows[j + 1] >= 0) reinterpret_cast<float*>(out + rows[j + 1] * row_bytes)[ch] = y1;
           }
-        } else {
+        }
+      }
+    } else {
+      uint8_t* turn = sm.x.out[warp];
+      const float up = pow2(scale);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {   // 64 channels
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t d[32];
+          tmem_ld32(acc + 64 * half + 32 * k, d);
+          tc_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            w[j] = bf16x2(__uint_as_float(d[0][2 * j]) * up, __uint_as_float(d[0][2 * j + 1]) * up);
+            w[16 * k + j] = bf16x2(__uint_as_float(d[2 * j]) * up, __uint_as_float(d[2 * j + 1]) * up);
         }
-        // (16 bytes of 8 neighbouring rows fall into different banks: piece i of row r at i ^ (r / 2))
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(turn + lane * 128 + ((i ^ (lane & 7)) << 4)) =
               make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rw = 8 * k + lane / 4, row = sm.to[group][32 * (warp & 3) + rw];
-          const uint4 v = *reinterpret_cast<const uint4*>(turn + rw * 64 + (((lane & 3) ^ (rw >> 1 & 3)) << 4));
-          if (row >= 0)
-            *reinterpret_cast<uint4*>(out + (size_t)row * c.Hkv * (D * SIZE) + (col + part) * SIZE + 16 * (lane & 3)) = v;
+        for (int k = 0; k < 8; ++k) {
+          const int rw = 4 * k + lane / 8, row = __shfl_sync(0xffffffffu, mine, rw);
+          const uint4 v = *reinterpret_cast<const uint4*>(turn + rw * 128 + (((lane & 7) ^ (rw & 7)) << 4));
+          if (row >= 0) *reinterpret_cast<uint4*>(out + row * row_bytes + 128 * half + 16 * (lane & 7)) = v;
         }
         __syncwarp();
       }
