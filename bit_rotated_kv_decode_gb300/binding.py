@@ -156,6 +156,8 @@ def _ptr(t) -> int | None:
 
 def _stream_ptr(stream) -> int | None:
     if stream is None:
+        if _torch is not None:   # (set once CUDA is there)
+            return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
         import torch
         if not torch.cuda.is_available():
             return None
@@ -193,6 +195,8 @@ class OscarCache:
         if st != OSCAR_OK:
             raise OscarError(st, "oscar_cache_create failed")
         self.h = handle
+        # what the marshalling extension takes of a cache
+        self._place = (handle.value, -1 if dry_run else self.mem.get_device(), cfg.num_kv_heads)
 
     # -- helpers ----------------------------------------------------------------
     def _check(self, st: int, what: str, allow_dry: bool = False) -> None:
@@ -204,6 +208,7 @@ class OscarCache:
         if getattr(self, "h", None):
             self.lib.oscar_cache_destroy(self.h)
             self.h = None
+            self._place = (0, -1, 0)
 
     def __del__(self):
         try:
@@ -310,6 +315,10 @@ class OscarCache:
     def extend(self, layer: int, reqs, k, v, new_lens=None, stream=None) -> None:
         """Append new_lens[i] tokens (one each by default) to every request of one layer, byte for byte as that many
         append() calls.  k, v bf16 [rows][Hkv][128], the requests' tokens one after another; rows may be strided."""
+        if not self.dry:
+            st = (_calls or _marshal()).extend(*self._place, layer, reqs, k, v, new_lens, stream)
+            if st is not None:
+                return self._check(st, "extend")
         n, hkv = len(reqs), self.cfg.num_kv_heads
         lens, rows = _counts(new_lens, n, "new_lens")
         if self.dry:
@@ -328,6 +337,10 @@ class OscarCache:
         """The keys and values that the cache holds of tokens [starts[i], starts[i] + counts[i]) of every request, in
         their own basis (history tokens dequantised and rotated back), into k_out and v_out [rows][Hkv][128], fp32 or
         bf16.  A request may be given more than once."""
+        if not self.dry:
+            st = (_calls or _marshal()).read_cache(*self._place, layer, reqs, starts, counts, k_out, v_out, stream)
+            if st is not None:
+                return self._check(st, "read")
         n, hkv = len(reqs), self.cfg.num_kv_heads
         first, _ = _counts(starts, n, "starts")
         count, rows = _counts(counts, n, "counts")
@@ -360,6 +373,13 @@ class OscarCache:
         over the new ones; the cache is not changed.  q bf16 [rows][Hq][128], k, v [rows][Hkv][128] (rows may be strided),
         out bf16 [rows][Hq][128].  Returns the workspace to pass to the next call: a new one where none is given or it is
         too small."""
+        if not self.dry:
+            st = (_calls or _marshal()).chunk(*self._place, layer, reqs, self.cfg.num_q_heads, q, k, v, out, new_lens,
+                                              workspace, stream)
+            if st == OSCAR_OK:
+                return workspace
+            if st is not None and self.lib.oscar_last_error(self.h) != b"workspace too small":
+                self._check(st, "chunk attention")
         n, hkv, hq = len(reqs), self.cfg.num_kv_heads, self.cfg.num_q_heads
         lens, rows = _counts(new_lens, n, "new_lens")
         layer = _int32("layer", layer)
@@ -493,7 +513,7 @@ _calls = None
 
 class _NotBuilt:
     """Takes no call, as the extension where it leaves one to Python."""
-    append = read = attend = staticmethod(lambda *args: None)
+    append = read = attend = prompt = extend = read_cache = chunk = staticmethod(lambda *args: None)
 
 
 def calls():
@@ -511,7 +531,8 @@ def calls():
         lib = load()
         mod.setup(tuple(ctypes.cast(fn, c_void_p).value for fn in (
             lib.oscar_bf16_append, lib.oscar_int4_append, lib.oscar_int4_read, lib.oscar_window_attention,
-            lib.oscar_int4_attention)))
+            lib.oscar_int4_attention, lib.oscar_prompt_attention, lib.oscar_extend, lib.oscar_read,
+            lib.oscar_chunk_attention)))
         _calls = mod
     return _calls
 
@@ -788,6 +809,11 @@ def prompt_attention(q, k, v, out, lens, window: int = -1, sinks: int = 0, scale
     be strided, as the parts of one projection's output), out [rows][Hq][128] fp32 or bf16, lse fp32 [rows][Hq] or None.
     The query at position p of its sequence sees the tokens t <= p with t < sinks or t > p - window (window < 0: all).
     Returns the workspace to pass to the next call: a new one where none is given or it is too small."""
+    st = (_calls or _marshal()).prompt(q, k, v, out, lens, window, sinks, scale, lse, workspace, error, stream)
+    if st == 0:
+        return workspace
+    if st is not None and load().oscar_paged_last_error() != b"workspace too small":
+        _paged_check(st, "prompt attention")
     n = len(lens)
     hq, hkv = _int32("query heads", q.shape[1]), _int32("kv heads", k.shape[1])
     window, sinks = _window(window), _int32("sinks", sinks)

@@ -1,4 +1,4 @@
-// Argument marshalling of the paged-cache calls for Python, in C++.
+// Argument marshalling of the paged-cache, prompt and chunk calls for Python, in C++.
 //
 // These calls are made for every layer of a decode step.  Reading eight tensors'
 // attributes and converting twenty arguments took Python 7.6 of a call's 11 us; through
@@ -38,12 +38,26 @@ using attend4_fn = oscar_status (*)(const void*, int64_t, const int32_t*, int32_
                                    int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, float, const uint16_t*,
                                    int64_t, void*, int32_t, float*, int32_t*, void*, size_t, void*);
 
+using prompt_fn = oscar_status (*)(const int32_t*, int32_t, int32_t, int32_t, int32_t, int32_t, float, const uint16_t*,
+                                  int64_t, const uint16_t*, int64_t, const uint16_t*, int64_t, void*, int32_t, float*,
+                                  int32_t*, void*, size_t, void*);
+using extend_fn = oscar_status (*)(oscar_cache*, int32_t, int32_t, const int32_t*, const int32_t*, const uint16_t*,
+                                  int64_t, const uint16_t*, int64_t, void*);
+using read2_fn = oscar_status (*)(oscar_cache*, int32_t, int32_t, const int32_t*, const int32_t*, const int32_t*, void*,
+                                 void*, int32_t, void*);
+using chunk_fn = oscar_status (*)(oscar_cache*, int32_t, int32_t, const int32_t*, const int32_t*, const uint16_t*, int64_t,
+                                 const uint16_t*, int64_t, const uint16_t*, int64_t, uint16_t*, void*, size_t, void*);
+
 struct {
   append16_fn append16;
   append4_fn append4;
   read4_fn read4;
   attend16_fn attend16;
   attend4_fn attend4;
+  prompt_fn prompt;
+  extend_fn extend;
+  read2_fn read2;
+  chunk_fn chunk;
 } g;
 
 // A tensor argument that is as it should be, or null.
@@ -273,6 +287,115 @@ int attend(PyObject* const* a, Py_ssize_t count) {
   return st;
 }
 
+// prompt(q, k, v, out, lens, window, sinks, scale, lse, workspace, error, stream)
+int prompt(PyObject* const* a, Py_ssize_t count) {
+  int32_t lens[MAX_REQ];
+  int device;
+  void* stream;
+  if (count != 12 || a[9] == Py_None || !context(a[11], &device, &stream)) return -1;
+  const Py_ssize_t n = requests(a[4]);
+  if (n == 0) return -1;
+  const int64_t rows = counts(a[4], n, lens);
+  if (rows < 0) return -1;
+  const long long window = PyLong_AsLongLong(a[5]), sinks = PyLong_AsLongLong(a[6]);
+  const double scale = PyFloat_AsDouble(a[7]);
+  if (PyErr_Occurred() || window < INT32_MIN || window > INT32_MAX || sinks < 0 || sinks > INT32_MAX) return -1;
+  int64_t qs, ks, vs;
+  const at::Tensor *q = heads_of(a[0], device, rows, -1, &qs), *k = heads_of(a[1], device, rows, -1, &ks), *lse = nullptr,
+                   *err = nullptr;
+  if (!q || !k) return -1;
+  const int64_t hq = q->size(1), hkv = k->size(1);
+  const bool f32 = tensor(a[3], F32, device) != nullptr;
+  const at::Tensor *v = heads_of(a[2], device, rows, hkv, &vs),
+                   *out = dense(a[3], f32 ? F32 : BF16, device, {rows, hq, HEAD_DIM}), *ws = dense(a[9], U8, device, {-1});
+  if (!v || !out || !ws || hq > INT32_MAX || hkv > INT32_MAX) return -1;
+  if (a[8] != Py_None && !(lse = dense(a[8], F32, device, {rows, hq}))) return -1;
+  if (a[10] != Py_None && !(err = error_word(a[10], device))) return -1;
+  if (rows == 0) return OSCAR_OK;
+  const auto *qp = at_ptr<const uint16_t>(q), *kp = at_ptr<const uint16_t>(k), *vp = at_ptr<const uint16_t>(v);
+  void *op = out->data_ptr(), *wp = ws->data_ptr();
+  auto* lp = at_ptr<float>(lse);
+  auto* ep = at_ptr<int32_t>(err);
+  const size_t ws_bytes = static_cast<size_t>(ws->size(0));
+  oscar_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g.prompt(lens, static_cast<int32_t>(n), static_cast<int32_t>(hq), static_cast<int32_t>(hkv),
+                static_cast<int32_t>(window), static_cast<int32_t>(sinks), static_cast<float>(scale), qp, qs, kp, ks, vp,
+                vs, op, f32 ? OSCAR_F32 : OSCAR_BF16, lp, ep, wp, ws_bytes, stream);
+  Py_END_ALLOW_THREADS
+  return st;
+}
+
+// A cache's calls begin with (handle, device, kv heads, layer, requests, ...).  The GIL is kept: a cache's calls come
+// from one thread at a time, and a cache may not be closed under one.
+struct CacheCall {
+  oscar_cache* cache;
+  long long hkv, layer;
+  Py_ssize_t n;
+  int device;
+  int32_t reqs[MAX_REQ];
+};
+bool cache_call(PyObject* const* a, PyObject* stream, CacheCall* c, void** raw) {
+  if (!context(stream, &c->device, raw)) return false;
+  c->cache = static_cast<oscar_cache*>(PyLong_AsVoidPtr(a[0]));
+  const long long device = PyLong_AsLongLong(a[1]);
+  c->hkv = PyLong_AsLongLong(a[2]);
+  c->layer = PyLong_AsLongLong(a[3]);
+  if (PyErr_Occurred() || !c->cache || device != c->device || c->hkv < 1 || c->layer < 0 || c->layer > INT32_MAX) return false;
+  c->n = requests(a[4]);
+  return c->n > 0 && counts(a[4], c->n, c->reqs) >= 0;
+}
+
+// extend(handle, device, kv heads, layer, reqs, k, v, new_lens, stream)
+int extend(PyObject* const* a, Py_ssize_t count) {
+  CacheCall c;
+  int32_t news[MAX_REQ];
+  void* stream;
+  if (count != 9 || !cache_call(a, a[8], &c, &stream)) return -1;
+  int64_t rows = c.n, ks, vs;
+  if (a[7] != Py_None && (rows = counts(a[7], c.n, news)) < 0) return -1;
+  const at::Tensor *k = heads_of(a[5], c.device, rows, c.hkv, &ks), *v = heads_of(a[6], c.device, rows, c.hkv, &vs);
+  if (!k || !v || rows == 0) return -1;
+  return g.extend(c.cache, static_cast<int32_t>(c.layer), static_cast<int32_t>(c.n), c.reqs,
+                  a[7] == Py_None ? nullptr : news, at_ptr<const uint16_t>(k), ks, at_ptr<const uint16_t>(v), vs, stream);
+}
+
+// read_cache(handle, device, kv heads, layer, reqs, starts, counts, k_out, v_out, stream)
+int read_cache(PyObject* const* a, Py_ssize_t count) {
+  CacheCall c;
+  int32_t starts[MAX_REQ], cnt[MAX_REQ];
+  void* stream;
+  if (count != 10 || !cache_call(a, a[9], &c, &stream) || counts(a[5], c.n, starts) < 0) return -1;
+  const int64_t rows = counts(a[6], c.n, cnt);
+  if (rows <= 0) return -1;
+  const bool f32 = tensor(a[7], F32, c.device) != nullptr;
+  const at::Tensor *k = dense(a[7], f32 ? F32 : BF16, c.device, {rows, c.hkv, HEAD_DIM}),
+                   *v = dense(a[8], f32 ? F32 : BF16, c.device, {rows, c.hkv, HEAD_DIM});
+  if (!k || !v) return -1;
+  return g.read2(c.cache, static_cast<int32_t>(c.layer), static_cast<int32_t>(c.n), c.reqs, starts, cnt, k->data_ptr(),
+                 v->data_ptr(), f32 ? OSCAR_F32 : OSCAR_BF16, stream);
+}
+
+// chunk(handle, device, kv heads, layer, reqs, query heads, q, k, v, out, new_lens, workspace, stream)
+int chunk(PyObject* const* a, Py_ssize_t count) {
+  CacheCall c;
+  int32_t news[MAX_REQ];
+  void* stream;
+  if (count != 13 || a[11] == Py_None || !cache_call(a, a[12], &c, &stream)) return -1;
+  const long long hq = PyLong_AsLongLong(a[5]);
+  if (PyErr_Occurred() || hq < 1) return -1;
+  int64_t rows = c.n, qs, ks, vs;
+  if (a[10] != Py_None && (rows = counts(a[10], c.n, news)) < 0) return -1;
+  const at::Tensor *q = heads_of(a[6], c.device, rows, hq, &qs), *k = heads_of(a[7], c.device, rows, c.hkv, &ks),
+                   *v = heads_of(a[8], c.device, rows, c.hkv, &vs), *out = dense(a[9], BF16, c.device, {rows, hq, HEAD_DIM}),
+                   *ws = dense(a[11], U8, c.device, {-1});
+  if (!q || !k || !v || !out || !ws || rows == 0) return -1;
+  return g.chunk(c.cache, static_cast<int32_t>(c.layer), static_cast<int32_t>(c.n), c.reqs,
+                 a[10] == Py_None ? nullptr : news, at_ptr<const uint16_t>(q), qs, at_ptr<const uint16_t>(k), ks,
+                 at_ptr<const uint16_t>(v), vs, at_ptr<uint16_t>(out), ws->data_ptr(), static_cast<size_t>(ws->size(0)),
+                 stream);
+}
+
 template <int (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t count) {
   int st = -1;
@@ -285,12 +408,15 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t count) {
   Py_RETURN_NONE;
 }
 
-// setup((five function addresses))
+// setup((nine function addresses))
 PyObject* setup(PyObject*, PyObject* args) {
-  unsigned long long at[5];
-  if (!PyArg_ParseTuple(args, "(KKKKK)", &at[0], &at[1], &at[2], &at[3], &at[4])) return nullptr;
+  unsigned long long at[9];
+  if (!PyArg_ParseTuple(args, "(KKKKKKKKK)", &at[0], &at[1], &at[2], &at[3], &at[4], &at[5], &at[6], &at[7], &at[8]))
+    return nullptr;
   g = {reinterpret_cast<append16_fn>(at[0]), reinterpret_cast<append4_fn>(at[1]), reinterpret_cast<read4_fn>(at[2]),
-       reinterpret_cast<attend16_fn>(at[3]), reinterpret_cast<attend4_fn>(at[4])};
+       reinterpret_cast<attend16_fn>(at[3]), reinterpret_cast<attend4_fn>(at[4]),
+       reinterpret_cast<prompt_fn>(at[5]), reinterpret_cast<extend_fn>(at[6]), reinterpret_cast<read2_fn>(at[7]),
+       reinterpret_cast<chunk_fn>(at[8])};
   Py_RETURN_NONE;
 }
 
@@ -302,6 +428,10 @@ PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, nullptr},
                          {"append", fast<append>(), METH_FASTCALL, nullptr},
                          {"read", fast<read>(), METH_FASTCALL, nullptr},
                          {"attend", fast<attend>(), METH_FASTCALL, nullptr},
+                         {"prompt", fast<prompt>(), METH_FASTCALL, nullptr},
+                         {"extend", fast<extend>(), METH_FASTCALL, nullptr},
+                         {"read_cache", fast<read_cache>(), METH_FASTCALL, nullptr},
+                         {"chunk", fast<chunk>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_oscar_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
