@@ -9,12 +9,14 @@
 //   chunk_merge_*_kernel   their sum, the history's times R_V^T, over the weights' sum.
 //
 // chunk_scan_kernel: a CTA takes 128 keys at a time.  Four warps unpack them, a key a thread,
-// into fp16 values z + s c in shared memory (times a power of two that keeps them in range;
-// rounded once, half a step 2^-12), from codes that were fetched into registers two steps before.  Per key tile and chain
+// into fp16 values z + s c in shared memory (rounded once, half a step 2^-12), a tile's keys times 2^-a and
+// its values times 2^-b: powers of two from their largest that keep them in range.  Per key tile and chain
 //   S = Q K^T            128 x 128 x 128, tcgen05.mma, both operands in shared memory
-//   p = exp2(S scale - m + 11)   one thread per row; fp16 (2^-12; the shift keeps weights down to
+//   p = exp2(S scale 2^a + b - m + 11)   one thread per row; fp16 (2^-12; the shift keeps weights down to
 //                        2^-25 of the row's largest in full, where fp16 alone would flush them)
 //   O = O + P V          tcgen05.mma, P from TMEM, O in TMEM
+// with m the running maximum of the exponents with b, so of what a key adds to O; the weights' sum takes
+// p 2^-b.
 // The two chains are two tiles of 128 query rows (a row being a (token, head of the group) pair)
 // that share every key, or, where a kv head has 128 rows or fewer, every other key tile each of
 // the one tile of queries: a chain by itself is S, softmax, PV one after another.
@@ -36,22 +38,27 @@ namespace {
 using namespace paged;
 
 constexpr int SC_THREADS = 512;                // softmax of chain 0, of chain 1, unpacking, the others
-constexpr int SC_UNPACK_WARP = 8, SC_MMA_WARP = 12, SC_LOAD_WARP = 14, SC_FETCH_WARP = 15;
+constexpr int SC_UNPACK_WARP = 8, SC_MMA_WARP = 12, SC_SIZE_WARP = 14, SC_FETCH_WARP = 15;
 // Registers a thread: 128 at launch, then 168 for the softmax's two warpgroups, which hold a row
 // of logits each, and 88 for the other two.
 constexpr int SC_REGS = 128, SC_SOFTMAX_REGS = 168, SC_OTHER_REGS = 88;
 static_assert(2 * SC_SOFTMAX_REGS + 2 * SC_OTHER_REGS <= 4 * SC_REGS, "a split above the launch's registers waits forever");
 constexpr int SC_STAGES = 2;                   // of V of a key tile and K of the next
 constexpr int SC_ROWS = 128, SC_KEYS = 128;
+// Steps whose tiles' exponents are kept: those of step s are written when its packed data is there, so SLOTS + 2
+// steps after the products of an earlier step were done.  P V of a tile, which awaits the weights that were made of
+// its exponents, comes LAG steps after them: SLOTS + 2 + LAG steps have to be kept, 9 at most.
+constexpr int SIZES = 16;
 constexpr float SC_LAZY = 4.0f;                // the softmax reference moves only when exceeded by 2^4
 constexpr float SC_SHIFT = 11.0f;              // weights are at most 2^15, and fp16's steps below 2^-14 cost nothing
 
-// Packed keys and values of a step: K codes of 128 keys, V codes of 128, K {s, z}, V {s, z}.
+// Packed keys and values of a step: K codes of a tile, V codes of an earlier one, the {s, z} of both, and those of
+// the tile's own values, for their exponent.
 template <int GK>
 struct Raw {
   static constexpr int META = SC_KEYS * meta_bytes_for(GK);
   alignas(16) uint8_t code[2][SC_KEYS * CODE_BYTES];
-  alignas(16) uint8_t meta[2][META];
+  alignas(16) uint8_t meta[3][META];
 };
 template <int GK, bool PAIR>
 struct alignas(1024) ScanSmem {
@@ -61,6 +68,8 @@ struct alignas(1024) ScanSmem {
   alignas(1024) uint8_t kv[SC_STAGES][2][TILE_BYTES];    // V of an earlier key tile, K of this one
   alignas(128) Raw<GK> raw[2];
   alignas(16) uint8_t out[8][32 * 32];                   // per softmax warp: 32 bytes of its 32 rows
+  alignas(16) float4 size[SIZES];                        // of a key tile: b, 2^a, 2^-b, 2^-a
+  uint64_t size_full[SIZES];
   uint64_t q_full, q_empty, kv_full[SC_STAGES], kv_empty[SC_STAGES], raw_full[SLOTS], raw_empty[SLOTS];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], turn[2];
   uint32_t tmem;
@@ -151,6 +160,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       mbar_init(&sm.raw_full[s], 1);
       mbar_init(&sm.raw_empty[s], 4);
     }
+    for (int s = 0; s < SIZES; ++s) mbar_init(&sm.size_full[s], 1);
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 2);
     for (int a = 0; a < 2; ++a) {
@@ -186,48 +196,61 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
 
   if (warp >= SC_MMA_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SC_OTHER_REGS));
-    if (warp == SC_LOAD_WARP) {
-      // ---- queries
-      if (lane == 0) {
-        bool ok = true;
-        int loads = 0;
-        Walk w = Walk::begin(A);
-        for (; ok && w.next(A); w.done(A)) {
-          if (loads > 0) ok = mbar_wait(&sm.q_empty, (loads - 1) & 1);
+    if (warp == SC_SIZE_WARP) {
+      // ---- exponents of a tile's keys and values, four tokens a lane
+      bool ok = true;
+      int step = 0;
+      Walk w = Walk::begin(A);
+      for (; ok && w.next(A); w.done(A)) {
+        const int n = w.s.j1 - w.s.j0;
+        int left = A.hist[w.s.req] - w.s.j0 * SC_KEYS - lane;   // keys from this lane's first on
+        for (int i = 0; i < n + LAG && ok; ++i, ++step, left -= SC_KEYS) {
+          const int at = step % SLOTS;
+          ok = mbar_wait_warp(&sm.raw_full[at], (step / SLOTS) & 1, ok);
           if (!ok) break;
-          const int tiles = row_tiles(w.s);
-          mbar_expect_tx(&sm.q_full, tiles * TILE_BYTES);
-          for (int a = 0; a < tiles; ++a)
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, w.s.head * A.G,
-                          A.row[w.s.req] + (w.s.block * (PAIR ? 2 : 1) + a) * per_tile, &sm.q_full);
-          ++loads;
-        }
-        if (!ok) gave_up();
-        // nothing may arrive after the CTA
-        if (loads > 0) {
-          mbar_wait(&sm.q_full, (loads - 1) & 1);
-          if (ok) mbar_wait(&sm.q_empty, (loads - 1) & 1);
+          uint32_t top[2] = {0, 0};
+          if (i < n) {
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+              const uint8_t* from = sm.slot(at).meta[2 * u];
+              __half2 most = __float2half2_rn(0.0f);
+#pragma unroll
+              for (int k = 0; k < SC_KEYS / 32; k += 2 / NG) {   // two groups of a token, or two tokens
+                uint2 m;
+                if constexpr (NG == 2) {
+                  m = reinterpret_cast<const uint2*>(from)[32 * k + lane];
+                } else {
+                  m = make_uint2(reinterpret_cast<const uint32_t*>(from)[32 * k + lane],
+                                 reinterpret_cast<const uint32_t*>(from)[32 * k + 32 + lane]);
+                  if (32 * k + 32 >= left) m.y = 0;
+                }
+                if (32 * k >= left) m = make_uint2(0, 0);
+                most = __hmax2(most, largest_values(m));
+              }
+              top[u] = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(__low2float(most), __high2float(most))));
+            }
+          }
+          if (lane == 0) {
+            const int a = value_exponent(top[0]), b = value_exponent(top[1]);
+            sm.size[step % SIZES] = make_float4(static_cast<float>(b), pow2(a), pow2(-b), pow2(-a));
+            mbar_arrive(&sm.size_full[step % SIZES]);
+          }
         }
       }
+      if (!ok && lane == 0) gave_up();
     } else if (warp == SC_FETCH_WARP) {
-      // ---- packed keys and values: 1152 bytes (1280 with two groups) of each page
+      // ---- queries, and packed keys and values
       if (lane == 0) {
         const uint8_t* const pool = c.int2 + A.layer * c.int2_layer_stride;
         const size_t page_bytes = (size_t)c.Hkv * c.record;
         bool ok = true;
-        int step = 0;
-        auto copy = [&](Raw<GK>& raw, int u, int page, int head, int which, uint64_t* bar) {
-          const uint8_t* rec = pool + page * page_bytes + head * c.record;
-          tma_load_1d(raw.code[which] + u * (PAGE * CODE_BYTES), rec + (which ? V_CODES_OFF : K_CODES_OFF), PAGE * CODE_BYTES, bar);
-          tma_load_1d(raw.meta[which] + u * (Raw<GK>::META / 2), rec + (which ? v_meta_off_for(GK) : k_meta_off_for(GK)),
-                      Raw<GK>::META / 2, bar);
-        };
+        int step = 0, loads = 0;
         Walk w = Walk::begin(A);
         for (; ok && w.next(A); w.done(A)) {
+          const int q_at = loads > 0;
           const int n = w.s.j1 - w.s.j0, pages = (A.hist[w.s.req] + PAGE - 1) / PAGE - 2 * w.s.j0, head = w.s.head;
           const int32_t* table = c.hist_pt + (size_t)A.slot[w.s.req] * c.max_pages + 2 * w.s.j0;
-          // page ids of tile i, looked up a step ahead (-1: none); V takes those of LAG steps before
+          // page ids of tile i, looked up a step ahead (-1: none); V's codes take those of LAG steps before
           int id[LAG + 2][2];
           auto look = [&](int i, int (&to)[2]) {
 #pragma unroll
@@ -241,7 +264,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
             const int at = step % SLOTS;
             if (step >= SLOTS) ok = mbar_wait(&sm.raw_empty[at], (step / SLOTS - 1) & 1);
             if (!ok) break;
-            int use[2][2], some = 0;   // [K or V][page]
+            int use[2][2], bytes = 0;   // [K, or V][page]
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -253,23 +276,51 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
                   page = 0;
                 }
                 use[which][u] = there ? page : -1;
-                some += there;
+                bytes += there ? PAGE * CODE_BYTES + (which ? Raw<GK>::META / 2 : Raw<GK>::META) : 0;
               }
-            mbar_expect_tx(&sm.raw_full[at], some * (PAGE * CODE_BYTES + Raw<GK>::META / 2));
+            uint64_t* const bar = &sm.raw_full[at];
+            mbar_expect_tx(bar, bytes);
+            Raw<GK>& raw = sm.slot(at);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int which = 0; which < 2; ++which)
-                if (use[which][u] >= 0) copy(sm.slot(at), u, use[which][u], head, which, &sm.raw_full[at]);
+            for (int u = 0; u < 2; ++u) {
+              const int code_at = u * (PAGE * CODE_BYTES), meta_at = u * (Raw<GK>::META / 2);
+              if (use[0][u] >= 0) {
+                const uint8_t* rec = pool + use[0][u] * page_bytes + head * c.record;
+                tma_load_1d(raw.code[0] + code_at, rec + K_CODES_OFF, PAGE * CODE_BYTES, bar);
+                tma_load_1d(raw.meta[0] + meta_at, rec + k_meta_off_for(GK), Raw<GK>::META / 2, bar);
+                tma_load_1d(raw.meta[2] + meta_at, rec + v_meta_off_for(GK), Raw<GK>::META / 2, bar);
+              }
+              if (use[1][u] >= 0) {
+                const uint8_t* rec = pool + use[1][u] * page_bytes + head * c.record;
+                tma_load_1d(raw.code[1] + code_at, rec + V_CODES_OFF, PAGE * CODE_BYTES, bar);
+                tma_load_1d(raw.meta[1] + meta_at, rec + v_meta_off_for(GK), Raw<GK>::META / 2, bar);
+              }
+            }
 #pragma unroll
             for (int j = 0; j <= LAG; ++j) id[j][0] = id[j + 1][0], id[j][1] = id[j + 1][1];
+            // the queries, behind what can be fetched while the last segment's are in use
+            if (i == q_at) {
+              if (loads > 0) ok = mbar_wait(&sm.q_empty, (loads - 1) & 1);
+              if (!ok) break;
+              const int tiles = row_tiles(w.s);
+              mbar_expect_tx(&sm.q_full, tiles * TILE_BYTES);
+              for (int a = 0; a < tiles; ++a)
+                for (int h = 0; h < 2; ++h)
+                  tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, head * A.G,
+                              A.row[w.s.req] + (w.s.block * (PAIR ? 2 : 1) + a) * per_tile, &sm.q_full);
+              ++loads;
+            }
           }
         }
         if (!ok) gave_up();
         // nothing may arrive after the CTA
+        if (loads > 0) {
+          mbar_wait(&sm.q_full, (loads - 1) & 1);
+          if (ok) mbar_wait(&sm.q_empty, (loads - 1) & 1);
+        }
         for (int k = max(0, step - SLOTS); k < step; ++k) mbar_wait(&sm.raw_full[k % SLOTS], (k / SLOTS) & 1);
       }
-    } else if (warp < SC_LOAD_WARP) {
+    } else if (warp < SC_SIZE_WARP) {
       // ---- products of chain a
       const int a = warp - SC_MMA_WARP;
       bool ok = true;
@@ -349,28 +400,29 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
     Walk w = Walk::begin(A);
     for (; ok && w.next(A); w.done(A)) {
       const int n = w.s.j1 - w.s.j0, left = A.hist[w.s.req] - w.s.j0 * SC_KEYS - r;   // keys from this thread's of tile 0 on
-      const size_t lh = (size_t)A.layer * c.Hkv + w.s.head;
-      const int k_exp = value_exponent(c.tau_k[lh]), v_exp = value_exponent(c.tau_v[lh]);
       for (int i = 0; i < n + LAG && ok; ++i, ++step) {
         const int st = step % SC_STAGES, at = step % SLOTS;
         const Raw<GK>& raw = sm.slot(at);
-        ok = mbar_wait_warp(&sm.raw_full[at], (step / SLOTS) & 1, ok);
+        ok = mbar_wait_warp(&sm.size_full[step % SIZES], (step / SIZES) & 1, ok);   // (behind the packed data)
+        if (!ok) break;
+        const bool now = i < n && i * SC_KEYS < left, then = i >= LAG && (i - LAG) * SC_KEYS < left;
+        const float k_down = sm.size[step % SIZES].w, v_down = i >= LAG ? sm.size[(step - LAG) % SIZES].z : 0.0f;
         if (step >= SC_STAGES) ok = mbar_wait_warp(&sm.kv_empty[st], (step / SC_STAGES - 1) & 1, ok);
         if (!ok) break;
         // V of tile i - LAG, K of tile i (a loop: the code of four roles together is more than the instruction
         // caches hold)
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
-          const int which = u ^ 1, tile = u ? i : i - LAG, e = u ? k_exp : v_exp;
-          const bool some = tile >= 0 && tile < n && tile * SC_KEYS < left;
-          const uint2* code = reinterpret_cast<const uint2*>(raw.code[which]) + 4 * r;
-          const uint32_t* meta = reinterpret_cast<const uint32_t*>(raw.meta[which]) + NG * r;
+          const float down = u ? k_down : v_down;
+          const bool some = u ? now : then;
+          const uint2* code = reinterpret_cast<const uint2*>(raw.code[u ^ 1]) + 4 * r;
+          const uint32_t* meta = reinterpret_cast<const uint32_t*>(raw.meta[u ^ 1]) + NG * r;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {   // 64 channels
             uint8_t* to = sm.kv[st][u] + h * (TILE_BYTES / 2) + r * 128;
             const uint32_t m = some ? meta[NG == 2 ? h : 0] : 0;
             __half2 s[5], z;
-            value_steps(m, e, s, z);
+            value_steps(m, down, s, z);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const uint2 word = some ? code[2 * h + p] : make_uint2(0, 0);
@@ -414,12 +466,13 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
     for (; ok && w.next(A); w.done(A)) {
       const Segment& s = w.s;
       const int n = s.j1 - s.j0, from = PAIR ? 0 : (a ^ step0) & 1;   // the chain's first tile
+      int step = step0 + from;
       step0 += n + LAG;
       if (PAIR && a >= row_tiles(s)) continue;
       const int m = A.m[s.req], tok0 = (s.block * (PAIR ? 2 : 1) + (PAIR ? a : 0)) * per_tile, tok = tok0 + (r >> A.lg);
       const int row = A.row[s.req] + min(tok, m - 1);
-      const float scale2 = A.scale2 * __ldcg(A.q_scale + (size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))) *
-                           pow2(value_exponent(c.tau_k[(size_t)A.layer * c.Hkv + s.head]));
+      // (above 0, so that a masked key's -inf stays that; logits of below 2^30 times 2^-100 are 0 for exp2)
+      const float scale2 = fmaxf(A.scale2 * __ldcg(A.q_scale + (size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))), 0x1p-100f);
       // warps of the tile that have rows; the first arrives for those without, which only meet the others behind the
       // segment: whatever their rows of P are, a row of O has the same row of P alone
       const int busy = min(4, (((m - tok0) << A.lg) + 31) / 32);
@@ -430,10 +483,13 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       bool any = false;
       const int tiles = n > from ? (n - from + LAG - 1) / LAG : 0;   // of the chain
       if (idle) tile += tiles;
-      for (int i = idle ? n : from; i < n; i += LAG, ++tile, left -= LAG * SC_KEYS) {
+      for (int i = idle ? n : from; i < n; i += LAG, step += LAG, ++tile, left -= LAG * SC_KEYS) {
         ok = mbar_wait_warp(&sm.s_full[a], tile & 1, ok);
         if (!ok) break;
         tc_fence_after();
+        // (written before the keys were unpacked, so before S)
+        const float2 size = *reinterpret_cast<const float2*>(&sm.size[step % SIZES]);
+        const float scale = scale2 * size.y;
         uint32_t xr[128];
 #pragma unroll
         for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, xr + 32 * h);
@@ -451,7 +507,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
         for (int j = 4; j < 124; j += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[j + 2 * k], x[j + 2 * k + 1]);
-        const float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])) * scale2;
+        const float top = fmaf(fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])), scale, size.x);
         const bool raise = top > mx + SC_LAZY || (mx == NEG_INF && top > NEG_INF);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
@@ -470,8 +526,8 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
           }
         }
         any = true;
-        const float ref = mx == NEG_INF ? 0.0f : SC_SHIFT - mx;
-        const float2 scale_2 = make_float2(scale2, scale2), ref_2 = make_float2(ref, ref);
+        const float ref = size.x + (mx == NEG_INF ? 0.0f : SC_SHIFT - mx);
+        const float2 scale_2 = make_float2(scale, scale), ref_2 = make_float2(ref, ref);
         float2 sum[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
@@ -500,7 +556,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
           }
         }
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l += sum[0].x + sum[0].y;
+        l = fmaf(sum[0].x + sum[0].y, sm.size[step % SIZES].z, l);
       }
       // the rows' sums, maximum and sum to the workspace
       if (tiles > 0) {
@@ -589,7 +645,7 @@ __device__ __forceinline__ void split_rotation(const float* m, Parts& s) {
 }
 // 2^e with 2^10 <= top 2^e < 2^11, so that what falls below fp16's normal values is below 2^-24 of the row's largest.
 __device__ __forceinline__ int row_exponent(float top) {
-  return min(max(137 - static_cast<int>(__float_as_uint(top) >> 23), -100), 100);
+  return min(137 - static_cast<int>(__float_as_uint(top) >> 23), 126);
 }
 
 constexpr int UNIT = 16;       // rows of a warp's product
@@ -804,13 +860,12 @@ __global__ void __launch_bounds__(MG_THREADS)
     const float4 u = reinterpret_cast<const float4*>(part[r][0])[lane], v = reinterpret_cast<const float4*>(part[r][1])[lane];
     l += part_l[r];
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const float up = inv * pow2(value_exponent(c.tau_v[(size_t)A.layer * c.Hkv + head]));   // (of the scan's values)
     // positions 4 lane, ...: channels 16 (lane / 4) + 2 (lane % 4), + 8, + 1, + 9
     float* to = &far[r][16 * (lane >> 2) + 2 * (lane & 3)];
-    to[0] = (x.x + u.x) * up;
-    to[8] = (x.y + u.y) * up;
-    to[1] = (x.z + u.z) * up;
-    to[9] = (x.w + u.w) * up;
+    to[0] = (x.x + u.x) * inv;
+    to[8] = (x.y + u.y) * inv;
+    to[1] = (x.z + u.z) * inv;
+    to[9] = (x.w + u.w) * inv;
     reinterpret_cast<float4*>(near[r])[lane] =
         make_float4((y.x + v.x) * inv, (y.y + v.y) * inv, (y.z + v.z) * inv, (y.w + v.w) * inv);
   }
@@ -832,7 +887,8 @@ struct MergeRowsSmem {
   alignas(16) uint16_t row[8][UNIT][PITCH];    // a warp's rows: the history's sums (fp16), then the results (bf16)
 };
 // A warp takes 16 rows of one request and kv head at a time; the CTA keeps that head's rotation.  (The history's
-// sums over the weights' and R are rounded to fp16, 2^-12 each, an eighth of what the result's rounding adds.)
+// sums, times a power of two of the row's, and R are rounded to fp16, 2^-12 each, an eighth of what the result's
+// rounding adds.)
 template <bool PAIR>
 __global__ void __launch_bounds__(MG_THREADS, 2)
     chunk_merge_rows_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
@@ -864,9 +920,6 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
   constexpr size_t STEP = (size_t)(PAIR ? 2 : 1) * SC_ROWS * PARTIAL_FLOATS;
   const size_t near_step = (size_t)c.Hkv * (2 * SC_ROWS) * PARTIAL_FLOATS;
   uint16_t (*buf)[PITCH] = sm.row[warp];
-  // the scan's values are at most 2^-8: times 2^8 here, which fp16 holds, the rest of their exponent at the end
-  const int v_exp = value_exponent(c.tau_v[(size_t)A.layer * c.Hkv + head]);
-  const float down = pow2(v_exp - 8);
   for (int unit = (blockIdx.x % per_head) * 8 + warp; unit < B.chunks; unit += per_head * 8) {
     int ri = 0, hi = A.n;
     while (hi - ri > 1) {
@@ -893,6 +946,7 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
 #pragma unroll 4
     for (int j = 0; j < count; ++j) l = fmaf(scan[j * STEP + mine + PARTIAL_L], ex2f(scan[j * STEP + mine + PARTIAL_M] - ref), l);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float down = 1.0f;   // of lane's row: what undoes its power of two
     __syncwarp();
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {   // eight rows, four channels a lane
@@ -900,7 +954,7 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
 #pragma unroll
       for (int r = 0; r < 8; ++r) sum[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int j = 0; j < count; ++j) {
-        const float f = ex2f(scan[j * STEP + mine + PARTIAL_M] - ref) * inv * 256.0f;
+        const float f = ex2f(scan[j * STEP + mine + PARTIAL_M] - ref);
         float4 v[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
@@ -915,9 +969,16 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
         }
       }
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        *reinterpret_cast<uint2*>(&buf[8 * half + r][4 * lane]) = make_uint2(f16x2(sum[r].x, sum[r].y), f16x2(sum[r].z, sum[r].w));
+      for (int r = 0; r < 8; ++r) {
+        const float top = fmaxf(fmaxf(fabsf(sum[r].x), fabsf(sum[r].y)), fmaxf(fabsf(sum[r].z), fabsf(sum[r].w)));
+        const int e = row_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+        const float up = pow2(e);
+        if (lane % UNIT == 8 * half + r) down = pow2(-e) * inv;
+        *reinterpret_cast<uint2*>(&buf[8 * half + r][4 * lane]) =
+            make_uint2(f16x2(sum[r].x * up, sum[r].y * up), f16x2(sum[r].z * up, sum[r].w * up));
+      }
     }
+    const float down0 = __shfl_sync(0xffffffffu, down, lane / 4), down1 = __shfl_sync(0xffffffffu, down, lane / 4 + 8);
     __syncwarp();
     uint32_t a[8][4];
 #pragma unroll
@@ -937,7 +998,7 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
         mma_f16(x[n + 1], a[s][0], a[s][1], a[s][2], a[s][3], b[2], b[3]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[n][i] *= down, x[n + 1][i] *= down;
+      for (int i = 0; i < 4; ++i) x[n][i] *= i < 2 ? down0 : down1, x[n + 1][i] *= i < 2 ? down0 : down1;
     }
     for (int j = 0; j < B.near_splits; ++j) {
       const float f = ex2f(bf[j * near_step + mine + PARTIAL_M] - ref) * inv;

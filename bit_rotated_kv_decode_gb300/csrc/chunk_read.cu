@@ -5,8 +5,8 @@
 //
 // read_history_kernel takes 128 history tokens of one kv head, K or V, at a time, whatever
 // requests they are of: a product of 128 x 128 x 128 on tcgen05.
-//   bf16 outputs  the values z + s c in fp16, times a power of two that keeps them in range, by
-//                 R in fp16: each off by 2^-12, an eighth of what the output's rounding adds;
+//   bf16 outputs  the values z + s c in fp16, times a power of two of the token's that keeps them in
+//                 range, by R in fp16: each off by 2^-12, an eighth of what the output's rounding adds;
 //   fp32 outputs  with c' = c - 1, whole numbers that any type holds,
 //                   x_j = s (c' R^T)_j + (z + s) sum_i R_ji     (per group of channels),
 //                 R in three bf16 parts (24 bits), the small ones first, the sums of its rows
@@ -162,13 +162,12 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
   }
 
   const int total = A.hist[A.n];
-  const float tau = (which ? c.tau_v : c.tau_k)[(size_t)A.layer * c.Hkv + head];
-  const int scale = value_exponent(tau);         // of the values in shared memory
   // (few tiles go to CTAs of their own)
   const int step = GROUPS * per_matrix, first = part + per_matrix * group;
   uint4 words[2];          // codes of this thread's row of the next tile
   uint32_t meta[NG];       // its {s, z}
   int to = -1;             // its row of the output
+  int scale = 0;           // exponent of the staged token's values
   auto fetch = [&](int t) {
     const int i = t * RD_ROWS + r;
     to = -1;
@@ -209,13 +208,18 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
     }
     const uint32_t w[8] = {words[0].x, words[0].y, words[0].z, words[0].w, words[1].x, words[1].y, words[1].z, words[1].w};
     __half2 s[5], z;
+    float down = 0.0f;
+    if constexpr (!F32) {
+      scale = value_exponent(largest_value(meta));
+      down = pow2(-scale);
+    }
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       uint32_t x[8];
       if constexpr (F32) {
         unpack_codes(w[p], x);
       } else {
-        if (p % (8 / NG) == 0) value_steps(meta[p / (8 / NG)], scale, s, z);
+        if (p % (8 / NG) == 0) value_steps(meta[p / (8 / NG)], down, s, z);
         unpack_values(w[p], s, z, x);
       }
       *reinterpret_cast<uint4*>(sm.code[group] + tile_at(r, 2 * p)) = make_uint4(x[0], x[1], x[2], x[3]);
@@ -258,7 +262,8 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
   const size_t row_bytes = (size_t)c.Hkv * (D * SIZE);
   const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + acc0;
   for (int t = first; t < tiles && ok; t += step, ++count) {
-    const int buf = count & 1, mine = now;   // (the row of this thread's token, staged a tile ago)
+    const int buf = count & 1, mine = now;   // (this thread's token, staged a tile ago: its row and exponent)
+    const float up = pow2(scale);
     const bool more = t + step < tiles;
     ok = group_all(group, mbar_wait(&sm.done[group], count & 1));
     if (!ok) break;
@@ -297,7 +302,6 @@ __global__ void __launch_bounds__(read_groups(GK, F32) * RD_ROWS, 1)
       }
     } else {
       uint8_t* turn = sm.x.out[warp];
-      const float up = pow2(scale);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {   // 64 channels
         uint32_t w[32];

@@ -631,3 +631,85 @@ def test_calls_without_the_extension_are_the_same(b, monkeypatch):
         got.append((out, ko, vo, two))
         h.cache.close(r)
     assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+@pytest.mark.parametrize("group", [128, 64])
+def test_thresholds_far_above_the_values(b, group):
+    """Thresholds that clip nothing, whatever the values' size: what is lost is relative to the values, not to them."""
+    h = Held(b, group=group, seed=21, requests=2, tokens=1600)
+    for size in (2.0 ** -9, 1.0, 2.0 ** 9):
+        tau = np.full((1, 2), 65504, np.float32)
+        h.cache = b.OscarCache(b.make_config(1, 8, 2, 2, 30, 60, group_size=group), *h.rot, tau, tau)
+        r = [h.cache.open() for _ in range(2)]
+        k, v = h.tokens(1500)
+        v = (v * size).bfloat16()
+        h.cache.extend(0, r, k, v, new_lens=[1300, 200])
+        for lens in ([5], [200]):
+            m = lens[0]
+            kn, vn = h.tokens(m)
+            q, vn = (h.rnd(m, 8, D) / 4).bfloat16(), (vn * size).bfloat16()
+            out = torch.empty_like(q)
+            h.cache.chunk_attention(0, r[:1], q, kn, vn, out, new_lens=lens)
+            (kc, vc), _, _ = h.stored(r[0])
+            p = torch.arange(1300 + m, device="cuda")
+            see = p[None] <= torch.arange(1300, 1300 + m, device="cuda")[:, None]
+            want = attend(q, torch.cat([kc, kn.double()]), torch.cat([vc, vn.double()]), see)[0]
+            assert off_by(out, want) < 4e-3, (size, m, off_by(out, want))
+        ko, vo = (torch.empty(1300, 2, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        h.cache.read(0, r[:1], [0], [1300], ko, vo)
+        assert off_by(ko, kc) < 3e-3 and off_by(vo, vc) < 3e-3, (size, off_by(ko, kc), off_by(vo, vc))
+        h.cache.check()
+
+
+@pytest.mark.parametrize("group", [128, 64])
+def test_values_of_many_sizes(b, group):
+    """Values whose size changes along the request by up to 2^12, and with it their weight in the sum."""
+    h = Held(b, group=group, seed=22, requests=1, tokens=1600)
+    tau = np.full((1, 2), 65504, np.float32)
+    h.cache = b.OscarCache(b.make_config(1, 8, 2, 1, 30, 30, group_size=group), *h.rot, tau, tau)
+    r = h.cache.open()
+    k, v = h.tokens(1500)
+    v = (v * torch.exp2(torch.randint(-12, 1, (47,), device="cuda").repeat_interleave(32)[:1500].float())[:, None, None]).bfloat16()
+    h.cache.extend(0, [r], k, v, new_lens=[1500])
+    for m in (3, 150):
+        kn, vn = h.tokens(m)
+        q, vn = (h.rnd(m, 8, D) / 4).bfloat16(), (vn / 4096).bfloat16()
+        out = torch.empty_like(q)
+        h.cache.chunk_attention(0, [r], q, kn, vn, out, new_lens=[m])
+        (kc, vc), _, _ = h.stored(r)
+        p = torch.arange(1500 + m, device="cuda")
+        see = p[None] <= torch.arange(1500, 1500 + m, device="cuda")[:, None]
+        want = attend(q, torch.cat([kc, kn.double()]), torch.cat([vc, vn.double()]), see)[0]
+        assert off_by(out, want) < 4e-3
+    h.cache.check()
+
+
+def test_values_that_are_not_finite(b):
+    """Infinities and NaN among the new tokens: what appends write; another request's rows do not see them."""
+    one, two = (Held(b, seed=23, tokens=900) for _ in range(2))
+    r = [one.cache.open() for _ in range(2)]
+    assert r == [two.cache.open() for _ in range(2)]
+    k, v = one.tokens(1000)
+    k[100, 0, 3], k[130, 1, 7], v[90, 0, 0], v[140] = math.inf, -math.inf, math.nan, -math.inf
+    one.cache.extend(0, r, k, v, new_lens=[600, 400])
+    for i in range(600):
+        some = r if i < 400 else r[:1]
+        rows = [i, 600 + i][:len(some)]
+        two.cache.append(0, some, k[rows].contiguous(), v[rows].contiguous())
+    one.cache.check()
+    for x in r:
+        pa, pb = one.cache.pages(x)[0], two.cache.pages(x)[0]
+        he = one.cache.length(x, 0)[1] - 64
+        for i, (p, q) in enumerate(zip(pa, pb)):
+            rows = min(64, he - 64 * i)
+            for at, w in ((0, 32), (2048, 32), (4096, 4), (4352, 4)):
+                a, c = one.cache.int2_pool(0)[p, :, at:at + rows * w], two.cache.int2_pool(0)[q, :, at:at + rows * w]
+                assert torch.equal(a, c), (x, i, at, (a != c).nonzero()[:8].tolist())
+    kn, vn = one.tokens(90)
+    q = one.rnd(90, 8, D).bfloat16()
+    out = torch.empty_like(q)
+    one.cache.chunk_attention(0, r, q, kn, vn, out, new_lens=[30, 60])
+    clean = out.clone()
+    kn[30:], vn[30:], q[30:] = math.nan, math.nan, math.nan
+    one.cache.chunk_attention(0, r, q, kn, vn, out, new_lens=[30, 60])
+    assert torch.equal(out[:30].view(torch.int16), clean[:30].view(torch.int16))
