@@ -52,13 +52,14 @@ constexpr int SIZES = 16;
 constexpr float SC_LAZY = 4.0f;                // the softmax reference moves only when exceeded by 2^4
 constexpr float SC_SHIFT = 11.0f;              // weights are at most 2^15, and fp16's steps below 2^-14 cost nothing
 
-// Packed keys and values of a step: K codes of a tile, V codes of an earlier one, the {s, z} of both, and those of
-// the tile's own values, for their exponent.
+// Packed data of a step: K codes of a tile, V codes of an earlier one and their {s, z}; {s, z} of the tile's own keys
+// and values, page by page as records have them.
 template <int GK>
 struct Raw {
   static constexpr int META = SC_KEYS * meta_bytes_for(GK);
   alignas(16) uint8_t code[2][SC_KEYS * CODE_BYTES];
-  alignas(16) uint8_t meta[3][META];
+  alignas(16) uint8_t v_meta[META];
+  alignas(16) uint8_t meta[2][META];
 };
 template <int GK, bool PAIR>
 struct alignas(1024) ScanSmem {
@@ -140,6 +141,16 @@ struct Walk {
   }
 };
 
+// A wait of a warp that is ahead of the others: one lane asks (all 32 of them asking all along slow the others'
+// shared memory: 2K tokens over 60K cached 1400 us, 1286 this way; for waits that are short this one is slower).
+__device__ __forceinline__ bool mbar_wait_lane(uint64_t* bar, uint32_t parity, bool ok) {
+  if (!ok) return false;
+  int done = 1;
+  if ((threadIdx.x & 31) == 0) done = mbar_wait(bar, parity);
+  done = __shfl_sync(0xffffffffu, done, 0);
+  __syncwarp();
+  return done != 0;
+}
 template <int GK, bool PAIR>
 __global__ void __launch_bounds__(SC_THREADS, 1)
     chunk_scan_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
@@ -206,22 +217,22 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
         int left = A.hist[w.s.req] - w.s.j0 * SC_KEYS - lane;   // keys from this lane's first on
         for (int i = 0; i < n + LAG && ok; ++i, ++step, left -= SC_KEYS) {
           const int at = step % SLOTS;
-          ok = mbar_wait_warp(&sm.raw_full[at], (step / SLOTS) & 1, ok);
+          ok = mbar_wait_lane(&sm.raw_full[at], (step / SLOTS) & 1, ok);
           if (!ok) break;
           uint32_t top[2] = {0, 0};
           if (i < n) {
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-              const uint8_t* from = sm.slot(at).meta[2 * u];
+              const uint8_t* from = sm.slot(at).meta[0] + u * (Raw<GK>::META / 2);
               __half2 most = __float2half2_rn(0.0f);
 #pragma unroll
               for (int k = 0; k < SC_KEYS / 32; k += 2 / NG) {   // two groups of a token, or two tokens
+                const uint8_t* page = from + (k >> 1) * Raw<GK>::META;
                 uint2 m;
                 if constexpr (NG == 2) {
-                  m = reinterpret_cast<const uint2*>(from)[32 * k + lane];
+                  m = reinterpret_cast<const uint2*>(page)[32 * (k & 1) + lane];
                 } else {
-                  m = make_uint2(reinterpret_cast<const uint32_t*>(from)[32 * k + lane],
-                                 reinterpret_cast<const uint32_t*>(from)[32 * k + 32 + lane]);
+                  m = make_uint2(reinterpret_cast<const uint32_t*>(page)[lane], reinterpret_cast<const uint32_t*>(page)[32 + lane]);
                   if (32 * k + 32 >= left) m.y = 0;
                 }
                 if (32 * k >= left) m = make_uint2(0, 0);
@@ -239,87 +250,67 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       }
       if (!ok && lane == 0) gave_up();
     } else if (warp == SC_FETCH_WARP) {
-      // ---- queries, and packed keys and values
-      if (lane == 0) {
-        const uint8_t* const pool = c.int2 + A.layer * c.int2_layer_stride;
-        const size_t page_bytes = (size_t)c.Hkv * c.record;
-        bool ok = true;
-        int step = 0, loads = 0;
-        Walk w = Walk::begin(A);
-        for (; ok && w.next(A); w.done(A)) {
-          const int q_at = loads > 0;
-          const int n = w.s.j1 - w.s.j0, pages = (A.hist[w.s.req] + PAGE - 1) / PAGE - 2 * w.s.j0, head = w.s.head;
-          const int32_t* table = c.hist_pt + (size_t)A.slot[w.s.req] * c.max_pages + 2 * w.s.j0;
-          // page ids of tile i, looked up a step ahead (-1: none); V's codes take those of LAG steps before
-          int id[LAG + 2][2];
-          auto look = [&](int i, int (&to)[2]) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) to[u] = i < n && 2 * i + u < pages ? __ldcg(table + 2 * i + u) : -1;
-          };
-#pragma unroll
-          for (int j = 0; j < LAG; ++j) id[j][0] = id[j][1] = -1;
-          look(0, id[LAG]);
-          for (int i = 0; i < n + LAG && ok; ++i, ++step) {
-            look(i + 1, id[LAG + 1]);
-            const int at = step % SLOTS;
-            if (step >= SLOTS) ok = mbar_wait(&sm.raw_empty[at], (step / SLOTS - 1) & 1);
-            if (!ok) break;
-            int use[2][2], bytes = 0;   // [K, or V][page]
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int which = 0; which < 2; ++which) {
-                const bool there = which ? i >= LAG && 2 * (i - LAG) + u < pages : i < n && 2 * i + u < pages;
-                int page = id[which ? 0 : LAG][u];
-                if (there && (page < 0 || page >= c.n_int2_pages)) {
-                  atomicOr(c.err, ERR_INT2_PAGE);
-                  page = 0;
-                }
-                use[which][u] = there ? page : -1;
-                bytes += there ? PAGE * CODE_BYTES + (which ? Raw<GK>::META / 2 : Raw<GK>::META) : 0;
-              }
-            uint64_t* const bar = &sm.raw_full[at];
-            mbar_expect_tx(bar, bytes);
-            Raw<GK>& raw = sm.slot(at);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int code_at = u * (PAGE * CODE_BYTES), meta_at = u * (Raw<GK>::META / 2);
-              if (use[0][u] >= 0) {
-                const uint8_t* rec = pool + use[0][u] * page_bytes + head * c.record;
-                tma_load_1d(raw.code[0] + code_at, rec + K_CODES_OFF, PAGE * CODE_BYTES, bar);
-                tma_load_1d(raw.meta[0] + meta_at, rec + k_meta_off_for(GK), Raw<GK>::META / 2, bar);
-                tma_load_1d(raw.meta[2] + meta_at, rec + v_meta_off_for(GK), Raw<GK>::META / 2, bar);
-              }
-              if (use[1][u] >= 0) {
-                const uint8_t* rec = pool + use[1][u] * page_bytes + head * c.record;
-                tma_load_1d(raw.code[1] + code_at, rec + V_CODES_OFF, PAGE * CODE_BYTES, bar);
-                tma_load_1d(raw.meta[1] + meta_at, rec + v_meta_off_for(GK), Raw<GK>::META / 2, bar);
-              }
+      // ---- queries, and packed keys and values: a lane a piece of a page, whose id it looks up a step ahead
+      static_assert(v_meta_off_for(GK) == k_meta_off_for(GK) + Raw<GK>::META / 2, "{s, z} of K and V side by side");
+      const uint8_t* const pool = c.int2 + A.layer * c.int2_layer_stride;
+      const size_t page_bytes = (size_t)c.Hkv * c.record;
+      const int u = lane & 1, kind = lane >> 1;   // page of the tile; K codes, {s, z}, V codes and {s, z} of LAG steps ago
+      const int lag = kind < 2 ? 0 : LAG, size = kind == 1 ? Raw<GK>::META : kind == 3 ? Raw<GK>::META / 2 : PAGE * CODE_BYTES;
+      const int off = kind == 0 ? K_CODES_OFF : kind == 1 ? k_meta_off_for(GK) : kind == 2 ? V_CODES_OFF : v_meta_off_for(GK);
+      const uint32_t to = u * size + static_cast<uint32_t>(kind == 0   ? offsetof(Raw<GK>, code)
+                                                           : kind == 1 ? offsetof(Raw<GK>, meta)
+                                                           : kind == 2 ? offsetof(Raw<GK>, code) + SC_KEYS * CODE_BYTES
+                                                                       : offsetof(Raw<GK>, v_meta));
+      bool ok = true;
+      int step = 0, loads = 0;
+      Walk w = Walk::begin(A);
+      for (; ok && w.next(A); w.done(A)) {
+        const int n = w.s.j1 - w.s.j0, pages = (A.hist[w.s.req] + PAGE - 1) / PAGE - 2 * w.s.j0, head = w.s.head;
+        const int q_at = loads > 0;   // the queries come behind what can be fetched while the last segment's are in use
+        const int32_t* table = c.hist_pt + (size_t)A.slot[w.s.req] * c.max_pages + 2 * w.s.j0;
+        auto has = [&](int i) { return lane < 8 && i >= lag && i - lag < n && 2 * (i - lag) + u < pages; };
+        auto look = [&](int i) { return has(i) ? __ldcg(table + 2 * (i - lag) + u) : 0; };
+        int next = look(0);
+        for (int i = 0; i < n + LAG; ++i, ++step) {
+          int page = next;
+          next = look(i + 1);
+          const int at = step % SLOTS;
+          if (step >= SLOTS) ok = mbar_wait_lane(&sm.raw_empty[at], (step / SLOTS - 1) & 1, ok);
+          if (!ok) break;
+          const bool some = has(i);
+          if (some && (page < 0 || page >= c.n_int2_pages)) {
+            atomicOr(c.err, ERR_INT2_PAGE);
+            page = 0;
+          }
+          const uint32_t bytes = __reduce_add_sync(0xffffffffu, some ? size : 0);
+          if (lane == 0) mbar_expect_tx(&sm.raw_full[at], bytes);
+          __syncwarp();
+          if (some)
+            tma_load_1d(reinterpret_cast<uint8_t*>(&sm.slot(at)) + to, pool + page * page_bytes + head * c.record + off, size,
+                        &sm.raw_full[at]);
+          if (i == q_at) {
+            if (loads > 0) ok = mbar_wait_lane(&sm.q_empty, (loads - 1) & 1, ok);
+            if (!ok) {
+              ++step;
+              break;
             }
-#pragma unroll
-            for (int j = 0; j <= LAG; ++j) id[j][0] = id[j + 1][0], id[j][1] = id[j + 1][1];
-            // the queries, behind what can be fetched while the last segment's are in use
-            if (i == q_at) {
-              if (loads > 0) ok = mbar_wait(&sm.q_empty, (loads - 1) & 1);
-              if (!ok) break;
-              const int tiles = row_tiles(w.s);
-              mbar_expect_tx(&sm.q_full, tiles * TILE_BYTES);
-              for (int a = 0; a < tiles; ++a)
-                for (int h = 0; h < 2; ++h)
-                  tma_load_3d(sm.q[a] + h * (TILE_BYTES / 2), &q_map, 64 * h, head * A.G,
-                              A.row[w.s.req] + (w.s.block * (PAIR ? 2 : 1) + a) * per_tile, &sm.q_full);
-              ++loads;
-            }
+            const int tiles = row_tiles(w.s);
+            if (lane == 0) mbar_expect_tx(&sm.q_full, tiles * TILE_BYTES);
+            __syncwarp();
+            if (lane < 2 * tiles)
+              tma_load_3d(sm.q[lane >> 1] + (lane & 1) * (TILE_BYTES / 2), &q_map, 64 * (lane & 1), head * A.G,
+                          A.row[w.s.req] + (w.s.block * (PAIR ? 2 : 1) + (lane >> 1)) * per_tile, &sm.q_full);
+            ++loads;
           }
         }
-        if (!ok) gave_up();
-        // nothing may arrive after the CTA
-        if (loads > 0) {
-          mbar_wait(&sm.q_full, (loads - 1) & 1);
-          if (ok) mbar_wait(&sm.q_empty, (loads - 1) & 1);
-        }
-        for (int k = max(0, step - SLOTS); k < step; ++k) mbar_wait(&sm.raw_full[k % SLOTS], (k / SLOTS) & 1);
       }
+      if (!ok && lane == 0) gave_up();
+      // nothing may arrive after the CTA
+      if (loads > 0) {
+        mbar_wait(&sm.q_full, (loads - 1) & 1);
+        if (ok) mbar_wait(&sm.q_empty, (loads - 1) & 1);
+      }
+      for (int k = max(0, step - SLOTS); k < step; ++k) mbar_wait(&sm.raw_full[k % SLOTS], (k / SLOTS) & 1);
     } else if (warp < SC_SIZE_WARP) {
       // ---- products of chain a
       const int a = warp - SC_MMA_WARP;
@@ -416,7 +407,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
           const float down = u ? k_down : v_down;
           const bool some = u ? now : then;
           const uint2* code = reinterpret_cast<const uint2*>(raw.code[u ^ 1]) + 4 * r;
-          const uint32_t* meta = reinterpret_cast<const uint32_t*>(raw.meta[u ^ 1]) + NG * r;
+          const uint32_t* meta = reinterpret_cast<const uint32_t*>(u ? raw.meta[r / PAGE] : raw.v_meta) + NG * (u ? r % PAGE : r);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {   // 64 channels
             uint8_t* to = sm.kv[st][u] + h * (TILE_BYTES / 2) + r * 128;
