@@ -27,6 +27,7 @@
 // cut into one equal range per SM: a long request is spread over all of them, and none waits for
 // the last segment.
 #include <atomic>
+#include <type_traits>
 
 #include "append_device.cuh"
 #include "chunk.h"
@@ -45,6 +46,7 @@ constexpr int SC_REGS = 128, SC_SOFTMAX_REGS = 168, SC_OTHER_REGS = 88;
 static_assert(2 * SC_SOFTMAX_REGS + 2 * SC_OTHER_REGS <= 4 * SC_REGS, "a split above the launch's registers waits forever");
 constexpr int SC_STAGES = 2;                   // of V of a key tile and K of the next
 constexpr int SC_ROWS = 128, SC_KEYS = 128;
+constexpr int SC_FEW = 64;                     // rows of which a chain's first two warps have the softmax
 // Steps whose tiles' exponents are kept: those of step s are written when its packed data is there, so SLOTS + 2
 // steps after the products of an earlier step were done.  P V of a tile, which awaits the weights that were made of
 // its exponents, comes LAG steps after them: SLOTS + 2 + LAG steps have to be kept, 9 at most.
@@ -151,7 +153,7 @@ __device__ __forceinline__ bool mbar_wait_lane(uint64_t* bar, uint32_t parity, b
   __syncwarp();
   return done != 0;
 }
-template <int GK, bool PAIR>
+template <int GK, bool PAIR, bool FEW>
 __global__ void __launch_bounds__(SC_THREADS, 1)
     chunk_scan_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
                       const __grid_constant__ CUtensorMap q_map) {
@@ -164,12 +166,12 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < SC_STAGES; ++s) {
-      mbar_init(&sm.kv_full[s], 4);
+      mbar_init(&sm.kv_full[s], FEW ? 8 : 4);
       mbar_init(&sm.kv_empty[s], PAIR ? 2 : 1);
     }
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&sm.raw_full[s], 1);
-      mbar_init(&sm.raw_empty[s], 4);
+      mbar_init(&sm.raw_empty[s], FEW ? 8 : 4);
     }
     for (int s = 0; s < SIZES; ++s) mbar_init(&sm.size_full[s], 1);
     mbar_init(&sm.q_full, 1);
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       mbar_init(&sm.p_full[a][0], 4);
       mbar_init(&sm.p_full[a][1], 4);
       mbar_init(&sm.o_full[a], 1);
-      mbar_init(&sm.o_empty[a], 4);
+      mbar_init(&sm.o_empty[a], FEW ? 2 : 4);
       mbar_init(&sm.turn[a], 1);
     }
     mbar_init_fence();
@@ -203,6 +205,222 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
   // tiles of rows of a segment's block
   auto row_tiles = [&](const Segment& s) {
     return PAIR && A.m[s.req] - s.block * 2 * per_tile > per_tile ? 2 : 1;
+  };
+
+  // keys' and values' values: thread r those of a tile's key r; what is 0 (V) and 1 (K) from u0 to u1
+  auto unpack = [&](int r, int u0, int u1) {
+    bool ok = true;
+    int step = 0;
+    Walk w = Walk::begin(A);
+    for (; ok && w.next(A); w.done(A)) {
+      const int n = w.s.j1 - w.s.j0, left = A.hist[w.s.req] - w.s.j0 * SC_KEYS - r;   // keys from this thread's of tile 0 on
+      for (int i = 0; i < n + LAG && ok; ++i, ++step) {
+        const int st = step % SC_STAGES, at = step % SLOTS;
+        const Raw<GK>& raw = sm.slot(at);
+        ok = mbar_wait_warp(&sm.size_full[step % SIZES], (step / SIZES) & 1, ok);   // (behind the packed data)
+        if (!ok) break;
+        const bool now = i < n && i * SC_KEYS < left, then = i >= LAG && (i - LAG) * SC_KEYS < left;
+        const float k_down = sm.size[step % SIZES].w, v_down = i >= LAG ? sm.size[(step - LAG) % SIZES].z : 0.0f;
+        if (step >= SC_STAGES) ok = mbar_wait_warp(&sm.kv_empty[st], (step / SC_STAGES - 1) & 1, ok);
+        if (!ok) break;
+        // V of tile i - LAG, K of tile i (a loop: the code of four roles together is more than the instruction
+        // caches hold)
+#pragma unroll 1
+        for (int u = u0; u < u1; ++u) {
+          const float down = u ? k_down : v_down;
+          const bool some = u ? now : then;
+          const uint2* code = reinterpret_cast<const uint2*>(raw.code[u ^ 1]) + 4 * r;
+          const uint32_t* meta = reinterpret_cast<const uint32_t*>(u ? raw.meta[r / PAGE] : raw.v_meta) + NG * (u ? r % PAGE : r);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {   // 64 channels
+            uint8_t* to = sm.kv[st][u] + h * (TILE_BYTES / 2) + r * 128;
+            const uint32_t m = some ? meta[NG == 2 ? h : 0] : 0;
+            __half2 s[5], z;
+            value_steps(m, down, s, z);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const uint2 word = some ? code[2 * h + p] : make_uint2(0, 0);
+              uint32_t x[8];
+              unpack_values(word.x, s, z, x);
+              *reinterpret_cast<uint4*>(to + (((4 * p) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(to + (((4 * p + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+              unpack_values(word.y, s, z, x);
+              *reinterpret_cast<uint4*>(to + (((4 * p + 2) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(to + (((4 * p + 3) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.kv_full[st]);
+          mbar_arrive(&sm.raw_empty[at]);
+        }
+      }
+    }
+    if (!ok && lane == 0) gave_up();
+  };
+  // softmax of chain a, one thread per row
+  auto softmax = [&]() {
+    const int a = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = lane_off + 128 * a, to = lane_off + 256 + 128 * a;
+    auto meet_chain = [&](bool mine) {   // a barrier of the chain's warps: whether all say yes
+      int all;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, %3, p;\n selp.b32 %0, 1, 0, q;\n}"
+          : "=r"(all)
+          : "r"(static_cast<int>(mine)), "r"(a + 1), "n"(FEW ? SC_FEW : SC_ROWS)
+          : "memory");
+      return all != 0;
+    };
+    bool ok = true;
+    int tile = 0, outs = 0, step0 = 0;   // key tiles and segments of this chain so far; steps of the CTA
+    Walk w = Walk::begin(A);
+    for (; ok && w.next(A); w.done(A)) {
+      const Segment& s = w.s;
+      const int n = s.j1 - s.j0, from = PAIR ? 0 : (a ^ step0) & 1;   // the chain's first tile
+      int step = step0 + from;
+      step0 += n + LAG;
+      if (PAIR && a >= row_tiles(s)) continue;
+      const int m = A.m[s.req], tok0 = (s.block * (PAIR ? 2 : 1) + (PAIR ? a : 0)) * per_tile, tok = tok0 + (r >> A.lg);
+      const int row = A.row[s.req] + min(tok, m - 1);
+      // (above 0, so that a masked key's -inf stays that; logits of below 2^30 times 2^-100 are 0 for exp2)
+      const float scale2 = fmaxf(A.scale2 * __ldcg(A.q_scale + (size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))), 0x1p-100f);
+      // warps of the tile that have rows; the first arrives for those without, which only meet the others behind the
+      // segment: whatever their rows of P are, a row of O has the same row of P alone
+      const int busy = min(4, (((m - tok0) << A.lg) + 31) / 32);
+      const uint32_t arrivals = (warp & 3) == 0 ? 5 - busy : 1;
+      const bool idle = (warp & 3) >= busy;
+      int left = A.hist[s.req] - (s.j0 + from) * SC_KEYS;   // keys from the tile on
+      float mx = NEG_INF, l = 0.0f;
+      bool any = false;
+      const int tiles = n > from ? (n - from + LAG - 1) / LAG : 0;   // of the chain
+      if (idle) tile += tiles;
+      for (int i = idle ? n : from; i < n; i += LAG, step += LAG, ++tile, left -= LAG * SC_KEYS) {
+        ok = mbar_wait_warp(&sm.s_full[a], tile & 1, ok);
+        if (!ok) break;
+        tc_fence_after();
+        // (written before the keys were unpacked, so before S)
+        const float2 size = *reinterpret_cast<const float2*>(&sm.size[step % SIZES]);
+        const float scale = scale2 * size.y;
+        uint32_t xr[128];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, xr + 32 * h);
+        tc_wait_ld();
+        float* x = reinterpret_cast<float*>(xr);
+        if (left < SC_KEYS) {   // keys behind the end
+#pragma unroll
+          for (int j = 0; j < SC_KEYS; ++j)
+            if (j >= left) x[j] = NEG_INF;
+        }
+        float t[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = x[k];
+#pragma unroll
+        for (int j = 4; j < 124; j += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[j + 2 * k], x[j + 2 * k + 1]);
+        const float top = fmaf(fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])), scale, size.x);
+        const bool raise = top > mx + SC_LAZY || (mx == NEG_INF && top > NEG_INF);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
+          l *= f;
+          if (raise) mx = top;
+          if (any) {   // the product before S is done: S was issued after it
+#pragma unroll 1
+            for (int col = 0; col < 128; col += 16) {   // in small pieces: the logits are live
+              uint32_t o[16];
+              tmem_ld16(to + col, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(to + col, o);
+            }
+          }
+        }
+        any = true;
+        const float ref = size.x + (mx == NEG_INF ? 0.0f : SC_SHIFT - mx);
+        const float2 scale_2 = make_float2(scale, scale), ref_2 = make_float2(ref, ref);
+        float2 sum[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {   // 32 keys
+          float2 y[16];
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = fma2(make_float2(x[32 * h + 2 * j], x[32 * h + 2 * j + 1]), scale_2, ref_2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            y[j].x = ex2f(y[j].x);
+            y[j].y = ex2f(y[j].y);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            pk[j] = f16x2(y[j].x, y[j].y);
+            sum[j & 3] = add2(sum[j & 3], y[j]);
+          }
+          tmem_st16(ts + 64 * (h >> 1) + 16 * (h & 1), pk);   // P lies over S, 64 keys in 32 columns
+          if (h & 1) {
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[a][h >> 1], arrivals);
+          }
+        }
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l = fmaf(sum[0].x + sum[0].y, sm.size[step % SIZES].z, l);
+      }
+      // the rows' sums, maximum and sum to the workspace
+      if (tiles > 0) {
+        if (!idle) ok = mbar_wait_warp(&sm.o_full[a], outs & 1, ok);
+        ok = meet_chain(ok);
+        if (!ok) break;
+        tc_fence_after();
+        ++outs;
+      }
+      if (!idle) {
+        float* part = A.records + ((size_t)(s.index + blockIdx.x) * 2 + a) * SC_ROWS * PARTIAL_FLOATS;
+        part[r * PARTIAL_FLOATS + PARTIAL_M] = mx - SC_SHIFT;
+        part[r * PARTIAL_FLOATS + PARTIAL_L] = l;
+        uint8_t* stage = sm.out[warp];
+#pragma unroll 1
+        for (int col = 0; col < 128; col += 32) {
+          uint32_t o[32];
+          if (tiles > 0) {
+            tmem_ld32(to + col, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+          }
+          // turned through shared memory, so that two lanes store 32 bytes of a row together
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ (lane >> 2 & 1)) << 4)) =
+                  make_uint4(o[8 * j + 4 * k], o[8 * j + 4 * k + 1], o[8 * j + 4 * k + 2], o[8 * j + 4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int rw = 16 * k + lane / 2, rr = 32 * (warp & 3) + rw;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * 32 + (((lane & 1) ^ (rw >> 2 & 1)) << 4));
+              if (tok0 + (rr >> A.lg) < m)
+                *reinterpret_cast<uint4*>(part + rr * PARTIAL_FLOATS + col + 8 * j + 4 * (lane & 1)) = v;
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (tiles > 0) {   // O is read: the next segment may write it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_empty[a]);
+      }
+    }
+    if (!ok && lane == 0) gave_up();
   };
 
   if (warp >= SC_MMA_WARP) {
@@ -385,219 +603,14 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
   } else if (warp >= SC_UNPACK_WARP) {
     // ---- keys and values, a key a thread
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SC_OTHER_REGS));
-    const int r = threadIdx.x & (SC_KEYS - 1);
-    bool ok = true;
-    int step = 0;
-    Walk w = Walk::begin(A);
-    for (; ok && w.next(A); w.done(A)) {
-      const int n = w.s.j1 - w.s.j0, left = A.hist[w.s.req] - w.s.j0 * SC_KEYS - r;   // keys from this thread's of tile 0 on
-      for (int i = 0; i < n + LAG && ok; ++i, ++step) {
-        const int st = step % SC_STAGES, at = step % SLOTS;
-        const Raw<GK>& raw = sm.slot(at);
-        ok = mbar_wait_warp(&sm.size_full[step % SIZES], (step / SIZES) & 1, ok);   // (behind the packed data)
-        if (!ok) break;
-        const bool now = i < n && i * SC_KEYS < left, then = i >= LAG && (i - LAG) * SC_KEYS < left;
-        const float k_down = sm.size[step % SIZES].w, v_down = i >= LAG ? sm.size[(step - LAG) % SIZES].z : 0.0f;
-        if (step >= SC_STAGES) ok = mbar_wait_warp(&sm.kv_empty[st], (step / SC_STAGES - 1) & 1, ok);
-        if (!ok) break;
-        // V of tile i - LAG, K of tile i (a loop: the code of four roles together is more than the instruction
-        // caches hold)
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          const float down = u ? k_down : v_down;
-          const bool some = u ? now : then;
-          const uint2* code = reinterpret_cast<const uint2*>(raw.code[u ^ 1]) + 4 * r;
-          const uint32_t* meta = reinterpret_cast<const uint32_t*>(u ? raw.meta[r / PAGE] : raw.v_meta) + NG * (u ? r % PAGE : r);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {   // 64 channels
-            uint8_t* to = sm.kv[st][u] + h * (TILE_BYTES / 2) + r * 128;
-            const uint32_t m = some ? meta[NG == 2 ? h : 0] : 0;
-            __half2 s[5], z;
-            value_steps(m, down, s, z);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const uint2 word = some ? code[2 * h + p] : make_uint2(0, 0);
-              uint32_t x[8];
-              unpack_values(word.x, s, z, x);
-              *reinterpret_cast<uint4*>(to + (((4 * p) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-              *reinterpret_cast<uint4*>(to + (((4 * p + 1) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-              unpack_values(word.y, s, z, x);
-              *reinterpret_cast<uint4*>(to + (((4 * p + 2) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-              *reinterpret_cast<uint4*>(to + (((4 * p + 3) ^ (r & 7)) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
-            }
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.kv_full[st]);
-          mbar_arrive(&sm.raw_empty[at]);
-        }
-      }
-    }
-    if (!ok && lane == 0) gave_up();
+    unpack(threadIdx.x & (SC_KEYS - 1), FEW ? 1 : 0, 2);
   } else {
-    // ---- softmax of chain a, one thread per row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SC_SOFTMAX_REGS));
-    const int a = warp >> 2, r = threadIdx.x & 127;
-    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = lane_off + 128 * a, to = lane_off + 256 + 128 * a;
-    auto meet_chain = [&](bool mine) {   // a barrier of the chain's four warps: whether all say yes
-      int all;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, 128, p;\n selp.b32 %0, 1, 0, q;\n}"
-          : "=r"(all)
-          : "r"(static_cast<int>(mine)), "r"(a + 1)
-          : "memory");
-      return all != 0;
-    };
-    bool ok = true;
-    int tile = 0, outs = 0, step0 = 0;   // key tiles and segments of this chain so far; steps of the CTA
-    Walk w = Walk::begin(A);
-    for (; ok && w.next(A); w.done(A)) {
-      const Segment& s = w.s;
-      const int n = s.j1 - s.j0, from = PAIR ? 0 : (a ^ step0) & 1;   // the chain's first tile
-      int step = step0 + from;
-      step0 += n + LAG;
-      if (PAIR && a >= row_tiles(s)) continue;
-      const int m = A.m[s.req], tok0 = (s.block * (PAIR ? 2 : 1) + (PAIR ? a : 0)) * per_tile, tok = tok0 + (r >> A.lg);
-      const int row = A.row[s.req] + min(tok, m - 1);
-      // (above 0, so that a masked key's -inf stays that; logits of below 2^30 times 2^-100 are 0 for exp2)
-      const float scale2 = fmaxf(A.scale2 * __ldcg(A.q_scale + (size_t)row * A.Hq + s.head * A.G + (r & (A.G - 1))), 0x1p-100f);
-      // warps of the tile that have rows; the first arrives for those without, which only meet the others behind the
-      // segment: whatever their rows of P are, a row of O has the same row of P alone
-      const int busy = min(4, (((m - tok0) << A.lg) + 31) / 32);
-      const uint32_t arrivals = (warp & 3) == 0 ? 5 - busy : 1;
-      const bool idle = (warp & 3) >= busy;
-      int left = A.hist[s.req] - (s.j0 + from) * SC_KEYS;   // keys from the tile on
-      float mx = NEG_INF, l = 0.0f;
-      bool any = false;
-      const int tiles = n > from ? (n - from + LAG - 1) / LAG : 0;   // of the chain
-      if (idle) tile += tiles;
-      for (int i = idle ? n : from; i < n; i += LAG, step += LAG, ++tile, left -= LAG * SC_KEYS) {
-        ok = mbar_wait_warp(&sm.s_full[a], tile & 1, ok);
-        if (!ok) break;
-        tc_fence_after();
-        // (written before the keys were unpacked, so before S)
-        const float2 size = *reinterpret_cast<const float2*>(&sm.size[step % SIZES]);
-        const float scale = scale2 * size.y;
-        uint32_t xr[128];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, xr + 32 * h);
-        tc_wait_ld();
-        float* x = reinterpret_cast<float*>(xr);
-        if (left < SC_KEYS) {   // keys behind the end
-#pragma unroll
-          for (int j = 0; j < SC_KEYS; ++j)
-            if (j >= left) x[j] = NEG_INF;
-        }
-        float t[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) t[k] = x[k];
-#pragma unroll
-        for (int j = 4; j < 124; j += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[j + 2 * k], x[j + 2 * k + 1]);
-        const float top = fmaf(fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])), scale, size.x);
-        const bool raise = top > mx + SC_LAZY || (mx == NEG_INF && top > NEG_INF);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
-          l *= f;
-          if (raise) mx = top;
-          if (any) {   // the product before S is done: S was issued after it
-#pragma unroll 1
-            for (int col = 0; col < 128; col += 16) {   // in small pieces: the logits are live
-              uint32_t o[16];
-              tmem_ld16(to + col, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(to + col, o);
-            }
-          }
-        }
-        any = true;
-        const float ref = size.x + (mx == NEG_INF ? 0.0f : SC_SHIFT - mx);
-        const float2 scale_2 = make_float2(scale, scale), ref_2 = make_float2(ref, ref);
-        float2 sum[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {   // 32 keys
-          float2 y[16];
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = fma2(make_float2(x[32 * h + 2 * j], x[32 * h + 2 * j + 1]), scale_2, ref_2);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            y[j].x = ex2f(y[j].x);
-            y[j].y = ex2f(y[j].y);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            pk[j] = f16x2(y[j].x, y[j].y);
-            sum[j & 3] = add2(sum[j & 3], y[j]);
-          }
-          tmem_st16(ts + 64 * (h >> 1) + 16 * (h & 1), pk);   // P lies over S, 64 keys in 32 columns
-          if (h & 1) {
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[a][h >> 1], arrivals);
-          }
-        }
-        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l = fmaf(sum[0].x + sum[0].y, sm.size[step % SIZES].z, l);
-      }
-      // the rows' sums, maximum and sum to the workspace
-      if (tiles > 0) {
-        if (!idle) ok = mbar_wait_warp(&sm.o_full[a], outs & 1, ok);
-        ok = meet_chain(ok);
-        if (!ok) break;
-        tc_fence_after();
-        ++outs;
-      }
-      if (!idle) {
-        float* part = A.records + ((size_t)(s.index + blockIdx.x) * 2 + a) * SC_ROWS * PARTIAL_FLOATS;
-        part[r * PARTIAL_FLOATS + PARTIAL_M] = mx - SC_SHIFT;
-        part[r * PARTIAL_FLOATS + PARTIAL_L] = l;
-        uint8_t* stage = sm.out[warp];
-#pragma unroll 1
-        for (int col = 0; col < 128; col += 32) {
-          uint32_t o[32];
-          if (tiles > 0) {
-            tmem_ld32(to + col, o);
-            tc_wait_ld();
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0;
-          }
-          // turned through shared memory, so that two lanes store 32 bytes of a row together
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ (lane >> 2 & 1)) << 4)) =
-                  make_uint4(o[8 * j + 4 * k], o[8 * j + 4 * k + 1], o[8 * j + 4 * k + 2], o[8 * j + 4 * k + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int rw = 16 * k + lane / 2, rr = 32 * (warp & 3) + rw;
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + rw * 32 + (((lane & 1) ^ (rw >> 2 & 1)) << 4));
-              if (tok0 + (rr >> A.lg) < m)
-                *reinterpret_cast<uint4*>(part + rr * PARTIAL_FLOATS + col + 8 * j + 4 * (lane & 1)) = v;
-            }
-            __syncwarp();
-          }
-        }
-      }
-      if (tiles > 0) {   // O is read: the next segment may write it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_empty[a]);
-      }
+    if (FEW && (warp & 2)) {
+      unpack(64 * (warp >> 2) + 32 * (warp & 1) + lane, 0, 1);
+    } else {
+      softmax();
     }
-    if (!ok && lane == 0) gave_up();
   }
   __syncwarp();
   grid_dep_wait();
@@ -1038,13 +1051,13 @@ cudaError_t set_up(K kernel, int bytes, std::atomic<unsigned>& done, int regs = 
   return e;
 }
 
-template <int GK, bool PAIR>
+template <int GK, bool PAIR, bool FEW>
 cudaError_t scan(const DevCache& c, const ScanArgs& a, const CUtensorMap& q_map, cudaStream_t s) {
   constexpr int bytes = static_cast<int>(sizeof(ScanSmem<GK, PAIR>)) + 1024;
   static std::atomic<unsigned> done;
-  const cudaError_t e = set_up(chunk_scan_kernel<GK, PAIR>, bytes, done, SC_REGS);
+  const cudaError_t e = set_up(chunk_scan_kernel<GK, PAIR, FEW>, bytes, done, SC_REGS);
   if (e != cudaSuccess) return e;
-  return launch_dependent(chunk_scan_kernel<GK, PAIR>, static_cast<unsigned>(a.ctas), SC_THREADS, bytes, s, c, a, q_map);
+  return launch_dependent(chunk_scan_kernel<GK, PAIR, FEW>, static_cast<unsigned>(a.ctas), SC_THREADS, bytes, s, c, a, q_map);
 }
 // CTAs of a kv head, of work for so many warps: two per SM in all.
 int ctas_per_head(int64_t units, int hkv, int sms) {
@@ -1088,8 +1101,13 @@ cudaError_t launch_rotate_queries(const DevCache& c, const RotateArgs& a, int sm
   return launch_dependent(rotate_queries_kernel, static_cast<unsigned>(per_head * c.Hkv), MG_THREADS, bytes, s, c, a, per_head);
 }
 cudaError_t launch_chunk_scan(const DevCache& c, const ScanArgs& a, bool pair, const CUtensorMap& q_map, cudaStream_t s) {
-  if (c.gk == 64) return pair ? scan<64, true>(c, a, q_map, s) : scan<64, false>(c, a, q_map, s);
-  return pair ? scan<128, true>(c, a, q_map, s) : scan<128, false>(c, a, q_map, s);
+  int rows = 0;
+  for (int i = 0; i < a.n; ++i) rows = a.m[i] << a.lg > rows ? a.m[i] << a.lg : rows;
+  auto go = [&](auto gk) {
+    constexpr int GK = decltype(gk)::value;
+    return pair ? scan<GK, true, false>(c, a, q_map, s) : rows > SC_FEW ? scan<GK, false, false>(c, a, q_map, s) : scan<GK, false, true>(c, a, q_map, s);
+  };
+  return c.gk == 64 ? go(std::integral_constant<int, 64>()) : go(std::integral_constant<int, 128>());
 }
 cudaError_t launch_chunk_merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, bool pair, int sms, cudaStream_t s) {
   return pair ? merge<true>(c, a, b, sms, s) : merge<false>(c, a, b, sms, s);
