@@ -468,7 +468,8 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       }
       if (!ok && lane == 0) gave_up();
     } else if (warp == SC_FETCH_WARP) {
-      // ---- queries, and packed keys and values: a lane a piece of a page, whose id it looks up a step ahead
+      // ---- queries, and packed keys and values: a lane a piece of a page; page ids are looked up 32 at a time, 16
+      // steps ahead (a look-up a step, one step ahead: 200K tokens 104 us, 96 this way)
       static_assert(v_meta_off_for(GK) == k_meta_off_for(GK) + Raw<GK>::META / 2, "{s, z} of K and V side by side");
       const uint8_t* const pool = c.int2 + A.layer * c.int2_layer_stride;
       const size_t page_bytes = (size_t)c.Hkv * c.record;
@@ -487,11 +488,12 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
         const int q_at = loads > 0;   // the queries come behind what can be fetched while the last segment's are in use
         const int32_t* table = c.hist_pt + (size_t)A.slot[w.s.req] * c.max_pages + 2 * w.s.j0;
         auto has = [&](int i) { return lane < 8 && i >= lag && i - lag < n && 2 * (i - lag) + u < pages; };
-        auto look = [&](int i) { return has(i) ? __ldcg(table + 2 * (i - lag) + u) : 0; };
-        int next = look(0);
+        auto look = [&](int first) { return first + lane < pages && first + lane < 2 * n ? __ldcg(table + first + lane) : 0; };
+        int before = 0, ids = 0, next = look(0);   // of pages from 32 (i / 16 - 1), 32 (i / 16) and 32 (i / 16 + 1) on
         for (int i = 0; i < n + LAG; ++i, ++step) {
-          int page = next;
-          next = look(i + 1);
+          if (i % 16 == 0) before = ids, ids = next, next = look(2 * i + 32);
+          const int mine = 2 * (i - lag) + u, new_id = __shfl_sync(0xffffffffu, ids, mine), old_id = __shfl_sync(0xffffffffu, before, mine);
+          int page = mine >> 5 == i >> 4 ? new_id : old_id;
           const int at = step % SLOTS;
           if (step >= SLOTS) ok = mbar_wait_lane(&sm.raw_empty[at], (step / SLOTS - 1) & 1, ok);
           if (!ok) break;
