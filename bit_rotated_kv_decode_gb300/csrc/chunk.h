@@ -97,9 +97,9 @@ struct MergeArgs {
 cudaError_t launch_chunk_merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, bool pair, int sms, cudaStream_t s);
 
 // The BF16 tokens of the cache and the new ones (tensor maps as launch_packed_prefill's and
-// launch_paged_prefill's): whole results where out is, else partial rows.
+// launch_paged_prefill's): whole results, or partial rows, of least key tiles or more each.
 cudaError_t launch_near_attention(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, bool partial,
                                   const CUtensorMap& q_map, const CUtensorMap& pool_map, const CUtensorMap& k_map,
-                                  const CUtensorMap& v_map, void* partials, NearPlan* plan, int sms, cudaStream_t s);
+                                  const CUtensorMap& v_map, void* partials, int least, NearPlan* plan, int sms, cudaStream_t s);
 
 }  // namespace oscar

@@ -819,23 +819,23 @@ __global__ void __launch_bounds__(MG_THREADS)
     if (B.chunk[mid] <= chunk) ri = mid; else hi = mid;
   }
   const int row0 = (chunk - B.chunk[ri]) * FEW, rows = A.m[ri] << A.lg;   // rows of the request and kv head
+  const int r = warp >> 1, share = warp & 1, rr = row0 + r;
+  constexpr int BLOCK = PAIR ? 2 * SC_ROWS : SC_ROWS;
+  const int64_t each = A.tiles[ri] + A.setup, k = (int64_t)head * A.blocks[ri] + rr / BLOCK, start = A.cost[ri] + k * each;
+  const int64_t c0 = chunk_of(A, start + A.setup), c1 = chunk_of(A, start + each - 1);
+  // record j of the row: of the scan's CTAs in turn, both chains of each unless they have rows of their own
+  const float* scan = A.records + ((size_t)(A.segment[ri] + k + c0) * 2 + (PAIR ? rr % BLOCK / SC_ROWS : 0)) * SC_ROWS * PARTIAL_FLOATS +
+                      (size_t)(rr % SC_ROWS) * PARTIAL_FLOATS;
+  const int count = static_cast<int>(c1 - c0 + 1) * (PAIR ? 1 : 2);
+  constexpr size_t STEP = (size_t)(PAIR ? 2 : 1) * SC_ROWS * PARTIAL_FLOATS;
+  const int back = B.near_blocks - 1 - (B.near_start[ri] + rr / (2 * SC_ROWS));
+  const float* bf = B.near + (((size_t)back * B.near_splits * c.Hkv + head) * (2 * SC_ROWS) + rr % (2 * SC_ROWS)) * PARTIAL_FLOATS;
+  const size_t near_step = (size_t)c.Hkv * (2 * SC_ROWS) * PARTIAL_FLOATS;
   grid_dep_launch();
   grid_dep_wait();
-  const int r = warp >> 1, share = warp & 1, rr = row0 + r;
   float4 x = make_float4(0, 0, 0, 0), y = x;
   float l = 0.0f;
   if (rr < rows) {
-    constexpr int BLOCK = PAIR ? 2 * SC_ROWS : SC_ROWS;
-    const int64_t each = A.tiles[ri] + A.setup, k = (int64_t)head * A.blocks[ri] + rr / BLOCK, start = A.cost[ri] + k * each;
-    const int64_t c0 = chunk_of(A, start + A.setup), c1 = chunk_of(A, start + each - 1);
-    // record j of the row: of the scan's CTAs in turn, both chains of each unless they have rows of their own
-    const float* scan = A.records + ((size_t)(A.segment[ri] + k + c0) * 2 + (PAIR ? rr % BLOCK / SC_ROWS : 0)) * SC_ROWS * PARTIAL_FLOATS +
-                        (size_t)(rr % SC_ROWS) * PARTIAL_FLOATS;
-    const int count = static_cast<int>(c1 - c0 + 1) * (PAIR ? 1 : 2);
-    constexpr size_t STEP = (size_t)(PAIR ? 2 : 1) * SC_ROWS * PARTIAL_FLOATS;
-    const int back = B.near_blocks - 1 - (B.near_start[ri] + rr / (2 * SC_ROWS));
-    const float* bf = B.near + (((size_t)back * B.near_splits * c.Hkv + head) * (2 * SC_ROWS) + rr % (2 * SC_ROWS)) * PARTIAL_FLOATS;
-    const size_t near_step = (size_t)c.Hkv * (2 * SC_ROWS) * PARTIAL_FLOATS;
     float top = NEG_INF;
     for (int j = lane; j < count; j += 32) top = fmaxf(top, scan[j * STEP + PARTIAL_M]);
     for (int j = lane; j < B.near_splits; j += 32) top = fmaxf(top, bf[j * near_step + PARTIAL_M]);
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(MG_THREADS)
       to.z = fmaf(v.z, w, to.z);
       to.w = fmaf(v.w, w, to.w);
     };
-#pragma unroll 8
+#pragma unroll 4
     for (int j = share; j < count; j += 2) add(scan + j * STEP, x);
     for (int j = share; j < B.near_splits; j += 2) add(bf + j * near_step, y);
   }

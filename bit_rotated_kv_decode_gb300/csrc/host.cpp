@@ -910,8 +910,8 @@ ChunkSpace chunk_space(const oscar_cache* c, int32_t n, const int32_t* new_lens)
     longest = std::max(longest, m);
   }
   const size_t record = (size_t)256 * PARTIAL_FLOATS * sizeof(float);
-  // a group's near rows are split so that they fill the SMs at most, in parts of four key tiles or more
-  const int64_t items = blocks * H, parts = std::max<int64_t>(1, ((SINK + RECENT + PAGE + longest) / 128 + 1) / 4);
+  // a group's near rows are split so that they fill the SMs at most, in parts of a key tile or more
+  const int64_t items = blocks * H, parts = (SINK + RECENT + PAGE + longest) / 128 + 1;
   const size_t near = (size_t)std::min(items * parts, std::max(items, sms)) * record;
   ChunkSpace s;
   s.scale = align256((size_t)rows * c->cfg.num_q_heads * D * 2);
@@ -937,10 +937,6 @@ cudaError_t chunk_group(oscar_cache* c, const AttnReq* reqs, int n, bool history
                         const CUtensorMap* maps, const ChunkSpace& space, char* ws, ScanArgs& sa, cudaStream_t s) {
   const DevCache& d = c->dc;
   const PagedView p{nullptr, d.bf16_pt, d.n_bf16_pages, BF16_PAGES_PER_REQ, n, d.Hkv, d.err};
-  NearPlan plan;
-  cudaError_t e = launch_near_attention(p, reqs, n, a, history, maps[0], maps[1], maps[2], maps[3], ws + space.near, &plan,
-                                        c->num_sms, s);
-  if (e != cudaSuccess || !history) return e;
   int64_t cost = 0, segments = 0;
   sa.n = n;
   sa.setup = CHUNK_SETUP;
@@ -956,6 +952,14 @@ cudaError_t chunk_group(oscar_cache* c, const AttnReq* reqs, int n, bool history
     segments += (int64_t)d.Hkv * sa.blocks[i];
     cost += (int64_t)d.Hkv * sa.blocks[i] * (sa.tiles[i] + sa.setup);
   }
+  // The near rows' kernel takes 14 us for a request's 320 tokens, 9 with a CTA a key tile.  Those CTAs are the scan's
+  // too, so that it is split where the scan is short and rows, so what there is to merge, are few (5 tokens over 400
+  // cached 18.6 us, 23.7 otherwise; over 20K 33.3, 37.4; over 100K 63.8 otherwise, 70.1; 150 tokens over 2K 48 otherwise, 76).
+  constexpr int64_t SPLIT = 16;
+  NearPlan plan;
+  cudaError_t e = launch_near_attention(p, reqs, n, a, history, maps[0], maps[1], maps[2], maps[3], ws + space.near,
+                                        history && !pair && cost <= SPLIT * c->num_sms ? 1 : 4, &plan, c->num_sms, s);
+  if (e != cudaSuccess || !history) return e;
   sa.total = cost;
   // the near rows' CTAs run beside the scan's, one per SM: where they are few, the scan leaves them theirs
   const int64_t sms = plan.ctas <= c->num_sms / 4 ? c->num_sms - plan.ctas : c->num_sms;

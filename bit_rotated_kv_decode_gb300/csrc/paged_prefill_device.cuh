@@ -745,7 +745,7 @@ cudaError_t launch_tiles(const PrefillArgs& A, const PrefillMaps& maps, int sms,
 
 // What every source has: the requests' blocks of rows, the parts of their key tiles.
 cudaError_t plan(PrefillArgs& A, const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, void* partials,
-                 int sms, Source source) {
+                 int sms, Source source, int least = 4) {   // least: key tiles of a part of an item's keys
   A.p = p;
   A.a = a;
   A.n = n;
@@ -770,8 +770,8 @@ cudaError_t plan(PrefillArgs& A, const PagedView& p, const AttnReq* reqs, int n,
   }
   A.bstart[n] = static_cast<int32_t>(blocks);
   const int most = paged_prefill_splits(blocks, p.Hkv, sms);
-  // a part has four key tiles or more
-  A.splits = static_cast<int>(longest / 4 < most ? (longest / 4 > 1 ? longest / 4 : 1) : most);
+  const int64_t parts = longest / least > 1 ? longest / least : 1;
+  A.splits = static_cast<int>(parts < most ? parts : most);
   A.partials = static_cast<float*>(partials);
   if (blocks * p.Hkv * A.splits > INT32_MAX / 2) return cudaErrorInvalidValue;
   A.items = static_cast<int>(blocks * p.Hkv * A.splits);

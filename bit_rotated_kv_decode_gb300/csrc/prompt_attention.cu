@@ -29,9 +29,9 @@ cudaError_t launch_packed_prefill(const AttnReq* reqs, int n, int hkv, const Att
 
 cudaError_t launch_near_attention(const PagedView& p, const AttnReq* reqs, int n, const AttnArgs& a, bool partial,
                                   const CUtensorMap& q_map, const CUtensorMap& pool_map, const CUtensorMap& k_map,
-                                  const CUtensorMap& v_map, void* partials, NearPlan* out, int sms, cudaStream_t s) {
+                                  const CUtensorMap& v_map, void* partials, int least, NearPlan* out, int sms, cudaStream_t s) {
   PrefillArgs A;
-  const cudaError_t e = plan(A, p, reqs, n, a, partials, sms, CACHE);
+  const cudaError_t e = plan(A, p, reqs, n, a, partials, sms, CACHE, least);
   if (e != cudaSuccess) return e;
   const PrefillMaps maps{q_map, pool_map, k_map, v_map};
   if (!partial && A.splits == 1) return launch_tiles<false, false, CACHE>(A, maps, sms, s);
