@@ -111,9 +111,10 @@ __device__ __forceinline__ bool grid_of(const Range& r, float e, Grid& g) {
   return sure && (r.mx_lo - z) * rs > 2.5f + g.margin && (r.mn_hi - z) * rs < 0.5f - g.margin && g.margin < 0.25f;
 }
 
-// The compensated product of warp_dot2 by eight lanes, 16 terms each: bounds lo <= exact <= hi.  The error terms
-// are at most 19 u S in all (a product's u, a sum's u of what it has so far) and their own sum, 21 additions deep,
-// is off by 21 u of that: 2^-39.4 S, within the 2^-36 S taken.
+// The compensated product of warp_dot2 by eight lanes, 16 terms each: bounds lo <= fp32_rn(exact) <= hi.  The error
+// terms are at most 19 u S in all (a product's u, a sum's u of what it has so far) and their own sum, 21 additions
+// deep, is off by 21 u of that: 2^-39.4 S, within the 2^-36 S taken.  Each bound is rounded once, and to nearest as
+// the exact sum is, so that the two are nearly always the same value.
 __device__ __forceinline__ void dot2_of_eight(const uint4* k, const float4* r, float S, float& lo, float& hi) {
   uint4 kw[2];
   float4 rv[4];
@@ -144,8 +145,8 @@ __device__ __forceinline__ void dot2_of_eight(const uint4* k, const float4* r, f
     c = __fadd_rn(c, __fadd_rn(c2, e));
   }
   const float E = __fmul_ru(S, 0x1p-36f);
-  lo = __fsub_rd(__fadd_rd(s, c), E);
-  hi = __fadd_ru(__fadd_ru(s, c), E);
+  lo = __fadd_rn(s, __fsub_rd(c, E));
+  hi = __fadd_rn(s, __fadd_ru(c, E));
 }
 
 constexpr float MAGIC = 12582912.0f;   // 1.5 2^23: adding it rounds to the nearest whole number
