@@ -290,8 +290,9 @@ oscar_status oscar_extend(oscar_cache* cache, int32_t layer, int32_t n, const in
  * request reqs[i] (which may repeat), in their own basis: BF16 tokens as they are, history
  * tokens (z + s c) R^T.
  *   k_out, v_out  device [rows][Hkv][128] of out_type (oscar_type), 16-byte aligned.
- * fp32 values are within 2^-20 of the token's largest term sum; bf16 ones are rounded once,
- * from values whose R is rounded to 11 bits. */
+ * History in fp32: R in 24 bits, sums in fp32 on the matrix unit (off by 2^-14 of their terms'
+ * magnitudes at most, by 1e-7 of the values as measured).  In bf16: z + s c and R are rounded to
+ * 11 bits (values below 2^-5 of the token's largest to 2^-16 of it), and the result once. */
 oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* starts,
                         const int32_t* counts, void* k_out, void* v_out, int32_t out_type, void* stream);
 
@@ -307,10 +308,11 @@ oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int3
  *   workspace  device, >= oscar_chunk_workspace_bytes() (for these new_lens, whatever the
  *              requests hold), 256-byte aligned; no contents are needed.  Calls that share
  *              a workspace must not overlap on the GPU.
- * New tokens that a query does not see must hold finite values.  Sums and softmax statistics are
- * fp32; in the history, q R_K, the values z + s c and the weights are rounded to 11 bits, elsewhere
- * weights to 8.  Page ids out of range and waits that gave up are reported by
- * oscar_cache_check. */
+ * New tokens of a request that some of its queries see and others do not must hold finite values.
+ * Sums and softmax statistics are fp32; in the history, q R_K, the values z + s c (those below 2^-5
+ * of the largest of their 128 tokens to 2^-16 of it), the weights, and for many rows the weighted sums
+ * and R_V are rounded to 11 bits; elsewhere weights to 8.  Page ids out of range and waits that gave
+ * up are reported by oscar_cache_check. */
 oscar_status oscar_chunk_workspace_bytes(const oscar_cache* cache, int32_t n, const int32_t* new_lens, size_t* bytes);
 oscar_status oscar_chunk_attention(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs,
                                    const int32_t* new_lens, const uint16_t* q, int64_t q_stride, const uint16_t* k,
