@@ -303,11 +303,17 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 
     const uint32_t acc = (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * group;
     const float e = __fmul_ru(S, EX_MMA_ERR);
-    // The values that lanes have open, bit i of a lane's mask channel ch0 + i of its token, each to within
-    // 2^-36 S and clipped: done(i, lo, hi) in its lane.  Four at a time, eight lanes each (one by one, every
+    // The values that lanes have open, bit i of a lane's mask[h] channel ch0 + 32 h + i of its token, each to within
+    // 2^-36 S and clipped: done(32 h + i, lo, hi) in its lane.  Four at a time, eight lanes each (one by one, every
     // value waited for a row of R and of k of its own).
-    auto narrow = [&](uint32_t mask, int ch0, auto done) {
-      for (uint32_t open = __ballot_sync(0xffffffffu, mask != 0); open; open = __ballot_sync(0xffffffffu, mask != 0)) {
+    auto narrow = [&](uint32_t (&mask)[4], int ch0, auto done) {
+#pragma unroll 1
+      for (;;) {
+        const int word = mask[0] ? 0 : mask[1] ? 1 : mask[2] ? 2 : 3;
+        const uint32_t bits = mask[0] ? mask[0] : mask[1] ? mask[1] : mask[2] ? mask[2] : mask[3];
+        const uint32_t open = __ballot_sync(0xffffffffu, bits != 0);
+        if (!open) break;
+        const int first = 32 * word + __ffs(bits) - 1;   // (of no use where none is open)
         uint32_t rest = open;
         int from = __ffs(open) - 1;   // the lane of these eight lanes' value
 #pragma unroll
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           if (lane >> 3 == j && rest) from = __ffs(rest) - 1;
           rest &= rest - 1;
         }
-        const int i = __ffs(__shfl_sync(0xffffffffu, mask, from)) - 1;
+        const int i = __shfl_sync(0xffffffffu, first, from);
         const auto* row = reinterpret_cast<const uint16_t*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
         const float bound_of = __shfl_sync(0xffffffffu, S, from);
@@ -325,9 +331,11 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         const int rank = __popc(open & ((1u << lane) - 1));
         lo = __shfl_sync(0xffffffffu, lo, 8 * (rank & 3));
         hi = __shfl_sync(0xffffffffu, hi, 8 * (rank & 3));
-        if (mask != 0 && rank < 4) {
-          done(__ffs(mask) - 1, clip_canon(lo, tau), clip_canon(hi, tau));
-          mask &= mask - 1;
+        if (bits != 0 && rank < 4) {
+          done(first, clip_canon(lo, tau), clip_canon(hi, tau));
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (h == word) mask[h] &= mask[h] - 1;
         }
       }
     };
@@ -358,6 +366,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         const bool low = range.mn_lo != range.mn_hi, high = range.mx_lo != range.mx_hi;
         const float below = low && !known ? __fadd_ru(mn, 2.0f * e) : -INFINITY, above = high && !known ? __fsub_rd(mx, 2.0f * e) : INFINITY;
         float lo0 = INFINITY, lo1 = INFINITY, hi0 = -INFINITY, hi1 = -INFINITY;
+        uint32_t open[4] = {0, 0, 0, 0};
 #pragma unroll 1
         for (int h = 0; h < GK / 32; ++h) {
           uint32_t w[32], mask = 0;
@@ -366,11 +375,14 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             mask |= __uint_as_float(w[i]) <= below || __uint_as_float(w[i]) >= above ? 1u << i : 0u;
-          narrow(mask, n * GK + 32 * h, [&](int, float lo, float hi) {
-            lo0 = fminf(lo0, lo), lo1 = fminf(lo1, hi);
-            hi0 = fmaxf(hi0, lo), hi1 = fmaxf(hi1, hi);
-          });
+#pragma unroll
+          for (int j = 0; j < GK / 32; ++j)
+            if (j == h) open[j] = mask;
         }
+        narrow(open, n * GK, [&](int, float lo, float hi) {
+          lo0 = fminf(lo0, lo), lo1 = fminf(lo1, hi);
+          hi0 = fmaxf(hi0, lo), hi1 = fmaxf(hi1, hi);
+        });
         if (!known) {
           if (low) range.mn_lo = lo0, range.mn_hi = lo1;
           if (high) range.mx_lo = hi0, range.mx_hi = hi1;
@@ -416,6 +428,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     }
     if (!to || !sure) close = 0;
     if (__any_sync(0xffffffffu, close != 0)) {
+      uint32_t open[4] = {0, 0, 0, 0};
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {
         if (!__any_sync(0xffffffffu, close >> h & 1)) continue;
@@ -430,16 +443,20 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           mask |= fabsf(fmaf(y, 3.0f, -whole)) < 0.5f - q.margin ? 0u : 1u << i;
         }
         if (!(close >> h & 1)) mask = 0;
-        narrow(mask, 32 * h, [&](int i, float lo, float hi) {
-          const float z = __half2float(__ushort_as_half(q.z_bits)), s = __half2float(__ushort_as_half(q.s_bits));
-          const uint32_t c0 = code_of(lo, z, s), at = 2 * (i & 15);
-          if (c0 != code_of(hi, z, s)) sure = false;
-          const int word = 2 * h + (i >> 4);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j == word) code[j] = (code[j] & ~(3u << at)) | c0 << at;
-        });
+        for (int j = 0; j < 4; ++j)
+          if (j == h) open[j] = mask;
       }
+      narrow(open, 0, [&](int i, float lo, float hi) {
+        const Grid& q = NG == 2 && i >= GK ? g[NG - 1] : g[0];
+        const float z = __half2float(__ushort_as_half(q.z_bits)), s = __half2float(__ushort_as_half(q.s_bits));
+        const uint32_t c0 = code_of(lo, z, s), at = 2 * (i & 15);
+        if (c0 != code_of(hi, z, s)) sure = false;
+        const int word = i >> 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j == word) code[j] = (code[j] & ~(3u << at)) | c0 << at;
+      });
     }
     tc_fence_before();
     if (to && sure) {
