@@ -732,10 +732,11 @@ __global__ void __launch_bounds__(MG_THREADS, 2)
 // row of it), where staging it in shared memory would take longer than the rest.
 constexpr int FEW = 4;
 // y[r][n] = sum_k x[r][k] m[n][k], thread (n, half) having m's row n from 64 half on in f; the same sum in both.
-__device__ __forceinline__ void times_rotation(const float4 (&f)[16], const float (*x)[D], float (&y)[FEW]) {
+template <int ROWS>
+__device__ __forceinline__ void times_rotation(const float4 (&f)[16], const float (*x)[D], float (&y)[ROWS]) {
   const int half = threadIdx.x & 1;
 #pragma unroll
-  for (int r = 0; r < FEW; ++r) {
+  for (int r = 0; r < ROWS; ++r) {
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -801,14 +802,15 @@ __global__ void __launch_bounds__(MG_THREADS)
   }
 }
 
-// Four rows of one request and kv head, two warps a row: partial rows of the scan's CTAs and of the BF16
-// tokens, each weighed with its maximum.
-template <bool PAIR>
+// Rows of one request and kv head, the CTA's eight warps shared among them: partial rows of the scan's CTAs and of the
+// BF16 tokens, each weighed with its maximum.
+template <bool PAIR, int ROWS>
 __global__ void __launch_bounds__(MG_THREADS)
     chunk_merge_few_kernel(const __grid_constant__ DevCache c, const __grid_constant__ ScanArgs A,
                            const __grid_constant__ MergeArgs B) {
-  __shared__ alignas(16) float far[FEW][D], near[FEW][D], part[FEW][2][D];
-  __shared__ float part_l[FEW];
+  constexpr int SHARES = 8 / ROWS;   // warps of a row
+  __shared__ alignas(16) float far[ROWS][D], near[ROWS][D], part[ROWS][SHARES - 1][2][D];
+  __shared__ float part_l[ROWS][SHARES - 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = threadIdx.x >> 1;
   const int head = blockIdx.x % c.Hkv, chunk = blockIdx.x / c.Hkv, G = 1 << A.lg;
   float4 f[16];
@@ -818,8 +820,8 @@ __global__ void __launch_bounds__(MG_THREADS)
     const int mid = (ri + hi) >> 1;
     if (B.chunk[mid] <= chunk) ri = mid; else hi = mid;
   }
-  const int row0 = (chunk - B.chunk[ri]) * FEW, rows = A.m[ri] << A.lg;   // rows of the request and kv head
-  const int r = warp >> 1, share = warp & 1, rr = row0 + r;
+  const int row0 = (chunk - B.chunk[ri]) * ROWS, rows = A.m[ri] << A.lg;   // rows of the request and kv head
+  const int r = warp / SHARES, share = warp % SHARES, rr = row0 + r;
   constexpr int BLOCK = PAIR ? 2 * SC_ROWS : SC_ROWS;
   const int64_t each = A.tiles[ri] + A.setup, k = (int64_t)head * A.blocks[ri] + rr / BLOCK, start = A.cost[ri] + k * each;
   const int64_t c0 = chunk_of(A, start + A.setup), c1 = chunk_of(A, start + each - 1);
@@ -853,33 +855,37 @@ __global__ void __launch_bounds__(MG_THREADS)
       to.w = fmaf(v.w, w, to.w);
     };
 #pragma unroll 4
-    for (int j = share; j < count; j += 2) add(scan + j * STEP, x);
-    for (int j = share; j < B.near_splits; j += 2) add(bf + j * near_step, y);
+    for (int j = share; j < count; j += SHARES) add(scan + j * STEP, x);
+    for (int j = share; j < B.near_splits; j += SHARES) add(bf + j * near_step, y);
   }
   if (share) {
-    reinterpret_cast<float4*>(part[r][0])[lane] = x;
-    reinterpret_cast<float4*>(part[r][1])[lane] = y;
-    if (lane == 0) part_l[r] = l;
+    reinterpret_cast<float4*>(part[r][share - 1][0])[lane] = x;
+    reinterpret_cast<float4*>(part[r][share - 1][1])[lane] = y;
+    if (lane == 0) part_l[r][share - 1] = l;
   }
   __syncthreads();
   if (!share) {
-    const float4 u = reinterpret_cast<const float4*>(part[r][0])[lane], v = reinterpret_cast<const float4*>(part[r][1])[lane];
-    l += part_l[r];
+#pragma unroll
+    for (int i = 0; i < SHARES - 1; ++i) {
+      const float4 u = reinterpret_cast<const float4*>(part[r][i][0])[lane], v = reinterpret_cast<const float4*>(part[r][i][1])[lane];
+      x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
+      y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+      l += part_l[r][i];
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     // positions 4 lane, ...: channels 16 (lane / 4) + 2 (lane % 4), + 8, + 1, + 9
     float* to = &far[r][16 * (lane >> 2) + 2 * (lane & 3)];
-    to[0] = (x.x + u.x) * inv;
-    to[8] = (x.y + u.y) * inv;
-    to[1] = (x.z + u.z) * inv;
-    to[9] = (x.w + u.w) * inv;
-    reinterpret_cast<float4*>(near[r])[lane] =
-        make_float4((y.x + v.x) * inv, (y.y + v.y) * inv, (y.z + v.z) * inv, (y.w + v.w) * inv);
+    to[0] = x.x * inv;
+    to[8] = x.y * inv;
+    to[1] = x.z * inv;
+    to[9] = x.w * inv;
+    reinterpret_cast<float4*>(near[r])[lane] = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
   }
   __syncthreads();
-  float out[FEW];
+  float out[ROWS];
   times_rotation(f, far, out);
 #pragma unroll
-  for (int i = 0; i < FEW; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     const float z = out[i] + near[i][n], next = __shfl_xor_sync(0xffffffffu, z, 2);
     const int row = row0 + i;
     if ((threadIdx.x & 3) == 0 && row < rows)   // outputs n and n + 1
@@ -1077,10 +1083,14 @@ template <bool PAIR>
 cudaError_t merge(const DevCache& c, const ScanArgs& a, MergeArgs& b, int sms, cudaStream_t s) {
   static std::atomic<unsigned> done;
   count_chunks(a, b, UNIT);
-  // few rows have many records: four rows a CTA spread them
+  // few rows have many records: two or four rows a CTA spread them
   if ((int64_t)b.chunks * c.Hkv < sms) {
-    count_chunks(a, b, FEW);
-    return launch_dependent(chunk_merge_few_kernel<PAIR>, static_cast<unsigned>(b.chunks * c.Hkv), MG_THREADS, 0, s, c, a, b);
+    auto few = [&](auto rows) {
+      constexpr int ROWS = decltype(rows)::value;
+      count_chunks(a, b, ROWS);
+      return launch_dependent(chunk_merge_few_kernel<PAIR, ROWS>, static_cast<unsigned>(b.chunks * c.Hkv), MG_THREADS, 0, s, c, a, b);
+    };
+    return (int64_t)b.chunks * c.Hkv * (UNIT / 2) <= sms ? few(std::integral_constant<int, 2>()) : few(std::integral_constant<int, FEW>());
   }
   constexpr int bytes = static_cast<int>(sizeof(MergeRowsSmem));
   const cudaError_t e = set_up(chunk_merge_rows_kernel<PAIR>, bytes, done);
