@@ -19,13 +19,17 @@
 // p 2^-b.
 // The two chains are two tiles of 128 query rows (a row being a (token, head of the group) pair)
 // that share every key, or, where a kv head has 128 rows or fewer, every other key tile each of
-// the one tile of queries: a chain by itself is S, softmax, PV one after another.
+// the one tile of queries: a chain by itself is S, softmax, PV one after another.  Where 64 rows or
+// fewer leave half of the softmax's warps idle, those unpack the values, the other four the keys
+// (5 tokens over 100K: 62 us, 67.5 without).
 //
-// Bytes of history are few (72 a token-head): with 20 rows the scan is bound by unpacking into
-// shared memory and reading it back, with 256 by the tensor core.  Work is a line of key tiles,
-// segment by segment -- (request, kv head, 256 rows) -- with some set-up units in front of each,
-// cut into one equal range per SM: a long request is spread over all of them, and none waits for
-// the last segment.
+// Bytes of history are few (72 a token-head).  With two tiles of rows a key tile moves 300 KB through
+// shared memory -- operands 192, unpacked values 64, packed data 45 -- or 2350 cycles, and is 2048 of the tensor
+// core's; it takes 3050 (tensor pipe 66 %).  2048 tokens over 60K, 32 heads of 8: 1258 us, 1.63 PFLOP/s.  With few
+// rows it is bound by its copies (2 KB and less) and the barriers around them: 5 tokens over 100K 59 us, of which 46
+// here, 0.39 us per 1K tokens.  Work is a line of key tiles, segment by segment -- (request, kv head, 256 rows) --
+// with some set-up units in front of each, cut into one equal range per SM: a long request is spread over all of
+// them, and none waits for the last segment.
 #include <atomic>
 #include <type_traits>
 
@@ -229,7 +233,15 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
         for (int u = u0; u < u1; ++u) {
           const float down = u ? k_down : v_down;
           const bool some = u ? now : then;
-          const uint2* code = reinterpret_cast<const uint2*>(raw.code[u ^ 1]) + 4 * r;
+          // 32 bytes of codes, four lanes of eight the second half first: no two of them meet in a bank
+          const uint4* code = reinterpret_cast<const uint4*>(raw.code[u ^ 1]) + 2 * r;
+          const int turn = r >> 2 & 1;
+          uint4 words[2] = {code[turn], code[turn ^ 1]};
+          if (turn) {
+            const uint4 swap = words[0];
+            words[0] = words[1], words[1] = swap;
+          }
+          if (!some) words[0] = words[1] = make_uint4(0, 0, 0, 0);
           const uint32_t* meta = reinterpret_cast<const uint32_t*>(u ? raw.meta[r / PAGE] : raw.v_meta) + NG * (u ? r % PAGE : r);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {   // 64 channels
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
             value_steps(m, down, s, z);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              const uint2 word = some ? code[2 * h + p] : make_uint2(0, 0);
+              const uint2 word = p ? make_uint2(words[h].z, words[h].w) : make_uint2(words[h].x, words[h].y);
               uint32_t x[8];
               unpack_values(word.x, s, z, x);
               *reinterpret_cast<uint4*>(to + (((4 * p) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
@@ -469,7 +481,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       if (!ok && lane == 0) gave_up();
     } else if (warp == SC_FETCH_WARP) {
       // ---- queries, and packed keys and values: a lane a piece of a page; page ids are looked up 32 at a time, 16
-      // steps ahead (a look-up a step, one step ahead: 200K tokens 104 us, 96 this way)
+      // steps ahead (a look-up a step, one step ahead: 200K tokens 104 us, 101 this way)
       static_assert(v_meta_off_for(GK) == k_meta_off_for(GK) + Raw<GK>::META / 2, "{s, z} of K and V side by side");
       const uint8_t* const pool = c.int2 + A.layer * c.int2_layer_stride;
       const size_t page_bytes = (size_t)c.Hkv * c.record;
@@ -660,7 +672,8 @@ struct RotateSmem {
   alignas(16) uint16_t q[8][UNIT][PITCH];
 };
 // A warp takes 16 rows -- (token, head of the group), whatever requests they are of -- of one
-// kv head at a time; the CTA keeps that head's rotation.
+// kv head at a time; the CTA keeps that head's rotation.  (1216 tokens of 32 heads: 14.5 us by itself, most of it
+// staging the rotation, which lies under the kernel before where there is one.)
 __global__ void __launch_bounds__(MG_THREADS, 2)
     rotate_queries_kernel(const __grid_constant__ DevCache c, const __grid_constant__ RotateArgs A, int per_head) {
   extern __shared__ __align__(16) uint8_t rt_raw[];
