@@ -2,7 +2,8 @@
 // that a projection wrote: the tiled kernel of paged_prefill.cu with its keys and values
 // loaded as rows (boxes of 64 tokens of one kv head) instead of pages.  And the near part of a
 // chunk's attention: the same over the three-segment cache's BF16 pages with the chunk's own
-// rows behind them.
+// rows behind them.  16K tokens of 32 heads (8 kv heads): 1138 us in runs of 20 calls, 1.93 PFLOP/s; in a loop of
+// seconds 1282 to 1312, at the power cap.
 namespace oscar {
 namespace {
 // Registers a thread: 168 at launch (three warpgroups share 504), then 208 for the
