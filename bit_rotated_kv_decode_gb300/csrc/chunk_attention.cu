@@ -56,6 +56,9 @@ constexpr int SC_FEW = 64;                     // rows of which a chain's first 
 // its exponents, comes LAG steps after them: SLOTS + 2 + LAG steps have to be kept, 9 at most.
 constexpr int SIZES = 16;
 constexpr float SC_LAZY = 4.0f;                // the softmax reference moves only when exceeded by 2^4
+// |S| is at most 128 x 2^11 x 2^-8: logits stay within 2^22, where the roundings of a product, of the maximum and of
+// the reference, 2^-2 each, leave a weight below 2^16.  (Logits beyond that have lost 2^10 to the rounding of q R_K.)
+constexpr float SC_STEEPEST = 0x1p12f;
 constexpr float SC_SHIFT = 11.0f;              // weights are at most 2^15, and fp16's steps below 2^-14 cost nothing
 
 // Packed data of a step: K codes of a tile, V codes of an earlier one and their {s, z}; {s, z} of the tile's own keys
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
         tc_fence_after();
         // (written before the keys were unpacked, so before S)
         const float2 size = *reinterpret_cast<const float2*>(&sm.size[step % SIZES]);
-        const float scale = scale2 * size.y;
+        const float scale = fminf(scale2 * size.y, SC_STEEPEST);
         uint32_t xr[128];
 #pragma unroll
         for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, xr + 32 * h);

@@ -23,6 +23,7 @@ constexpr int PF_FLUSH = 4;                    // key tiles between additions to
 constexpr int PF_ITEMS = 4;                    // items looked up ahead
 constexpr int PF_READERS = 11;                 // warps that read them
 constexpr int PF_ROWS = 128;                   // rows of a query tile
+constexpr float HUGE_LOGIT = 0x1p20f;
 constexpr int PF_KEYS = 2 * PAGE;              // keys of a tile
 
 struct PrefillArgs {
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         for (int i = 4; i < 124; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[i + 2 * k], x[i + 2 * k + 1]);
-        const float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])) * scale2;
+        const float most = fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])), top = most * scale2;
         const bool raise = top > mx + LAZY_MAX || (mx == NEG_INF && top > NEG_INF);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
@@ -531,7 +532,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tmem_st16(to - 128 + c, o);
           }
         }
-        const float ref = mx == NEG_INF ? 0.0f : -mx;
+        float ref = mx == NEG_INF ? 0.0f : -mx;
+        // Logits so large that a product's rounding shows in the weights (beyond 2^31 as an infinity): as differences to
+        // the tile's largest.  (Over pages as before: 1 % of a long prompt's time.)
+        const bool huge = S != PAGES && fabsf(top) > HUGE_LOGIT && top != NEG_INF;
+        if (S != PAGES && __any_sync(0xffffffffu, huge)) {
+          const float from = huge ? most : 0.0f;
+          if (huge) ref = __fsub_rn(top, mx);   // (the product rounded, as mx is)
+#pragma unroll
+          for (int i = 0; i < PF_KEYS; ++i) x[i] -= from;
+        }
         const float2 scale_2 = make_float2(scale2, scale2), ref_2 = make_float2(ref, ref);
         float2 sum[4];
 #pragma unroll

@@ -309,10 +309,10 @@ oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int3
  *              requests hold), 256-byte aligned; no contents are needed.  Calls that share
  *              a workspace must not overlap on the GPU.
  * New tokens of a request that some of its queries see and others do not must hold finite values.
- * Sums and softmax statistics are fp32; in the history, q R_K, the values z + s c (those below 2^-5
- * of the largest of their 128 tokens to 2^-16 of it), the weights, and for many rows the weighted sums
- * and R_V are rounded to 11 bits; elsewhere weights to 8.  Page ids out of range and waits that gave
- * up are reported by oscar_cache_check. */
+ * q · k is finite in fp32.  Sums and softmax statistics are fp32; in the history, q R_K, the values
+ * z + s c (those below 2^-5 of the largest of their 128 tokens to 2^-16 of it), the weights, and for
+ * many rows the weighted sums and R_V are rounded to 11 bits; elsewhere weights to 8.  Page ids out of
+ * range and waits that gave up are reported by oscar_cache_check. */
 oscar_status oscar_chunk_workspace_bytes(const oscar_cache* cache, int32_t n, const int32_t* new_lens, size_t* bytes);
 oscar_status oscar_chunk_attention(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs,
                                    const int32_t* new_lens, const uint16_t* q, int64_t q_stride, const uint16_t* k,
@@ -494,8 +494,8 @@ const char* oscar_paged_last_error(void);
  *              not overlap on the GPU.
  * Hq / Hkv in {1, 2, 4, 8}.  Tokens that a query does not see do not touch its result,
  * whatever other sequences hold; within a sequence, those that some queries see and others
- * do not must hold finite values.  Sums and softmax statistics are fp32; weights enter the
- * product with V to 24 bits for fp32 outputs, to 8 for bf16. */
+ * do not must hold finite values; q · k is finite in fp32.  Sums and softmax statistics are
+ * fp32; weights enter the product with V to 24 bits for fp32 outputs, to 8 for bf16. */
 size_t oscar_prompt_workspace_bytes(int32_t n, const int32_t* lens, int32_t num_q_heads, int32_t num_kv_heads);
 oscar_status oscar_prompt_attention(const int32_t* lens, int32_t n, int32_t num_q_heads, int32_t num_kv_heads,
                                     int32_t window, int32_t sinks, float scale, const uint16_t* q, int64_t q_stride,

@@ -713,3 +713,74 @@ def test_values_that_are_not_finite(b):
     kn[30:], vn[30:], q[30:] = math.nan, math.nan, math.nan
     one.cache.chunk_attention(0, r, q, kn, vn, out, new_lens=[30, 60])
     assert torch.equal(out[:30].view(torch.int16), clean[:30].view(torch.int16))
+
+
+@pytest.mark.parametrize("group", [128, 64])
+@pytest.mark.parametrize("m", [8, 9, 16, 17, 32, 33])
+def test_chunk_rows_at_the_borders_of_the_forms(b, m, group):
+    """64 and 72 rows a kv head (8 to a token), 128 and 136, 256 and 264."""
+    h = Held(b, hq=16, hkv=2, group=group, seed=24 + m, requests=2, tokens=3500)
+    r = [h.cache.open() for _ in range(2)]
+    h.cache.extend(0, r, *h.tokens(3300 + 500), new_lens=[3300, 500])
+    check_chunk(h, r, [m, m])
+    check_chunk(h, r[:1], [m])
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1), (96, 96), (160, 160)])
+def test_chunk_any_number_of_heads(b, hq, hkv):
+    h = Held(b, hq=hq, hkv=hkv, seed=hq, requests=2, tokens=800)
+    r = [h.cache.open() for _ in range(2)]
+    h.cache.extend(0, r, *h.tokens(1000), new_lens=[650, 350])
+    check_chunk(h, r, [3, 1])
+    check_chunk(h, r, [200, 2])
+    k, v = (torch.empty(1000, hkv, D, device="cuda") for _ in range(2))
+    h.cache.read(0, r, [0, 0], [650, 350], k, v)
+    want = torch.cat([h.stored(x)[0][1] for x in r])
+    assert off_by(v, want) < 1e-6
+
+
+def test_chunk_queries_of_any_size(b):
+    """Zeros (the mean of all values), tiny and huge queries beside ordinary ones, each its own scale."""
+    h = Held(b, seed=30, requests=1, tokens=1200)
+    r = h.cache.open()
+    h.cache.extend(0, [r], *h.tokens(1111), new_lens=[1111])
+    (kc, vc), _, _ = h.stored(r)
+    for m in (4, 80):
+        kn, vn = h.tokens(m)
+        q = h.rnd(m, 8, D).bfloat16()
+        q[0] = 0
+        q[1] *= 2.0 ** -60
+        q[2] = (q[2].float() * 2.0 ** -130).bfloat16()
+        q[3, ::2] *= 2.0 ** 40
+        out = torch.empty_like(q)
+        h.cache.chunk_attention(0, [r], q, kn, vn, out, new_lens=[m])
+        p = torch.arange(1111 + m, device="cuda")
+        see = p[None] <= torch.arange(1111, 1111 + m, device="cuda")[:, None]
+        want = attend(q, torch.cat([kc, kn.double()]), torch.cat([vc, vn.double()]), see)[0]
+        for i in range(m):
+            # logits of 2^40: one weight is 1, and which one it is fp32 decides where two are 2^-11 apart
+            if i != 3:
+                assert off_by(out[i], want[i]) < 2e-2, (m, i, off_by(out[i], want[i]))
+        assert bool(out.isfinite().all())
+        seen = torch.cat([vc, vn.double()]).abs().amax(0)
+        assert bool((out[3].double().abs() <= 1.01 * seen.repeat_interleave(4, 0).view(8, D)).all())
+    h.cache.check()
+
+
+@pytest.mark.parametrize("out_type", [torch.bfloat16, torch.float32])
+def test_prompt_queries_of_any_size(b, out_type):
+    """Logits far beyond fp32's whole numbers: one key has the weight, and rows beside them are what they were."""
+    rnd = rand(31)
+    q, k, v = rnd(150, 8, D).bfloat16(), rnd(150, 2, D).bfloat16(), rnd(150, 2, D).bfloat16()
+    out = torch.empty(150, 8, D, device="cuda", dtype=out_type)
+    b.prompt_attention(q, k, v, out, [150])
+    clean = out.clone()
+    huge = q.clone()
+    huge[40], huge[90] = huge[40] * 2.0 ** 40, huge[90] * 2.0 ** 90
+    b.prompt_attention(huge, k, v, out, [150])
+    rest = [i for i in range(150) if i not in (40, 90)]
+    assert torch.equal(out[rest], clean[rest])
+    see = torch.ones(150, 150, device="cuda").tril().bool()
+    want = attend(huge, k, v, see)[0]
+    # the two largest logits of a row are 2^-24 of them apart nowhere here
+    assert off_by(out[[40, 90]], want[[40, 90]]) < (1e-6 if out_type == torch.float32 else 3e-3)
