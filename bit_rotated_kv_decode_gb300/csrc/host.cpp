@@ -937,7 +937,7 @@ cudaError_t chunk_group(oscar_cache* c, const AttnReq* reqs, int n, bool history
                         const CUtensorMap* maps, const ChunkSpace& space, char* ws, ScanArgs& sa, cudaStream_t s) {
   const DevCache& d = c->dc;
   const PagedView p{nullptr, d.bf16_pt, d.n_bf16_pages, BF16_PAGES_PER_REQ, n, d.Hkv, d.err};
-  int64_t cost = 0, segments = 0;
+  int64_t cost = 0, segments = 0, units = 0;   // (units: 16 rows of a kv head)
   sa.n = n;
   sa.setup = CHUNK_SETUP;
   for (int i = 0; i < n; ++i) {
@@ -950,15 +950,18 @@ cudaError_t chunk_group(oscar_cache* c, const AttnReq* reqs, int n, bool history
     sa.segment[i] = static_cast<int32_t>(segments);
     sa.cost[i] = cost;
     segments += (int64_t)d.Hkv * sa.blocks[i];
+    units += ((int64_t)reqs[i].m * d.G + 15) / 16;
     cost += (int64_t)d.Hkv * sa.blocks[i] * (sa.tiles[i] + sa.setup);
   }
   // The near rows' kernel takes 14 us for a request's 320 tokens, 9 with a CTA a key tile.  Those CTAs are the scan's
-  // too, so that it is split where the scan is short and rows, so what there is to merge, are few (5 tokens over 400
-  // cached 18.6 us, 23.7 otherwise; over 20K 33.3, 37.4; over 100K 63.8 otherwise, 70.1; 150 tokens over 2K 48 otherwise, 76).
+  // too, so that it is split where the scan is short (SPLIT units an SM) and rows, so what there is to merge, are few
+  // (32 heads of 8: 5 tokens over 400 cached 17.4 us, 23.7 otherwise; over 20K 30, 37; over 100K 59 otherwise, 65; 40
+  // tokens over 400 27, 33; 150 over 2K 37.6 otherwise, 47).
   constexpr int64_t SPLIT = 16;
+  const bool split = history && cost <= SPLIT * c->num_sms && units * d.Hkv < c->num_sms;
   NearPlan plan;
   cudaError_t e = launch_near_attention(p, reqs, n, a, history, maps[0], maps[1], maps[2], maps[3], ws + space.near,
-                                        history && !pair && cost <= SPLIT * c->num_sms ? 1 : 4, &plan, c->num_sms, s);
+                                        split ? 1 : 4, &plan, c->num_sms, s);
   if (e != cudaSuccess || !history) return e;
   sa.total = cost;
   // the near rows' CTAs run beside the scan's, one per SM: where they are few, the scan leaves them theirs
