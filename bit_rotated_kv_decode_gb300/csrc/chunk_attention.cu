@@ -56,9 +56,11 @@ constexpr int SC_FEW = 64;                     // rows of which a chain's first 
 // its exponents, comes LAG steps after them: SLOTS + 2 + LAG steps have to be kept, 9 at most.
 constexpr int SIZES = 16;
 constexpr float SC_LAZY = 4.0f;                // the softmax reference moves only when exceeded by 2^4
-// |S| is at most 128 x 2^11 x 2^-8: logits stay within 2^22, where the roundings of a product, of the maximum and of
-// the reference, 2^-2 each, leave a weight below 2^16.  (Logits beyond that have lost 2^10 to the rounding of q R_K.)
-constexpr float SC_STEEPEST = 0x1p12f;
+// |S| is at most 128 x 2^11 x 2^-8.  Up to this scale logits stay within 2^22, where the roundings of a product, of the
+// maximum and of the reference, 2^-2 each, leave a weight below 2^16.  Beyond it S is taken as differences to the row's
+// largest of the tile, before the scale, so that logits of any size keep their order over tiles and segments.
+constexpr float SC_STEEP = 0x1p12f;
+constexpr float SC_STEEPEST = 0x1p117f;        // (so that a logit is finite)
 constexpr float SC_SHIFT = 11.0f;              // weights are at most 2^15, and fp16's steps below 2^-14 cost nothing
 
 // Packed data of a step: K codes of a tile, V codes of an earlier one and their {s, z}; {s, z} of the tile's own keys
@@ -312,80 +314,120 @@ __global__ void __launch_bounds__(SC_THREADS, 1)
       bool any = false;
       const int tiles = n > from ? (n - from + LAG - 1) / LAG : 0;   // of the chain
       if (idle) tile += tiles;
-      for (int i = idle ? n : from; i < n; i += LAG, step += LAG, ++tile, left -= LAG * SC_KEYS) {
-        ok = mbar_wait_warp(&sm.s_full[a], tile & 1, ok);
-        if (!ok) break;
-        tc_fence_after();
-        // (written before the keys were unpacked, so before S)
-        const float2 size = *reinterpret_cast<const float2*>(&sm.size[step % SIZES]);
-        const float scale = fminf(scale2 * size.y, SC_STEEPEST);
-        uint32_t xr[128];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, xr + 32 * h);
-        tc_wait_ld();
-        float* x = reinterpret_cast<float*>(xr);
-        if (left < SC_KEYS) {   // keys behind the end
-#pragma unroll
-          for (int j = 0; j < SC_KEYS; ++j)
-            if (j >= left) x[j] = NEG_INF;
-        }
-        float t[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) t[k] = x[k];
-#pragma unroll
-        for (int j = 4; j < 124; j += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[j + 2 * k], x[j + 2 * k + 1]);
-        const float top = fmaf(fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])), scale, size.x);
-        const bool raise = top > mx + SC_LAZY || (mx == NEG_INF && top > NEG_INF);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
-          l *= f;
-          if (raise) mx = top;
-          if (any) {   // the product before S is done: S was issued after it
+      auto keys = [&](auto any_scale) {   // the chain's key tiles; false: no row's scale is above SC_STEEP
+        constexpr bool ANY_SCALE = decltype(any_scale)::value;
+        for (int i = idle ? n : from; i < n; i += LAG, step += LAG, ++tile, left -= LAG * SC_KEYS) {
+          ok = mbar_wait_warp(&sm.s_full[a], tile & 1, ok);
+          if (!ok) break;
+          tc_fence_after();
+          // (written before the keys were unpacked, so before S)
+          const float2 size = *reinterpret_cast<const float2*>(&sm.size[step % SIZES]);
+          const float scale = fminf(scale2 * size.y, SC_STEEPEST);
+          const bool steep = ANY_SCALE && scale > SC_STEEP;
+          float zero = size.x;   // exponent of what S holds as 0
+          if (ANY_SCALE && __any_sync(0xffffffffu, steep)) {   // a row's form depends on the row alone
+            float most = NEG_INF;
 #pragma unroll 1
-            for (int col = 0; col < 128; col += 16) {   // in small pieces: the logits are live
+            for (int col = 0; col < SC_KEYS; col += 16) {
               uint32_t o[16];
-              tmem_ld16(to + col, o);
+              tmem_ld16(ts + col, o);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(to + col, o);
+              for (int j = 0; j < 16; ++j)
+                if (col + j < left) most = fmaxf(most, __uint_as_float(o[j]));
+            }
+            const float less = steep ? most : 0.0f;
+#pragma unroll 1
+            for (int col = 0; col < SC_KEYS; col += 16) {
+              uint32_t o[16];
+              tmem_ld16(ts + col, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) - less);
+              tmem_st16(ts + col, o);
+            }
+            tc_wait_st();
+            zero = fmaf(less, scale, size.x);
+          }
+          uint32_t xr[128];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) tmem_ld32(ts + 32 * h, xr + 32 * h);
+          tc_wait_ld();
+          float* x = reinterpret_cast<float*>(xr);
+          if (left < SC_KEYS) {   // keys behind the end
+#pragma unroll
+            for (int j = 0; j < SC_KEYS; ++j)
+              if (j >= left) x[j] = NEG_INF;
+          }
+          float t[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = x[k];
+#pragma unroll
+          for (int j = 4; j < 124; j += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[j + 2 * k], x[j + 2 * k + 1]);
+          const float top = fmaf(fmaxf(max3(t[0], t[1], max3(t[2], t[3], x[124])), max3(x[125], x[126], x[127])), scale, zero);
+          // (as a difference: it is exact near a large maximum, where mx + SC_LAZY may be rounded up by more than that)
+          const bool raise = top - mx > SC_LAZY;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = raise ? (mx == NEG_INF ? 0.0f : ex2f(mx - top)) : 1.0f;
+            l *= f;
+            if (raise) mx = top;
+            if (any) {   // the product before S is done: S was issued after it
+#pragma unroll 1
+              for (int col = 0; col < 128; col += 16) {   // in small pieces: the logits are live
+                uint32_t o[16];
+                tmem_ld16(to + col, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(to + col, o);
+              }
             }
           }
+          any = true;
+          const float ref = steep ? (zero - mx) + SC_SHIFT : size.x + (mx == NEG_INF ? 0.0f : SC_SHIFT - mx);
+          const float2 scale_2 = make_float2(scale, scale), ref_2 = make_float2(ref, ref);
+          float2 sum[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {   // 32 keys
+            float2 y[16];
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = fma2(make_float2(x[32 * h + 2 * j], x[32 * h + 2 * j + 1]), scale_2, ref_2);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              y[j].x = ex2f(y[j].x);
+              y[j].y = ex2f(y[j].y);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              pk[j] = f16x2(y[j].x, y[j].y);
+              sum[j & 3] = add2(sum[j & 3], y[j]);
+            }
+            tmem_st16(ts + 64 * (h >> 1) + 16 * (h & 1), pk);   // P lies over S, 64 keys in 32 columns
+            if (h & 1) {
+              tc_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.p_full[a][h >> 1], arrivals);
+            }
+          }
+          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          l = fmaf(sum[0].x + sum[0].y, sm.size[step % SIZES].z, l);
         }
-        any = true;
-        const float ref = size.x + (mx == NEG_INF ? 0.0f : SC_SHIFT - mx);
-        const float2 scale_2 = make_float2(scale, scale), ref_2 = make_float2(ref, ref);
-        float2 sum[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {   // 32 keys
-          float2 y[16];
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = fma2(make_float2(x[32 * h + 2 * j], x[32 * h + 2 * j + 1]), scale_2, ref_2);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            y[j].x = ex2f(y[j].x);
-            y[j].y = ex2f(y[j].y);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            pk[j] = f16x2(y[j].x, y[j].y);
-            sum[j & 3] = add2(sum[j & 3], y[j]);
-          }
-          tmem_st16(ts + 64 * (h >> 1) + 16 * (h & 1), pk);   // P lies over S, 64 keys in 32 columns
-          if (h & 1) {
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[a][h >> 1], arrivals);
-          }
-        }
-        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l = fmaf(sum[0].x + sum[0].y, sm.size[step % SIZES].z, l);
+      };
+      if constexpr (PAIR) {
+        // The head's threshold, which clips what is rotated, bounds 2^a (1 % and 2^-22 for the roundings of s and z).
+        // A loop for rows that it keeps below: 2048 tokens over 60K 1319 us, 1345 with the other loop alone -- which is
+        // the one where rows are few: 5 over 100K 59.1, 61.1 with both.  (Rows beyond SC_STEEP: 2186 and 80.)
+        const float tau = c.tau_k[(size_t)A.layer * c.Hkv + s.head];
+        const float most = pow2(value_exponent(__float_as_uint(fmaf(1.01f, tau, 0x1p-22f))));
+        if (__any_sync(0xffffffffu, scale2 * most > SC_STEEP)) keys(std::true_type()); else keys(std::false_type());
+      } else {
+        keys(std::true_type());
       }
       // the rows' sums, maximum and sum to the workspace
       if (tiles > 0) {

@@ -309,7 +309,8 @@ oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int3
  *              requests hold), 256-byte aligned; no contents are needed.  Calls that share
  *              a workspace must not overlap on the GPU.
  * New tokens of a request that some of its queries see and others do not must hold finite values.
- * q · k is finite in fp32.  Sums and softmax statistics are fp32; in the history, q R_K, the values
+ * |q| |k|, the lengths of a query and a key, is below 2^117, and so is its product with the softmax
+ * scale.  Sums and softmax statistics are fp32; in the history, q R_K, the values
  * z + s c (those below 2^-5 of the largest of their 128 tokens to 2^-16 of it), the weights, and for
  * many rows the weighted sums and R_V are rounded to 11 bits; elsewhere weights to 8.  Page ids out of
  * range and waits that gave up are reported by oscar_cache_check. */

@@ -784,3 +784,81 @@ def test_prompt_queries_of_any_size(b, out_type):
     want = attend(huge, k, v, see)[0]
     # the two largest logits of a row are 2^-24 of them apart nowhere here
     assert off_by(out[[40, 90]], want[[40, 90]]) < (1e-6 if out_type == torch.float32 else 3e-3)
+
+
+def unit(x):
+    return x / x.norm(dim=-1, keepdim=True)
+
+
+def unclipped(b, h, tokens, threshold=65504):
+    """One request of thresholds that clip nothing."""
+    tau = np.full((1, h.hkv), threshold, np.float32)
+    h.cache = b.OscarCache(b.make_config(1, h.hq, h.hkv, 1, tokens // 64 + 1, tokens // 64 + 1, group_size=h.group), *h.rot, tau, tau)
+    h.cache.int2_pool(0).fill_(255)
+    return h.cache.open()
+
+
+@pytest.mark.parametrize("group", [128, 64])
+@pytest.mark.parametrize("threshold", [65504, 160])
+@pytest.mark.parametrize("m", [5, 30, 200])
+def test_chunk_large_logits_keep_their_order(b, m, threshold, group):
+    """The best key is a history token among long ones; a token of a tile of short ones, or one of the recent window or
+    of the chunk, lies closer to the query's direction.  With queries of 2^10 to 2^100 the best key has all the weight: its
+    logit is ahead by 2^-5 of the longest key's length times the query's or more, where the roundings of q R_K and of the
+    keys are 2^-11 each.  Each row against float64, and ordinary rows beside them have the bits that they had."""
+    h = Held(b, group=group, seed=40 + m, requests=1, tokens=1400)
+    t, he = 1111, 855
+    r = unclipped(b, h, t, threshold)
+    length = torch.full((t,), 32.0, device="cuda")
+    tile = (torch.arange(t, device="cuda") - 64) // 128
+    length[(tile % 2 == 0) & (torch.arange(t, device="cuda") >= 64) & (torch.arange(t, device="cuda") < he)] = 256
+    k = (unit(h.rnd(t, 2, D)) * length[:, None, None]).bfloat16()
+    h.cache.extend(0, [r], k, h.tokens(t)[1], new_lens=[t])
+    assert h.cache.length(r, 0) == (t, he)
+    (kc, vc), (_, vm), _ = h.stored(r)
+    kn, vn = (unit(h.rnd(m, 2, D)) * 32).bfloat16(), h.tokens(m)[1]
+    keys, values, mags = (torch.cat(x) for x in ((kc, kn.double()), (vc, vn.double()), (vm, vn.double().abs())))
+    p = torch.arange(t + m, device="cuda")
+    see = p[None] <= torch.arange(t, t + m, device="cuda")[:, None]
+    # per row and head: its best key, and one that lies closer to it
+    rng = np.random.default_rng(m + group)
+    short = [x for x in range(64, he) if (x - 64) // 128 % 2]
+    long = [x for x in range(64, he) if (x - 64) // 128 % 2 == 0]
+    best = torch.tensor(rng.choice(long, (m, 8)), device="cuda")
+    far = torch.tensor(rng.choice(short, (m, 8)), device="cuda")
+    near = torch.tensor([[int(rng.integers(he, t + i + 1)) for _ in range(8)] for i in range(m)], device="cuda")
+    head = torch.arange(8, device="cuda") // 4
+    other = torch.where(head == (torch.arange(m, device="cuda") // 2 % 2)[:, None], far, near)
+    to = unit(keys)
+    w, d = to[best, head], to[other, head]
+    q = ((0.55 * w + 0.82 * unit(d - (d * w).sum(-1, keepdim=True) * w)) * 11).bfloat16()
+    plain = (h.rnd(m, 8, D) / 16).bfloat16()   # ordinary rows: weights of many keys
+    ordinary = torch.arange(m, device="cuda") % 4 == 1
+    q[ordinary] = plain[ordinary]
+
+    def run(q):
+        out = torch.full((m, 8, D), float("nan"), device="cuda", dtype=torch.bfloat16)
+        h.cache.chunk_attention(0, [r], q, kn, vn, out, new_lens=[m])
+        h.cache.check()
+        return out
+
+    clean = run(plain)
+    logit = torch.einsum("mhd,thd->mht", q.double(), keys.repeat_interleave(4, 1)).masked_fill(~see[:, None], -math.inf)
+    top = logit.topk(2, -1)
+    ahead = (top.values[..., 0] - top.values[..., 1]) / (q.double().norm(dim=-1) * keys.norm(dim=-1).max())
+    big = ~ordinary
+    assert torch.equal(top.indices[big][..., 0], best[big]) and float(ahead[big].min()) > 2 ** -5
+    closer = torch.einsum("mhd,mhd->mh", q.double(), d) > torch.einsum("mhd,mhd->mh", q.double(), w)
+    assert bool(closer[big].all())
+    for e in (10, 13, 16, 20, 40, 100):
+        x = torch.where(ordinary[:, None, None], q.float(), q.float() * 2.0 ** e).bfloat16()
+        out = run(x)
+        want, mag = attend(x, keys, values, see)[0], attend(x, keys, mags, see)[0]
+        # one value: it, R_V, its weight and the sum that is rotated back in fp16; 2^-15 of its tile's largest, some 4
+        # deviations, by the 11 that |R_V| sums, where mag is some 8 deviations: below 2^-12; and the result in bf16
+        tol = (4 * 2 ** -11 + 2 ** -12) * mag + 2 ** -8 * want.abs()
+        bad = ((out.double() - want).abs() > tol).flatten(1).any(-1) & big
+        wrong = int(bad.sum())
+        assert wrong == 0, (e, wrong, int(big.sum()))
+        assert off_by(out[big], want[big]) < 4e-3
+        assert torch.equal(out[ordinary].view(torch.int16), clean[ordinary].view(torch.int16)), e
