@@ -9,10 +9,11 @@
 //   chunk_merge_*_kernel   their sum, the history's times R_V^T, over the weights' sum.
 //
 // chunk_scan_kernel: a CTA takes 128 keys at a time.  Four warps unpack them, a key a thread,
-// into fp16 values z + s c in shared memory (rounded once, half a step 2^-12), a tile's keys times 2^-a and
-// its values times 2^-b: powers of two from their largest that keep them in range.  Per key tile and chain
+// into fp16 values z + s c in shared memory (off by 2^-11 of them and 2^-15 of the tile's largest), a tile's
+// keys times 2^-a and its values times 2^-b: powers of two from their largest that keep them in range.  Per key
+// tile and chain
 //   S = Q K^T            128 x 128 x 128, tcgen05.mma, both operands in shared memory
-//   p = exp2(S scale 2^a + b - m + 11)   one thread per row; fp16 (2^-12; the shift keeps weights down to
+//   p = exp2(S scale 2^a + b - m + 11)   one thread per row; fp16 (2^-11; the shift keeps weights down to
 //                        2^-25 of the row's largest in full, where fp16 alone would flush them)
 //   O = O + P V          tcgen05.mma, P from TMEM, O in TMEM
 // with m the running maximum of the exponents with b, so of what a key adds to O; the weights' sum takes
@@ -957,7 +958,7 @@ struct MergeRowsSmem {
   alignas(16) uint16_t row[8][UNIT][PITCH];    // a warp's rows: the history's sums (fp16), then the results (bf16)
 };
 // A warp takes 16 rows of one request and kv head at a time; the CTA keeps that head's rotation.  (The history's
-// sums, times a power of two of the row's, and R are rounded to fp16, 2^-12 each, an eighth of what the result's
+// sums, times a power of two of the row's, and R are rounded to fp16, 2^-11 each, an eighth of what the result's
 // rounding adds.)
 template <bool PAIR>
 __global__ void __launch_bounds__(MG_THREADS, 2)

@@ -6,7 +6,7 @@
 // read_history_kernel takes 128 history tokens of one kv head, K or V, at a time, whatever
 // requests they are of: a product of 128 x 128 x 128 on tcgen05.
 //   bf16 outputs  the values z + s c in fp16, times a power of two of the token's that keeps them in
-//                 range, by R in fp16: each off by 2^-12, an eighth of what the output's rounding adds;
+//                 range, by R in fp16: each off by 2^-11, an eighth of what the output's rounding adds;
 //   fp32 outputs  with c' = c - 1, whole numbers that any type holds,
 //                   x_j = s (c' R^T)_j + (z + s) sum_i R_ji     (per group of channels),
 //                 R in three bf16 parts (24 bits), the small ones first, the sums of its rows

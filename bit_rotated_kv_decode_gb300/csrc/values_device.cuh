@@ -8,8 +8,8 @@ namespace paged {
 
 // Values are held as x 2^-k, with 2^k from 2^8 to 2^9 times the largest of the tokens that share k (3 s is at
 // most twice that): a code's two bits, as the half that they are where they stand in a word, count
-// c 2^(2 at - 24), and s 2^(24 - 2 at - k) is a half too, at most 2^16 2/3, so that one fma gives z + s c rounded
-// once: by 2^-12 of it, or 2^-16 of the largest where it falls below fp16's normal values.
+// c 2^(2 at - 24), and s 2^(24 - 2 at - k) is a half too, at most 2^16 2/3, so that one fma gives z + s c: off
+// by 2^-11 of it, its rounding, and by 2^-15 of the largest where it and z fall below fp16's normal values (2^-16 each).
 // (Thresholds say nothing of the values' size: they may be far above it.)
 // The largest value of a token, as bits that compare as it does; k from it.  (fp16 holds nothing below 2^-24.)
 template <int NG>

@@ -292,7 +292,7 @@ oscar_status oscar_extend(oscar_cache* cache, int32_t layer, int32_t n, const in
  *   k_out, v_out  device [rows][Hkv][128] of out_type (oscar_type), 16-byte aligned.
  * History in fp32: R in 24 bits, sums in fp32 on the matrix unit (off by 2^-14 of their terms'
  * magnitudes at most, by 1e-7 of the values as measured).  In bf16: z + s c and R are rounded to
- * 11 bits (values below 2^-5 of the token's largest to 2^-16 of it), and the result once. */
+ * 11 bits (2^-11), z + s c by up to 2^-15 of its token's largest besides, and the result once. */
 oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs, const int32_t* starts,
                         const int32_t* counts, void* k_out, void* v_out, int32_t out_type, void* stream);
 
@@ -311,8 +311,8 @@ oscar_status oscar_read(oscar_cache* cache, int32_t layer, int32_t n, const int3
  * New tokens of a request that some of its queries see and others do not must hold finite values.
  * |q| |k|, the lengths of a query and a key, is below 2^117, and so is its product with the softmax
  * scale.  Sums and softmax statistics are fp32; in the history, q R_K, the values
- * z + s c (those below 2^-5 of the largest of their 128 tokens to 2^-16 of it), the weights, and for
- * many rows the weighted sums and R_V are rounded to 11 bits; elsewhere weights to 8.  Page ids out of
+ * z + s c (by up to 2^-15 of the largest of their 128 tokens besides), the weights, and for many rows
+ * the weighted sums and R_V are rounded to 11 bits (2^-11); elsewhere weights to 8 (2^-8).  Page ids out of
  * range and waits that gave up are reported by oscar_cache_check. */
 oscar_status oscar_chunk_workspace_bytes(const oscar_cache* cache, int32_t n, const int32_t* new_lens, size_t* bytes);
 oscar_status oscar_chunk_attention(oscar_cache* cache, int32_t layer, int32_t n, const int32_t* reqs,

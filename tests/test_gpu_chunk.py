@@ -862,3 +862,42 @@ def test_chunk_large_logits_keep_their_order(b, m, threshold, group):
         assert wrong == 0, (e, wrong, int(big.sum()))
         assert off_by(out[big], want[big]) < 4e-3
         assert torch.equal(out[ordinary].view(torch.int16), clean[ordinary].view(torch.int16)), e
+
+
+@pytest.mark.parametrize("group", [128, 64])
+@pytest.mark.parametrize("m", [5, 200])
+def test_small_values_beside_large_ones(b, m, group):
+    """Rows whose weight lies on one history token whose value is 2^-6 to 2^-12 of its tile's largest: fp16's 2^-11 of the
+    value, and 2^-15 of that largest."""
+    h = Held(b, group=group, seed=50 + m, requests=1, tokens=1400)
+    t, he = 1111, 855
+    r = unclipped(b, h, t)
+    k, v = (unit(h.rnd(t, 2, D)) * 11).bfloat16(), h.rnd(t, 2, D)
+    small = torch.arange(t, device="cuda") % 3 == 0
+    v = torch.where(small[:, None, None], v * torch.exp2(-6.0 - 2 * (torch.arange(t, device="cuda") // 3 % 4))[:, None, None], v).bfloat16()
+    h.cache.extend(0, [r], k, v, new_lens=[t])
+    assert h.cache.length(r, 0) == (t, he)
+    (kc, vc), (_, vm), _ = h.stored(r)
+    kn, vn = (unit(h.rnd(m, 2, D)) * 11).bfloat16(), h.rnd(m, 2, D).bfloat16()
+    best = torch.tensor(np.random.default_rng(m + group).choice([x for x in range(64, he) if x % 3 == 0], (m, 8)), device="cuda")
+    head = torch.arange(8, device="cuda") // 4
+    # (logits of 15 the best key's length, others' at most half of that: weights below 2^-30)
+    q = (unit(kc[best, head]) * 11 * 16).bfloat16()
+    out = torch.full((m, 8, D), float("nan"), device="cuda", dtype=torch.bfloat16)
+    h.cache.chunk_attention(0, [r], q, kn, vn, out, new_lens=[m])
+    h.cache.check()
+    p = torch.arange(t + m, device="cuda")
+    see = p[None] <= torch.arange(t, t + m, device="cuda")[:, None]
+    keys, values = torch.cat([kc, kn.double()]), torch.cat([vc, vn.double()])
+    logit = torch.einsum("mhd,thd->mht", q.double(), keys.repeat_interleave(4, 1)).masked_fill(~see[:, None], -math.inf)
+    top = logit.topk(2, -1)
+    assert torch.equal(top.indices[..., 0], best) and float((top.values[..., 0] - top.values[..., 1]).min()) / math.sqrt(D) > 30
+    want = attend(q, keys, values, see)[0]
+    # the largest rotated value of each tile, and what rotating it back sums of 2^-15 of it
+    rot = h.rot[1][0].double()
+    y = torch.einsum("thi,hij->thj", vc[64:he], rot).abs().amax(-1)
+    most = torch.stack([y[64 * (2 * i):64 * (2 * i + 2)].amax(0) for i in range((he - 64 + 127) // 128)])   # [tiles][hkv]
+    reach = rot.abs().sum(-1)                                                                               # [hkv][128]
+    tile = (best - 64) // 128
+    tol = (4 * 2 ** -11) * vm[best, head] + 2 ** -8 * want.abs() + 2 ** -15 * most[tile, head][..., None] * reach[head]
+    assert bool(((out.double() - want).abs() <= tol).all()), float(((out.double() - want).abs() / tol).max())
