@@ -12,8 +12,8 @@
 //                 R in three bf16 parts (24 bits), the small ones first, the sums of its rows
 //                 once per CTA; two groups of channels have an accumulator each.
 //
-// Bound by the stores (30K tokens of 8 kv heads: bf16 32 us, 61 MB of 79 written; fp32 63 us, 123 MB of 141) and
-// 8 us of set-up.
+// Bound by the stores (30K tokens of 8 kv heads: bf16 32 us, 123 MB written of 141 moved; fp32 63 us, 246 of 264:
+// 4.2 to 4.4 TB/s) and 8 us of set-up.
 //
 // Two to four groups of four warps per CTA take tiles in turn: what one waits for (its codes, two
 // loads apart, and its products), the others' outputs cover.

@@ -19,7 +19,7 @@
 // R2 before (2^-8 of that) 290 u S; what R1 + R2 leave of R 2^-18 S = 64 u S; x's own rounding
 // u S: 355 u S < 0x1.7p-16 S.
 //
-// 8192 tokens of 8 kv heads: 37 us, of which the floor (k and v read once, 72 bytes a token-head written) is 6.4.  Half
+// 8192 tokens of 8 kv heads: 37 us, of which the floor (k and v read once, 72 bytes a token-head written) is 5.7.  Half
 // of it is latency and set-up -- a group of warps has two tiles, 10 us the first -- and 8 to 15 us are open values, most in
 // the head whose tokens differ most in length, whose CTAs are the last.
 //

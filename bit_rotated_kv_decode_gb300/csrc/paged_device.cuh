@@ -16,12 +16,15 @@ constexpr float LAZY_MAX = 8.0f;              // the softmax reference moves onl
 constexpr float NEG_INF = -INFINITY;
 
 // Programmatic dependent launch: a kernel's blocks are scheduled while the grid before it in
-// the stream ends.  It calls grid_dep_wait() before it touches global memory: the grid
-// before (and all before that) is then complete and its writes are visible -- to ordinary
-// loads.  Inputs (q, page ids, the rotation's table) may thus be written within this kernel's
-// life, where non-coherent loads (__ldg, ld.global.nc) promise nothing: none is used, but
-// plain ones, as fast (through the L2, by __ldcg, the threads of a row look their page up
-// sixteen times: 4-bit read-back as bf16 20.0 against 17.1 us).
+// the stream ends.  It calls grid_dep_wait() before it touches global memory (what was written
+// once at a cache's creation apart): the grid before (and all before that) is then complete and
+// its writes are visible -- to ordinary loads.  Inputs (q, page ids, the rotation's table) may
+// thus be written within this kernel's life, where non-coherent loads (__ldg, ld.global.nc)
+// promise nothing: none is used, but plain ones, as fast (through the L2, by __ldcg, the threads
+// of a row look their page up sixteen times: 4-bit read-back as bf16 20.0 against 17.1 us).
+// One kernel does otherwise: chunk_scan_kernel waits at its end, reads past the L1 caches, and
+// counts on the grid before it, launch_near_attention()'s, to let it start only behind its own
+// wait (the order of the two calls in paged_prefill_kernel<..., CACHE> must stay).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... P, typename... A>

@@ -495,8 +495,8 @@ const char* oscar_paged_last_error(void);
  *              not overlap on the GPU.
  * Hq / Hkv in {1, 2, 4, 8}.  Tokens that a query does not see do not touch its result,
  * whatever other sequences hold; within a sequence, those that some queries see and others
- * do not must hold finite values; q · k is finite in fp32.  Sums and softmax statistics are
- * fp32; weights enter the product with V to 24 bits for fp32 outputs, to 8 for bf16. */
+ * do not must hold finite values; q · k, and 1.5 scale q · k, are finite in fp32.  Sums and
+ * softmax statistics are fp32; weights enter the product with V to 24 bits for fp32 outputs, to 8 for bf16. */
 size_t oscar_prompt_workspace_bytes(int32_t n, const int32_t* lens, int32_t num_q_heads, int32_t num_kv_heads);
 oscar_status oscar_prompt_attention(const int32_t* lens, int32_t n, int32_t num_q_heads, int32_t num_kv_heads,
                                     int32_t window, int32_t sinks, float scale, const uint16_t* q, int64_t q_stride,
